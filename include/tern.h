@@ -41,6 +41,12 @@
  *   The bit order lets the kernels turn a byte into the fp8 e4m3 encoding of
  *   w/8 with one shift and one AND.
  * Scales: fp16 [N][K/128], scale (n, g) applies to k in [128g, 128g+128).
+ *
+ * Beside the layer, the operators that stand between two such layers of a
+ * decoder: tern_add_rmsnorm_s8 (residual, norm and int8 codes),
+ * tern_linear_s8 (the layer on such codes), tern_kv8_append and
+ * tern_kv8_attention (a paged int8 cache of keys and values and the attention
+ * that reads it).
  */
 #ifndef TERN_H_
 #define TERN_H_
@@ -59,8 +65,17 @@ typedef enum {
   TERN_ENOSPACE = -3, /* workspace smaller than tern_linear_workspace_bytes() */
   TERN_ENODEV = -4,   /* no usable sm_103 device current */
   TERN_ECUDA = -5,    /* a CUDA runtime call or launch failed */
-  TERN_ETIMEOUT = -6  /* a device-side bounded wait ran out (see tern_device_status) */
+  TERN_ETIMEOUT = -6, /* a device-side bounded wait ran out (see tern_device_status) */
+  TERN_EINDEX = -7    /* a kernel met a page, length or row index out of range and
+                         skipped it (see tern_device_status) */
 } tern_status;
+
+/* Element types of the operators that take more than one. */
+typedef enum {
+  TERN_F32 = 0,
+  TERN_BF16 = 1,
+  TERN_F16 = 2
+} tern_type;
 
 /* Rung identifiers (tern_select_rung / tern_last_rung_id). */
 typedef enum {
@@ -222,6 +237,140 @@ int tern_linear(const uint32_t* Wpacked, const uint16_t* scales,
                 const uint16_t* x, float* y, int T, int K, int N,
                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* The layer on int8 codes and token scales that the caller already has
+ * (tern_quant_act_s8's or tern_add_rmsnorm_s8's):
+ *   acc[t][n][g] = sum_{k in g} q[t][k] * w[n][k]   (exact integers)
+ *   y[t][n]      = x_scale[t] * sum_g s[n][g] * acc[t][n][g]   (fp32),
+ * the s8 definition at every T, without quantising again.  T <= 16 runs on
+ * the small-T rungs' kernels, T >= 17 on the s8 rung's; TERN_RUNG forces a
+ * rung as for tern_linear (bf16 has no such form: TERN_EINVAL), the other
+ * environment overrides (TERN_ROTATE, TERN_PREFILL, TERN_DECODE_ACT) do not
+ * apply.
+ *   q        device int8 [T][K], any value of -128..127
+ *   x_scale  device fp32 [T]
+ *   the others and the workspace as for tern_linear. */
+int tern_linear_s8(const uint32_t* Wpacked, const uint16_t* scales,
+                   const int8_t* q, const float* x_scale, float* y, int T,
+                   int K, int N, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Residual addition, root-mean-square norm and int8 codes of token rows:
+ *   r = x + residual, rounded to the residual's type (r = x without one)
+ *   y = r * weight / sqrt(mean_k(r^2) + eps)             (fp32)
+ *   x_scale[t] = max_k |y[t][k]| / 127                   (IEEE division)
+ *   q[t][k]    = clamp(rint(y / x_scale), -127, 127), to nearest even;
+ *                a token whose y is all zeros gets x_scale 0 and q 0.
+ *   x        device [T][K] of x_type (TERN_F32, as tern_linear writes it, or
+ *            TERN_BF16); row t starts at element t * x_ld (x_ld >= K, rows
+ *            16-byte aligned)
+ *   residual device [T][K] of residual_type (TERN_BF16 or TERN_F32), or NULL
+ *   residual_out device [T][K] of residual_type, written with r; may be
+ *            residual itself, may be NULL; NULL when residual is
+ *   weight   device [K] of weight_type (TERN_BF16 or TERN_F32)
+ *   q, x_scale device int8 [T][K] and fp32 [T], written; both or neither NULL
+ *   y        device bf16 [T][K], written with y rounded once (what the
+ *            bf16-activation rungs take), or NULL; q or y must be given
+ *   T >= 1; K > 0, K % 16 == 0, K <= 32768; eps >= 0.
+ * The statistics are fp32.  A row that holds an infinity or a NaN gives
+ * unspecified codes and a scale that is not finite or 0. */
+int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
+                        const void* residual, void* residual_out,
+                        int residual_type, const void* weight, int weight_type,
+                        float eps, int8_t* q, float* x_scale, uint16_t* y,
+                        int T, int K, void* stream);
+
+/* ---------------------------------------------------------------- int8 cache
+ * A paged cache of keys and values in int8.  A page holds TERN_KV8_BLOCK
+ * tokens of one sequence, keys and values of every head, and is the block
+ * that shares a scale: one fp32 scale for each (page, keys | values, head).
+ *   codes   device int8 [pages][2][kv_heads][TERN_KV8_BLOCK][head_dim],
+ *           keys at [0], values at [1] of the second index
+ *   scales  device fp32 [pages][2][kv_heads]; a stored value is scale * code
+ *   page_table  device int32 [seqs][table_width]: page of tokens
+ *           [64 j, 64 j + 64) of each sequence; entries past a sequence's
+ *           last token are not read
+ *   seq_lens    device int32 [seqs]: tokens of each sequence, the new ones
+ *           included
+ *   row_start   device int32 [seqs + 1], ascending: the new tokens of sequence
+ *           b are rows [row_start[b], row_start[b + 1]) of q, k and v; they
+ *           are its last tokens, in order
+ * Sequences may be empty and may have no new tokens.  These arrays are read
+ * on the device, so a captured call can be replayed with other contents.  A
+ * sequence whose entries are inconsistent (a length that is negative or does
+ * not fit table_width, more new tokens than tokens or than max_new, rows
+ * outside [0, rows)) is skipped and its rows of the output are left as they
+ * are; a page outside [0, pages) is skipped, as if its tokens were masked;
+ * both are recorded for tern_device_status (TERN_EINDEX).  */
+#define TERN_KV8_BLOCK 64
+
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* row_start;
+  int pages, seqs, table_width;
+  int kv_heads, head_dim; /* head_dim 64 or 128 */
+} tern_kv8_cache;
+
+/* Write the new keys and values of every sequence into the cache.  For each
+ * page that receives new tokens, keys and values apart, and each head:
+ *   s = max(s_old if the page holds older tokens, max |new| / 127)  (fp32,
+ *       IEEE division);
+ *   where s > s_old, the older tokens' codes become rint(code * (s_old / s));
+ *   new codes are clamp(rint(x / s), -127, 127), rint to nearest even.
+ * Codes of the page's slots past the last token are left as they are; the
+ * scale of a page without older tokens is overwritten whatever it held.  An
+ * infinite or NaN input makes its block's scale NaN (the block's values then
+ * read as NaN), and no other block's.
+ *   k, v    device [rows][kv_heads][head_dim] of `type` (TERN_F32, TERN_BF16
+ *           or TERN_F16); row r, head h start at element r * ld + h * hd
+ *           (k and v have the same strides); every start 16-byte aligned
+ *   rows    rows of k and v; 0: nothing is done
+ *   max_new at least the most new tokens of a sequence (sizes the grid)
+ * No two sequences of a call may share a page that receives new tokens. */
+int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v,
+                    int type, long long ld, long long hd, int rows,
+                    int max_new, void* stream);
+
+/* Bytes of device workspace tern_kv8_attention needs for `rows` query rows of
+ * `seqs` sequences (the synchronisation area, then partial results of
+ * sequences that several CTAs share).  Host-only; 0 for sizes out of range. */
+size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
+                                          int kv_heads, int head_dim);
+
+/* Attention of the new tokens of every sequence over the cache (which must
+ * already hold them).  Query row i of the m new rows of a sequence of n tokens
+ * stands at position p = n - m + i and sees the tokens j <= p with, if window
+ * > 0, j > p - window or j < sinks:
+ *   o[row][h] = sum_j softmax_j(softmax_scale q[row][h] . k_j) v_j,
+ * k_j and v_j the cache's scale * code of key-value head h / (heads /
+ * kv_heads).  Codes of tokens that a row does not see (stale slots, pages
+ * outside the window) do not enter its result, whatever they and, where no
+ * row of the call sees the page, their scales hold.
+ *   q       device [rows][heads][head_dim] of `type` (TERN_BF16 or TERN_F16);
+ *           row r, head h start at element r * ld + h * hd, 16-byte aligned
+ *   rows    rows of q; 0: nothing is done
+ *   out     device [rows][heads][head_dim] of `type`, dense, written
+ *   lse     device fp32 [rows][heads], written with log sum_j exp(s_j)
+ *           (natural logarithm), or NULL
+ *   heads   a multiple of kv_heads, at most 64 times as many
+ *   max_new at least the most new tokens of a sequence
+ *   window  0 (none) or the tokens that a row sees, itself included
+ *   sinks   first tokens that stay visible outside the window (>= 0)
+ *   softmax_scale > 0
+ *   workspace as for tern_linear: zero its first TERN_SYNC_BYTES once.
+ * Numbers: q is scaled by a power of two per row and held in fp16 (exact for
+ * every element within 2^-31 of the row's largest), codes are exact in fp16,
+ * products and sums are fp32; the weights exp(.) are rounded to fp16 for
+ * their products with the values (relative 2^-11), their sum is fp32 and
+ * unrounded.  Results are bit-for-bit reproducible. */
+int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type,
+                       long long ld, long long hd, int rows, int heads,
+                       int max_new, int window, int sinks, float softmax_scale,
+                       void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Bytes of the fixed device scratch tern_linear_small_t_noalloc uses. */
 #define TERN_NOALLOC_SCRATCH_BYTES (8u << 20)
 
@@ -288,8 +437,9 @@ const char* tern_rung_name(int rung);
 int tern_last_rung_id(void);
 const char* tern_last_rung(void);
 
-/* Number of kernels this thread's last successful tern_linear (or
- * tern_linear_small_t_noalloc) launched: per token tile of the bandwidth
+/* Number of kernels this thread's last successful tern_linear,
+ * tern_linear_s8, tern_linear_small_t_noalloc, tern_add_rmsnorm_s8,
+ * tern_kv8_append or tern_kv8_attention launched: per token tile of the bandwidth
  * rungs one main kernel, plus the activation-prep kernel where the tile
  * uses one; 2 on the s8 rung (activation pieces, then the GEMM).  0 before
  * any call.  Host-only; for benchmarks and tests. */
@@ -308,7 +458,8 @@ void tern_reload_env(void);
  * asynchronous error word: TERN_OK, or TERN_ETIMEOUT if a kernel's bounded
  * wait ran out since the last call (in which case it also zeroes the
  * synchronisation area of tern_linear_small_t_noalloc's scratch, if that
- * scratch is set up on this device). */
+ * scratch is set up on this device), or TERN_EINDEX if a cache kernel skipped
+ * an index that was out of range. */
 int tern_device_status(void* stream);
 
 #ifdef __cplusplus

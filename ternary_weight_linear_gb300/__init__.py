@@ -10,7 +10,9 @@ every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -24,6 +26,8 @@ __all__ = [
     "tern_last_launches",
     "tern_reload_env", "tern_device_status", "tern_status_string", "TernError", "load",
     "tern_linear_small_t_noalloc", "tern_repack_t5", "tern_rotate_bf16",
+    "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append", "tern_kv8_attention",
+    "tern_kv8_attention_workspace_bytes", "KV8_BLOCK",
     "tern_selftest_wait_timeout", "RUNGS",
     "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES", "SYNC_BYTES", "T5_GROUP_BYTES", "ROTATION_BLOCK",
 ]
@@ -36,7 +40,8 @@ EXPORTED_SYMBOLS = (
     "tern_select_rung", "tern_rung_name", "tern_last_rung_id", "tern_last_rung",
     "tern_last_launches", "tern_status_string", "tern_reload_env", "tern_device_status",
     "tern_linear_small_t_noalloc", "tern_repack_t5", "tern_rotate_bf16",
-    "tern_selftest_wait_timeout",
+    "tern_selftest_wait_timeout", "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append",
+    "tern_kv8_attention", "tern_kv8_attention_workspace_bytes",
 )
 
 # Size of the library's fixed scratch for tern_linear_small_t_noalloc.
@@ -48,6 +53,20 @@ SYNC_BYTES = 4096
 T5_GROUP_BYTES = 26
 # Width of the Hadamard rotation's blocks along K.
 ROTATION_BLOCK = 1024
+# Tokens of a page of the int8 cache, which is the block that shares a scale.
+KV8_BLOCK = 64
+
+# tern_type
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class _KV8Cache(ctypes.Structure):
+    """tern_kv8_cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("codes", "scales", "page_table", "seq_lens", "row_start")] + [
+                    (n, ctypes.c_int) for n in
+                    ("pages", "seqs", "table_width", "kv_heads", "head_dim")]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -62,6 +81,8 @@ class TernError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libtern.so.  Raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -101,6 +122,18 @@ def load() -> ctypes.CDLL:
         lib.tern_repack_t5.restype = I
         lib.tern_rotate_bf16.argtypes = [P, P, I, I, P]
         lib.tern_rotate_bf16.restype = I
+        L, F = ctypes.c_longlong, ctypes.c_float
+        C = ctypes.POINTER(_KV8Cache)
+        lib.tern_linear_s8.argtypes = [P, P, P, P, P, I, I, I, P, Z, P]
+        lib.tern_linear_s8.restype = I
+        lib.tern_add_rmsnorm_s8.argtypes = [P, I, L, P, P, I, P, I, F, P, P, P, I, I, P]
+        lib.tern_add_rmsnorm_s8.restype = I
+        lib.tern_kv8_append.argtypes = [C, P, P, I, L, L, I, I, P]
+        lib.tern_kv8_append.restype = I
+        lib.tern_kv8_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.tern_kv8_attention_workspace_bytes.restype = Z
+        lib.tern_kv8_attention.argtypes = [C, P, I, L, L, I, I, I, I, I, F, P, P, P, Z, P]
+        lib.tern_kv8_attention.restype = I
         lib.tern_selftest_wait_timeout.argtypes = [I, P]
         lib.tern_selftest_wait_timeout.restype = I
         _lib = lib
@@ -123,24 +156,65 @@ def _check(func: str, rc: int) -> None:
         raise TernError(func, rc)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# torch's own way to the current stream's handle without building a Stream
+# object (0.2 us against 3 us, of calls that take ten)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _dev(t: torch.Tensor, name: str, dtype, shape=None) -> ctypes.c_void_p:
+def _dev(t: torch.Tensor, name: str, dtype, shape=None) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _strided(t: torch.Tensor, name: str, dtypes, ndim: int) -> int:
+    """A CUDA tensor whose last dimension is contiguous; the others may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _heads_strides(t: torch.Tensor):
+    """(row, head) strides of a [rows, heads, dim] tensor; where there is one
+    row or head its stride does not matter."""
+    rows, heads, dim = t.shape
+    hd = t.stride(1) if heads > 1 else dim
+    return t.stride(0) if rows > 1 else heads * dim, hd
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """What a call allocates for itself belongs to the stream that it runs on."""
+    if stream is None:
+        return _CURRENT
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------------ entry points
@@ -229,6 +303,172 @@ def tern_linear(Wpacked: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
         T, K, N, pws, nws, _stream(stream))
     _check("tern_linear", rc)
     return y
+
+
+def tern_linear_s8(Wpacked: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
+                   x_scale: torch.Tensor, y: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [T, N] fp32 = the ternary linear layer on int8 codes q [T, K] with
+    token scales x_scale [T] (tern_quant_act_s8's or tern_add_rmsnorm_s8's):
+    y[t, n] = x_scale[t] * sum_g scales[n, g] * (exact integer sum of group g).
+
+    The workspace is tern_linear's, with the same rules."""
+    T, K = q.shape
+    N = Wpacked.shape[0]
+    need = tern_linear_workspace_bytes(T, K, N)
+    with _allocating(stream):
+        if y is None:
+            y = torch.empty((T, N), dtype=torch.float32, device=q.device)
+        if workspace is None and need:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    pws = _dev(workspace, "workspace", torch.uint8) if workspace is not None else None
+    nws = workspace.numel() if workspace is not None else 0
+    rc = load().tern_linear_s8(
+        _dev(Wpacked, "Wpacked", torch.int32, (N, K // 16)),
+        _dev(scales, "scales", torch.float16, (N, K // 128)),
+        _dev(q, "q", torch.int8), _dev(x_scale, "x_scale", torch.float32, (T,)),
+        _dev(y, "y", torch.float32, (T, N)), T, K, N, pws, nws, _stream(stream))
+    _check("tern_linear_s8", rc)
+    return y
+
+
+def tern_add_rmsnorm_s8(x: torch.Tensor, weight: torch.Tensor,
+                        residual: torch.Tensor | None = None, eps: float = 1e-6, *,
+                        residual_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                        x_scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                        quantise: bool = True, stream=None):
+    """Residual addition, root-mean-square norm and int8 codes of token rows.
+
+    r = x + residual, rounded to the residual's type (r = x without one);
+    y = r * weight / sqrt(mean(r^2) + eps); x_scale[t] = max|y[t]| / 127;
+    q = rint(y / x_scale) in [-127, 127].  x [T, K] is fp32 (as tern_linear
+    gives it) or bf16, its rows may be strided; residual bf16 or fp32; weight
+    [K] bf16 or fp32.  `residual_out` (allocated when omitted) may be
+    `residual` itself.  `y`, if given, is written with the bf16 norm output,
+    which the bf16-activation rungs take; with quantise=False it is all that
+    is written.  Returns (q, x_scale, r)."""
+    T, K = x.shape
+    px = _strided(x, "x", (torch.float32, torch.bfloat16), 2)
+    ld = x.stride(0) if T > 1 else K
+    with _allocating(stream):
+        if quantise:
+            if q is None:
+                q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+            if x_scale is None:
+                x_scale = torch.empty((T,), dtype=torch.float32, device=x.device)
+        elif q is not None or x_scale is not None or y is None:
+            raise ValueError("quantise=False writes y alone")
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(residual)
+    pr = pro = None
+    rt = 0
+    if residual is not None:
+        if residual.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"residual must be float32 or bfloat16, got {residual.dtype}")
+        rt = _TYPES[residual.dtype]
+        pr = _dev(residual, "residual", residual.dtype, (T, K))
+        pro = _dev(residual_out, "residual_out", residual.dtype, (T, K))
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"weight must be float32 or bfloat16, got {weight.dtype}")
+    rc = load().tern_add_rmsnorm_s8(
+        px, _TYPES[x.dtype], ld, pr, pro, rt, _dev(weight, "weight", weight.dtype, (K,)),
+        _TYPES[weight.dtype], eps, _dev(q, "q", torch.int8, (T, K)) if quantise else None,
+        _dev(x_scale, "x_scale", torch.float32, (T,)) if quantise else None,
+        _dev(y, "y", torch.bfloat16, (T, K)) if y is not None else None, T, K, _stream(stream))
+    _check("tern_add_rmsnorm_s8", rc)
+    return q, x_scale, residual_out
+
+
+def _kv8_cache(codes, scales, page_table, row_start, seq_lens) -> _KV8Cache:
+    if codes.dim() != 5 or codes.shape[1] != 2 or codes.shape[3] != KV8_BLOCK:
+        raise ValueError(f"codes must be [pages, 2, kv_heads, {KV8_BLOCK}, head_dim], "
+                         f"got {tuple(codes.shape)}")
+    pages, _, heads, _, dim = codes.shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [seqs, pages of a sequence]")
+    seqs, width = page_table.shape
+    return _KV8Cache(
+        _dev(codes, "codes", torch.int8), _dev(scales, "scales", torch.float32, (pages, 2, heads)),
+        _dev(page_table, "page_table", torch.int32),
+        _dev(seq_lens, "seq_lens", torch.int32, (seqs,)),
+        _dev(row_start, "row_start", torch.int32, (seqs + 1,)), pages, seqs, width, heads, dim)
+
+
+def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                    page_table: torch.Tensor, row_start: torch.Tensor, seq_lens: torch.Tensor,
+                    max_new: int | None = None, stream=None) -> None:
+    """Write the new keys and values of every sequence into the paged int8 cache.
+
+    k, v [rows, kv_heads, head_dim] (fp32, bf16 or fp16; rows and heads may be
+    strided, both alike): the rows of sequence b are [row_start[b],
+    row_start[b + 1]), its last tokens of seq_lens[b].  codes int8 [pages, 2,
+    kv_heads, 64, head_dim] and scales fp32 [pages, 2, kv_heads] are updated;
+    page_table int32 [seqs, width].  `max_new` bounds the new tokens of a
+    sequence (the rows of the call when omitted).  tern_device_status tells
+    of inconsistent index arrays, whose sequences or pages are skipped."""
+    cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
+    pk = _strided(k, "k", _TYPES, 3)
+    pv = _strided(v, "v", (k.dtype,), 3)
+    if k.shape != v.shape or k.stride() != v.stride() or k.shape[1:] != (codes.shape[2],
+                                                                         codes.shape[4]):
+        raise ValueError("k and v must be [rows, kv_heads, head_dim] with the same strides")
+    rows = k.shape[0]
+    rc = load().tern_kv8_append(
+        ctypes.byref(cache), pk, pv, _TYPES[k.dtype], *_heads_strides(k), rows,
+        max(1, rows) if max_new is None else int(max_new), _stream(stream))
+    _check("tern_kv8_append", rc)
+
+
+def tern_kv8_attention_workspace_bytes(seqs: int, rows: int, heads: int, kv_heads: int,
+                                       head_dim: int) -> int:
+    return int(load().tern_kv8_attention_workspace_bytes(int(seqs), int(rows), int(heads),
+                                                         int(kv_heads), int(head_dim)))
+
+
+def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                       page_table: torch.Tensor, row_start: torch.Tensor, seq_lens: torch.Tensor,
+                       max_new: int | None = None, window: int = 0, sinks: int = 0,
+                       softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Causal attention of the newest tokens of every sequence over the paged
+    int8 cache (which already holds them).
+
+    q [rows, heads, head_dim] (bf16 or fp16, rows and heads may be strided),
+    rows of sequence b at [row_start[b], row_start[b + 1]).  window > 0: a
+    token sees the last `window` tokens, itself included, and the first
+    `sinks`.  softmax_scale defaults to head_dim ** -0.5.  Returns `out`
+    [rows, heads, head_dim] of q's type; `lse` fp32 [rows, heads], if given,
+    is written with the logarithm of the softmax's sum.
+
+    `workspace` (uint8, tern_kv8_attention_workspace_bytes bytes) is allocated
+    zeroed per call when omitted; one kept across calls starts with SYNC_BYTES
+    zero bytes and is then left alone."""
+    cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
+    pq = _strided(q, "q", (torch.bfloat16, torch.float16), 3)
+    rows, heads, dim = q.shape
+    kv_heads = codes.shape[2]
+    if dim != codes.shape[4]:
+        raise ValueError(f"q's head_dim {dim} is not the cache's {codes.shape[4]}")
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.zeros(
+                tern_kv8_attention_workspace_bytes(cache.seqs, max(1, rows), heads, kv_heads,
+                                                   dim),
+                dtype=torch.uint8, device=q.device)
+    rc = load().tern_kv8_attention(
+        ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads,
+        max(1, rows) if max_new is None else int(max_new), int(window), int(sinks),
+        1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
+        _dev(out, "out", q.dtype, (rows, heads, dim)),
+        _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("tern_kv8_attention", rc)
+    return out
 
 
 def tern_linear_small_t_noalloc(Wpacked: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,

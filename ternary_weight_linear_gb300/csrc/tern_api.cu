@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include "tern.h"
+#include "tern_device.cuh"
 #include "tern_internal.h"
 
 namespace tern {
@@ -154,6 +155,7 @@ int device_state(DevState** out) {
     if (s8_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (quant_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (bf16_set_attributes() != cudaSuccess) return TERN_ECUDA;
+    if (kv8_rows_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (!g_encode) {
       cudaDriverEntryPointQueryResult q;
       void* fn = nullptr;
@@ -199,6 +201,10 @@ int make_map_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
   return r == CUDA_SUCCESS ? TERN_OK : TERN_ECUDA;
 }
 
+// Largest row or head stride in elements: products with 32-bit row numbers
+// and an element's size stay within 64 bits.
+constexpr long long kMaxStride = 1ll << 28;
+
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // s8 scratch: the two fp8 pieces [T][K] each, then x_scale [T] (rounded up to
@@ -233,9 +239,10 @@ void small_t_tile(int rung, int left, int K, int N, int num_sms, int* tt, int* t
 }
 
 // ws: workspace whose first kSyncBytes are the zeroed sync area.
+// codes: the activations for act == kActCodes (x is null then).
 int run_small_t(DevState* d, int rung, const uint32_t* Wp, const uint16_t* s, const uint16_t* x,
-                float* y, int T, int K, int N, uint8_t* ws, int act, cudaStream_t st,
-                int* launches) {
+                const ActCodes& codes, float* y, int T, int K, int N, uint8_t* ws, int act,
+                cudaStream_t st, int* launches) {
   CUtensorMap tmW;
   int rc = make_map_u8(&tmW, Wp, static_cast<uint64_t>(K) / 4, static_cast<uint64_t>(N),
                        static_cast<uint64_t>(K) / 4, 128, smallt_rows(1),
@@ -244,12 +251,83 @@ int run_small_t(DevState* d, int rung, const uint32_t* Wp, const uint16_t* s, co
   for (int tok0 = 0; tok0 < T;) {
     int tt = 0, take = 0;
     small_t_tile(rung, T - tok0, K, N, d->sms, &tt, &take);
-    if (launch_smallt(tt, &tmW, Wp, s, x, reinterpret_cast<int*>(ws), ws + kSyncBytes, y, K, N,
-                      tok0, take, d->sms, act, d->err, st, launches) != cudaSuccess)
+    if (launch_smallt(tt, &tmW, Wp, s, x, codes, reinterpret_cast<int*>(ws), ws + kSyncBytes, y,
+                      K, N, tok0, take, d->sms, act, d->err, st, launches) != cudaSuccess)
       return TERN_ECUDA;
     tok0 += take;
   }
   return TERN_OK;
+}
+
+// The s8 rung: the activations' pieces (of x quantised, or of codes when x is
+// null), then the GEMM.
+int run_s8(DevState* d, const uint32_t* Wp, const uint16_t* s, const uint16_t* x,
+           const ActCodes& codes, float* y, int T, int K, int N, uint8_t* ws, int rotate,
+           cudaStream_t st, int* launches) {
+  // after the sync area (whose tickets the chunked last wave uses)
+  uint8_t* scratch = ws + kSyncBytes;
+  const size_t piece = align_up(static_cast<size_t>(T) * K, 256);
+  uint8_t* p1 = scratch;
+  uint8_t* p2 = scratch + piece;
+  float* xs = reinterpret_cast<float*>(scratch + 2 * piece);
+  const cudaError_t e =
+      x ? launch_quant_pieces(x, p1, p2, xs, T, K, rotate, d->sms, d->err, st)
+        : launch_code_pieces(codes.q, codes.x_scale, p1, p2, xs, T, K, d->sms, st);
+  if (e != cudaSuccess) return TERN_ECUDA;
+  ++*launches;
+  CUtensorMap tmW, tmP1, tmP2;
+  int rc = make_map_u8(&tmW, Wp, static_cast<uint64_t>(K) / 4, static_cast<uint64_t>(N),
+                       static_cast<uint64_t>(K) / 4, 32, kS8TileN, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (rc != TERN_OK) return rc;
+  const uint32_t tok = static_cast<uint32_t>(s8_token_tile(T));
+  rc = make_map_u8(&tmP1, p1, static_cast<uint64_t>(K), static_cast<uint64_t>(T),
+                   static_cast<uint64_t>(K), 128, tok, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != TERN_OK) return rc;
+  rc = make_map_u8(&tmP2, p2, static_cast<uint64_t>(K), static_cast<uint64_t>(T),
+                   static_cast<uint64_t>(K), 128, tok, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != TERN_OK) return rc;
+  float* partials =
+      reinterpret_cast<float*>(scratch + 2 * piece + align_up(sizeof(float) * T, 256));
+  rc = launch_s8(&tmW, &tmP1, &tmP2, s, xs, y, T, K, N, reinterpret_cast<int*>(ws), partials,
+                 d->sms, d->l2, d->err, st) == cudaSuccess
+           ? TERN_OK
+           : TERN_ECUDA;
+  ++*launches;
+  return rc;
+}
+
+// The cache's fields, checked: sizes, null pointers and alignment.
+int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
+  if (!c || !c->codes || !c->scales || !c->page_table || !c->seq_lens || !c->row_start ||
+      c->pages < 1 || c->seqs < 1 || c->table_width < 1 || c->kv_heads < 1 ||
+      c->kv_heads > 16384 || (c->head_dim != 64 && c->head_dim != 128))
+    return TERN_EINVAL;
+  // rows of the codes' tensor map have 32-bit coordinates; a sequence's
+  // tokens have 32-bit positions
+  if (static_cast<long long>(c->pages) * 2 * c->kv_heads * TERN_KV8_BLOCK > 0x7FFFFFFFll ||
+      static_cast<long long>(c->table_width) * TERN_KV8_BLOCK > 0x7FFFFFFFll)
+    return TERN_EINVAL;
+  if (!aligned16(c->codes) || !aligned16(c->scales) || !aligned16(c->page_table) ||
+      !aligned16(c->seq_lens) || !aligned16(c->row_start))
+    return TERN_EALIGN;
+  *a = Kv8Args{};
+  a->codes = c->codes;
+  a->scales = c->scales;
+  a->table = c->page_table;
+  a->lens = c->seq_lens;
+  a->starts = c->row_start;
+  a->pages = c->pages;
+  a->seqs = c->seqs;
+  a->width = c->table_width;
+  a->hkv = c->kv_heads;
+  a->dim = c->head_dim;
+  return TERN_OK;
+}
+
+// Strides of a [rows][heads][dim] operand: rows and heads start on 16 bytes
+// and a head's elements are consecutive.
+bool kv8_strides_ok(long long ld, long long hd, int dim) {
+  return ld >= dim && hd >= dim && ld <= kMaxStride && hd <= kMaxStride;
 }
 
 // Scratch of tern_linear_small_t_noalloc for T tokens and K, for any (N,
@@ -310,6 +388,7 @@ const char* tern_status_string(int st) {
     case TERN_ENODEV: return "no sm_103 CUDA device current";
     case TERN_ECUDA: return "CUDA runtime error";
     case TERN_ETIMEOUT: return "device-side wait timed out";
+    case TERN_EINDEX: return "page, length or row index out of range";
     default: return "unknown status";
   }
 }
@@ -417,39 +496,13 @@ int tern_linear(const uint32_t* Wpacked, const uint16_t* scales, const uint16_t*
     case TERN_RUNG_GEMV:
     case TERN_RUNG_SMALL_T:
     case TERN_RUNG_SMALL_T_TILED:
-      rc = run_small_t(d, rung, Wpacked, scales, x, y, T, K, N, static_cast<uint8_t*>(workspace),
-                       small_t_act(c), st, &launches);
+      rc = run_small_t(d, rung, Wpacked, scales, x, {}, y, T, K, N,
+                       static_cast<uint8_t*>(workspace), small_t_act(c), st, &launches);
       break;
-    case TERN_RUNG_S8: {
-      // after the sync area (whose tickets the chunked last wave uses)
-      uint8_t* scratch = static_cast<uint8_t*>(workspace) + kSyncBytes;
-      const size_t piece = align_up(static_cast<size_t>(T) * K, 256);
-      uint8_t* p1 = scratch;
-      uint8_t* p2 = scratch + piece;
-      float* xs = reinterpret_cast<float*>(scratch + 2 * piece);
-      if (launch_quant_pieces(x, p1, p2, xs, T, K, rotate, d->sms, d->err, st) != cudaSuccess)
-        return TERN_ECUDA;
-      ++launches;
-      CUtensorMap tmW, tmP1, tmP2;
-      rc = make_map_u8(&tmW, Wpacked, static_cast<uint64_t>(K) / 4, static_cast<uint64_t>(N),
-                       static_cast<uint64_t>(K) / 4, 32, kS8TileN, CU_TENSOR_MAP_SWIZZLE_NONE);
-      if (rc != TERN_OK) return rc;
-      const uint32_t tok = static_cast<uint32_t>(s8_token_tile(T));
-      rc = make_map_u8(&tmP1, p1, static_cast<uint64_t>(K), static_cast<uint64_t>(T),
-                       static_cast<uint64_t>(K), 128, tok, CU_TENSOR_MAP_SWIZZLE_128B);
-      if (rc != TERN_OK) return rc;
-      rc = make_map_u8(&tmP2, p2, static_cast<uint64_t>(K), static_cast<uint64_t>(T),
-                       static_cast<uint64_t>(K), 128, tok, CU_TENSOR_MAP_SWIZZLE_128B);
-      if (rc != TERN_OK) return rc;
-      float* partials = reinterpret_cast<float*>(scratch + 2 * piece +
-                                                 align_up(sizeof(float) * T, 256));
-      rc = launch_s8(&tmW, &tmP1, &tmP2, scales, xs, y, T, K, N, static_cast<int*>(workspace),
-                     partials, d->sms, d->l2, d->err, st) == cudaSuccess
-               ? TERN_OK
-               : TERN_ECUDA;
-      ++launches;
+    case TERN_RUNG_S8:
+      rc = run_s8(d, Wpacked, scales, x, {}, y, T, K, N, static_cast<uint8_t*>(workspace), rotate,
+                  st, &launches);
       break;
-    }
     case TERN_RUNG_BF16: {
       // after the sync area: x reordered for the MMA, 2 T K bytes (within
       // the s8 scratch the workspace size covers)
@@ -492,6 +545,158 @@ int tern_linear(const uint32_t* Wpacked, const uint16_t* scales, const uint16_t*
   return rc;
 }
 
+int tern_linear_s8(const uint32_t* Wpacked, const uint16_t* scales, const int8_t* q,
+                   const float* x_scale, float* y, int T, int K, int N, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (!Wpacked || !scales || !q || !x_scale || !y || T < 1 || N < 1 || K < 128 || (K % 128) != 0)
+    return TERN_EINVAL;
+  if (!aligned16(Wpacked) || !aligned16(scales) || !aligned16(q) || !aligned16(x_scale) ||
+      !aligned16(y))
+    return TERN_EALIGN;
+  Config c = config();
+  c.prefill_bf16 = c.rotate = c.decode_int8 = false;
+  const int rung = pick_rung(c, T);
+  if (rung == TERN_RUNG_BF16) return TERN_EINVAL;
+  DevState* d = nullptr;
+  int rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  if (!workspace || workspace_bytes < tern_linear_workspace_bytes(T, K, N)) return TERN_ENOSPACE;
+  if (!aligned16(workspace)) return TERN_EALIGN;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ActCodes codes;
+  codes.q = q;
+  codes.x_scale = x_scale;
+  int launches = 0;
+  rc = rung == TERN_RUNG_S8
+           ? run_s8(d, Wpacked, scales, nullptr, codes, y, T, K, N, ws, 0, st, &launches)
+           : run_small_t(d, rung, Wpacked, scales, nullptr, codes, y, T, K, N, ws, kActCodes, st,
+                         &launches);
+  if (rc == TERN_OK) {
+    t_last_rung = rung;
+    t_last_launches = launches;
+    probe(c, rung, T, K, N);
+  }
+  return rc;
+}
+
+int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld, const void* residual,
+                        void* residual_out, int residual_type, const void* weight,
+                        int weight_type, float eps, int8_t* q, float* x_scale, uint16_t* y, int T,
+                        int K, void* stream) {
+  auto f32_or_bf16 = [](int t) { return t == TERN_F32 || t == TERN_BF16; };
+  if (!x || !weight || T < 1 || K <= 0 || (K % 16) != 0 || K > kNormMaxK || x_ld < K ||
+      !f32_or_bf16(x_type) || !f32_or_bf16(weight_type) || !(eps >= 0.f) || (!q && !y) ||
+      (q != nullptr) != (x_scale != nullptr) || x_ld > kMaxStride)
+    return TERN_EINVAL;
+  if (residual ? !f32_or_bf16(residual_type) : residual_out != nullptr) return TERN_EINVAL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(weight) ||
+      !aligned16(q) || !aligned16(x_scale) || !aligned16(y) ||
+      (x_ld * (x_type == TERN_F32 ? 4 : 2)) % 16 != 0)
+    return TERN_EALIGN;
+  DevState* d = nullptr;
+  int rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  const NormArgs a = {x,   x_ld, x_type,  residual, residual_out, residual_type, weight, weight_type,
+                      eps, q,    x_scale, y,        T,            K};
+  if (launch_add_rmsnorm_s8(a, d->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return TERN_ECUDA;
+  t_last_launches = 1;
+  return TERN_OK;
+}
+
+int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v, int type,
+                    long long ld, long long hd, int rows, int max_new, void* stream) {
+  Kv8Args a;
+  int rc = kv8_args(cache, &a);
+  if (rc != TERN_OK) return rc;
+  if (type < TERN_F32 || type > TERN_F16 || rows < 0 || max_new < 1 ||
+      !kv8_strides_ok(ld, hd, a.dim))
+    return TERN_EINVAL;
+  if (rows == 0) return TERN_OK;
+  if (!k || !v) return TERN_EINVAL;
+  const int size = type == TERN_F32 ? 4 : 2;
+  if (!aligned16(k) || !aligned16(v) || ld * size % 16 != 0 || hd * size % 16 != 0)
+    return TERN_EALIGN;
+  DevState* d = nullptr;
+  rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  a.k = k;
+  a.v = v;
+  a.type = type;
+  a.ld = ld;
+  a.hd = hd;
+  a.rows = rows;
+  a.max_new = max_new < rows ? max_new : rows;
+  a.err = d->err;
+  int launches = 0;
+  if (launch_kv8_append(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
+    return TERN_ECUDA;
+  t_last_launches = launches;
+  return TERN_OK;
+}
+
+size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads, int kv_heads,
+                                          int head_dim) {
+  if (seqs < 1 || rows < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
+  return kSyncBytes + kv8_rows_partial_bytes(head_dim);
+}
+
+int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, long long ld,
+                       long long hd, int rows, int heads, int max_new, int window, int sinks,
+                       float softmax_scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  Kv8Args a;
+  int rc = kv8_args(cache, &a);
+  if (rc != TERN_OK) return rc;
+  if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
+      heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < 1 || window < 0 || sinks < 0 ||
+      !(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f) || !kv8_strides_ok(ld, hd, a.dim))
+    return TERN_EINVAL;
+  if (rows == 0) return TERN_OK;
+  if (!q || !out) return TERN_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ld % 8 != 0 || hd % 8 != 0)
+    return TERN_EALIGN;
+  if (!workspace || workspace_bytes < tern_kv8_attention_workspace_bytes(a.seqs, rows, heads,
+                                                                         a.hkv, a.dim))
+    return TERN_ENOSPACE;
+  if (!aligned16(workspace)) return TERN_EALIGN;
+  DevState* d = nullptr;
+  rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  a.q = q;
+  a.type = type;
+  a.ld = ld;
+  a.hd = hd;
+  a.rows = rows;
+  a.max_new = max_new < rows ? max_new : rows;
+  a.heads = heads;
+  a.group = heads / a.hkv;
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  a.tickets = static_cast<int*>(workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSyncBytes);
+  a.err = d->err;
+  CUtensorMap tm;
+  const uint64_t dim = static_cast<uint64_t>(a.dim);
+  rc = make_map_u8(&tm, a.codes, dim,
+                   static_cast<uint64_t>(a.pages) * 2 * a.hkv * TERN_KV8_BLOCK, dim,
+                   static_cast<uint32_t>(dim), kKvRowsBox,
+                   a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  if (rc != TERN_OK) return rc;
+  int launches = 0;
+  if (launch_kv8_rows(&tm, a, 1ll << 40, d->sms, static_cast<cudaStream_t>(stream), &launches) !=
+      cudaSuccess)
+    return TERN_ECUDA;
+  t_last_launches = launches;
+  return TERN_OK;
+}
+
 int tern_linear_small_t_noalloc(const uint32_t* Wpacked, const uint16_t* scales,
                                 const uint16_t* x, float* y, int T, int K, int N,
                                 void* stream) {
@@ -512,7 +717,7 @@ int tern_linear_small_t_noalloc(const uint32_t* Wpacked, const uint16_t* scales,
   rc = noalloc_scratch(&scratch);
   if (rc != TERN_OK) return rc;
   int launches = 0;
-  rc = run_small_t(d, rung, Wpacked, scales, x, y, T, K, N, scratch, small_t_act(c),
+  rc = run_small_t(d, rung, Wpacked, scales, x, {}, y, T, K, N, scratch, small_t_act(c),
                    static_cast<cudaStream_t>(stream), &launches);
   if (rc == TERN_OK) {
     t_last_rung = rung;
@@ -544,6 +749,7 @@ int tern_device_status(void* stream) {
   if (v) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return TERN_ECUDA;
+    if (!(v & kErrTimeout)) return TERN_EINDEX;
     // counters of an interrupted call may be left set in the no-alloc scratch
     int dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {

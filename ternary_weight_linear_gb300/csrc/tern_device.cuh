@@ -10,8 +10,9 @@
 namespace tern {
 
 // ---------------------------------------------------------------- error word
-// One int per device; kernels OR bits into it when a bounded wait runs out.
-enum : int { kErrTimeout = 1 };
+// One int per device; kernels OR bits into it when a bounded wait runs out or
+// an index array holds a value out of range.
+enum : int { kErrTimeout = 1, kErrIndex = 2 };
 
 // A wait gives up after this many nanoseconds of %globaltimer time.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

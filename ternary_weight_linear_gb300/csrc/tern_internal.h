@@ -42,13 +42,18 @@ cudaError_t smallt_set_attributes();
 // smallt_work_bytes(tt, K) bytes.  act: how the activations are staged
 // (kActExact: exact bf16 pieces; kActRotated: the same for the
 // Hadamard-rotated activations, K % 1024 == 0; kActInt8: per-token int8
-// codes, the s8 definition).  Adds the number of kernels launched to
+// codes, the s8 definition; kActCodes: the s8 definition on the caller's codes
+// and token scales, x unused).  Adds the number of kernels launched to
 // *launches.
-enum : int { kActExact = 0, kActRotated = 1, kActInt8 = 2 };
+enum : int { kActExact = 0, kActRotated = 1, kActInt8 = 2, kActCodes = 3 };
+struct ActCodes {
+  const int8_t* q = nullptr;       // [T][K]
+  const float* x_scale = nullptr;  // [T]
+};
 cudaError_t launch_smallt(int tt, const CUtensorMap* tmW, const uint32_t* Wp,
-                          const uint16_t* scales, const uint16_t* x, int* sync, uint8_t* work,
-                          float* y, int K, int N, int tok0, int Tt, int num_sms, int act,
-                          int* err, cudaStream_t stream, int* launches);
+                          const uint16_t* scales, const uint16_t* x, const ActCodes& codes,
+                          int* sync, uint8_t* work, float* y, int K, int N, int tok0, int Tt,
+                          int num_sms, int act, int* err, cudaStream_t stream, int* launches);
 
 // s8 rung: tiles of 128 weight rows x 128 tokens on tcgen05.
 constexpr int kS8TileN = 128;
@@ -146,6 +151,9 @@ cudaError_t launch_quant_s8(const uint16_t* x, int8_t* q, float* xs, int T, int 
 // K <= kRotateMaxK: the rotated row is staged in shared memory).
 cudaError_t launch_quant_pieces(const uint16_t* x, uint8_t* p1, uint8_t* p2, float* xs, int T,
                                 int K, int rotate, int num_sms, int* err, cudaStream_t stream);
+// The same pieces of the caller's codes, and a copy of its token scales.
+cudaError_t launch_code_pieces(const int8_t* q, const float* x_scale, uint8_t* p1, uint8_t* p2,
+                               float* xs, int T, int K, int num_sms, cudaStream_t stream);
 cudaError_t quant_set_attributes();
 
 // Base-3 packed weights (26 bytes per 128-weight group) -> 2-bit codes.
@@ -158,6 +166,63 @@ constexpr int kRotBlock = 1024;
 constexpr int kRotateMaxK = 65536;
 cudaError_t launch_rotate_bf16(const uint16_t* x, uint16_t* xr, int T, int K,
                                cudaStream_t stream);
+
+// Residual addition, root-mean-square norm and int8 codes of [T][K] rows;
+// see tern_add_rmsnorm_s8.  K <= kNormMaxK.
+constexpr int kNormMaxK = 32768;
+struct NormArgs {
+  const void* x;
+  long long x_ld;  // elements
+  int x_type;
+  const void* residual;  // may be null
+  void* residual_out;    // may be null
+  int residual_type;
+  const void* weight;
+  int weight_type;
+  float eps;
+  int8_t* q;       // may be null
+  float* x_scale;  // with q
+  uint16_t* y;     // may be null
+  int T, K;
+};
+cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, int num_sms, cudaStream_t stream);
+
+// The int8 cache (see tern_kv8_cache) and one call's rows.
+struct Kv8Args {
+  int8_t* codes;
+  float* scales;
+  const int* table;
+  const int* lens;
+  const int* starts;
+  int pages, seqs, width, hkv, dim;
+  int type;           // of q, or of k and v
+  long long ld, hd;   // row and head strides in elements
+  int rows, max_new;
+  // append
+  const void *k, *v;
+  // attention
+  const void* q;
+  int heads, group;  // query heads; query heads per key-value head
+  int window, sinks;
+  float scale_log2;  // softmax scale * log2(e)
+  void* out;
+  float* lse;
+  int* tickets;
+  float* partials;
+  int* err;
+};
+cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t stream, int* launches);
+
+// Attention of sequences with few query rows per key-value head.  tm: the
+// codes as bytes [pages * 2 * hkv * 64][dim], box dim x kKvRowsBox rows,
+// swizzle of the row's width.  Sequences with more than max_rows query rows
+// (new tokens * group) are left to the prompt kernel.
+constexpr int kKvRowsBox = 32;
+constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
+size_t kv8_rows_partial_bytes(int dim);
+cudaError_t kv8_rows_set_attributes();
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, long long max_rows,
+                            int num_sms, cudaStream_t stream, int* launches);
 
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier
 // phase nobody completes; 1: a device counter nobody raises) and records the

@@ -1,0 +1,114 @@
+// The int8 cache of keys and values as its kernels see it: arguments, checks
+// of the index arrays, and which pages a sequence's query rows see.
+#pragma once
+
+#include <stdint.h>
+
+#include "tern.h"
+#include "tern_device.cuh"
+#include "tern_internal.h"
+
+namespace tern {
+
+constexpr int kBlk = TERN_KV8_BLOCK;
+
+// A sequence of the batch.  ok: its entries are consistent.
+struct KvSeq {
+  int len, m, row0;  // tokens, new tokens, first row of q / k / v
+  bool ok;
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
+  KvSeq s;
+  s.len = a.lens[b];
+  s.row0 = a.starts[b];
+  const int end = a.starts[b + 1];
+  s.ok = s.row0 >= 0 && end >= s.row0 && end <= a.rows;
+  s.m = s.ok ? end - s.row0 : 0;
+  s.ok = s.ok && s.len >= 0 && (static_cast<long long>(s.len) + kBlk - 1) / kBlk <= a.width &&
+         s.m <= s.len && s.m <= a.max_new;
+  return s;
+}
+
+// The pages that query positions [p0, p1] see: [0, sinks) then [first, last].
+// Entry i of that list is page i or first + i - sinks.
+struct KvPages {
+  int sinks, first, count;
+  __device__ __forceinline__ int page(int i) const { return i < sinks ? i : first + i - sinks; }
+};
+
+__device__ __forceinline__ KvPages kv_pages(const Kv8Args& a, int p0, int p1) {
+  KvPages v;
+  v.first = 0;
+  v.sinks = 0;
+  if (a.window > 0 && p0 >= a.window) {
+    v.first = (p0 - a.window + 1) / kBlk;
+    const int s = a.sinks / kBlk + (a.sinks % kBlk != 0);
+    v.sinks = s < v.first ? s : v.first;
+  }
+  v.count = v.sinks + p1 / kBlk - v.first + 1;
+  return v;
+}
+
+// Whether the row at position p sees token j.
+__device__ __forceinline__ bool kv_sees(const Kv8Args& a, int p, int j) {
+  return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+}
+
+// Whether any row at positions [p0, p1] sees one of the tokens [j0, j1].
+__device__ __forceinline__ bool kv_any(const Kv8Args& a, int p0, int p1, int j0, int j1) {
+  return j0 <= p1 && (a.window == 0 || j1 > p0 - a.window || j0 < a.sinks);
+}
+
+// Whether every row at positions [p0, p1] sees all tokens [j0, j1].
+__device__ __forceinline__ bool kv_all(const Kv8Args& a, int p0, int p1, int j0, int j1) {
+  return j1 <= p0 && (a.window == 0 || j0 > p1 - a.window || j1 < a.sinks);
+}
+
+// A value scale as 2^e * f, f in [1, 2): the codes take 2^e (exactly, in
+// fp16, relative to a running exponent) and the weights take f.  A scale that
+// is not finite keeps out of the exponents and makes f NaN, so that exactly
+// the rows that see its block get NaN; 0 (whose codes are 0) and subnormals
+// count as 2^-127.
+struct VScale {
+  int e;
+  float f;
+};
+__device__ __forceinline__ VScale split_vscale(float s) {
+  const uint32_t u = __float_as_uint(s);
+  const int ex = (u >> 23) & 0xFF;
+  VScale v;
+  if (ex == 255) {
+    v.e = -127;
+    v.f = __uint_as_float(0x7FC00000u);
+  } else if (ex == 0) {
+    v.e = -127;
+    v.f = 1.f;
+  } else {
+    v.e = ex - 127;
+    v.f = __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four int8 codes of a word as fp16 pairs (bytes 0, 1) and (2, 3), exactly:
+// code + 128 in the low mantissa bits of 1024, less 1152.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+// 2^k as an fp16 bit pattern for k <= 0 (0 below the smallest subnormal).
+__device__ __forceinline__ uint32_t half_pow2(int k) {
+  return k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : (k >= -24 ? 1u << (k + 24) : 0u);
+}
+
+}  // namespace tern

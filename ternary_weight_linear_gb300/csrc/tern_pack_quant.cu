@@ -5,6 +5,7 @@
 // tern_rotate_bf16: blockwise Hadamard rotation of bf16 activations.
 #include "tern_device.cuh"
 #include "tern_internal.h"
+#include "tern_quant.cuh"
 
 #include <cuda_fp8.h>
 
@@ -54,29 +55,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const int8_t* __restrict__ W,
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// Per-token code of v: rint(v / scale) clamped to [-127, 127], the quotient
-// rounded as one IEEE single-precision division (nearest-even, as rint).
-// Without a division per element: with inv = 1 / scale rounded, q0 = v * inv
-// differs from v / scale by less than 128 * (2^-23 + 2^-48) < 1.53e-5 (|v| <=
-// absmax, so |v / scale| < 128; two roundings of relative error 2^-24 each),
-// and the rounded quotient from v / scale by at most half an ulp below 128,
-// 2^-18; so the two are less than kQMargin = 2^-15 apart.  When q0 lies
-// farther than kQMargin from every half-integer, both fall strictly inside
-// the same rounding interval and rint(q0) is the code; otherwise the element
-// takes the division.  fast: scale and 1 / scale normal (absmax >= 127 *
-// 2^-126), where those relative bounds hold; else every element divides.
-constexpr float kQMargin = 3.0517578125e-05f;  // 2^-15
-__device__ __forceinline__ float quant_code(float v, float scale, float inv, bool fast) {
-  float r;
-  if (fast) {
-    const float q0 = v * inv;
-    r = rintf(q0);
-    if (!(fabsf(q0 - r) < 0.5f - kQMargin)) r = rintf(v / scale);
-  } else {
-    r = rintf(v / scale);
-  }
-  return fminf(fmaxf(r, -127.f), 127.f);
-}
 // Pairs of fp32 values in one 64-bit register for the packed fp32x2
 // arithmetic (each half rounded as its scalar instruction would be).
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
@@ -107,9 +85,6 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
-}
-__device__ __forceinline__ bool quant_fast(float scale) {
-  return scale >= 1.1754943508222875e-38f && scale < 8.507059173023462e+37f;  // [2^-126, 2^126)
 }
 
 // One CTA per token.  Pass 1: absmax.  Pass 2: codes.
@@ -156,6 +131,42 @@ __global__ void __launch_bounds__(kQThreads) quant_s8_kernel(const uint16_t* __r
     }
     *reinterpret_cast<uint2*>(qrow + 8 * c) = make_uint2(out[0], out[1]);
   }
+}
+
+// The two e4m3 pieces of a 16-wide block of codes r (exact integers as
+// floats, -128..127), stored at d1 and d2 in the decoder's k order.
+__device__ __forceinline__ void store_pieces(const float (&r)[16], uint8_t* d1, uint8_t* d2) {
+  // pieces of the codes as exact floats, two at a time: p1 = 16 rint(q /
+  // 16) (q / 16 + 1.5 * 2^23 rounds to an integer, ties to even), p2 = q -
+  // p1 in [-8, 8]; every step is exact in fp32
+  float f1[16], f2[16];
+  const uint64_t c16th = pack_f32x2(0.0625f, 0.0625f), cbig = pack_f32x2(12582912.f, 12582912.f);
+  const uint64_t c16 = pack_f32x2(16.f, 16.f), cneg = pack_f32x2(-201326592.f, -201326592.f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint64_t r2 = pack_f32x2(r[2 * j], r[2 * j + 1]);
+    const uint64_t p12 = fma_f32x2(fma_f32x2(r2, c16th, cbig), c16, cneg);
+    unpack_f32x2(p12, f1[2 * j], f1[2 * j + 1]);
+    unpack_f32x2(sub_f32x2(r2, p12), f2[2 * j], f2[2 * j + 1]);
+  }
+  // word i of a piece block holds k = i, i + 4, i + 8, i + 12 in bytes 0..3
+  // (slot 4i + b holds k = 4b + i), converted two at a time
+  uint32_t o1[4], o2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o1[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f1[i], f1[i + 4]),
+                                                           __NV_SATFINITE, __NV_E4M3)) |
+            (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f1[i + 8], f1[i + 12]),
+                                                            __NV_SATFINITE, __NV_E4M3))
+             << 16);
+    o2[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f2[i], f2[i + 4]),
+                                                           __NV_SATFINITE, __NV_E4M3)) |
+            (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f2[i + 8], f2[i + 12]),
+                                                            __NV_SATFINITE, __NV_E4M3))
+             << 16);
+  }
+  *reinterpret_cast<uint4*>(d1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+  *reinterpret_cast<uint4*>(d2) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
 }
 
 // s8 rung input: the codes q of quant_s8_kernel (same arithmetic), split
@@ -223,38 +234,8 @@ __device__ __forceinline__ void quant_row_pieces(const uint16_t* row, int t, int
                                     inv, false)
                        : 0.f;
     }
-    // pieces of the codes as exact floats, two at a time: p1 = 16 rint(q /
-    // 16) (q / 16 + 1.5 * 2^23 rounds to an integer, ties to even), p2 = q -
-    // p1 in [-8, 8]; every step is exact in fp32
-    float f1[16], f2[16];
-    const uint64_t c16th = pack_f32x2(0.0625f, 0.0625f), cbig = pack_f32x2(12582912.f, 12582912.f);
-    const uint64_t c16 = pack_f32x2(16.f, 16.f), cneg = pack_f32x2(-201326592.f, -201326592.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint64_t r2 = pack_f32x2(r[2 * j], r[2 * j + 1]);
-      const uint64_t p12 = fma_f32x2(fma_f32x2(r2, c16th, cbig), c16, cneg);
-      unpack_f32x2(p12, f1[2 * j], f1[2 * j + 1]);
-      unpack_f32x2(sub_f32x2(r2, p12), f2[2 * j], f2[2 * j + 1]);
-    }
-    // word i of a piece block holds k = i, i + 4, i + 8, i + 12 in bytes 0..3
-    // (slot 4i + b holds k = 4b + i), converted two at a time
-    uint32_t o1[4], o2[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o1[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f1[i], f1[i + 4]),
-                                                             __NV_SATFINITE, __NV_E4M3)) |
-              (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f1[i + 8], f1[i + 12]),
-                                                              __NV_SATFINITE, __NV_E4M3))
-               << 16);
-      o2[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f2[i], f2[i + 4]),
-                                                             __NV_SATFINITE, __NV_E4M3)) |
-              (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f2[i + 8], f2[i + 12]),
-                                                              __NV_SATFINITE, __NV_E4M3))
-               << 16);
-    }
     const size_t off = static_cast<size_t>(t) * K + 16 * blk;
-    *reinterpret_cast<uint4*>(p1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    *reinterpret_cast<uint4*>(p2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    store_pieces(r, p1 + off, p2 + off);
   }
 }
 
@@ -358,6 +339,31 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t*
       fence_proxy_async_smem();
       issue(tn, 0);
     }
+  }
+}
+
+// The pieces of codes that the caller already has (tern_linear_s8), and the
+// token scales beside them: the main kernel copies x_scale in whole 16-byte
+// chunks, past T if T is not a multiple of four, so it reads the workspace's
+// padded copy and not the caller's array.  One thread per 16 codes: 16 bytes
+// in, 32 out, bound by HBM (or L2, where the codes have just been written).
+constexpr int kCodeThreads = 256;
+__global__ void __launch_bounds__(kCodeThreads) code_pieces_kernel(
+    const int8_t* __restrict__ q, const float* __restrict__ x_scale, uint8_t* __restrict__ p1,
+    uint8_t* __restrict__ p2, float* __restrict__ xs, int T, long long blocks) {
+  grid_dependents_launch();
+  grid_dependency_wait();  // the codes and the output buffers come from earlier work
+  const long long first = static_cast<long long>(blockIdx.x) * kCodeThreads + threadIdx.x;
+  const long long stride = static_cast<long long>(gridDim.x) * kCodeThreads;
+  for (long long t = first; t < T; t += stride) xs[t] = x_scale[t];
+  for (long long i = first; i < blocks; i += stride) {
+    const uint4 v = *reinterpret_cast<const uint4*>(q + 16 * i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float r[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      r[k] = static_cast<float>(static_cast<int8_t>((w[k >> 2] >> (8 * (k & 3))) & 0xFFu));
+    store_pieces(r, p1 + 16 * i, p2 + 16 * i);
   }
 }
 
@@ -521,6 +527,18 @@ cudaError_t launch_quant_s8(const uint16_t* x, int8_t* q, float* xs, int T, int 
                             cudaStream_t stream) {
   quant_s8_kernel<<<T, kQThreads, 0, stream>>>(x, q, xs, K);
   return cudaGetLastError();
+}
+
+cudaError_t launch_code_pieces(const int8_t* q, const float* x_scale, uint8_t* p1, uint8_t* p2,
+                               float* xs, int T, int K, int num_sms, cudaStream_t stream) {
+  const long long blocks = static_cast<long long>(T) * (K / 16);
+  long long grid = (blocks + kCodeThreads - 1) / kCodeThreads;
+  const long long cap = static_cast<long long>(num_sms) * 8;
+  if (grid > cap) grid = cap;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)), dim3(kCodeThreads), 0, stream);
+  return cudaLaunchKernelEx(&cfg, code_pieces_kernel, q, x_scale, p1, p2, xs, T, blocks);
 }
 
 cudaError_t quant_set_attributes() {

@@ -544,6 +544,48 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_i8_kernel(
   }
 }
 
+// int8 activations that the caller already has as codes q and token scales xs
+// (tern_linear_s8): the blocks of xprep_i8_kernel without its quantiser, one
+// warp per (token slot, group).  The factor's sign bit marks a group with
+// leftovers (which the main kernel would read from bf16 x), so it stays
+// clear: a negative xs is carried by the pieces.
+template <int TT>
+__global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_codes_kernel(
+    const int8_t* __restrict__ q, const float* __restrict__ x_scale, uint8_t* __restrict__ out,
+    int K, int tok0, int Tt, int KS) {
+  grid_dependents_launch();
+  grid_dependency_wait();  // q (and this buffer's last reader) come from earlier work
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = kGS * KS;
+  const int tasks = TC<TT>::kH * groups;
+  for (int task = blockIdx.x * kPrepWarps + warp; task < tasks; task += gridDim.x * kPrepWarps) {
+    const int t = task / groups, gi = task % groups;
+    const int kbase = gi * 128 + 4 * lane;
+    uint32_t raw = 0;
+    float xs = 0.f;
+    if (t < Tt) {
+      xs = x_scale[tok0 + t];
+      if (kbase < K)
+        raw = *reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(tok0 + t) * K + kbase);
+    }
+    const int sign = signbit(xs) ? -1 : 1;
+    uint32_t hp[3] = {0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = sign * static_cast<int8_t>((raw >> (8 * i)) & 0xFFu);
+      const int h = (c + 8) >> 4;  // floor((c + 8) / 16), in [-8, 8]
+      hp[0] |= static_cast<uint32_t>(
+                   __nv_cvt_float_to_fp8(static_cast<float>(16 * h), __NV_SATFINITE, __NV_E5M2))
+               << (8 * i);
+      hp[1] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(static_cast<float>(c - 16 * h),
+                                                           __NV_SATFINITE, __NV_E5M2))
+               << (8 * i);
+    }
+    prep_write<TT>(hp, 8.0f * fabsf(xs), 0.f, out + static_cast<size_t>(gi / kGS) * TC<TT>::kXBytes,
+                   t, gi % kGS, lane);
+  }
+}
+
 // Rotated activations (the Hadamard rotation of every 1024-wide block, fused
 // into the staging): one warp per (token slot, stage), the stage being one
 // rotation block.  The warp loads the block with lane l holding elements
@@ -1661,9 +1703,9 @@ int t1_slots(const SmallTGrid& g) {
 
 template <int TT>
 cudaError_t launch_tt(const CUtensorMap* tmW, const uint32_t* Wp, const uint16_t* scales,
-                      const uint16_t* x, int* sync, uint8_t* work, float* y, int K, int N,
-                      int tok0, int Tt, int num_sms, int act, int* err, cudaStream_t stream,
-                      int* launches) {
+                      const uint16_t* x, const ActCodes& codes, int* sync, uint8_t* work,
+                      float* y, int K, int N, int tok0, int Tt, int num_sms, int act, int* err,
+                      cudaStream_t stream, int* launches) {
   const bool rotate = act == kActRotated;
   using C = TC<TT>;
   const SmallTGrid g = smallt_grid(K, N, num_sms, TT);
@@ -1679,7 +1721,16 @@ cudaError_t launch_tt(const CUtensorMap* tmW, const uint32_t* Wp, const uint16_t
   // its weight stream).
   const int build_x = C::kInKernelX && act == kActExact && max_units_per_cta(g) <= 2 ? 1 : 0;
   cudaLaunchAttribute attr[1];
-  if (act == kActInt8) {
+  if (act == kActCodes) {
+    const int tasks = C::kH * kGS * g.KS;
+    int blocks = (tasks + kPrepWarps - 1) / kPrepWarps;
+    if (blocks > num_sms) blocks = num_sms;
+    cudaLaunchConfig_t pc = pdl_config(attr, dim3(blocks), dim3(kPrepWarps * 32), 0, stream);
+    cudaError_t e = cudaLaunchKernelEx(&pc, xprep_codes_kernel<TT>, codes.q, codes.x_scale, xprep,
+                                       K, tok0, Tt, g.KS);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  } else if (act == kActInt8) {
     // one 4-warp CTA per (token slot, stage)
     const int tasks = C::kH * g.KS;
     const int blocks = tasks < num_sms ? tasks : num_sms;
@@ -1756,22 +1807,22 @@ cudaError_t smallt_set_attributes() {
 }
 
 cudaError_t launch_smallt(int tt, const CUtensorMap* tmW, const uint32_t* Wp,
-                          const uint16_t* scales, const uint16_t* x, int* sync, uint8_t* work,
-                          float* y, int K, int N, int tok0, int Tt, int num_sms, int act,
-                          int* err, cudaStream_t stream, int* launches) {
+                          const uint16_t* scales, const uint16_t* x, const ActCodes& codes, int* sync,
+                          uint8_t* work, float* y, int K, int N, int tok0, int Tt, int num_sms,
+                          int act, int* err, cudaStream_t stream, int* launches) {
   switch (tt) {
     case 1:
-      return launch_tt<1>(tmW, Wp, scales, x, sync, work, y, K, N, tok0, Tt, num_sms, act, err,
-                          stream, launches);
+      return launch_tt<1>(tmW, Wp, scales, x, codes, sync, work, y, K, N, tok0, Tt, num_sms, act,
+                          err, stream, launches);
     case 4:
-      return launch_tt<4>(tmW, Wp, scales, x, sync, work, y, K, N, tok0, Tt, num_sms, act, err,
-                          stream, launches);
+      return launch_tt<4>(tmW, Wp, scales, x, codes, sync, work, y, K, N, tok0, Tt, num_sms, act,
+                          err, stream, launches);
     case 8:
-      return launch_tt<8>(tmW, Wp, scales, x, sync, work, y, K, N, tok0, Tt, num_sms, act, err,
-                          stream, launches);
+      return launch_tt<8>(tmW, Wp, scales, x, codes, sync, work, y, K, N, tok0, Tt, num_sms, act,
+                          err, stream, launches);
     default:
-      return launch_tt<16>(tmW, Wp, scales, x, sync, work, y, K, N, tok0, Tt, num_sms, act,
-                           err, stream, launches);
+      return launch_tt<16>(tmW, Wp, scales, x, codes, sync, work, y, K, N, tok0, Tt, num_sms, act,
+                          err, stream, launches);
   }
 }
 
