@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libtern.so")
 SOURCES = ["tern_api.cu", "tern_pack_quant.cu", "tern_smallt.cu", "tern_s8.cu", "tern_bf16.cu",
-           "tern_norm.cu", "tern_kv8_append.cu", "tern_kv8_rows.cu", "tern_selftest.cu"]
+           "tern_norm.cu", "tern_kv8_append.cu", "tern_kv8_rows.cu", "tern_kv8_prompt.cu",
+           "tern_selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-I" + os.path.join(HERE, "..", "include"), "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
            "-Xptxas", "-warn-spills"]

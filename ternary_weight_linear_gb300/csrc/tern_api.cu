@@ -156,6 +156,7 @@ int device_state(DevState** out) {
     if (quant_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (bf16_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (kv8_rows_set_attributes() != cudaSuccess) return TERN_ECUDA;
+    if (kv8_prompt_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (!g_encode) {
       cudaDriverEntryPointQueryResult q;
       void* fn = nullptr;
@@ -323,6 +324,10 @@ int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
   a->dim = c->head_dim;
   return TERN_OK;
 }
+
+// Query rows per key-value head (new tokens times group) up to which a
+// sequence takes the few-row kernel: two of its 16-row tiles.
+constexpr int kKvFewRows = 32;
 
 // Strides of a [rows][heads][dim] operand: rows and heads start on 16 bytes
 // and a head's elements are consecutive.
@@ -641,7 +646,10 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads, int kv_
   if (seqs < 1 || rows < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return kSyncBytes + kv8_rows_partial_bytes(head_dim);
+  size_t n = kSyncBytes + kv8_rows_partial_bytes(head_dim);
+  if (static_cast<long long>(rows) * (heads / kv_heads) > kKvFewRows)
+    n += kv8_prompt_partial_bytes(head_dim);
+  return n;
 }
 
 int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, long long ld,
@@ -674,8 +682,10 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   a.max_new = max_new < rows ? max_new : rows;
   a.heads = heads;
   a.group = heads / a.hkv;
-  a.window = window;
-  a.sinks = window > 0 ? sinks : 0;
+  // a window of every token that the table can hold is none
+  const int most_tokens = a.width * TERN_KV8_BLOCK;
+  a.window = window < most_tokens ? window : 0;
+  a.sinks = a.window > 0 ? (sinks < most_tokens ? sinks : most_tokens) : 0;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = out;
   a.lse = lse;
@@ -690,9 +700,22 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
                    a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc != TERN_OK) return rc;
   int launches = 0;
-  if (launch_kv8_rows(&tm, a, 1ll << 40, d->sms, static_cast<cudaStream_t>(stream), &launches) !=
-      cudaSuccess)
-    return TERN_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Each sequence goes by its own rows: up to kKvFewRows per key-value head to
+  // the kernel that is bound by the cache's bytes, more to the one on the
+  // tensor cores.  A single sequence takes one launch, of the latter where
+  // max_new allows more than the former takes.
+  const bool many = static_cast<long long>(a.max_new) * a.group > kKvFewRows;
+  if (!many || a.seqs > 1) {
+    if (launch_kv8_rows(&tm, a, kKvFewRows, d->sms, st, &launches) != cudaSuccess)
+      return TERN_ECUDA;
+  }
+  if (many) {
+    if (launch_kv8_prompt(a, a.seqs > 1 ? kKvFewRows + 1 : 1,
+                          a.partials + kv8_rows_partial_bytes(a.dim) / sizeof(float),
+                          a.tickets + 512, d->sms, st, &launches) != cudaSuccess)
+      return TERN_ECUDA;
+  }
   t_last_launches = launches;
   return TERN_OK;
 }

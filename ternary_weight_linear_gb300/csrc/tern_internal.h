@@ -224,6 +224,13 @@ cudaError_t kv8_rows_set_attributes();
 cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, long long max_rows,
                             int num_sms, cudaStream_t stream, int* launches);
 
+// Attention of sequences with at least min_rows query rows per key-value
+// head, on the tensor cores.  tickets: kSmallTMaxCtas zeroed ints.
+size_t kv8_prompt_partial_bytes(int dim);
+cudaError_t kv8_prompt_set_attributes();
+cudaError_t launch_kv8_prompt(const Kv8Args& a, long long min_rows, float* partials, int* tickets,
+                              int num_sms, cudaStream_t stream, int* launches);
+
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier
 // phase nobody completes; 1: a device counter nobody raises) and records the
 // timeout in *err.

@@ -1,0 +1,739 @@
+// tern_kv8_attention for sequences with many query rows per key-value head
+// (prompt chunks): bound by the tensor cores.
+//
+// The rows of a sequence that share a key-value head (row r = new token
+// r / group, head r % group) are cut into blocks of 256, two tiles of 128 that
+// share every key and value tile of 128 tokens (two pages).  Per tile pair,
+// with tcgen05 kind::f16 (fp16 operands, fp32 accumulators in TMEM):
+//   S = Q Kc^T,  s = S * (softmax_scale * log2(e) * k_scale * 2^-a(row))
+//   P = 2^(s + log2 f - ref + 10),  O += P (2^(e - E) Vc),  l += P / f
+// with Q scaled by 2^a per row into fp16, Kc and Vc the int8 codes (exact in
+// fp16), v_scale = 2^e f and E the largest e so far.  ref is the row's running
+// maximum, raised (and O rescaled) only when a score passes it by 2^4: P stays
+// below 2^15 (fp16 ends at 65504) and its range below is 2^-34 of that
+// reference, so a weight is lost only where it is that much smaller.
+//
+// There is no int8 tcgen05 on sm_103a, so four warps turn each tile of codes
+// into fp16 in shared memory, once for the two query tiles: 2 * 128 * 128
+// elements at 1.25 instructions against the 2048 cycles that the tile pair's
+// four 128^3 products take.
+//
+// Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (S read
+// from TMEM twice, for the maximum and for the weights; P written over S);
+// 8-11 the conversion; 12 the MMAs (one thread), in the order
+//   PV0(j), S0(j+1), PV1(j), S1(j+1),
+// so that one tile's softmax runs under the other's products; 13 the copies
+// (one thread, a page of a head is one contiguous block).  The MMAs of a CTA
+// run in the order of their issue, so S(j+1) may follow the PV(j) that reads
+// the same columns.
+// Work: one CTA per (block of rows, sequence, head, part of the keys), the
+// longest rows first.  When there are too few blocks for the SMs the keys are
+// cut into parts, whose (max, sum, O) go to the workspace, and the last CTA of
+// a block adds them in order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tern_kv8.cuh"
+
+namespace tern {
+namespace {
+
+constexpr int kPRows = 128;  // rows of a query tile
+constexpr int kKeys = 128;   // tokens of a key tile: two pages
+constexpr int kSoftW = 8, kConvW = 4;
+constexpr int kMmaW = kSoftW + kConvW, kCopyW = kMmaW + 1;
+constexpr int kPThreads = (kCopyW + 1) * 32;
+constexpr int kPRecs = 512;  // page records held at a time
+constexpr int kPConv = 3;    // converted tiles
+constexpr float kPOff = 10.f, kPLazy = 4.f;
+
+template <int D>
+struct PL {
+  static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
+  static constexpr int kBlockB = kPRows * 128;        // 16 KB
+  static constexpr int kTileB = kBlocks * kBlockB;    // an fp16 tile
+  static constexpr int kRawB = kKeys * D;             // a tile of codes
+  static constexpr int kRaw = D == 128 ? 3 : 4;       // tiles of codes in flight
+  static constexpr int kQOff = 0;
+  static constexpr int kConvOff = kQOff + 2 * kTileB;
+  static constexpr int kRawOff = kConvOff + kPConv * kTileB;
+  static constexpr int kRecOff = kRawOff + kRaw * kRawB;  // page, e, ks, log2 f, 1 / f
+  static constexpr int kBarOff = kRecOff + kPRecs * 20;
+  static constexpr int kNumBars = 2 * kRaw + 2 * kPConv + 6 + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, emax[2], last
+  static constexpr int kBytes = kMiscOff + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kSCol = 0, kOCol = 256;
+  static_assert(kBarOff % 8 == 0, "alignment");
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+
+// 128-byte swizzled operand: rows of 128 bytes, 8-row atoms 1024 bytes apart.
+// K-major (rows are M or N) and MN-major (rows are K, 64 elements of N wide,
+// the next 64 a block further) share the bytes; lbo is the block stride of the
+// latter.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// All threads of the CTA, from any role.
+__device__ __forceinline__ void cta_barrier() {
+  asm volatile("bar.sync 0;" ::: "memory");
+}
+// The softmax warps.
+__device__ __forceinline__ void softmax_barrier() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+    kv8_prompt_kernel(const Kv8Args a, long long min_rows, int row_blocks, int parts,
+                      float* partials, int* tickets) {
+  using L = PL<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* raw_empty = raw_full + L::kRaw;
+  uint64_t* conv_full = raw_empty + L::kRaw;
+  uint64_t* conv_empty = conv_full + kPConv;
+  uint64_t* s_full = conv_empty + kPConv;  // [2] scores of a query tile
+  uint64_t* p_full = s_full + 2;           // [2] its weights, O rescaled
+  uint64_t* o_done = p_full + 2;           // [2] its O holds the tile
+  uint64_t* mma_end = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  int* emax = reinterpret_cast<int*>(tmem_slot + 1);  // [2] by chunk parity
+  int* is_last = emax + 2;
+  int* rec_page = reinterpret_cast<int*>(smem + L::kRecOff);
+  int* rec_e = rec_page + kPRecs;
+  float* rec_ks = reinterpret_cast<float*>(rec_e + kPRecs);
+  float* rec_lf = rec_ks + kPRecs;
+  float* rec_rf = rec_lf + kPRecs;
+
+  grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
+
+  // ---- this CTA's block of rows, sequence, head and part; late rows first
+  const int part = blockIdx.x % parts;
+  const int item = blockIdx.x / parts;
+  const int hk = item % a.hkv;
+  const int b = (item / a.hkv) % a.seqs;
+  const int rb = row_blocks - 1 - item / a.hkv / a.seqs;
+  const KvSeq sq = kv_seq(a, b);
+  const long long R = static_cast<long long>(sq.m) * a.group;
+  const long long r0 = static_cast<long long>(rb) * (2 * kPRows);
+  if (!sq.ok && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+  if (!sq.ok || R < min_rows || r0 >= R) return;
+  const int rows = R - r0 < 2 * kPRows ? static_cast<int>(R - r0) : 2 * kPRows;
+  const int tiles_q = rows > kPRows ? 2 : 1;
+  const int p_base = sq.len - sq.m;
+  const int p_first = p_base + static_cast<int>(r0 / a.group);
+  const int p_last = p_base + static_cast<int>((r0 + rows - 1) / a.group);
+  const KvPages pages = kv_pages(a, p_first, p_last);
+  const int all_tiles = (pages.count + 1) / 2;
+  const int t_begin = static_cast<int>(static_cast<long long>(all_tiles) * part / parts);
+  const int t_end = static_cast<int>(static_cast<long long>(all_tiles) * (part + 1) / parts);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kConvW);
+    }
+    for (int s = 0; s < kPConv; ++s) {
+      mbar_init(&conv_full[s], kConvW);
+      mbar_init(&conv_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+      emax[i] = -127;
+    }
+    mbar_init(mma_end, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  cta_barrier();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  // only now: a dependent kernel's CTA that took this SM's TMEM first would
+  // hold it until this grid ends
+  grid_dependents_launch();
+
+  // ---- softmax warps: a row per thread
+  const int qt = warp >> 2;  // query tile (softmax warps)
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const int tr = (warp & 3) * 32 + lane;  // row of the tile
+  const int r = qt * kPRows + tr;         // row of the block
+  const bool live = warp < kSoftW && r < rows;
+  long long qrow = 0;
+  int qhead = 0, pos = -1;
+  float cs = 0.f;
+  if (warp < kSoftW && qt < tiles_q) {
+    if (live) {
+      const long long rr = r0 + r;
+      const int tok = static_cast<int>(rr / a.group);
+      qrow = sq.row0 + tok;
+      qhead = hk * a.group + static_cast<int>(rr % a.group);
+      pos = p_base + tok;
+    }
+    // the row scaled by a power of two into fp16, largest element in
+    // [2^14, 2^15)
+    uint32_t w[D / 2];
+    float big = 0.f;
+    const uint4* src =
+        reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qrow * a.ld +
+                                       static_cast<long long>(qhead) * a.hd);
+    auto lo_of = [&](uint32_t v) {
+      return a.type == TERN_BF16 ? __uint_as_float(v << 16)
+                                 : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
+    };
+    auto hi_of = [&](uint32_t v) {
+      return a.type == TERN_BF16 ? __uint_as_float(v & 0xFFFF0000u)
+                                 : __half2float(__ushort_as_half(static_cast<uint16_t>(v >> 16)));
+    };
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 v = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 2; ++c) big = fmaxf(big, fmaxf(fabsf(lo_of(w[c])), fabsf(hi_of(w[c]))));
+    int ex = static_cast<int>((__float_as_uint(big) >> 23) & 0xFF) - 127;
+    if (big == 0.f) ex = 14;
+    const int up = 14 - ex;
+    const float up1 = __uint_as_float(static_cast<uint32_t>(up / 2 + 127) << 23);
+    const float up2 = __uint_as_float(static_cast<uint32_t>(up - up / 2 + 127) << 23);
+    cs = a.scale_log2 / up1 / up2;
+    uint8_t* dst = smem + L::kQOff + qt * L::kTileB + tr * 128;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        h[e] = half2_bits(lo_of(w[4 * c + e]) * up1 * up2, hi_of(w[4 * c + e]) * up1 * up2);
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kBlockB + (((c & 7) ^ (tr & 7)) << 4)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    fence_proxy_async_smem();
+  }
+  // positions of this thread's query tile, for the tests of whole pages
+  const int i_first = qt * kPRows < rows ? p_base + static_cast<int>((r0 + qt * kPRows) / a.group)
+                                         : 0;
+  const int i_last = static_cast<int>(
+      (r0 + (rows < (qt + 1) * kPRows ? rows : (qt + 1) * kPRows) - 1) / a.group) + p_base;
+
+  int E = -127;
+  float ref = -INFINITY, sum = 0.f;
+  bool ok = true;
+  int jt = 0;             // key tiles so far
+  unsigned n_raw = 0;     // (copies, conversion) tiles of codes so far
+  unsigned n_conv = 0;    // (MMA) converted tiles used
+  unsigned n_issued = 0;  // (copies) tiles requested
+
+  for (int t0 = t_begin, chunk = 0; t0 < t_end; t0 += kPRecs / 2, ++chunk) {
+    const int t1 = t_end < t0 + kPRecs / 2 ? t_end : t0 + kPRecs / 2;
+    // ---- records of the pages of tiles [t0, t1)
+    cta_barrier();  // the records of the chunk before have been used
+    for (int i = threadIdx.x; i < 2 * (t1 - t0); i += kPThreads) {
+      const int li = 2 * t0 + i;
+      int page = -1, e = -127;
+      if (li < pages.count) {
+        page = a.table[static_cast<size_t>(b) * a.width + pages.page(li)];
+        if (page < 0 || page >= a.pages) {
+          atomicOr(a.err, kErrIndex);
+          page = -1;
+        } else {
+          const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
+          const VScale v = split_vscale(sc[a.hkv]);
+          rec_ks[i] = sc[0];
+          rec_lf[i] = log2f(v.f);
+          rec_rf[i] = 1.0f / v.f;
+          e = v.e;
+          atomicMax(&emax[chunk & 1], e);
+        }
+      }
+      rec_page[i] = page;
+      rec_e[i] = e;
+    }
+    if (threadIdx.x == 0) emax[(chunk & 1) ^ 1] = -127;
+    cta_barrier();
+    const int En = emax[chunk & 1] > E ? emax[chunk & 1] : E;
+
+    if (warp == kCopyW) {
+      // ---------------------------------------------------------- copies
+      if (lane == 0 && ok) {
+        for (int u = 2 * t0; u < 2 * t1 && ok; ++u, ++n_issued) {
+          // tile u / 2, keys then values
+          const int s = n_issued % L::kRaw;
+          if (n_issued >= L::kRaw &&
+              !mbar_wait(&raw_empty[s], ((n_issued / L::kRaw) & 1) ^ 1, a.err)) {
+            ok = false;
+            break;
+          }
+          const int i = 2 * ((u >> 1) - t0);
+          uint32_t bytes = 0;
+          for (int h = 0; h < 2; ++h)
+            if (rec_page[i + h] >= 0) bytes += kBlk * D;
+          mbar_arrive_expect_tx(&raw_full[s], bytes);
+          for (int h = 0; h < 2; ++h)
+            if (rec_page[i + h] >= 0)
+              bulk_load(smem + L::kRawOff + s * L::kRawB + h * (kBlk * D),
+                        a.codes + ((static_cast<size_t>(rec_page[i + h]) * 2 + (u & 1)) * a.hkv +
+                                   hk) * (kBlk * D),
+                        kBlk * D, &raw_full[s]);
+        }
+      }
+    } else if (warp == kMmaW) {
+      // ---------------------------------------------------------- MMAs
+      if (lane == 0 && ok) {
+        constexpr uint32_t idesc_s = idesc_f16_f32(kPRows, kKeys, false);
+        constexpr uint32_t idesc_o = idesc_f16_f32(kPRows, D, true);
+        const uint64_t dq = desc_sw128(smem_addr(smem + L::kQOff), 16);
+        const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
+        auto scores = [&](int i, unsigned n) {  // S_i = Q_i K^T, keys in converted tile n
+          const uint64_t q = dq + static_cast<uint64_t>((i * L::kTileB) >> 4);
+          const uint64_t k = dc + static_cast<uint64_t>(((n % kPConv) * L::kTileB) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4);
+            mma_ss(tbase + L::kSCol + i * kKeys, q + o, k + o, idesc_s, kk != 0);
+          }
+          mma_commit(&s_full[i]);
+        };
+        auto values = [&](int i, unsigned n, bool first) {  // O_i += P_i V
+          const uint64_t v = dc + static_cast<uint64_t>(((n % kPConv) * L::kTileB) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(tbase + L::kOCol + i * 128, tbase + L::kSCol + i * kKeys + kk * 8,
+                   v + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o, !(first && kk == 0));
+          mma_commit(&o_done[i]);
+        };
+        auto wait_conv = [&](unsigned n) {
+          return mbar_wait(&conv_full[n % kPConv], (n / kPConv) & 1, a.err);
+        };
+        // the chunk's first scores
+        ok = wait_conv(n_conv);
+        tc_fence_after();
+        if (ok) {
+          for (int i = 0; i < tiles_q; ++i) scores(i, n_conv);
+          mma_commit(&conv_empty[n_conv % kPConv]);
+        }
+        ++n_conv;
+        int j = jt;
+        for (int tt = t0; tt < t1 && ok; ++tt, ++j) {
+          const unsigned nv = n_conv, nk = n_conv + 1;
+          const bool more = tt + 1 < t1;
+          ok = wait_conv(nv);
+          for (int i = 0; i < tiles_q && ok; ++i) {
+            ok = mbar_wait(&p_full[i], j & 1, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            values(i, nv, j == 0);
+            if (i == tiles_q - 1) mma_commit(&conv_empty[nv % kPConv]);
+            if (more) {
+              if (i == 0) ok = wait_conv(nk);
+              if (ok) scores(i, nk);
+            }
+          }
+          if (ok && more) mma_commit(&conv_empty[nk % kPConv]);
+          n_conv += more ? 2 : 1;
+        }
+      }
+    } else if (warp >= kSoftW) {
+      // ---------------------------------------------------------- conversion
+      const int tid = threadIdx.x - kSoftW * 32;
+      constexpr int kC = D / 16;            // 16-byte chunks of a row of codes
+      constexpr int kStep = 128 / kC;       // rows per step
+      const int c = tid % kC, row0 = tid / kC;
+      for (int u = 2 * t0; u < 2 * t1; ++u, ++n_raw) {
+        const int s = n_raw % L::kRaw, d = n_raw % kPConv;
+        ok = ok && mbar_wait(&raw_full[s], (n_raw / L::kRaw) & 1, a.err);
+        ok = ok && (n_raw < kPConv ||
+                    mbar_wait(&conv_empty[d], ((n_raw / kPConv) & 1) ^ 1, a.err));
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* raw = smem + L::kRawOff + s * L::kRawB;
+        uint8_t* out = smem + L::kConvOff + d * L::kTileB;
+        const int i = 2 * ((u >> 1) - t0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool there = rec_page[i + h] >= 0;
+          const uint32_t hp = (u & 1) ? half_pow2(rec_e[i + h] - En) : 0x3C00u;
+          const uint32_t mul = hp | (hp << 16);
+          uint32_t add;  // -1152 * 2^(e - E), exact
+          asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
+#pragma unroll
+          for (int k = 0; k < 64 / kStep; ++k) {
+            const int row = h * 64 + row0 + k * kStep;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (there) v = lds_v4(raw + row * D + c * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = w[e] ^ 0x80808080u;
+              const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140);
+              const uint32_t hi = __byte_perm(x, 0x64646464u, 0x4342);
+              asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e]) : "r"(lo), "r"(mul), "r"(add));
+              asm("fma.rn.f16x2 %0, %1, %2, %3;"
+                  : "=r"(o[2 * e + 1])
+                  : "r"(hi), "r"(mul), "r"(add));
+            }
+            // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks; the
+            // upper half of the lanes stores them in the other order (banks)
+            uint8_t* dst = out + (c >> 2) * L::kBlockB + row * 128;
+            const int sw = (c >> 2) & 1;
+            const int c0 = (((2 * c + sw) & 7) ^ (row & 7)) << 4;
+            const int c1 = (((2 * c + (sw ^ 1)) & 7) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(dst + c0) =
+                sw ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + c1) =
+                sw ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[s]);
+          mbar_arrive(&conv_full[d]);
+        }
+      }
+    } else if (qt < tiles_q) {
+      // ---------------------------------------------------------- softmax
+      const uint32_t s_col = tbase + lane_off + L::kSCol + qt * kKeys;
+      const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
+      float escale = En == E ? 1.f : exp2f(static_cast<float>(E - En));
+      int j = jt;
+      for (int tt = t0; tt < t1; ++tt, ++j) {
+        ok = ok && mbar_wait(&s_full[qt], j & 1, a.err);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int i = 2 * (tt - t0);
+        // limits of the visible tokens relative to each page's first
+        bool whole[2];
+        int hi[2], lo[2], sk[2];
+        float c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool there = rec_page[i + h] >= 0;
+          const int jb = there ? pages.page(2 * t0 + i + h) * kBlk : 0;
+          whole[h] = there && kv_all(a, i_first, i_last, jb, jb + kBlk - 1);
+          hi[h] = there ? pos - jb : -1;
+          lo[h] = a.window ? pos - a.window + 1 - jb : 0;
+          sk[h] = a.window ? (a.sinks > jb ? a.sinks - jb : 0) : 0;
+          c[h] = there ? cs * rec_ks[i + h] : 0.f;
+        }
+        auto sees = [&](int h, int k) { return k <= hi[h] && (k >= lo[h] || k < sk[h]); };
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float big = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[32];
+            tmem_ld32(s_col + 64 * h + 32 * q, v);
+            tmem_wait_ld();
+            if (whole[h]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) big = fmaxf(big, __uint_as_float(v[k]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                big = fmaxf(big, sees(h, 32 * q + k) ? __uint_as_float(v[k]) : -INFINITY);
+            }
+          }
+          // (no visible token: -inf times a scale of 0 must not count)
+          if (big != -INFINITY) top = fmaxf(top, big * c[h]);
+        }
+        const bool raise = top > ref + kPLazy;
+        float alpha = escale;
+        if (raise) {
+          alpha *= exp2_approx(ref - top);  // 0 for the row's first
+          sum *= exp2_approx(ref - top);
+          ref = top;
+        }
+        if (__any_sync(0xffffffffu, raise || escale != 1.f) && j > 0) {
+          // O has to hold everything up to the tile before
+          ok = ok && mbar_wait(&o_done[qt], (j - 1) & 1, a.err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(o_col + 32 * q, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st32(o_col + 32 * q, v);
+          }
+        }
+        escale = 1.f;
+        const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool there = rec_page[i + h] >= 0;
+          const float add = kPOff + (there ? rec_lf[i + h] : 0.f) - base;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[32];
+            tmem_ld32(s_col + 64 * h + 32 * q, v);
+            tmem_wait_ld();
+            uint32_t pw[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float p0 = exp2_approx(fmaf(__uint_as_float(v[k]), c[h], add));
+              float p1 = exp2_approx(fmaf(__uint_as_float(v[k + 1]), c[h], add));
+              if (!whole[h]) {
+                p0 = sees(h, 32 * q + k) ? p0 : 0.f;
+                p1 = sees(h, 32 * q + k + 1) ? p1 : 0.f;
+              }
+              s0 += p0;
+              s1 += p1;
+              pw[k / 2] = half2_bits(p0, p1);
+            }
+            tmem_st16(s_col + 32 * h + 16 * q, pw);
+          }
+          const float sp = s0 + s1;
+          if (sp != 0.f) sum = fmaf(sp, rec_rf[i + h], sum);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[qt]);
+      }
+    }
+    __syncwarp();  // one-thread roles
+    E = En;
+    jt += t1 - t0;
+  }
+
+  // ---- results
+  if (warp == kMmaW && lane == 0) {
+    mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
+    mbar_wait(mma_end, 0, a.err);
+  }
+  if (warp == kCopyW && lane == 0) {
+    // no copy outlives the CTA
+    for (unsigned n = n_issued > L::kRaw ? n_issued - L::kRaw : 0; n < n_issued; ++n)
+      if (!mbar_wait(&raw_full[n % L::kRaw], (n / L::kRaw) & 1, a.err)) break;
+  }
+  if (warp < kSoftW) {
+    const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
+    float* mine = partials + static_cast<size_t>(blockIdx.x) * (2 * kPRows * (D + 2));
+    const long long orow = (qrow * a.heads + qhead);
+    const bool have = qt < tiles_q && jt > 0 &&
+                      __all_sync(0xffffffffu, ok && mbar_wait(&o_done[qt], (jt - 1) & 1, a.err));
+    tc_fence_after();
+    const float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
+    if (qt < tiles_q) {
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 0u;
+        if (have) {
+          tmem_ld32(o_col + 32 * q, v);
+          tmem_wait_ld();
+        }
+        if (parts == 1) {
+          if (live) {
+            uint16_t* o = static_cast<uint16_t*>(a.out) + orow * D + 32 * q;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = __uint_as_float(v[k + 2 * e]) * inv;
+                const float y = __uint_as_float(v[k + 2 * e + 1]) * inv;
+                w[e] = a.type == TERN_BF16
+                           ? static_cast<uint32_t>(
+                                 __bfloat16_as_ushort(__float2bfloat16_rn(x))) |
+                                 (static_cast<uint32_t>(
+                                      __bfloat16_as_ushort(__float2bfloat16_rn(y)))
+                                  << 16)
+                           : half2_bits(x, y);
+              }
+              *reinterpret_cast<uint4*>(o + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            mine[(32 * q + k) * (2 * kPRows) + r] = __uint_as_float(v[k]) * inv;
+        }
+      }
+      if (parts == 1) {
+        if (live && a.lse)
+          a.lse[orow] = sum == 0.f ? -INFINITY
+                                   : (ref - kPOff + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        mine[D * (2 * kPRows) + r] = ref;
+        mine[(D + 1) * (2 * kPRows) + r] = sum;
+      }
+    }
+    if (parts > 1) {
+      // the last part to arrive adds them all, in order
+      __threadfence();
+      softmax_barrier();
+      if (threadIdx.x == 0) *is_last = atomic_add_acq_rel_gpu(&tickets[item], 1) == parts - 1;
+      softmax_barrier();
+      if (*is_last) {
+        if (threadIdx.x == 0) tickets[item] = 0;
+        if (live) {
+          const float* first = partials + static_cast<size_t>(item) * parts *
+                                              (2 * kPRows * (D + 2)) + r;
+          auto at = [&](int p, int d) {
+            return __ldcg(first + static_cast<size_t>(p) * (2 * kPRows * (D + 2)) +
+                          d * (2 * kPRows));
+          };
+          float top = -INFINITY, l = 0.f;
+          for (int p = 0; p < parts; ++p)
+            if (at(p, D + 1) != 0.f) top = fmaxf(top, at(p, D));
+          const float base = top == -INFINITY ? 0.f : top;
+          for (int p = 0; p < parts; ++p) {
+            const float s = at(p, D + 1);
+            if (s != 0.f) l += s * exp2f(at(p, D) - base);
+          }
+          for (int d0 = 0; d0 < D; d0 += 8) {
+            float acc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            for (int p = 0; p < parts; ++p) {
+              const float s = at(p, D + 1);
+              if (s != 0.f) {
+                const float f = s * exp2f(at(p, D) - base);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, at(p, d0 + e), acc[e]);
+              }
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = l == 0.f ? 0.f : acc[2 * e] / l;
+              const float y = l == 0.f ? 0.f : acc[2 * e + 1] / l;
+              w[e] = a.type == TERN_BF16
+                         ? static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(x))) |
+                               (static_cast<uint32_t>(
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(y)))
+                                << 16)
+                         : half2_bits(x, y);
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + d0) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (a.lse)
+            a.lse[orow] =
+                l == 0.f ? -INFINITY : (top - kPOff + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cta_barrier();
+  tc_fence_after();
+  if (warp == kMmaW) tmem_dealloc(tbase, 512);
+}
+
+}  // namespace
+
+size_t kv8_prompt_partial_bytes(int dim) {
+  return static_cast<size_t>(kSmallTMaxCtas) * 2 * kPRows * (dim + 2) * sizeof(float);
+}
+
+cudaError_t kv8_prompt_set_attributes() {
+  const cudaError_t e = cudaFuncSetAttribute(
+      kv8_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PL<64>::kAlloc);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kv8_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              PL<128>::kAlloc);
+}
+
+cudaError_t launch_kv8_prompt(const Kv8Args& a, long long min_rows, float* partials, int* tickets,
+                              int num_sms, cudaStream_t stream, int* launches) {
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  const long long row_blocks = (most + 2 * kPRows - 1) / (2 * kPRows);
+  // parts of the keys: as many as fill the SMs once, each of at least four
+  // tiles of the longest sequence that the table allows
+  long long items = row_blocks * a.hkv * a.seqs;
+  const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
+  int parts = 1;
+  if (items < sms) {
+    const long long tiles = (static_cast<long long>(a.width) + 1) / 2;
+    long long p = sms / items;
+    if (p > tiles / 4) p = tiles / 4;
+    if (p > 1) parts = static_cast<int>(p);
+  }
+  if (items * parts > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1];
+  const dim3 grid(static_cast<unsigned>(items * parts));
+  if (a.dim == 128) {
+    const cudaLaunchConfig_t cfg =
+        pdl_launch_config(attr, grid, dim3(kPThreads), PL<128>::kAlloc, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<128>, a, min_rows,
+                                             static_cast<int>(row_blocks), parts, partials,
+                                             tickets);
+    if (e != cudaSuccess) return e;
+  } else {
+    const cudaLaunchConfig_t cfg =
+        pdl_launch_config(attr, grid, dim3(kPThreads), PL<64>::kAlloc, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<64>, a, min_rows,
+                                             static_cast<int>(row_blocks), parts, partials,
+                                             tickets);
+    if (e != cudaSuccess) return e;
+  }
+  ++*launches;
+  return cudaSuccess;
+}
+
+}  // namespace tern
