@@ -57,15 +57,22 @@ struct PL {
   static constexpr int kQOff = 0;
   static constexpr int kConvOff = kQOff + 2 * kTileB;
   static constexpr int kRawOff = kConvOff + kPConv * kTileB;
-  static constexpr int kRecOff = kRawOff + kRaw * kRawB;  // page, e, ks, log2 f, 1 / f
-  static constexpr int kBarOff = kRecOff + kPRecs * 20;
+  static constexpr int kRecOff = kRawOff + kRaw * kRawB;  // PageRec, then pages and e
+  static constexpr int kBarOff = kRecOff + kPRecs * 24;
   static constexpr int kNumBars = 2 * kRaw + 2 * kPConv + 6 + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, emax[2], last
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kSCol = 0, kOCol = 256;
-  static_assert(kBarOff % 8 == 0, "alignment");
+  static_assert(kBarOff % 8 == 0 && kRecOff % 16 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+// What the softmax needs of a page, in one 16-byte load.
+struct __align__(16) PageRec {
+  float ks, lf, rf;  // key scale; log2 f and 1 / f of the value scale 2^e f
+  int meta;          // page index in the sequence * 4, bit q: every row of query
+                     // tile q sees the whole page; -1: no page
 };
 
 constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -144,11 +151,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   int* emax = reinterpret_cast<int*>(tmem_slot + 1);  // [2] by chunk parity
   int* is_last = emax + 2;
-  int* rec_page = reinterpret_cast<int*>(smem + L::kRecOff);
+  PageRec* recs = reinterpret_cast<PageRec*>(smem + L::kRecOff);
+  int* rec_page = reinterpret_cast<int*>(recs + kPRecs);  // -1: none
   int* rec_e = rec_page + kPRecs;
-  float* rec_ks = reinterpret_cast<float*>(rec_e + kPRecs);
-  float* rec_lf = rec_ks + kPRecs;
-  float* rec_rf = rec_lf + kPRecs;
 
   grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
 
@@ -257,11 +262,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     fence_proxy_async_smem();
   }
-  // positions of this thread's query tile, for the tests of whole pages
-  const int i_first = qt * kPRows < rows ? p_base + static_cast<int>((r0 + qt * kPRows) / a.group)
-                                         : 0;
-  const int i_last = static_cast<int>(
-      (r0 + (rows < (qt + 1) * kPRows ? rows : (qt + 1) * kPRows) - 1) / a.group) + p_base;
+  // positions of the block's last rows of tile 0 and first rows of tile 1
+  const int p_end0 =
+      p_base + static_cast<int>((r0 + (rows < kPRows ? rows : kPRows) - 1) / a.group);
+  const int p_beg1 = p_base + static_cast<int>((r0 + kPRows) / a.group);
 
   int E = -127;
   float ref = -INFINITY, sum = 0.f;
@@ -278,21 +282,31 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int i = threadIdx.x; i < 2 * (t1 - t0); i += kPThreads) {
       const int li = 2 * t0 + i;
       int page = -1, e = -127;
+      PageRec rec = {0.f, 0.f, 0.f, -1};
       if (li < pages.count) {
-        page = a.table[static_cast<size_t>(b) * a.width + pages.page(li)];
+        const int lp = pages.page(li);
+        page = a.table[static_cast<size_t>(b) * a.width + lp];
         if (page < 0 || page >= a.pages) {
           atomicOr(a.err, kErrIndex);
           page = -1;
         } else {
           const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
+          const float ks = sc[0];
           const VScale v = split_vscale(sc[a.hkv]);
-          rec_ks[i] = sc[0];
-          rec_lf[i] = log2f(v.f);
-          rec_rf[i] = 1.0f / v.f;
+          // a scale that is not finite keeps out of the arithmetic and makes
+          // 1 / f NaN
+          const bool good = fabsf(ks) < INFINITY && v.f == v.f;
+          rec.ks = good ? ks : 0.f;
+          rec.lf = good ? log2f(v.f) : 0.f;
+          rec.rf = good ? 1.0f / v.f : __uint_as_float(0x7FC00000u);
+          const int j0 = lp * kBlk, j1 = j0 + kBlk - 1;
+          rec.meta = lp * 4 | (kv_all(a, p_first, p_end0, j0, j1) ? 1 : 0) |
+                     (kv_all(a, p_beg1, p_last, j0, j1) ? 2 : 0);
           e = v.e;
           atomicMax(&emax[chunk & 1], e);
         }
       }
+      recs[i] = rec;
       rec_page[i] = page;
       rec_e[i] = e;
     }
@@ -385,7 +399,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int tid = threadIdx.x - kSoftW * 32;
       constexpr int kC = D / 16;            // 16-byte chunks of a row of codes
       constexpr int kStep = 128 / kC;       // rows per step
-      const int c = tid % kC, row0 = tid / kC;
+      // lanes of a row's second half take the row beside it: the stores of
+      // eight lanes then cover all banks
+      const int c = tid % kC, row0 = (tid / kC) ^ ((c >> 2) & 1);
       for (int u = 2 * t0; u < 2 * t1; ++u, ++n_raw) {
         const int s = n_raw % L::kRaw, d = n_raw % kPConv;
         ok = ok && mbar_wait(&raw_full[s], (n_raw / L::kRaw) & 1, a.err);
@@ -398,18 +414,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint8_t* raw = smem + L::kRawOff + s * L::kRawB;
         uint8_t* out = smem + L::kConvOff + d * L::kTileB;
         const int i = 2 * ((u >> 1) - t0);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          // (no page: whatever the buffer holds times 0)
           const bool there = rec_page[i + h] >= 0;
-          const uint32_t hp = (u & 1) ? half_pow2(rec_e[i + h] - En) : 0x3C00u;
+          const uint32_t hp =
+              !there ? 0u : (u & 1) ? half_pow2(rec_e[i + h] - En) : 0x3C00u;
           const uint32_t mul = hp | (hp << 16);
           uint32_t add;  // -1152 * 2^(e - E), exact
           asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
 #pragma unroll
           for (int k = 0; k < 64 / kStep; ++k) {
             const int row = h * 64 + row0 + k * kStep;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (there) v = lds_v4(raw + row * D + c * 16);
+            const uint4 v = lds_v4(raw + row * D + c * 16);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[8];
 #pragma unroll
@@ -422,16 +439,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
                   : "=r"(o[2 * e + 1])
                   : "r"(hi), "r"(mul), "r"(add));
             }
-            // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks; the
-            // upper half of the lanes stores them in the other order (banks)
+            // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks
             uint8_t* dst = out + (c >> 2) * L::kBlockB + row * 128;
-            const int sw = (c >> 2) & 1;
-            const int c0 = (((2 * c + sw) & 7) ^ (row & 7)) << 4;
-            const int c1 = (((2 * c + (sw ^ 1)) & 7) ^ (row & 7)) << 4;
-            *reinterpret_cast<uint4*>(dst + c0) =
-                sw ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + c1) =
-                sw ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + ((((2 * c) & 7) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async_smem();
@@ -449,102 +462,100 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int j = jt;
       for (int tt = t0; tt < t1; ++tt, ++j) {
         ok = ok && mbar_wait(&s_full[qt], j & 1, a.err);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const int i = 2 * (tt - t0);
-        // limits of the visible tokens relative to each page's first
-        bool whole[2];
-        int hi[2], lo[2], sk[2];
-        float c[2];
-#pragma unroll
+        // one page at a time: its 64 scores in registers, read once.  (The
+        // loop is not unrolled: the roles' code has to stay in the
+        // instruction cache.)
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          const bool there = rec_page[i + h] >= 0;
-          const int jb = there ? pages.page(2 * t0 + i + h) * kBlk : 0;
-          whole[h] = there && kv_all(a, i_first, i_last, jb, jb + kBlk - 1);
-          hi[h] = there ? pos - jb : -1;
-          lo[h] = a.window ? pos - a.window + 1 - jb : 0;
-          sk[h] = a.window ? (a.sinks > jb ? a.sinks - jb : 0) : 0;
-          c[h] = there ? cs * rec_ks[i + h] : 0.f;
-        }
-        auto sees = [&](int h, int k) { return k <= hi[h] && (k >= lo[h] || k < sk[h]); };
-        float top = -INFINITY;
+          float v[64];
+          tmem_ld32(s_col + 64 * h, reinterpret_cast<uint32_t*>(v));
+          tmem_ld32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(v) + 32);
+          const PageRec rec = recs[i + h];
+          // (a scale of 0 must not turn a masked -inf into a NaN)
+          const float c = fmaxf(cs * rec.ks, 1e-37f);
+          tmem_wait_ld();
+          if (!(rec.meta >= 0 && ((rec.meta >> qt) & 1))) {
+            // limits of the visible tokens relative to the page's first
+            const int jb = (rec.meta >> 2) * kBlk;
+            const int hi = rec.meta >= 0 ? pos - jb : -1;
+            const int lo = a.window ? pos - a.window + 1 - jb : 0;
+            const int sk = a.window ? a.sinks - jb : 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float big = -INFINITY;
+            for (int k = 0; k < 64; ++k)
+              if (k > hi || (k < lo && k >= sk)) v[k] = -INFINITY;
+          }
+          float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t v[32];
-            tmem_ld32(s_col + 64 * h + 32 * q, v);
-            tmem_wait_ld();
-            if (whole[h]) {
+          for (int k = 4; k < 64; k += 8)
 #pragma unroll
-              for (int k = 0; k < 32; ++k) big = fmaxf(big, __uint_as_float(v[k]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                big = fmaxf(big, sees(h, 32 * q + k) ? __uint_as_float(v[k]) : -INFINITY);
+            for (int e = 0; e < 4; ++e)
+              m4[e] = fmaxf(fmaxf(m4[e], v[k + e]), k + e + 4 < 64 ? v[k + e + 4] : v[k + e]);
+          const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float top = big * c;  // -inf: no visible token
+          const bool raise = top > ref + kPLazy;
+          if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
+            float alpha = 1.f;
+            if (raise) {
+              alpha = exp2_approx(ref - top);  // 0 for the row's first
+              sum *= alpha;
+              ref = top;
             }
-          }
-          // (no visible token: -inf times a scale of 0 must not count)
-          if (big != -INFINITY) top = fmaxf(top, big * c[h]);
-        }
-        const bool raise = top > ref + kPLazy;
-        float alpha = escale;
-        if (raise) {
-          alpha *= exp2_approx(ref - top);  // 0 for the row's first
-          sum *= exp2_approx(ref - top);
-          ref = top;
-        }
-        if (__any_sync(0xffffffffu, raise || escale != 1.f) && j > 0) {
-          // O has to hold everything up to the tile before
-          ok = ok && mbar_wait(&o_done[qt], (j - 1) & 1, a.err);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+            if (j > 0) {
+              // O has to hold everything up to the tile before
+              ok = ok && mbar_wait(&o_done[qt], (j - 1) & 1, a.err);
+              tc_fence_after();
+              const float f = alpha * escale;
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t x[16];
+                tmem_ld16(o_col + 16 * q, x);
+                tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t v[32];
-            tmem_ld32(o_col + 32 * q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-            tmem_st32(o_col + 32 * q, v);
-          }
-        }
-        escale = 1.f;
-        const float base = ref == -INFINITY ? 0.f : ref;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool there = rec_page[i + h] >= 0;
-          const float add = kPOff + (there ? rec_lf[i + h] : 0.f) - base;
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t v[32];
-            tmem_ld32(s_col + 64 * h + 32 * q, v);
-            tmem_wait_ld();
-            uint32_t pw[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float p0 = exp2_approx(fmaf(__uint_as_float(v[k]), c[h], add));
-              float p1 = exp2_approx(fmaf(__uint_as_float(v[k + 1]), c[h], add));
-              if (!whole[h]) {
-                p0 = sees(h, 32 * q + k) ? p0 : 0.f;
-                p1 = sees(h, 32 * q + k + 1) ? p1 : 0.f;
+                for (int k = 0; k < 16; ++k)
+                  x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                tmem_st16(o_col + 16 * q, x);
               }
-              s0 += p0;
-              s1 += p1;
-              pw[k / 2] = half2_bits(p0, p1);
             }
-            tmem_st16(s_col + 32 * h + 16 * q, pw);
+            if (h > 0) {
+              // and so do the weights of the page before
+              const uint32_t f = half2_bits(alpha, alpha);
+              tmem_wait_st();
+#pragma unroll 1
+              for (int q = 0; q < 2; ++q) {
+                uint32_t x[16];
+                tmem_ld16(s_col + 16 * q, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[k]) : "r"(x[k]), "r"(f));
+                tmem_st16(s_col + 16 * q, x);
+              }
+            }
+            escale = 1.f;
           }
-          const float sp = s0 + s1;
-          if (sp != 0.f) sum = fmaf(sp, rec_rf[i + h], sum);
+          const float add = kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref);
+          const uint64_t c2 = pair_f32(c, c), add2 = pair_f32(add, add);
+          uint64_t s2[2] = {0, 0};  // pairs of sums from +0
+          uint32_t pw[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            float p0, p1;
+            unpair_f32(fma_pair(pair_f32(v[k], v[k + 1]), c2, add2), p0, p1);
+            p0 = exp2_approx(p0);
+            p1 = exp2_approx(p1);
+            s2[(k >> 1) & 1] = add_pair(s2[(k >> 1) & 1], pair_f32(p0, p1));
+            pw[k / 2] = half2_bits(p0, p1);
+          }
+          tmem_st32(s_col + 32 * h, pw);
+          float s0, s1;
+          unpair_f32(add_pair(s2[0], s2[1]), s0, s1);
+          // (a scale that is not finite has 1 / f = NaN: the rows that see its
+          // page, and only they, become NaN)
+          if (big != -INFINITY) sum = fmaf(s0 + s1, rec.rf, sum);
         }
         tmem_wait_st();
         tc_fence_before();
