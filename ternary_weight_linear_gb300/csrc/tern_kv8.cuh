@@ -97,6 +97,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Whether the phase has completed, without waiting for it (a try_wait may
+// suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // fp32 pairs in one 64-bit register (each half as its scalar instruction).
 __device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
   uint64_t d;

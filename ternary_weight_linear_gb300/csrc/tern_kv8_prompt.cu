@@ -20,12 +20,12 @@
 //
 // Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (S read
 // from TMEM twice, for the maximum and for the weights; P written over S);
-// 8-11 the conversion; 12 the MMAs (one thread), in the order
-//   PV0(j), S0(j+1), PV1(j), S1(j+1),
-// so that one tile's softmax runs under the other's products; 13 the copies
-// (one thread, a page of a head is one contiguous block).  The MMAs of a CTA
-// run in the order of their issue, so S(j+1) may follow the PV(j) that reads
-// the same columns.
+// 8-11 the conversion; 12 and 13 the MMAs of a query tile each (one thread:
+// its barrier waits cost about 200 cycles each, which the other's products
+// cover), the scores a page ahead of the values (two score buffers a tile), so
+// that a softmax does not wait for its scores; 14 the copies (one thread, a
+// page of a head is one contiguous block).  The MMAs of a thread run in the
+// order of their issue.
 // Work: one CTA per (block of rows, sequence, head, part of the keys), the
 // longest rows first.  When there are too few blocks for the SMs the keys are
 // cut into parts, whose (max, sum, O) go to the workspace, and the last CTA of
@@ -39,27 +39,28 @@ namespace tern {
 namespace {
 
 constexpr int kPRows = 128;  // rows of a query tile
-constexpr int kKeys = 128;   // tokens of a key tile: two pages
 constexpr int kSoftW = 8, kConvW = 4;
-constexpr int kMmaW = kSoftW + kConvW, kCopyW = kMmaW + 1;
+constexpr int kMmaW = kSoftW + kConvW, kCopyW = kMmaW + 2;
 constexpr int kPThreads = (kCopyW + 1) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
-constexpr int kPConv = 3;    // converted tiles
+constexpr int kPConv = 3;    // converted pages (keys and values)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
 
 template <int D>
 struct PL {
-  static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
-  static constexpr int kBlockB = kPRows * 128;        // 16 KB
-  static constexpr int kTileB = kBlocks * kBlockB;    // an fp16 tile
-  static constexpr int kRawB = kKeys * D;             // a tile of codes
-  static constexpr int kRaw = D == 128 ? 3 : 4;       // tiles of codes in flight
+  static constexpr int kBlocks = D / 64;               // 128-byte wide blocks of a row
+  static constexpr int kQBlockB = kPRows * 128;
+  static constexpr int kQTileB = kBlocks * kQBlockB;   // a query tile in fp16
+  static constexpr int kBlockB = kBlk * 128;
+  static constexpr int kTileB = kBlocks * kBlockB;     // a page's keys or values in fp16
+  static constexpr int kRawB = kBlk * D;               // and as codes
+  static constexpr int kRaw = D == 128 ? 3 : 6;        // pages of codes in flight
   static constexpr int kQOff = 0;
-  static constexpr int kConvOff = kQOff + 2 * kTileB;
-  static constexpr int kRawOff = kConvOff + kPConv * kTileB;
-  static constexpr int kRecOff = kRawOff + kRaw * kRawB;  // PageRec, then pages and e
+  static constexpr int kConvOff = kQOff + 2 * kQTileB;
+  static constexpr int kRawOff = kConvOff + 2 * kPConv * kTileB;
+  static constexpr int kRecOff = kRawOff + 2 * kRaw * kRawB;  // PageRec, then pages and e
   static constexpr int kBarOff = kRecOff + kPRecs * 24;
-  static constexpr int kNumBars = 2 * kRaw + 2 * kPConv + 6 + 1;
+  static constexpr int kNumBars = 2 * kRaw + 3 * kPConv + 4 + 4 + 4 + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, emax[2], last
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -142,12 +143,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* raw_empty = raw_full + L::kRaw;
-  uint64_t* conv_full = raw_empty + L::kRaw;
-  uint64_t* conv_empty = conv_full + kPConv;
-  uint64_t* s_full = conv_empty + kPConv;  // [2] scores of a query tile
-  uint64_t* p_full = s_full + 2;           // [2] its weights, O rescaled
-  uint64_t* o_done = p_full + 2;           // [2] its O holds the tile
-  uint64_t* mma_end = o_done + 2;
+  uint64_t* k_full = raw_empty + L::kRaw;  // converted keys
+  uint64_t* v_full = k_full + kPConv;      // converted values
+  uint64_t* conv_empty = v_full + kPConv;
+  uint64_t* s_full = conv_empty + kPConv;  // [tile][buffer] scores
+  uint64_t* p_full = s_full + 4;           // [tile][buffer] weights, O rescaled
+  uint64_t* o_done = p_full + 4;           // [tile][page parity] O holds the page
+  uint64_t* mma_end = o_done + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   int* emax = reinterpret_cast<int*>(tmem_slot + 1);  // [2] by chunk parity
   int* is_last = emax + 2;
@@ -174,9 +176,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int p_first = p_base + static_cast<int>(r0 / a.group);
   const int p_last = p_base + static_cast<int>((r0 + rows - 1) / a.group);
   const KvPages pages = kv_pages(a, p_first, p_last);
-  const int all_tiles = (pages.count + 1) / 2;
-  const int t_begin = static_cast<int>(static_cast<long long>(all_tiles) * part / parts);
-  const int t_end = static_cast<int>(static_cast<long long>(all_tiles) * (part + 1) / parts);
+  const int t_begin = static_cast<int>(static_cast<long long>(pages.count) * part / parts);
+  const int t_end = static_cast<int>(static_cast<long long>(pages.count) * (part + 1) / parts);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kRaw; ++s) {
@@ -184,16 +185,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&raw_empty[s], kConvW);
     }
     for (int s = 0; s < kPConv; ++s) {
-      mbar_init(&conv_full[s], kConvW);
-      mbar_init(&conv_empty[s], 1);
+      mbar_init(&k_full[s], kConvW);
+      mbar_init(&v_full[s], kConvW);
+      mbar_init(&conv_empty[s], tiles_q);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
-      emax[i] = -127;
     }
-    mbar_init(mma_end, 1);
+    emax[0] = emax[1] = -127;
+    mbar_init(mma_end, 2);
     fence_mbar_init();
   }
   if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
@@ -250,14 +252,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const float up1 = __uint_as_float(static_cast<uint32_t>(up / 2 + 127) << 23);
     const float up2 = __uint_as_float(static_cast<uint32_t>(up - up / 2 + 127) << 23);
     cs = a.scale_log2 / up1 / up2;
-    uint8_t* dst = smem + L::kQOff + qt * L::kTileB + tr * 128;
+    uint8_t* dst = smem + L::kQOff + qt * L::kQTileB + tr * 128;
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
       uint32_t h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         h[e] = half2_bits(lo_of(w[4 * c + e]) * up1 * up2, hi_of(w[4 * c + e]) * up1 * up2);
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kBlockB + (((c & 7) ^ (tr & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kQBlockB + (((c & 7) ^ (tr & 7)) << 4)) =
           make_uint4(h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
@@ -267,25 +269,33 @@ __global__ void __launch_bounds__(kPThreads, 1)
       p_base + static_cast<int>((r0 + (rows < kPRows ? rows : kPRows) - 1) / a.group);
   const int p_beg1 = p_base + static_cast<int>((r0 + kPRows) / a.group);
 
+  // columns of tile i's scores (and weights) of page j
+  auto s_col = [](int i, int j) -> uint32_t { return L::kSCol + i * 128 + (j & 1) * kBlk; };
+
+  int jt = 0;  // pages so far
+  // Waits until tile i's O holds page j.  Two pages may be under way and a
+  // parity tells only neighbouring phases apart, so odd and even pages have
+  // barriers of their own: page j - 2 is done before page j's scores exist,
+  // which is before anyone waits for page j.
+  auto wait_values = [&](int i, int j) {
+    return mbar_wait(&o_done[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+  };
+
   int E = -127;
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
-  int jt = 0;             // key tiles so far
-  unsigned n_raw = 0;     // (copies, conversion) tiles of codes so far
-  unsigned n_conv = 0;    // (MMA) converted tiles used
-  unsigned n_issued = 0;  // (copies) tiles requested
+  int n_issued = 0;  // (copies) pages requested so far
 
-  for (int t0 = t_begin, chunk = 0; t0 < t_end; t0 += kPRecs / 2, ++chunk) {
-    const int t1 = t_end < t0 + kPRecs / 2 ? t_end : t0 + kPRecs / 2;
-    // ---- records of the pages of tiles [t0, t1)
+  for (int t0 = t_begin, chunk = 0; t0 < t_end; t0 += kPRecs, ++chunk) {
+    const int t1 = t_end < t0 + kPRecs ? t_end : t0 + kPRecs;
+    // ---- records of pages [t0, t1) of the list
     cta_barrier();  // the records of the chunk before have been used
-    for (int i = threadIdx.x; i < 2 * (t1 - t0); i += kPThreads) {
-      const int li = 2 * t0 + i;
-      int page = -1, e = -127;
+    for (int i = threadIdx.x; i < t1 - t0; i += kPThreads) {
+      int e = -127;
       PageRec rec = {0.f, 0.f, 0.f, -1};
-      if (li < pages.count) {
-        const int lp = pages.page(li);
-        page = a.table[static_cast<size_t>(b) * a.width + lp];
+      {
+        const int lp = pages.page(t0 + i);
+        int page = a.table[static_cast<size_t>(b) * a.width + lp];
         if (page < 0 || page >= a.pages) {
           atomicOr(a.err, kErrIndex);
           page = -1;
@@ -305,9 +315,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
           e = v.e;
           atomicMax(&emax[chunk & 1], e);
         }
+        rec_page[i] = page;
       }
       recs[i] = rec;
-      rec_page[i] = page;
       rec_e[i] = e;
     }
     if (threadIdx.x == 0) emax[(chunk & 1) ^ 1] = -127;
@@ -317,81 +327,75 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (warp == kCopyW) {
       // ---------------------------------------------------------- copies
       if (lane == 0 && ok) {
-        for (int u = 2 * t0; u < 2 * t1 && ok; ++u, ++n_issued) {
-          // tile u / 2, keys then values
+        for (int i = 0; i < t1 - t0; ++i, ++n_issued) {
           const int s = n_issued % L::kRaw;
           if (n_issued >= L::kRaw &&
               !mbar_wait(&raw_empty[s], ((n_issued / L::kRaw) & 1) ^ 1, a.err)) {
             ok = false;
             break;
           }
-          const int i = 2 * ((u >> 1) - t0);
-          uint32_t bytes = 0;
-          for (int h = 0; h < 2; ++h)
-            if (rec_page[i + h] >= 0) bytes += kBlk * D;
-          mbar_arrive_expect_tx(&raw_full[s], bytes);
-          for (int h = 0; h < 2; ++h)
-            if (rec_page[i + h] >= 0)
-              bulk_load(smem + L::kRawOff + s * L::kRawB + h * (kBlk * D),
-                        a.codes + ((static_cast<size_t>(rec_page[i + h]) * 2 + (u & 1)) * a.hkv +
-                                   hk) * (kBlk * D),
-                        kBlk * D, &raw_full[s]);
+          const int page = rec_page[i];
+          mbar_arrive_expect_tx(&raw_full[s], page >= 0 ? 2 * L::kRawB : 0);
+          if (page >= 0) {
+            const int8_t* src = a.codes + (static_cast<size_t>(page) * 2 * a.hkv + hk) * L::kRawB;
+            uint8_t* dst = smem + L::kRawOff + s * (2 * L::kRawB);
+            bulk_load(dst, src, L::kRawB, &raw_full[s]);
+            bulk_load(dst + L::kRawB, src + static_cast<size_t>(a.hkv) * L::kRawB, L::kRawB,
+                      &raw_full[s]);
+          }
         }
       }
-    } else if (warp == kMmaW) {
+    } else if (warp >= kMmaW) {
       // ---------------------------------------------------------- MMAs
-      if (lane == 0 && ok) {
-        constexpr uint32_t idesc_s = idesc_f16_f32(kPRows, kKeys, false);
+      const int i = warp - kMmaW;  // query tile
+      if (lane == 0 && ok && i < tiles_q) {
+        constexpr uint32_t idesc_s = idesc_f16_f32(kPRows, kBlk, false);
         constexpr uint32_t idesc_o = idesc_f16_f32(kPRows, D, true);
         const uint64_t dq = desc_sw128(smem_addr(smem + L::kQOff), 16);
         const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
-        auto scores = [&](int i, unsigned n) {  // S_i = Q_i K^T, keys in converted tile n
-          const uint64_t q = dq + static_cast<uint64_t>((i * L::kTileB) >> 4);
-          const uint64_t k = dc + static_cast<uint64_t>(((n % kPConv) * L::kTileB) >> 4);
+        auto wait_conv = [&](uint64_t* full, int j) {
+          return mbar_wait(&full[j % kPConv], (j / kPConv) & 1, a.err);
+        };
+        // S of page j
+        auto scores = [&](int j) {
+          const uint64_t q = dq + static_cast<uint64_t>((i * L::kQTileB) >> 4);
+          const uint64_t k = dc + static_cast<uint64_t>(((j % kPConv) * 2 * L::kTileB) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t o = static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4);
-            mma_ss(tbase + L::kSCol + i * kKeys, q + o, k + o, idesc_s, kk != 0);
-          }
-          mma_commit(&s_full[i]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tbase + s_col(i, j),
+                   q + static_cast<uint64_t>(((kk >> 2) * L::kQBlockB + (kk & 3) * 32) >> 4),
+                   k + static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4),
+                   idesc_s, kk != 0);
+          mma_commit(&s_full[2 * i + (j & 1)]);
         };
-        auto values = [&](int i, unsigned n, bool first) {  // O_i += P_i V
-          const uint64_t v = dc + static_cast<uint64_t>(((n % kPConv) * L::kTileB) >> 4);
+        // O += P V of page j
+        auto values = [&](int j) {
+          const uint64_t v =
+              dc + static_cast<uint64_t>((((j % kPConv) * 2 + 1) * L::kTileB) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tbase + L::kOCol + i * 128, tbase + L::kSCol + i * kKeys + kk * 8,
-                   v + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o, !(first && kk == 0));
-          mma_commit(&o_done[i]);
+          for (int kk = 0; kk < kBlk / 16; ++kk)
+            mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, j) + kk * 8,
+                   v + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o, j != 0 || kk != 0);
+          mma_commit(&o_done[2 * i + (j & 1)]);
         };
-        auto wait_conv = [&](unsigned n) {
-          return mbar_wait(&conv_full[n % kPConv], (n / kPConv) & 1, a.err);
-        };
-        // the chunk's first scores
-        ok = wait_conv(n_conv);
-        tc_fence_after();
+        const int j_end = jt + t1 - t0;
+        // The scores of page j + 1 go into the columns of page j - 1's weights,
+        // which the products issued before them read.  The conversions are in
+        // order, so page j + 1's keys come after page j's values.
+        ok = wait_conv(k_full, jt);
         if (ok) {
-          for (int i = 0; i < tiles_q; ++i) scores(i, n_conv);
-          mma_commit(&conv_empty[n_conv % kPConv]);
+          tc_fence_after();
+          scores(jt);
         }
-        ++n_conv;
-        int j = jt;
-        for (int tt = t0; tt < t1 && ok; ++tt, ++j) {
-          const unsigned nv = n_conv, nk = n_conv + 1;
-          const bool more = tt + 1 < t1;
-          ok = wait_conv(nv);
-          for (int i = 0; i < tiles_q && ok; ++i) {
-            ok = mbar_wait(&p_full[i], j & 1, a.err);
-            if (!ok) break;
-            tc_fence_after();
-            values(i, nv, j == 0);
-            if (i == tiles_q - 1) mma_commit(&conv_empty[nv % kPConv]);
-            if (more) {
-              if (i == 0) ok = wait_conv(nk);
-              if (ok) scores(i, nk);
-            }
-          }
-          if (ok && more) mma_commit(&conv_empty[nk % kPConv]);
-          n_conv += more ? 2 : 1;
+        for (int j = jt; j < j_end && ok; ++j) {
+          const bool more = j + 1 < j_end;
+          ok = more ? wait_conv(k_full, j + 1) : wait_conv(v_full, j);
+          if (ok && more) scores(j + 1);
+          ok = ok && mbar_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          values(j);
+          mma_commit(&conv_empty[j % kPConv]);
         }
       }
     } else if (warp >= kSoftW) {
@@ -402,165 +406,157 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // lanes of a row's second half take the row beside it: the stores of
       // eight lanes then cover all banks
       const int c = tid % kC, row0 = (tid / kC) ^ ((c >> 2) & 1);
-      for (int u = 2 * t0; u < 2 * t1; ++u, ++n_raw) {
-        const int s = n_raw % L::kRaw, d = n_raw % kPConv;
-        ok = ok && mbar_wait(&raw_full[s], (n_raw / L::kRaw) & 1, a.err);
-        ok = ok && (n_raw < kPConv ||
-                    mbar_wait(&conv_empty[d], ((n_raw / kPConv) & 1) ^ 1, a.err));
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* raw = smem + L::kRawOff + s * L::kRawB;
-        uint8_t* out = smem + L::kConvOff + d * L::kTileB;
-        const int i = 2 * ((u >> 1) - t0);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          // (no page: whatever the buffer holds times 0)
-          const bool there = rec_page[i + h] >= 0;
-          const uint32_t hp =
-              !there ? 0u : (u & 1) ? half_pow2(rec_e[i + h] - En) : 0x3C00u;
-          const uint32_t mul = hp | (hp << 16);
-          uint32_t add;  // -1152 * 2^(e - E), exact
-          asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
+      // a page's 64 rows from raw to out, times mul (and add = -1152 mul)
+      auto convert = [&](const uint4 (&v)[kBlk / kStep], uint8_t* out, uint32_t mul,
+                         uint32_t add) {
 #pragma unroll
-          for (int k = 0; k < 64 / kStep; ++k) {
-            const int row = h * 64 + row0 + k * kStep;
-            const uint4 v = lds_v4(raw + row * D + c * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[8];
+        for (int k = 0; k < kBlk / kStep; ++k) {
+          const int row = row0 + k * kStep;
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t x = w[e] ^ 0x80808080u;
-              const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140);
-              const uint32_t hi = __byte_perm(x, 0x64646464u, 0x4342);
-              asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e]) : "r"(lo), "r"(mul), "r"(add));
-              asm("fma.rn.f16x2 %0, %1, %2, %3;"
-                  : "=r"(o[2 * e + 1])
-                  : "r"(hi), "r"(mul), "r"(add));
-            }
-            // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks
-            uint8_t* dst = out + (c >> 2) * L::kBlockB + row * 128;
-            *reinterpret_cast<uint4*>(dst + ((((2 * c) & 7) ^ (row & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = w[e] ^ 0x80808080u;
+            const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140);
+            const uint32_t hi = __byte_perm(x, 0x64646464u, 0x4342);
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e]) : "r"(lo), "r"(mul), "r"(add));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e + 1]) : "r"(hi), "r"(mul), "r"(add));
           }
+          // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks
+          uint8_t* dst = out + row * 128;
+          *reinterpret_cast<uint4*>(dst + ((((2 * c) & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
+      };
+      // Both barriers of a page are tried a page ahead, so that their answers
+      // (some 200 cycles) come under the conversion.
+      auto try_page = [&](int j) {
+        return mbar_test(&raw_full[j % L::kRaw], (j / L::kRaw) & 1) &&
+               (j < kPConv || mbar_test(&conv_empty[j % kPConv], ((j / kPConv) & 1) ^ 1));
+      };
+      const int j_end = jt + t1 - t0;
+      bool ready = false;
+      for (int j = jt; j < j_end; ++j) {
+        const int s = j % L::kRaw, d = j % kPConv;
+        if (!ready) {
+          ok = ok && mbar_wait(&raw_full[s], (j / L::kRaw) & 1, a.err);
+          ok = ok && (j < kPConv || mbar_wait(&conv_empty[d], ((j / kPConv) & 1) ^ 1, a.err));
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* raw = smem + L::kRawOff + s * (2 * L::kRawB) + row0 * D + c * 16;
+        uint8_t* out = smem + L::kConvOff + d * (2 * L::kTileB) + (c >> 2) * L::kBlockB;
+        uint4 kv[kBlk / kStep], vv[kBlk / kStep];
+#pragma unroll
+        for (int k = 0; k < kBlk / kStep; ++k) {
+          kv[k] = lds_v4(raw + k * kStep * D);
+          vv[k] = lds_v4(raw + L::kRawB + k * kStep * D);
+        }
+        // (no page: whatever the buffer holds times 0)
+        const bool there = rec_page[j - jt] >= 0;
+        const uint32_t hp = there ? half_pow2(rec_e[j - jt] - En) : 0u;
+        const uint32_t mul = hp | (hp << 16);
+        uint32_t add;  // -1152 * 2^(e - E), exact
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
+        ready = j + 1 < j_end && try_page(j + 1);
+        convert(kv, out, there ? 0x3C003C00u : 0u, there ? 0xE480E480u : 0u);
+        if (lane == 0) mbar_arrive(&k_full[d]);
+        convert(vv, out + L::kTileB, mul, add);
         if (lane == 0) {
+          mbar_arrive(&v_full[d]);
           mbar_arrive(&raw_empty[s]);
-          mbar_arrive(&conv_full[d]);
         }
       }
     } else if (qt < tiles_q) {
       // ---------------------------------------------------------- softmax
-      const uint32_t s_col = tbase + lane_off + L::kSCol + qt * kKeys;
       const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
       float escale = En == E ? 1.f : exp2f(static_cast<float>(E - En));
-      int j = jt;
-      for (int tt = t0; tt < t1; ++tt, ++j) {
-        ok = ok && mbar_wait(&s_full[qt], j & 1, a.err);
+      const int j_end = jt + t1 - t0;
+      for (int j = jt; j < j_end; ++j) {
+        ok = ok && mbar_wait(&s_full[2 * qt + (j & 1)], (j >> 1) & 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int i = 2 * (tt - t0);
-        // one page at a time: its 64 scores in registers, read once.  (The
-        // loop is not unrolled: the roles' code has to stay in the
-        // instruction cache.)
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float v[64];
-          tmem_ld32(s_col + 64 * h, reinterpret_cast<uint32_t*>(v));
-          tmem_ld32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(v) + 32);
-          const PageRec rec = recs[i + h];
-          // (a scale of 0 must not turn a masked -inf into a NaN)
-          const float c = fmaxf(cs * rec.ks, 1e-37f);
-          tmem_wait_ld();
-          if (!(rec.meta >= 0 && ((rec.meta >> qt) & 1))) {
-            // limits of the visible tokens relative to the page's first
-            const int jb = (rec.meta >> 2) * kBlk;
-            const int hi = rec.meta >= 0 ? pos - jb : -1;
-            const int lo = a.window ? pos - a.window + 1 - jb : 0;
-            const int sk = a.window ? a.sinks - jb : 0;
+        // the page's 64 scores in registers, read once
+        const uint32_t sc = tbase + lane_off + s_col(qt, j);
+        float v[64];
+        tmem_ld32(sc, reinterpret_cast<uint32_t*>(v));
+        tmem_ld32(sc + 32, reinterpret_cast<uint32_t*>(v) + 32);
+        const PageRec rec = recs[j - jt];
+        // (a scale of 0 must not turn a masked -inf into a NaN)
+        const float c = fmaxf(cs * rec.ks, 1e-37f);
+        tmem_wait_ld();
+        if (!(rec.meta >= 0 && ((rec.meta >> qt) & 1))) {
+          // limits of the visible tokens relative to the page's first
+          const int jb = (rec.meta >> 2) * kBlk;
+          const int hi = rec.meta >= 0 ? pos - jb : -1;
+          const int lo = a.window ? pos - a.window + 1 - jb : 0;
+          const int sk = a.window ? a.sinks - jb : 0;
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (k > hi || (k < lo && k >= sk)) v[k] = -INFINITY;
-          }
-          float m4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int k = 4; k < 64; k += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              m4[e] = fmaxf(fmaxf(m4[e], v[k + e]), k + e + 4 < 64 ? v[k + e + 4] : v[k + e]);
-          const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          const float top = big * c;  // -inf: no visible token
-          const bool raise = top > ref + kPLazy;
-          if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
-            float alpha = 1.f;
-            if (raise) {
-              alpha = exp2_approx(ref - top);  // 0 for the row's first
-              sum *= alpha;
-              ref = top;
-            }
-            if (j > 0) {
-              // O has to hold everything up to the tile before
-              ok = ok && mbar_wait(&o_done[qt], (j - 1) & 1, a.err);
-              tc_fence_after();
-              const float f = alpha * escale;
-#pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t x[16];
-                tmem_ld16(o_col + 16 * q, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-                tmem_st16(o_col + 16 * q, x);
-              }
-            }
-            if (h > 0) {
-              // and so do the weights of the page before
-              const uint32_t f = half2_bits(alpha, alpha);
-              tmem_wait_st();
-#pragma unroll 1
-              for (int q = 0; q < 2; ++q) {
-                uint32_t x[16];
-                tmem_ld16(s_col + 16 * q, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[k]) : "r"(x[k]), "r"(f));
-                tmem_st16(s_col + 16 * q, x);
-              }
-            }
-            escale = 1.f;
-          }
-          const float add = kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref);
-          const uint64_t c2 = pair_f32(c, c), add2 = pair_f32(add, add);
-          uint64_t s2[2] = {0, 0};  // pairs of sums from +0
-          uint32_t pw[32];
-#pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            float p0, p1;
-            unpair_f32(fma_pair(pair_f32(v[k], v[k + 1]), c2, add2), p0, p1);
-            p0 = exp2_approx(p0);
-            p1 = exp2_approx(p1);
-            s2[(k >> 1) & 1] = add_pair(s2[(k >> 1) & 1], pair_f32(p0, p1));
-            pw[k / 2] = half2_bits(p0, p1);
-          }
-          tmem_st32(s_col + 32 * h, pw);
-          float s0, s1;
-          unpair_f32(add_pair(s2[0], s2[1]), s0, s1);
-          // (a scale that is not finite has 1 / f = NaN: the rows that see its
-          // page, and only they, become NaN)
-          if (big != -INFINITY) sum = fmaf(s0 + s1, rec.rf, sum);
+          for (int k = 0; k < 64; ++k)
+            if (k > hi || (k < lo && k >= sk)) v[k] = -INFINITY;
         }
+        float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int k = 4; k < 64; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m4[e] = fmaxf(fmaxf(m4[e], v[k + e]), k + e + 4 < 64 ? v[k + e + 4] : v[k + e]);
+        const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float top = big * c;  // -inf: no visible token
+        const bool raise = top > ref + kPLazy;
+        if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
+          float alpha = escale;
+          escale = 1.f;
+          if (raise) {
+            const float f = exp2_approx(ref - top);  // 0 for the row's first
+            alpha *= f;
+            sum *= f;
+            ref = top;
+          }
+          if (j > 0) {
+            // O has to hold everything up to the page before
+            ok = ok && wait_values(qt, j - 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t x[16];
+              tmem_ld16(o_col + 16 * q, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+              tmem_st16(o_col + 16 * q, x);
+            }
+          }
+        }
+        const float add = kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref);
+        const uint64_t c2 = pair_f32(c, c), add2 = pair_f32(add, add);
+        uint64_t s2[2] = {0, 0};  // pairs of sums from +0
+        uint32_t pw[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          float p0, p1;
+          unpair_f32(fma_pair(pair_f32(v[k], v[k + 1]), c2, add2), p0, p1);
+          p0 = exp2_approx(p0);
+          p1 = exp2_approx(p1);
+          s2[(k >> 1) & 1] = add_pair(s2[(k >> 1) & 1], pair_f32(p0, p1));
+          pw[k / 2] = half2_bits(p0, p1);
+        }
+        tmem_st32(sc, pw);
+        float s0, s1;
+        unpair_f32(add_pair(s2[0], s2[1]), s0, s1);
+        // (a scale that is not finite has 1 / f = NaN: the rows that see its
+        // page, and only they, become NaN)
+        if (big != -INFINITY) sum = fmaf(s0 + s1, rec.rf, sum);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[qt]);
+        if (lane == 0) mbar_arrive(&p_full[2 * qt + (j & 1)]);
       }
     }
     __syncwarp();  // one-thread roles
@@ -569,13 +565,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 
   // ---- results
-  if (warp == kMmaW && lane == 0) {
+  if ((warp == kMmaW || warp == kMmaW + 1) && lane == 0) {
     mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
     mbar_wait(mma_end, 0, a.err);
   }
   if (warp == kCopyW && lane == 0) {
     // no copy outlives the CTA
-    for (unsigned n = n_issued > L::kRaw ? n_issued - L::kRaw : 0; n < n_issued; ++n)
+    for (int n = n_issued > L::kRaw ? n_issued - L::kRaw : 0; n < n_issued; ++n)
       if (!mbar_wait(&raw_full[n % L::kRaw], (n / L::kRaw) & 1, a.err)) break;
   }
   if (warp < kSoftW) {
@@ -583,7 +579,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     float* mine = partials + static_cast<size_t>(blockIdx.x) * (2 * kPRows * (D + 2));
     const long long orow = (qrow * a.heads + qhead);
     const bool have = qt < tiles_q && jt > 0 &&
-                      __all_sync(0xffffffffu, ok && mbar_wait(&o_done[qt], (jt - 1) & 1, a.err));
+                      __all_sync(0xffffffffu, ok && wait_values(qt, jt - 1));
     tc_fence_after();
     const float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
     if (qt < tiles_q) {
@@ -720,9 +716,8 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, long long min_rows, float* parti
   const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   int parts = 1;
   if (items < sms) {
-    const long long tiles = (static_cast<long long>(a.width) + 1) / 2;
     long long p = sms / items;
-    if (p > tiles / 4) p = tiles / 4;
+    if (p > a.width / 8) p = a.width / 8;
     if (p > 1) parts = static_cast<int>(p);
   }
   if (items * parts > 0x7FFFFFFFll) return cudaErrorInvalidValue;
