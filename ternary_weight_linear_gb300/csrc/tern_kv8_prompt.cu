@@ -20,12 +20,12 @@
 //
 // Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (S read
 // from TMEM twice, for the maximum and for the weights; P written over S);
-// 8-11 the conversion; 12 and 13 the MMAs of a query tile each (one thread:
-// its barrier waits cost about 200 cycles each, which the other's products
-// cover), the scores a page ahead of the values (two score buffers a tile), so
-// that a softmax does not wait for its scores; 14 the copies (one thread, a
-// page of a head is one contiguous block).  The MMAs of a thread run in the
-// order of their issue.
+// 8-11 the conversion; 12-15 the MMAs, for each query tile one thread that
+// issues the scores and one that issues the products with the values: a
+// barrier wait costs an issuing thread about 200 cycles even on a completed
+// phase, which the other three cover.  Each tile has two score buffers, so the
+// scores run up to two pages ahead of the values and the softmax finds them
+// ready.
 // Work: one CTA per (block of rows, sequence, head, part of the keys), the
 // longest rows first.  When there are too few blocks for the SMs the keys are
 // cut into parts, whose (max, sum, O) go to the workspace, and the last CTA of
@@ -40,10 +40,9 @@ namespace {
 
 constexpr int kPRows = 128;  // rows of a query tile
 constexpr int kSoftW = 8, kConvW = 4;
-constexpr int kMmaW = kSoftW + kConvW, kCopyW = kMmaW + 2;
-constexpr int kPThreads = (kCopyW + 1) * 32;
+constexpr int kMmaW = kSoftW + kConvW;
+constexpr int kPThreads = (kMmaW + 4) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
-constexpr int kPConv = 3;    // converted pages (keys and values)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
 
 template <int D>
@@ -54,13 +53,12 @@ struct PL {
   static constexpr int kBlockB = kBlk * 128;
   static constexpr int kTileB = kBlocks * kBlockB;     // a page's keys or values in fp16
   static constexpr int kRawB = kBlk * D;               // and as codes
-  static constexpr int kRaw = D == 128 ? 3 : 6;        // pages of codes in flight
+  static constexpr int kConv = D == 128 ? 4 : 6;       // converted pages (keys and values)
   static constexpr int kQOff = 0;
   static constexpr int kConvOff = kQOff + 2 * kQTileB;
-  static constexpr int kRawOff = kConvOff + 2 * kPConv * kTileB;
-  static constexpr int kRecOff = kRawOff + 2 * kRaw * kRawB;  // PageRec, then pages and e
+  static constexpr int kRecOff = kConvOff + 2 * kConv * kTileB;  // PageRec, then pages and e
   static constexpr int kBarOff = kRecOff + kPRecs * 24;
-  static constexpr int kNumBars = 2 * kRaw + 3 * kPConv + 4 + 4 + 4 + 1;
+  static constexpr int kNumBars = 3 * kConv + 4 + 4 + 4 + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, emax[2], last
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -141,12 +139,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint64_t* raw_empty = raw_full + L::kRaw;
-  uint64_t* k_full = raw_empty + L::kRaw;  // converted keys
-  uint64_t* v_full = k_full + kPConv;      // converted values
-  uint64_t* conv_empty = v_full + kPConv;
-  uint64_t* s_full = conv_empty + kPConv;  // [tile][buffer] scores
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // converted keys
+  uint64_t* v_full = k_full + L::kConv;                               // converted values
+  uint64_t* conv_empty = v_full + L::kConv;
+  uint64_t* s_full = conv_empty + L::kConv;  // [tile][buffer] scores
   uint64_t* p_full = s_full + 4;           // [tile][buffer] weights, O rescaled
   uint64_t* o_done = p_full + 4;           // [tile][page parity] O holds the page
   uint64_t* mma_end = o_done + 4;
@@ -180,14 +176,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int t_end = static_cast<int>(static_cast<long long>(pages.count) * (part + 1) / parts);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kRaw; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kConvW);
-    }
-    for (int s = 0; s < kPConv; ++s) {
+    for (int s = 0; s < L::kConv; ++s) {
       mbar_init(&k_full[s], kConvW);
       mbar_init(&v_full[s], kConvW);
-      mbar_init(&conv_empty[s], tiles_q);
+      mbar_init(&conv_empty[s], 2 * tiles_q);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -195,7 +187,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     emax[0] = emax[1] = -127;
-    mbar_init(mma_end, 2);
+    mbar_init(mma_end, 4);
     fence_mbar_init();
   }
   if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
@@ -284,7 +276,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int E = -127;
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
-  int n_issued = 0;  // (copies) pages requested so far
 
   for (int t0 = t_begin, chunk = 0; t0 < t_end; t0 += kPRecs, ++chunk) {
     const int t1 = t_end < t0 + kPRecs ? t_end : t0 + kPRecs;
@@ -324,78 +315,49 @@ __global__ void __launch_bounds__(kPThreads, 1)
     cta_barrier();
     const int En = emax[chunk & 1] > E ? emax[chunk & 1] : E;
 
-    if (warp == kCopyW) {
-      // ---------------------------------------------------------- copies
-      if (lane == 0 && ok) {
-        for (int i = 0; i < t1 - t0; ++i, ++n_issued) {
-          const int s = n_issued % L::kRaw;
-          if (n_issued >= L::kRaw &&
-              !mbar_wait(&raw_empty[s], ((n_issued / L::kRaw) & 1) ^ 1, a.err)) {
-            ok = false;
-            break;
-          }
-          const int page = rec_page[i];
-          mbar_arrive_expect_tx(&raw_full[s], page >= 0 ? 2 * L::kRawB : 0);
-          if (page >= 0) {
-            const int8_t* src = a.codes + (static_cast<size_t>(page) * 2 * a.hkv + hk) * L::kRawB;
-            uint8_t* dst = smem + L::kRawOff + s * (2 * L::kRawB);
-            bulk_load(dst, src, L::kRawB, &raw_full[s]);
-            bulk_load(dst + L::kRawB, src + static_cast<size_t>(a.hkv) * L::kRawB, L::kRawB,
-                      &raw_full[s]);
-          }
-        }
-      }
-    } else if (warp >= kMmaW) {
+    if (warp >= kMmaW) {
       // ---------------------------------------------------------- MMAs
-      const int i = warp - kMmaW;  // query tile
+      const int i = (warp - kMmaW) >> 1;  // query tile
+      const int j_end = jt + t1 - t0;
+      auto wait_conv = [&](uint64_t* full, int j) {
+        return mbar_wait(&full[j % L::kConv], (j / L::kConv) & 1, a.err);
+      };
+      const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
       if (lane == 0 && ok && i < tiles_q) {
-        constexpr uint32_t idesc_s = idesc_f16_f32(kPRows, kBlk, false);
-        constexpr uint32_t idesc_o = idesc_f16_f32(kPRows, D, true);
-        const uint64_t dq = desc_sw128(smem_addr(smem + L::kQOff), 16);
-        const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
-        auto wait_conv = [&](uint64_t* full, int j) {
-          return mbar_wait(&full[j % kPConv], (j / kPConv) & 1, a.err);
-        };
-        // S of page j
-        auto scores = [&](int j) {
-          const uint64_t q = dq + static_cast<uint64_t>((i * L::kQTileB) >> 4);
-          const uint64_t k = dc + static_cast<uint64_t>(((j % kPConv) * 2 * L::kTileB) >> 4);
+        if (((warp - kMmaW) & 1) == 0) {
+          // S of page j, into the columns of page j - 2's scores and weights
+          constexpr uint32_t idesc = idesc_f16_f32(kPRows, kBlk, false);
+          const uint64_t q = desc_sw128(smem_addr(smem + L::kQOff + i * L::kQTileB), 16);
+          for (int j = jt; j < j_end && ok; ++j) {
+            ok = wait_conv(k_full, j) && (j < 2 || wait_values(i, j - 2));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = dc + static_cast<uint64_t>(((j % L::kConv) * 2 * L::kTileB) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tbase + s_col(i, j),
-                   q + static_cast<uint64_t>(((kk >> 2) * L::kQBlockB + (kk & 3) * 32) >> 4),
-                   k + static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4),
-                   idesc_s, kk != 0);
-          mma_commit(&s_full[2 * i + (j & 1)]);
-        };
-        // O += P V of page j
-        auto values = [&](int j) {
-          const uint64_t v =
-              dc + static_cast<uint64_t>((((j % kPConv) * 2 + 1) * L::kTileB) >> 4);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tbase + s_col(i, j),
+                     q + static_cast<uint64_t>(((kk >> 2) * L::kQBlockB + (kk & 3) * 32) >> 4),
+                     k + static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4),
+                     idesc, kk != 0);
+            mma_commit(&s_full[2 * i + (j & 1)]);
+            mma_commit(&conv_empty[j % L::kConv]);
+          }
+        } else {
+          // O += P V of page j
+          constexpr uint32_t idesc = idesc_f16_f32(kPRows, D, true);
+          for (int j = jt; j < j_end && ok; ++j) {
+            ok = wait_conv(v_full, j) && mbar_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t v =
+                dc + static_cast<uint64_t>((((j % L::kConv) * 2 + 1) * L::kTileB) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBlk / 16; ++kk)
-            mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, j) + kk * 8,
-                   v + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o, j != 0 || kk != 0);
-          mma_commit(&o_done[2 * i + (j & 1)]);
-        };
-        const int j_end = jt + t1 - t0;
-        // The scores of page j + 1 go into the columns of page j - 1's weights,
-        // which the products issued before them read.  The conversions are in
-        // order, so page j + 1's keys come after page j's values.
-        ok = wait_conv(k_full, jt);
-        if (ok) {
-          tc_fence_after();
-          scores(jt);
-        }
-        for (int j = jt; j < j_end && ok; ++j) {
-          const bool more = j + 1 < j_end;
-          ok = more ? wait_conv(k_full, j + 1) : wait_conv(v_full, j);
-          if (ok && more) scores(j + 1);
-          ok = ok && mbar_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
-          if (!ok) break;
-          tc_fence_after();
-          values(j);
-          mma_commit(&conv_empty[j % kPConv]);
+            for (int kk = 0; kk < kBlk / 16; ++kk)
+              mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, j) + kk * 8,
+                     v + static_cast<uint64_t>((kk * 2048) >> 4), idesc, j != 0 || kk != 0);
+            mma_commit(&o_done[2 * i + (j & 1)]);
+            mma_commit(&conv_empty[j % L::kConv]);
+          }
         }
       }
     } else if (warp >= kSoftW) {
@@ -406,7 +368,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // lanes of a row's second half take the row beside it: the stores of
       // eight lanes then cover all banks
       const int c = tid % kC, row0 = (tid / kC) ^ ((c >> 2) & 1);
-      // a page's 64 rows from raw to out, times mul (and add = -1152 mul)
+      // a page's 64 rows to out, times mul (add = -1152 mul)
       auto convert = [&](const uint4 (&v)[kBlk / kStep], uint8_t* out, uint32_t mul,
                          uint32_t add) {
 #pragma unroll
@@ -432,44 +394,47 @@ __global__ void __launch_bounds__(kPThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      // Both barriers of a page are tried a page ahead, so that their answers
-      // (some 200 cycles) come under the conversion.
-      auto try_page = [&](int j) {
-        return mbar_test(&raw_full[j % L::kRaw], (j / L::kRaw) & 1) &&
-               (j < kPConv || mbar_test(&conv_empty[j % kPConv], ((j / kPConv) & 1) ^ 1));
-      };
+      // A page's codes are in registers a page ahead: their way from L2 (or
+      // HBM) comes under the conversion of the page before, and they cross
+      // shared memory once, as fp16.
       const int j_end = jt + t1 - t0;
-      bool ready = false;
-      for (int j = jt; j < j_end; ++j) {
-        const int s = j % L::kRaw, d = j % kPConv;
-        if (!ready) {
-          ok = ok && mbar_wait(&raw_full[s], (j / L::kRaw) & 1, a.err);
-          ok = ok && (j < kPConv || mbar_wait(&conv_empty[d], ((j / kPConv) & 1) ^ 1, a.err));
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* raw = smem + L::kRawOff + s * (2 * L::kRawB) + row0 * D + c * 16;
-        uint8_t* out = smem + L::kConvOff + d * (2 * L::kTileB) + (c >> 2) * L::kBlockB;
-        uint4 kv[kBlk / kStep], vv[kBlk / kStep];
+      uint4 kv[kBlk / kStep], vv[kBlk / kStep];
+      auto load_page = [&](int j) {
+        const int page = rec_page[j - jt];
+        const int8_t* src = a.codes + (static_cast<size_t>(page < 0 ? 0 : page) * 2 * a.hkv + hk) *
+                                          L::kRawB + row0 * D + c * 16;
 #pragma unroll
         for (int k = 0; k < kBlk / kStep; ++k) {
-          kv[k] = lds_v4(raw + k * kStep * D);
-          vv[k] = lds_v4(raw + L::kRawB + k * kStep * D);
+          kv[k] = vv[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (page >= 0) {
+            kv[k] = ldg_nc_v4(src + k * kStep * D);
+            vv[k] = ldg_nc_v4(src + static_cast<size_t>(a.hkv) * L::kRawB + k * kStep * D);
+          }
         }
-        // (no page: whatever the buffer holds times 0)
-        const bool there = rec_page[j - jt] >= 0;
-        const uint32_t hp = there ? half_pow2(rec_e[j - jt] - En) : 0u;
+      };
+      load_page(jt);
+      for (int j = jt; j < j_end; ++j) {
+        const int d = j % L::kConv;
+        ok = ok && (j < L::kConv ||
+                    mbar_wait(&conv_empty[d], ((j / L::kConv) & 1) ^ 1, a.err));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* out = smem + L::kConvOff + d * (2 * L::kTileB) + (c >> 2) * L::kBlockB;
+        const uint32_t hp = half_pow2(rec_e[j - jt] - En);
         const uint32_t mul = hp | (hp << 16);
         uint32_t add;  // -1152 * 2^(e - E), exact
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
-        ready = j + 1 < j_end && try_page(j + 1);
-        convert(kv, out, there ? 0x3C003C00u : 0u, there ? 0xE480E480u : 0u);
-        if (lane == 0) mbar_arrive(&k_full[d]);
-        convert(vv, out + L::kTileB, mul, add);
-        if (lane == 0) {
-          mbar_arrive(&v_full[d]);
-          mbar_arrive(&raw_empty[s]);
+        uint4 kc[kBlk / kStep], vc[kBlk / kStep];
+#pragma unroll
+        for (int k = 0; k < kBlk / kStep; ++k) {
+          kc[k] = kv[k];
+          vc[k] = vv[k];
         }
+        if (j + 1 < j_end) load_page(j + 1);
+        convert(kc, out, 0x3C003C00u, 0xE480E480u);
+        if (lane == 0) mbar_arrive(&k_full[d]);
+        convert(vc, out + L::kTileB, mul, add);
+        if (lane == 0) mbar_arrive(&v_full[d]);
       }
     } else if (qt < tiles_q) {
       // ---------------------------------------------------------- softmax
@@ -565,14 +530,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 
   // ---- results
-  if ((warp == kMmaW || warp == kMmaW + 1) && lane == 0) {
+  if (warp >= kMmaW && lane == 0) {
     mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
     mbar_wait(mma_end, 0, a.err);
-  }
-  if (warp == kCopyW && lane == 0) {
-    // no copy outlives the CTA
-    for (int n = n_issued > L::kRaw ? n_issued - L::kRaw : 0; n < n_issued; ++n)
-      if (!mbar_wait(&raw_full[n % L::kRaw], (n / L::kRaw) & 1, a.err)) break;
   }
   if (warp < kSoftW) {
     const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
