@@ -456,10 +456,11 @@ def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
         if out is None:
             out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
         if workspace is None:
-            workspace = torch.zeros(
+            workspace = torch.empty(
                 tern_kv8_attention_workspace_bytes(cache.seqs, max(1, rows), heads, kv_heads,
                                                    dim),
                 dtype=torch.uint8, device=q.device)
+            workspace[:SYNC_BYTES].zero_()  # the rest is scratch
     rc = load().tern_kv8_attention(
         ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads,
         max(1, rows) if max_new is None else int(max_new), int(window), int(sinks),

@@ -8,6 +8,8 @@
 // thresholds read once per process, and a probe that prints which rung ran
 // (section 2: every reachable branch reports itself), limited by a minimum T
 // and a line budget.  Names of the variables are this library's own.
+#include <limits.h>
+
 #include <mutex>
 #include <stdio.h>
 #include <stdlib.h>
@@ -661,6 +663,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   if (rc != TERN_OK) return rc;
   if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
       heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < 1 || window < 0 || sinks < 0 ||
+      static_cast<long long>(rows) * (heads / a.hkv) > INT_MAX ||
       !(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f) || !kv8_strides_ok(ld, hd, a.dim))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
@@ -681,7 +684,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   a.rows = rows;
   a.max_new = max_new < rows ? max_new : rows;
   a.heads = heads;
-  a.group = heads / a.hkv;
+  kv8_set_group(&a, heads / a.hkv);
   // a window of every token that the table can hold is none
   const int most_tokens = a.width * TERN_KV8_BLOCK;
   a.window = window < most_tokens ? window : 0;
@@ -699,13 +702,13 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
                    static_cast<uint32_t>(dim), kKvRowsBox,
                    a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc != TERN_OK) return rc;
-  int launches = 0;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Each sequence goes by its own rows: up to kKvFewRows per key-value head to
   // the kernel that is bound by the cache's bytes, more to the one on the
   // tensor cores.  A single sequence takes one launch, of the latter where
   // max_new allows more than the former takes.
-  const bool many = static_cast<long long>(a.max_new) * a.group > kKvFewRows;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool many = a.max_new * a.group > kKvFewRows;
+  int launches = 0;
   if (!many || a.seqs > 1) {
     if (launch_kv8_rows(&tm, a, kKvFewRows, d->sms, st, &launches) != cudaSuccess)
       return TERN_ECUDA;

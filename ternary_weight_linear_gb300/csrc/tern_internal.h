@@ -203,6 +203,7 @@ struct Kv8Args {
   // attention
   const void* q;
   int heads, group;  // query heads; query heads per key-value head
+  unsigned group_mul, group_shift;
   int window, sinks;
   float scale_log2;  // softmax scale * log2(e)
   void* out;
@@ -211,24 +212,33 @@ struct Kv8Args {
   float* partials;
   int* err;
 };
+// n / group = (high half of n * mul + n) >> shift for n < 2^31: with shift =
+// ceil(log2 group), mul = floor(2^32 (2^shift - group) / group) + 1.
+inline void kv8_set_group(Kv8Args* a, int group) {
+  a->group = group;
+  a->group_shift = 0;
+  while ((1u << a->group_shift) < static_cast<unsigned>(group)) ++a->group_shift;
+  a->group_mul = static_cast<unsigned>(((1ull << 32) * ((1ull << a->group_shift) - group)) / group +
+                                       1);
+}
 cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t stream, int* launches);
 
-// Attention of sequences with few query rows per key-value head.  tm: the
+// Attention of sequences with few query rows per key-value head (new tokens *
+// group), at most max_rows; the others are left to the prompt kernel.  tm: the
 // codes as bytes [pages * 2 * hkv * 64][dim], box dim x kKvRowsBox rows,
-// swizzle of the row's width.  Sequences with more than max_rows query rows
-// (new tokens * group) are left to the prompt kernel.
+// swizzle of the row's width.
 constexpr int kKvRowsBox = 32;
 constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
 size_t kv8_rows_partial_bytes(int dim);
 cudaError_t kv8_rows_set_attributes();
-cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, long long max_rows,
-                            int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
+                            cudaStream_t stream, int* launches);
 
 // Attention of sequences with at least min_rows query rows per key-value
 // head, on the tensor cores.  tickets: kSmallTMaxCtas zeroed ints.
 size_t kv8_prompt_partial_bytes(int dim);
 cudaError_t kv8_prompt_set_attributes();
-cudaError_t launch_kv8_prompt(const Kv8Args& a, long long min_rows, float* partials, int* tickets,
+cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches);
 
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier

@@ -2,6 +2,8 @@
 // of the index arrays, and which pages a sequence's query rows see.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "tern.h"
@@ -28,6 +30,13 @@ __device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
   s.ok = s.ok && s.len >= 0 && (static_cast<long long>(s.len) + kBlk - 1) / kBlk <= a.width &&
          s.m <= s.len && s.m <= a.max_new;
   return s;
+}
+
+// New token of row n (row = new token * group + head): n / group, by a
+// multiplication (n < 2^31; see kv8_set_group).
+__device__ __forceinline__ int kv_token(const Kv8Args& a, int n) {
+  return static_cast<int>((__umulhi(static_cast<unsigned>(n), a.group_mul) +
+                           static_cast<unsigned>(n)) >> a.group_shift);
 }
 
 // The pages that query positions [p0, p1] see: [0, sinks) then [first, last].
@@ -97,18 +106,79 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Whether the phase has completed, without waiting for it (a try_wait may
-// suspend the thread).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
+// mbar_wait for loops that pass many barriers per microsecond: the time limit
+// is kept with the SM's clock, which is read in some 20 cycles (%globaltimer
+// takes about a microsecond, which every wait that did not succeed at once
+// would pay).  Gives up after kWaitCycles, 2 s at the highest clock and
+// longer below it.
+constexpr long long kWaitCycles = 4140000000ll;
+__device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > kWaitCycles) {
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+
+// The lowest n bits of 64 (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+// A bit for each of the 64 tokens from j0 that the row at position p sees.
+__device__ __forceinline__ uint64_t kv_mask(const Kv8Args& a, int p, int j0) {
+  uint64_t see = bits_below(p - j0 + 1);
+  if (a.window) see &= ~bits_below(p - a.window + 1 - j0) | bits_below(a.sinks - j0);
+  return see;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two values as 16-bit words of the type.
+__device__ __forceinline__ uint32_t pack_out(int type, float lo, float hi) {
+  if (type != TERN_BF16) return half2_bits(lo, hi);
+  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
+         (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
+}
+// The two 16-bit elements of a word.
+__device__ __forceinline__ void unpack16(uint32_t w, int type, float& lo, float& hi) {
+  if (type == TERN_BF16) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xFFFF0000u);
+  } else {
+    lo = __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+    hi = __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
+  }
+}
+
+// Queries are held in fp16, each row scaled by a power of two that takes its
+// largest element to [2^14, 2^15): exact for every element within 2^-31 of
+// it.  big: the row's largest magnitude, as the bits of the type (which order
+// as the magnitudes do).  The power's exponent is at most 126, so that it and
+// its inverse are normal floats: rows below 2^-112 are scaled by less.
+__device__ __forceinline__ int q_exponent(uint32_t big, int type) {
+  if (big == 0) return 0;
+  const uint32_t f = type == TERN_BF16
+                         ? big << 16
+                         : __float_as_uint(__half2float(
+                               __ushort_as_half(static_cast<uint16_t>(big))));
+  const int ex = static_cast<int>(f >> 23) - 127;
+  return 14 - (ex < -112 ? -112 : ex);
+}
+__device__ __forceinline__ float pow2f(int x) {
+  return __uint_as_float(static_cast<uint32_t>(x + 127) << 23);
+}
+
+// log sum_j exp(s_j) from the weights' reference (base 2; they are 2^off times
+// larger) and sum.
+__device__ __forceinline__ float kv_log_sum(float ref, float sum, float off) {
+  return sum == 0.f ? -INFINITY : (ref - off + log2f(sum)) * 0.6931471805599453f;
 }
 
 // fp32 pairs in one 64-bit register (each half as its scalar instruction).

@@ -30,9 +30,6 @@
 // longest rows first.  When there are too few blocks for the SMs the keys are
 // cut into parts, whose (max, sum, O) go to the workspace, and the last CTA of
 // a block adds them in order.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "tern_kv8.cuh"
 
 namespace tern {
@@ -124,16 +121,10 @@ __device__ __forceinline__ void softmax_barrier() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kPThreads, 1)
-    kv8_prompt_kernel(const Kv8Args a, long long min_rows, int row_blocks, int parts,
-                      float* partials, int* tickets) {
+    kv8_prompt_kernel(const Kv8Args a, int min_rows, int row_blocks, int parts,
+                      float* __restrict__ partials, int* __restrict__ tickets) {
   using L = PL<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -162,19 +153,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int b = (item / a.hkv) % a.seqs;
   const int rb = row_blocks - 1 - item / a.hkv / a.seqs;
   const KvSeq sq = kv_seq(a, b);
-  const long long R = static_cast<long long>(sq.m) * a.group;
-  const long long r0 = static_cast<long long>(rb) * (2 * kPRows);
+  const int R = sq.m * a.group;
+  const int r0 = rb * (2 * kPRows);
   if (!sq.ok && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
   if (!sq.ok || R < min_rows || r0 >= R) return;
-  const int rows = R - r0 < 2 * kPRows ? static_cast<int>(R - r0) : 2 * kPRows;
+  const int rows = R - r0 < 2 * kPRows ? R - r0 : 2 * kPRows;
   const int tiles_q = rows > kPRows ? 2 : 1;
   const int p_base = sq.len - sq.m;
-  const int p_first = p_base + static_cast<int>(r0 / a.group);
-  const int p_last = p_base + static_cast<int>((r0 + rows - 1) / a.group);
+  const int p_first = p_base + kv_token(a, r0);
+  const int p_last = p_base + kv_token(a, r0 + rows - 1);
   const KvPages pages = kv_pages(a, p_first, p_last);
   const int t_begin = static_cast<int>(static_cast<long long>(pages.count) * part / parts);
   const int t_end = static_cast<int>(static_cast<long long>(pages.count) * (part + 1) / parts);
 
+  // warps of query tile i that have rows
+  auto soft_warps = [&](int i) {
+    const int w = (rows - i * kPRows + 31) / 32;
+    return w < 0 ? 0 : w > 4 ? 4 : w;
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kConv; ++s) {
       mbar_init(&k_full[s], kConvW);
@@ -183,7 +179,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], soft_warps(i >> 1) > 0 ? soft_warps(i >> 1) : 1);
       mbar_init(&o_done[i], 1);
     }
     emax[0] = emax[1] = -127;
@@ -205,61 +201,67 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int tr = (warp & 3) * 32 + lane;  // row of the tile
   const int r = qt * kPRows + tr;         // row of the block
   const bool live = warp < kSoftW && r < rows;
-  long long qrow = 0;
-  int qhead = 0, pos = -1;
-  float cs = 0.f;
-  if (warp < kSoftW && qt < tiles_q) {
-    if (live) {
-      const long long rr = r0 + r;
-      const int tok = static_cast<int>(rr / a.group);
-      qrow = sq.row0 + tok;
-      qhead = hk * a.group + static_cast<int>(rr % a.group);
-      pos = p_base + tok;
-    }
-    // the row scaled by a power of two into fp16, largest element in
-    // [2^14, 2^15)
-    uint32_t w[D / 2];
-    float big = 0.f;
-    const uint4* src =
-        reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qrow * a.ld +
-                                       static_cast<long long>(qhead) * a.hd);
-    auto lo_of = [&](uint32_t v) {
-      return a.type == TERN_BF16 ? __uint_as_float(v << 16)
-                                 : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
+  int pos = -1;           // its position
+  long long orow = 0;     // its row of out
+  float cs = 0.f;         // softmax scale * log2(e) * 2^-a
+  const bool soft = warp < kSoftW && (warp & 3) < soft_warps(qt);
+  if (soft) {
+    const int rr = r0 + (live ? r : rows - 1);  // (past the last: a copy of it)
+    const int tok = kv_token(a, rr);
+    const int head = hk * a.group + rr - tok * a.group;
+    const long long qrow = sq.row0 + tok;
+    if (live) pos = p_base + tok;
+    orow = qrow * a.heads + head;
+    // The warp's rows are copied to their places as they are, D / 8 lanes a
+    // row, then each thread scales its own.
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(
+        static_cast<const uint16_t*>(a.q) + qrow * a.ld + static_cast<long long>(head) * a.hd);
+    constexpr int kLanes = D / 8;
+    auto place = [&](int row, int c) {
+      return smem + L::kQOff + qt * L::kQTileB + (c >> 3) * L::kQBlockB + row * 128 +
+             (((c & 7) ^ (row & 7)) << 4);
     };
-    auto hi_of = [&](uint32_t v) {
-      return a.type == TERN_BF16 ? __uint_as_float(v & 0xFFFF0000u)
-                                 : __half2float(__ushort_as_half(static_cast<uint16_t>(v >> 16)));
-    };
+#pragma unroll 4
+    for (int i = lane / kLanes; i < 32; i += 32 / kLanes)
+      cp_async_16(place((warp & 3) * 32 + i, lane % kLanes),
+                  reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, i)) +
+                      16 * (lane % kLanes),
+                  16);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    uint32_t m2 = 0;  // the largest magnitudes of the even and the odd elements
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 v = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-      w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+    for (int c = 0; c < kLanes; ++c) {
+      const uint4 w = lds_v4(place(tr, c));
+      m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                 __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
     }
+    const uint32_t big = (m2 & 0xFFFFu) > (m2 >> 16) ? m2 & 0xFFFFu : m2 >> 16;
+    const int up = q_exponent(big, a.type);
+    const float f = pow2f(up);
+    cs = a.scale_log2 * pow2f(-up);
+#pragma unroll 1
+    for (int c0 = 0; c0 < kLanes; c0 += 4) {
+      uint4 raw[4];
 #pragma unroll
-    for (int c = 0; c < D / 2; ++c) big = fmaxf(big, fmaxf(fabsf(lo_of(w[c])), fabsf(hi_of(w[c]))));
-    int ex = static_cast<int>((__float_as_uint(big) >> 23) & 0xFF) - 127;
-    if (big == 0.f) ex = 14;
-    const int up = 14 - ex;
-    const float up1 = __uint_as_float(static_cast<uint32_t>(up / 2 + 127) << 23);
-    const float up2 = __uint_as_float(static_cast<uint32_t>(up - up / 2 + 127) << 23);
-    cs = a.scale_log2 / up1 / up2;
-    uint8_t* dst = smem + L::kQOff + qt * L::kQTileB + tr * 128;
+      for (int c = 0; c < 4; ++c) raw[c] = lds_v4(place(tr, c0 + c));
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint32_t h[4];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        h[e] = half2_bits(lo_of(w[4 * c + e]) * up1 * up2, hi_of(w[4 * c + e]) * up1 * up2);
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kQBlockB + (((c & 7) ^ (tr & 7)) << 4)) =
-          make_uint4(h[0], h[1], h[2], h[3]);
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          unpack16(w[e], a.type, lo, hi);
+          w[e] = half2_bits(lo * f, hi * f);
+        }
+        *reinterpret_cast<uint4*>(place(tr, c0 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
     fence_proxy_async_smem();
   }
   // positions of the block's last rows of tile 0 and first rows of tile 1
-  const int p_end0 =
-      p_base + static_cast<int>((r0 + (rows < kPRows ? rows : kPRows) - 1) / a.group);
-  const int p_beg1 = p_base + static_cast<int>((r0 + kPRows) / a.group);
+  const int p_end0 = p_base + kv_token(a, r0 + (rows < kPRows ? rows : kPRows) - 1);
+  const int p_beg1 = p_base + kv_token(a, r0 + kPRows);
 
   // columns of tile i's scores (and weights) of page j
   auto s_col = [](int i, int j) -> uint32_t { return L::kSCol + i * 128 + (j & 1) * kBlk; };
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // barriers of their own: page j - 2 is done before page j's scores exist,
   // which is before anyone waits for page j.
   auto wait_values = [&](int i, int j) {
-    return mbar_wait(&o_done[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+    return mbar_wait_clk(&o_done[2 * i + (j & 1)], (j >> 1) & 1, a.err);
   };
 
   int E = -127;
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int i = (warp - kMmaW) >> 1;  // query tile
       const int j_end = jt + t1 - t0;
       auto wait_conv = [&](uint64_t* full, int j) {
-        return mbar_wait(&full[j % L::kConv], (j / L::kConv) & 1, a.err);
+        return mbar_wait_clk(&full[j % L::kConv], (j / L::kConv) & 1, a.err);
       };
       const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
       if (lane == 0 && ok && i < tiles_q) {
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // O += P V of page j
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, D, true);
           for (int j = jt; j < j_end && ok; ++j) {
-            ok = wait_conv(v_full, j) && mbar_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+            ok = wait_conv(v_full, j) && mbar_wait_clk(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const uint64_t v =
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int j = jt; j < j_end; ++j) {
         const int d = j % L::kConv;
         ok = ok && (j < L::kConv ||
-                    mbar_wait(&conv_empty[d], ((j / L::kConv) & 1) ^ 1, a.err));
+                    mbar_wait_clk(&conv_empty[d], ((j / L::kConv) & 1) ^ 1, a.err));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* out = smem + L::kConvOff + d * (2 * L::kTileB) + (c >> 2) * L::kBlockB;
@@ -436,13 +438,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         convert(vc, out + L::kTileB, mul, add);
         if (lane == 0) mbar_arrive(&v_full[d]);
       }
-    } else if (qt < tiles_q) {
+    } else if (soft) {
       // ---------------------------------------------------------- softmax
       const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
       float escale = En == E ? 1.f : exp2f(static_cast<float>(E - En));
       const int j_end = jt + t1 - t0;
       for (int j = jt; j < j_end; ++j) {
-        ok = ok && mbar_wait(&s_full[2 * qt + (j & 1)], (j >> 1) & 1, a.err);
+        ok = ok && mbar_wait_clk(&s_full[2 * qt + (j & 1)], (j >> 1) & 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -456,14 +458,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float c = fmaxf(cs * rec.ks, 1e-37f);
         tmem_wait_ld();
         if (!(rec.meta >= 0 && ((rec.meta >> qt) & 1))) {
-          // limits of the visible tokens relative to the page's first
-          const int jb = (rec.meta >> 2) * kBlk;
-          const int hi = rec.meta >= 0 ? pos - jb : -1;
-          const int lo = a.window ? pos - a.window + 1 - jb : 0;
-          const int sk = a.window ? a.sinks - jb : 0;
+          const uint64_t see = rec.meta >= 0 ? kv_mask(a, pos, (rec.meta >> 2) * kBlk) : 0;
+          const uint32_t see0 = static_cast<uint32_t>(see);
+          const uint32_t see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k > hi || (k < lo && k >= sk)) v[k] = -INFINITY;
+          for (int k = 0; k < 32; ++k) {
+            if (!(see0 & (1u << k))) v[k] = -INFINITY;
+            if (!(see1 & (1u << k))) v[k + 32] = -INFINITY;
+          }
         }
         float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -532,115 +534,116 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // ---- results
   if (warp >= kMmaW && lane == 0) {
     mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
-    mbar_wait(mma_end, 0, a.err);
+    mbar_wait_clk(mma_end, 0, a.err);
   }
-  if (warp < kSoftW) {
+  constexpr size_t kPart = 2 * kPRows * (D + 2);  // O of the rows, then (ref, sum)
+  if (soft) {
     const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
-    float* mine = partials + static_cast<size_t>(blockIdx.x) * (2 * kPRows * (D + 2));
-    const long long orow = (qrow * a.heads + qhead);
-    const bool have = qt < tiles_q && jt > 0 &&
-                      __all_sync(0xffffffffu, ok && wait_values(qt, jt - 1));
+    float* mine = partials + blockIdx.x * kPart;
+    const bool have = jt > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, jt - 1));
     tc_fence_after();
     const float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
-    if (qt < tiles_q) {
+#pragma unroll 2
+    for (int q = 0; q < D / 16; ++q) {
+      uint32_t x[16];
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = 0u;
-        if (have) {
-          tmem_ld32(o_col + 32 * q, v);
-          tmem_wait_ld();
-        }
-        if (parts == 1) {
-          if (live) {
-            uint16_t* o = static_cast<uint16_t*>(a.out) + orow * D + 32 * q;
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x = __uint_as_float(v[k + 2 * e]) * inv;
-                const float y = __uint_as_float(v[k + 2 * e + 1]) * inv;
-                w[e] = a.type == TERN_BF16
-                           ? static_cast<uint32_t>(
-                                 __bfloat16_as_ushort(__float2bfloat16_rn(x))) |
-                                 (static_cast<uint32_t>(
-                                      __bfloat16_as_ushort(__float2bfloat16_rn(y)))
-                                  << 16)
-                           : half2_bits(x, y);
-              }
-              *reinterpret_cast<uint4*>(o + k) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            mine[(32 * q + k) * (2 * kPRows) + r] = __uint_as_float(v[k]) * inv;
-        }
+      for (int k = 0; k < 16; ++k) x[k] = 0u;
+      if (have) {
+        tmem_ld16(o_col + 16 * q, x);
+        tmem_wait_ld();
       }
-      if (parts == 1) {
-        if (live && a.lse)
-          a.lse[orow] = sum == 0.f ? -INFINITY
-                                   : (ref - kPOff + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        mine[D * (2 * kPRows) + r] = ref;
-        mine[(D + 1) * (2 * kPRows) + r] = sum;
+      float f[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(x[k]) * inv;
+      if (live && parts == 1) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + 16 * q);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else if (live) {
+        float4* o = reinterpret_cast<float4*>(mine + r * D + 16 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
-    if (parts > 1) {
-      // the last part to arrive adds them all, in order
-      __threadfence();
-      softmax_barrier();
-      if (threadIdx.x == 0) *is_last = atomic_add_acq_rel_gpu(&tickets[item], 1) == parts - 1;
-      softmax_barrier();
-      if (*is_last) {
-        if (threadIdx.x == 0) tickets[item] = 0;
-        if (live) {
-          const float* first = partials + static_cast<size_t>(item) * parts *
-                                              (2 * kPRows * (D + 2)) + r;
-          auto at = [&](int p, int d) {
-            return __ldcg(first + static_cast<size_t>(p) * (2 * kPRows * (D + 2)) +
-                          d * (2 * kPRows));
-          };
-          float top = -INFINITY, l = 0.f;
-          for (int p = 0; p < parts; ++p)
-            if (at(p, D + 1) != 0.f) top = fmaxf(top, at(p, D));
-          const float base = top == -INFINITY ? 0.f : top;
-          for (int p = 0; p < parts; ++p) {
-            const float s = at(p, D + 1);
-            if (s != 0.f) l += s * exp2f(at(p, D) - base);
-          }
-          for (int d0 = 0; d0 < D; d0 += 8) {
-            float acc[8];
+    if (live && parts > 1)
+      reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
+    if (live && parts == 1 && a.lse) a.lse[orow] = kv_log_sum(ref, sum, kPOff);
+  }
+  __syncwarp();
+  if (parts > 1) {
+    // the last part to arrive adds them all in order, a row per warp and the
+    // loads of four rows in flight
+    __threadfence();
+    cta_barrier();
+    if (threadIdx.x == 0) *is_last = atomic_add_acq_rel_gpu(&tickets[item], 1) == parts - 1;
+    cta_barrier();
+    if (*is_last) {
+      if (threadIdx.x == 0) tickets[item] = 0;
+      const float* first = partials + static_cast<size_t>(item) * parts * kPart;
+      constexpr int kV = D / 32;  // elements of a lane
+      constexpr int kRowsAtOnce = 4, kWarps = kPThreads / 32;
+      for (int q0 = warp; q0 < rows; q0 += kWarps * kRowsAtOnce) {
+        float top[kRowsAtOnce], l[kRowsAtOnce], acc[kRowsAtOnce][kV];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-            for (int p = 0; p < parts; ++p) {
-              const float s = at(p, D + 1);
-              if (s != 0.f) {
-                const float f = s * exp2f(at(p, D) - base);
+        for (int q = 0; q < kRowsAtOnce; ++q) {
+          top[q] = -INFINITY;
+          l[q] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, at(p, d0 + e), acc[e]);
+          for (int x = 0; x < kV; ++x) acc[q][x] = 0.f;
+        }
+#pragma unroll 2
+        for (int p = 0; p < parts; ++p) {
+          const float* from = first + p * kPart;
+          float2 ms[kRowsAtOnce];
+          float v[kRowsAtOnce][kV];
+#pragma unroll
+          for (int q = 0; q < kRowsAtOnce; ++q) {
+            const int row = q0 + q * kWarps;
+            ms[q] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int x = 0; x < kV; ++x) v[q][x] = 0.f;
+            if (row < rows) {
+              ms[q] = __ldcg(reinterpret_cast<const float2*>(from + 2 * kPRows * D) + row);
+              const float* src = from + row * D + kV * lane;
+              if constexpr (kV == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
+              } else {
+                const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+                v[q][0] = f.x, v[q][1] = f.y;
               }
             }
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = l == 0.f ? 0.f : acc[2 * e] / l;
-              const float y = l == 0.f ? 0.f : acc[2 * e + 1] / l;
-              w[e] = a.type == TERN_BF16
-                         ? static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(x))) |
-                               (static_cast<uint32_t>(
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(y)))
-                                << 16)
-                         : half2_bits(x, y);
-            }
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + d0) =
-                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (a.lse)
-            a.lse[orow] =
-                l == 0.f ? -INFINITY : (top - kPOff + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+          for (int q = 0; q < kRowsAtOnce; ++q) {
+            if (ms[q].y == 0.f) continue;  // nothing seen in that part
+            const float now = fmaxf(top[q], ms[q].x);
+            const float base = now == -INFINITY ? 0.f : now;
+            const float old = exp2f(top[q] - base), f = ms[q].y * exp2f(ms[q].x - base);
+            l[q] = l[q] * old + f;
+#pragma unroll
+            for (int x = 0; x < kV; ++x) acc[q][x] = fmaf(f, v[q][x], acc[q][x] * old);
+            top[q] = now;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kRowsAtOnce; ++q) {
+          const int row = q0 + q * kWarps;
+          if (row >= rows) continue;
+          const int tok = kv_token(a, r0 + row);
+          const long long out = static_cast<long long>(sq.row0 + tok) * a.heads + hk * a.group +
+                                (r0 + row - tok * a.group);
+          const float inv = l[q] == 0.f ? 0.f : 1.0f / l[q];
+          uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out * D) +
+                        lane * (kV / 2);
+#pragma unroll
+          for (int x = 0; x < kV; x += 2)
+            o[x / 2] = pack_out(a.type, acc[q][x] * inv, acc[q][x + 1] * inv);
+          if (a.lse && lane == 0) a.lse[out] = kv_log_sum(top[q], l[q], kPOff);
         }
       }
     }
@@ -666,9 +669,9 @@ cudaError_t kv8_prompt_set_attributes() {
                               PL<128>::kAlloc);
 }
 
-cudaError_t launch_kv8_prompt(const Kv8Args& a, long long min_rows, float* partials, int* tickets,
+cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches) {
-  const long long most = static_cast<long long>(a.max_new) * a.group;
+  const long long most = a.max_new * a.group;
   const long long row_blocks = (most + 2 * kPRows - 1) / (2 * kPRows);
   // parts of the keys: as many as fill the SMs once, each of at least four
   // tiles of the longest sequence that the table allows

@@ -27,9 +27,6 @@
 // warps stands in the loop; at a segment's end the warps' (max, sum, O) are
 // merged through shared memory.  Segments cut by a range's end go to the
 // workspace, and the last CTA to finish one adds its parts in CTA order.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "tern_kv8.cuh"
 
 namespace tern {
@@ -78,23 +75,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The two 16-bit elements of a word.
-__device__ __forceinline__ void unpack16(uint32_t w, int type, float& lo, float& hi) {
-  if (type == TERN_BF16) {
-    lo = __uint_as_float(w << 16);
-    hi = __uint_as_float(w & 0xFFFF0000u);
-  } else {
-    lo = __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
-    hi = __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
-  }
-}
-
 __device__ __forceinline__ void store_out(const Kv8Args& a, long long i, float v) {
   uint16_t* o = static_cast<uint16_t*>(a.out);
   o[i] = a.type == TERN_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
@@ -103,7 +83,7 @@ __device__ __forceinline__ void store_out(const Kv8Args& a, long long i, float v
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kRW * 32, 1)
-    kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, long long max_rows) {
+    kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, int max_rows) {
   using L = RL<D, MT>;
   constexpr int kW = D / 16;   // words of a lane per key row: 8 or 4 (k steps)
   constexpr int kNT = D / 8;   // output column tiles
@@ -367,7 +347,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         const int rec = rec_page[i];
         if (rec < 0 || !((rec >> half) & 1)) continue;
         const int s = used % L::kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (used / L::kStages) & 1, a.err));
+        ok = __all_sync(0xffffffffu, mbar_wait_clk(&full[s], (used / L::kStages) & 1, a.err));
         if (!ok) break;
         const uint8_t* kb = ring + s * L::kStage;
         const uint8_t* vb = kb + kHalf * D;
@@ -640,11 +620,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   }
   // no copy of this warp outlives it
   for (; used < issued; ++used)
-    if (!mbar_wait(&full[used % L::kStages], (used / L::kStages) & 1, a.err)) break;
+    if (!mbar_wait_clk(&full[used % L::kStages], (used / L::kStages) & 1, a.err)) break;
 }
 
 template <int D, int MT>
-cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, long long max_rows, int num_sms,
+cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
                        cudaStream_t stream, int* launches) {
   cudaLaunchAttribute attr[1];
   for (int b0 = 0; b0 < a.seqs; b0 += kKvSeqsPerLaunch) {
@@ -683,9 +663,9 @@ cudaError_t kv8_rows_set_attributes() {
   return e;
 }
 
-cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, long long max_rows,
-                            int num_sms, cudaStream_t stream, int* launches) {
-  const bool one = static_cast<long long>(a.max_new) * a.group <= 16;
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
+                            cudaStream_t stream, int* launches) {
+  const bool one = a.max_new * a.group <= 16;
   if (a.dim == 128)
     return one ? launch_one<128, 1>(tm, a, max_rows, num_sms, stream, launches)
                : launch_one<128, 2>(tm, a, max_rows, num_sms, stream, launches);
