@@ -328,8 +328,8 @@ int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
 }
 
 // Query rows per key-value head (new tokens times group) up to which a
-// sequence takes the few-row kernel: two of its 16-row tiles.
-constexpr int kKvFewRows = 32;
+// sequence takes the few-row kernel: its tile.
+constexpr int kKvFewRows = 16;
 
 // Strides of a [rows][heads][dim] operand: rows and heads start on 16 bytes
 // and a head's elements are consecutive.
