@@ -127,8 +127,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                       float* __restrict__ partials, int* __restrict__ tickets) {
   using L = PL<D>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // converted keys
   uint64_t* v_full = k_full + L::kConv;                               // converted values

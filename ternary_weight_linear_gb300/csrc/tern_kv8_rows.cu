@@ -48,8 +48,8 @@ struct RL {
   static constexpr int kRing = kRW * kStages * kStage;  // 1024-aligned stages
   static constexpr int kQStride = 2 * D + 16;           // bytes of a staged query row
   static constexpr int kQOff = kRing;
-  static constexpr int kMergeOff = kQOff + kRows * kQStride;  // [kRW][4][D] fp32
-  static constexpr int kMlOff = kMergeOff + kRW * 4 * D * 4;  // [kRW][kRows] (ref, sum)
+  static constexpr int kMergeOff = kQOff + kRows * kQStride;  // [kRW][2][D] fp32
+  static constexpr int kMlOff = kMergeOff + kRW * 2 * D * 4;  // [kRW][kRows] (ref, sum)
   static constexpr int kFacOff = kMlOff + kRW * kRows * 8;    // [kRows][kRW] factors
   static constexpr int kTotOff = kFacOff + kRW * kRows * 4;   // [kRows] (ref, sum)
   static constexpr int kQScaleOff = kTotOff + kRows * 8;      // [kRows] 2^-a
@@ -94,8 +94,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   constexpr int kVW = D / 32;  // words of a lane per value row: 4 or 2
   grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff) + warp * L::kStages;
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
       return make_int2(seq_row0[b] + tok, hk * a.group + r - tok * a.group);
     };
 
-    // queries: each warp scales two rows by a power of two into fp16
+    // queries: each warp scales one or two rows by a power of two into fp16
     {
       uint32_t raw[2][D / 64];
 #pragma unroll
@@ -250,6 +249,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = warp + x * kRW;
+        if (r >= kRows) break;
         uint32_t m2 = 0;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) m2 = __vmaxu2(m2, raw[x][e] & 0x7FFF7FFFu);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
       // this warp's half-pages of [u, piece): those congruent to its number
       const int h_end = static_cast<int>(2 * (piece - c0));
       int h = static_cast<int>(2 * (u - c0));
-      h += (warp - h) & (kRW - 1);
+      h += (warp + kRW - h % kRW) % kRW;
       for (; h < h_end && ok; h += kRW) {
         const int rec_row = where[h >> 1];
         const int half = h & 1;
@@ -361,29 +361,33 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         const uint8_t* vb = kb + kHalf * D;
 
         // S = Q Kc^T for 32 tokens
+        // (the four column tiles side by side: four independent chains of
+        // products)
         float sc[4][4];
+        uint32_t kw[4][kW];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
-          uint32_t w[kW];
           const uint8_t* kr = kb + (8 * n + g) * D;
           if constexpr (D == 128) {
             const uint4 x = lds_v4(kr + (((2 * t) ^ g) << 4));
             const uint4 y = lds_v4(kr + (((2 * t + 1) ^ g) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+            kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
+            kw[n][4] = y.x, kw[n][5] = y.y, kw[n][6] = y.z, kw[n][7] = y.w;
           } else {
             const uint4 x = lds_v4(kr + ((t ^ ((g >> 1) & 3)) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-          }
-#pragma unroll
-          for (int j = 0; j < kW; ++j) {
-            uint32_t b0, b1;
-            codes_to_half(w[j], b0, b1);
-            mma_16816(sc[n], qf[j], b0, b1);
+            kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
           }
         }
+#pragma unroll
+        for (int j = 0; j < kW; ++j)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            uint32_t b0, b1;
+            codes_to_half(kw[n][j], b0, b1);
+            mma_16816(sc[n], qf[j], b0, b1);
+          }
         if (!(rec_row & (kMAll << half))) {
           const int in = static_cast<int>((h >> 1) + c0 - s_begin);
           const int j0 = pages.page(in) * kBlk + half * kHalf;
@@ -398,6 +402,24 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           }
         }
 
+        // the values' codes, on their way under the softmax
+        uint32_t vw[2][4][kVW];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t(&w)[4][kVW] = vw[k];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the step's 16
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = 16 * k + 2 * t + (x & 1) + 8 * (x >> 1);
+            if constexpr (D == 128) {
+              const uint4 v = lds_v4(vb + row * D + ((g ^ (row & 7)) << 4));
+              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+            } else {
+              const uint2 v =
+                  lds_v2(vb + row * D + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
+              w[x][0] = v.x, w[x][1] = v.y;
+            }
+          }
+        }
         // softmax of the half-page
         const int En = rec.e > E ? rec.e : E;
         float scale[2] = {1.f, 1.f};
@@ -462,19 +484,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(vadd) : "r"(vmul), "r"(0xE480E480u));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t w[4][kVW];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the step's 16
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = 16 * k + 2 * t + (x & 1) + 8 * (x >> 1);
-            if constexpr (D == 128) {
-              const uint4 v = lds_v4(vb + row * D + ((g ^ (row & 7)) << 4));
-              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
-            } else {
-              const uint2 v =
-                  lds_v2(vb + row * D + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
-              w[x][0] = v.x, w[x][1] = v.y;
-            }
-          }
+          const uint32_t(&w)[4][kVW] = vw[k];
 #pragma unroll
           for (int q = 0; q < kVW; ++q) {
             const uint32_t lo[2] = {__byte_perm(w[0][q], w[1][q], 0x5140) ^ 0x80808080u,
@@ -513,19 +523,20 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     if (lane == 0) wexp[warp] = E;
     const bool whole = s_begin >= u_begin && s_end <= u_end;
     __syncthreads();
-    if (threadIdx.x < kRows * kRW) {
+    if (threadIdx.x < kRows * 16) {
       // factor of warp w's O in row r: its weight over the sum, in units of 1
-      const int r = threadIdx.x / kRW, w = threadIdx.x % kRW;
-      const float2 v = ml[w * kRows + r];
+      const int r = threadIdx.x / 16, w = threadIdx.x % 16;
+      const float2 v = w < kRW ? ml[w * kRows + r] : make_float2(0.f, 0.f);
       float big = v.y == 0.f ? -INFINITY : v.x;
 #pragma unroll
-      for (int k = kRW / 2; k > 0; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+      for (int k = 8; k > 0; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
       const float base = big == -INFINITY ? 0.f : big;
       const float f = v.y == 0.f ? 0.f : exp2f(v.x - base);
       float l = v.y == 0.f ? 0.f : v.y * f;
 #pragma unroll
-      for (int k = kRW / 2; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-      fac[r * kRW + w] = l == 0.f ? 0.f : f / l * exp2f(static_cast<float>(wexp[w]));
+      for (int k = 8; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      if (w < kRW)
+        fac[r * kRW + w] = l == 0.f ? 0.f : f / l * exp2f(static_cast<float>(wexp[w]));
       if (w == 0) tot[r] = make_float2(big, l);
     }
     const long long cta_first = whole ? 0 : s_begin / per;
@@ -533,11 +544,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
       return a.partials + (2 * cta + (cta == cta_first ? 1 : 0)) * (kRows * (D + 2));
     };
     float* mine = part_of(blockIdx.x);
-    for (int r0 = 0; r0 < R; r0 += 4) {
-      // rows r0 .. r0 + 3 of every warp
+    for (int r0 = 0; r0 < R; r0 += 2) {
+      // rows r0 and r0 + 1 of every warp
       const int x = (r0 >> 3) & 1;
-      if ((g >> 2) == ((r0 >> 2) & 1)) {
-        float* dst = merge + (warp * 4 + (g & 3)) * D + (D / 4) * t;
+      if ((g >> 1) == ((r0 >> 1) & 3)) {
+        float* dst = merge + (warp * 2 + (g & 1)) * D + (D / 4) * t;
 #pragma unroll
         for (int n = 0; n < kNT; n += 4) {
           *reinterpret_cast<float4*>(dst + n) =
@@ -549,34 +560,23 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         }
       }
       __syncthreads();
-      // two (one) elements of a row per thread, 64 threads a row
-      constexpr int kV = D / 64;
-      const int r = r0 + threadIdx.x / 64, d = (threadIdx.x % 64) * kV;
-      if (r < R) {
-        float acc[kV];
-#pragma unroll
-        for (int y = 0; y < kV; ++y) acc[y] = 0.f;
+      const int r = r0 + threadIdx.x / D, d = threadIdx.x % D;
+      if (threadIdx.x < 2 * D && r < R) {
+        float acc = 0.f;
 #pragma unroll
         for (int w = 0; w < kRW; ++w) {
           const float f = fac[r * kRW + w];
-#pragma unroll
-          for (int y = 0; y < kV; ++y)
-            if (f != 0.f) acc[y] = fmaf(f, merge[(w * 4 + threadIdx.x / 64) * D + d + y], acc[y]);
+          if (f != 0.f) acc = fmaf(f, merge[(w * 2 + threadIdx.x / D) * D + d], acc);
         }
         const float2 v = tot[r];
         if (whole) {
           const int2 at = row_of(r);
           const long long ob = static_cast<long long>(at.x) * a.heads + at.y;
-          if constexpr (kV == 2)
-            reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + ob * D)[d / 2] =
-                pack_out(a.type, acc[0], acc[1]);
-          else
-            static_cast<uint16_t*>(a.out)[ob * D + d] =
-                static_cast<uint16_t>(pack_out(a.type, acc[0], 0.f));
+          static_cast<uint16_t*>(a.out)[ob * D + d] =
+              static_cast<uint16_t>(pack_out(a.type, acc, 0.f));
           if (a.lse && d == 0) a.lse[ob] = kv_log_sum(v.x, v.y, kROff);
         } else {
-#pragma unroll
-          for (int y = 0; y < kV; ++y) mine[r * D + d + y] = acc[y];
+          mine[r * D + d] = acc;
           if (d == 0) reinterpret_cast<float2*>(mine + kRows * D)[r] = v;
         }
       }
