@@ -124,6 +124,11 @@ __device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, in
   }
 }
 
+// Requests the 128-byte line of src into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+}
+
 // The lowest n bits of 64 (none for n <= 0, all for n >= 64).
 __device__ __forceinline__ uint64_t bits_below(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;

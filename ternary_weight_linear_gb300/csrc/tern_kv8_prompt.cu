@@ -40,6 +40,7 @@ constexpr int kSoftW = 8, kConvW = 4;
 constexpr int kMmaW = kSoftW + kConvW;
 constexpr int kPThreads = (kMmaW + 4) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
+constexpr int kAhead = 4;    // pages requested into L2 ahead of their conversion (kSplit)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
 
 template <int D>
@@ -116,12 +117,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void cta_barrier() {
   asm volatile("bar.sync 0;" ::: "memory");
 }
-// The softmax warps.
-__device__ __forceinline__ void softmax_barrier() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-
-template <int D>
+// kSplit: no sequence of the batch has more than kSplitRows = 64 rows for a
+// key-value head.  Both query tiles are then the same rows and take alternate
+// pages (page j of the CTA is tile i's page j / 2, for j % 2 == i), joined at
+// the end, and the four softmax warps without rows are a second group for the
+// conversion.  Measured, with it and without: 36.5 and 42.9 us (8 sequences, 20
+// rows, window 4096), 92 and 123 us (4 sequences of 32000 tokens, 24 rows); at
+// 96 rows, where no warps are idle, it loses (46.5 and 43.2 us, 16 tokens over
+// 16000).
+constexpr int kSplitRows = 64;
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv8_prompt_kernel(const Kv8Args a, int min_rows, int row_blocks, int parts,
                       float* __restrict__ partials, int* __restrict__ tickets) {
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (!sq.ok && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
   if (!sq.ok || R < min_rows || r0 >= R) return;
   const int rows = R - r0 < 2 * kPRows ? R - r0 : 2 * kPRows;
-  const int tiles_q = rows > kPRows ? 2 : 1;
+  const int tiles_q = rows > kPRows ? 2 : 1;  // that see a page
+  constexpr int kStep = kSplit ? 2 : 1;
   const int p_base = sq.len - sq.m;
   const int p_first = p_base + kv_token(a, r0);
   const int p_last = p_base + kv_token(a, r0 + rows - 1);
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   // warps of query tile i that have rows
   auto soft_warps = [&](int i) {
-    const int w = (rows - i * kPRows + 31) / 32;
+    const int w = (rows - (kSplit ? 0 : i * kPRows) + 31) / 32;
     return w < 0 ? 0 : w > 4 ? 4 : w;
   };
   if (threadIdx.x == 0) {
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int qt = warp >> 2;  // query tile (softmax warps)
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const int tr = (warp & 3) * 32 + lane;  // row of the tile
-  const int r = qt * kPRows + tr;         // row of the block
+  const int r = (kSplit ? 0 : qt * kPRows) + tr;  // row of the block
   const bool live = warp < kSoftW && r < rows;
   int pos = -1;           // its position
   long long orow = 0;     // its row of out
@@ -260,18 +266,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   // positions of the block's last rows of tile 0 and first rows of tile 1
   const int p_end0 = p_base + kv_token(a, r0 + (rows < kPRows ? rows : kPRows) - 1);
-  const int p_beg1 = p_base + kv_token(a, r0 + kPRows);
+  const int p_beg1 = kSplit ? p_first : p_base + kv_token(a, r0 + kPRows);
 
-  // columns of tile i's scores (and weights) of page j
-  auto s_col = [](int i, int j) -> uint32_t { return L::kSCol + i * 128 + (j & 1) * kBlk; };
+  // columns of tile i's scores (and weights) of its page n
+  auto s_col = [](int i, int n) -> uint32_t { return L::kSCol + i * 128 + (n & 1) * kBlk; };
 
   int jt = 0;  // pages so far
-  // Waits until tile i's O holds page j.  Two pages may be under way and a
+  // Waits until tile i's O holds its page n.  Two pages may be under way and a
   // parity tells only neighbouring phases apart, so odd and even pages have
-  // barriers of their own: page j - 2 is done before page j's scores exist,
-  // which is before anyone waits for page j.
-  auto wait_values = [&](int i, int j) {
-    return mbar_wait_clk(&o_done[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+  // barriers of their own: page n - 2 is done before page n's scores exist,
+  // which is before anyone waits for page n.
+  auto wait_values = [&](int i, int n) {
+    return mbar_wait_clk(&o_done[2 * i + (n & 1)], (n >> 1) & 1, a.err);
   };
 
   int E = -127;
@@ -324,57 +330,62 @@ __global__ void __launch_bounds__(kPThreads, 1)
         return mbar_wait_clk(&full[j % L::kConv], (j / L::kConv) & 1, a.err);
       };
       const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
-      if (lane == 0 && ok && i < tiles_q) {
+      if (lane == 0 && ok && (kSplit || i < tiles_q)) {
         if (((warp - kMmaW) & 1) == 0) {
-          // S of page j, into the columns of page j - 2's scores and weights
+          // S of page n, into the columns of page n - 2's scores and weights
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, kBlk, false);
           const uint64_t q = desc_sw128(smem_addr(smem + L::kQOff + i * L::kQTileB), 16);
-          for (int j = jt; j < j_end && ok; ++j) {
-            ok = wait_conv(k_full, j) && (j < 2 || wait_values(i, j - 2));
+          for (int j = jt + (kSplit ? i : 0); j < j_end && ok; j += kStep) {
+            const int n = j / kStep;
+            ok = wait_conv(k_full, j) && (n < 2 || wait_values(i, n - 2));
             if (!ok) break;
             tc_fence_after();
             const uint64_t k = dc + static_cast<uint64_t>(((j % L::kConv) * 2 * L::kTileB) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tbase + s_col(i, j),
+              mma_ss(tbase + s_col(i, n),
                      q + static_cast<uint64_t>(((kk >> 2) * L::kQBlockB + (kk & 3) * 32) >> 4),
                      k + static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4),
                      idesc, kk != 0);
-            mma_commit(&s_full[2 * i + (j & 1)]);
+            mma_commit(&s_full[2 * i + (n & 1)]);
             mma_commit(&conv_empty[j % L::kConv]);
           }
         } else {
           // O += P V of page j
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, D, true);
-          for (int j = jt; j < j_end && ok; ++j) {
-            ok = wait_conv(v_full, j) && mbar_wait_clk(&p_full[2 * i + (j & 1)], (j >> 1) & 1, a.err);
+          for (int j = jt + (kSplit ? i : 0); j < j_end && ok; j += kStep) {
+            const int n = j / kStep;
+            ok = wait_conv(v_full, j) && mbar_wait_clk(&p_full[2 * i + (n & 1)], (n >> 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const uint64_t v =
                 dc + static_cast<uint64_t>((((j % L::kConv) * 2 + 1) * L::kTileB) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kBlk / 16; ++kk)
-              mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, j) + kk * 8,
-                     v + static_cast<uint64_t>((kk * 2048) >> 4), idesc, j != 0 || kk != 0);
-            mma_commit(&o_done[2 * i + (j & 1)]);
+              mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, n) + kk * 8,
+                     v + static_cast<uint64_t>((kk * 2048) >> 4), idesc, n != 0 || kk != 0);
+            mma_commit(&o_done[2 * i + (n & 1)]);
             mma_commit(&conv_empty[j % L::kConv]);
           }
         }
       }
-    } else if (warp >= kSoftW) {
+    } else if (warp >= kSoftW || (kSplit && (warp & 2))) {
       // ---------------------------------------------------------- conversion
-      const int tid = threadIdx.x - kSoftW * 32;
+      constexpr int groups = kSplit ? 2 : 1;
+      const int group = warp >= kSoftW ? 0 : 1;
+      const int tid =
+          (group ? (warp & 1) + ((warp >> 1) & 2) : warp - kSoftW) * 32 + lane;
       constexpr int kC = D / 16;            // 16-byte chunks of a row of codes
-      constexpr int kStep = 128 / kC;       // rows per step
+      constexpr int kRowStep = 128 / kC;    // rows per step
       // lanes of a row's second half take the row beside it: the stores of
       // eight lanes then cover all banks
       const int c = tid % kC, row0 = (tid / kC) ^ ((c >> 2) & 1);
       // a page's 64 rows to out, times mul (add = -1152 mul)
-      auto convert = [&](const uint4 (&v)[kBlk / kStep], uint8_t* out, uint32_t mul,
+      auto convert = [&](const uint4 (&v)[kBlk / kRowStep], uint8_t* out, uint32_t mul,
                          uint32_t add) {
 #pragma unroll
-        for (int k = 0; k < kBlk / kStep; ++k) {
-          const int row = row0 + k * kStep;
+        for (int k = 0; k < kBlk / kRowStep; ++k) {
+          const int row = row0 + k * kRowStep;
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           uint32_t o[8];
 #pragma unroll
@@ -395,27 +406,42 @@ __global__ void __launch_bounds__(kPThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      // A page's codes are in registers a page ahead: their way from L2 (or
+      // A page's codes are in registers a page (of the group) ahead: their way from L2 (or
       // HBM) comes under the conversion of the page before, and they cross
       // shared memory once, as fp16.
       const int j_end = jt + t1 - t0;
-      uint4 kv[kBlk / kStep], vv[kBlk / kStep];
+      uint4 kv[kBlk / kRowStep], vv[kBlk / kRowStep];
       auto load_page = [&](int j) {
         const int page = rec_page[j - jt];
         const int8_t* src = a.codes + (static_cast<size_t>(page < 0 ? 0 : page) * 2 * a.hkv + hk) *
                                           L::kRawB + row0 * D + c * 16;
 #pragma unroll
-        for (int k = 0; k < kBlk / kStep; ++k) {
+        for (int k = 0; k < kBlk / kRowStep; ++k) {
           kv[k] = vv[k] = make_uint4(0u, 0u, 0u, 0u);
           if (page >= 0) {
-            kv[k] = ldg_nc_v4(src + k * kStep * D);
-            vv[k] = ldg_nc_v4(src + static_cast<size_t>(a.hkv) * L::kRawB + k * kStep * D);
+            kv[k] = ldg_nc_v4(src + k * kRowStep * D);
+            vv[k] = ldg_nc_v4(src + static_cast<size_t>(a.hkv) * L::kRawB + k * kRowStep * D);
           }
         }
       };
-      load_page(jt);
-      for (int j = jt; j < j_end; ++j) {
+      // (few rows: a page is read once, from HBM; a line per thread is
+      // requested into L2 kAhead pages before)
+      constexpr int kLines = L::kRawB / 128;  // of a page's keys or values
+      auto request_page = [&](int j) {
+        const int page = rec_page[j - jt];
+        if (page >= 0 && tid < 2 * kLines)
+          prefetch_l2(a.codes + ((static_cast<size_t>(page) * 2 + tid / kLines) * a.hkv + hk) *
+                                    L::kRawB + tid % kLines * 128);
+      };
+      if (kSplit)
+        for (int j = jt + group; j < jt + kAhead && j < j_end; j += groups) request_page(j);
+      if (!kSplit) load_page(jt);
+      for (int j = jt + group; j < j_end; j += groups) {
         const int d = j % L::kConv;
+        if (kSplit) {
+          if (j + kAhead < j_end) request_page(j + kAhead);
+          load_page(j);
+        }
         ok = ok && (j < L::kConv ||
                     mbar_wait_clk(&conv_empty[d], ((j / L::kConv) & 1) ^ 1, a.err));
         ok = __all_sync(0xffffffffu, ok);
@@ -425,16 +451,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint32_t mul = hp | (hp << 16);
         uint32_t add;  // -1152 * 2^(e - E), exact
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
-        uint4 kc[kBlk / kStep], vc[kBlk / kStep];
+        auto both = [&](const uint4 (&kc)[kBlk / kRowStep], const uint4 (&vc)[kBlk / kRowStep]) {
+          convert(kc, out, 0x3C003C00u, 0xE480E480u);
+          if (lane == 0) mbar_arrive(&k_full[d]);
+          convert(vc, out + L::kTileB, mul, add);
+        };
+        if constexpr (kSplit) {
+          both(kv, vv);
+        } else {
+          uint4 kc[kBlk / kRowStep], vc[kBlk / kRowStep];
 #pragma unroll
-        for (int k = 0; k < kBlk / kStep; ++k) {
-          kc[k] = kv[k];
-          vc[k] = vv[k];
+          for (int k = 0; k < kBlk / kRowStep; ++k) {
+            kc[k] = kv[k];
+            vc[k] = vv[k];
+          }
+          if (j + 1 < j_end) load_page(j + 1);
+          both(kc, vc);
         }
-        if (j + 1 < j_end) load_page(j + 1);
-        convert(kc, out, 0x3C003C00u, 0xE480E480u);
-        if (lane == 0) mbar_arrive(&k_full[d]);
-        convert(vc, out + L::kTileB, mul, add);
         if (lane == 0) mbar_arrive(&v_full[d]);
       }
     } else if (soft) {
@@ -442,13 +475,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
       float escale = En == E ? 1.f : exp2f(static_cast<float>(E - En));
       const int j_end = jt + t1 - t0;
-      for (int j = jt; j < j_end; ++j) {
-        ok = ok && mbar_wait_clk(&s_full[2 * qt + (j & 1)], (j >> 1) & 1, a.err);
+      for (int j = jt + (kSplit ? qt : 0); j < j_end; j += kStep) {
+        const int n = j / kStep;
+        ok = ok && mbar_wait_clk(&s_full[2 * qt + (n & 1)], (n >> 1) & 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         // the page's 64 scores in registers, read once
-        const uint32_t sc = tbase + lane_off + s_col(qt, j);
+        const uint32_t sc = tbase + lane_off + s_col(qt, n);
         float v[64];
         tmem_ld32(sc, reinterpret_cast<uint32_t*>(v));
         tmem_ld32(sc + 32, reinterpret_cast<uint32_t*>(v) + 32);
@@ -484,9 +518,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
             sum *= f;
             ref = top;
           }
-          if (j > 0) {
+          if (n > 0) {
             // O has to hold everything up to the page before
-            ok = ok && wait_values(qt, j - 1);
+            ok = ok && wait_values(qt, n - 1);
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -522,7 +556,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * qt + (j & 1)]);
+        if (lane == 0) mbar_arrive(&p_full[2 * qt + (n & 1)]);
       }
     }
     __syncwarp();  // one-thread roles
@@ -535,13 +569,33 @@ __global__ void __launch_bounds__(kPThreads, 1)
     mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
     mbar_wait_clk(mma_end, 0, a.err);
   }
+  __syncwarp();
+  if (kSplit) cta_barrier();  // no converted page is read any more
   constexpr size_t kPart = 2 * kPRows * (D + 2);  // O of the rows, then (ref, sum)
   if (soft) {
+    const bool mine_out = !(kSplit && qt);  // (tile 0 writes for both)
+    // both tiles' softmax warps
+    auto softmax_barrier = [&] { asm volatile("bar.sync 1, %0;" ::"r"(64 * soft_warps(0)) : "memory"); };
     const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
     float* mine = partials + blockIdx.x * kPart;
-    const bool have = jt > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, jt - 1));
+    const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
+    const bool have = n > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, n - 1));
     tc_fence_after();
-    const float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
+    float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
+    float inv1 = 0.f;  // tile 1's share of the sum
+    // tile 1's sixteen columns q of the row, in the converted pages' place
+    float4* other = reinterpret_cast<float4*>(smem + L::kConvOff) + tr;
+    if (kSplit && qt == 0) {
+      softmax_barrier();  // (tile 1 has written)
+      const float2 ms = *reinterpret_cast<const float2*>(other + (D / 4) * kPRows);
+      const float top = fmaxf(ref, ms.x), base = top == -INFINITY ? 0.f : top;
+      const float w0 = sum * exp2f(ref - base), w1 = ms.y * exp2f(ms.x - base);
+      const float all = w0 + w1;
+      inv = all == 0.f ? 0.f : inv * (w0 / all);
+      inv1 = all == 0.f ? 0.f : w1 / all;
+      ref = top;
+      sum = all;
+    }
 #pragma unroll 2
     for (int q = 0; q < D / 16; ++q) {
       uint32_t x[16];
@@ -554,7 +608,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
       float f[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(x[k]) * inv;
-      if (live && parts == 1) {
+      if (kSplit) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float4* o = other + (4 * q + k) * kPRows;
+          if (qt) {
+            *o = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          } else {
+            const float4 y = *o;
+            f[4 * k] = fmaf(y.x, inv1, f[4 * k]);
+            f[4 * k + 1] = fmaf(y.y, inv1, f[4 * k + 1]);
+            f[4 * k + 2] = fmaf(y.z, inv1, f[4 * k + 2]);
+            f[4 * k + 3] = fmaf(y.w, inv1, f[4 * k + 3]);
+          }
+        }
+      }
+      if (!mine_out) {
+      } else if (live && parts == 1) {
         uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
@@ -568,9 +638,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
-    if (live && parts > 1)
+    if (kSplit && qt) {
+      *reinterpret_cast<float2*>(other + (D / 4) * kPRows) = make_float2(ref, sum);
+      softmax_barrier();
+    }
+    if (mine_out && live && parts > 1)
       reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
-    if (live && parts == 1 && a.lse) a.lse[orow] = kv_log_sum(ref, sum, kPOff);
+    if (mine_out && live && parts == 1 && a.lse) a.lse[orow] = kv_log_sum(ref, sum, kPOff);
   }
   __syncwarp();
   if (parts > 1) {
@@ -661,11 +735,14 @@ size_t kv8_prompt_partial_bytes(int dim) {
 }
 
 cudaError_t kv8_prompt_set_attributes() {
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv8_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PL<64>::kAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kv8_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              PL<128>::kAlloc);
+  const auto allow = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  cudaError_t e = allow(kv8_prompt_kernel<64, false>, PL<64>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<64, true>, PL<64>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, false>, PL<128>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, true>, PL<128>::kAlloc);
+  return e;
 }
 
 cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
@@ -684,22 +761,16 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
   }
   if (items * parts > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
-  const dim3 grid(static_cast<unsigned>(items * parts));
-  if (a.dim == 128) {
-    const cudaLaunchConfig_t cfg =
-        pdl_launch_config(attr, grid, dim3(kPThreads), PL<128>::kAlloc, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<128>, a, min_rows,
-                                             static_cast<int>(row_blocks), parts, partials,
-                                             tickets);
-    if (e != cudaSuccess) return e;
-  } else {
-    const cudaLaunchConfig_t cfg =
-        pdl_launch_config(attr, grid, dim3(kPThreads), PL<64>::kAlloc, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<64>, a, min_rows,
-                                             static_cast<int>(row_blocks), parts, partials,
-                                             tickets);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaLaunchConfig_t cfg =
+      pdl_launch_config(attr, dim3(static_cast<unsigned>(items * parts)), dim3(kPThreads),
+                        a.dim == 128 ? PL<128>::kAlloc : PL<64>::kAlloc, stream);
+  const auto kernel = most <= kSplitRows
+                          ? (a.dim == 128 ? kv8_prompt_kernel<128, true> : kv8_prompt_kernel<64, true>)
+                          : (a.dim == 128 ? kv8_prompt_kernel<128, false>
+                                          : kv8_prompt_kernel<64, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, min_rows, static_cast<int>(row_blocks),
+                                           parts, partials, tickets);
+  if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;
 }
