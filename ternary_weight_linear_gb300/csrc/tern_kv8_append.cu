@@ -69,17 +69,10 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
   const int pg = begin / kBlk + static_cast<int>(blockIdx.x);
   if (pg > (s.len - 1) / kBlk) return;
   const int page = a.table[static_cast<size_t>(b) * a.width + pg];
-  if (page < 0 || page >= a.pages) {
-    if (threadIdx.x == 0) atomicOr(a.err, kErrIndex);
-    return;
-  }
-  const size_t blk = (static_cast<size_t>(page) * 2 + which) * a.hkv + h;
-  int8_t* codes = a.codes + blk * (kBlk * D);
   const int first = begin > pg * kBlk ? begin - pg * kBlk : 0;       // new slots [first, last)
   const int last = s.len - pg * kBlk < kBlk ? s.len - pg * kBlk : kBlk;
   const int chunk = threadIdx.x % kChunks, slot0 = threadIdx.x / kChunks;
   const void* src = which ? a.v : a.k;
-  const float old = first > 0 ? a.scales[blk] : 0.f;
 
   float x[kSteps][8];
   float amax = 0.f;
@@ -94,6 +87,14 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
       for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
     }
   }
+  // only now: the rows' loads need not wait for the table's
+  if (page < 0 || page >= a.pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+    return;
+  }
+  const size_t blk = (static_cast<size_t>(page) * 2 + which) * a.hkv + h;
+  int8_t* codes = a.codes + blk * (kBlk * D);
+  const float old = first > 0 ? a.scales[blk] : 0.f;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i)
 #pragma unroll

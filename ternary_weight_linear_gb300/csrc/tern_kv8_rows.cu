@@ -37,19 +37,21 @@ namespace {
 
 constexpr int kRW = 8;        // warps
 constexpr int kHalf = 32;     // tokens of a stage
-constexpr int kRows = 16;     // rows of the tile
+constexpr int kMergeRows = 4; // rows merged at a time
 constexpr int kRecs = 256;    // pages whose records are held at a time
 constexpr float kROff = 10.f, kRLazy = 4.f;
 
-template <int D>
+// D: elements of a head.  NT: tiles of eight rows.
+template <int D, int NT>
 struct RL {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * kHalf * D;  // bytes: keys, then values
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kRing = kRW * kStages * kStage;  // 1024-aligned stages
   static constexpr int kQStride = 2 * D + 16;           // bytes of a staged query row
   static constexpr int kQOff = kRing;
-  static constexpr int kMergeOff = kQOff + kRows * kQStride;  // [kRW][2][D] fp32
-  static constexpr int kMlOff = kMergeOff + kRW * 2 * D * 4;  // [kRW][kRows] (ref, sum)
+  static constexpr int kMergeOff = kQOff + kRows * kQStride;  // [kRW][kMergeRows][D] fp32
+  static constexpr int kMlOff = kMergeOff + kRW * kMergeRows * D * 4;  // [kRW][kRows] (ref, sum)
   static constexpr int kFacOff = kMlOff + kRW * kRows * 8;    // [kRows][kRW] factors
   static constexpr int kTotOff = kFacOff + kRW * kRows * 4;   // [kRows] (ref, sum)
   static constexpr int kQScaleOff = kTotOff + kRows * 8;      // [kRows] 2^-a
@@ -84,13 +86,21 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The transpose of the warp's 8 x 8 matrix of 16-bit elements (lane 4 i + j
+// holds elements 2 j and 2 j + 1 of row i).
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kRW * 32, 1)
     kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, int max_rows) {
-  using L = RL<D>;
+  using L = RL<D, NT>;
+  constexpr int kRows = L::kRows;
   constexpr int kW = D / 16;   // words of a lane per key row: 8 or 4 (k steps)
-  constexpr int kNT = D / 8;   // output column tiles
+  constexpr int kMT = D / 16;  // tiles of 16 elements of the output
   constexpr int kVW = D / 32;  // words of a lane per value row: 4 or 2
   grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
@@ -176,10 +186,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   };
 
   // ---- state of the current segment (one sequence and head)
-  uint32_t qf[kW][4];  // the query fragments
-  float o[kNT][4];
-  float ref[2], sum[2], cs[2];
-  int pos[2];  // the rows' positions; -1: no row
+  // (lane 4 g + t: rows 8 n + 2 t + x of tile n; sum: of the lane's tokens)
+  uint2 qf[NT][kW];  // the query fragments
+  float o[NT][kMT][4];
+  float ref[NT][2], sum[NT][2], cs[NT][2];
+  int pos[NT][2];  // the rows' positions; -1: no row
   int E = -127;
 
   unsigned issued = 0, used = 0;  // stages of this warp so far
@@ -225,11 +236,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
       return make_int2(seq_row0[b] + tok, hk * a.group + r - tok * a.group);
     };
 
-    // queries: each warp scales one or two rows by a power of two into fp16
+    // queries: each warp scales a row of each tile by a power of two into fp16
     {
-      uint32_t raw[2][D / 64];
+      uint32_t raw[NT][D / 64];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NT; ++x) {
         const int r = warp + x * kRW;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) raw[x][e] = 0u;
@@ -247,9 +258,8 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         }
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NT; ++x) {
         const int r = warp + x * kRW;
-        if (r >= kRows) break;
         uint32_t m2 = 0;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) m2 = __vmaxu2(m2, raw[x][e] & 0x7FFF7FFFu);
@@ -323,25 +333,26 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         __syncthreads();  // queries staged
         first_piece = false;
 #pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          const int unit = (D / 16) * t + j;
-          const int at = (unit ^ (unit / (D / 8))) * 8;
-          const uint2 x = lds_v2(smem + L::kQOff + g * L::kQStride + at);
-          const uint2 y = lds_v2(smem + L::kQOff + (g + 8) * L::kQStride + at);
-          qf[j][0] = x.x, qf[j][2] = x.y, qf[j][1] = y.x, qf[j][3] = y.y;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int j = 0; j < kW; ++j) {
+            const int unit = (D / 16) * t + j;
+            qf[n][j] = lds_v2(smem + L::kQOff + (8 * n + g) * L::kQStride +
+                              (unit ^ (unit / (D / 8))) * 8);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = 8 * n + 2 * t + x;
+            ref[n][x] = -INFINITY;
+            sum[n][x] = 0.f;
+            cs[n][x] = qscale[r] * a.scale_log2;
+            pos[n][x] = r < R ? p_first + kv_token(a, r) : -1;
+          }
+#pragma unroll
+          for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = g + 8 * x;
-          ref[x] = -INFINITY;
-          sum[x] = 0.f;
-          cs[x] = qscale[r] * a.scale_log2;
-          pos[x] = r < R ? p_first + kv_token(a, r) : -1;
-        }
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
         E = -127;
       }
       const long long piece = e_here < c1 ? e_here : c1;
@@ -360,15 +371,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         const uint8_t* kb = ring + s * L::kStage;
         const uint8_t* vb = kb + kHalf * D;
 
-        // S = Q Kc^T for 32 tokens
-        // (the four column tiles side by side: four independent chains of
-        // products)
-        float sc[4][4];
+        // S^T = Kc Q^T for 32 tokens, two tiles of 16 side by side
+        float sc[NT][2][4];
         uint32_t kw[4][kW];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
           const uint8_t* kr = kb + (8 * n + g) * D;
           if constexpr (D == 128) {
             const uint4 x = lds_v4(kr + (((2 * t) ^ g) << 4));
@@ -381,25 +388,33 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           }
         }
 #pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[n][i][x] = 0.f;
+#pragma unroll
         for (int j = 0; j < kW; ++j)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t b0, b1;
-            codes_to_half(kw[n][j], b0, b1);
-            mma_16816(sc[n], qf[j], b0, b1);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t af[4];
+            codes_to_half(kw[2 * i][j], af[0], af[2]);
+            codes_to_half(kw[2 * i + 1][j], af[1], af[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(sc[n][i], af, qf[n][j].x, qf[n][j].y);
           }
         if (!(rec_row & (kMAll << half))) {
           const int in = static_cast<int>((h >> 1) + c0 - s_begin);
           const int j0 = pages.page(in) * kBlk + half * kHalf;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t see = static_cast<uint32_t>(kv_mask(a, pos[x], j0)) >> (2 * t);
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t see = static_cast<uint32_t>(kv_mask(a, pos[n][x], j0)) >> g;
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (!(see & (1u << (8 * n + y)))) sc[n][2 * x + y] = -INFINITY;
-          }
+              for (int k = 0; k < 4; ++k)
+                if (!(see & (1u << (8 * k)))) sc[n][k >> 1][2 * (k & 1) + x] = -INFINITY;
+            }
         }
 
         // the values' codes, on their way under the softmax
@@ -422,62 +437,70 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         }
         // softmax of the half-page
         const int En = rec.e > E ? rec.e : E;
-        float scale[2] = {1.f, 1.f};
-        bool rescale = En != E;
-        if (rescale) {
-          scale[0] = scale[1] = exp2f(static_cast<float>(E - En));
-          E = En;
-        }
-        float c[2], add[2];
+        bool raise = En != E;
+        float c[NT][2], big[NT][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          // (a scale of 0 must not turn a masked -inf into a NaN)
-          c[x] = fmaxf(cs[x] * rec.ks, 1e-37f);
-          float big = fmaxf(sc[0][2 * x], sc[0][2 * x + 1]);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 1; n < 4; ++n) big = fmaxf(fmaxf(big, sc[n][2 * x]), sc[n][2 * x + 1]);
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          const float top = big * c[x];  // -inf: no visible token
-          if (top > ref[x] + kRLazy) {
-            const float f = exp2_approx(ref[x] - top);  // 0 for the row's first
-            scale[x] *= f;
-            sum[x] *= f;
-            ref[x] = top;
-            rescale = true;
+          for (int x = 0; x < 2; ++x) {
+            // (a scale of 0 must not turn a masked -inf into a NaN)
+            c[n][x] = fmaxf(cs[n][x] * rec.ks, 1e-37f);
+            big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
+                              fmaxf(sc[n][1][x], sc[n][1][x + 2]));
+            raise = raise || big[n][x] * c[n][x] > ref[n][x] + kRLazy;
           }
-          add[x] = kROff + rec.lf - (ref[x] == -INFINITY ? 0.f : ref[x]);
-          // (a scale that is not finite: the rows that see its page, and only
-          // they, become NaN)
-          float part = 0.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float shift = En != E ? exp2f(static_cast<float>(E - En)) : 1.f;
+          E = En;
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int n = 0; n < NT; ++n) {
+            float scale[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              sc[n][2 * x + y] = exp2_approx(fmaf(sc[n][2 * x + y], c[x], add[x]));
-              part += sc[n][2 * x + y];
+            for (int x = 0; x < 2; ++x) {
+              float top = big[n][x] * c[n][x];  // -inf: no visible token
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+              scale[x] = shift;
+              if (top > ref[n][x] + kRLazy) {
+                const float f = exp2_approx(ref[n][x] - top);  // 0 for the row's first
+                scale[x] *= f;
+                sum[n][x] *= f;
+                ref[n][x] = top;
+              }
             }
-          if (big != -INFINITY) sum[x] = fmaf(part, rec.rf, sum[x]);
-        }
-        uint32_t pf[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          pf[k][0] = half2_bits(sc[2 * k][0], sc[2 * k][1]);
-          pf[k][1] = half2_bits(sc[2 * k][2], sc[2 * k][3]);
-          pf[k][2] = half2_bits(sc[2 * k + 1][0], sc[2 * k + 1][1]);
-          pf[k][3] = half2_bits(sc[2 * k + 1][2], sc[2 * k + 1][3]);
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
+            for (int i = 0; i < kMT; ++i)
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            o[n][0] *= scale[0];
-            o[n][1] *= scale[0];
-            o[n][2] *= scale[1];
-            o[n][3] *= scale[1];
+              for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
+          }
+        }
+        uint2 pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float add = kROff + rec.lf - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int y = x; y < 4; y += 2) {
+                sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
+                part += sc[n][i][y];
+              }
+            // (a scale that is not finite: the rows that see its page, and
+            // only they, become NaN)
+            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rf, sum[n][x]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            pf[n][i].x = transposed(half2_bits(sc[n][i][0], sc[n][i][1]));
+            pf[n][i].y = transposed(half2_bits(sc[n][i][2], sc[n][i][3]));
           }
         }
 
-        // O += P Vc 2^(e - E)
+        // O^T += Vc^T 2^(e - E) P^T
         const uint32_t hp = half_pow2(rec.e - E);
         const uint32_t vmul = hp | (hp << 16);
         uint32_t vadd;  // -1152 * 2^(e - E), exact
@@ -492,15 +515,18 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             const uint32_t hi[2] = {__byte_perm(w[0][q], w[1][q], 0x7362) ^ 0x80808080u,
                                     __byte_perm(w[2][q], w[3][q], 0x7362) ^ 0x80808080u};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t bf[2];
+            for (int e = 0; e < 4; e += 2) {
+              // elements 4 q + e and 4 q + e + 1 of the lane's group of D / 8
+              uint32_t af[4];
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t v =
-                    __byte_perm(e < 2 ? lo[x] : hi[x], 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
-                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(bf[x]) : "r"(v), "r"(vmul), "r"(vadd));
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t v = __byte_perm(e < 2 ? lo[x >> 1] : hi[x >> 1], 0x64646464u,
+                                               (x & 1) ? 0x4342 : 0x4140);
+                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(af[x]) : "r"(v), "r"(vmul), "r"(vadd));
               }
-              mma_16816(o[4 * q + e], pf[k], bf[0], bf[1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_16816(o[n][2 * q + e / 2], af, pf[n][k].x, pf[n][k].y);
             }
           }
         }
@@ -515,11 +541,13 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 
     // ---- the segment's end in this CTA: merge the warps
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-      if (t == 0) ml[warp * kRows + g + 8 * x] = make_float2(ref[x], sum[x]);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) sum[n][x] += __shfl_xor_sync(0xffffffffu, sum[n][x], k);
+        if (g == 0) ml[warp * kRows + 8 * n + 2 * t + x] = make_float2(ref[n][x], sum[n][x]);
+      }
     if (lane == 0) wexp[warp] = E;
     const bool whole = s_begin >= u_begin && s_end <= u_end;
     __syncthreads();
@@ -544,39 +572,55 @@ __global__ void __launch_bounds__(kRW * 32, 1)
       return a.partials + (2 * cta + (cta == cta_first ? 1 : 0)) * (kRows * (D + 2));
     };
     float* mine = part_of(blockIdx.x);
-    for (int r0 = 0; r0 < R; r0 += 2) {
-      // rows r0 and r0 + 1 of every warp
-      const int x = (r0 >> 3) & 1;
-      if ((g >> 1) == ((r0 >> 1) & 3)) {
-        float* dst = merge + (warp * 2 + (g & 1)) * D + (D / 4) * t;
+    // element d of a merged row, in chunks of four that eight lanes' stores
+    // spread over all banks
+    auto spread = [](int group, int chunk) {  // group of D / 8 elements, chunk of it
+      constexpr int kChunks = D / 32;
+      return group * (D / 8) + 4 * ((chunk + group / (8 / kChunks)) % kChunks);
+    };
 #pragma unroll
-        for (int n = 0; n < kNT; n += 4) {
-          *reinterpret_cast<float4*>(dst + n) =
-              x ? make_float4(o[n][2], o[n + 1][2], o[n + 2][2], o[n + 3][2])
-                : make_float4(o[n][0], o[n + 1][0], o[n + 2][0], o[n + 3][0]);
-          *reinterpret_cast<float4*>(dst + kNT + n) =
-              x ? make_float4(o[n][3], o[n + 1][3], o[n + 2][3], o[n + 3][3])
-                : make_float4(o[n][1], o[n + 1][1], o[n + 2][1], o[n + 3][1]);
-        }
+    for (int r0 = 0; r0 < kRows; r0 += kMergeRows) {
+      // rows r0 to r0 + 3 of every warp
+      if (r0 >= R) break;
+      if ((t >> 1) == ((r0 >> 2) & 1)) {
+        const int n = r0 / 8;
+        float* dst = merge + (warp * kMergeRows + 2 * (t & 1)) * D;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int q = 0; q < kVW; ++q)
+            *reinterpret_cast<float4*>(dst + x * D + spread(g, q)) =
+                make_float4(o[n][2 * q][x], o[n][2 * q][x + 2], o[n][2 * q + 1][x],
+                            o[n][2 * q + 1][x + 2]);
       }
       __syncthreads();
-      const int r = r0 + threadIdx.x / D, d = threadIdx.x % D;
-      if (threadIdx.x < 2 * D && r < R) {
-        float acc = 0.f;
+      constexpr int kDT = D / 64;  // elements of a thread
+      const int rl = threadIdx.x / 64, r = r0 + rl, d = threadIdx.x % 64 * kDT;
+      if (r < R) {
+        const float* src = merge + rl * D + spread(d / (D / 8), d / 4 % (D / 32)) + d % 4;
+        float acc[kDT];
+#pragma unroll
+        for (int y = 0; y < kDT; ++y) acc[y] = 0.f;
 #pragma unroll
         for (int w = 0; w < kRW; ++w) {
           const float f = fac[r * kRW + w];
-          if (f != 0.f) acc = fmaf(f, merge[(w * 2 + threadIdx.x / D) * D + d], acc);
+#pragma unroll
+          for (int y = 0; y < kDT; ++y)
+            if (f != 0.f) acc[y] = fmaf(f, src[w * kMergeRows * D + y], acc[y]);
         }
         const float2 v = tot[r];
         if (whole) {
           const int2 at = row_of(r);
           const long long ob = static_cast<long long>(at.x) * a.heads + at.y;
-          static_cast<uint16_t*>(a.out)[ob * D + d] =
-              static_cast<uint16_t>(pack_out(a.type, acc, 0.f));
+          uint16_t* out = static_cast<uint16_t*>(a.out) + ob * D + d;
+          if constexpr (kDT == 2)
+            *reinterpret_cast<uint32_t*>(out) = pack_out(a.type, acc[0], acc[1]);
+          else
+            *out = static_cast<uint16_t>(pack_out(a.type, acc[0], 0.f));
           if (a.lse && d == 0) a.lse[ob] = kv_log_sum(v.x, v.y, kROff);
         } else {
-          mine[r * D + d] = acc;
+#pragma unroll
+          for (int y = 0; y < kDT; ++y) mine[r * D + d + y] = acc[y];
           if (d == 0) reinterpret_cast<float2*>(mine + kRows * D)[r] = v;
         }
       }
@@ -649,7 +693,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     if (!mbar_wait_clk(&full[used % L::kStages], (used / L::kStages) & 1, a.err)) break;
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
                        cudaStream_t stream, int* launches) {
   cudaLaunchAttribute attr[1];
@@ -661,8 +705,8 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
     p.starts += b0;
     const int grid = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
     const cudaLaunchConfig_t cfg =
-        pdl_launch_config(attr, dim3(grid), dim3(kRW * 32), RL<D>::kAlloc, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_rows_kernel<D>, *tm, p, max_rows);
+        pdl_launch_config(attr, dim3(grid), dim3(kRW * 32), RL<D, NT>::kAlloc, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_rows_kernel<D, NT>, *tm, p, max_rows);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
@@ -672,21 +716,28 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
 }  // namespace
 
 size_t kv8_rows_partial_bytes(int dim) {
-  return static_cast<size_t>(kSmallTMaxCtas) * 2 * kRows * (dim + 2) * sizeof(float);
+  return static_cast<size_t>(kSmallTMaxCtas) * 2 * 16 * (dim + 2) * sizeof(float);
 }
 
 cudaError_t kv8_rows_set_attributes() {
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv8_rows_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, RL<64>::kAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kv8_rows_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              RL<128>::kAlloc);
+  const auto allow = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  cudaError_t e = allow(kv8_rows_kernel<64, 1>, RL<64, 1>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<64, 2>, RL<64, 2>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 1>, RL<128, 1>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 2>, RL<128, 2>::kAlloc);
+  return e;
 }
 
 cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
                             cudaStream_t stream, int* launches) {
-  return a.dim == 128 ? launch_one<128>(tm, a, max_rows, num_sms, stream, launches)
-                      : launch_one<64>(tm, a, max_rows, num_sms, stream, launches);
+  // one tile of rows where no sequence has more than eight
+  if (static_cast<long long>(a.max_new) * a.group <= 8)
+    return a.dim == 128 ? launch_one<128, 1>(tm, a, max_rows, num_sms, stream, launches)
+                        : launch_one<64, 1>(tm, a, max_rows, num_sms, stream, launches);
+  return a.dim == 128 ? launch_one<128, 2>(tm, a, max_rows, num_sms, stream, launches)
+                      : launch_one<64, 2>(tm, a, max_rows, num_sms, stream, launches);
 }
 
 }  // namespace tern
