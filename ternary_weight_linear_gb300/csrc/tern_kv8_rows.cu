@@ -40,6 +40,14 @@ constexpr int kHalf = 32;     // tokens of a stage
 constexpr int kMergeRows = 4; // rows merged at a time
 constexpr int kRecs = 256;    // pages whose records are held at a time
 constexpr float kROff = 10.f, kRLazy = 4.f;
+// From this many pages per CTA an eighth of the units is left for short ranges.
+// A static split ends when the SM with the least share of the HBM rate does,
+// up to 19 % after the mean; a short range costs its CTA 3 us of records,
+// merge and join.  Measured, with them and without: 181 and 197 us (447 pages
+// a CTA), 121 and 107 us (237 pages a CTA, 12 rows).
+constexpr int kQueueUnits = 384;
+constexpr int kQueue = 511;                // the ticket that counts the short ranges taken
+constexpr uint32_t kNeg128 = 0x80808080u;   // a pair of -128 * 2^-24 in fp16
 
 // D: elements of a head.  NT: tiles of eight rows.
 template <int D, int NT>
@@ -69,8 +77,9 @@ struct RL {
 
 // What a half-page's arithmetic needs of its page, in one 16-byte load.
 struct __align__(16) PageRec {
-  float ks, lf, rf;  // key scale; log2 f and 1 / f of the value scale 2^e f
-  int e;
+  float ks, vs;  // scales of the keys and of the values
+  float one;     // 1, or NaN where a scale is not finite
+  int e;         // vs < 2^(e + 1)
 };
 // Beside it, the first row of the page's keys in the codes' tensor map (a
 // multiple of 64) with these bits, or -1 for a page out of range.
@@ -85,6 +94,17 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The bytes of u (codes + 128) that sel picks, as a pair in fp16: kBiased the
+// subnormals (code + 128) 2^-24, a byte beside a zero byte; otherwise the codes
+// themselves, from 1024 + (code + 128).  Both are exact.
+template <bool kBiased>
+__device__ __forceinline__ uint32_t code_pair(uint32_t u, uint32_t sel) {
+  if (kBiased) return __byte_perm(u, 0u, sel);
+  const uint32_t v = __byte_perm(u, 0x64646464u, sel);
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x64806480u));
+  return d;
 }
 // The transpose of the warp's 8 x 8 matrix of 16-bit elements (lane 4 i + j
 // holds elements 2 j and 2 j + 1 of row i).
@@ -102,6 +122,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   constexpr int kW = D / 16;   // words of a lane per key row: 8 or 4 (k steps)
   constexpr int kMT = D / 16;  // tiles of 16 elements of the output
   constexpr int kVW = D / 32;  // words of a lane per value row: 4 or 2
+  // One tile of rows takes the codes as biased subnormals, which saves an
+  // instruction per pair, and products of all -128 for the bias; with two
+  // tiles the values' separate sums would not fit the registers.
+  constexpr bool kBiased = NT == 1;
+  constexpr float kUp = kBiased ? 16777216.f : 1.f;  // 1 over the codes' unit
   grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
@@ -121,7 +146,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   int* seq_len = reinterpret_cast<int*>(before + kKvSeqsPerLaunch + 1);
   int* seq_m = seq_len + kKvSeqsPerLaunch;
   int* seq_row0 = seq_m + kKvSeqsPerLaunch;
-  __shared__ int s_last;
+  __shared__ int s_last, s_next;
 
   if (lane == 0) {
     for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], 1);
@@ -163,9 +188,23 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     __syncthreads();
   }
   const long long U = before[a.seqs];
-  const long long per = (U + gridDim.x - 1) / gridDim.x;  // units of a CTA
-  const long long u_begin = static_cast<long long>(blockIdx.x) * per;
-  const long long u_end = U < u_begin + per ? U : u_begin + per;
+  // Ranges of units: one for each CTA, of [0, fixed), and where there is enough
+  // work the rest in short ones that CTAs take as they finish.
+  const int ctas = static_cast<int>(gridDim.x);
+  long long per = (U + ctas - 1) / ctas, fixed = U, per2 = 1;
+  int extra = 0;  // short ranges
+  if (per >= kQueueUnits) {
+    per = per * 7 / 8;
+    fixed = per * ctas;
+    per2 = (U - fixed + ctas - 1) / ctas;
+    extra = static_cast<int>((U - fixed + per2 - 1) / per2);
+  }
+  auto range_of = [&](long long u) {
+    return static_cast<int>(u < fixed ? u / per : ctas + (u - fixed) / per2);
+  };
+  int range = blockIdx.x;
+  long long u_begin = static_cast<long long>(range) * per;
+  long long u_end = fixed < u_begin + per ? fixed : u_begin + per;
   if (u_begin >= u_end) return;
 
   // the sequence of unit u
@@ -191,7 +230,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   float o[NT][kMT][4];
   float ref[NT][2], sum[NT][2], cs[NT][2];
   int pos[NT][2];  // the rows' positions; -1: no row
+  float s0[NT][4];  // -128 * 2^-24 times the sums of the rows' queries
   int E = -127;
+  float down = 0.f;  // 2^-E
+  const uint32_t neg128[4] = {kNeg128, kNeg128, kNeg128, kNeg128};
 
   unsigned issued = 0, used = 0;  // stages of this warp so far
   bool ok = true;
@@ -219,7 +261,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   };
 
   long long u = u_begin;
-  while (u < u_end) {
+  while (u < u_end) {  // (the range changes at its end, below)
     // ---- the segment that starts (or continues) at unit u
     const int b = seq_of(u);
     const int len = seq_len[b], m = seq_m[b];
@@ -299,21 +341,21 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           split(uu - before[bb], pp.count, hh, lp);
           lp = pp.page(lp);
           const int page = a.table[static_cast<size_t>(bb) * a.width + lp];
-          PageRec rec = {0.f, 0.f, 0.f, -127};
+          PageRec rec = {0.f, 0.f, 1.f, -127};
           int row = -1;
           if (page < 0 || page >= a.pages) {
             atomicOr(a.err, kErrIndex);
           } else {
             const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hh;
             const float ks = sc[0];
-            const VScale v = split_vscale(sc[a.hkv]);
-            // a scale that is not finite keeps out of the arithmetic and makes
-            // 1 / f NaN
-            const bool good = fabsf(ks) < INFINITY && v.f == v.f;
+            const float vs = sc[a.hkv];
+            // a scale that is not finite keeps out of the arithmetic
+            const bool good = fabsf(ks) < INFINITY && fabsf(vs) < INFINITY;
             rec.ks = good ? ks : 0.f;
-            rec.lf = good ? log2f(v.f) : 0.f;
-            rec.rf = good ? 1.0f / v.f : __uint_as_float(0x7FC00000u);
-            rec.e = v.e;
+            rec.vs = good ? vs : 0.f;
+            rec.one = good ? 1.f : __uint_as_float(0x7FC00000u);
+            const int ex = static_cast<int>((__float_as_uint(rec.vs) >> 23) & 0xFFu) - 127;
+            rec.e = ex;  // (-127: zero and subnormals)
             row = (page * 2 * a.hkv + hh) * kBlk;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -352,8 +394,13 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s0[n][x] = 0.f;
+#pragma unroll
+          for (int j = 0; kBiased && j < kW; ++j) mma_16816(s0[n], neg128, qf[n][j].x, qf[n][j].y);
         }
         E = -127;
+        down = exp2f(127.f);
       }
       const long long piece = e_here < c1 ? e_here : c1;
       // this warp's half-pages of [u, piece): those congruent to its number
@@ -392,14 +439,18 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[n][i][x] = 0.f;
+            for (int x = 0; x < 4; ++x) sc[n][i][x] = s0[n][x];
 #pragma unroll
         for (int j = 0; j < kW; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t af[4];
-            codes_to_half(kw[2 * i][j], af[0], af[2]);
-            codes_to_half(kw[2 * i + 1][j], af[1], af[3]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t u = kw[2 * i + x][j] ^ 0x80808080u;
+              af[x] = code_pair<kBiased>(u, 0x4140);
+              af[x + 2] = code_pair<kBiased>(u, 0x4342);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_16816(sc[n][i], af, qf[n][j].x, qf[n][j].y);
           }
@@ -444,7 +495,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             // (a scale of 0 must not turn a masked -inf into a NaN)
-            c[n][x] = fmaxf(cs[n][x] * rec.ks, 1e-37f);
+            c[n][x] = fmaxf(cs[n][x] * rec.ks * kUp, 1e-37f);
             big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
                               fmaxf(sc[n][1][x], sc[n][1][x + 2]));
             raise = raise || big[n][x] * c[n][x] > ref[n][x] + kRLazy;
@@ -452,6 +503,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         if (__any_sync(0xffffffffu, raise)) {
           const float shift = En != E ? exp2f(static_cast<float>(E - En)) : 1.f;
           E = En;
+          down = exp2f(static_cast<float>(-E));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float scale[2];
@@ -475,12 +527,13 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
           }
         }
+        const float vs = rec.vs * down;  // below 2
         uint2 pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float add = kROff + rec.lf - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
+            const float add = kROff - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -488,10 +541,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               for (int y = x; y < 4; y += 2) {
                 sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
                 part += sc[n][i][y];
+                sc[n][i][y] *= vs;
               }
             // (a scale that is not finite: the rows that see its page, and
             // only they, become NaN)
-            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rf, sum[n][x]);
+            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.one, sum[n][x]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -500,34 +554,48 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           }
         }
 
-        // O^T += Vc^T 2^(e - E) P^T
-        const uint32_t hp = half_pow2(rec.e - E);
-        const uint32_t vmul = hp | (hp << 16);
-        uint32_t vadd;  // -1152 * 2^(e - E), exact
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(vadd) : "r"(vmul), "r"(0xE480E480u));
+        // O^T += Vc^T P^T
+        float oc[NT][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t(&w)[4][kVW] = vw[k];
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int q = 0; q < kVW; ++q) {
-            const uint32_t lo[2] = {__byte_perm(w[0][q], w[1][q], 0x5140) ^ 0x80808080u,
-                                    __byte_perm(w[2][q], w[3][q], 0x5140) ^ 0x80808080u};
-            const uint32_t hi[2] = {__byte_perm(w[0][q], w[1][q], 0x7362) ^ 0x80808080u,
-                                    __byte_perm(w[2][q], w[3][q], 0x7362) ^ 0x80808080u};
+          for (int x = 0; x < 4; ++x) oc[n][x] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              // elements 4 q + e and 4 q + e + 1 of the lane's group of D / 8
-              uint32_t af[4];
+          for (int k = 0; kBiased && k < 2; ++k) mma_16816(oc[n], neg128, pf[n][k].x, pf[n][k].y);
+        }
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t v = __byte_perm(e < 2 ? lo[x >> 1] : hi[x >> 1], 0x64646464u,
-                                               (x & 1) ? 0x4342 : 0x4140);
-                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(af[x]) : "r"(v), "r"(vmul), "r"(vadd));
-              }
+        for (int q = 0; q < kVW; ++q) {
+          // elements 4 q to 4 q + 3 of the lane's group of D / 8, two at a time
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma_16816(o[n][2 * q + e / 2], af, pf[n][k].x, pf[n][k].y);
+          for (int i = 0; i < 2; ++i) {
+            float od[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) od[n][x] = kBiased ? oc[n][x] : o[n][2 * q + i][x];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t(&w)[4][kVW] = vw[k];
+              const uint32_t sel = i ? 0x7362 : 0x5140;
+              const uint32_t u0 = __byte_perm(w[0][q], w[1][q], sel) ^ 0x80808080u;
+              const uint32_t u1 = __byte_perm(w[2][q], w[3][q], sel) ^ 0x80808080u;
+              const uint32_t af[4] = {
+                  code_pair<kBiased>(u0, 0x4140), code_pair<kBiased>(u0, 0x4342),
+                  code_pair<kBiased>(u1, 0x4140), code_pair<kBiased>(u1, 0x4342)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_16816(od[n], af, pf[n][k].x, pf[n][k].y);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) {
+                float(&to)[4] = o[n][2 * q + i];
+                if (kBiased)
+                  unpair_f32(add_pair(pair_f32(to[x], to[x + 1]), pair_f32(od[n][x], od[n][x + 1])),
+                             to[x], to[x + 1]);
+                else
+                  to[x] = od[n][x], to[x + 1] = od[n][x + 1];
+              }
           }
         }
         __syncwarp();  // the stage has been read
@@ -549,6 +617,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         if (g == 0) ml[warp * kRows + 8 * n + 2 * t + x] = make_float2(ref[n][x], sum[n][x]);
       }
     if (lane == 0) wexp[warp] = E;
+    if (u >= u_end && extra > 0 && threadIdx.x == 0) {
+      // the next range; every CTA fails once, and the last one clears the count
+      s_next = atomicAdd(&a.tickets[kQueue], 1);
+      if (s_next == extra + ctas - 1) a.tickets[kQueue] = 0;
+    }
     const bool whole = s_begin >= u_begin && s_end <= u_end;
     __syncthreads();
     if (threadIdx.x < kRows * 16) {
@@ -567,31 +640,30 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         fac[r * kRW + w] = l == 0.f ? 0.f : f / l * exp2f(static_cast<float>(wexp[w]));
       if (w == 0) tot[r] = make_float2(big, l);
     }
-    const long long cta_first = whole ? 0 : s_begin / per;
-    auto part_of = [&](long long cta) {  // the partial results of the segment in that CTA
-      return a.partials + (2 * cta + (cta == cta_first ? 1 : 0)) * (kRows * (D + 2));
+    const int first = whole ? 0 : range_of(s_begin);  // the segment's first range
+    auto part_of = [&](int i) {  // the partial results of the segment in that range
+      return a.partials + static_cast<size_t>(2 * i + (i == first ? 1 : 0)) * (kRows * (D + 2));
     };
-    float* mine = part_of(blockIdx.x);
+    float* mine = part_of(range);
     // element d of a merged row, in chunks of four that eight lanes' stores
     // spread over all banks
     auto spread = [](int group, int chunk) {  // group of D / 8 elements, chunk of it
       constexpr int kChunks = D / 32;
       return group * (D / 8) + 4 * ((chunk + group / (8 / kChunks)) % kChunks);
     };
-#pragma unroll
-    for (int r0 = 0; r0 < kRows; r0 += kMergeRows) {
+    // (this and the join below run once or twice per launch: what counts is
+    // that there is little code to fetch)
+    auto merge_rows = [&](int r0, const float (&on)[kMT][4]) {
       // rows r0 to r0 + 3 of every warp
-      if (r0 >= R) break;
       if ((t >> 1) == ((r0 >> 2) & 1)) {
-        const int n = r0 / 8;
         float* dst = merge + (warp * kMergeRows + 2 * (t & 1)) * D;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int q = 0; q < kVW; ++q)
             *reinterpret_cast<float4*>(dst + x * D + spread(g, q)) =
-                make_float4(o[n][2 * q][x], o[n][2 * q][x + 2], o[n][2 * q + 1][x],
-                            o[n][2 * q + 1][x + 2]);
+                make_float4(kUp * on[2 * q][x], kUp * on[2 * q][x + 2], kUp * on[2 * q + 1][x],
+                            kUp * on[2 * q + 1][x + 2]);
       }
       __syncthreads();
       constexpr int kDT = D / 64;  // elements of a thread
@@ -625,54 +697,75 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         }
       }
       __syncthreads();
-    }
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll 1
+      for (int r0 = 8 * n; r0 < 8 * n + 8 && r0 < R; r0 += kMergeRows) merge_rows(r0, o[n]);
     if (!whole) {
-      // the last of the segment's CTAs adds the parts in CTA order, a row per
+      // the last of the segment's CTAs adds the parts in their order, a row per
       // warp
-      const int parts = static_cast<int>((s_end - 1) / per - cta_first + 1);
+      const int parts = range_of(s_end - 1) - first + 1;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0)
-        s_last = atomic_add_acq_rel_gpu(&a.tickets[cta_first], 1) == parts - 1;
+        s_last = atomic_add_acq_rel_gpu(&a.tickets[first], 1) == parts - 1;
       __syncthreads();
       if (s_last) {
-        if (threadIdx.x == 0) a.tickets[cta_first] = 0;
+        if (threadIdx.x == 0) a.tickets[first] = 0;
         constexpr int kV = D / 32;
         for (int r = warp; r < R; r += kRW) {
           float top = -INFINITY, l = 0.f, acc[kV];
 #pragma unroll
           for (int y = 0; y < kV; ++y) acc[y] = 0.f;
-          for (int p0 = 0; p0 < parts; p0 += 8) {
-            // eight parts' loads in flight
-            float2 ms[8];
-            float v[8][kV];
+#pragma unroll 1
+          for (int p0 = 0; p0 < parts; p0 += 32) {
+            // a part per lane: its weight, 0 if its rows saw nothing
+            const int n = parts - p0 < 32 ? parts - p0 : 32;
+            float2 ms = make_float2(-INFINITY, 0.f);
+            if (lane < n)
+              ms = __ldcg(reinterpret_cast<const float2*>(part_of(first + p0 + lane) + kRows * D) +
+                          r);
+            float now = ms.y == 0.f ? -INFINITY : ms.x;
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              ms[p] = make_float2(-INFINITY, 0.f);
+            for (int k = 16; k > 0; k >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, k));
+            now = fmaxf(now, top);
+            const float base = now == -INFINITY ? 0.f : now;
+            const float w = ms.y == 0.f ? 0.f : ms.y * exp2f(ms.x - base);
+            const float old = exp2f(top - base);
+            float all = w;
 #pragma unroll
-              for (int y = 0; y < kV; ++y) v[p][y] = 0.f;
-              if (p0 + p < parts) {
-                const float* src = part_of(cta_first + p0 + p);
-                ms[p] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + r);
-                if constexpr (kV == 4) {
-                  const float4 f = __ldcg(reinterpret_cast<const float4*>(src + r * D) + lane);
-                  v[p][0] = f.x, v[p][1] = f.y, v[p][2] = f.z, v[p][3] = f.w;
-                } else {
-                  const float2 f = __ldcg(reinterpret_cast<const float2*>(src + r * D) + lane);
-                  v[p][0] = f.x, v[p][1] = f.y;
+            for (int k = 16; k > 0; k >>= 1) all += __shfl_xor_sync(0xffffffffu, all, k);
+            l = l * old + all;
+            top = now;
+#pragma unroll
+            for (int y = 0; y < kV; ++y) acc[y] *= old;
+            constexpr int kAtOnce = 16;  // parts whose loads are in flight
+#pragma unroll 1
+            for (int p1 = 0; p1 < n; p1 += kAtOnce) {
+              float v[kAtOnce][kV];
+#pragma unroll
+              for (int p = 0; p < kAtOnce; ++p) {
+                const float* src = part_of(first + p0 + p1 + p) + r * D;
+#pragma unroll
+                for (int y = 0; y < kV; ++y) v[p][y] = 0.f;
+                if (p1 + p < n) {
+                  if constexpr (kV == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                    v[p][0] = x.x, v[p][1] = x.y, v[p][2] = x.z, v[p][3] = x.w;
+                  } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                    v[p][0] = x.x, v[p][1] = x.y;
+                  }
                 }
               }
-            }
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              if (ms[p].y == 0.f) continue;  // nothing seen in that part
-              const float now = fmaxf(top, ms[p].x);
-              const float base = now == -INFINITY ? 0.f : now;
-              const float old = exp2f(top - base), f = ms[p].y * exp2f(ms[p].x - base);
-              l = l * old + f;
+              for (int p = 0; p < kAtOnce; ++p) {
+                const float f = __shfl_sync(0xffffffffu, w, p1 + p);
 #pragma unroll
-              for (int y = 0; y < kV; ++y) acc[y] = fmaf(f, v[p][y], acc[y] * old);
-              top = now;
+                for (int y = 0; y < kV; ++y)
+                  if (f != 0.f) acc[y] = fmaf(f, v[p][y], acc[y]);
+              }
             }
           }
           const int2 at = row_of(r);
@@ -686,6 +779,13 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         }
       }
       __syncthreads();
+    }
+    if (u >= u_end && extra > 0) {
+      const int n = s_next;
+      if (n >= extra) break;
+      range = ctas + n;
+      u_begin = u = c0 = c1 = fixed + n * per2;
+      u_end = U < u_begin + per2 ? U : u_begin + per2;
     }
   }
   // no copy of this warp outlives it
@@ -716,7 +816,9 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
 }  // namespace
 
 size_t kv8_rows_partial_bytes(int dim) {
-  return static_cast<size_t>(kSmallTMaxCtas) * 2 * 16 * (dim + 2) * sizeof(float);
+  // two parts a range: each CTA's, and as many short ones
+  static_assert(2 * kSmallTMaxCtas <= kQueue, "tickets");
+  return static_cast<size_t>(2 * kSmallTMaxCtas) * 2 * 16 * (dim + 2) * sizeof(float);
 }
 
 cudaError_t kv8_rows_set_attributes() {
