@@ -117,6 +117,109 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void cta_barrier() {
   asm volatile("bar.sync 0;" ::: "memory");
 }
+// A block's rows of the output, staged in shared memory where the queries were
+// (a warp's own rows, whose products are done): chunks of 16 bytes swizzled by
+// the row, written D / 8 lanes a row.
+template <int D>
+struct OutRows {
+  const Kv8Args& a;
+  uint8_t* stage;
+  int r0, row0, hk;
+  __device__ __forceinline__ uint8_t* staged(int row, int c) const {
+    return stage + row * (2 * D) + ((c ^ (row & 7)) << 4);
+  }
+  __device__ __forceinline__ long long row(int r) const {  // of out and lse
+    const int tok = kv_token(a, r0 + r);
+    return static_cast<long long>(row0 + tok) * a.heads + hk * a.group +
+           (r0 + r - tok * a.group);
+  }
+  // (whole warp) rows [begin, end), none if end <= begin
+  __device__ __forceinline__ void write_out(int lane, int begin, int end) const {
+    constexpr int kLanes = D / 8;
+#pragma unroll 4
+    for (int r = begin + lane / kLanes; r < end; r += 32 / kLanes)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row(r) * D +
+                                8 * (lane % kLanes)) = lds_v4(staged(r, lane % kLanes));
+  }
+};
+
+// The last part to arrive adds them all in order (every thread of the CTA) and
+// stages the rows.
+template <int D>
+__device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, const float* first,
+                                        int parts, int rows, int r0, int row0, int hk) {
+  using L = PL<D>;
+  constexpr size_t kPart = 2 * kPRows * (D + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const OutRows<D> put{a, smem + L::kQOff, r0, row0, hk};
+  const int rows32 = (rows + 31) & ~31;
+  float* weight = reinterpret_cast<float*>(smem + L::kConvOff);  // [part][rows32]
+  // a row per thread: the parts' weights over the row's sum
+  if (threadIdx.x < rows) {
+    const int row = threadIdx.x;
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
+      const float2 ms =
+          __ldcg(reinterpret_cast<const float2*>(first + p * kPart + 2 * kPRows * D) + row);
+      const float w = ms.y == 0.f ? -INFINITY : ms.x + log2f(ms.y);
+      weight[p * rows32 + row] = w;
+      top = fmaxf(top, w);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float w = exp2f(weight[p * rows32 + row] - base);
+      weight[p * rows32 + row] = w;
+      l += w;
+    }
+    const float one = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) weight[p * rows32 + row] *= one;
+    if (a.lse) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
+  }
+  cta_barrier();
+  // sixteen elements of 32 rows per warp, four parts' loads in flight
+  for (int i = warp; i < rows32 / 32 * (D / 16); i += kPThreads / 32) {
+    constexpr int kAtOnce = 4, kC = 4;
+    const int c = i % (D / 16) * kC, row = i / (D / 16) * 32 + lane;
+    if (row >= rows) continue;
+    const float4* from = reinterpret_cast<const float4*>(first) + c * (2 * kPRows) + row;
+    float4 acc[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += kAtOnce) {
+      float4 v[kAtOnce][kC];
+#pragma unroll
+      for (int p = 0; p < kAtOnce; ++p)
+#pragma unroll
+        for (int k = 0; k < kC; ++k) {
+          v[p][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p0 + p < parts) v[p][k] = __ldcg(from + (p0 + p) * (kPart / 4) + k * (2 * kPRows));
+        }
+#pragma unroll
+      for (int p = 0; p < kAtOnce; ++p) {
+        const float w = p0 + p < parts ? weight[(p0 + p) * rows32 + row] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kC; ++k) {
+          acc[k].x = fmaf(w, v[p][k].x, acc[k].x);
+          acc[k].y = fmaf(w, v[p][k].y, acc[k].y);
+          acc[k].z = fmaf(w, v[p][k].z, acc[k].z);
+          acc[k].w = fmaf(w, v[p][k].w, acc[k].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kC; k += 2)
+      *reinterpret_cast<uint4*>(put.staged(row, (c + k) >> 1)) =
+          make_uint4(pack_out(a.type, acc[k].x, acc[k].y), pack_out(a.type, acc[k].z, acc[k].w),
+                     pack_out(a.type, acc[k + 1].x, acc[k + 1].y),
+                     pack_out(a.type, acc[k + 1].z, acc[k + 1].w));
+  }
+}
+
 // kSplit: no sequence of the batch has more than kSplitRows = 64 rows for a
 // key-value head.  Both query tiles are then the same rows and take alternate
 // pages (page j of the CTA is tile i's page j / 2, for j % 2 == i), joined at
@@ -128,7 +231,7 @@ __device__ __forceinline__ void cta_barrier() {
 constexpr int kSplitRows = 64;
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kPThreads, 1)
-    kv8_prompt_kernel(const Kv8Args a, int min_rows, int row_blocks, int parts,
+    kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole, int tail_parts,
                       float* __restrict__ partials, int* __restrict__ tickets) {
   using L = PL<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -151,8 +254,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
 
   // ---- this CTA's block of rows, sequence, head and part; late rows first
-  const int part = blockIdx.x % parts;
-  const int item = blockIdx.x / parts;
+  const int tail = static_cast<int>(blockIdx.x) - whole;  // of the items in parts
+  const int parts = tail < 0 ? 1 : tail_parts;
+  const int part = tail < 0 ? 0 : tail % parts;
+  const int item = tail < 0 ? static_cast<int>(blockIdx.x) : whole + tail / parts;
   const int hk = item % a.hkv;
   const int b = (item / a.hkv) % a.seqs;
   const int rb = row_blocks - 1 - item / a.hkv / a.seqs;
@@ -207,7 +312,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int r = (kSplit ? 0 : qt * kPRows) + tr;  // row of the block
   const bool live = warp < kSoftW && r < rows;
   int pos = -1;           // its position
-  long long orow = 0;     // its row of out
   float cs = 0.f;         // softmax scale * log2(e) * 2^-a
   const bool soft = warp < kSoftW && (warp & 3) < soft_warps(qt);
   if (soft) {
@@ -216,7 +320,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int head = hk * a.group + rr - tok * a.group;
     const long long qrow = sq.row0 + tok;
     if (live) pos = p_base + tok;
-    orow = qrow * a.heads + head;
     // The warp's rows are copied to their places as they are, D / 8 lanes a
     // row, then each thread scales its own.
     const unsigned long long mine = reinterpret_cast<unsigned long long>(
@@ -571,13 +674,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   __syncwarp();
   if (kSplit) cta_barrier();  // no converted page is read any more
-  constexpr size_t kPart = 2 * kPRows * (D + 2);  // O of the rows, then (ref, sum)
+  // A part: O in chunks of four elements, [D / 4][rows], then (ref, sum).
+  constexpr size_t kPart = 2 * kPRows * (D + 2);
+  const OutRows<D> put{a, smem + L::kQOff, r0, sq.row0, hk};
+  int out0 = 0, out1 = 0;  // the staged rows that this warp writes
   if (soft) {
     const bool mine_out = !(kSplit && qt);  // (tile 0 writes for both)
     // both tiles' softmax warps
     auto softmax_barrier = [&] { asm volatile("bar.sync 1, %0;" ::"r"(64 * soft_warps(0)) : "memory"); };
     const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
-    float* mine = partials + blockIdx.x * kPart;
+    float* mine = partials + static_cast<size_t>(tail < 0 ? 0 : tail) * kPart;
     const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
     const bool have = n > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, n - 1));
     tc_fence_after();
@@ -628,15 +734,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
         uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + 16 * q);
-        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (kSplit) {  // (few rows: straight to their places)
+          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + put.row(r) * D + 16 * q);
+          o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+          *reinterpret_cast<uint4*>(put.staged(r, 2 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(put.staged(r, 2 * q + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       } else if (live) {
-        float4* o = reinterpret_cast<float4*>(mine + r * D + 16 * q);
+        float4* o = reinterpret_cast<float4*>(mine) + 4 * q * (2 * kPRows) + r;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          o[k * (2 * kPRows)] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
+    }
+    if (!kSplit && parts == 1) {
+      out0 = r - lane;
+      out1 = rows < out0 + 32 ? rows : out0 + 32;
     }
     if (kSplit && qt) {
       *reinterpret_cast<float2*>(other + (D / 4) * kPRows) = make_float2(ref, sum);
@@ -644,83 +759,28 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (mine_out && live && parts > 1)
       reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
-    if (mine_out && live && parts == 1 && a.lse) a.lse[orow] = kv_log_sum(ref, sum, kPOff);
+    if (mine_out && live && parts == 1 && a.lse) a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
   }
   __syncwarp();
   if (parts > 1) {
-    // the last part to arrive adds them all in order, a row per warp and the
-    // loads of four rows in flight
+    // The last part to arrive adds them all in order.
     __threadfence();
     cta_barrier();
-    if (threadIdx.x == 0) *is_last = atomic_add_acq_rel_gpu(&tickets[item], 1) == parts - 1;
+    if (threadIdx.x == 0)
+      *is_last = atomic_add_acq_rel_gpu(&tickets[item - whole], 1) == parts - 1;
     cta_barrier();
     if (*is_last) {
-      if (threadIdx.x == 0) tickets[item] = 0;
-      const float* first = partials + static_cast<size_t>(item) * parts * kPart;
-      constexpr int kV = D / 32;  // elements of a lane
-      constexpr int kRowsAtOnce = 4, kWarps = kPThreads / 32;
-      for (int q0 = warp; q0 < rows; q0 += kWarps * kRowsAtOnce) {
-        float top[kRowsAtOnce], l[kRowsAtOnce], acc[kRowsAtOnce][kV];
-#pragma unroll
-        for (int q = 0; q < kRowsAtOnce; ++q) {
-          top[q] = -INFINITY;
-          l[q] = 0.f;
-#pragma unroll
-          for (int x = 0; x < kV; ++x) acc[q][x] = 0.f;
-        }
-#pragma unroll 2
-        for (int p = 0; p < parts; ++p) {
-          const float* from = first + p * kPart;
-          float2 ms[kRowsAtOnce];
-          float v[kRowsAtOnce][kV];
-#pragma unroll
-          for (int q = 0; q < kRowsAtOnce; ++q) {
-            const int row = q0 + q * kWarps;
-            ms[q] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int x = 0; x < kV; ++x) v[q][x] = 0.f;
-            if (row < rows) {
-              ms[q] = __ldcg(reinterpret_cast<const float2*>(from + 2 * kPRows * D) + row);
-              const float* src = from + row * D + kV * lane;
-              if constexpr (kV == 4) {
-                const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
-              } else {
-                const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                v[q][0] = f.x, v[q][1] = f.y;
-              }
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < kRowsAtOnce; ++q) {
-            if (ms[q].y == 0.f) continue;  // nothing seen in that part
-            const float now = fmaxf(top[q], ms[q].x);
-            const float base = now == -INFINITY ? 0.f : now;
-            const float old = exp2f(top[q] - base), f = ms[q].y * exp2f(ms[q].x - base);
-            l[q] = l[q] * old + f;
-#pragma unroll
-            for (int x = 0; x < kV; ++x) acc[q][x] = fmaf(f, v[q][x], acc[q][x] * old);
-            top[q] = now;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < kRowsAtOnce; ++q) {
-          const int row = q0 + q * kWarps;
-          if (row >= rows) continue;
-          const int tok = kv_token(a, r0 + row);
-          const long long out = static_cast<long long>(sq.row0 + tok) * a.heads + hk * a.group +
-                                (r0 + row - tok * a.group);
-          const float inv = l[q] == 0.f ? 0.f : 1.0f / l[q];
-          uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out * D) +
-                        lane * (kV / 2);
-#pragma unroll
-          for (int x = 0; x < kV; x += 2)
-            o[x / 2] = pack_out(a.type, acc[q][x] * inv, acc[q][x + 1] * inv);
-          if (a.lse && lane == 0) a.lse[out] = kv_log_sum(top[q], l[q], kPOff);
-        }
-      }
+      if (threadIdx.x == 0) tickets[item - whole] = 0;
+      join_parts<D>(a, smem, partials + static_cast<size_t>(item - whole) * parts * kPart, parts,
+                    rows, r0, sq.row0, hk);
+      cta_barrier();
+      static_assert(kPThreads / 32 * 16 == 2 * kPRows, "rows of a warp");
+      out0 = 16 * warp;
+      out1 = rows < out0 + 16 ? rows : out0 + 16;
     }
   }
+  __syncwarp();
+  put.write_out(lane, out0, out1);
   __syncwarp();
   tc_fence_before();
   cta_barrier();
@@ -731,7 +791,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 }  // namespace
 
 size_t kv8_prompt_partial_bytes(int dim) {
-  return static_cast<size_t>(kSmallTMaxCtas) * 2 * kPRows * (dim + 2) * sizeof(float);
+  return static_cast<size_t>(2 * kSmallTMaxCtas) * 2 * kPRows * (dim + 2) * sizeof(float);
 }
 
 cudaError_t kv8_prompt_set_attributes() {
@@ -749,27 +809,38 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
                               int num_sms, cudaStream_t stream, int* launches) {
   const long long most = a.max_new * a.group;
   const long long row_blocks = (most + 2 * kPRows - 1) / (2 * kPRows);
-  // parts of the keys: as many as fill the SMs once, each of at least four
-  // tiles of the longest sequence that the table allows
-  long long items = row_blocks * a.hkv * a.seqs;
-  const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
-  int parts = 1;
-  if (items < sms) {
-    long long p = sms / items;
-    if (p > a.width / 8) p = a.width / 8;
-    if (p > 1) parts = static_cast<int>(p);
+  // Whole waves of items run as they are.  The keys of the items left (the
+  // earliest rows, the last to start) are cut into parts so that they end
+  // together: as many as cost the least pages of time in sequence on an SM,
+  // where a part costs some pages for its start, its result and the join.
+  // Measured, with the cut and without (2048 tokens of 6 heads over 8190, 384
+  // items on 152 SMs): 316 and 328 us; 4096 tokens over 16384: 1106 and 1227 us.
+  const long long items = row_blocks * a.hkv * a.seqs;
+  const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
+  const long long tail = items % sms, whole = items - tail;
+  constexpr int kPartCost = 14;
+  long long parts = 1, best = a.width;
+  // (the join holds a weight per part and row in the converted pages' place)
+  const long long rows32 = most < 2 * kPRows ? (most + 31) / 32 * 32 : 2 * kPRows;
+  const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32;
+  static_assert(PL<64>::kConv * PL<64>::kTileB <= PL<128>::kConv * PL<128>::kTileB, "room");
+  for (long long p = 2; p * tail <= 2 * sms && p <= a.width / 8 && p <= room; ++p) {
+    const long long cost = (tail * p + sms - 1) / sms * ((a.width + p - 1) / p + kPartCost);
+    if (cost < best) best = cost, parts = p;
   }
-  if (items * parts > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const long long grid = whole + tail * parts;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
-      pdl_launch_config(attr, dim3(static_cast<unsigned>(items * parts)), dim3(kPThreads),
+      pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)), dim3(kPThreads),
                         a.dim == 128 ? PL<128>::kAlloc : PL<64>::kAlloc, stream);
   const auto kernel = most <= kSplitRows
                           ? (a.dim == 128 ? kv8_prompt_kernel<128, true> : kv8_prompt_kernel<64, true>)
                           : (a.dim == 128 ? kv8_prompt_kernel<128, false>
                                           : kv8_prompt_kernel<64, false>);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, min_rows, static_cast<int>(row_blocks),
-                                           parts, partials, tickets);
+                                           static_cast<int>(whole), static_cast<int>(parts),
+                                           partials, tickets);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;
