@@ -148,6 +148,40 @@ def test_long_context_is_split_and_reproducible(tl, m):
     assert not ws[:tl.SYNC_BYTES].any()
 
 
+@pytest.mark.parametrize("m", [1, 5])
+def test_long_batch_on_shared_pages(tl, m):
+    """A batch long enough that CTAs take further ranges as they finish (the
+    sequences share pages, as after a common prefix): the same bits each time,
+    and a workspace that is left as it was found."""
+    import torch
+    seqs, rng = 30, np.random.default_rng(61)
+    c = Case([8192], [m], 32, 16, 64, seed=62)
+    lens = [8192 - 37 * b for b in range(seqs)]
+    c.table = np.stack([rng.permutation(c.table[0, :128]) for _ in range(seqs)]).astype(np.int32)
+    c.lens = np.asarray(lens, dtype=np.int32)
+    c.start = (np.arange(seqs + 1) * m).astype(np.int32)
+    c.q_dev = torch.randn(seqs * m, 32, 64, device="cuda").bfloat16()
+    a = c.check(tl)
+    ws = torch.zeros(tl.tern_kv8_attention_workspace_bytes(seqs, seqs * m, 32, 16, 64),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(a, c.run(tl, workspace=ws))
+    assert not ws[:tl.SYNC_BYTES].any()
+
+
+@pytest.mark.parametrize("m", [20, 70])
+def test_last_wave_in_parts(tl, m):
+    """Blocks of rows that outnumber the SMs by a few: the last ones are cut."""
+    import torch
+    c = Case([2500, 2400, 2300, 2200, 2100], [m] * 5, 32, 32, 64, seed=63)
+    a = c.check(tl)
+    ws = torch.zeros(tl.tern_kv8_attention_workspace_bytes(5, 5 * m, 32, 32, 64),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(a, c.run(tl, workspace=ws))
+    assert not ws[:tl.SYNC_BYTES].any()
+
+
 def test_more_sequences_than_one_launch_takes(tl):
     lens = [(31 * i) % 190 for i in range(300)]
     Case(lens, [min(1 + i % 2, n) for i, n in enumerate(lens)], 2, 1, 64, seed=31).check(tl)
@@ -164,6 +198,15 @@ def test_strided_queries(tl, new):
     assert torch.equal(want, c.run(tl, q=wide[:, 2:6]))
     by_head = c.q_dev.transpose(0, 1).contiguous().transpose(0, 1)  # [heads][rows] in memory
     assert torch.equal(want, c.run(tl, q=by_head))
+
+
+@pytest.mark.parametrize("new", [[2, 1, 4], [1, 1, 9], [100, 1, 90]])
+def test_value_scales_of_the_whole_range(tl, new):
+    """Value blocks of 2^-100, 1 and 2^100 times the usual scale in one sequence."""
+    c = Case([400, 300, 90], new, 4, 2, 128, seed=53)
+    rng = np.random.default_rng(54)
+    c.scales[:, 1] *= (2.0 ** rng.choice([-100, 0, 100], c.scales[:, 1].shape)).astype(np.float32)
+    c.check(tl)
 
 
 @pytest.mark.parametrize("new", [[2, 1, 4], [100, 1, 90]])
