@@ -294,6 +294,8 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
  *   row_start   device int32 [seqs + 1], ascending: the new tokens of sequence
  *           b are rows [row_start[b], row_start[b + 1]) of q, k and v; they
  *           are its last tokens, in order
+ * pages * 2 * kv_heads * 64, table_width * 64 and rows * heads / kv_heads
+ * have to fit in 31 bits (TERN_EINVAL).
  * Sequences may be empty and may have no new tokens.  These arrays are read
  * on the device, so a captured call can be replayed with other contents.  A
  * sequence whose entries are inconsistent (a length that is negative or does
@@ -360,8 +362,8 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
  *   sinks   first tokens that stay visible outside the window (>= 0)
  *   softmax_scale > 0
  *   workspace as for tern_linear: zero its first TERN_SYNC_BYTES once.
- * Numbers: q is scaled by a power of two per row and held in fp16 (exact for
- * every element within 2^-31 of the row's largest), codes are exact in fp16,
+ * Numbers: q is scaled by a power of two per row and held in fp16 (a bf16 or
+ * fp16 element is exact down to 2^-31 of the row's largest), codes are exact in fp16,
  * products and sums are fp32; the weights exp(.) are rounded to fp16 for
  * their products with the values (relative 2^-11), their sum is fp32 and
  * unrounded.  Results are bit-for-bit reproducible. */

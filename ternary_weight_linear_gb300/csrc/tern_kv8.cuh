@@ -59,11 +59,6 @@ __device__ __forceinline__ KvPages kv_pages(const Kv8Args& a, int p0, int p1) {
   return v;
 }
 
-// Whether the row at position p sees token j.
-__device__ __forceinline__ bool kv_sees(const Kv8Args& a, int p, int j) {
-  return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
-}
-
 // Whether any row at positions [p0, p1] sees one of the tokens [j0, j1].
 __device__ __forceinline__ bool kv_any(const Kv8Args& a, int p0, int p1, int j0, int j1) {
   return j0 <= p1 && (a.window == 0 || j1 > p0 - a.window || j0 < a.sinks);
@@ -204,20 +199,6 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// Four int8 codes of a word as fp16 pairs (bytes 0, 1) and (2, 3), exactly:
-// code + 128 in the low mantissa bits of 1024, less 1152.
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
 // 2^k as an fp16 bit pattern for k <= 0 (0 below the smallest subnormal).

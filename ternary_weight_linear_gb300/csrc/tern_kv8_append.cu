@@ -7,7 +7,13 @@
 // (a token's code is rounded once more per growth, each time by at most half
 // a step of the scale then reached).  Every input is read once; a prompt is
 // bound by HBM, a decode step by the latency of one load, one reduction and
-// one store.
+// one store.  The rows are loaded beside the page table, which only the
+// stores need.
+//
+// Measured (8 heads of 128): 16 sequences' decode step (bf16) 2.9 us; three
+// ragged prompt chunks, 3554 tokens in fp32, 11.8 us, 3.1 TB/s (0.45 of the
+// copy rate: three waves of CTAs, each a load, a reduction and a store; 12.3 us
+// with the rows' loads behind the table's).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,35 +1,42 @@
 // tern_kv8_attention for sequences with many query rows per key-value head
-// (prompt chunks): bound by the tensor cores.
+// (prompt chunks): bound by the tensor cores and what feeds them.
 //
 // The rows of a sequence that share a key-value head (row r = new token
 // r / group, head r % group) are cut into blocks of 256, two tiles of 128 that
-// share every key and value tile of 128 tokens (two pages).  Per tile pair,
-// with tcgen05 kind::f16 (fp16 operands, fp32 accumulators in TMEM):
+// share every page of keys and values.  Per tile and page of 64 tokens, with
+// tcgen05 kind::f16 (fp16 operands, fp32 accumulators in TMEM):
 //   S = Q Kc^T,  s = S * (softmax_scale * log2(e) * k_scale * 2^-a(row))
 //   P = 2^(s + log2 f - ref + 10),  O += P (2^(e - E) Vc),  l += P / f
 // with Q scaled by 2^a per row into fp16, Kc and Vc the int8 codes (exact in
-// fp16), v_scale = 2^e f and E the largest e so far.  ref is the row's running
-// maximum, raised (and O rescaled) only when a score passes it by 2^4: P stays
-// below 2^15 (fp16 ends at 65504) and its range below is 2^-34 of that
-// reference, so a weight is lost only where it is that much smaller.
+// fp16), v_scale = 2^e f and E the largest e so far.  P is rounded to fp16
+// (relative 2^-11, the tensor instruction's operand; the row's sum takes it
+// unrounded).  ref is the row's running maximum, raised (and O rescaled) only
+// when a score passes it by 2^4: P stays below 2^15 (fp16 ends at 65504) and
+// its range below is 2^-34 of that reference, so a weight is lost only where
+// it is that much smaller.
 //
-// There is no int8 tcgen05 on sm_103a, so four warps turn each tile of codes
-// into fp16 in shared memory, once for the two query tiles: 2 * 128 * 128
-// elements at 1.25 instructions against the 2048 cycles that the tile pair's
-// four 128^3 products take.
+// There is no int8 tcgen05 on sm_103a, so four warps turn each page of codes
+// into fp16 in shared memory, once for the two query tiles.
 //
-// Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (S read
-// from TMEM twice, for the maximum and for the weights; P written over S);
-// 8-11 the conversion; 12-15 the MMAs, for each query tile one thread that
-// issues the scores and one that issues the products with the values: a
-// barrier wait costs an issuing thread about 200 cycles even on a completed
-// phase, which the other three cover.  Each tile has two score buffers, so the
-// scores run up to two pages ahead of the values and the softmax finds them
-// ready.
-// Work: one CTA per (block of rows, sequence, head, part of the keys), the
-// longest rows first.  When there are too few blocks for the SMs the keys are
-// cut into parts, whose (max, sum, O) go to the workspace, and the last CTA of
-// a block adds them in order.
+// Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (a
+// page's 64 scores read from TMEM once; P written over them); 8-11 the
+// conversion; 12-15 the MMAs, for each query tile one thread that issues the
+// scores and one that issues the products with the values: a barrier wait
+// costs an issuing thread about 200 cycles even on a completed phase, which
+// the other three cover.  Each tile has two score buffers, so the scores run
+// up to two pages ahead of the values and the softmax finds them ready.
+// Work: one CTA per (block of rows, sequence, head), the longest rows first;
+// the blocks of the last wave are cut along the keys into parts, whose (ref,
+// sum, O) go to the workspace, and the last CTA of a block adds them in order.
+//
+// Measured: 2048 tokens of 6 query heads per key-value head over 8190 cached,
+// head of 128: 316 us, 1143 TFLOP/s (0.60 of the bf16 GEMM rate); 4096 over
+// 16384: 1106 us, 1305 TFLOP/s (0.69).  A page takes 1840 cycles where its
+// four products need 1024: the scores' products read their 128 query rows from
+// shared memory for 64 columns (48 cycles a step instead of 32), and 16384
+// exponentials take 1024 cycles.  Both score buffers in one product pair that
+// reads the queries once lost more (423 us): the softmax then waits for each
+// pair.
 #include "tern_kv8.cuh"
 
 namespace tern {
@@ -231,8 +238,8 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
 constexpr int kSplitRows = 64;
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kPThreads, 1)
-    kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole, int tail_parts,
-                      float* __restrict__ partials, int* __restrict__ tickets) {
+    kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole,
+                      int tail_parts, float* __restrict__ partials, int* __restrict__ tickets) {
   using L = PL<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
@@ -458,7 +465,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, D, true);
           for (int j = jt + (kSplit ? i : 0); j < j_end && ok; j += kStep) {
             const int n = j / kStep;
-            ok = wait_conv(v_full, j) && mbar_wait_clk(&p_full[2 * i + (n & 1)], (n >> 1) & 1, a.err);
+            ok = wait_conv(v_full, j) &&
+                 mbar_wait_clk(&p_full[2 * i + (n & 1)], (n >> 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const uint64_t v =
@@ -681,7 +689,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (soft) {
     const bool mine_out = !(kSplit && qt);  // (tile 0 writes for both)
     // both tiles' softmax warps
-    auto softmax_barrier = [&] { asm volatile("bar.sync 1, %0;" ::"r"(64 * soft_warps(0)) : "memory"); };
+    auto softmax_barrier = [&] {
+      asm volatile("bar.sync 1, %0;" ::"r"(64 * soft_warps(0)) : "memory");
+    };
     const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
     float* mine = partials + static_cast<size_t>(tail < 0 ? 0 : tail) * kPart;
     const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
@@ -735,7 +745,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
         if (kSplit) {  // (few rows: straight to their places)
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + put.row(r) * D + 16 * q);
+          uint4* o =
+              reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + put.row(r) * D + 16 * q);
           o[0] = make_uint4(w[0], w[1], w[2], w[3]);
           o[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {

@@ -10,6 +10,13 @@
 // monotonic, so max|(r w) inv| = max|r w| inv exactly, and one barrier
 // separates the loads from the stores.  A single token is bound by that
 // latency chain (launch, one load round trip, one barrier, the stores).
+// A thread holds as few of the row's vectors as a CTA of 1024 allows: with two
+// each and half the threads the 2048 rows below take 23.6 us (each thread's
+// chain of loads, sums and stores is longer, and no more of them are resident).
+//
+// Measured (width 5120, fp32 x, bf16 residual and weight): one token 2.8 us;
+// 2048 tokens 19.9 us, 4.75 TB/s (0.70 of the copy rate); 4096 tokens with y
+// 39.1 us, 5.9 TB/s (0.87): some 5 us of each call start and drain the SMs.
 #include <cuda_bf16.h>
 
 #include "tern.h"
