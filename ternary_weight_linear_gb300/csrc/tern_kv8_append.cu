@@ -10,10 +10,10 @@
 // one store.  The rows are loaded beside the page table, which only the
 // stores need.
 //
-// Measured (8 heads of 128): 16 sequences' decode step (bf16) 2.9 us; three
-// ragged prompt chunks, 3554 tokens in fp32, 11.8 us, 3.1 TB/s (0.45 of the
-// copy rate: three waves of CTAs, each a load, a reduction and a store; 12.3 us
-// with the rows' loads behind the table's).
+// Measured (8 heads of 128): 16 sequences' decode step (bf16) 2.6 us; three
+// ragged prompt chunks, 3554 tokens in fp32, 9.8 us, 3.7 TB/s (0.55 of the
+// copy rate; 5 waves of CTAs, each a load, a reduction and a store).  Four
+// CTAs an SM at 64 registers take as long as two at 90.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -146,15 +146,9 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
   for (int i = 0; i < kSteps; ++i) {
     const int slot = slot0 + i * kTok;
     if (slot >= first && slot < last) {
-      uint32_t w[2] = {0u, 0u};
-      if (scale > 0.f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = static_cast<int>(quant_code(x[i][e], scale, inv, fast));
-          w[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
-        }
-      }
-      *reinterpret_cast<uint2*>(codes + slot * D + 8 * chunk) = make_uint2(w[0], w[1]);
+      uint2 w = make_uint2(0u, 0u);
+      if (scale > 0.f) w = quant_codes8(x[i], scale, inv, fast);
+      *reinterpret_cast<uint2*>(codes + slot * D + 8 * chunk) = w;
     }
   }
 }

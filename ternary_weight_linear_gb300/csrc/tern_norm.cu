@@ -11,12 +11,14 @@
 // separates the loads from the stores.  A single token is bound by that
 // latency chain (launch, one load round trip, one barrier, the stores).
 // A thread holds as few of the row's vectors as a CTA of 1024 allows: with two
-// each and half the threads the 2048 rows below take 23.6 us (each thread's
+// each and half the threads the 2048 rows below take 20.5 us (each thread's
 // chain of loads, sums and stores is longer, and no more of them are resident).
+// 32 registers a thread keep three CTAs of 640 threads on an SM; with 41 the
+// same rows take 21.8 us.
 //
-// Measured (width 5120, fp32 x, bf16 residual and weight): one token 2.8 us;
-// 2048 tokens 19.9 us, 4.75 TB/s (0.70 of the copy rate); 4096 tokens with y
-// 39.1 us, 5.9 TB/s (0.87): some 5 us of each call start and drain the SMs.
+// Measured (width 5120, fp32 x, bf16 residual and weight): one token 2.6 us;
+// 2048 tokens 19.0 us, 4.96 TB/s (0.73 of the copy rate); 4096 tokens with y
+// 37.8 us, 6.1 TB/s (0.90): some 4 us of each call start and drain the SMs.
 #include <cuda_bf16.h>
 
 #include "tern.h"
@@ -85,7 +87,8 @@ constexpr int kNoResidual = -1;
 // XT, RT: types of x and of the residual (kNoResidual: none; the norm then
 // runs on x itself).  NV: vectors of eight elements per thread.
 template <int XT, int RT, int NV>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
+    add_rmsnorm_kernel(const NormArgs a) {
   grid_dependents_launch();
   __shared__ float red_s[32], red_m[32];
   const int t = blockIdx.x;
@@ -170,15 +173,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
             make_uint4(pack_bf16(r[j].v[0], r[j].v[1]), pack_bf16(r[j].v[2], r[j].v[3]),
                        pack_bf16(r[j].v[4], r[j].v[5]), pack_bf16(r[j].v[6], r[j].v[7]));
       if (a.q) {
-        uint32_t out[2] = {0u, 0u};
-        if (amax > 0.f) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = static_cast<int>(quant_code(r[j].v[e], scale, sinv, fast));
-            out[e >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e & 3));
-          }
-        }
-        *reinterpret_cast<uint2*>(a.q + row + 8ll * i) = make_uint2(out[0], out[1]);
+        uint2 out = make_uint2(0u, 0u);
+        if (amax > 0.f) out = quant_codes8(r[j].v, scale, sinv, fast);
+        *reinterpret_cast<uint2*>(a.q + row + 8ll * i) = out;
       }
     }
   }
