@@ -111,7 +111,17 @@ __device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, in
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    // (asleep for up to 20 us: attempts would take issue slots of the warps at
+    // work)
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
     if (clock64() - t0 > kWaitCycles) {
       atomicOr(err, kErrTimeout);
       return false;

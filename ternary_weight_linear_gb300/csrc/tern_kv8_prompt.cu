@@ -30,11 +30,11 @@
 // sum, O) go to the workspace, and the last CTA of a block adds them in order.
 //
 // Measured: 2048 tokens of 6 query heads per key-value head over 8190 cached,
-// head of 128: 316 us, 1143 TFLOP/s (0.60 of the bf16 GEMM rate); 4096 over
-// 16384: 1106 us, 1305 TFLOP/s (0.69).  A page takes 1840 cycles where its
+// head of 128: 314 us, 1149 TFLOP/s (0.61 of the bf16 GEMM rate); 4096 over
+// 16384: 1098 us, 1315 TFLOP/s (0.69).  A page takes 1840 cycles where its
 // four products need 1024: the scores' products read their 128 query rows from
 // shared memory for 64 columns (48 cycles a step instead of 32), and 16384
-// exponentials take 1024 cycles.  Both score buffers in one product pair that
+// exponentials, their sums and roundings keep the softmax warps busy for 1400.  Both score buffers in one product pair that
 // reads the queries once lost more (423 us): the softmax then waits for each
 // pair.
 #include "tern_kv8.cuh"
