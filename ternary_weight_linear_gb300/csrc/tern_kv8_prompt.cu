@@ -30,13 +30,10 @@
 // sum, O) go to the workspace, and the last CTA of a block adds them in order.
 //
 // Measured: 2048 tokens of 6 query heads per key-value head over 8190 cached,
-// head of 128: 314 us, 1149 TFLOP/s (0.61 of the bf16 GEMM rate); 4096 over
-// 16384: 1098 us, 1315 TFLOP/s (0.69).  A page takes 1840 cycles where its
-// four products need 1024: the scores' products read their 128 query rows from
-// shared memory for 64 columns (48 cycles a step instead of 32), and 16384
-// exponentials, their sums and roundings keep the softmax warps busy for 1400.  Both score buffers in one product pair that
-// reads the queries once lost more (423 us): the softmax then waits for each
-// pair.
+// head of 128: 293 us, 1229 TFLOP/s (0.65 of the bf16 GEMM rate); 4096 over
+// 16384: 1016 us, 1421 TFLOP/s (0.75).  Both score buffers in one product pair
+// that reads the queries from shared memory once lost a quarter: the softmax
+// then waits for each pair.
 #include "tern_kv8.cuh"
 
 namespace tern {
@@ -84,20 +81,31 @@ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The whole warp calls these, and one lane issues: with uniform control flow
+// the descriptors stay in uniform registers (under a branch of one lane each
+// product moved six of them, and eight products took 1050 cycles to issue).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
       : "memory");
 }
 
@@ -434,49 +442,55 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
     if (warp >= kMmaW) {
       // ---------------------------------------------------------- MMAs
-      const int i = (warp - kMmaW) >> 1;  // query tile
-      const int j_end = jt + t1 - t0;
+      const int role = __shfl_sync(0xffffffffu, warp, 0) - kMmaW;
+      const int i = role >> 1;  // query tile
+      const int j0 = __shfl_sync(0xffffffffu, jt, 0) + (kSplit ? i : 0);
+      const int j_end = __shfl_sync(0xffffffffu, jt + t1 - t0, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0);
+      const int see = __shfl_sync(0xffffffffu, kSplit ? 2 : tiles_q, 0);
       auto wait_conv = [&](uint64_t* full, int j) {
         return mbar_wait_clk(&full[j % L::kConv], (j / L::kConv) & 1, a.err);
       };
       const uint64_t dc = desc_sw128(smem_addr(smem + L::kConvOff), L::kBlockB);
-      if (lane == 0 && ok && (kSplit || i < tiles_q)) {
-        if (((warp - kMmaW) & 1) == 0) {
+      if (i < see) {
+        if ((role & 1) == 0) {
           // S of page n, into the columns of page n - 2's scores and weights
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, kBlk, false);
           const uint64_t q = desc_sw128(smem_addr(smem + L::kQOff + i * L::kQTileB), 16);
-          for (int j = jt + (kSplit ? i : 0); j < j_end && ok; j += kStep) {
+          for (int j = j0; j < j_end; j += kStep) {
             const int n = j / kStep;
-            ok = wait_conv(k_full, j) && (n < 2 || wait_values(i, n - 2));
+            ok = ok && wait_conv(k_full, j) && (n < 2 || wait_values(i, n - 2));
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             const uint64_t k = dc + static_cast<uint64_t>(((j % L::kConv) * 2 * L::kTileB) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tbase + s_col(i, n),
+              mma_ss(tm + s_col(i, n),
                      q + static_cast<uint64_t>(((kk >> 2) * L::kQBlockB + (kk & 3) * 32) >> 4),
                      k + static_cast<uint64_t>(((kk >> 2) * L::kBlockB + (kk & 3) * 32) >> 4),
                      idesc, kk != 0);
-            mma_commit(&s_full[2 * i + (n & 1)]);
-            mma_commit(&conv_empty[j % L::kConv]);
+            mma_commit_warp(&s_full[2 * i + (n & 1)]);
+            mma_commit_warp(&conv_empty[j % L::kConv]);
           }
         } else {
           // O += P V of page j
           constexpr uint32_t idesc = idesc_f16_f32(kPRows, D, true);
-          for (int j = jt + (kSplit ? i : 0); j < j_end && ok; j += kStep) {
+          for (int j = j0; j < j_end; j += kStep) {
             const int n = j / kStep;
-            ok = wait_conv(v_full, j) &&
+            ok = ok && wait_conv(v_full, j) &&
                  mbar_wait_clk(&p_full[2 * i + (n & 1)], (n >> 1) & 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             const uint64_t v =
                 dc + static_cast<uint64_t>((((j % L::kConv) * 2 + 1) * L::kTileB) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kBlk / 16; ++kk)
-              mma_ts(tbase + L::kOCol + i * 128, tbase + s_col(i, n) + kk * 8,
+              mma_ts(tm + L::kOCol + i * 128, tm + s_col(i, n) + kk * 8,
                      v + static_cast<uint64_t>((kk * 2048) >> 4), idesc, n != 0 || kk != 0);
-            mma_commit(&o_done[2 * i + (n & 1)]);
-            mma_commit(&conv_empty[j % L::kConv]);
+            mma_commit_warp(&o_done[2 * i + (n & 1)]);
+            mma_commit_warp(&conv_empty[j % L::kConv]);
           }
         }
       }
@@ -676,8 +690,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 
   // ---- results
-  if (warp >= kMmaW && lane == 0) {
-    mma_commit(mma_end);  // every MMA of the CTA has run before TMEM is freed
+  if (warp >= kMmaW) {
+    __syncwarp();
+    mma_commit_warp(mma_end);  // every MMA of the CTA has run before TMEM is freed
     mbar_wait_clk(mma_end, 0, a.err);
   }
   __syncwarp();
