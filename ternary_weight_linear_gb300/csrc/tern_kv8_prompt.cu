@@ -16,7 +16,8 @@
 // it is that much smaller.
 //
 // There is no int8 tcgen05 on sm_103a, so four warps turn each page of codes
-// into fp16 in shared memory, once for the two query tiles.
+// into fp16 in shared memory, once for the two query tiles: the keys as
+// (code + 128) 2^-24, whose bias each row takes off its scores.
 //
 // Warps: 0-3 and 4-7 the two query tiles' softmax, one row per thread (a
 // page's 64 scores read from TMEM once; P written over them); 8-11 the
@@ -46,6 +47,7 @@ constexpr int kPThreads = (kMmaW + 4) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
 constexpr int kAhead = 4;    // pages requested into L2 ahead of their conversion (kSplit)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
+constexpr float kUp = 16777216.f;  // 2^24, 1 over the keys' unit
 
 template <int D>
 struct PL {
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const bool live = warp < kSoftW && r < rows;
   int pos = -1;           // its position
   float cs = 0.f;         // softmax scale * log2(e) * 2^-a
+  float bias = 0.f;       // what 128 in every key's place adds to the row's scores
   const bool soft = warp < kSoftW && (warp & 3) < soft_warps(qt);
   if (soft) {
     const int rr = r0 + (live ? r : rows - 1);  // (past the last: a copy of it)
@@ -376,10 +379,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           float lo, hi;
           unpack16(w[e], a.type, lo, hi);
           w[e] = half2_bits(lo * f, hi * f);
+          unpack16(w[e], TERN_F16, lo, hi);
+          bias += lo + hi;
         }
         *reinterpret_cast<uint4*>(place(tr, c0 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    bias *= 128.f / kUp;
     fence_proxy_async_smem();
   }
   // positions of the block's last rows of tile 0 and first rows of tile 1
@@ -505,8 +511,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // lanes of a row's second half take the row beside it: the stores of
       // eight lanes then cover all banks
       const int c = tid % kC, row0 = (tid / kC) ^ ((c >> 2) & 1);
-      // a page's 64 rows to out, times mul (add = -1152 mul)
-      auto convert = [&](const uint4 (&v)[kBlk / kRowStep], uint8_t* out, uint32_t mul,
+      // a page's 64 rows to out: the values as code * mul (add = -1152 mul), the
+      // keys as subnormals (code + 128) 2^-24, a byte beside a zero byte
+      auto convert = [&](const uint4 (&v)[kBlk / kRowStep], uint8_t* out, bool keys, uint32_t mul,
                          uint32_t add) {
 #pragma unroll
         for (int k = 0; k < kBlk / kRowStep; ++k) {
@@ -516,10 +523,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t x = w[e] ^ 0x80808080u;
-            const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140);
-            const uint32_t hi = __byte_perm(x, 0x64646464u, 0x4342);
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e]) : "r"(lo), "r"(mul), "r"(add));
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * e + 1]) : "r"(hi), "r"(mul), "r"(add));
+            const uint32_t high = keys ? 0u : 0x64646464u;
+            o[2 * e] = __byte_perm(x, high, 0x4140);
+            o[2 * e + 1] = __byte_perm(x, high, 0x4342);
+            if (!keys) {
+              asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(o[2 * e]) : "r"(mul), "r"(add));
+              asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(o[2 * e + 1]) : "r"(mul), "r"(add));
+            }
           }
           // 16-byte chunks 2c and 2c + 1 of the row's 128-byte blocks
           uint8_t* dst = out + row * 128;
@@ -577,9 +587,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         uint32_t add;  // -1152 * 2^(e - E), exact
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
         auto both = [&](const uint4 (&kc)[kBlk / kRowStep], const uint4 (&vc)[kBlk / kRowStep]) {
-          convert(kc, out, 0x3C003C00u, 0xE480E480u);
+          convert(kc, out, true, 0u, 0u);
           if (lane == 0) mbar_arrive(&k_full[d]);
-          convert(vc, out + L::kTileB, mul, add);
+          convert(vc, out + L::kTileB, false, mul, add);
         };
         if constexpr (kSplit) {
           both(kv, vv);
@@ -613,7 +623,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_ld32(sc + 32, reinterpret_cast<uint32_t*>(v) + 32);
         const PageRec rec = recs[j - jt];
         // (a scale of 0 must not turn a masked -inf into a NaN)
-        const float c = fmaxf(cs * rec.ks, 1e-37f);
+        const float c = fmaxf(cs * rec.ks * kUp, 1e-37f);
         tmem_wait_ld();
         if (!(rec.meta >= 0 && ((rec.meta >> qt) & 1))) {
           const uint64_t see = rec.meta >= 0 ? kv_mask(a, pos, (rec.meta >> 2) * kBlk) : 0;
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int e = 0; e < 4; ++e)
             m4[e] = fmaxf(fmaxf(m4[e], v[k + e]), k + e + 4 < 64 ? v[k + e + 4] : v[k + e]);
         const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        const float top = big * c;  // -inf: no visible token
+        const float top = (big - bias) * c;  // -inf: no visible token
         const bool raise = top > ref + kPLazy;
         if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
           float alpha = escale;
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
           }
         }
-        const float add = kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref);
+        const float add = fmaf(-bias, c, kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref));
         const uint64_t c2 = pair_f32(c, c), add2 = pair_f32(add, add);
         uint64_t s2[2] = {0, 0};  // pairs of sums from +0
         uint32_t pw[32];
