@@ -31,8 +31,8 @@
 // sum, O) go to the workspace, and the last CTA of a block adds them in order.
 //
 // Measured: 2048 tokens of 6 query heads per key-value head over 8190 cached,
-// head of 128: 293 us, 1229 TFLOP/s (0.65 of the bf16 GEMM rate); 4096 over
-// 16384: 1016 us, 1421 TFLOP/s (0.75).  Both score buffers in one product pair
+// head of 128: 291 us, 1240 TFLOP/s (0.65 of the bf16 GEMM rate); 4096 over
+// 16384: 1010 us, 1430 TFLOP/s (0.75).  Both score buffers in one product pair
 // that reads the queries from shared memory once lost a quarter: the softmax
 // then waits for each pair.
 #include "tern_kv8.cuh"
@@ -162,6 +162,15 @@ struct OutRows {
 
 // The last part to arrive adds them all in order (every thread of the CTA) and
 // stages the rows.
+// Named barriers (0 is the whole CTA's, 1 the softmax warps').
+enum : int { kUsed = 2, kReady, kWritten, kQueries };
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, const float* first,
                                         int parts, int rows, int r0, int row0, int hk) {
@@ -241,8 +250,8 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
 // key-value head.  Both query tiles are then the same rows and take alternate
 // pages (page j of the CTA is tile i's page j / 2, for j % 2 == i), joined at
 // the end, and the four softmax warps without rows are a second group for the
-// conversion.  Measured, with it and without: 36.5 and 42.9 us (8 sequences, 20
-// rows, window 4096), 92 and 123 us (4 sequences of 32000 tokens, 24 rows); at
+// conversion.  Measured when it came, with it and without: 36.5 and 42.9 us (8
+// sequences, 20 rows, window 4096), 92 and 123 us (4 sequences of 32000 tokens, 24 rows); at
 // 96 rows, where no warps are idle, it loses (46.5 and 43.2 us, 16 tokens over
 // 16000).
 constexpr int kSplitRows = 64;
@@ -411,8 +420,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   for (int t0 = t_begin, chunk = 0; t0 < t_end; t0 += kPRecs, ++chunk) {
     const int t1 = t_end < t0 + kPRecs ? t_end : t0 + kPRecs;
     // ---- records of pages [t0, t1) of the list
-    cta_barrier();  // the records of the chunk before have been used
-    for (int i = threadIdx.x; i < t1 - t0; i += kPThreads) {
+    // (written by the warps that do not stage queries, so that the conversion
+    // starts under that)
+    if (warp >= kSoftW) {
+      if (chunk > 0) named_sync(kUsed, kPThreads);  // those of the chunk before
+    } else if (chunk > 0) {
+      named_arrive(kUsed, kPThreads);
+    }
+    for (int i = static_cast<int>(threadIdx.x) - kSoftW * 32; i >= 0 && i < t1 - t0;
+         i += kPThreads - kSoftW * 32) {
       int e = -127;
       PageRec rec = {0.f, 0.f, 0.f, -1};
       {
@@ -442,8 +458,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
       recs[i] = rec;
       rec_e[i] = e;
     }
-    if (threadIdx.x == 0) emax[(chunk & 1) ^ 1] = -127;
-    cta_barrier();
+    if (threadIdx.x == kSoftW * 32) emax[(chunk & 1) ^ 1] = -127;
+    __syncwarp();
+    if (warp >= kSoftW) {
+      named_arrive(kReady, kPThreads);
+      named_sync(kWritten, kPThreads - kSoftW * 32);
+      if (chunk == 0 && warp >= kMmaW) named_sync(kQueries, kPThreads - kConvW * 32);
+    } else {
+      if (chunk == 0) named_arrive(kQueries, kPThreads - kConvW * 32);
+      named_sync(kReady, kPThreads);
+    }
     const int En = emax[chunk & 1] > E ? emax[chunk & 1] : E;
 
     if (warp >= kMmaW) {

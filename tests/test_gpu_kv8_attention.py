@@ -182,6 +182,33 @@ def test_last_wave_in_parts(tl, m):
     assert not ws[:tl.SYNC_BYTES].any()
 
 
+@pytest.mark.parametrize("m", [20, 70])
+def test_blocks_of_more_pages_than_records(tl, m):
+    """More than 512 pages for a block of rows that is not cut into parts (the
+    sequences share pages); the sums' error grows with the n tokens, n * 2^-24
+    of A beside the others'."""
+    import torch
+    seqs, n, rng = 20, 33500, np.random.default_rng(64)
+    c = Case([3200], [m], 8, 8, 64, seed=65)
+    c.table = rng.permuted(np.tile(c.table[0, :50], (seqs, 11)), axis=1)[:, :530]
+    c.lens = (n - 64 * np.arange(seqs)).astype(np.int32)
+    c.start = (np.arange(seqs + 1) * m).astype(np.int32)
+    c.q_dev = torch.randn(seqs * m, 8, 64, device="cuda").bfloat16()
+    out = c.run(tl)
+    torch.cuda.synchronize()
+    assert tl.tern_device_status() == 0
+    assert torch.equal(out, c.run(tl))
+    for b in (0, seqs - 1):
+        rows = slice(b * m, (b + 1) * m)
+        q = c.q_dev[rows].float().cpu().numpy().astype(np.float64)
+        ref, _, absum = od.kv8_attention(q, c.codes, c.scales, c.table[b:b + 1],
+                                         np.asarray([0, m], np.int32), c.lens[b:b + 1], 0, 0,
+                                         64 ** -0.5)
+        err = np.abs(out[rows].float().cpu().numpy() - ref)
+        assert np.all(err <= (5 * 2.0 ** -11 + n * 2.0 ** -24) * absum + 2.0 ** -9 * np.abs(ref)
+                      + 2.0 ** -25)
+
+
 def test_more_sequences_than_one_launch_takes(tl):
     lens = [(31 * i) % 190 for i in range(300)]
     Case(lens, [min(1 + i % 2, n) for i, n in enumerate(lens)], 2, 1, 64, seed=31).check(tl)
