@@ -327,12 +327,6 @@ int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
   return TERN_OK;
 }
 
-// Query rows per key-value head (new tokens times group) up to which a
-// sequence takes the few-row kernel: its two tiles of eight.  Measured, that
-// kernel and the one on the tensor cores: 9.0 and 16.6 us (one token over 777,
-// 6 rows), 181 and 630 us (32 single tokens, 544000 cached); a form of the
-// former with four tiles, at 20 rows (4 new tokens, window 4096): 86 and 37 us.
-constexpr int kKvFewRows = 16;
 
 // Strides of a [rows][heads][dim] operand: rows and heads start on 16 bytes
 // and a head's elements are consecutive.
@@ -705,19 +699,26 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
                    static_cast<uint32_t>(dim), kKvRowsBox,
                    a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc != TERN_OK) return rc;
-  // Each sequence goes by its own rows: up to kKvFewRows per key-value head to
-  // the kernel that is bound by the cache's bytes, more to the one on the
-  // tensor cores.  A single sequence takes one launch, of the latter where
+  // Each sequence goes by its own rows: few of them per key-value head to the
+  // kernel that is bound by the cache's bytes, more to the one on the tensor
+  // cores.  A single sequence takes one launch, of the latter where
   // max_new allows more than the former takes.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool many = a.max_new * a.group > kKvFewRows;
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  long long pages = a.width;  // that a sequence's rows see, at most
+  if (a.window > 0) {
+    const long long seen = (static_cast<long long>(a.window) + a.max_new + a.sinks) / TERN_KV8_BLOCK + 4;
+    if (seen < pages) pages = seen;
+  }
+  const bool long_batch = pages * a.hkv * a.seqs >= static_cast<long long>(kKvLongPages) * d->sms;
+  const int few = most <= kKvFewRowsLong && long_batch ? kKvFewRowsLong : kKvFewRows;
+  const bool many = most > few;
   int launches = 0;
   if (!many || a.seqs > 1) {
-    if (launch_kv8_rows(&tm, a, kKvFewRows, d->sms, st, &launches) != cudaSuccess)
-      return TERN_ECUDA;
+    if (launch_kv8_rows(&tm, a, few, d->sms, st, &launches) != cudaSuccess) return TERN_ECUDA;
   }
   if (many) {
-    if (launch_kv8_prompt(a, a.seqs > 1 ? kKvFewRows + 1 : 1,
+    if (launch_kv8_prompt(a, a.seqs > 1 ? few + 1 : 1,
                           a.partials + kv8_rows_partial_bytes(a.dim) / sizeof(float),
                           a.tickets + 512, d->sms, st, &launches) != cudaSuccess)
       return TERN_ECUDA;

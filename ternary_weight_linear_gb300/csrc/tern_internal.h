@@ -228,6 +228,17 @@ cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t stream, int* launch
 // codes as bytes [pages * 2 * hkv * 64][dim], box dim x kKvRowsBox rows,
 // swizzle of the row's width.
 constexpr int kKvRowsBox = 32;
+// Query rows per key-value head (new tokens times group) up to which a
+// sequence takes the few-row kernel.  Measured, that kernel and the one on the
+// tensor cores: 9.0 and 16.6 us (one token over 777, 6 rows), 181 and 630 us
+// (32 single tokens, 544000 cached).
+constexpr int kKvFewRows = 16;
+// The same where no sequence has more and each SM gets at least kKvLongPages
+// pages: its three tiles of eight rows.  At 24 rows of 4 sequences: 71 and 90
+// us (105 pages an SM), 48 and 53 (53), 36.6 and 34.6 (26); at 20 rows under a
+// window 36.9 and 34.9 (28).  (With longer sequences in the batch the single
+// tokens among them would pay for the third tile.)
+constexpr int kKvFewRowsLong = 24, kKvLongPages = 40;
 constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
 size_t kv8_rows_partial_bytes(int dim);
 cudaError_t kv8_rows_set_attributes();

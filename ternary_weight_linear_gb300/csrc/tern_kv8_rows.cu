@@ -2,7 +2,7 @@
 // (decode steps): bound by the bytes of the cache.
 //
 // The rows of a sequence that share a key-value head (new tokens x heads of
-// the group, up to 16) are one or two tiles of eight, so every cache byte is
+// the group, up to 24) are one to three tiles of eight, so every cache byte is
 // read once for all of them.  Per half-page of 32 tokens a warp computes, with
 // m16n8k16 fp16 tensor instructions and fp32 sums, transposed so that tokens
 // (and then the elements of the output) are the operand of 16 rows and the
@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // instruction per pair, and products of all -128 for the bias; with two
   // tiles the values' separate sums would not fit the registers.
   constexpr bool kBiased = NT == 1;
+  // (three tiles read their queries from shared memory at each half-page)
+  constexpr bool kQRegs = NT < 3;
   constexpr float kUp = kBiased ? 16777216.f : 1.f;  // 1 over the codes' unit
   grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
@@ -240,7 +242,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 
   // ---- state of the current segment (one sequence and head)
   // (lane 4 g + t: rows 8 n + 2 t + x of tile n; sum: of the lane's tokens)
-  uint2 qf[NT][kW];  // the query fragments
+  uint2 qf[NT][kQRegs ? kW : 1];  // the query fragments
+  auto query = [&](int n, int j) {
+    const int unit = (D / 16) * t + j;
+    return lds_v2(smem + L::kQOff + (8 * n + g) * L::kQStride + (unit ^ (unit / (D / 8))) * 8);
+  };
   float o[NT][kMT][4];
   float ref[NT][2], sum[NT][2], cs[NT][2];
   int pos[NT][2];  // the rows' positions; -1: no row
@@ -391,11 +397,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int j = 0; j < kW; ++j) {
-            const int unit = (D / 16) * t + j;
-            qf[n][j] = lds_v2(smem + L::kQOff + (8 * n + g) * L::kQStride +
-                              (unit ^ (unit / (D / 8))) * 8);
-          }
+          for (int j = 0; kQRegs && j < kW; ++j) qf[n][j] = query(n, j);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int r = 8 * n + 2 * t + x;
@@ -466,7 +468,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               af[x + 2] = code_pair<kBiased>(u, 0x4342);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(sc[n][i], af, qf[n][j].x, qf[n][j].y);
+            for (int n = 0; n < NT; ++n) {
+              if (!kQRegs && i == 0) qf[n][0] = query(n, j);
+              mma_16816(sc[n][i], af, qf[n][kQRegs ? j : 0].x, qf[n][kQRegs ? j : 0].y);
+            }
           }
         if (!(rec_row & (kMAll << half))) {
           const int in = static_cast<int>((h >> 1) + c0 - s_begin);
@@ -638,9 +643,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     }
     const bool whole = s_begin >= u_begin && s_end <= u_end;
     __syncthreads();
-    if (threadIdx.x < kRows * 16) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < kRows * 16; i += kRW * 32) {
       // factor of warp w's O in row r: its weight over the sum, in units of 1
-      const int r = threadIdx.x / 16, w = threadIdx.x % 16;
+      const int r = i / 16, w = i % 16;
       const float2 v = w < kRW ? ml[w * kRows + r] : make_float2(0.f, 0.f);
       float big = v.y == 0.f ? -INFINITY : v.x;
 #pragma unroll
@@ -833,7 +839,7 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
 size_t kv8_rows_partial_bytes(int dim) {
   // two parts a range: each CTA's, and as many short ones
   static_assert(2 * kSmallTMaxCtas <= kQueue, "tickets");
-  return static_cast<size_t>(2 * kSmallTMaxCtas) * 2 * 16 * (dim + 2) * sizeof(float);
+  return static_cast<size_t>(2 * kSmallTMaxCtas) * 2 * kKvFewRowsLong * (dim + 2) * sizeof(float);
 }
 
 cudaError_t kv8_rows_set_attributes() {
@@ -842,6 +848,8 @@ cudaError_t kv8_rows_set_attributes() {
   };
   cudaError_t e = allow(kv8_rows_kernel<64, 1>, RL<64, 1>::kAlloc);
   if (e == cudaSuccess) e = allow(kv8_rows_kernel<64, 2>, RL<64, 2>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<64, 3>, RL<64, 3>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 3>, RL<128, 3>::kAlloc);
   if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 1>, RL<128, 1>::kAlloc);
   if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 2>, RL<128, 2>::kAlloc);
   return e;
@@ -849,12 +857,14 @@ cudaError_t kv8_rows_set_attributes() {
 
 cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
                             cudaStream_t stream, int* launches) {
-  // one tile of rows where no sequence has more than eight
-  if (static_cast<long long>(a.max_new) * a.group <= 8)
-    return a.dim == 128 ? launch_one<128, 1>(tm, a, max_rows, num_sms, stream, launches)
-                        : launch_one<64, 1>(tm, a, max_rows, num_sms, stream, launches);
-  return a.dim == 128 ? launch_one<128, 2>(tm, a, max_rows, num_sms, stream, launches)
-                      : launch_one<64, 2>(tm, a, max_rows, num_sms, stream, launches);
+  // as many tiles of rows as the largest of the kernel's sequences can have
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  const int tiles = static_cast<int>(((most < max_rows ? most : max_rows) + 7) / 8);
+  const bool wide = a.dim == 128;
+  const auto launch = tiles == 1   ? (wide ? launch_one<128, 1> : launch_one<64, 1>)
+                      : tiles == 2 ? (wide ? launch_one<128, 2> : launch_one<64, 2>)
+                                   : (wide ? launch_one<128, 3> : launch_one<64, 3>);
+  return launch(tm, a, max_rows, num_sms, stream, launches);
 }
 
 }  // namespace tern

@@ -148,7 +148,7 @@ def test_long_context_is_split_and_reproducible(tl, m):
     assert not ws[:tl.SYNC_BYTES].any()
 
 
-@pytest.mark.parametrize("m", [1, 5])
+@pytest.mark.parametrize("m", [1, 5, 10])
 def test_long_batch_on_shared_pages(tl, m):
     """A batch long enough that CTAs take further ranges as they finish (the
     sequences share pages, as after a common prefix): the same bits each time,
@@ -167,6 +167,26 @@ def test_long_batch_on_shared_pages(tl, m):
     for _ in range(3):
         assert torch.equal(a, c.run(tl, workspace=ws))
     assert not ws[:tl.SYNC_BYTES].any()
+
+
+@pytest.mark.parametrize("dim,heads,kv,m", [(128, 6, 1, 4), (64, 40, 8, 5), (64, 32, 8, 5),
+                                               (128, 34, 2, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3000, 70)])
+def test_three_tiles_of_rows(tl, dim, heads, kv, m, window, sinks):
+    """17 to 25 rows per key-value head of a long batch, on shared pages."""
+    import torch
+    seqs, rng = -(-7000 // (46 * kv)), np.random.default_rng(66)
+    c = Case([3200], [m], heads, kv, dim, seed=67)
+    c.table = np.stack([rng.permutation(c.table[0, :50]) for _ in range(seqs)]).astype(np.int32)
+    c.lens = (3200 - rng.integers(0, 300, seqs)).astype(np.int32)
+    c.lens[1] = 0
+    new = np.minimum(m, c.lens)
+    new[2] = min(1, m - 1)
+    c.start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    c.q_dev = torch.randn(int(c.start[-1]), heads, dim, device="cuda").bfloat16()
+    c.check(tl, window, sinks)
+    # (25 rows: the kernel for more rows, beside the one for sequences of few)
+    assert tl.tern_last_launches() == -(-seqs // 128) + (m * heads // kv > 24)
 
 
 @pytest.mark.parametrize("m", [20, 70])
