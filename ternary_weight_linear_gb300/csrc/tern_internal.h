@@ -230,7 +230,7 @@ cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t stream, int* launch
 constexpr int kKvRowsBox = 32;
 // Query rows per key-value head (new tokens times group) up to which a
 // sequence takes the few-row kernel.  Measured, that kernel and the one on the
-// tensor cores: 9.0 and 16.6 us (one token over 777, 6 rows), 181 and 630 us
+// tensor cores: 9.3 and 16.6 us (one token over 777, 6 rows), 181 and 630 us
 // (32 single tokens, 544000 cached).
 constexpr int kKvFewRows = 16;
 // The same where no sequence has more and each SM gets at least kKvLongPages
