@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     return mbar_wait_clk(&o_done[2 * i + (n & 1)], (n >> 1) & 1, a.err);
   };
 
-  int E = -127;
+  int E = -127;     // of the converted pages
+  int lead = -127;  // (softmax) of the tile's O: it has E's once a page has rescaled it, and
+                    // the second tile of kSplit may have none in a set of records
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
 
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     } else if (soft) {
       // ---------------------------------------------------------- softmax
       const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
-      float escale = En == E ? 1.f : exp2f(static_cast<float>(E - En));
+      float escale = En == lead ? 1.f : exp2f(static_cast<float>(lead - En));
       const int j_end = jt + t1 - t0;
       for (int j = jt + (kSplit ? qt : 0); j < j_end; j += kStep) {
         const int n = j / kStep;
@@ -671,6 +673,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
           float alpha = escale;
           escale = 1.f;
+          lead = En;
           if (raise) {
             const float f = exp2_approx(ref - top);  // 0 for the row's first
             alpha *= f;
@@ -746,7 +749,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
     const bool have = n > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, n - 1));
     tc_fence_after();
-    float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(E)) / sum;
+    float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(lead)) / sum;
     float inv1 = 0.f;  // tile 1's share of the sum
     // tile 1's sixteen columns q of the row, in the converted pages' place
     float4* other = reinterpret_cast<float4*>(smem + L::kConvOff) + tr;
