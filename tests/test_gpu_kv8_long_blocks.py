@@ -92,3 +92,35 @@ def test_value_exponent_rises_with_the_last_records(tl, dim, pages, m):
     torch.cuda.synchronize()
     assert tl.tern_device_status() == 0 and tl.tern_last_launches() == 2
     check_sequences(c, tl, out, (0, 18, 19), m)
+
+
+# What only the split form of the prompt kernel does (25 to 64 rows a head; up
+# to 24 a long batch of few rows goes to the other kernel, which would be one
+# launch).
+
+@pytest.mark.parametrize("m", [30, 64])
+def test_split_blocks_of_more_pages_than_records(tl, m):
+    import torch
+    seqs, kv, dim = 20, 8, 64
+    c = shared_pages(seqs, 531, 1, kv, kv, dim, m, seed=m)
+    c.lens = (530 * 64 + 1 - 64 * np.arange(seqs)).astype(np.int32)  # 531 pages to 512
+    out = c.run(tl)
+    torch.cuda.synchronize()
+    assert tl.tern_device_status() == 0 and tl.tern_last_launches() == 2
+    assert torch.equal(out, c.run(tl))
+    check_sequences(c, tl, out, (0, 7, 18, 19), m)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,m", [(32, 30), (64, 32), (96, 9)])
+def test_split_blocks_of_the_last_wave_in_parts(tl, heads, m, dim):
+    """160 blocks of rows: the last ones are cut along the keys."""
+    import torch
+    c = Case([2500, 2400, 2300, 2200, 2100], [m] * 5, heads, 32, dim, seed=heads + m)
+    a = c.check(tl)
+    ws = torch.zeros(tl.tern_kv8_attention_workspace_bytes(5, 5 * m, heads, 32, dim),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(a, c.run(tl, workspace=ws))
+        assert tl.tern_last_launches() == 2
+    assert not ws[:tl.SYNC_BYTES].any()
