@@ -276,6 +276,24 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   return v;
 }
 
+// Loads of what an earlier kernel of the stream writes.  A kernel launched with
+// programmatic serialisation begins before that kernel has ended, and ld.global.nc
+// (which the compiler may also choose for const __restrict__ pointers) asks
+// for memory that does not change while the kernel lives: so plain loads, after
+// grid_dependency_wait.
+__device__ __forceinline__ uint4 ldg_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // Shared-memory loads through ordinary pointers: the compiler sees them as
 // memory reads, keeps them after the mbarrier waits (which clobber memory) and
 // is free to schedule them early against the arithmetic.

@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int k = 0; k < kBlk / kRowStep; ++k) {
           kv[k] = vv[k] = make_uint4(0u, 0u, 0u, 0u);
           if (page >= 0) {
-            kv[k] = ldg_nc_v4(src + k * kRowStep * D);
-            vv[k] = ldg_nc_v4(src + static_cast<size_t>(a.hkv) * L::kRawB + k * kRowStep * D);
+            kv[k] = ldg_v4(src + k * kRowStep * D);
+            vv[k] = ldg_v4(src + static_cast<size_t>(a.hkv) * L::kRawB + k * kRowStep * D);
           }
         }
       };

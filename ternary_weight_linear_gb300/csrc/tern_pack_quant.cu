@@ -355,9 +355,9 @@ __global__ void __launch_bounds__(kCodeThreads) code_pieces_kernel(
   grid_dependency_wait();  // the codes and the output buffers come from earlier work
   const long long first = static_cast<long long>(blockIdx.x) * kCodeThreads + threadIdx.x;
   const long long stride = static_cast<long long>(gridDim.x) * kCodeThreads;
-  for (long long t = first; t < T; t += stride) xs[t] = x_scale[t];
+  for (long long t = first; t < T; t += stride) xs[t] = __uint_as_float(ldg_u32(x_scale + t));
   for (long long i = first; i < blocks; i += stride) {
-    const uint4 v = *reinterpret_cast<const uint4*>(q + 16 * i);
+    const uint4 v = ldg_v4(q + 16 * i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float r[16];
 #pragma unroll

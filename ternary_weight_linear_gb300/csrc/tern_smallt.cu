@@ -564,9 +564,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_codes_kernel(
     uint32_t raw = 0;
     float xs = 0.f;
     if (t < Tt) {
-      xs = x_scale[tok0 + t];
-      if (kbase < K)
-        raw = *reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(tok0 + t) * K + kbase);
+      xs = __uint_as_float(ldg_u32(x_scale + tok0 + t));
+      if (kbase < K) raw = ldg_u32(q + static_cast<size_t>(tok0 + t) * K + kbase);
     }
     const int sign = signbit(xs) ? -1 : 1;
     uint32_t hp[3] = {0u, 0u, 0u};
