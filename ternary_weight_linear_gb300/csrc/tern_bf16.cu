@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(256) interleave_kernel(const uint16_t* __restr
   grid_dependency_wait();  // x and the output buffer come from earlier work
   for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < blocks;
        b += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const uint4 lo = ldg_nc_v4(x + 16 * b);      // k 0..7
-    const uint4 hi = ldg_nc_v4(x + 16 * b + 8);  // k 8..15
+    const uint4 lo = ldg_v4(x + 16 * b);      // k 0..7
+    const uint4 hi = ldg_v4(x + 16 * b + 8);  // k 8..15
     const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w};
     const uint32_t c[4] = {hi.x, hi.y, hi.z, hi.w};
     uint32_t o[8];
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(256) interleave_rot_kernel(const uint16_t* __r
     float v[32];
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      const uint2 raw = *reinterpret_cast<const uint2*>(src + 128 * g + 4 * lane);
+      const uint2 raw = ldg_v2(src + 128 * g + 4 * lane);
       v[4 * g + 0] = __uint_as_float(raw.x << 16);
       v[4 * g + 1] = __uint_as_float(raw.x & 0xFFFF0000u);
       v[4 * g + 2] = __uint_as_float(raw.y << 16);

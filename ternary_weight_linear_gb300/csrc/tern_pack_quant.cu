@@ -253,7 +253,7 @@ constexpr uint32_t kQCopy = 16384;
 constexpr size_t kQSmemPerSm = 228 * 1024;  // shared memory of an SM
 constexpr int kQCtasPerSm = 4;              // the kernel's registers allow four CTAs
 enum : int { kQGlobal = 0, kQRotate = 1, kQStaged = 2 };
-__global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t* __restrict__ x,
+__global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t* x,
                                                                  uint8_t* __restrict__ p1,
                                                                  uint8_t* __restrict__ p2,
                                                                  float* __restrict__ xs, int T,
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t*
       float v[32];
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        const uint2 raw = *reinterpret_cast<const uint2*>(row + b * kRotBlock + 128 * g + 4 * lane);
+        const uint2 raw = ldg_v2(row + b * kRotBlock + 128 * g + 4 * lane);
         v[4 * g + 0] = bf16_lo(raw.x);
         v[4 * g + 1] = bf16_hi(raw.x);
         v[4 * g + 2] = bf16_lo(raw.y);

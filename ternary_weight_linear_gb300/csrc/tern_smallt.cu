@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_kernel(const uint16
       const int t = task / groups, kbase = (task % groups) * 128 + 4 * lane;
       raw[u] = make_uint2(0u, 0u);
       if (task < tasks && t < Tt && kbase < K)
-        raw[u] = *reinterpret_cast<const uint2*>(x + static_cast<size_t>(tok0 + t) * K + kbase);
+        raw[u] = ldg_v2(x + static_cast<size_t>(tok0 + t) * K + kbase);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_kernel(const uint16
 // 16 bytes of shared memory: it fits beside a main-kernel CTA.
 template <int TT>
 __global__ void __launch_bounds__(kPrepWarps * 32, 16) xprep_i8_kernel(
-    const uint16_t* __restrict__ x, uint8_t* __restrict__ out, int K, int tok0, int Tt, int KS) {
+    const uint16_t* x, uint8_t* out, int K, int tok0, int Tt, int KS) {
   grid_dependents_launch();
   grid_dependency_wait();  // x (and this buffer's last reader) come from earlier work
   __shared__ float red[kPrepWarps];
@@ -608,8 +608,7 @@ __global__ void __launch_bounds__(32, 32) xprep_rot_kernel(const uint16_t* __res
     for (int g = 0; g < kGS; ++g) {
       uint2 raw = make_uint2(0u, 0u);
       if (t < Tt)  // K is a multiple of 1024: every group of the stage exists
-        raw = *reinterpret_cast<const uint2*>(x + static_cast<size_t>(tok0 + t) * K +
-                                              ks * kSTStageK + 128 * g + 4 * lane);
+        raw = ldg_v2(x + static_cast<size_t>(tok0 + t) * K + ks * kSTStageK + 128 * g + 4 * lane);
       v[4 * g + 0] = __uint_as_float(raw.x << 16);
       v[4 * g + 1] = __uint_as_float(raw.x & 0xFFFF0000u);
       v[4 * g + 2] = __uint_as_float(raw.y << 16);
@@ -1323,8 +1322,7 @@ __global__ void __launch_bounds__(TC<TT>::kThreads, 1)
         raw[q] = make_uint2(0u, 0u);
         const int gi = q < nq ? new_stage(vs, q) * kGS + jg : G;
         if (gi < G)
-          raw[q] = *reinterpret_cast<const uint2*>(x + static_cast<size_t>(tok0) * K + gi * 128 +
-                                                   4 * lane);
+          raw[q] = ldg_v2(x + static_cast<size_t>(tok0) * K + gi * 128 + 4 * lane);
       }
 #pragma unroll
       for (int q = 0; q < kSmallTX1MaxSlots; ++q) {
@@ -1378,8 +1376,7 @@ __global__ void __launch_bounds__(TC<TT>::kThreads, 1)
       // the group's x into this warp's staging area, the row's weights at the
       // same time: one memory round trip
       const int ga = ks * kGS + g;
-      const uint2 xv = *reinterpret_cast<const uint2*>(
-          x + static_cast<size_t>(tok0 + t) * K + ga * 128 + 4 * lane);
+      const uint2 xv = ldg_v2(x + static_cast<size_t>(tok0 + t) * K + ga * 128 + 4 * lane);
       uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
       if (pred) {
         const uint4* wq =

@@ -81,3 +81,35 @@ def test_layer_reads_the_codes_that_the_norm_wrote(tl, T):
 
     _same(step, 12)
     assert tl.tern_device_status() == 0
+
+
+# T of every token tile and rung; the switches that choose another reader of x
+@pytest.mark.parametrize("T", [1, 4, 12, 40])
+@pytest.mark.parametrize("env", [{}, {"TERN_DECODE_ACT": "int8", "TERN_PREFILL": "bf16"},
+                                 {"TERN_ROTATE": "1"},
+                                 {"TERN_ROTATE": "1", "TERN_PREFILL": "bf16"}])
+def test_layer_reads_the_activations_that_the_norm_wrote(tl, monkeypatch, T, env):
+    import torch
+    c = synth.case("tiny", T, K=2048, N=700, seed=T)
+    W, s, _ = to_device(c)
+    Wp = tl.tern_pack(W)
+    xs = [torch.randn(T, 2048, device="cuda") for _ in range(12)]
+    w = torch.ones(2048, device="cuda")
+    y = torch.empty(T, 2048, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(tl.tern_linear_workspace_bytes(T, 2048, 700), dtype=torch.uint8,
+                     device="cuda")
+
+    def step(i):
+        tl.tern_add_rmsnorm_s8(xs[i], w, y=y, quantise=False)
+        return tl.tern_linear(Wp, s, y, workspace=ws)
+
+    for k, v in env.items():
+        monkeypatch.setenv(k, v)
+    tl.tern_reload_env()
+    try:
+        _same(step, 12)
+    finally:
+        for k in env:
+            monkeypatch.delenv(k)
+        tl.tern_reload_env()
+    assert tl.tern_device_status() == 0
