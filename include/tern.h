@@ -243,9 +243,9 @@ int tern_linear(const uint32_t* Wpacked, const uint16_t* scales,
  *   y[t][n]      = x_scale[t] * sum_g s[n][g] * acc[t][n][g]   (fp32),
  * the s8 definition at every T, without quantising again.  T <= 16 runs on
  * the small-T rungs' kernels, T >= 17 on the s8 rung's; TERN_RUNG forces a
- * rung as for tern_linear (bf16 has no such form: TERN_EINVAL), the other
- * environment overrides (TERN_ROTATE, TERN_PREFILL, TERN_DECODE_ACT) do not
- * apply.
+ * rung as for tern_linear (bf16 has no such form: TERN_EINVAL).  Codes have no
+ * rotated form either: with TERN_ROTATE, TERN_EINVAL.  TERN_PREFILL and
+ * TERN_DECODE_ACT do not apply.
  *   q        device int8 [T][K], any value of -128..127
  *   x_scale  device fp32 [T]
  *   the others and the workspace as for tern_linear. */

@@ -312,7 +312,8 @@ def tern_linear_s8(Wpacked: torch.Tensor, scales: torch.Tensor, q: torch.Tensor,
     token scales x_scale [T] (tern_quant_act_s8's or tern_add_rmsnorm_s8's):
     y[t, n] = x_scale[t] * sum_g scales[n, g] * (exact integer sum of group g).
 
-    The workspace is tern_linear's, with the same rules."""
+    The workspace is tern_linear's, with the same rules.  Refused where
+    TERN_ROTATE is set: codes cannot be rotated any more."""
     T, K = q.shape
     N = Wpacked.shape[0]
     need = tern_linear_workspace_bytes(T, K, N)

@@ -558,7 +558,10 @@ int tern_linear_s8(const uint32_t* Wpacked, const uint16_t* scales, const int8_t
       !aligned16(y))
     return TERN_EALIGN;
   Config c = config();
-  c.prefill_bf16 = c.rotate = c.decode_int8 = false;
+  // codes cannot be rotated any more, and the layer's weights are in the
+  // rotated basis where the switch is set
+  if (c.rotate) return TERN_EINVAL;
+  c.prefill_bf16 = c.decode_int8 = false;
   const int rung = pick_rung(c, T);
   if (rung == TERN_RUNG_BF16) return TERN_EINVAL;
   DevState* d = nullptr;
