@@ -412,8 +412,8 @@ def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
     pk = _strided(k, "k", _TYPES, 3)
     pv = _strided(v, "v", (k.dtype,), 3)
-    if k.shape != v.shape or k.stride() != v.stride() or k.shape[1:] != (codes.shape[2],
-                                                                         codes.shape[4]):
+    if (k.shape != v.shape or _heads_strides(k) != _heads_strides(v)
+            or k.shape[1:] != (codes.shape[2], codes.shape[4])):
         raise ValueError("k and v must be [rows, kv_heads, head_dim] with the same strides")
     rows = k.shape[0]
     rc = load().tern_kv8_append(

@@ -1,0 +1,40 @@
+"""Corners of the norm's and the append's arguments."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tl():
+    import torch
+    import ternary_weight_linear_gb300 as tl
+    tl.build()
+    tl.load()
+    torch.cuda.init()
+    return tl
+
+
+def test_append_takes_one_row_or_head_of_any_stride(tl):
+    """The stride of a dimension of one element does not matter: keys from a
+    fused projection, values of their own."""
+    import torch
+    for rows, heads in ((1, 4), (3, 1), (1, 1)):
+        wide = torch.randn(rows, 3 * heads + 1, 64, device="cuda")
+        k, v = wide[:, heads:2 * heads], torch.randn(rows, heads, 64, device="cuda")
+        if heads == 1 and rows > 1:
+            v = torch.randn(rows, 4, 64, device="cuda")[:, 2:3]  # rows apart as k's
+        got = []
+        for a, b in ((k, v), (k.contiguous(), v.contiguous())):
+            codes = torch.zeros(2, 2, heads, 64, 64, dtype=torch.int8, device="cuda")
+            scales = torch.zeros(2, 2, heads, device="cuda")
+            table = torch.tensor([[1]], dtype=torch.int32, device="cuda")
+            start = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+            tl.tern_kv8_append(a, b, codes, scales, table, start, start[1:].clone())
+            got.append((codes, scales))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert tl.tern_device_status() == 0
+    k, v = (torch.randn(2, 4, 64, device="cuda"), torch.randn(2, 6, 64, device="cuda")[:, :4])
+    codes = torch.zeros(2, 2, 4, 64, 64, dtype=torch.int8, device="cuda")
+    with pytest.raises(ValueError):  # two rows: their strides have to agree
+        tl.tern_kv8_append(k, v, codes, torch.zeros(2, 2, 4, device="cuda"), table, start,
+                           start[1:].clone())
