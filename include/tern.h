@@ -271,8 +271,8 @@ int tern_linear_s8(const uint32_t* Wpacked, const uint16_t* scales,
  *   y        device bf16 [T][K], written with y rounded once (what the
  *            bf16-activation rungs take), or NULL; q or y must be given
  *   T >= 1; K > 0, K % 16 == 0, K <= 32768; eps >= 0.
- * The statistics are fp32.  A row that holds an infinity or a NaN gives
- * unspecified codes and a scale that is not finite or 0. */
+ * The statistics are fp32.  A row that holds an infinity or a NaN, in r or in
+ * y, gives unspecified codes and a scale that is not finite or 0. */
 int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
                         const void* residual, void* residual_out,
                         int residual_type, const void* weight, int weight_type,

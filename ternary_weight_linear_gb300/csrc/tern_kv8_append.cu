@@ -25,13 +25,6 @@ namespace {
 
 constexpr int kAppThreads = 256;
 
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* p, long long i, float (&v)[8]) {
   if constexpr (TYPE == TERN_F32) {

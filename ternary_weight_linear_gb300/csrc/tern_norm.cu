@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
         for (int e = 0; e < 8; ++e) {
           sum = fmaf(rj.v[e], rj.v[e], sum);
           rj.v[e] *= w[k].v[e];
-          big = fmaxf(big, fabsf(rj.v[e]));
+          big = max_nan(big, fabsf(rj.v[e]));  // (the weight's NaN is not in the sum)
         }
       }
     }
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
   }
   if (lane == 0) {
     red_s[warp] = sum;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
     }
   }
   const float inv = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);

@@ -6,6 +6,13 @@
 
 namespace tern {
 
+// max that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Per-token code of v: rint(v / scale) clamped to [-127, 127], the quotient
 // rounded as one IEEE single-precision division (nearest-even, as rint).
 // Without a division per element: with inv = 1 / scale rounded, q0 = v * inv

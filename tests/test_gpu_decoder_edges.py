@@ -38,3 +38,20 @@ def test_append_takes_one_row_or_head_of_any_stride(tl):
     with pytest.raises(ValueError):  # two rows: their strides have to agree
         tl.tern_kv8_append(k, v, codes, torch.zeros(2, 2, 4, device="cuda"), table, start,
                            start[1:].clone())
+
+
+@pytest.mark.parametrize("width", [256, 9984, 32768])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_norm_weight_that_is_not_finite(tl, width, bad):
+    """Such a y reaches the scale: max|y| / 127 is not finite."""
+    import torch
+    x = torch.randn(3, width, device="cuda")
+    x[1, 8] = 0  # 0 * inf
+    w = torch.ones(width, device="cuda")
+    w[8] = float(bad)
+    y = torch.empty(3, width, dtype=torch.bfloat16, device="cuda")
+    q, s, _ = tl.tern_add_rmsnorm_s8(x, w, y=y)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(s).any()
+    assert torch.isnan(s[1]) and torch.isnan(y[1, 8].float())
+    assert torch.isfinite(y[:, 9:].float()).all()
