@@ -329,7 +329,8 @@ typedef struct {
  *           or TERN_F16); row r, head h start at element r * ld + h * hd
  *           (k and v have the same strides); every start 16-byte aligned
  *   rows    rows of k and v; 0: nothing is done
- *   max_new at least the most new tokens of a sequence (sizes the grid)
+ *   max_new at least the most new tokens of a sequence, and at least 1 where
+ *           there are rows (sizes the grid)
  * No two sequences of a call may share a page that receives new tokens. */
 int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v,
                     int type, long long ld, long long hd, int rows,

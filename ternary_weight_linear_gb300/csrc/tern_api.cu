@@ -617,7 +617,7 @@ int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v, i
   Kv8Args a;
   int rc = kv8_args(cache, &a);
   if (rc != TERN_OK) return rc;
-  if (type < TERN_F32 || type > TERN_F16 || rows < 0 || max_new < 1 ||
+  if (type < TERN_F32 || type > TERN_F16 || rows < 0 || max_new < (rows > 0) ||
       !kv8_strides_ok(ld, hd, a.dim))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
@@ -662,7 +662,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   int rc = kv8_args(cache, &a);
   if (rc != TERN_OK) return rc;
   if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
-      heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < 1 || window < 0 || sinks < 0 ||
+      heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < (rows > 0) || window < 0 || sinks < 0 ||
       static_cast<long long>(rows) * (heads / a.hkv) > INT_MAX ||
       !(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f) || !kv8_strides_ok(ld, hd, a.dim))
     return TERN_EINVAL;

@@ -1,5 +1,7 @@
 """Host-side checks of the decoder operators' C entries that need no GPU: what
 is refused before any device work."""
+import ctypes
+
 import pytest
 
 import ternary_weight_linear_gb300 as tl
@@ -24,3 +26,22 @@ def test_layer_on_codes_has_no_rotated_form(monkeypatch):
     finally:
         monkeypatch.delenv("TERN_ROTATE")
         tl.tern_reload_env()
+
+
+def cache(pages=8, seqs=2, width=4, kv_heads=8, dim=64):
+    return ctypes.byref(tl._KV8Cache(P, P, P, P, P, pages, seqs, width, kv_heads, dim))
+
+
+def attention(c, rows, max_new, heads=8, ws=1 << 40):
+    return tl.load().tern_kv8_attention(c, P, 1, heads * 64, 64, rows, heads, max_new, 0, 0, 0.125,
+                                        P, None, P, ws, None)
+
+
+def test_no_rows_need_no_max_new():
+    lib = tl.load()
+    assert attention(cache(), 0, 0) == 0
+    assert lib.tern_kv8_append(cache(), None, None, 1, 512, 64, 0, 0, None) == 0
+    for max_new in (-1, 0):
+        assert attention(cache(), 1, max_new) == EINVAL
+        assert lib.tern_kv8_append(cache(), P, P, 1, 512, 64, 1, max_new, None) == EINVAL
+    assert attention(cache(), 0, -1) == EINVAL
