@@ -294,8 +294,8 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
  *   row_start   device int32 [seqs + 1], ascending: the new tokens of sequence
  *           b are rows [row_start[b], row_start[b + 1]) of q, k and v; they
  *           are its last tokens, in order
- * pages * 2 * kv_heads * 64, table_width * 64 and rows * heads / kv_heads
- * have to fit in 31 bits (TERN_EINVAL).
+ * pages * 2 * kv_heads * 64, table_width * 64, table_width * kv_heads and
+ * rows * heads / kv_heads have to fit in 31 bits (TERN_EINVAL).
  * Sequences may be empty and may have no new tokens.  These arrays are read
  * on the device, so a captured call can be replayed with other contents.  A
  * sequence whose entries are inconsistent (a length that is negative or does

@@ -306,9 +306,11 @@ int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
       c->kv_heads > 16384 || (c->head_dim != 64 && c->head_dim != 128))
     return TERN_EINVAL;
   // rows of the codes' tensor map have 32-bit coordinates; a sequence's
-  // tokens have 32-bit positions
+  // tokens have 32-bit positions, and so have its pages of all heads (of which
+  // a table may name one more than once)
   if (static_cast<long long>(c->pages) * 2 * c->kv_heads * TERN_KV8_BLOCK > 0x7FFFFFFFll ||
-      static_cast<long long>(c->table_width) * TERN_KV8_BLOCK > 0x7FFFFFFFll)
+      static_cast<long long>(c->table_width) * TERN_KV8_BLOCK > 0x7FFFFFFFll ||
+      static_cast<long long>(c->table_width) * c->kv_heads > 0x7FFFFFFFll)
     return TERN_EINVAL;
   if (!aligned16(c->codes) || !aligned16(c->scales) || !aligned16(c->page_table) ||
       !aligned16(c->seq_lens) || !aligned16(c->row_start))

@@ -45,3 +45,12 @@ def test_no_rows_need_no_max_new():
         assert attention(cache(), 1, max_new) == EINVAL
         assert lib.tern_kv8_append(cache(), P, P, 1, 512, 64, 1, max_new, None) == EINVAL
     assert attention(cache(), 0, -1) == EINVAL
+
+
+def test_a_sequence_of_too_many_pages_and_heads_is_refused():
+    """The pages of a sequence's heads are counted in 32 bits."""
+    wide = cache(pages=64, seqs=1, width=1 << 20, kv_heads=4096)
+    assert attention(wide, 1, 1, heads=4096, ws=0) == EINVAL
+    assert tl.load().tern_kv8_append(wide, P, P, 1, 4096 * 64, 64, 0, 1, None) == EINVAL
+    # (the next check is the workspace's)
+    assert attention(cache(64, 1, (1 << 19) - 1, 4096), 1, 1, heads=4096, ws=0) == -3
