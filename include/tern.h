@@ -358,7 +358,9 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
  *   lse     device fp32 [rows][heads], written with log sum_j exp(s_j)
  *           (natural logarithm), or NULL
  *   heads   a multiple of kv_heads, at most 64 times as many
- *   max_new at least the most new tokens of a sequence
+ *   max_new at least the most new tokens of a sequence, and at least 1 where
+ *           there are rows; ceil(max_new * heads / kv_heads / 256) * kv_heads *
+ *           seqs has to stay below 2^31 - 1000 (TERN_EINVAL)
  *   window  0 (none) or the tokens that a row sees, itself included
  *   sinks   first tokens that stay visible outside the window (>= 0)
  *   softmax_scale > 0

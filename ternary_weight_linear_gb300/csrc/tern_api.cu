@@ -669,7 +669,8 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
       !(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f) || !kv8_strides_ok(ld, hd, a.dim))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
-  if (!q || !out) return TERN_EINVAL;
+  if (!q || !out || !kv8_prompt_fits(max_new < rows ? max_new : rows, heads / a.hkv, a.hkv, a.seqs))
+    return TERN_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ld % 8 != 0 || hd % 8 != 0)
     return TERN_EALIGN;
   if (!workspace || workspace_bytes < tern_kv8_attention_workspace_bytes(a.seqs, rows, heads,

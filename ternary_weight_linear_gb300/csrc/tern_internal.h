@@ -249,6 +249,8 @@ cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_row
 // head, on the tensor cores.  tickets: kSmallTMaxCtas zeroed ints.
 size_t kv8_prompt_partial_bytes(int dim);
 cudaError_t kv8_prompt_set_attributes();
+// Whether the kernel's grid holds the blocks of rows of such a call.
+bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs);
 cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches);
 

@@ -857,6 +857,16 @@ size_t kv8_prompt_partial_bytes(int dim) {
   return static_cast<size_t>(2 * kSmallTMaxCtas) * 2 * kPRows * (dim + 2) * sizeof(float);
 }
 
+// Blocks of rows of a sequence, a CTA each (and more where the last wave is cut).
+static long long row_blocks_of(long long max_new, int group) {
+  return (max_new * group + 2 * kPRows - 1) / (2 * kPRows);
+}
+
+bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs) {
+  return row_blocks_of(max_new, group) * kv_heads <=
+         (0x7FFFFFFFll - 2 * kSmallTMaxCtas) / seqs;
+}
+
 cudaError_t kv8_prompt_set_attributes() {
   const auto allow = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -870,8 +880,8 @@ cudaError_t kv8_prompt_set_attributes() {
 
 cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches) {
-  const long long most = a.max_new * a.group;
-  const long long row_blocks = (most + 2 * kPRows - 1) / (2 * kPRows);
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  const long long row_blocks = row_blocks_of(a.max_new, a.group);
   // Whole waves of items run as they are.  The keys of the items left (the
   // earliest rows, the last to start) are cut into parts so that they end
   // together: as many as cost the least pages of time in sequence on an SM,
@@ -892,7 +902,6 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
     if (cost < best) best = cost, parts = p;
   }
   const long long grid = whole + tail * parts;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)), dim3(kPThreads),

@@ -54,3 +54,10 @@ def test_a_sequence_of_too_many_pages_and_heads_is_refused():
     assert tl.load().tern_kv8_append(wide, P, P, 1, 4096 * 64, 64, 0, 1, None) == EINVAL
     # (the next check is the workspace's)
     assert attention(cache(64, 1, (1 << 19) - 1, 4096), 1, 1, heads=4096, ws=0) == -3
+
+
+def test_a_grid_of_too_many_blocks_is_refused_before_any_launch():
+    """2^17 sequences of at most 2^20 new tokens, 8 heads: 2^32 blocks of rows."""
+    many = cache(seqs=1 << 17)
+    assert attention(many, 1 << 20, 1 << 20, ws=0) == EINVAL
+    assert attention(many, 1 << 20, 1, ws=0) == -3  # (the next check is the workspace's)
