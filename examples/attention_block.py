@@ -129,8 +129,9 @@ def main():
         end.synchronize()
         print(f"{rows:5d} new tokens, {sum(pages.lens):5d} cached: "
               f"{begin.elapsed_time(end) * 1e3:8.1f} us")
-    if tl.tern_device_status():
-        raise RuntimeError(tl.tern_status_string(tl.tern_device_status()))
+    status = tl.tern_device_status()  # (reading it clears it)
+    if status:
+        raise RuntimeError(tl.tern_status_string(status))
 
 
 if __name__ == "__main__":
