@@ -69,30 +69,20 @@ __device__ __forceinline__ bool kv_all(const Kv8Args& a, int p0, int p1, int j0,
   return j1 <= p0 && (a.window == 0 || j0 > p1 - a.window || j1 < a.sinks);
 }
 
-// A value scale as 2^e * f, f in [1, 2): the codes take 2^e (exactly, in
-// fp16, relative to a running exponent) and the weights take f.  A scale that
-// is not finite keeps out of the exponents and makes f NaN, so that exactly
-// the rows that see its block get NaN; 0 (whose codes are 0) and subnormals
-// count as 2^-127.
+// A value scale as 2^e * f, f in [1, 2), for scales > 0 (subnormal ones too).
+// Zero is kZeroExp: below every other exponent, so that 2^(e - E) is 0, whatever
+// the block's codes are.
+constexpr int kZeroExp = -100000, kNoExp = -150;  // kNoExp: below every scale's exponent
 struct VScale {
   int e;
   float f;
 };
 __device__ __forceinline__ VScale split_vscale(float s) {
-  const uint32_t u = __float_as_uint(s);
-  const int ex = (u >> 23) & 0xFF;
-  VScale v;
-  if (ex == 255) {
-    v.e = -127;
-    v.f = __uint_as_float(0x7FC00000u);
-  } else if (ex == 0) {
-    v.e = -127;
-    v.f = 1.f;
-  } else {
-    v.e = ex - 127;
-    v.f = __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u);
-  }
-  return v;
+  if (s == 0.f) return {kZeroExp, 1.f};
+  const bool sub = s < 1.17549435e-38f;  // 2^-126
+  const uint32_t u = __float_as_uint(sub ? s * 16777216.f : s);
+  return {static_cast<int>(u >> 23) - 127 - (sub ? 24 : 0),
+          __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u)};
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

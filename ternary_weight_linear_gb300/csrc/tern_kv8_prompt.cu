@@ -8,7 +8,9 @@
 //   S = Q Kc^T,  s = S * (softmax_scale * log2(e) * k_scale * 2^-a(row))
 //   P = 2^(s + log2 f - ref + 10),  O += P (2^(e - E) Vc),  l += P / f
 // with Q scaled by 2^a per row into fp16, Kc and Vc the int8 codes (exact in
-// fp16), v_scale = 2^e f and E the largest e so far.  P is rounded to fp16
+// fp16), v_scale = 2^e f and E the largest e so far.  (Where the blocks' e lie
+// more than 24 apart, which fp16 does not hold, P takes the whole v_scale and
+// each row has a reference of its own for it: wide_pages.)  P is rounded to fp16
 // (relative 2^-11, the tensor instruction's operand; the row's sum takes it
 // unrounded).  ref is the row's running maximum, raised (and O rescaled) only
 // when a score passes it by 2^4: P stays below 2^15 (fp16 ends at 65504) and
@@ -47,6 +49,9 @@ constexpr int kPThreads = (kMmaW + 4) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
 constexpr int kAhead = 4;    // pages requested into L2 ahead of their conversion (kSplit)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
+// Value scales whose exponents lie up to this far apart share one: a code times
+// 2^-24 is exact in fp16.
+constexpr int kSpan = 24;
 constexpr float kUp = 16777216.f;  // 2^24, 1 over the keys' unit
 
 template <int D>
@@ -63,7 +68,7 @@ struct PL {
   static constexpr int kRecOff = kConvOff + 2 * kConv * kTileB;  // PageRec, then pages and e
   static constexpr int kBarOff = kRecOff + kPRecs * 24;
   static constexpr int kNumBars = 3 * kConv + 4 + 4 + 4 + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, emax[2], last
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // TMEM address, last, emax, emin
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kSCol = 0, kOCol = 256;
@@ -127,6 +132,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -246,6 +258,115 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
   }
 }
 
+// The row of O at o_col times alpha.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t o_col, float alpha) {
+#pragma unroll 1
+  for (int q = 0; q < D / 16; ++q) {
+    uint32_t x[16];
+    tmem_ld16(o_col + 16 * q, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+    tmem_st16(o_col + 16 * q, x);
+  }
+}
+
+// A row's softmax: its reference and sum, and the unit of its O, 2^(ref + lead).
+struct SoftState {
+  float ref, sum, lead;
+  bool ok;
+};
+
+// The softmax warps' part where value scales are too far apart for one
+// exponent: a row's O has a unit of its own, which follows its largest weight
+// times value scale, beside the sum's 2^ref.  A set of `count` pages from page
+// jt on, every kStep-th of them of query tile qt; row: the row's place in TMEM.
+// (Rare, and a function of its own: inlined, it cost the usual loop 1.5 % by its
+// registers; 2048 tokens over 8190 296 and 292 us.)
+template <int D, int kStep>
+__device__ __noinline__ SoftState wide_pages(uint8_t* smem, const Kv8Args& a, SoftState st, int qt,
+                                             int jt, int count, uint32_t row, int pos, float cs,
+                                             float bias) {
+  using L = PL<D>;
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff) + 3 * L::kConv;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_done = p_full + 4;
+  const PageRec* recs = reinterpret_cast<const PageRec*>(smem + L::kRecOff);
+  const int* rec_e = reinterpret_cast<const int*>(recs + kPRecs) + kPRecs;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int j = jt + (kStep == 2 ? qt : 0); j < jt + count; j += kStep) {
+    const int n = j / kStep, buf = 2 * qt + (n & 1);
+    st.ok = st.ok && mbar_wait_clk(&s_full[buf], (n >> 1) & 1, a.err);
+    st.ok = __all_sync(0xffffffffu, st.ok);
+    if (!st.ok) break;
+    tc_fence_after();
+    const uint32_t sc = row + L::kSCol + qt * 128 + (n & 1) * kBlk;
+    const PageRec rec = recs[j - jt];
+    const float c = fmaxf(cs * rec.ks * kUp, 1e-37f);
+    const uint64_t see = rec.meta >= 0 ? kv_mask(a, pos, (rec.meta >> 2) * kBlk) : 0;
+    auto scores = [&](int q, uint32_t (&x)[16]) {
+      tmem_ld16(sc + 16 * q, x);
+      tmem_wait_ld();
+      const uint32_t bits = static_cast<uint32_t>(see >> (16 * q));
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (!(bits & (1u << k))) x[k] = __float_as_uint(-INFINITY);
+    };
+    float big = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t x[16];
+      scores(q, x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) big = fmaxf(big, __uint_as_float(x[k]));
+    }
+    const float top = (big - bias) * c;  // -inf: no visible token
+    const float lv = rec.lf + static_cast<float>(rec_e[j - jt]);
+    float unit = st.ref + st.lead, alpha = 1.f;  // (-inf at the row's first)
+    const bool raise = top + lv > unit + kPLazy;
+    if (raise) {
+      alpha = exp2_approx(unit - (top + lv));
+      unit = top + lv;
+    }
+    if (top > st.ref + kPLazy) {
+      st.sum *= exp2_approx(st.ref - top);
+      st.ref = top;
+    }
+    if (st.ref != -INFINITY) st.lead = unit - st.ref;
+    if (__any_sync(0xffffffffu, raise) && n > 0) {
+      // O has to hold everything up to the page before
+      st.ok = st.ok && mbar_wait_clk(&o_done[buf ^ 1], ((n - 1) >> 1) & 1, a.err);
+      tc_fence_after();
+      rescale_row<D>(row + L::kOCol + qt * 128, alpha);
+    }
+    // weights for the sum and, times the value scale, for the products
+    const float add = fmaf(-bias, c, kPOff - (st.ref == -INFINITY ? 0.f : st.ref));
+    const float add_o = add + (lv - st.lead);
+    float part = 0.f;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t x[16], w[8];
+      scores(q, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
+        part += exp2_approx(fmaf(x0, c, add)) + exp2_approx(fmaf(x1, c, add));
+        w[k] = half2_bits(exp2_approx(fmaf(x0, c, add_o)), exp2_approx(fmaf(x1, c, add_o)));
+      }
+      tmem_st8(sc + 8 * q, w);  // (over scores that have been read)
+    }
+    // (a NaN for the rows that see a block whose scale is not finite)
+    if (big != -INFINITY) st.sum = rec.rf == rec.rf ? st.sum + part : rec.rf;
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&p_full[buf]);
+  }
+  return st;
+}
+
 // kSplit: no sequence of the batch has more than kSplitRows = 64 rows for a
 // key-value head.  Both query tiles are then the same rows and take alternate
 // pages (page j of the CTA is tile i's page j / 2, for j % 2 == i), joined at
@@ -271,8 +392,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint64_t* o_done = p_full + 4;           // [tile][page parity] O holds the page
   uint64_t* mma_end = o_done + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
-  int* emax = reinterpret_cast<int*>(tmem_slot + 1);  // [2] by chunk parity
-  int* is_last = emax + 2;
+  int* is_last = reinterpret_cast<int*>(tmem_slot + 1);
+  int* emax = is_last + 1;  // largest and smallest exponent of the value scales so far
+  int* emin = emax + 1;
   PageRec* recs = reinterpret_cast<PageRec*>(smem + L::kRecOff);
   int* rec_page = reinterpret_cast<int*>(recs + kPRecs);  // -1: none
   int* rec_e = rec_page + kPRecs;
@@ -318,7 +440,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&p_full[i], soft_warps(i >> 1) > 0 ? soft_warps(i >> 1) : 1);
       mbar_init(&o_done[i], 1);
     }
-    emax[0] = emax[1] = -127;
+    *emax = kNoExp;
+    *emin = -kNoExp;
     mbar_init(mma_end, 4);
     fence_mbar_init();
   }
@@ -413,9 +536,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     return mbar_wait_clk(&o_done[2 * i + (n & 1)], (n >> 1) & 1, a.err);
   };
 
-  int E = -127;     // of the converted pages
-  int lead = -127;  // (softmax) of the tile's O: it has E's once a page has rescaled it, and
-                    // the second tile of kSplit may have none in a set of records
+  float lead = kNoExp;  // (softmax) the row's O is in units of 2^(ref + lead): E's once a page
+                        // has rescaled it, which in kSplit may not be this set of records'
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
 
@@ -431,7 +553,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int i = static_cast<int>(threadIdx.x) - kSoftW * 32; i >= 0 && i < t1 - t0;
          i += kPThreads - kSoftW * 32) {
-      int e = -127;
+      int e = kZeroExp;
       PageRec rec = {0.f, 0.f, 0.f, -1};
       {
         const int lp = pages.page(t0 + i);
@@ -442,10 +564,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         } else {
           const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
           const float ks = sc[0];
-          const VScale v = split_vscale(sc[a.hkv]);
+          const float vs = sc[a.hkv];
           // a scale that is not finite keeps out of the arithmetic and makes
           // 1 / f NaN
-          const bool good = fabsf(ks) < INFINITY && v.f == v.f;
+          const bool good = fabsf(ks) < INFINITY && fabsf(vs) < INFINITY;
+          const VScale v = split_vscale(good ? fabsf(vs) : 0.f);
           rec.ks = good ? ks : 0.f;
           rec.lf = good ? log2f(v.f) : 0.f;
           rec.rf = good ? 1.0f / v.f : __uint_as_float(0x7FC00000u);
@@ -453,14 +576,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           rec.meta = lp * 4 | (kv_all(a, p_first, p_end0, j0, j1) ? 1 : 0) |
                      (kv_all(a, p_beg1, p_last, j0, j1) ? 2 : 0);
           e = v.e;
-          atomicMax(&emax[chunk & 1], e);
+          if (e != kZeroExp) {
+            atomicMax(emax, e);
+            atomicMin(emin, e);
+          }
         }
         rec_page[i] = page;
       }
       recs[i] = rec;
       rec_e[i] = e;
     }
-    if (threadIdx.x == kSoftW * 32) emax[(chunk & 1) ^ 1] = -127;
     __syncwarp();
     if (warp >= kSoftW) {
       named_arrive(kReady, kPThreads);
@@ -470,7 +595,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (chunk == 0) named_arrive(kQueries, kPThreads - kConvW * 32);
       named_sync(kReady, kPThreads);
     }
-    const int En = emax[chunk & 1] > E ? emax[chunk & 1] : E;
+    // The exponent that the converted values share, unless (and then to the end)
+    // they lie too far apart.  (The next pages' records wait until every thread
+    // has been here.)
+    const int E = *emax;
+    const bool wide = E - *emin > kSpan;
 
     if (warp >= kMmaW) {
       // ---------------------------------------------------------- MMAs
@@ -608,7 +737,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* out = smem + L::kConvOff + d * (2 * L::kTileB) + (c >> 2) * L::kBlockB;
-        const uint32_t hp = half_pow2(rec_e[j - jt] - En);
+        const uint32_t hp = half_pow2((rec_e[j - jt] - E) & (wide ? 0 : -1));
         const uint32_t mul = hp | (hp << 16);
         uint32_t add;  // -1152 * 2^(e - E), exact
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(add) : "r"(mul), "r"(0xE480E480u));
@@ -634,9 +763,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     } else if (soft) {
       // ---------------------------------------------------------- softmax
       const uint32_t o_col = tbase + lane_off + L::kOCol + qt * 128;
-      float escale = En == lead ? 1.f : exp2f(static_cast<float>(lead - En));
       const int j_end = jt + t1 - t0;
-      for (int j = jt + (kSplit ? qt : 0); j < j_end; j += kStep) {
+      float escale = lead == static_cast<float>(E) ? 1.f : exp2f(lead - static_cast<float>(E));
+      if (wide) {
+        const SoftState now = wide_pages<D, kStep>(
+            smem, a, {ref, sum, lead, ok}, qt, jt, t1 - t0, tbase + lane_off, pos, cs, bias);
+        ref = now.ref, sum = now.sum, lead = now.lead, ok = now.ok;
+      }
+      for (int j = jt + (kSplit ? qt : 0); !wide && j < j_end; j += kStep) {
         const int n = j / kStep;
         ok = ok && mbar_wait_clk(&s_full[2 * qt + (n & 1)], (n >> 1) & 1, a.err);
         ok = __all_sync(0xffffffffu, ok);
@@ -673,7 +807,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (__any_sync(0xffffffffu, raise || escale != 1.f)) {
           float alpha = escale;
           escale = 1.f;
-          lead = En;
+          lead = static_cast<float>(E);
           if (raise) {
             const float f = exp2_approx(ref - top);  // 0 for the row's first
             alpha *= f;
@@ -684,16 +818,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // O has to hold everything up to the page before
             ok = ok && wait_values(qt, n - 1);
             tc_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t x[16];
-              tmem_ld16(o_col + 16 * q, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
-              tmem_st16(o_col + 16 * q, x);
-            }
+            rescale_row<D>(o_col, alpha);
           }
         }
         const float add = fmaf(-bias, c, kPOff + rec.lf - (ref == -INFINITY ? 0.f : ref));
@@ -722,7 +847,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
     }
     __syncwarp();  // one-thread roles
-    E = En;
     jt += t1 - t0;
   }
 
@@ -749,7 +873,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
     const bool have = n > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, n - 1));
     tc_fence_after();
-    float inv = sum == 0.f ? 0.f : exp2f(static_cast<float>(lead)) / sum;
+    float inv = sum == 0.f ? 0.f : exp2f(lead) / sum;
     float inv1 = 0.f;  // tile 1's share of the sum
     // tile 1's sixteen columns q of the row, in the converted pages' place
     float4* other = reinterpret_cast<float4*>(smem + L::kConvOff) + tr;
