@@ -8,13 +8,14 @@
 // (and then the elements of the output) are the operand of 16 rows and the
 // queries the one of eight:
 //   S^T = Kc Q^T,  s = S * (softmax_scale * log2(e) * k_scale * 2^-a(row))
-//   p = 2^(s - ref + 10),  O^T += Vc^T (p v_scale 2^-E),  l += p
+//   w = 2^(s + log2(v_scale) - ref + 10),  O^T += Vc^T w,  l += w / v_scale
 // with Q scaled by 2^a per row into fp16, Kc and Vc the int8 codes (exact in
-// fp16), E the exponent of the warp's largest v_scale so far.  p v_scale 2^-E
-// is rounded to fp16 (relative 2^-11, the tensor instruction's operand; the
-// row's sum takes p unrounded).  ref is the row's running maximum in the warp,
-// raised (and O rescaled) only when a score passes it by 2^4: the weights stay
-// below 2^15 (fp16 ends at 65504), and the lanes' maxima are joined only then.
+// fp16).  w is rounded to fp16 (relative 2^-11, the tensor instruction's operand;
+// the row's sum takes it unrounded).  ref is the running maximum of s +
+// log2(v_scale) over what the row sees in the warp, raised (and O rescaled) only
+// when a score passes it by 2^4: w stays below 2^15 (fp16 ends at 65504), and the
+// lanes' maxima are joined only then.  What w loses, below 2^-24, is small beside
+// the row's own largest weight times value scale, whatever other rows see.
 //
 // Why these instructions: the work is 2 MFLOP per 16 KB page and eight rows,
 // and operands that come straight from registers never write the codes back:
@@ -54,6 +55,15 @@ constexpr int kHalf = 32;     // tokens of a stage
 constexpr int kMergeRows = 4; // rows merged at a time
 constexpr int kRecs = 256;    // pages whose records are held at a time
 constexpr float kROff = 10.f, kRLazy = 4.f;
+// Value scales of 2^-38 to 2^38 (and 0) have their logarithm in the weights'
+// exponents; blocks of others are left to far_row.  (The least weight that the
+// sum must have, 2^(10 - 76) times 2^-40 beside the largest, is a normal number.)
+constexpr float kMinScale = 3.637978807091713e-12f, kMaxScale = 274877906944.f;
+// Whether a block is left to far_row.
+__device__ __forceinline__ bool far_scales(float ks, float vs) {
+  return fabsf(ks) < INFINITY && fabsf(vs) < INFINITY && vs != 0.f &&
+         !(vs >= kMinScale && vs <= kMaxScale);
+}
 // From this many pages per CTA an eighth of the units is left for short ranges.
 // A static split ends when the SM with the least share of the HBM rate does,
 // up to 19 % after the mean; a short range costs its CTA 3 us of records,
@@ -61,6 +71,7 @@ constexpr float kROff = 10.f, kRLazy = 4.f;
 // a CTA), 121 and 107 us (237 pages a CTA, 12 rows).
 constexpr int kQueueUnits = 384;
 constexpr int kQueue = 511;                // the ticket that counts the short ranges taken
+constexpr float kCodeUp = 16777216.f;        // 2^24
 constexpr uint32_t kNeg128 = 0x80808080u;   // a pair of -128 * 2^-24 in fp16
 
 // D: elements of a head.  NT: tiles of eight rows.
@@ -77,8 +88,7 @@ struct RL {
   static constexpr int kFacOff = kMlOff + kRW * kRows * 8;    // [kRows][kRW] factors
   static constexpr int kTotOff = kFacOff + kRW * kRows * 4;   // [kRows] (ref, sum)
   static constexpr int kQScaleOff = kTotOff + kRows * 8;      // [kRows] 2^-a
-  static constexpr int kExpOff = kQScaleOff + kRows * 4;      // [kRW] E
-  static constexpr int kRecOff = kExpOff + kRW * 4;           // [kRecs] PageRec, then rows
+  static constexpr int kRecOff = kQScaleOff + kRows * 4;  // [kRecs] PageRec, then rows
   static constexpr int kSeqOff = kRecOff + kRecs * 20;        // before[n + 1], len, m, row0
   static constexpr int kBarOff = kSeqOff + (kKvSeqsPerLaunch + 1) * 8 + kKvSeqsPerLaunch * 12;
   static constexpr int kBytes = kBarOff + kRW * kStages * 8;
@@ -91,9 +101,9 @@ struct RL {
 
 // What a half-page's arithmetic needs of its page, in one 16-byte load.
 struct __align__(16) PageRec {
-  float ks, vs;  // scales of the keys and of the values
-  float one;     // 1, or NaN where a scale is not finite
-  int e;         // vs < 2^(e + 1)
+  float ks, lv;  // scale of the keys; log2 of the scale of the values
+  float rv;      // 1 over the latter, or NaN where a scale is not finite
+  float any;     // 1, or 0 where the values have no part in the output
 };
 // Beside it, the first row of the page's keys in the codes' tensor map (a
 // multiple of 64) with these bits, or -1 for a page out of range.
@@ -128,6 +138,299 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
+// One tile of rows takes the codes as biased subnormals, which saves an
+// instruction per pair, and products of all -128 for the bias; with two tiles the
+// values' separate sums would not fit the registers.
+constexpr bool biased(int tiles) { return tiles == 1; }
+
+// Element unit j of a lane's part of the staged query 8 n + g.
+template <int D>
+__device__ __forceinline__ uint2 staged_query(const uint8_t* q, int n, int j, int g, int t) {
+  const int unit = (D / 16) * t + j;
+  return lds_v2(q + (8 * n + g) * (2 * D + 16) + (unit ^ (unit / (D / 8))) * 8);
+}
+
+// What the scores of a tile of queries start from: -128 * 2^-24 times the sums
+// of the rows' queries.
+template <int D, bool kBiased, typename Query>
+__device__ __forceinline__ void query_bias(const Query& query, float (&s0)[4]) {
+  const uint32_t neg128[4] = {kNeg128, kNeg128, kNeg128, kNeg128};
+#pragma unroll
+  for (int x = 0; x < 4; ++x) s0[x] = 0.f;
+#pragma unroll
+  for (int j = 0; kBiased && j < D / 16; ++j) {
+    const uint2 q = query(j);
+    mma_16816(s0, neg128, q.x, q.y);
+  }
+}
+
+// A warp's ring of half-pages and where they come from.
+template <int D>
+struct HalfRing {
+  uint8_t* ring;
+  uint64_t* full;
+  const int* where;
+  const CUtensorMap* tm;
+  int hkv;
+  // (whole warp) requests half-pages of the records, pre to end, until the ring
+  // is full
+  __device__ __forceinline__ void issue(int end, int& pre, unsigned& issued, unsigned used,
+                                        int lane) const {
+    constexpr int kStages = RL<D, 1>::kStages, kStage = RL<D, 1>::kStage;
+    while (pre < end && issued - used < kStages) {
+      const int rec = where[pre >> 1];
+      const int half = pre & 1;
+      if (rec >= 0 && (rec & (kMHalf << half))) {
+        if (lane == 0) {
+          const int s = issued % kStages;
+          const int row = (rec & ~(kBlk - 1)) + half * kHalf;
+          mbar_arrive_expect_tx(&full[s], kStage);
+          tma_load_2d(ring + s * kStage, tm, 0, row, &full[s]);
+          tma_load_2d(ring + s * kStage + kHalf * D, tm, 0, row + hkv * kBlk, &full[s]);
+        }
+        ++issued;
+      }
+      pre += kRW;
+    }
+  }
+};
+
+// S^T = Kc Q^T for 32 tokens, two tiles of 16 side by side.
+template <int D, int NT, typename Query>
+__device__ __forceinline__ void half_scores(const uint8_t* kb, int g, int t,
+                                            const float (&s0)[NT][4], float (&sc)[NT][2][4],
+                                            const Query& query) {
+  constexpr int kW = D / 16;  // words of a lane per key row (k steps)
+  uint32_t kw[4][kW];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint8_t* kr = kb + (8 * n + g) * D;
+    if constexpr (D == 128) {
+      const uint4 x = lds_v4(kr + (((2 * t) ^ g) << 4));
+      const uint4 y = lds_v4(kr + (((2 * t + 1) ^ g) << 4));
+      kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
+      kw[n][4] = y.x, kw[n][5] = y.y, kw[n][6] = y.z, kw[n][7] = y.w;
+    } else {
+      const uint4 x = lds_v4(kr + ((t ^ ((g >> 1) & 3)) << 4));
+      kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc[n][i][x] = s0[n][x];
+#pragma unroll
+  for (int j = 0; j < kW; ++j) {
+    uint2 q[NT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t af[4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t u = kw[2 * i + x][j] ^ 0x80808080u;
+        af[x] = code_pair<biased(NT)>(u, 0x4140);
+        af[x + 2] = code_pair<biased(NT)>(u, 0x4342);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (i == 0) q[n] = query(n, j);
+        mma_16816(sc[n][i], af, q[n].x, q[n].y);
+      }
+    }
+  }
+}
+
+// Scores of tokens (32 from j0) that the rows at pos do not see: -inf.
+template <int NT>
+__device__ __forceinline__ void half_mask(const Kv8Args& a, const int (&pos)[NT][2], int j0, int g,
+                                          float (&sc)[NT][2][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t see = static_cast<uint32_t>(kv_mask(a, pos[n][x], j0)) >> g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (!(see & (1u << (8 * k)))) sc[n][k >> 1][2 * (k & 1) + x] = -INFINITY;
+    }
+}
+
+// The values' codes: tokens 2t, 2t+1, 2t+8, 2t+9 of each step's 16.
+template <int D>
+__device__ __forceinline__ void half_values(const uint8_t* vb, int g, int t,
+                                            uint32_t (&vw)[2][4][D / 32]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t(&w)[4][D / 32] = vw[k];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = 16 * k + 2 * t + (x & 1) + 8 * (x >> 1);
+      if constexpr (D == 128) {
+        const uint4 v = lds_v4(vb + row * D + ((g ^ (row & 7)) << 4));
+        w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+      } else {
+        const uint2 v =
+            lds_v2(vb + row * D + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
+        w[x][0] = v.x, w[x][1] = v.y;
+      }
+    }
+  }
+}
+
+// O^T += Vc^T P^T, the weights P in the scores' place.
+template <int D, int NT>
+__device__ __forceinline__ void half_products(const float (&sc)[NT][2][4],
+                                              const uint32_t (&vw)[2][4][D / 32],
+                                              float (&o)[NT][D / 16][4]) {
+  constexpr bool kBiased = biased(NT);
+  const uint32_t neg128[4] = {kNeg128, kNeg128, kNeg128, kNeg128};
+  uint2 pf[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pf[n][i].x = transposed(half2_bits(sc[n][i][0], sc[n][i][1]));
+      pf[n][i].y = transposed(half2_bits(sc[n][i][2], sc[n][i][3]));
+    }
+  float oc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) oc[n][x] = 0.f;
+#pragma unroll
+    for (int k = 0; kBiased && k < 2; ++k) mma_16816(oc[n], neg128, pf[n][k].x, pf[n][k].y);
+  }
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) {
+    // elements 4 q to 4 q + 3 of the lane's group of D / 8, two at a time
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float od[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) od[n][x] = kBiased ? oc[n][x] : o[n][2 * q + i][x];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t(&w)[4][D / 32] = vw[k];
+        const uint32_t sel = i ? 0x7362 : 0x5140;
+        const uint32_t u0 = __byte_perm(w[0][q], w[1][q], sel) ^ 0x80808080u;
+        const uint32_t u1 = __byte_perm(w[2][q], w[3][q], sel) ^ 0x80808080u;
+        const uint32_t af[4] = {code_pair<kBiased>(u0, 0x4140), code_pair<kBiased>(u0, 0x4342),
+                                code_pair<kBiased>(u1, 0x4140), code_pair<kBiased>(u1, 0x4342)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_16816(od[n], af, pf[n][k].x, pf[n][k].y);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          float(&to)[4] = o[n][2 * q + i];
+          if (kBiased)
+            unpair_f32(add_pair(pair_f32(to[x], to[x + 1]), pair_f32(od[n][x], od[n][x + 1])),
+                       to[x], to[x + 1]);
+          else
+            to[x] = od[n][x], to[x + 1] = od[n][x + 1];
+        }
+    }
+  }
+}
+
+// A row's softmax over some pages: l = sum 2^(ref - kROff), and the row's output
+// of them (elements lane * D / 32 on).
+template <int D>
+struct FarRow {
+  float ref, sum, o[D / 32];
+};
+// The row at position p over those pages [begin, end) of the segment's list whose
+// value scales are out of [kMinScale, kMaxScale], by a warp: a token per lane for
+// the scores, elements per lane for the output, which has a reference of its own
+// (it follows the largest weight times value scale).  Such blocks are rare: what
+// counts is that there is little code.  query: the staged row; c: what a score
+// is times, but for the key scale.
+template <int D>
+__device__ __forceinline__ FarRow<D> far_row(const Kv8Args& a, const uint8_t* query, float c, int p,
+                                             int b, int hk, const KvPages& pages, int begin,
+                                             int end) {
+  const int lane = threadIdx.x & 31;
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kV = D / 32;
+  FarRow<D> f;
+  f.ref = -INFINITY;
+  f.sum = 0.f;
+#pragma unroll
+  for (int y = 0; y < kV; ++y) f.o[y] = 0.f;
+  float unit = -INFINITY;
+#pragma unroll 1
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    // a page per lane: is it one?
+    int page = -1, lp = 0;
+    float ks = 0.f, vs = 0.f;
+    if (i0 + lane < end) {
+      lp = pages.page(i0 + lane);
+      page = a.table[static_cast<size_t>(b) * a.width + lp];
+      if (page >= 0 && page < a.pages) {
+        const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
+        ks = sc[0], vs = sc[a.hkv];
+      }
+    }
+#pragma unroll 1
+    for (unsigned set = __ballot_sync(kAll, far_scales(ks, vs)); set; set &= set - 1) {
+      const int from = __ffs(set) - 1;
+      const size_t at = static_cast<size_t>(__shfl_sync(kAll, page, from)) * 2 * a.hkv + hk;
+      const float ck = fmaxf(c * __shfl_sync(kAll, ks, from), 1e-37f);
+      const float lv = log2f(__shfl_sync(kAll, vs, from));
+      const uint64_t see = kv_mask(a, p, __shfl_sync(kAll, lp, from) * kBlk);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int8_t* kr = a.codes + (at * kBlk + half * kHalf + lane) * D;
+        float s = 0.f;
+#pragma unroll 1
+        for (int e = 0; e < D; e += 4) {
+          const uint2 q = lds_v2(query + ((e / 4) ^ (e / 4 / (D / 8))) * 8);
+          const char4 k = *reinterpret_cast<const char4*>(kr + e);
+          float q0, q1, q2, q3;
+          unpack16(q.x, TERN_F16, q0, q1);
+          unpack16(q.y, TERN_F16, q2, q3);
+          s = fmaf(q0, k.x, fmaf(q1, k.y, fmaf(q2, k.z, fmaf(q3, k.w, s))));
+        }
+        s = (see >> (half * kHalf + lane)) & 1 ? s * ck : -INFINITY;
+        float top = s;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, k));
+        if (!__any_sync(kAll, s != -INFINITY)) continue;
+        if (top > f.ref) {
+          f.sum *= exp2_approx(f.ref - top);
+          f.ref = top;
+        }
+        if (top + lv > unit) {
+          const float less = exp2_approx(unit - (top + lv));
+          unit = top + lv;
+#pragma unroll
+          for (int y = 0; y < kV; ++y) f.o[y] *= less;
+        }
+        f.sum += exp2_approx(s - f.ref + kROff);
+        const float w = exp2_approx(s + lv - unit);
+        const int8_t* vr = a.codes + ((at + a.hkv) * kBlk + half * kHalf) * D + lane * kV;
+#pragma unroll 1
+        for (int j = 0; j < kHalf; ++j) {
+          const float wj = __shfl_sync(kAll, w, j);
+#pragma unroll
+          for (int y = 0; y < kV; ++y) f.o[y] = fmaf(wj, vr[j * D + y], f.o[y]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) f.sum += __shfl_xor_sync(kAll, f.sum, k);
+  const float one = f.sum == 0.f ? 0.f : exp2f(unit - f.ref + kROff) / f.sum;
+#pragma unroll
+  for (int y = 0; y < kV; ++y) f.o[y] *= one;
+  return f;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kRW * 32, 1)
     kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, int max_rows,
@@ -137,13 +440,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   constexpr int kW = D / 16;   // words of a lane per key row: 8 or 4 (k steps)
   constexpr int kMT = D / 16;  // tiles of 16 elements of the output
   constexpr int kVW = D / 32;  // words of a lane per value row: 4 or 2
-  // One tile of rows takes the codes as biased subnormals, which saves an
-  // instruction per pair, and products of all -128 for the bias; with two
-  // tiles the values' separate sums would not fit the registers.
-  constexpr bool kBiased = NT == 1;
+  constexpr bool kBiased = biased(NT);
   // (three tiles read their queries from shared memory at each half-page)
   constexpr bool kQRegs = NT < 3;
-  constexpr float kUp = kBiased ? 16777216.f : 1.f;  // 1 over the codes' unit
+  constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
   grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
@@ -156,7 +456,6 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   float2* tot = reinterpret_cast<float2*>(smem + L::kTotOff);
   float* qscale = reinterpret_cast<float*>(smem + L::kQScaleOff);
-  int* wexp = reinterpret_cast<int*>(smem + L::kExpOff);
   PageRec* recs = reinterpret_cast<PageRec*>(smem + L::kRecOff);
   int* where = reinterpret_cast<int*>(recs + kRecs);
   long long* before = reinterpret_cast<long long*>(smem + L::kSeqOff);  // units before a sequence
@@ -164,6 +463,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   int* seq_m = seq_len + kKvSeqsPerLaunch;
   int* seq_row0 = seq_m + kKvSeqsPerLaunch;
   __shared__ int s_last, s_next;
+  __shared__ int s_far;  // the CTA has met pages that are left to far_row
 
   if (lane == 0) {
     for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], 1);
@@ -184,7 +484,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     seq_m[b] = s.m;
     seq_row0[b] = s.row0;
   }
-  if (threadIdx.x == 0) before[0] = 0;
+  if (threadIdx.x == 0) {
+    before[0] = 0;
+    s_far = 0;
+  }
   __syncthreads();
   if (a.seqs > 1) {
     if (warp == 0) {
@@ -268,41 +571,20 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // ---- state of the current segment (one sequence and head)
   // (lane 4 g + t: rows 8 n + 2 t + x of tile n; sum: of the lane's tokens)
   uint2 qf[NT][kQRegs ? kW : 1];  // the query fragments
-  auto query = [&](int n, int j) {
-    const int unit = (D / 16) * t + j;
-    return lds_v2(smem + L::kQOff + (8 * n + g) * L::kQStride + (unit ^ (unit / (D / 8))) * 8);
-  };
+  auto query = [&](int n, int j) { return staged_query<D>(smem + L::kQOff, n, j, g, t); };
   float o[NT][kMT][4];
   float ref[NT][2], sum[NT][2], cs[NT][2];
   int pos[NT][2];  // the rows' positions; -1: no row
   float s0[NT][4];  // -128 * 2^-24 times the sums of the rows' queries
-  int E = -127;
-  float down = 0.f;  // 2^-E
-  const uint32_t neg128[4] = {kNeg128, kNeg128, kNeg128, kNeg128};
 
   unsigned issued = 0, used = 0;  // stages of this warp so far
   bool ok = true;
   long long c0 = u_begin, c1 = u_begin;  // units whose records are held
   int pre = 0;                           // next half-page of them that this warp requests
 
+  const HalfRing<D> from{ring, full, where, &tm, a.hkv};
   auto issue_ahead = [&]() {
-    // (whole warp) request half-pages until the ring is full
-    const int end = static_cast<int>(2 * (c1 - c0));
-    while (pre < end && issued - used < L::kStages) {
-      const int rec = where[pre >> 1];
-      const int half = pre & 1;
-      if (rec >= 0 && (rec & (kMHalf << half))) {
-        if (lane == 0) {
-          const int s = issued % L::kStages;
-          const int row = (rec & ~(kBlk - 1)) + half * kHalf;
-          mbar_arrive_expect_tx(&full[s], L::kStage);
-          tma_load_2d(ring + s * L::kStage, &tm, 0, row, &full[s]);
-          tma_load_2d(ring + s * L::kStage + kHalf * D, &tm, 0, row + a.hkv * kBlk, &full[s]);
-        }
-        ++issued;
-      }
-      pre += kRW;
-    }
+    from.issue(static_cast<int>(2 * (c1 - c0)), pre, issued, used, lane);
   };
 
   long long u = u_begin;
@@ -386,7 +668,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           split(uu - before[bb], pp.count, hh, lp);
           lp = pp.page(lp);
           const int page = a.table[static_cast<size_t>(bb) * a.width + lp];
-          PageRec rec = {0.f, 0.f, 1.f, -127};
+          PageRec rec = {0.f, 0.f, 1.f, 0.f};
           int row = -1;
           if (page < 0 || page >= a.pages) {
             atomicOr(a.err, kErrIndex);
@@ -394,18 +676,25 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hh;
             const float ks = sc[0];
             const float vs = sc[a.hkv];
-            // a scale that is not finite keeps out of the arithmetic
+            // (a scale of 0 weighs as one of 1; one that is not finite keeps out of
+            // the arithmetic)
             const bool good = fabsf(ks) < INFINITY && fabsf(vs) < INFINITY;
+            const bool far = far_scales(ks, vs);
             rec.ks = good ? ks : 0.f;
-            rec.vs = good ? vs : 0.f;
-            rec.one = good ? 1.f : __uint_as_float(0x7FC00000u);
-            const int ex = static_cast<int>((__float_as_uint(rec.vs) >> 23) & 0xFFu) - 127;
-            rec.e = ex;  // (-127: zero and subnormals)
+            if (!good) {
+              rec.rv = __uint_as_float(0x7FC00000u);
+            } else if (far) {
+              s_far = 1;
+            } else if (vs != 0.f) {
+              rec.lv = log2f(vs);
+              rec.rv = 1.0f / vs;
+              rec.any = 1.f;
+            }
             row = (page * 2 * a.hkv + hh) * kBlk;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const int j0 = lp * kBlk + hf * kHalf, j1 = j0 + kHalf - 1;
-              if (kv_any(a, p0, ll - 1, j0, j1)) row |= kMHalf << hf;
+              if (!far && kv_any(a, p0, ll - 1, j0, j1)) row |= kMHalf << hf;
               if (kv_all(a, p0, ll - 1, j0, j1)) row |= kMAll << hf;
             }
           }
@@ -435,13 +724,8 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s0[n][x] = 0.f;
-#pragma unroll
-          for (int j = 0; kBiased && j < kW; ++j) mma_16816(s0[n], neg128, qf[n][j].x, qf[n][j].y);
+          query_bias<D, kBiased>([&](int j) { return qf[n][j]; }, s0[n]);
         }
-        E = -127;
-        down = exp2f(127.f);
       }
       const long long piece = e_here < c1 ? e_here : c1;
       // this warp's half-pages of [u, piece): those congruent to its number
@@ -459,80 +743,21 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         const uint8_t* kb = ring + s * L::kStage;
         const uint8_t* vb = kb + kHalf * D;
 
-        // S^T = Kc Q^T for 32 tokens, two tiles of 16 side by side
         float sc[NT][2][4];
-        uint32_t kw[4][kW];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint8_t* kr = kb + (8 * n + g) * D;
-          if constexpr (D == 128) {
-            const uint4 x = lds_v4(kr + (((2 * t) ^ g) << 4));
-            const uint4 y = lds_v4(kr + (((2 * t + 1) ^ g) << 4));
-            kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
-            kw[n][4] = y.x, kw[n][5] = y.y, kw[n][6] = y.z, kw[n][7] = y.w;
-          } else {
-            const uint4 x = lds_v4(kr + ((t ^ ((g >> 1) & 3)) << 4));
-            kw[n][0] = x.x, kw[n][1] = x.y, kw[n][2] = x.z, kw[n][3] = x.w;
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) sc[n][i][x] = s0[n][x];
-#pragma unroll
-        for (int j = 0; j < kW; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t af[4];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t u = kw[2 * i + x][j] ^ 0x80808080u;
-              af[x] = code_pair<kBiased>(u, 0x4140);
-              af[x + 2] = code_pair<kBiased>(u, 0x4342);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (!kQRegs && i == 0) qf[n][0] = query(n, j);
-              mma_16816(sc[n][i], af, qf[n][kQRegs ? j : 0].x, qf[n][kQRegs ? j : 0].y);
-            }
-          }
+        half_scores<D, NT>(kb, g, t, s0, sc, [&](int n, int j) {
+          if (kQRegs) return qf[n][j];
+          return query(n, j);
+        });
         if (!(rec_row & (kMAll << half))) {
           const int in = static_cast<int>((h >> 1) + c0 - s_begin);
-          const int j0 = pages.page(in) * kBlk + half * kHalf;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t see = static_cast<uint32_t>(kv_mask(a, pos[n][x], j0)) >> g;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (!(see & (1u << (8 * k)))) sc[n][k >> 1][2 * (k & 1) + x] = -INFINITY;
-            }
+          half_mask<NT>(a, pos, pages.page(in) * kBlk + half * kHalf, g, sc);
         }
 
         // the values' codes, on their way under the softmax
-        uint32_t vw[2][4][kVW];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t(&w)[4][kVW] = vw[k];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the step's 16
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = 16 * k + 2 * t + (x & 1) + 8 * (x >> 1);
-            if constexpr (D == 128) {
-              const uint4 v = lds_v4(vb + row * D + ((g ^ (row & 7)) << 4));
-              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
-            } else {
-              const uint2 v =
-                  lds_v2(vb + row * D + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
-              w[x][0] = v.x, w[x][1] = v.y;
-            }
-          }
-        }
+        uint32_t vw[2][4][D / 32];
+        half_values<D>(vb, g, t, vw);
         // softmax of the half-page
-        const int En = rec.e > E ? rec.e : E;
-        bool raise = En != E;
+        bool raise = false;
         float c[NT][2], big[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -542,26 +767,22 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             c[n][x] = fmaxf(cs[n][x] * rec.ks * kUp, 1e-37f);
             big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
                               fmaxf(sc[n][1][x], sc[n][1][x + 2]));
-            raise = raise || big[n][x] * c[n][x] > ref[n][x] + kRLazy;
+            raise = raise || fmaf(big[n][x], c[n][x], rec.lv) > ref[n][x] + kRLazy;
           }
         if (__any_sync(0xffffffffu, raise)) {
-          const float shift = En != E ? exp2f(static_cast<float>(E - En)) : 1.f;
-          E = En;
-          down = exp2f(static_cast<float>(-E));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float scale[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float top = big[n][x] * c[n][x];  // -inf: no visible token
+              float top = fmaf(big[n][x], c[n][x], rec.lv);  // -inf: no visible token
 #pragma unroll
               for (int k = 4; k < 32; k <<= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-              scale[x] = shift;
+              scale[x] = 1.f;
               if (top > ref[n][x] + kRLazy) {
-                const float f = exp2_approx(ref[n][x] - top);  // 0 for the row's first
-                scale[x] *= f;
-                sum[n][x] *= f;
+                scale[x] = exp2_approx(ref[n][x] - top);  // 0 for the row's first
+                sum[n][x] *= scale[x];
                 ref[n][x] = top;
               }
             }
@@ -571,13 +792,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
           }
         }
-        const float vs = rec.vs * down;  // below 2
-        uint2 pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float add = kROff - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
+            const float add = kROff + rec.lv - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -585,63 +804,15 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               for (int y = x; y < 4; y += 2) {
                 sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
                 part += sc[n][i][y];
-                sc[n][i][y] *= vs;
+                sc[n][i][y] *= rec.any;
               }
             // (a scale that is not finite: the rows that see its page, and
             // only they, become NaN)
-            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.one, sum[n][x]);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            pf[n][i].x = transposed(half2_bits(sc[n][i][0], sc[n][i][1]));
-            pf[n][i].y = transposed(half2_bits(sc[n][i][2], sc[n][i][3]));
+            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rv, sum[n][x]);
           }
         }
 
-        // O^T += Vc^T P^T
-        float oc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) oc[n][x] = 0.f;
-#pragma unroll
-          for (int k = 0; kBiased && k < 2; ++k) mma_16816(oc[n], neg128, pf[n][k].x, pf[n][k].y);
-        }
-#pragma unroll
-        for (int q = 0; q < kVW; ++q) {
-          // elements 4 q to 4 q + 3 of the lane's group of D / 8, two at a time
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float od[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) od[n][x] = kBiased ? oc[n][x] : o[n][2 * q + i][x];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t(&w)[4][kVW] = vw[k];
-              const uint32_t sel = i ? 0x7362 : 0x5140;
-              const uint32_t u0 = __byte_perm(w[0][q], w[1][q], sel) ^ 0x80808080u;
-              const uint32_t u1 = __byte_perm(w[2][q], w[3][q], sel) ^ 0x80808080u;
-              const uint32_t af[4] = {
-                  code_pair<kBiased>(u0, 0x4140), code_pair<kBiased>(u0, 0x4342),
-                  code_pair<kBiased>(u1, 0x4140), code_pair<kBiased>(u1, 0x4342)};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma_16816(od[n], af, pf[n][k].x, pf[n][k].y);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                float(&to)[4] = o[n][2 * q + i];
-                if (kBiased)
-                  unpair_f32(add_pair(pair_f32(to[x], to[x + 1]), pair_f32(od[n][x], od[n][x + 1])),
-                             to[x], to[x + 1]);
-                else
-                  to[x] = od[n][x], to[x + 1] = od[n][x + 1];
-              }
-          }
-        }
+        half_products<D, NT>(sc, vw, o);
         __syncwarp();  // the stage has been read
         ++used;
         issue_ahead();
@@ -660,7 +831,6 @@ __global__ void __launch_bounds__(kRW * 32, 1)
         for (int k = 4; k < 32; k <<= 1) sum[n][x] += __shfl_xor_sync(0xffffffffu, sum[n][x], k);
         if (g == 0) ml[warp * kRows + 8 * n + 2 * t + x] = make_float2(ref[n][x], sum[n][x]);
       }
-    if (lane == 0) wexp[warp] = E;
     if (u >= u_end && extra > 0 && threadIdx.x == 0) {
       // the next range; every CTA fails once, and the last one clears the count
       s_next = atomicAdd(&a.tickets[kQueue], 1);
@@ -682,14 +852,16 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
       for (int k = 8; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
       if (w < kRW)
-        fac[r * kRW + w] = l == 0.f ? 0.f : f / l * exp2f(static_cast<float>(wexp[w]));
+        fac[r * kRW + w] = l == 0.f ? 0.f : f / l;
       if (w == 0) tot[r] = make_float2(big, l);
     }
-    const int first = whole ? 0 : range_of(s_begin);  // the segment's first range
+    // the segment's first range (a whole one has its place to itself)
+    const int first = whole ? range : range_of(s_begin);
     auto part_of = [&](int i) {  // the partial results of the segment in that range
       return a.partials + static_cast<size_t>(2 * i + (i == first ? 1 : 0)) * (kRows * (D + 2));
     };
     float* mine = part_of(range);
+    const bool far = s_far;
     // element d of a merged row, in chunks of four that eight lanes' stores
     // spread over all banks
     auto spread = [](int group, int chunk) {  // group of D / 8 elements, chunk of it
@@ -726,7 +898,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             if (f != 0.f) acc[y] = fmaf(f, src[w * kMergeRows * D + y], acc[y]);
         }
         const float2 v = tot[r];
-        if (whole) {
+        if (whole && !far) {
           const int2 at = row_of(r);
           const long long ob = static_cast<long long>(at.x) * a.heads + at.y;
           uint16_t* out = static_cast<uint16_t*>(a.out) + ob * D + d;
@@ -747,6 +919,42 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     for (int n = 0; n < NT; ++n)
 #pragma unroll 1
       for (int r0 = 8 * n; r0 < 8 * n + 8 && r0 < R; r0 += kMergeRows) merge_rows(r0, o[n]);
+    if (far) {
+      // the pages left out join what has been written beside them
+      for (int r = warp; r < R; r += kRW) {
+        const FarRow<D> f = far_row<D>(
+            a, smem + L::kQOff + r * L::kQStride, qscale[r] * a.scale_log2,
+            p_first + kv_token(a, r), b, hk, pages,
+            s_begin < u_begin ? static_cast<int>(u_begin - s_begin) : 0,
+            static_cast<int>(e_here - s_begin));
+        float* to = mine + r * D + lane * (D / 32);
+        float2* at = reinterpret_cast<float2*>(mine + kRows * D) + r;
+        const float2 v = *at;
+        const float top = fmaxf(v.y == 0.f ? -INFINITY : v.x, f.ref);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float w0 = v.y == 0.f ? 0.f : v.y * exp2f(v.x - base);
+        const float w1 = f.sum * exp2f(f.ref - base), l = w0 + w1;
+        const float f0 = l == 0.f ? 0.f : w0 / l, f1 = l == 0.f ? 0.f : w1 / l;
+        const int2 row = row_of(r);
+        const long long ob = static_cast<long long>(row.x) * a.heads + row.y;
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y) {
+          const float x = to[y] * f0 + f.o[y] * f1;
+          if (whole)
+            static_cast<uint16_t*>(a.out)[ob * D + lane * (D / 32) + y] =
+                static_cast<uint16_t>(pack_out(a.type, x, 0.f));
+          else
+            to[y] = x;
+        }
+        if (lane == 0) {
+          if (!whole)
+            *at = make_float2(base, l);
+          else if (a.lse)
+            a.lse[ob] = kv_log_sum(base, l, kROff);
+        }
+      }
+    }
     if (!whole) {
       // the last of the segment's CTAs adds the parts in their order, a row per
       // warp
