@@ -285,7 +285,9 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
  * that shares a scale: one fp32 scale for each (page, keys | values, head).
  *   codes   device int8 [pages][2][kv_heads][TERN_KV8_BLOCK][head_dim],
  *           keys at [0], values at [1] of the second index
- *   scales  device fp32 [pages][2][kv_heads]; a stored value is scale * code
+ *   scales  device fp32 [pages][2][kv_heads], not negative (the append writes
+ *           none that are; the attention reads a negative one as NaN); a stored
+ *           value is scale * code
  *   page_table  device int32 [seqs][table_width]: page of tokens
  *           [64 j, 64 j + 64) of each sequence; entries past a sequence's
  *           last token are not read

@@ -85,6 +85,12 @@ __device__ __forceinline__ VScale split_vscale(float s) {
           __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u)};
 }
 
+// Whether a block's scales can be used: finite and not negative.  (A block
+// whose scales cannot makes the rows that see it NaN, and only them.)
+__device__ __forceinline__ bool good_scales(float ks, float vs) {
+  return ks >= 0.f && ks < INFINITY && vs >= 0.f && vs < INFINITY;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

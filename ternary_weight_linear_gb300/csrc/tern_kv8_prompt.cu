@@ -357,7 +357,7 @@ __device__ __noinline__ SoftState wide_pages(uint8_t* smem, const Kv8Args& a, So
       }
       tmem_st8(sc + 8 * q, w);  // (over scores that have been read)
     }
-    // (a NaN for the rows that see a block whose scale is not finite)
+    // (a NaN for the rows that see a block whose scales cannot be used)
     if (big != -INFINITY) st.sum = rec.rf == rec.rf ? st.sum + part : rec.rf;
     tmem_wait_st();
     tc_fence_before();
@@ -565,10 +565,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
           const float ks = sc[0];
           const float vs = sc[a.hkv];
-          // a scale that is not finite keeps out of the arithmetic and makes
-          // 1 / f NaN
-          const bool good = fabsf(ks) < INFINITY && fabsf(vs) < INFINITY;
-          const VScale v = split_vscale(good ? fabsf(vs) : 0.f);
+          // scales that cannot be used keep out of the arithmetic and make 1 / f
+          // NaN
+          const bool good = good_scales(ks, vs);
+          const VScale v = split_vscale(good ? vs : 0.f);
           rec.ks = good ? ks : 0.f;
           rec.lf = good ? log2f(v.f) : 0.f;
           rec.rf = good ? 1.0f / v.f : __uint_as_float(0x7FC00000u);
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_st32(sc, pw);
         float s0, s1;
         unpair_f32(add_pair(s2[0], s2[1]), s0, s1);
-        // (a scale that is not finite has 1 / f = NaN: the rows that see its
+        // (scales that cannot be used have 1 / f = NaN: the rows that see the
         // page, and only they, become NaN)
         if (big != -INFINITY) sum = fmaf(s0 + s1, rec.rf, sum);
         tmem_wait_st();

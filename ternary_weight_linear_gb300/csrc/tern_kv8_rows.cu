@@ -61,8 +61,7 @@ constexpr float kROff = 10.f, kRLazy = 4.f;
 constexpr float kMinScale = 3.637978807091713e-12f, kMaxScale = 274877906944.f;
 // Whether a block is left to far_row.
 __device__ __forceinline__ bool far_scales(float ks, float vs) {
-  return fabsf(ks) < INFINITY && fabsf(vs) < INFINITY && vs != 0.f &&
-         !(vs >= kMinScale && vs <= kMaxScale);
+  return good_scales(ks, vs) && vs != 0.f && !(vs >= kMinScale && vs <= kMaxScale);
 }
 // From this many pages per CTA an eighth of the units is left for short ranges.
 // A static split ends when the SM with the least share of the HBM rate does,
@@ -102,7 +101,7 @@ struct RL {
 // What a half-page's arithmetic needs of its page, in one 16-byte load.
 struct __align__(16) PageRec {
   float ks, lv;  // scale of the keys; log2 of the scale of the values
-  float rv;      // 1 over the latter, or NaN where a scale is not finite
+  float rv;      // 1 over the latter, or NaN where the scales cannot be used
   float any;     // 1, or 0 where the values have no part in the output
 };
 // Beside it, the first row of the page's keys in the codes' tensor map (a
@@ -676,9 +675,9 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hh;
             const float ks = sc[0];
             const float vs = sc[a.hkv];
-            // (a scale of 0 weighs as one of 1; one that is not finite keeps out of
-            // the arithmetic)
-            const bool good = fabsf(ks) < INFINITY && fabsf(vs) < INFINITY;
+            // (a value scale of 0 weighs as one of 1; scales that cannot be used keep
+            // out of the arithmetic)
+            const bool good = good_scales(ks, vs);
             const bool far = far_scales(ks, vs);
             rec.ks = good ? ks : 0.f;
             if (!good) {
@@ -806,8 +805,8 @@ __global__ void __launch_bounds__(kRW * 32, 1)
                 part += sc[n][i][y];
                 sc[n][i][y] *= rec.any;
               }
-            // (a scale that is not finite: the rows that see its page, and
-            // only they, become NaN)
+            // (scales that cannot be used: the rows that see the page, and only
+            // they, become NaN)
             if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rv, sum[n][x]);
           }
         }

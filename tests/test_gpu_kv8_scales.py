@@ -159,3 +159,24 @@ def test_blocks_of_zero_scale(tl, seqs, m, heads, scale):
         page = c.own_page(at)
         c.scales[page, 1] = 0
     c.check_all(tl, (0, seqs - 1))
+
+
+@pytest.mark.parametrize("seqs,m,heads", FORMS)
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_negative_scale_reads_as_nan(tl, seqs, m, heads, which):
+    """The append writes none: the rows that see such a block, and only they,
+    become NaN, as with a scale that is not finite."""
+    import torch
+    c = Batch(seqs, 43 * 64 + 7, m, heads, 8, 64, seed=m)
+    window = 20 * 64
+    clean = c.run(tl, window=window)
+    page = c.own_page(43)
+    c.scales[page, which, 1] *= -1
+    got = c.run(tl, window=window).view(seqs, m, 8, -1)
+    clean = clean.view(got.shape)
+    torch.cuda.synchronize()
+    sees = (torch.arange(m, device="cuda") + 43 * 64 + 7 - m) >= 43 * 64
+    assert torch.isnan(got[:, sees, 1].float()).all()
+    assert torch.equal(got[:, ~sees], clean[:, ~sees])
+    rest = [h for h in range(8) if h != 1]
+    assert torch.equal(got[:, :, rest], clean[:, :, rest])
