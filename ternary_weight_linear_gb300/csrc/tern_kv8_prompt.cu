@@ -52,6 +52,14 @@ constexpr float kPOff = 10.f, kPLazy = 4.f;
 // Value scales whose exponents lie up to this far apart share one: a code times
 // 2^-24 is exact in fp16.
 constexpr int kSpan = 24;
+// Pages of time in sequence on an SM when `items` blocks of `pages` pages are cut
+// into parts, each of which costs some pages for its start, its result and the
+// join.  Parts have kPartPages pages at least.
+constexpr int kPartPages = 8, kPartCost = 14;
+__host__ __device__ constexpr unsigned part_cost(unsigned pages, unsigned parts, unsigned items,
+                                                 unsigned sms) {
+  return (items * parts + sms - 1) / sms * ((pages + parts - 1) / parts + kPartCost);
+}
 constexpr float kUp = 16777216.f;  // 2^24, 1 over the keys' unit
 
 template <int D>
@@ -379,7 +387,8 @@ constexpr int kSplitRows = 64;
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole,
-                      int tail_parts, float* __restrict__ partials, int* __restrict__ tickets) {
+                      int tail_parts, int tail_items, int sms, float* __restrict__ partials,
+                      int* __restrict__ tickets) {
   using L = PL<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
@@ -403,9 +412,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   // ---- this CTA's block of rows, sequence, head and part; late rows first
   const int tail = static_cast<int>(blockIdx.x) - whole;  // of the items in parts
-  const int parts = tail < 0 ? 1 : tail_parts;
-  const int part = tail < 0 ? 0 : tail % parts;
-  const int item = tail < 0 ? static_cast<int>(blockIdx.x) : whole + tail / parts;
+  const int part = tail < 0 ? 0 : tail % tail_parts;
+  const int item = tail < 0 ? static_cast<int>(blockIdx.x) : whole + tail / tail_parts;
   const int hk = item % a.hkv;
   const int b = (item / a.hkv) % a.seqs;
   const int rb = row_blocks - 1 - item / a.hkv / a.seqs;
@@ -421,6 +429,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int p_first = p_base + kv_token(a, r0);
   const int p_last = p_base + kv_token(a, r0 + rows - 1);
   const KvPages pages = kv_pages(a, p_first, p_last);
+  // (The launch chose the parts by the table's width, the most pages that a
+  // block can have: by its own it may need fewer, or none.)
+  int parts = 1;
+  if (tail >= 0 && tail_parts > 1) {
+    const int fit = pages.count / kPartPages;
+    const int p = tail_parts < fit ? tail_parts : fit;
+    if (p > 1 && part_cost(pages.count, p, tail_items, sms) <
+                     static_cast<unsigned>(pages.count + kPartCost))
+      parts = p;
+  }
+  if (part >= parts) return;
   const int t_begin = static_cast<int>(static_cast<long long>(pages.count) * part / parts);
   const int t_end = static_cast<int>(static_cast<long long>(pages.count) * (part + 1) / parts);
 
@@ -958,7 +977,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     cta_barrier();
     if (*is_last) {
       if (threadIdx.x == 0) tickets[item - whole] = 0;
-      join_parts<D>(a, smem, partials + static_cast<size_t>(item - whole) * parts * kPart, parts,
+      join_parts<D>(a, smem, partials + static_cast<size_t>(item - whole) * tail_parts * kPart, parts,
                     rows, r0, sq.row0, hk);
       cta_barrier();
       static_assert(kPThreads / 32 * 16 == 2 * kPRows, "rows of a warp");
@@ -1008,21 +1027,23 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
   const long long row_blocks = row_blocks_of(a.max_new, a.group);
   // Whole waves of items run as they are.  The keys of the items left (the
   // earliest rows, the last to start) are cut into parts so that they end
-  // together: as many as cost the least pages of time in sequence on an SM,
-  // where a part costs some pages for its start, its result and the join.
+  // together: as many as cost the least pages of time in sequence on an SM (at
+  // the table's width; the kernel leaves blocks of few pages whole).
   // Measured, with the cut and without (2048 tokens of 6 heads over 8190, 384
   // items on 152 SMs): 316 and 328 us; 4096 tokens over 16384: 1106 and 1227 us.
   const long long items = row_blocks * a.hkv * a.seqs;
   const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   const long long tail = items % sms, whole = items - tail;
-  constexpr int kPartCost = 14;
-  long long parts = 1, best = a.width;
+  unsigned parts = 1, best = a.width;
   // (the join holds a weight per part and row in the converted pages' place)
   const long long rows32 = most < 2 * kPRows ? (most + 31) / 32 * 32 : 2 * kPRows;
   const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32;
   static_assert(PL<64>::kConv * PL<64>::kTileB <= PL<128>::kConv * PL<128>::kTileB, "room");
-  for (long long p = 2; p * tail <= 2 * sms && p <= a.width / 8 && p <= room; ++p) {
-    const long long cost = (tail * p + sms - 1) / sms * ((a.width + p - 1) / p + kPartCost);
+  for (unsigned p = 2; p * tail <= 2 * sms && p <= static_cast<unsigned>(a.width) / kPartPages &&
+                       p <= room;
+       ++p) {
+    const unsigned cost = part_cost(a.width, p, static_cast<unsigned>(tail),
+                                    static_cast<unsigned>(sms));
     if (cost < best) best = cost, parts = p;
   }
   const long long grid = whole + tail * parts;
@@ -1036,6 +1057,7 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
                                           : kv8_prompt_kernel<64, false>);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, min_rows, static_cast<int>(row_blocks),
                                            static_cast<int>(whole), static_cast<int>(parts),
+                                           static_cast<int>(tail), static_cast<int>(sms),
                                            partials, tickets);
   if (e != cudaSuccess) return e;
   ++*launches;

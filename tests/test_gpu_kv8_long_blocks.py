@@ -124,3 +124,18 @@ def test_split_blocks_of_the_last_wave_in_parts(tl, heads, m, dim):
         assert torch.equal(a, c.run(tl, workspace=ws))
         assert tl.tern_last_launches() == 2
     assert not ws[:tl.SYNC_BYTES].any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,heads", [([600], [512], 48), ([2000], [512], 48),
+                                            ([300, 900], [60, 500], 16)])
+def test_a_wide_table_leaves_short_blocks_whole(tl, lens, new, heads, dim):
+    """A table of the longest context that a program allows gives what a tight
+    one does: blocks of few pages are not cut for its width."""
+    import torch
+    c = Case(lens, new, heads, 8, dim, seed=heads + dim)
+    tight = c.check(tl)
+    wide = np.full((len(lens), 512), -7, dtype=np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    assert torch.equal(c.check(tl), tight)
