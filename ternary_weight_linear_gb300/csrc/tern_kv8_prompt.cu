@@ -9,8 +9,8 @@
 //   P = 2^(s + log2 f - ref + 10),  O += P (2^(e - E) Vc),  l += P / f
 // with Q scaled by 2^a per row into fp16, Kc and Vc the int8 codes (exact in
 // fp16), v_scale = 2^e f and E the largest e so far.  (Where the blocks' e lie
-// more than 24 apart, which fp16 does not hold, P takes the whole v_scale and
-// each row has a reference of its own for it: wide_pages.)  P is rounded to fp16
+// more than 8 apart P takes the whole v_scale and each row has a reference of its
+// own for it: wide_pages.)  P is rounded to fp16
 // (relative 2^-11, the tensor instruction's operand; the row's sum takes it
 // unrounded).  ref is the row's running maximum, raised (and O rescaled) only
 // when a score passes it by 2^4: P stays below 2^15 (fp16 ends at 65504) and
@@ -49,9 +49,10 @@ constexpr int kPThreads = (kMmaW + 4) * 32;
 constexpr int kPRecs = 512;  // page records held at a time
 constexpr int kAhead = 4;    // pages requested into L2 ahead of their conversion (kSplit)
 constexpr float kPOff = 10.f, kPLazy = 4.f;
-// Value scales whose exponents lie up to this far apart share one: a code times
-// 2^-24 is exact in fp16.
-constexpr int kSpan = 24;
+// Value scales whose exponents lie up to this far apart share one.  (A code times
+// 2^-8 is exact in fp16; a weight below 2^-35 of the row's largest is lost, and
+// with it at most 2^-27 of the largest weight times value scale.)
+constexpr int kSpan = 8;
 // Pages of time in sequence on an SM when `items` blocks of `pages` pages are cut
 // into parts, each of which costs some pages for its start, its result and the
 // join.  Parts have kPartPages pages at least.

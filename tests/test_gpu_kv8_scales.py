@@ -138,6 +138,23 @@ def test_a_block_of_small_weights(tl, seqs, m, heads, up):
     c.check_all(tl, (0, seqs - 1))
 
 
+@pytest.mark.parametrize("up", [6, 12, 18, 24])
+@pytest.mark.parametrize("seqs,m,heads", FORMS)
+def test_a_block_whose_weights_fp16_cannot_hold(tl, seqs, m, heads, up):
+    """One token has nearly all the weight, those of a block 2^-35 to 2^-36 of
+    it: they are a part of the result where their values are 2^up times as
+    large."""
+    import torch
+    c = Batch(seqs, 40 * 64, m, heads, 8, 64, seed=up + 300)
+    first, page = c.own_page(5), c.own_page(17)
+    c.scales[page, 1] *= np.float32(2.0 ** up)
+    c.codes[:, 0] = -127
+    c.codes[first, 0, :, 9] = 100
+    c.codes[page, 0] = -50  # 150 codes below: 64 / 8 * 0.02 * 150 = 24 = 34.6 ln 2
+    c.q_dev = torch.full_like(c.q_dev, 1.0) + 0.05 * torch.rand_like(c.q_dev)
+    c.check_all(tl, (0, seqs - 1))
+
+
 @pytest.mark.parametrize("up", [4, 30, 100])
 @pytest.mark.parametrize("m,heads", [(3, 8), (30, 8), (70, 8)])
 def test_a_rise_beyond_the_first_records(tl, m, heads, up):
