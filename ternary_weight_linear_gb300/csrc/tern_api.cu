@@ -329,7 +329,6 @@ int kv8_args(const tern_kv8_cache* c, Kv8Args* a) {
   return TERN_OK;
 }
 
-
 // Strides of a [rows][heads][dim] operand: rows and heads start on 16 bytes
 // and a head's elements are consecutive.
 bool kv8_strides_ok(long long ld, long long hd, int dim) {
@@ -608,7 +607,7 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld, const void* r
   if (rc != TERN_OK) return rc;
   const NormArgs a = {x,   x_ld, x_type,  residual, residual_out, residual_type, weight, weight_type,
                       eps, q,    x_scale, y,        T,            K};
-  if (launch_add_rmsnorm_s8(a, d->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (launch_add_rmsnorm_s8(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return TERN_ECUDA;
   t_last_launches = 1;
   return TERN_OK;

@@ -185,7 +185,7 @@ struct NormArgs {
   uint16_t* y;     // may be null
   int T, K;
 };
-cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, cudaStream_t stream);
 
 // The int8 cache (see tern_kv8_cache) and one call's rows.
 struct Kv8Args {

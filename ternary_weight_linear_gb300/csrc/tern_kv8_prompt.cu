@@ -181,8 +181,6 @@ struct OutRows {
   }
 };
 
-// The last part to arrive adds them all in order (every thread of the CTA) and
-// stages the rows.
 // Named barriers (0 is the whole CTA's, 1 the softmax warps').
 enum : int { kUsed = 2, kReady, kWritten, kQueries };
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -192,9 +190,11 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The last part to arrive adds them all in order (every thread of the CTA) and
+// stages the rows.
 template <int D>
 __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, const float* first,
-                                        int parts, int rows, int r0, int row0, int hk) {
+                                           int parts, int rows, int r0, int row0, int hk) {
   using L = PL<D>;
   constexpr size_t kPart = 2 * kPRows * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1030,8 +1030,9 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
   // earliest rows, the last to start) are cut into parts so that they end
   // together: as many as cost the least pages of time in sequence on an SM (at
   // the table's width; the kernel leaves blocks of few pages whole).
-  // Measured, with the cut and without (2048 tokens of 6 heads over 8190, 384
-  // items on 152 SMs): 316 and 328 us; 4096 tokens over 16384: 1106 and 1227 us.
+  // Measured when it came, with the cut and without (2048 tokens of 6 heads over
+  // 8190, 384 items on 152 SMs): 316 and 328 us; 4096 tokens over 16384: 1106 and
+  // 1227 us.
   const long long items = row_blocks * a.hkv * a.seqs;
   const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   const long long tail = items % sms, whole = items - tail;

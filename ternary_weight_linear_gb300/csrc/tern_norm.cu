@@ -190,10 +190,9 @@ cudaError_t launch_one(const NormArgs& a, int threads, cudaStream_t stream) {
 }
 
 template <int XT, int RT>
-cudaError_t launch_types(const NormArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
   const int vecs = a.K / 8;
   auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
-  (void)num_sms;
   if (vecs <= 1024) return launch_one<XT, RT, 1>(a, threads(1), stream);
   if (vecs <= 2048) return launch_one<XT, RT, 2>(a, threads(2), stream);
   return launch_one<XT, RT, 4>(a, threads(4), stream);
@@ -201,10 +200,10 @@ cudaError_t launch_types(const NormArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, cudaStream_t stream) {
   const int rt = a.residual ? a.residual_type : kNoResidual;
 #define TERN_NORM_CASE(XT, RT) \
-  if (a.x_type == XT && rt == RT) return launch_types<XT, RT>(a, num_sms, stream);
+  if (a.x_type == XT && rt == RT) return launch_types<XT, RT>(a, stream);
   TERN_NORM_CASE(TERN_F32, TERN_BF16)
   TERN_NORM_CASE(TERN_F32, TERN_F32)
   TERN_NORM_CASE(TERN_F32, kNoResidual)
