@@ -323,6 +323,11 @@ typedef struct {
  *       IEEE division);
  *   where s > s_old, the older tokens' codes become rint(code * (s_old / s));
  *   new codes are clamp(rint(x / s), -127, 127), rint to nearest even.
+ * So a code is rounded once more at each growth: a token's error is at most half
+ * the sum of the scales that its block has had since it was written.  For 64
+ * normal tokens appended one by one (some 5 growths) the root mean square error
+ * of the first sixteen is 1.6 times that of the same tokens appended together,
+ * and 2.5 times where the magnitudes grow fourfold on the way (some 16).
  * Codes of the page's slots past the last token are left as they are; the
  * scale of a page without older tokens is overwritten whatever it held.  An
  * infinite or NaN input makes its block's scale NaN (the block's values then
@@ -350,9 +355,9 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
  * > 0, j > p - window or j < sinks:
  *   o[row][h] = sum_j softmax_j(softmax_scale q[row][h] . k_j) v_j,
  * k_j and v_j the cache's scale * code of key-value head h / (heads /
- * kv_heads).  Codes of tokens that a row does not see (stale slots, pages
- * outside the window) do not enter its result, whatever they and, where no
- * row of the call sees the page, their scales hold.
+ * kv_heads).  Codes and scales of blocks that a row does not see do not enter
+ * its result, whatever they hold, nor do the codes of tokens that it does not
+ * see in a block that it does.
  *   q       device [rows][heads][head_dim] of `type` (TERN_BF16 or TERN_F16);
  *           row r, head h start at element r * ld + h * hd, 16-byte aligned
  *   rows    rows of q; 0: nothing is done
@@ -362,16 +367,24 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
  *   heads   a multiple of kv_heads, at most 64 times as many
  *   max_new at least the most new tokens of a sequence, and at least 1 where
  *           there are rows; ceil(max_new * heads / kv_heads / 256) * kv_heads *
- *           seqs has to stay below 2^31 - 1000 (TERN_EINVAL)
+ *           seqs has to stay below 2^31 - 1000 (TERN_EINVAL).  It and
+ *           table_width, which the launch knows alone, choose the kernels: a
+ *           decode step whose max_new is the call's rows takes a launch more and
+ *           wider tiles than one with max_new 1
  *   window  0 (none) or the tokens that a row sees, itself included
  *   sinks   first tokens that stay visible outside the window (>= 0)
  *   softmax_scale > 0
  *   workspace as for tern_linear: zero its first TERN_SYNC_BYTES once.
  * Numbers: q is scaled by a power of two per row and held in fp16 (a bf16 or
- * fp16 element is exact down to 2^-31 of the row's largest), codes are exact in fp16,
- * products and sums are fp32; the weights exp(.) are rounded to fp16 for
- * their products with the values (relative 2^-11), their sum is fp32 and
- * unrounded.  Results are bit-for-bit reproducible. */
+ * fp16 element is exact down to 2^-31 of the row's largest), codes are exact in
+ * fp16, products and sums are fp32, some of them of code + 128 with the 128s
+ * taken off the sum: the roundings of a score follow 128 k_scale sum |q|, and
+ * those of an output 128 v_scale sum p, a few 2^-24 of them.  The weights are
+ * rounded to fp16 for their products with the values (relative 2^-11, down to
+ * 2^-24 of the row's largest weight, or weight times v_scale); their sum is fp32
+ * and unrounded.  Value scales may lie any number of powers of two apart, which
+ * costs time: more than 2^8 within a block of prompt rows, or out of 2^-38 to
+ * 2^38.  Results are bit-for-bit reproducible. */
 int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type,
                        long long ld, long long hd, int rows, int heads,
                        int max_new, int window, int sinks, float softmax_scale,

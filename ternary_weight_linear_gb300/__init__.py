@@ -346,8 +346,9 @@ def tern_add_rmsnorm_s8(x: torch.Tensor, weight: torch.Tensor,
     gives it) or bf16, its rows may be strided; residual bf16 or fp32; weight
     [K] bf16 or fp32.  `residual_out` (allocated when omitted) may be
     `residual` itself.  `y`, if given, is written with the bf16 norm output,
-    which the bf16-activation rungs take; with quantise=False it is all that
-    is written.  Returns (q, x_scale, r)."""
+    which the bf16-activation rungs take; with quantise=False there are no
+    codes beside it.  Returns (q, x_scale, r), None for what is not written
+    (r without a residual)."""
     T, K = x.shape
     px = _strided(x, "x", (torch.float32, torch.bfloat16), 2)
     ld = x.stride(0) if T > 1 else K
@@ -407,8 +408,9 @@ def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale
     row_start[b + 1]), its last tokens of seq_lens[b].  codes int8 [pages, 2,
     kv_heads, 64, head_dim] and scales fp32 [pages, 2, kv_heads] are updated;
     page_table int32 [seqs, width].  `max_new` bounds the new tokens of a
-    sequence (the rows of the call when omitted).  tern_device_status tells
-    of inconsistent index arrays, whose sequences or pages are skipped."""
+    sequence (the rows of the call when omitted: right, but with CTAs for as
+    many pages of every sequence).  tern_device_status tells of inconsistent
+    index arrays, whose sequences or pages are skipped."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
     pk = _strided(k, "k", _TYPES, 3)
     pv = _strided(v, "v", (k.dtype,), 3)
@@ -443,6 +445,11 @@ def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     `sinks`.  softmax_scale defaults to head_dim ** -0.5.  Returns `out`
     [rows, heads, head_dim] of q's type; `lse` fp32 [rows, heads], if given,
     is written with the logarithm of the softmax's sum.
+
+    Give `max_new`, the most new tokens of a sequence: without it the call's
+    rows are taken, and a decode step of several sequences runs the prompt
+    kernel for nothing and wider tiles.  page_table's width also chooses the
+    kernels of 17 to 24 rows a head: a tight one is best.
 
     `workspace` (uint8, tern_kv8_attention_workspace_bytes bytes) is allocated
     zeroed per call when omitted; one kept across calls starts with SYNC_BYTES
