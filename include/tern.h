@@ -373,7 +373,7 @@ size_t tern_kv8_attention_workspace_bytes(int seqs, int rows, int heads,
  *           wider tiles than one with max_new 1
  *   window  0 (none) or the tokens that a row sees, itself included
  *   sinks   first tokens that stay visible outside the window (>= 0)
- *   softmax_scale > 0
+ *   softmax_scale > 0, and times log2(e) a finite float
  *   workspace as for tern_linear: zero its first TERN_SYNC_BYTES once.
  * Numbers: q is scaled by a power of two per row and held in fp16 (a bf16 or
  * fp16 element is exact down to 2^-31 of the row's largest), codes are exact in

@@ -9,6 +9,7 @@
 // (section 2: every reachable branch reports itself), limited by a minimum T
 // and a line budget.  Names of the variables are this library's own.
 #include <limits.h>
+#include <math.h>
 
 #include <mutex>
 #include <stdio.h>
@@ -207,6 +208,8 @@ int make_map_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
 // Largest row or head stride in elements: products with 32-bit row numbers
 // and an element's size stay within 64 bits.
 constexpr long long kMaxStride = 1ll << 28;
+
+constexpr float kLog2E = 1.4426950408889634f;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -665,7 +668,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
       heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < (rows > 0) || window < 0 || sinks < 0 ||
       static_cast<long long>(rows) * (heads / a.hkv) > INT_MAX ||
-      !(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f) || !kv8_strides_ok(ld, hd, a.dim))
+      !(softmax_scale > 0.f) || !(softmax_scale * kLog2E < HUGE_VALF) || !kv8_strides_ok(ld, hd, a.dim))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
   if (!q || !out || !kv8_prompt_fits(max_new < rows ? max_new : rows, heads / a.hkv, a.hkv, a.seqs))
@@ -691,7 +694,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   const int most_tokens = a.width * TERN_KV8_BLOCK;
   a.window = window < most_tokens ? window : 0;
   a.sinks = a.window > 0 ? (sinks < most_tokens ? sinks : most_tokens) : 0;
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.scale_log2 = softmax_scale * kLog2E;
   a.out = out;
   a.lse = lse;
   a.tickets = static_cast<int*>(workspace);

@@ -32,8 +32,8 @@ def cache(pages=8, seqs=2, width=4, kv_heads=8, dim=64):
     return ctypes.byref(tl._KV8Cache(P, P, P, P, P, pages, seqs, width, kv_heads, dim))
 
 
-def attention(c, rows, max_new, heads=8, ws=1 << 40):
-    return tl.load().tern_kv8_attention(c, P, 1, heads * 64, 64, rows, heads, max_new, 0, 0, 0.125,
+def attention(c, rows, max_new, heads=8, ws=1 << 40, scale=0.125):
+    return tl.load().tern_kv8_attention(c, P, 1, heads * 64, 64, rows, heads, max_new, 0, 0, scale,
                                         P, None, P, ws, None)
 
 
@@ -61,3 +61,10 @@ def test_a_grid_of_too_many_blocks_is_refused_before_any_launch():
     many = cache(seqs=1 << 17)
     assert attention(many, 1 << 20, 1 << 20, ws=0) == EINVAL
     assert attention(many, 1 << 20, 1, ws=0) == -3  # (the next check is the workspace's)
+
+
+def test_a_scale_that_overflows_is_refused():
+    """In base 2 it is 1.44 times as large."""
+    for scale in (2.5e38, float("inf"), float("nan"), 0.0, -1.0):
+        assert attention(cache(), 1, 1, scale=scale, ws=0) == EINVAL
+    assert attention(cache(), 1, 1, scale=2.3e38, ws=0) == -3
