@@ -205,6 +205,12 @@ def _heads_strides(t: torch.Tensor):
     return t.stride(0) if rows > 1 else heads * dim, hd
 
 
+def _most(n) -> int:
+    """An upper bound as a C int, which holds every size that there can be
+    (ctypes would keep the low bits of a larger one)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 _CURRENT = contextlib.nullcontext()
 
 
@@ -420,7 +426,7 @@ def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale
     rows = k.shape[0]
     rc = load().tern_kv8_append(
         ctypes.byref(cache), pk, pv, _TYPES[k.dtype], *_heads_strides(k), rows,
-        max(1, rows) if max_new is None else int(max_new), _stream(stream))
+        max(1, rows) if max_new is None else _most(max_new), _stream(stream))
     _check("tern_kv8_append", rc)
 
 
@@ -471,7 +477,7 @@ def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
             workspace[:SYNC_BYTES].zero_()  # the rest is scratch
     rc = load().tern_kv8_attention(
         ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads,
-        max(1, rows) if max_new is None else int(max_new), int(window), int(sinks),
+        max(1, rows) if max_new is None else _most(max_new), _most(window), _most(sinks),
         1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
         _dev(out, "out", q.dtype, (rows, heads, dim)),
         _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,

@@ -55,3 +55,27 @@ def test_norm_weight_that_is_not_finite(tl, width, bad):
     assert not torch.isfinite(s).any()
     assert torch.isnan(s[1]) and torch.isnan(y[1, 8].float())
     assert torch.isfinite(y[:, 9:].float()).all()
+
+
+def test_bounds_past_32_bits_are_no_bounds(tl):
+    """A window, sinks or max_new of any size: not their low 32 bits."""
+    import torch
+    from test_gpu_kv8_attention import Case
+    c = Case([200, 130], [3, 70], 4, 2, 64, seed=7)
+    want = c.run(tl)
+    assert torch.equal(c.run(tl, window=2 ** 32 + 5), want)
+    some = c.run(tl, window=20, sinks=10 ** 6)
+    assert torch.equal(c.run(tl, window=20, sinks=2 ** 33 + 1), some)
+    assert torch.equal(some, want) and not torch.equal(c.run(tl, window=20), want)
+    assert torch.equal(c.run(tl, max_new=2 ** 32 + 70), c.run(tl, max_new=73))
+    for kw in (dict(window=-2 ** 40), dict(sinks=-2 ** 33), dict(max_new=-2 ** 32)):
+        with pytest.raises(tl.TernError):
+            c.run(tl, **kw)
+    kv = torch.randn(2, 2, 64, device="cuda")
+    codes = torch.zeros(2, 2, 2, 64, 64, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(2, 2, 2, device="cuda")
+    ix = (torch.tensor([[1]], dtype=torch.int32, device="cuda"),
+          torch.tensor([0, 2], dtype=torch.int32, device="cuda"),
+          torch.tensor([2], dtype=torch.int32, device="cuda"))
+    tl.tern_kv8_append(kv, kv, codes, scales, *ix, max_new=2 ** 32 + 1)
+    assert tl.tern_device_status() == 0 and scales[1].all()
