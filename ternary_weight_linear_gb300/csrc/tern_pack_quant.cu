@@ -347,17 +347,18 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t*
 // chunks, past T if T is not a multiple of four, so it reads the workspace's
 // padded copy and not the caller's array.  One thread per 16 codes: 16 bytes
 // in, 32 out, bound by HBM (or L2, where the codes have just been written).
+// (No __restrict__: the codes' writer may still run when this kernel begins, and
+// loads through such pointers may become ld.global.nc.)
 constexpr int kCodeThreads = 256;
 __global__ void __launch_bounds__(kCodeThreads) code_pieces_kernel(
-    const int8_t* __restrict__ q, const float* __restrict__ x_scale, uint8_t* __restrict__ p1,
-    uint8_t* __restrict__ p2, float* __restrict__ xs, int T, long long blocks) {
+    const int8_t* q, const float* x_scale, uint8_t* p1, uint8_t* p2, float* xs, int T, long long blocks) {
   grid_dependents_launch();
   grid_dependency_wait();  // the codes and the output buffers come from earlier work
   const long long first = static_cast<long long>(blockIdx.x) * kCodeThreads + threadIdx.x;
   const long long stride = static_cast<long long>(gridDim.x) * kCodeThreads;
-  for (long long t = first; t < T; t += stride) xs[t] = __uint_as_float(ldg_u32(x_scale + t));
+  for (long long t = first; t < T; t += stride) xs[t] = x_scale[t];
   for (long long i = first; i < blocks; i += stride) {
-    const uint4 v = ldg_v4(q + 16 * i);
+    const uint4 v = *reinterpret_cast<const uint4*>(q + 16 * i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float r[16];
 #pragma unroll
