@@ -278,9 +278,10 @@ __device__ __forceinline__ void half_values(const uint8_t* vb, int g, int t,
   }
 }
 
-// O^T += Vc^T P^T, the weights P in the scores' place.
+// O^T += Vc^T P^T, the weights P in the scores' place, times any (a pair of 1 or 0
+// in fp16).
 template <int D, int NT>
-__device__ __forceinline__ void half_products(const float (&sc)[NT][2][4],
+__device__ __forceinline__ void half_products(const float (&sc)[NT][2][4], uint32_t any,
                                               const uint32_t (&vw)[2][4][D / 32],
                                               float (&o)[NT][D / 16][4]) {
   constexpr bool kBiased = biased(NT);
@@ -290,8 +291,13 @@ __device__ __forceinline__ void half_products(const float (&sc)[NT][2][4],
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      pf[n][i].x = transposed(half2_bits(sc[n][i][0], sc[n][i][1]));
-      pf[n][i].y = transposed(half2_bits(sc[n][i][2], sc[n][i][3]));
+      auto mul = [&](uint32_t p) {
+        uint32_t r;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(any));
+        return r;
+      };
+      pf[n][i].x = transposed(mul(half2_bits(sc[n][i][0], sc[n][i][1])));
+      pf[n][i].y = transposed(mul(half2_bits(sc[n][i][2], sc[n][i][3])));
     }
   float oc[NT][4];
 #pragma unroll
@@ -803,7 +809,6 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               for (int y = x; y < 4; y += 2) {
                 sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
                 part += sc[n][i][y];
-                sc[n][i][y] *= rec.any;
               }
             // (scales that cannot be used: the rows that see the page, and only
             // they, become NaN)
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           }
         }
 
-        half_products<D, NT>(sc, vw, o);
+        half_products<D, NT>(sc, half2_bits(rec.any, rec.any), vw, o);
         __syncwarp();  // the stage has been read
         ++used;
         issue_ahead();

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const uint16_t*
 // loads through such pointers may become ld.global.nc.)
 constexpr int kCodeThreads = 256;
 __global__ void __launch_bounds__(kCodeThreads) code_pieces_kernel(
-    const int8_t* q, const float* x_scale, uint8_t* p1, uint8_t* p2, float* xs, int T, long long blocks) {
+    const int8_t* q, const float* x_scale, uint8_t* p1, uint8_t* p2, float* xs, int T,
+    long long blocks) {
   grid_dependents_launch();
   grid_dependency_wait();  // the codes and the output buffers come from earlier work
   const long long first = static_cast<long long>(blockIdx.x) * kCodeThreads + threadIdx.x;
