@@ -33,8 +33,10 @@
 // sum, O) go to the workspace, and the last CTA of a block adds them in order.
 //
 // Measured: 2048 tokens of 6 query heads per key-value head over 8190 cached,
-// head of 128: 291 us, 1240 TFLOP/s (0.65 of the bf16 GEMM rate); 4096 over
-// 16384: 1010 us, 1430 TFLOP/s (0.75).  Both score buffers in one product pair
+// head of 128: 292 us, 1233 TFLOP/s (0.65 of the bf16 GEMM rate; 484 us by
+// wide_pages); 4096 over 16384: 1017 us, 1420 TFLOP/s (0.75); 2048 over 8192 of 32
+// query and 8 key-value heads of 64: 172 us, 699 TFLOP/s (0.37: a page's
+// exponentials are as many for half the products).  Both score buffers in one product pair
 // that reads the queries from shared memory once lost a quarter: the softmax
 // then waits for each pair.
 #include "tern_kv8.cuh"

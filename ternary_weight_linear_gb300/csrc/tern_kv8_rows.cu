@@ -42,9 +42,10 @@
 //
 // Measured: 32 decode sequences of 544000 cached tokens, 8 key-value heads of
 // 128, 48 query heads: 181 us, 6.15 TB/s (0.90 of the copy rate; the loads
-// alone take 167).  One token over 32000: 21.7 us; over 777: 9.3 us, of which
+// alone take 167).  One token over 32000: 21.7 us; over 777: 9.5 us, of which
 // the launch, four dependent reads of indexes, pages and scales, the merge and
-// the join are all but one.
+// the join are all but one.  (A block of the 32 sequences each left to far_row:
+// 528 us.)
 #include "tern_kv8.cuh"
 
 namespace tern {
