@@ -682,8 +682,9 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hh;
             const float ks = sc[0];
             const float vs = sc[a.hkv];
-            // (a value scale of 0 weighs as one of 1; scales that cannot be used keep
-            // out of the arithmetic)
+            // (a value scale of 0 weighs as the least, so that its block hardly
+            // raises a row's reference; scales that cannot be used keep out of the
+            // arithmetic)
             const bool good = good_scales(ks, vs);
             const bool far = far_scales(ks, vs);
             rec.ks = good ? ks : 0.f;
@@ -691,10 +692,11 @@ __global__ void __launch_bounds__(kRW * 32, 1)
               rec.rv = __uint_as_float(0x7FC00000u);
             } else if (far) {
               s_far = 1;
-            } else if (vs != 0.f) {
-              rec.lv = log2f(vs);
-              rec.rv = 1.0f / vs;
-              rec.any = 1.f;
+            } else {
+              const float v = fmaxf(vs, kMinScale);
+              rec.lv = log2f(v);
+              rec.rv = 1.0f / v;
+              rec.any = vs != 0.f ? 1.f : 0.f;
             }
             row = (page * 2 * a.hkv + hh) * kBlk;
 #pragma unroll

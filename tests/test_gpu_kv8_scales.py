@@ -166,7 +166,7 @@ def test_a_rise_beyond_the_first_records(tl, m, heads, up):
     c.check_all(tl, (0, 9, 19))
 
 
-@pytest.mark.parametrize("scale", [0.02, 2.0 ** -60, 2.0 ** 60])
+@pytest.mark.parametrize("scale", [0.02, 2.0 ** -20, 2.0 ** -37, 2.0 ** -60, 2.0 ** 30, 2.0 ** 60])
 @pytest.mark.parametrize("seqs,m,heads", FORMS)
 def test_blocks_of_zero_scale(tl, seqs, m, heads, scale):
     """A value scale of 0 makes its block's values 0 whatever its codes are."""
