@@ -106,7 +106,8 @@ struct __align__(16) PageRec {
   float any;     // 1, or 0 where the values have no part in the output
 };
 // Beside it, the first row of the page's keys in the codes' tensor map (a
-// multiple of 64) with these bits, or -1 for a page out of range.
+// multiple of 64) with these bits (no kMHalf where it is left to far_row), or -1
+// for a page out of range.
 enum : int {
   kMHalf = 1,  // << half: some row sees a token of the half
   kMAll = 4    // << half: every row sees all of them
@@ -961,6 +962,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
             a.lse[ob] = kv_log_sum(base, l, kROff);
         }
       }
+      __syncthreads();  // the queries have been read
     }
     if (!whole) {
       // the last of the segment's CTAs adds the parts in their order, a row per

@@ -197,3 +197,19 @@ def test_a_negative_scale_reads_as_nan(tl, seqs, m, heads, which):
     assert torch.equal(got[:, ~sees], clean[:, ~sees])
     rest = [h for h in range(8) if h != 1]
     assert torch.equal(got[:, :, rest], clean[:, :, rest])
+
+
+@pytest.mark.parametrize("m,heads", [(1, 8), (2, 64)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_short_sequences_with_far_blocks(tl, m, heads, dim):
+    """Several whole segments a CTA, one after the other, each with a block that
+    is left to the plain path: the oracle's result, and the same bits each time."""
+    import torch
+    c = Batch(100, 4 * 64 + 9, m, heads, 8, dim, seed=m)
+    for at, up in ((1, 90), (3, -80)):
+        page = c.own_page(at)
+        c.scales[page, 1] *= np.float32(2.0 ** up)
+    c.check_all(tl, (0, 50, 99))
+    first = c.run(tl)
+    for _ in range(5):
+        assert torch.equal(c.run(tl), first)
