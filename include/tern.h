@@ -44,9 +44,11 @@
  *
  * Beside the layer, the operators that stand between two such layers of a
  * decoder: tern_add_rmsnorm_s8 (residual, norm and int8 codes),
- * tern_linear_s8 (the layer on such codes), tern_kv8_append and
- * tern_kv8_attention (a paged int8 cache of keys and values and the attention
- * that reads it).
+ * tern_norm_add_norm_s8 (a norm before that, with gate and residual scale),
+ * tern_linear_s8 (the layer on such codes), tern_rope (rotary positions),
+ * tern_kv8_append, tern_kv8_append_rope, tern_kv8_attention and
+ * tern_kv8_attention_shared (a paged int8 cache of keys and values and the
+ * attention that reads it, also behind pages that the whole batch shares).
  */
 #ifndef TERN_H_
 #define TERN_H_
@@ -279,6 +281,93 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld,
                         float eps, int8_t* q, float* x_scale, uint16_t* y,
                         int T, int K, void* stream);
 
+/* The norm after a block, its gate, the residual's addition, and the norm
+ * before the next block with its int8 codes, of token rows:
+ *   n = x * post_weight / sqrt(mean_k(x^2) + eps)        (n = x without one)
+ *   r = residual_scale * residual + branch_scale * gate * n, rounded once to
+ *       the residual's type (gate 1 without one)
+ *   y = r * weight / sqrt(mean_k(r^2) + eps)             (fp32)
+ *   x_scale, q and y as for tern_add_rmsnorm_s8.
+ *   x        device [T][K] of x_type (TERN_F32 or TERN_BF16); row t starts at
+ *            element t * x_ld (x_ld >= K, rows 16-byte aligned)
+ *   post_weight  device [K] of post_type (TERN_F32 or TERN_BF16), or NULL
+ *   gate     device [T][K] of gate_type (TERN_F32 or TERN_BF16), row t at
+ *            element t * gate_ld (gate_ld >= K, 16-byte aligned, or 0: one row
+ *            for all tokens), or NULL
+ *   branch_scale, residual_scale finite
+ *   residual device [T][K] of residual_type (TERN_F32 or TERN_BF16)
+ *   residual_out device [T][K] of residual_type, written with r; may be
+ *            residual itself, may be NULL
+ *   weight   device [K] of weight_type (TERN_F32 or TERN_BF16)
+ *   q, x_scale, y, T, K, eps as for tern_add_rmsnorm_s8.
+ * The statistics and r before its rounding are fp32. */
+int tern_norm_add_norm_s8(const void* x, int x_type, long long x_ld,
+                          const void* post_weight, int post_type,
+                          const void* gate, int gate_type, long long gate_ld,
+                          float branch_scale, const void* residual,
+                          void* residual_out, int residual_type,
+                          float residual_scale, const void* weight,
+                          int weight_type, float eps, int8_t* q, float* x_scale,
+                          uint16_t* y, int T, int K, void* stream);
+
+/* ---------------------------------------------------------------- rotation
+ * Rotary positions.  The first rotary_dim elements of a head are rotary_dim / 2
+ * pairs; pair i of a token at position p is turned by p * theta_i:
+ *   u' = m (u cos - v sin),  v' = m (u sin + v cos).
+ * interleaved 0: elements i and i + rotary_dim / 2 are pair i; otherwise
+ * elements 2 i and 2 i + 1.  The head's other elements stay as they are. */
+typedef struct {
+  const uint64_t* freq; /* device [rotary_dim / 2]: theta_i / (2 pi) in units of
+                           2^-64, turns a token (tern_rope_frequencies) */
+  int rotary_dim;       /* a multiple of 16, at most the head's dim */
+  int interleaved;
+  float magnitude;      /* m, finite */
+} tern_rotation;
+
+/* How the frequencies theta_i = base^(-2 i / rotary_dim) follow a context
+ * `factor` times longer than the trained one.  Pair i turns n_i = trained
+ * theta_i / (2 pi) times in the latter. */
+typedef enum {
+  TERN_ROPE_NONE = 0,
+  TERN_ROPE_LINEAR = 1, /* theta_i / factor */
+  TERN_ROPE_BASE = 2,   /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+  TERN_ROPE_BANDS = 3,  /* theta_i (s + (1 - s) / factor), s = (n_i - low) /
+                           (high - low) held in [0, 1] */
+  TERN_ROPE_RAMP = 4    /* the same with s falling from 1 to 0 in i, between the
+                           floor of the i that turns `high` times and the ceiling
+                           of the one that turns `low` times (held in [0,
+                           rotary_dim - 1]); magnitude 0.1 ln(factor) + 1 */
+} tern_rope_scaling;
+
+/* The table of a rotation, on the host.
+ *   rotary_dim a multiple of 16, 16..1024;  base > 1
+ *   scaling  a tern_rope_scaling;  factor >= 1 (not read for TERN_ROPE_NONE)
+ *   trained > 0 and 0 < low < high: read for TERN_ROPE_BANDS and _RAMP
+ *   freq     host [rotary_dim / 2], written (the caller copies it to the device)
+ *   magnitude host, written: 1, or that of TERN_ROPE_RAMP
+ * Computed in double precision.  Host-only. */
+int tern_rope_frequencies(int rotary_dim, double base, int scaling,
+                          double factor, double trained, double low,
+                          double high, uint64_t* freq, float* magnitude);
+
+/* Turn the rows of x:
+ *   x        device [T][heads][dim] of `type` (TERN_F32, TERN_BF16 or
+ *            TERN_F16); row t, head h start at element t * ld + h * hd,
+ *            16-byte aligned
+ *   out      the same of out_type at t * out_ld + h * out_hd, written; x itself
+ *            (same type and strides), or memory apart from it
+ *   positions device int32 [T]; a negative one turns backwards, so the call
+ *            with all of them negated is the inverse (for magnitude 1) and the
+ *            transpose, which is its gradient
+ *   T, heads >= 1; dim a multiple of 16, at most 1024.
+ * The angle is exact modulo a turn for every position; its sine and cosine and
+ * the products are fp32 (an element is off by less than 2^-21 m (|u| + |v|)),
+ * rounded once to out_type. */
+int tern_rope(const void* x, int type, long long ld, long long hd, void* out,
+              int out_type, long long out_ld, long long out_hd,
+              const int32_t* positions, const tern_rotation* rotation, int T,
+              int heads, int dim, void* stream);
+
 /* ---------------------------------------------------------------- int8 cache
  * A paged cache of keys and values in int8.  A page holds TERN_KV8_BLOCK
  * tokens of one sequence, keys and values of every head, and is the block
@@ -342,6 +431,27 @@ typedef struct {
 int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v,
                     int type, long long ld, long long hd, int rows,
                     int max_new, void* stream);
+
+/* tern_kv8_append with the keys turned on the way (the values are not), and the
+ * same rows' queries turned into q_out, in one launch:
+ *   q        device [rows][heads][head_dim] of `type`; row r, head h start at
+ *            element r * q_ld + h * q_hd, 16-byte aligned; NULL: no queries
+ *   heads    at most 64 * kv_heads (not read without queries)
+ *   positions device int32 [rows]: the rows' positions, or NULL: those of the
+ *            tokens in the cache
+ *   rotation as for tern_rope, rotary_dim at most head_dim
+ *   q_out    device [rows][heads][head_dim] of q_type (TERN_BF16 or TERN_F16),
+ *            dense, written, apart from q; rows of no sequence and of skipped
+ *            ones are left as they are (a page that is skipped does not keep its
+ *            rows' queries)
+ *   the others as for tern_kv8_append.
+ * Keys are turned in fp32 and rounded once, to their codes. */
+int tern_kv8_append_rope(const tern_kv8_cache* cache, const void* q,
+                         const void* k, const void* v, int type, long long q_ld,
+                         long long q_hd, int heads, long long ld, long long hd,
+                         const int32_t* positions,
+                         const tern_rotation* rotation, void* q_out, int q_type,
+                         int rows, int max_new, void* stream);
 
 /* Bytes of device workspace tern_kv8_attention needs for `rows` query rows of
  * `seqs` sequences (the synchronisation area, then partial results of
@@ -459,8 +569,9 @@ const char* tern_last_rung(void);
 
 /* Number of kernels this thread's last successful tern_linear,
  * tern_linear_s8, tern_linear_small_t_noalloc, tern_add_rmsnorm_s8,
- * tern_kv8_append or tern_kv8_attention launched: per token tile of the bandwidth
- * rungs one main kernel, plus the activation-prep kernel where the tile
+ * tern_norm_add_norm_s8, tern_rope, tern_kv8_append, tern_kv8_append_rope,
+ * tern_kv8_attention or tern_kv8_attention_shared launched: per token tile of the
+ * bandwidth rungs one main kernel, plus the activation-prep kernel where the tile
  * uses one; 2 on the s8 rung (activation pieces, then the GEMM).  0 before
  * any call.  Host-only; for benchmarks and tests. */
 int tern_last_launches(void);

@@ -28,6 +28,8 @@ __all__ = [
     "tern_linear_small_t_noalloc", "tern_repack_t5", "tern_rotate_bf16",
     "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append", "tern_kv8_attention",
     "tern_kv8_attention_workspace_bytes", "KV8_BLOCK",
+    "tern_norm_add_norm_s8", "tern_rope_frequencies", "tern_rope", "tern_kv8_append_rope",
+    "ROPE_SCALINGS",
     "tern_selftest_wait_timeout", "RUNGS",
     "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES", "SYNC_BYTES", "T5_GROUP_BYTES", "ROTATION_BLOCK",
 ]
@@ -41,7 +43,8 @@ EXPORTED_SYMBOLS = (
     "tern_last_launches", "tern_status_string", "tern_reload_env", "tern_device_status",
     "tern_linear_small_t_noalloc", "tern_repack_t5", "tern_rotate_bf16",
     "tern_selftest_wait_timeout", "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append",
-    "tern_kv8_attention", "tern_kv8_attention_workspace_bytes",
+    "tern_kv8_attention", "tern_kv8_attention_workspace_bytes", "tern_norm_add_norm_s8",
+    "tern_rope_frequencies", "tern_rope", "tern_kv8_append_rope",
 )
 
 # Size of the library's fixed scratch for tern_linear_small_t_noalloc.
@@ -55,6 +58,8 @@ T5_GROUP_BYTES = 26
 ROTATION_BLOCK = 1024
 # Tokens of a page of the int8 cache, which is the block that shares a scale.
 KV8_BLOCK = 64
+# tern_rope_scaling
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 # tern_type
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -66,6 +71,12 @@ class _KV8Cache(ctypes.Structure):
                 ("codes", "scales", "page_table", "seq_lens", "row_start")] + [
                     (n, ctypes.c_int) for n in
                     ("pages", "seqs", "table_width", "kv_heads", "head_dim")]
+
+
+class _Rotation(ctypes.Structure):
+    """tern_rotation."""
+    _fields_ = [("freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -134,6 +145,16 @@ def load() -> ctypes.CDLL:
         lib.tern_kv8_attention_workspace_bytes.restype = Z
         lib.tern_kv8_attention.argtypes = [C, P, I, L, L, I, I, I, I, I, F, P, P, P, Z, P]
         lib.tern_kv8_attention.restype = I
+        R, Dbl = ctypes.POINTER(_Rotation), ctypes.c_double
+        lib.tern_norm_add_norm_s8.argtypes = [P, I, L, P, I, P, I, L, F, P, P, I, F, P, I, F, P, P,
+                                              P, I, I, P]
+        lib.tern_norm_add_norm_s8.restype = I
+        lib.tern_rope_frequencies.argtypes = [I, Dbl, I, Dbl, Dbl, Dbl, Dbl, P, P]
+        lib.tern_rope_frequencies.restype = I
+        lib.tern_rope.argtypes = [P, I, L, L, P, I, L, L, P, R, I, I, I, P]
+        lib.tern_rope.restype = I
+        lib.tern_kv8_append_rope.argtypes = [C, P, P, P, I, L, L, I, L, L, P, R, P, I, I, I, P]
+        lib.tern_kv8_append_rope.restype = I
         lib.tern_selftest_wait_timeout.argtypes = [I, P]
         lib.tern_selftest_wait_timeout.restype = I
         _lib = lib
@@ -389,6 +410,122 @@ def tern_add_rmsnorm_s8(x: torch.Tensor, weight: torch.Tensor,
     return q, x_scale, residual_out
 
 
+def tern_norm_add_norm_s8(x: torch.Tensor, post_weight: torch.Tensor | None,
+                          residual: torch.Tensor, weight: torch.Tensor,
+                          gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                          branch_scale: float = 1.0, eps: float = 1e-6, *,
+                          residual_out: torch.Tensor | None = None,
+                          q: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
+                          y: torch.Tensor | None = None, quantise: bool = True, stream=None):
+    """The norm after a block, its gate, the residual's addition, and the norm
+    before the next block with its int8 codes.
+
+    n = x * post_weight / sqrt(mean(x^2) + eps) (n = x where post_weight is
+    None); r = residual_scale * residual + branch_scale * gate * n, rounded to
+    the residual's type; y, x_scale and q of r and `weight` as in
+    tern_add_rmsnorm_s8.  x [T, K] fp32 or bf16, its rows may be strided; gate
+    [K] (the same for every token) or [T, K] (rows may be strided or expanded);
+    residual [T, K]; all of fp32 or bf16.  `residual_out` (allocated when
+    omitted) may be `residual` itself.  `y`, `quantise` as there.  Returns (q,
+    x_scale, r), None for codes that are not written."""
+    T, K = x.shape
+    floats = (torch.float32, torch.bfloat16)
+    px = _strided(x, "x", floats, 2)
+    ld = x.stride(0) if T > 1 else K
+    for t, name in ((residual, "residual"), (weight, "weight"), (post_weight, "post_weight")):
+        if t is not None and t.dtype not in floats:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    pg, gt, gld = None, 0, 0
+    if gate is not None:
+        pg = _strided(gate, "gate", floats, gate.dim())
+        if tuple(gate.shape) not in ((K,), (T, K)):
+            raise ValueError(f"gate must have shape ({K},) or ({T}, {K}), got {tuple(gate.shape)}")
+        gt = _TYPES[gate.dtype]
+        gld = gate.stride(0) if gate.dim() == 2 and T > 1 else 0
+    with _allocating(stream):
+        if quantise:
+            if q is None:
+                q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+            if x_scale is None:
+                x_scale = torch.empty((T,), dtype=torch.float32, device=x.device)
+        elif q is not None or x_scale is not None or y is None:
+            raise ValueError("quantise=False writes y alone")
+        if residual_out is None:
+            residual_out = torch.empty((T, K), dtype=residual.dtype, device=x.device)
+    rc = load().tern_norm_add_norm_s8(
+        px, _TYPES[x.dtype], ld,
+        _dev(post_weight, "post_weight", post_weight.dtype, (K,)) if post_weight is not None
+        else None, _TYPES[post_weight.dtype] if post_weight is not None else 0,
+        pg, gt, gld, branch_scale, _dev(residual, "residual", residual.dtype, (T, K)),
+        _dev(residual_out, "residual_out", residual.dtype, (T, K)), _TYPES[residual.dtype],
+        residual_scale, _dev(weight, "weight", weight.dtype, (K,)), _TYPES[weight.dtype], eps,
+        _dev(q, "q", torch.int8, (T, K)) if quantise else None,
+        _dev(x_scale, "x_scale", torch.float32, (T,)) if quantise else None,
+        _dev(y, "y", torch.bfloat16, (T, K)) if y is not None else None, T, K, _stream(stream))
+    _check("tern_norm_add_norm_s8", rc)
+    return q, x_scale, residual_out
+
+
+def tern_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                          factor: float = 1.0, trained: float = 0.0, low: float = 1.0,
+                          high: float | None = None, device="cuda"):
+    """The table of a rotation and its magnitude: (freq, magnitude).
+
+    freq int64 [rotary_dim / 2] on `device`: turns a token in units of 2^-64 of
+    theta_i = base^(-2 i / rotary_dim), scaled for a context `factor` times the
+    `trained` one: "linear" (theta / factor), "base" (a larger base), "bands"
+    (pairs that turn `high` = 4 times and more in the trained context stay,
+    those that turn `low` = 1 times and less are slowed, linear in their turns
+    between) or "ramp" (the same between `high` = 32 and `low` = 1 turns, linear
+    in the pair's number, with a magnitude of 0.1 ln(factor) + 1)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}, got {scaling!r}")
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
+    rotary_dim = int(rotary_dim)
+    freq = torch.zeros(max(1, rotary_dim // 2), dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    _check("tern_rope_frequencies", load().tern_rope_frequencies(
+        rotary_dim, base, ROPE_SCALINGS[scaling], factor, trained, low, high, freq.data_ptr(),
+        ctypes.addressof(magnitude)))
+    return freq.to(device), magnitude.value
+
+
+def _rotation(freq, interleaved, magnitude) -> _Rotation:
+    p = _dev(freq, "freq", torch.int64, (freq.numel(),))
+    return _Rotation(p, 2 * freq.numel(), int(bool(interleaved)), float(magnitude))
+
+
+def tern_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *,
+              interleaved: bool = False, magnitude: float = 1.0,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of rows x [T, heads, dim] (fp32, bf16 or fp16; rows and
+    heads may be strided) at int32 positions [T].
+
+    The first 2 * len(freq) elements of a head are pairs: the two halves, or
+    neighbours where `interleaved`; freq and magnitude are those of
+    tern_rope_frequencies.  `out` may be x itself, or of another of the three
+    types; it is allocated like a dense x when omitted.  Negated positions turn
+    backwards, which is also the gradient."""
+    px = _strided(x, "x", _TYPES, 3)
+    T, heads, dim = x.shape
+    if out is None:
+        with _allocating(stream):
+            out = torch.empty((T, heads, dim), dtype=x.dtype, device=x.device)
+    po = _strided(out, "out", _TYPES, 3)
+    if out.shape != x.shape:
+        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    if T == 0 or heads == 0:
+        return out
+    rot = _rotation(freq, interleaved, magnitude)
+    rc = load().tern_rope(
+        px, _TYPES[x.dtype], *_heads_strides(x), po, _TYPES[out.dtype], *_heads_strides(out),
+        _dev(positions, "positions", torch.int32, (T,)), ctypes.byref(rot), T, heads, dim,
+        _stream(stream))
+    _check("tern_rope", rc)
+    return out
+
+
 def _kv8_cache(codes, scales, page_table, row_start, seq_lens) -> _KV8Cache:
     if codes.dim() != 5 or codes.shape[1] != 2 or codes.shape[3] != KV8_BLOCK:
         raise ValueError(f"codes must be [pages, 2, kv_heads, {KV8_BLOCK}, head_dim], "
@@ -428,6 +565,51 @@ def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale
         ctypes.byref(cache), pk, pv, _TYPES[k.dtype], *_heads_strides(k), rows,
         max(1, rows) if max_new is None else _most(max_new), _stream(stream))
     _check("tern_kv8_append", rc)
+
+
+def tern_kv8_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                         codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
+                         row_start: torch.Tensor, seq_lens: torch.Tensor, freq: torch.Tensor, *,
+                         interleaved: bool = False, magnitude: float = 1.0,
+                         positions: torch.Tensor | None = None, max_new: int | None = None,
+                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """tern_kv8_append with the keys turned on the way, and the same rows'
+    queries turned into q_out, in one launch.
+
+    q [rows, heads, head_dim] of k's type (rows and heads may be strided), or
+    None; q_out bf16 (allocated when omitted) or fp16 [rows, heads, head_dim].
+    The rotation as in tern_rope, at the tokens' positions in the cache or at
+    int32 `positions` [rows].  Returns q_out."""
+    cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
+    pk = _strided(k, "k", _TYPES, 3)
+    pv = _strided(v, "v", (k.dtype,), 3)
+    if (k.shape != v.shape or _heads_strides(k) != _heads_strides(v)
+            or k.shape[1:] != (codes.shape[2], codes.shape[4])):
+        raise ValueError("k and v must be [rows, kv_heads, head_dim] with the same strides")
+    rows, _, dim = k.shape
+    pq = po = None
+    qs, heads, qt = (0, 0), 0, 0
+    if q is not None:
+        pq = _strided(q, "q", (k.dtype,), 3)
+        heads = q.shape[1]
+        if q.shape != (rows, heads, dim):
+            raise ValueError(f"q must be [{rows}, heads, {dim}], got {tuple(q.shape)}")
+        if q_out is None:
+            with _allocating(stream):
+                q_out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=q.device)
+        if q_out.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"q_out must be bfloat16 or float16, got {q_out.dtype}")
+        po, qt, qs = _dev(q_out, "q_out", q_out.dtype, q.shape), _TYPES[q_out.dtype], _heads_strides(q)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = _rotation(freq, interleaved, magnitude)
+    rc = load().tern_kv8_append_rope(
+        ctypes.byref(cache), pq, pk, pv, _TYPES[k.dtype], *qs, heads, *_heads_strides(k),
+        _dev(positions, "positions", torch.int32, (rows,)) if positions is not None else None,
+        ctypes.byref(rot), po, qt, rows, max(1, rows) if max_new is None else _most(max_new),
+        _stream(stream))
+    _check("tern_kv8_append_rope", rc)
+    return q_out
 
 
 def tern_kv8_attention_workspace_bytes(seqs: int, rows: int, heads: int, kv_heads: int,

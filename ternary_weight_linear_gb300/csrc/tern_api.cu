@@ -338,6 +338,16 @@ bool kv8_strides_ok(long long ld, long long hd, int dim) {
   return ld >= dim && hd >= dim && ld <= kMaxStride && hd <= kMaxStride;
 }
 
+// A rotation's arguments for heads of `dim` elements.
+int rope_args(const tern_rotation* r, int dim, RopeArgs* a) {
+  if (!r || !r->freq || r->rotary_dim < 16 || r->rotary_dim % 16 != 0 || r->rotary_dim > dim ||
+      !isfinite(r->magnitude))
+    return TERN_EINVAL;
+  if (!aligned16(r->freq)) return TERN_EALIGN;
+  *a = {r->freq, r->rotary_dim, r->interleaved != 0, r->magnitude};
+  return TERN_OK;
+}
+
 // Scratch of tern_linear_small_t_noalloc for T tokens and K, for any (N,
 // device): at T = 1 the call may run on the one-token or the four-token tile.
 size_t noalloc_need(int T, int K) {
@@ -616,6 +626,96 @@ int tern_add_rmsnorm_s8(const void* x, int x_type, long long x_ld, const void* r
   return TERN_OK;
 }
 
+int tern_norm_add_norm_s8(const void* x, int x_type, long long x_ld, const void* post_weight,
+                          int post_type, const void* gate, int gate_type, long long gate_ld,
+                          float branch_scale, const void* residual, void* residual_out,
+                          int residual_type, float residual_scale, const void* weight,
+                          int weight_type, float eps, int8_t* q, float* x_scale, uint16_t* y, int T,
+                          int K, void* stream) {
+  auto f32_or_bf16 = [](int t) { return t == TERN_F32 || t == TERN_BF16; };
+  if (!x || !residual || !weight || T < 1 || K <= 0 || (K % 16) != 0 || K > kNormMaxK || x_ld < K ||
+      x_ld > kMaxStride || !f32_or_bf16(x_type) || !f32_or_bf16(residual_type) ||
+      !f32_or_bf16(weight_type) || (post_weight && !f32_or_bf16(post_type)) ||
+      (gate && (!f32_or_bf16(gate_type) || (gate_ld != 0 && gate_ld < K) || gate_ld > kMaxStride)) ||
+      !(eps >= 0.f) || !isfinite(branch_scale) || !isfinite(residual_scale) || (!q && !y) ||
+      (q != nullptr) != (x_scale != nullptr))
+    return TERN_EINVAL;
+  if (!aligned16(x) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(residual) ||
+      !aligned16(residual_out) || !aligned16(weight) || !aligned16(q) || !aligned16(x_scale) ||
+      !aligned16(y) || (x_ld * (x_type == TERN_F32 ? 4 : 2)) % 16 != 0 ||
+      (gate && (gate_ld * (gate_type == TERN_F32 ? 4 : 2)) % 16 != 0))
+    return TERN_EALIGN;
+  DevState* d = nullptr;
+  int rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  NormPairArgs a = {};
+  a.x = x;
+  a.x_ld = x_ld;
+  a.x_type = x_type;
+  a.post = post_weight;
+  a.post_type = post_type;
+  a.gate = gate;
+  a.gate_type = gate_type;
+  a.gate_ld = gate_ld;
+  a.branch_scale = branch_scale;
+  a.residual = residual;
+  a.residual_out = residual_out;
+  a.residual_type = residual_type;
+  a.residual_scale = residual_scale;
+  a.weight = weight;
+  a.weight_type = weight_type;
+  a.eps = eps;
+  a.q = q;
+  a.x_scale = x_scale;
+  a.y = y;
+  a.T = T;
+  a.K = K;
+  if (launch_norm_add_norm_s8(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return TERN_ECUDA;
+  t_last_launches = 1;
+  return TERN_OK;
+}
+
+int tern_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double trained,
+                          double low, double high, uint64_t* freq, float* magnitude) {
+  if (!freq || !magnitude || rotary_dim < 16 || rotary_dim % 16 != 0 ||
+      rotary_dim > kRopeMaxDim || !(base > 1.0) || !isfinite(base) || scaling < TERN_ROPE_NONE ||
+      scaling > TERN_ROPE_RAMP)
+    return TERN_EINVAL;
+  if (scaling != TERN_ROPE_NONE && (!(factor >= 1.0) || !isfinite(factor))) return TERN_EINVAL;
+  if ((scaling == TERN_ROPE_BANDS || scaling == TERN_ROPE_RAMP) &&
+      (!(trained > 0.0) || !isfinite(trained) || !(low > 0.0) || !(high > low) || !isfinite(high)))
+    return TERN_EINVAL;
+  if (scaling == TERN_ROPE_NONE) factor = 1.0;
+  return rope_frequencies(rotary_dim, base, scaling, factor, trained, low, high, freq, magnitude)
+             ? TERN_OK
+             : TERN_EINVAL;
+}
+
+int tern_rope(const void* x, int type, long long ld, long long hd, void* out, int out_type,
+              long long out_ld, long long out_hd, const int32_t* positions,
+              const tern_rotation* rotation, int T, int heads, int dim, void* stream) {
+  RopeArgs r;
+  int rc = rope_args(rotation, dim, &r);
+  if (rc != TERN_OK) return rc;
+  if (!x || !out || !positions || T < 1 || heads < 1 || dim % 16 != 0 || dim > kRopeMaxDim ||
+      type < TERN_F32 || type > TERN_F16 || out_type < TERN_F32 || out_type > TERN_F16 ||
+      !kv8_strides_ok(ld, hd, dim) || !kv8_strides_ok(out_ld, out_hd, dim))
+    return TERN_EINVAL;
+  const int size = type == TERN_F32 ? 4 : 2, out_size = out_type == TERN_F32 ? 4 : 2;
+  if (!aligned16(x) || !aligned16(out) || !aligned16(positions) || ld * size % 16 != 0 ||
+      hd * size % 16 != 0 || out_ld * out_size % 16 != 0 || out_hd * out_size % 16 != 0)
+    return TERN_EALIGN;
+  DevState* d = nullptr;
+  rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  const RopeRows a = {r,  x,      out,    type,      out_type, ld,  hd,
+                      out_ld, out_hd, positions, T,        heads, dim};
+  if (launch_rope(a, d->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TERN_ECUDA;
+  t_last_launches = 1;
+  return TERN_OK;
+}
+
 int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v, int type,
                     long long ld, long long hd, int rows, int max_new, void* stream) {
   Kv8Args a;
@@ -642,6 +742,54 @@ int tern_kv8_append(const tern_kv8_cache* cache, const void* k, const void* v, i
   a.err = d->err;
   int launches = 0;
   if (launch_kv8_append(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
+    return TERN_ECUDA;
+  t_last_launches = launches;
+  return TERN_OK;
+}
+
+int tern_kv8_append_rope(const tern_kv8_cache* cache, const void* q, const void* k, const void* v,
+                         int type, long long q_ld, long long q_hd, int heads, long long ld,
+                         long long hd, const int32_t* positions, const tern_rotation* rotation,
+                         void* q_out, int q_type, int rows, int max_new, void* stream) {
+  Kv8Args a;
+  int rc = kv8_args(cache, &a);
+  if (rc != TERN_OK) return rc;
+  Kv8Turn t = {};
+  rc = rope_args(rotation, a.dim, &t.rope);
+  if (rc != TERN_OK) return rc;
+  if (type < TERN_F32 || type > TERN_F16 || rows < 0 || max_new < (rows > 0) ||
+      !kv8_strides_ok(ld, hd, a.dim) || (q != nullptr) != (q_out != nullptr))
+    return TERN_EINVAL;
+  if (q && (heads < 1 || heads > 64 * a.hkv || (q_type != TERN_BF16 && q_type != TERN_F16) ||
+            !kv8_strides_ok(q_ld, q_hd, a.dim)))
+    return TERN_EINVAL;
+  if (rows == 0) return TERN_OK;
+  if (!k || !v) return TERN_EINVAL;
+  const int size = type == TERN_F32 ? 4 : 2;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) ||
+      !aligned16(positions) || ld * size % 16 != 0 || hd * size % 16 != 0 ||
+      (q && (q_ld * size % 16 != 0 || q_hd * size % 16 != 0)))
+    return TERN_EALIGN;
+  DevState* d = nullptr;
+  rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.heads = heads;
+  a.type = type;
+  a.ld = ld;
+  a.hd = hd;
+  a.rows = rows;
+  a.max_new = max_new < rows ? max_new : rows;
+  a.err = d->err;
+  t.positions = positions;
+  t.q_ld = q_ld;
+  t.q_hd = q_hd;
+  t.out = q_out;
+  t.out_type = q_type;
+  int launches = 0;
+  if (launch_kv8_append_rope(a, t, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
     return TERN_ECUDA;
   t_last_launches = launches;
   return TERN_OK;

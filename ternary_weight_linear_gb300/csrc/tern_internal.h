@@ -187,6 +187,52 @@ struct NormArgs {
 };
 cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, cudaStream_t stream);
 
+// Norm of a block's output, its gated addition to the scaled residual, and the
+// next block's norm with int8 codes; see tern_norm_add_norm_s8.
+struct NormPairArgs {
+  const void* x;
+  long long x_ld;  // elements
+  int x_type;
+  const void* post;  // the first norm's weight; null: no first norm
+  int post_type;
+  const void* gate;  // may be null
+  int gate_type;
+  long long gate_ld;  // 0: the same for every token
+  const void* residual;
+  void* residual_out;  // may be null
+  int residual_type;
+  const void* weight;
+  int weight_type;
+  float residual_scale, branch_scale, eps;
+  int8_t* q;       // may be null
+  float* x_scale;  // with q
+  uint16_t* y;     // may be null
+  int T, K;
+};
+cudaError_t launch_norm_add_norm_s8(const NormPairArgs& a, cudaStream_t stream);
+
+// Rotary positions (see tern_rope).
+struct RopeArgs {
+  const uint64_t* freq;  // [rotary / 2]
+  int rotary, interleaved;
+  float magnitude;
+};
+struct RopeRows {
+  RopeArgs rope;
+  const void* x;
+  void* out;
+  int type, out_type;
+  long long ld, hd, out_ld, out_hd;  // row and head strides in elements
+  const int32_t* positions;
+  int T, heads, dim;
+};
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxDim = 1024;
+cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream);
+// false: a frequency of a turn a token and more.  All in range otherwise.
+bool rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
+                      double low, double high, uint64_t* freq, float* magnitude);
+
 // The int8 cache (see tern_kv8_cache) and one call's rows.
 struct Kv8Args {
   int8_t* codes;
@@ -222,6 +268,19 @@ inline void kv8_set_group(Kv8Args* a, int group) {
                                        1);
 }
 cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t stream, int* launches);
+
+// The append with keys and queries turned on the way: a.k, a.v, and a.q (of
+// a.type too, may be null) with a.heads heads into `out` of out_type, dense.
+struct Kv8Turn {
+  RopeArgs rope;
+  const int32_t* positions;  // of the rows; null: those in the cache
+  long long q_ld, q_hd;
+  void* out;
+  int out_type;
+  int q_heads;  // heads of a CTA
+};
+cudaError_t launch_kv8_append_rope(const Kv8Args& a, const Kv8Turn& t, cudaStream_t stream,
+                                   int* launches);
 
 // Attention of sequences with few query rows per key-value head (new tokens *
 // group), at most max_rows; the others are left to the prompt kernel.  tm: the

@@ -198,6 +198,160 @@ cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
   return launch_one<XT, RT, 4>(a, threads(4), stream);
 }
 
+// tern_norm_add_norm_s8: the norm after a block, its gate, the residual's
+// addition and the norm before the next block:
+//   n = (x w1) (mean(x^2) + eps)^-1/2;    r = round(a res + b g n);
+//   y = (r w2) (mean(r^2) + eps)^-1/2;    codes and scale of y as above.
+// The same plan with a second reduction: one CTA per token, the row in
+// registers from the first load to the last store, so every input is read and
+// every output written once.  Rows of one vector a thread load what the second
+// half takes before the first barrier; longer ones, whose registers are the
+// row's, behind it.
+template <int XT, int RT, int NV>
+__global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a) {
+  grid_dependents_launch();
+  __shared__ float red_x[32], red_s[32], red_m[32];
+  const int t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = a.K >> 3, warps = blockDim.x >> 5;
+  const long long row = static_cast<long long>(t) * a.K;
+  const long long xrow = static_cast<long long>(t) * a.x_ld;
+  const long long grow = static_cast<long long>(t) * a.gate_ld;
+  auto weight8 = [](const void* p, int type, long long i) {
+    return type == TERN_F32 ? load8<TERN_F32>(p, i) : load8<TERN_BF16>(p, i);
+  };
+  // what an element of the block's output is multiplied with beside its norm
+  auto factors = [&](long long i) {
+    F8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = a.branch_scale;
+    if (a.post) {
+      const F8 p = weight8(a.post, a.post_type, i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f.v[e] *= p.v[e];
+    }
+    if (a.gate) {
+      const F8 g = weight8(a.gate, a.gate_type, grow + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f.v[e] *= g.v[e];
+    }
+    return f;
+  };
+  constexpr bool kEarly = NV == 1;
+  grid_dependency_wait();  // the inputs and the output buffers come from earlier work
+  F8 r[NV], f, res, w;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < vecs) {
+      r[j] = load8<XT>(a.x, xrow + 8ll * i);
+      if (kEarly) {
+        f = factors(8ll * i);
+        res = load8<RT>(a.residual, row + 8ll * i);
+        w = weight8(a.weight, a.weight_type, 8ll * i);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(r[j].v[e], r[j].v[e], sum);
+    }
+  }
+  float inv = 1.f;
+  if (a.post) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red_x[warp] = sum;
+    __syncthreads();
+    sum = lane < warps ? red_x[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
+  }
+  sum = 0.f;
+  float big = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < vecs) {
+      if (!kEarly) {
+        // (the barriers to the compiler keep four vectors' loads out of each
+        // other's registers, which there are not enough of)
+        if (NV == 4) asm volatile("" ::: "memory");
+        f = factors(8ll * i);
+        res = load8<RT>(a.residual, row + 8ll * i);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        r[j].v[e] = fmaf(r[j].v[e] * inv, f.v[e], a.residual_scale * res.v[e]);
+      if (NV == 4) asm volatile("" ::: "memory");
+      if (!kEarly) w = weight8(a.weight, a.weight_type, 8ll * i);
+      round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(r[j].v[e], r[j].v[e], sum);
+        r[j].v[e] *= w.v[e];
+        big = max_nan(big, fabsf(r[j].v[e]));  // (the weight's NaN is not in the sum)
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
+  }
+  if (lane == 0) {
+    red_s[warp] = sum;
+    red_m[warp] = big;
+  }
+  __syncthreads();
+  sum = lane < warps ? red_s[lane] : 0.f;
+  big = lane < warps ? red_m[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
+  }
+  inv = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
+  const float amax = big * inv;
+  const float scale = amax / 127.0f;  // IEEE single-precision division
+  if (a.q && threadIdx.x == 0) a.x_scale[t] = scale;
+  const float sinv = 1.0f / scale;
+  const bool fast = quant_fast(scale);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < vecs) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[j].v[e] *= inv;
+      if (a.y)
+        *reinterpret_cast<uint4*>(a.y + row + 8ll * i) =
+            make_uint4(pack_bf16(r[j].v[0], r[j].v[1]), pack_bf16(r[j].v[2], r[j].v[3]),
+                       pack_bf16(r[j].v[4], r[j].v[5]), pack_bf16(r[j].v[6], r[j].v[7]));
+      if (a.q) {
+        uint2 out = make_uint2(0u, 0u);
+        if (amax > 0.f) out = quant_codes8(r[j].v, scale, sinv, fast);
+        *reinterpret_cast<uint2*>(a.q + row + 8ll * i) = out;
+      }
+    }
+  }
+}
+
+template <int XT, int RT, int NV>
+cudaError_t launch_pair_one(const NormPairArgs& a, int threads, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      pdl_launch_config(attr, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream);
+  return cudaLaunchKernelEx(&cfg, norm_pair_kernel<XT, RT, NV>, a);
+}
+
+template <int XT, int RT>
+cudaError_t launch_pair_types(const NormPairArgs& a, cudaStream_t stream) {
+  const int vecs = a.K / 8;
+  auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
+  if (vecs <= 1024) return launch_pair_one<XT, RT, 1>(a, threads(1), stream);
+  if (vecs <= 2048) return launch_pair_one<XT, RT, 2>(a, threads(2), stream);
+  return launch_pair_one<XT, RT, 4>(a, threads(4), stream);
+}
+
 }  // namespace
 
 cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, cudaStream_t stream) {
@@ -210,6 +364,17 @@ cudaError_t launch_add_rmsnorm_s8(const NormArgs& a, cudaStream_t stream) {
   TERN_NORM_CASE(TERN_BF16, TERN_BF16)
   TERN_NORM_CASE(TERN_BF16, TERN_F32)
   TERN_NORM_CASE(TERN_BF16, kNoResidual)
+#undef TERN_NORM_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_norm_add_norm_s8(const NormPairArgs& a, cudaStream_t stream) {
+#define TERN_NORM_CASE(XT, RT) \
+  if (a.x_type == XT && a.residual_type == RT) return launch_pair_types<XT, RT>(a, stream);
+  TERN_NORM_CASE(TERN_F32, TERN_BF16)
+  TERN_NORM_CASE(TERN_F32, TERN_F32)
+  TERN_NORM_CASE(TERN_BF16, TERN_BF16)
+  TERN_NORM_CASE(TERN_BF16, TERN_F32)
 #undef TERN_NORM_CASE
   return cudaErrorInvalidValue;
 }

@@ -1,0 +1,108 @@
+// tern_rope: rotary positions of the rows of [T][heads][dim], and the host's
+// tables of frequencies.
+//   (u, v) -> m (u cos - v sin, u sin + v cos),  angle = position * freq
+// for the pairs of a head's first `rotary` elements, the others as they are.
+//
+// A thread holds a unit of sixteen elements (eight pairs) of a row in
+// registers, computes its eight turns once and applies them to that unit of
+// several heads of the token.  Every element is read and written once: a
+// prompt is bound by HBM, a decode step by one load after the position's.
+// Several heads a thread where that leaves work for all SMs: a turn costs some
+// 30 instructions, a unit's loads and stores 8.
+#include <math.h>
+
+#include "tern_device.cuh"
+#include "tern_rope.cuh"
+
+namespace tern {
+namespace {
+
+template <int TYPE, int OUT>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeRows a) {
+  grid_dependents_launch();
+  // x: units of a head; y: heads; z: tokens
+  const long long t = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
+  const RopeUnit unit(a.rope, threadIdx.x);
+  grid_dependency_wait();  // the inputs and the output come from earlier work
+  if (t >= a.T) return;
+  float2 turn[8];
+  if (unit.pair >= 0) rope_turns(a.rope, unit.pair, a.positions[t], turn);
+#pragma unroll 2
+  for (int h = threadIdx.y; h < a.heads; h += blockDim.y) {
+    const long long from = t * a.ld + h * a.hd, to = t * a.out_ld + h * a.out_hd;
+    float u[8], v[8];
+    load8<TYPE>(a.x, from + unit.a, u);
+    load8<TYPE>(a.x, from + unit.b, v);
+    if (unit.pair >= 0) rope_apply(a.rope, turn, u, v);
+    store8<OUT>(a.out, to + unit.a, u);
+    store8<OUT>(a.out, to + unit.b, v);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream) {
+  const int units = a.dim / 16;
+  // one head a thread until every SM has its threads, then up to four
+  const long long all = static_cast<long long>(a.T) * a.heads * units;
+  int each = static_cast<int>(all / (static_cast<long long>(num_sms) * 2048));
+  each = each < 1 ? 1 : each > 4 ? 4 : each;
+  int lanes = (a.heads + each - 1) / each;
+  if (lanes > kRopeThreads / units) lanes = kRopeThreads / units;
+  int tokens = 128 / (units * lanes);
+  if (tokens < 1) tokens = 1;
+  if (tokens > a.T) tokens = a.T;
+  if (tokens > 64) tokens = 64;  // (a block's third extent)
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      pdl_launch_config(attr, dim3((a.T + tokens - 1) / tokens), dim3(units, lanes, tokens), 0,
+                        stream);
+#define TERN_ROPE_CASE(TYPE, OUT) \
+  if (a.type == TYPE && a.out_type == OUT) return cudaLaunchKernelEx(&cfg, rope_kernel<TYPE, OUT>, a);
+  TERN_ROPE_CASE(TERN_F32, TERN_F32)
+  TERN_ROPE_CASE(TERN_F32, TERN_BF16)
+  TERN_ROPE_CASE(TERN_F32, TERN_F16)
+  TERN_ROPE_CASE(TERN_BF16, TERN_F32)
+  TERN_ROPE_CASE(TERN_BF16, TERN_BF16)
+  TERN_ROPE_CASE(TERN_BF16, TERN_F16)
+  TERN_ROPE_CASE(TERN_F16, TERN_F32)
+  TERN_ROPE_CASE(TERN_F16, TERN_BF16)
+  TERN_ROPE_CASE(TERN_F16, TERN_F16)
+#undef TERN_ROPE_CASE
+  return cudaErrorInvalidValue;
+}
+
+bool rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
+                      double low, double high, uint64_t* freq, float* magnitude) {
+  const double kTurn = 6.283185307179586;
+  double grow = 1.0;
+  if (scaling == TERN_ROPE_BASE) base *= pow(factor, static_cast<double>(rotary) / (rotary - 2));
+  // the pairs (as real numbers) that turn `high` and `low` times in the trained
+  // context
+  double first = 0, last = 0;
+  if (scaling == TERN_ROPE_RAMP) {
+    const double per = rotary / (2 * log(base));
+    first = floor(per * log(trained / (kTurn * high)));
+    last = ceil(per * log(trained / (kTurn * low)));
+    if (first < 0) first = 0;
+    if (last > rotary - 1) last = rotary - 1;
+    grow = 0.1 * log(factor) + 1.0;
+  }
+  for (int i = 0; i < rotary / 2; ++i) {
+    double theta = pow(base, -2.0 * i / rotary);
+    double keep = 1.0;  // share of the frequency that is not slowed
+    if (scaling == TERN_ROPE_LINEAR) keep = 0.0;
+    if (scaling == TERN_ROPE_BANDS) keep = (trained * theta / kTurn - low) / (high - low);
+    if (scaling == TERN_ROPE_RAMP)
+      keep = 1.0 - (i - first) / (last - first > 0.001 ? last - first : 0.001);
+    keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+    theta *= keep + (1.0 - keep) / factor;
+    const double turns = ldexp(theta / kTurn, 64);
+    if (!(turns < 18446744073709551616.0)) return false;
+    freq[i] = static_cast<uint64_t>(turns);
+  }
+  *magnitude = static_cast<float>(grow);
+  return true;
+}
+
+}  // namespace tern
