@@ -501,6 +501,37 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type,
                        void* out, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace tern_kv8_attention_shared needs: that of
+ * tern_kv8_attention, fp32 results of the rows' own tokens, and partial results
+ * of the prefix.  Host-only; 0 for sizes out of range. */
+size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
+                                                 int kv_heads, int head_dim);
+
+/* tern_kv8_attention for a batch whose sequences begin with the same tokens: the
+ * first `shared` tokens of every sequence with new tokens lie in the same pages
+ * (the first shared / 64 entries of their rows of page_table are alike), written
+ * once and not by this step.  Keys and values of those pages are read once for
+ * all rows of the batch instead of once for each sequence; the result is
+ * tern_kv8_attention's of the same arguments, up to the roundings stated there.
+ *   shared   tokens, a multiple of 64, 0 (none) to 64 * table_width; a sequence
+ *            whose new tokens do not all lie behind them is inconsistent
+ *            (skipped, its rows left as they are, TERN_EINDEX).  An argument of
+ *            the call: a captured call keeps it
+ *   page_table the shared entries are read from its first row (which must so
+ *            hold them, even where the first sequence has no tokens) or from each
+ *   rows, heads ceil(rows * heads / kv_heads / 256) * kv_heads has to stay below
+ *            2^31 - 1000
+ *   the others as for tern_kv8_attention; workspace of
+ *            tern_kv8_attention_shared_workspace_bytes, zeroed and kept as there.
+ * The prefix's and the own tokens' parts are joined in fp32 by their
+ * log-sum-exps; results are bit-for-bit reproducible. */
+int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type,
+                              long long ld, long long hd, int rows, int heads,
+                              int shared, int max_new, int window, int sinks,
+                              float softmax_scale, void* out, float* lse,
+                              void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Bytes of the fixed device scratch tern_linear_small_t_noalloc uses. */
 #define TERN_NOALLOC_SCRATCH_BYTES (8u << 20)
 

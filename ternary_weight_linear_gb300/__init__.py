@@ -29,7 +29,7 @@ __all__ = [
     "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append", "tern_kv8_attention",
     "tern_kv8_attention_workspace_bytes", "KV8_BLOCK",
     "tern_norm_add_norm_s8", "tern_rope_frequencies", "tern_rope", "tern_kv8_append_rope",
-    "ROPE_SCALINGS",
+    "ROPE_SCALINGS", "tern_kv8_attention_shared", "tern_kv8_attention_shared_workspace_bytes",
     "tern_selftest_wait_timeout", "RUNGS",
     "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES", "SYNC_BYTES", "T5_GROUP_BYTES", "ROTATION_BLOCK",
 ]
@@ -44,7 +44,8 @@ EXPORTED_SYMBOLS = (
     "tern_linear_small_t_noalloc", "tern_repack_t5", "tern_rotate_bf16",
     "tern_selftest_wait_timeout", "tern_linear_s8", "tern_add_rmsnorm_s8", "tern_kv8_append",
     "tern_kv8_attention", "tern_kv8_attention_workspace_bytes", "tern_norm_add_norm_s8",
-    "tern_rope_frequencies", "tern_rope", "tern_kv8_append_rope",
+    "tern_rope_frequencies", "tern_rope", "tern_kv8_append_rope", "tern_kv8_attention_shared",
+    "tern_kv8_attention_shared_workspace_bytes",
 )
 
 # Size of the library's fixed scratch for tern_linear_small_t_noalloc.
@@ -155,6 +156,10 @@ def load() -> ctypes.CDLL:
         lib.tern_rope.restype = I
         lib.tern_kv8_append_rope.argtypes = [C, P, P, P, I, L, L, I, L, L, P, R, P, I, I, I, P]
         lib.tern_kv8_append_rope.restype = I
+        lib.tern_kv8_attention_shared_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.tern_kv8_attention_shared_workspace_bytes.restype = Z
+        lib.tern_kv8_attention_shared.argtypes = [C, P, I, L, L, I, I, I, I, I, I, F, P, P, P, Z, P]
+        lib.tern_kv8_attention_shared.restype = I
         lib.tern_selftest_wait_timeout.argtypes = [I, P]
         lib.tern_selftest_wait_timeout.restype = I
         _lib = lib
@@ -665,6 +670,52 @@ def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
         _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("tern_kv8_attention", rc)
+    return out
+
+
+def tern_kv8_attention_shared_workspace_bytes(seqs: int, rows: int, heads: int, kv_heads: int,
+                                              head_dim: int) -> int:
+    return int(load().tern_kv8_attention_shared_workspace_bytes(int(seqs), int(rows), int(heads),
+                                                                int(kv_heads), int(head_dim)))
+
+
+def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                              page_table: torch.Tensor, row_start: torch.Tensor,
+                              seq_lens: torch.Tensor, shared: int, max_new: int | None = None,
+                              window: int = 0, sinks: int = 0,
+                              softmax_scale: float | None = None,
+                              out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """tern_kv8_attention for a batch whose sequences begin with the same pages.
+
+    The first `shared` tokens (a multiple of 64) of every sequence lie in the
+    same pages: the first shared / 64 entries of the rows of page_table are
+    alike.  They are read once for all rows of the batch.  New tokens lie behind
+    them.  The result is tern_kv8_attention's; the other arguments are as there,
+    the workspace of tern_kv8_attention_shared_workspace_bytes bytes."""
+    cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
+    pq = _strided(q, "q", (torch.bfloat16, torch.float16), 3)
+    rows, heads, dim = q.shape
+    kv_heads = codes.shape[2]
+    if dim != codes.shape[4]:
+        raise ValueError(f"q's head_dim {dim} is not the cache's {codes.shape[4]}")
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(
+                tern_kv8_attention_shared_workspace_bytes(cache.seqs, max(1, rows), heads,
+                                                          kv_heads, dim),
+                dtype=torch.uint8, device=q.device)
+            workspace[:SYNC_BYTES].zero_()  # the rest is scratch
+    rc = load().tern_kv8_attention_shared(
+        ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads, _most(shared),
+        max(1, rows) if max_new is None else _most(max_new), _most(window), _most(sinks),
+        1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
+        _dev(out, "out", q.dtype, (rows, heads, dim)),
+        _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("tern_kv8_attention_shared", rc)
     return out
 
 

@@ -338,6 +338,93 @@ bool kv8_strides_ok(long long ld, long long hd, int dim) {
   return ld >= dim && hd >= dim && ld <= kMaxStride && hd <= kMaxStride;
 }
 
+// Tickets of the tensor-core attention in the synchronisation area, behind the
+// few-row kernel's, and of the shared prefix's launch.
+constexpr int kPromptTickets = 512, kPrefixTickets = 768;
+static_assert((kPrefixTickets + kSmallTMaxCtas) * sizeof(int) <= kSyncBytes &&
+                  kPromptTickets + kSmallTMaxCtas <= kPrefixTickets,
+              "sync area");
+
+// The attention's arguments, but for what belongs to the workspace and the
+// device.
+int kv8_attention_args(const tern_kv8_cache* cache, const void* q, int type, long long ld,
+                       long long hd, int rows, int heads, int max_new, int window, int sinks,
+                       float softmax_scale, void* out, float* lse, Kv8Args* args) {
+  Kv8Args& a = *args;
+  const int rc = kv8_args(cache, &a);
+  if (rc != TERN_OK) return rc;
+  if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
+      heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < (rows > 0) || window < 0 || sinks < 0 ||
+      static_cast<long long>(rows) * (heads / a.hkv) > INT_MAX ||
+      !(softmax_scale > 0.f) || !(softmax_scale * kLog2E < HUGE_VALF) || !kv8_strides_ok(ld, hd, a.dim))
+    return TERN_EINVAL;
+  if (rows == 0) return TERN_OK;
+  if (!q || !out || !kv8_prompt_fits(max_new < rows ? max_new : rows, heads / a.hkv, a.hkv, a.seqs))
+    return TERN_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ld % 8 != 0 || hd % 8 != 0)
+    return TERN_EALIGN;
+  a.q = q;
+  a.type = type;
+  a.ld = ld;
+  a.hd = hd;
+  a.rows = rows;
+  a.max_new = max_new < rows ? max_new : rows;
+  a.heads = heads;
+  kv8_set_group(&a, heads / a.hkv);
+  // a window of every token that the table can hold is none
+  const int most_tokens = a.width * TERN_KV8_BLOCK;
+  a.window = window < most_tokens ? window : 0;
+  a.sinks = a.window > 0 ? (sinks < most_tokens ? sinks : most_tokens) : 0;
+  a.scale_log2 = softmax_scale * kLog2E;
+  a.out = out;
+  a.lse = lse;
+  return TERN_OK;
+}
+
+// The attention's launches, with the workspace that tern_kv8_attention asks for.
+int run_kv8_attention(Kv8Args* args, Kv8Mode mode, uint8_t* workspace, const DevState* d,
+                      cudaStream_t st, int* launches) {
+  Kv8Args& a = *args;
+  a.tickets = reinterpret_cast<int*>(workspace);
+  a.partials = reinterpret_cast<float*>(workspace + kSyncBytes);
+  a.err = d->err;
+  CUtensorMap tm;
+  const uint64_t dim = static_cast<uint64_t>(a.dim);
+  const int rc = make_map_u8(&tm, a.codes, dim,
+                             static_cast<uint64_t>(a.pages) * 2 * a.hkv * TERN_KV8_BLOCK, dim,
+                             static_cast<uint32_t>(dim), kKvRowsBox,
+                             a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  if (rc != TERN_OK) return rc;
+  // Each sequence goes by its own rows: few of them per key-value head to the
+  // kernel that is bound by the cache's bytes, more to the one on the tensor
+  // cores.  A single sequence takes one launch, of the latter where
+  // max_new allows more than the former takes.
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  long long pages = a.width - a.shared / TERN_KV8_BLOCK;  // that a sequence's rows see, at most
+  if (a.window > 0) {
+    const long long seen = (static_cast<long long>(a.window) + a.max_new + a.sinks) / TERN_KV8_BLOCK + 4;
+    if (seen < pages) pages = seen;
+  }
+  const bool long_batch = pages * a.hkv * a.seqs >= static_cast<long long>(kKvLongPages) * d->sms;
+  const int few = most <= kKvFewRowsLong && long_batch ? kKvFewRowsLong : kKvFewRows;
+  const bool many = most > few;
+  if (!many || a.seqs > 1) {
+    if (launch_kv8_rows(&tm, a, mode, few, d->sms, st, launches) != cudaSuccess) return TERN_ECUDA;
+  }
+  if (many) {
+    if (launch_kv8_prompt(a, mode, a.seqs > 1 ? few + 1 : 1,
+                          a.partials + kv8_rows_partial_bytes(a.dim) / sizeof(float),
+                          a.tickets + kPromptTickets, d->sms, st, launches) != cudaSuccess)
+      return TERN_ECUDA;
+  }
+  return TERN_OK;
+}
+
+// fp32 results and log-sum-exps of the rows' own tokens.
+size_t own_bytes(int rows, int heads, int dim) {
+  return align_up(sizeof(float) * rows * heads * (static_cast<size_t>(dim) + 1), 256);
+}
+
 // A rotation's arguments for heads of `dim` elements.
 int rope_args(const tern_rotation* r, int dim, RopeArgs* a) {
   if (!r || !r->freq || r->rotary_dim < 16 || r->rotary_dim % 16 != 0 || r->rotary_dim > dim ||
@@ -811,18 +898,9 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
                        float softmax_scale, void* out, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream) {
   Kv8Args a;
-  int rc = kv8_args(cache, &a);
-  if (rc != TERN_OK) return rc;
-  if ((type != TERN_BF16 && type != TERN_F16) || rows < 0 || heads < 1 ||
-      heads % a.hkv != 0 || heads / a.hkv > 64 || max_new < (rows > 0) || window < 0 || sinks < 0 ||
-      static_cast<long long>(rows) * (heads / a.hkv) > INT_MAX ||
-      !(softmax_scale > 0.f) || !(softmax_scale * kLog2E < HUGE_VALF) || !kv8_strides_ok(ld, hd, a.dim))
-    return TERN_EINVAL;
-  if (rows == 0) return TERN_OK;
-  if (!q || !out || !kv8_prompt_fits(max_new < rows ? max_new : rows, heads / a.hkv, a.hkv, a.seqs))
-    return TERN_EINVAL;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ld % 8 != 0 || hd % 8 != 0)
-    return TERN_EALIGN;
+  int rc = kv8_attention_args(cache, q, type, ld, hd, rows, heads, max_new, window, sinks,
+                              softmax_scale, out, lse, &a);
+  if (rc != TERN_OK || rows == 0) return rc;
   if (!workspace || workspace_bytes < tern_kv8_attention_workspace_bytes(a.seqs, rows, heads,
                                                                          a.hkv, a.dim))
     return TERN_ENOSPACE;
@@ -830,57 +908,71 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   DevState* d = nullptr;
   rc = device_state(&d);
   if (rc != TERN_OK) return rc;
-  a.q = q;
-  a.type = type;
-  a.ld = ld;
-  a.hd = hd;
-  a.rows = rows;
-  a.max_new = max_new < rows ? max_new : rows;
-  a.heads = heads;
-  kv8_set_group(&a, heads / a.hkv);
-  // a window of every token that the table can hold is none
-  const int most_tokens = a.width * TERN_KV8_BLOCK;
-  a.window = window < most_tokens ? window : 0;
-  a.sinks = a.window > 0 ? (sinks < most_tokens ? sinks : most_tokens) : 0;
-  a.scale_log2 = softmax_scale * kLog2E;
-  a.out = out;
-  a.lse = lse;
-  a.tickets = static_cast<int*>(workspace);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSyncBytes);
-  a.err = d->err;
-  CUtensorMap tm;
-  const uint64_t dim = static_cast<uint64_t>(a.dim);
-  rc = make_map_u8(&tm, a.codes, dim,
-                   static_cast<uint64_t>(a.pages) * 2 * a.hkv * TERN_KV8_BLOCK, dim,
-                   static_cast<uint32_t>(dim), kKvRowsBox,
-                   a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-  if (rc != TERN_OK) return rc;
-  // Each sequence goes by its own rows: few of them per key-value head to the
-  // kernel that is bound by the cache's bytes, more to the one on the tensor
-  // cores.  A single sequence takes one launch, of the latter where
-  // max_new allows more than the former takes.
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long most = static_cast<long long>(a.max_new) * a.group;
-  long long pages = a.width;  // that a sequence's rows see, at most
-  if (a.window > 0) {
-    const long long seen = (static_cast<long long>(a.window) + a.max_new + a.sinks) / TERN_KV8_BLOCK + 4;
-    if (seen < pages) pages = seen;
-  }
-  const bool long_batch = pages * a.hkv * a.seqs >= static_cast<long long>(kKvLongPages) * d->sms;
-  const int few = most <= kKvFewRowsLong && long_batch ? kKvFewRowsLong : kKvFewRows;
-  const bool many = most > few;
   int launches = 0;
-  if (!many || a.seqs > 1) {
-    if (launch_kv8_rows(&tm, a, few, d->sms, st, &launches) != cudaSuccess) return TERN_ECUDA;
+  rc = run_kv8_attention(&a, kKvWhole, static_cast<uint8_t*>(workspace), d,
+                         static_cast<cudaStream_t>(stream), &launches);
+  if (rc == TERN_OK) t_last_launches = launches;
+  return rc;
+}
+
+size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads, int kv_heads,
+                                                 int head_dim) {
+  const size_t n = tern_kv8_attention_workspace_bytes(seqs, rows, heads, kv_heads, head_dim);
+  return n == 0 ? 0 : align_up(n, 256) + own_bytes(rows, heads, head_dim) +
+                          kv8_prompt_partial_bytes(head_dim);
+}
+
+int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type, long long ld,
+                              long long hd, int rows, int heads, int shared, int max_new,
+                              int window, int sinks, float softmax_scale, void* out, float* lse,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  Kv8Args a;
+  int rc = kv8_attention_args(cache, q, type, ld, hd, rows, heads, max_new, window, sinks,
+                              softmax_scale, out, lse, &a);
+  if (rc != TERN_OK) return rc;
+  if (shared < 0 || shared % TERN_KV8_BLOCK != 0 || shared / TERN_KV8_BLOCK > a.width ||
+      !kv8_prompt_fits(rows, heads / a.hkv, a.hkv, 1))
+    return TERN_EINVAL;
+  if (rows == 0) return TERN_OK;
+  const size_t base = align_up(
+      tern_kv8_attention_workspace_bytes(a.seqs, rows, heads, a.hkv, a.dim), 256);
+  if (!workspace || workspace_bytes < tern_kv8_attention_shared_workspace_bytes(
+                                          a.seqs, rows, heads, a.hkv, a.dim))
+    return TERN_ENOSPACE;
+  if (!aligned16(workspace)) return TERN_EALIGN;
+  DevState* d = nullptr;
+  rc = device_state(&d);
+  if (rc != TERN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int launches = 0;
+  a.behind = shared;
+  if (a.seqs == 1 || shared == 0) {
+    rc = run_kv8_attention(&a, kKvWhole, ws, d, st, &launches);
+  } else {
+    // the own tokens' part in fp32, then the prefix's, which joins them
+    float* o = reinterpret_cast<float*>(ws + base);
+    float* l = o + static_cast<size_t>(rows) * heads * a.dim;
+    Kv8Args own = a;
+    own.shared = shared;
+    own.table += shared / TERN_KV8_BLOCK;
+    own.sinks = a.sinks > shared ? a.sinks - shared : 0;
+    own.out = o;
+    own.lse = l;
+    rc = run_kv8_attention(&own, kKvOwn, ws, d, st, &launches);
+    if (rc != TERN_OK) return rc;
+    a.err = d->err;
+    a.shared = shared;
+    a.own = o;
+    a.own_lse = l;
+    if (launch_kv8_prompt(a, kKvPrefix, 1,
+                          reinterpret_cast<float*>(ws + base + own_bytes(rows, heads, a.dim)),
+                          static_cast<int*>(workspace) + kPrefixTickets, d->sms, st,
+                          &launches) != cudaSuccess)
+      rc = TERN_ECUDA;
   }
-  if (many) {
-    if (launch_kv8_prompt(a, a.seqs > 1 ? few + 1 : 1,
-                          a.partials + kv8_rows_partial_bytes(a.dim) / sizeof(float),
-                          a.tickets + 512, d->sms, st, &launches) != cudaSuccess)
-      return TERN_ECUDA;
-  }
-  t_last_launches = launches;
-  return TERN_OK;
+  if (rc == TERN_OK) t_last_launches = launches;
+  return rc;
 }
 
 int tern_linear_small_t_noalloc(const uint32_t* Wpacked, const uint16_t* scales,

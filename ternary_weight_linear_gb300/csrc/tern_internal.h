@@ -257,7 +257,19 @@ struct Kv8Args {
   int* tickets;
   float* partials;
   int* err;
+  // Attention behind a shared prefix.  shared: tokens that precede what table
+  // and lens are read for, the same for every sequence of the call (its first
+  // pages are left out of the table's rows); 0 otherwise.  behind: the position
+  // that no new token may precede.  own, own_lse: what the sequences' own tokens
+  // gave, fp32 [rows][heads][dim] and [rows][heads].
+  int shared, behind;
+  const float* own;
+  const float* own_lse;
 };
+// What an attention kernel computes: a call's result; the part of it that comes
+// from the tokens behind a shared prefix, in fp32; or the prefix's part for all
+// rows of the batch, joined with the former.
+enum Kv8Mode : int { kKvWhole, kKvOwn, kKvPrefix };
 // n / group = (high half of n * mul + n) >> shift for n < 2^31: with shift =
 // ceil(log2 group), mul = floor(2^32 (2^shift - group) / group) + 1.
 inline void kv8_set_group(Kv8Args* a, int group) {
@@ -301,8 +313,8 @@ constexpr int kKvFewRowsLong = 24, kKvLongPages = 40;
 constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
 size_t kv8_rows_partial_bytes(int dim);
 cudaError_t kv8_rows_set_attributes();
-cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
-                            cudaStream_t stream, int* launches);
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, Kv8Mode mode, int max_rows,
+                            int num_sms, cudaStream_t stream, int* launches);
 
 // Attention of sequences with at least min_rows query rows per key-value
 // head, on the tensor cores.  tickets: kSmallTMaxCtas zeroed ints.
@@ -310,8 +322,8 @@ size_t kv8_prompt_partial_bytes(int dim);
 cudaError_t kv8_prompt_set_attributes();
 // Whether the kernel's grid holds the blocks of rows of such a call.
 bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs);
-cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
-                              int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches);
 
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier
 // phase nobody completes; 1: a device counter nobody raises) and records the

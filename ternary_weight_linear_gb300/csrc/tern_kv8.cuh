@@ -16,7 +16,7 @@ constexpr int kBlk = TERN_KV8_BLOCK;
 
 // A sequence of the batch.  ok: its entries are consistent.
 struct KvSeq {
-  int len, m, row0;  // tokens, new tokens, first row of q / k / v
+  int len, m, row0;  // tokens (behind the shared ones), new tokens, first row of q / k / v
   bool ok;
 };
 
@@ -29,6 +29,9 @@ __device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
   s.m = s.ok ? end - s.row0 : 0;
   s.ok = s.ok && s.len >= 0 && (static_cast<long long>(s.len) + kBlk - 1) / kBlk <= a.width &&
          s.m <= s.len && s.m <= a.max_new;
+  // (new tokens lie behind what the call shares)
+  s.ok = s.ok && (s.m == 0 || s.len - s.m >= a.behind);
+  s.len -= a.shared;
   return s;
 }
 
@@ -56,6 +59,22 @@ __device__ __forceinline__ KvPages kv_pages(const Kv8Args& a, int p0, int p1) {
     v.sinks = s < v.first ? s : v.first;
   }
   v.count = v.sinks + p1 / kBlk - v.first + 1;
+  return v;
+}
+
+// The pages of the shared prefix that rows at p0 and later see.
+__device__ __forceinline__ KvPages kv_prefix_pages(const Kv8Args& a, int p0) {
+  const int all = a.shared / kBlk;
+  KvPages v;
+  v.first = 0;
+  v.sinks = 0;
+  if (a.window > 0 && p0 >= a.window) {
+    const int first = (p0 - a.window + 1) / kBlk;
+    v.first = first < all ? first : all;
+    const int s = a.sinks / kBlk + (a.sinks % kBlk != 0);
+    v.sinks = s < v.first ? s : v.first;
+  }
+  v.count = v.sinks + all - v.first;
   return v;
 }
 

@@ -39,6 +39,8 @@
 // exponentials are as many for half the products).  Both score buffers in one product pair
 // that reads the queries from shared memory once lost a quarter: the softmax
 // then waits for each pair.
+#include <limits.h>
+
 #include "tern_kv8.cuh"
 
 namespace tern {
@@ -160,11 +162,14 @@ __device__ __forceinline__ void cta_barrier() {
 // A block's rows of the output, staged in shared memory where the queries were
 // (a warp's own rows, whose products are done): chunks of 16 bytes swizzled by
 // the row, written D / 8 lanes a row.
-template <int D>
+// kPrefix: rows of skipped sequences, and of none, stay as they are (pos: the
+// tokens' positions from the block's first, negative for such).
+template <int D, bool kPrefix>
 struct OutRows {
   const Kv8Args& a;
   uint8_t* stage;
   int r0, row0, hk;
+  const int* pos;
   __device__ __forceinline__ uint8_t* staged(int row, int c) const {
     return stage + row * (2 * D) + ((c ^ (row & 7)) << 4);
   }
@@ -173,13 +178,17 @@ struct OutRows {
     return static_cast<long long>(row0 + tok) * a.heads + hk * a.group +
            (r0 + r - tok * a.group);
   }
+  __device__ __forceinline__ bool written(int r) const {
+    return !kPrefix || pos[kv_token(a, r0 + r) - kv_token(a, r0)] >= 0;
+  }
   // (whole warp) rows [begin, end), none if end <= begin
   __device__ __forceinline__ void write_out(int lane, int begin, int end) const {
     constexpr int kLanes = D / 8;
 #pragma unroll 4
     for (int r = begin + lane / kLanes; r < end; r += 32 / kLanes)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row(r) * D +
-                                8 * (lane % kLanes)) = lds_v4(staged(r, lane % kLanes));
+      if (written(r))
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row(r) * D +
+                                  8 * (lane % kLanes)) = lds_v4(staged(r, lane % kLanes));
   }
 };
 
@@ -192,15 +201,21 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// What a row's own tokens gave, as a part beside the prefix's: its weight in the
+// parts' units.
+__device__ __forceinline__ float own_weight(const Kv8Args& a, long long row) {
+  return fmaf(__ldcg(a.own_lse + row), 1.4426950408889634f, kPOff);
+}
+
 // The last part to arrive adds them all in order (every thread of the CTA) and
-// stages the rows.
-template <int D>
+// stages the rows, or writes them in fp32.
+template <int D, int kMode>
 __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, const float* first,
-                                           int parts, int rows, int r0, int row0, int hk) {
+                                           int parts, int rows,
+                                           const OutRows<D, kMode == kKvPrefix>& put) {
   using L = PL<D>;
   constexpr size_t kPart = 2 * kPRows * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const OutRows<D> put{a, smem + L::kQOff, r0, row0, hk};
   const int rows32 = (rows + 31) & ~31;
   float* weight = reinterpret_cast<float*>(smem + L::kConvOff);  // [part][rows32]
   // a row per thread: the parts' weights over the row's sum
@@ -215,6 +230,11 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
       weight[p * rows32 + row] = w;
       top = fmaxf(top, w);
     }
+    float own = -INFINITY;
+    if (kMode == kKvPrefix) {
+      own = own_weight(a, put.row(row));
+      top = fmaxf(top, own);
+    }
     const float base = top == -INFINITY ? 0.f : top;
     float l = 0.f;
 #pragma unroll 4
@@ -223,10 +243,15 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
       weight[p * rows32 + row] = w;
       l += w;
     }
+    if (kMode == kKvPrefix) {
+      own = exp2f(own - base);
+      l += own;
+    }
     const float one = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) weight[p * rows32 + row] *= one;
-    if (a.lse) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
+    if (kMode == kKvPrefix) weight[parts * rows32 + row] = own * one;
+    if (a.lse && put.written(row)) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
   }
   cta_barrier();
   // sixteen elements of 32 rows per warp, four parts' loads in flight
@@ -259,6 +284,24 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
           acc[k].w = fmaf(w, v[p][k].w, acc[k].w);
         }
       }
+    }
+    if constexpr (kMode == kKvPrefix) {
+      const float w = weight[parts * rows32 + row];
+      const float4* own = reinterpret_cast<const float4*>(a.own + put.row(row) * D) + c;
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        const float4 v = __ldcg(own + k);
+        acc[k].x = fmaf(w, v.x, acc[k].x);
+        acc[k].y = fmaf(w, v.y, acc[k].y);
+        acc[k].z = fmaf(w, v.z, acc[k].z);
+        acc[k].w = fmaf(w, v.w, acc[k].w);
+      }
+    }
+    if constexpr (kMode == kKvOwn) {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + put.row(row) * D) + c;
+#pragma unroll
+      for (int k = 0; k < kC; ++k) out[k] = acc[k];
+      continue;
     }
 #pragma unroll
     for (int k = 0; k < kC; k += 2)
@@ -387,7 +430,12 @@ __device__ __noinline__ SoftState wide_pages(uint8_t* smem, const Kv8Args& a, So
 // 96 rows, where no warps are idle, it loses (46.5 and 43.2 us, 16 tokens over
 // 16000).
 constexpr int kSplitRows = 64;
-template <int D, bool kSplit>
+//
+// kMode kKvOwn: the part of the tokens behind a shared prefix, in fp32, whose
+// positions and pages count from its end.  kKvPrefix: the part of the prefix
+// itself, one "sequence" of all the call's rows, which see all of it (but for a
+// window); the result joins it with what kKvOwn wrote.
+template <int D, bool kSplit, int kMode>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole,
                       int tail_parts, int tail_items, int sms, float* __restrict__ partials,
@@ -418,20 +466,58 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int part = tail < 0 ? 0 : tail % tail_parts;
   const int item = tail < 0 ? static_cast<int>(blockIdx.x) : whole + tail / tail_parts;
   const int hk = item % a.hkv;
-  const int b = (item / a.hkv) % a.seqs;
-  const int rb = row_blocks - 1 - item / a.hkv / a.seqs;
-  const KvSeq sq = kv_seq(a, b);
-  const int R = sq.m * a.group;
+  const int b = kMode == kKvPrefix ? 0 : (item / a.hkv) % a.seqs;
+  const int rb = row_blocks - 1 - item / a.hkv / (kMode == kKvPrefix ? 1 : a.seqs);
   const int r0 = rb * (2 * kPRows);
-  if (!sq.ok && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+  constexpr int kStep = kSplit ? 2 : 1;
+  // kKvPrefix: the positions of the block's tokens (negative for rows of no
+  // sequence), the least and the largest
+  __shared__ int tok_pos[kMode == kKvPrefix ? 2 * kPRows : 1], pos_range[2];
+  KvSeq sq;
+  if constexpr (kMode == kKvPrefix) {
+    sq = {a.shared, a.rows, 0, true};
+  } else {
+    sq = kv_seq(a, b);
+    if (!sq.ok && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+  }
+  const int R = sq.m * a.group;
   if (!sq.ok || R < min_rows || r0 >= R) return;
   const int rows = R - r0 < 2 * kPRows ? R - r0 : 2 * kPRows;
   const int tiles_q = rows > kPRows ? 2 : 1;  // that see a page
-  constexpr int kStep = kSplit ? 2 : 1;
   const int p_base = sq.len - sq.m;
-  const int p_first = p_base + kv_token(a, r0);
-  const int p_last = p_base + kv_token(a, r0 + rows - 1);
-  const KvPages pages = kv_pages(a, p_first, p_last);
+  const int tok0 = kv_token(a, r0);
+  int p_first, p_last;
+  KvPages pages;
+  if constexpr (kMode == kKvPrefix) {
+    const int toks = kv_token(a, r0 + rows - 1) + 1;  // past the block's last
+    if (threadIdx.x < 2 * kPRows) tok_pos[threadIdx.x] = -1;
+    if (threadIdx.x == 0) {
+      pos_range[0] = INT_MAX;
+      pos_range[1] = -1;
+    }
+    cta_barrier();
+    for (int i = threadIdx.x; i < a.seqs; i += kPThreads) {
+      const KvSeq s = kv_seq(a, i);
+      if (!s.ok || s.m == 0) continue;
+      const int t0 = s.row0 > tok0 ? s.row0 : tok0;
+      const int t1 = s.row0 + s.m < toks ? s.row0 + s.m : toks;
+      const int from = a.shared + s.len - s.m - s.row0;  // position of row 0
+      for (int t = t0; t < t1; ++t) tok_pos[t - tok0] = from + t;
+      if (t0 < t1) {
+        atomicMin(&pos_range[0], from + t0);
+        atomicMax(&pos_range[1], from + t1 - 1);
+      }
+    }
+    cta_barrier();
+    p_first = pos_range[0];
+    p_last = pos_range[1];
+    if (p_last < 0) return;
+    pages = kv_prefix_pages(a, p_first);
+  } else {
+    p_first = p_base + tok0;
+    p_last = p_base + kv_token(a, r0 + rows - 1);
+    pages = kv_pages(a, p_first, p_last);
+  }
   // (The launch chose the parts by the table's width, the most pages that a
   // block can have: by its own it may need fewer, or none.)
   int parts = 1;
@@ -491,7 +577,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tok = kv_token(a, rr);
     const int head = hk * a.group + rr - tok * a.group;
     const long long qrow = sq.row0 + tok;
-    if (live) pos = p_base + tok;
+    if (live) pos = kMode == kKvPrefix ? tok_pos[tok - tok0] : p_base + tok;
     // The warp's rows are copied to their places as they are, D / 8 lanes a
     // row, then each thread scales its own.
     const unsigned long long mine = reinterpret_cast<unsigned long long>(
@@ -543,8 +629,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     fence_proxy_async_smem();
   }
   // positions of the block's last rows of tile 0 and first rows of tile 1
-  const int p_end0 = p_base + kv_token(a, r0 + (rows < kPRows ? rows : kPRows) - 1);
-  const int p_beg1 = kSplit ? p_first : p_base + kv_token(a, r0 + kPRows);
+  const int p_end0 = kMode == kKvPrefix
+                         ? p_last
+                         : p_base + kv_token(a, r0 + (rows < kPRows ? rows : kPRows) - 1);
+  const int p_beg1 =
+      kSplit || kMode == kKvPrefix ? p_first : p_base + kv_token(a, r0 + kPRows);
 
   // columns of tile i's scores (and weights) of its page n
   auto s_col = [](int i, int n) -> uint32_t { return L::kSCol + i * 128 + (n & 1) * kBlk; };
@@ -882,7 +971,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (kSplit) cta_barrier();  // no converted page is read any more
   // A part: O in chunks of four elements, [D / 4][rows], then (ref, sum).
   constexpr size_t kPart = 2 * kPRows * (D + 2);
-  const OutRows<D> put{a, smem + L::kQOff, r0, sq.row0, hk};
+  const OutRows<D, kMode == kKvPrefix> put{a, smem + L::kQOff, r0, sq.row0, hk, tok_pos};
   int out0 = 0, out1 = 0;  // the staged rows that this warp writes
   if (soft) {
     const bool mine_out = !(kSplit && qt);  // (tile 0 writes for both)
@@ -909,6 +998,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
       inv1 = all == 0.f ? 0.f : w1 / all;
       ref = top;
       sum = all;
+    }
+    // kKvPrefix, one part: the own tokens' share of the result
+    float own_f = 0.f;
+    const float* own = nullptr;
+    if constexpr (kMode == kKvPrefix) {
+      if (mine_out && live && parts == 1) {
+        own = a.own + put.row(r) * D;
+        const float w0 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+        const float w1 = own_weight(a, put.row(r));
+        const float top = fmaxf(w0, w1), base = top == -INFINITY ? 0.f : top;
+        const float l0 = exp2f(w0 - base), l1 = exp2f(w1 - base), all = l0 + l1;
+        const float one = all == 0.f ? 0.f : 1.0f / all;
+        inv *= l0 * one;
+        inv1 *= l0 * one;
+        own_f = l1 * one;
+        ref = base;
+        sum = all;
+      }
     }
 #pragma unroll 2
     for (int q = 0; q < D / 16; ++q) {
@@ -938,11 +1045,27 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       if (!mine_out) {
+      } else if (kMode == kKvOwn && live && parts == 1) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + put.row(r) * D + 16 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       } else if (live && parts == 1) {
+        if constexpr (kMode == kKvPrefix) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(own + 16 * q) + k);
+            f[4 * k] = fmaf(own_f, v.x, f[4 * k]);
+            f[4 * k + 1] = fmaf(own_f, v.y, f[4 * k + 1]);
+            f[4 * k + 2] = fmaf(own_f, v.z, f[4 * k + 2]);
+            f[4 * k + 3] = fmaf(own_f, v.w, f[4 * k + 3]);
+          }
+        }
         uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
         if (kSplit) {  // (few rows: straight to their places)
+          if (!put.written(r)) continue;
           uint4* o =
               reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + put.row(r) * D + 16 * q);
           o[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -958,7 +1081,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           o[k * (2 * kPRows)] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
-    if (!kSplit && parts == 1) {
+    if (!kSplit && kMode != kKvOwn && parts == 1) {
       out0 = r - lane;
       out1 = rows < out0 + 32 ? rows : out0 + 32;
     }
@@ -968,7 +1091,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (mine_out && live && parts > 1)
       reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
-    if (mine_out && live && parts == 1 && a.lse) a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
+    if (mine_out && live && parts == 1 && a.lse && put.written(r))
+      a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
   }
   __syncwarp();
   if (parts > 1) {
@@ -980,12 +1104,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
     cta_barrier();
     if (*is_last) {
       if (threadIdx.x == 0) tickets[item - whole] = 0;
-      join_parts<D>(a, smem, partials + static_cast<size_t>(item - whole) * tail_parts * kPart, parts,
-                    rows, r0, sq.row0, hk);
+      join_parts<D, kMode>(a, smem,
+                           partials + static_cast<size_t>(item - whole) * tail_parts * kPart, parts,
+                           rows, put);
       cta_barrier();
       static_assert(kPThreads / 32 * 16 == 2 * kPRows, "rows of a warp");
-      out0 = 16 * warp;
-      out1 = rows < out0 + 16 ? rows : out0 + 16;
+      if (kMode != kKvOwn) {
+        out0 = 16 * warp;
+        out1 = rows < out0 + 16 ? rows : out0 + 16;
+      }
     }
   }
   __syncwarp();
@@ -1017,17 +1144,27 @@ cudaError_t kv8_prompt_set_attributes() {
   const auto allow = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = allow(kv8_prompt_kernel<64, false>, PL<64>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<64, true>, PL<64>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, false>, PL<128>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, true>, PL<128>::kAlloc);
+  cudaError_t e = cudaSuccess;
+#define TERN_PROMPT_ATTR(MODE)                                                               \
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<64, false, MODE>, PL<64>::kAlloc);       \
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<64, true, MODE>, PL<64>::kAlloc);        \
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, false, MODE>, PL<128>::kAlloc);     \
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, true, MODE>, PL<128>::kAlloc);
+  TERN_PROMPT_ATTR(kKvWhole)
+  TERN_PROMPT_ATTR(kKvOwn)
+  TERN_PROMPT_ATTR(kKvPrefix)
+#undef TERN_PROMPT_ATTR
   return e;
 }
 
-cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, int* tickets,
-                              int num_sms, cudaStream_t stream, int* launches) {
-  const long long most = static_cast<long long>(a.max_new) * a.group;
-  const long long row_blocks = row_blocks_of(a.max_new, a.group);
+cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches) {
+  const bool prefix = mode == kKvPrefix;
+  const int longest = prefix ? a.rows : a.max_new;  // tokens of a "sequence"
+  const int seqs = prefix ? 1 : a.seqs;
+  const int width = prefix ? a.shared / kBlk : a.width - a.shared / kBlk;  // its pages
+  const long long most = static_cast<long long>(longest) * a.group;
+  const long long row_blocks = row_blocks_of(longest, a.group);
   // Whole waves of items run as they are.  The keys of the items left (the
   // earliest rows, the last to start) are cut into parts so that they end
   // together: as many as cost the least pages of time in sequence on an SM (at
@@ -1035,18 +1172,19 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
   // Measured when it came, with the cut and without (2048 tokens of 6 heads over
   // 8190, 384 items on 152 SMs): 316 and 328 us; 4096 tokens over 16384: 1106 and
   // 1227 us.
-  const long long items = row_blocks * a.hkv * a.seqs;
+  const long long items = row_blocks * a.hkv * seqs;
   const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   const long long tail = items % sms, whole = items - tail;
-  unsigned parts = 1, best = a.width;
-  // (the join holds a weight per part and row in the converted pages' place)
+  unsigned parts = 1, best = width;
+  // (the join holds a weight per part, the own tokens' among them, and row in the
+  // converted pages' place)
   const long long rows32 = most < 2 * kPRows ? (most + 31) / 32 * 32 : 2 * kPRows;
-  const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32;
+  const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32 - (prefix ? 1 : 0);
   static_assert(PL<64>::kConv * PL<64>::kTileB <= PL<128>::kConv * PL<128>::kTileB, "room");
-  for (unsigned p = 2; p * tail <= 2 * sms && p <= static_cast<unsigned>(a.width) / kPartPages &&
+  for (unsigned p = 2; p * tail <= 2 * sms && p <= static_cast<unsigned>(width) / kPartPages &&
                        p <= room;
        ++p) {
-    const unsigned cost = part_cost(a.width, p, static_cast<unsigned>(tail),
+    const unsigned cost = part_cost(width, p, static_cast<unsigned>(tail),
                                     static_cast<unsigned>(sms));
     if (cost < best) best = cost, parts = p;
   }
@@ -1055,10 +1193,20 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, int min_rows, float* partials, i
   const cudaLaunchConfig_t cfg =
       pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)), dim3(kPThreads),
                         a.dim == 128 ? PL<128>::kAlloc : PL<64>::kAlloc, stream);
-  const auto kernel = most <= kSplitRows
-                          ? (a.dim == 128 ? kv8_prompt_kernel<128, true> : kv8_prompt_kernel<64, true>)
-                          : (a.dim == 128 ? kv8_prompt_kernel<128, false>
-                                          : kv8_prompt_kernel<64, false>);
+  auto kernel = kv8_prompt_kernel<128, false, kKvWhole>;
+#define TERN_PROMPT_CASE(D, SPLIT, MODE)                                 \
+  if (a.dim == D && (most <= kSplitRows) == SPLIT && mode == MODE)       \
+    kernel = kv8_prompt_kernel<D, SPLIT, MODE>;
+#define TERN_PROMPT_CASES(MODE)      \
+  TERN_PROMPT_CASE(64, false, MODE)  \
+  TERN_PROMPT_CASE(64, true, MODE)   \
+  TERN_PROMPT_CASE(128, false, MODE) \
+  TERN_PROMPT_CASE(128, true, MODE)
+  TERN_PROMPT_CASES(kKvWhole)
+  TERN_PROMPT_CASES(kKvOwn)
+  TERN_PROMPT_CASES(kKvPrefix)
+#undef TERN_PROMPT_CASES
+#undef TERN_PROMPT_CASE
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, min_rows, static_cast<int>(row_blocks),
                                            static_cast<int>(whole), static_cast<int>(parts),
                                            static_cast<int>(tail), static_cast<int>(sms),

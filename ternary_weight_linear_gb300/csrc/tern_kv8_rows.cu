@@ -438,7 +438,11 @@ __device__ __forceinline__ FarRow<D> far_row(const Kv8Args& a, const uint8_t* qu
   return f;
 }
 
-template <int D, int NT>
+// kOwn: the part of the tokens behind a shared prefix (positions, pages and
+// lengths are those behind it), fp32 and with its log-sum-exp, for the launch
+// after it to join.  That launch does not wait for all of this one before it
+// begins, so it may begin once what came before this one is done.
+template <int D, int NT, bool kOwn>
 __global__ void __launch_bounds__(kRW * 32, 1)
     kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, int max_rows,
                     int per_head) {
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // (three tiles read their queries from shared memory at each half-page)
   constexpr bool kQRegs = NT < 3;
   constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
-  grid_dependents_launch();
+  if (!kOwn) grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -478,6 +482,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     prefetch_tensormap(&tm);
   }
   grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
+  if (kOwn) grid_dependents_launch();
 
   // ---- the launch's units: (sequence, head, page), pages fastest
   for (int b = threadIdx.x; b < a.seqs; b += kRW * 32) {
@@ -910,7 +915,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           const int2 at = row_of(r);
           const long long ob = static_cast<long long>(at.x) * a.heads + at.y;
           uint16_t* out = static_cast<uint16_t*>(a.out) + ob * D + d;
-          if constexpr (kDT == 2)
+          if constexpr (kOwn) {
+#pragma unroll
+            for (int y = 0; y < kDT; ++y) static_cast<float*>(a.out)[ob * D + d + y] = acc[y];
+          } else if constexpr (kDT == 2)
             *reinterpret_cast<uint32_t*>(out) = pack_out(a.type, acc[0], acc[1]);
           else
             *out = static_cast<uint16_t>(pack_out(a.type, acc[0], 0.f));
@@ -949,7 +957,9 @@ __global__ void __launch_bounds__(kRW * 32, 1)
 #pragma unroll
         for (int y = 0; y < D / 32; ++y) {
           const float x = to[y] * f0 + f.o[y] * f1;
-          if (whole)
+          if (whole && kOwn)
+            static_cast<float*>(a.out)[ob * D + lane * (D / 32) + y] = x;
+          else if (whole)
             static_cast<uint16_t*>(a.out)[ob * D + lane * (D / 32) + y] =
                 static_cast<uint16_t>(pack_out(a.type, x, 0.f));
           else
@@ -1036,8 +1046,13 @@ __global__ void __launch_bounds__(kRW * 32, 1)
           uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + ob * D) +
                           lane * (kV / 2);
 #pragma unroll
-          for (int y = 0; y < kV; y += 2)
-            out[y / 2] = pack_out(a.type, acc[y] * inv, acc[y + 1] * inv);
+          for (int y = 0; y < kV; y += 2) {
+            if (kOwn)
+              reinterpret_cast<float2*>(static_cast<float*>(a.out) + ob * D)[(lane * kV + y) / 2] =
+                  make_float2(acc[y] * inv, acc[y + 1] * inv);
+            else
+              out[y / 2] = pack_out(a.type, acc[y] * inv, acc[y + 1] * inv);
+          }
           if (a.lse && lane == 0) a.lse[ob] = kv_log_sum(top, l, kROff);
         }
       }
@@ -1056,7 +1071,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     if (!mbar_wait_clk(&full[used % L::kStages], (used / L::kStages) & 1, a.err)) break;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kOwn>
 cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
                        cudaStream_t stream, int* launches) {
   cudaLaunchAttribute attr[1];
@@ -1069,7 +1084,7 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
     const int grid = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
     const cudaLaunchConfig_t cfg =
         pdl_launch_config(attr, dim3(grid), dim3(kRW * 32), RL<D, NT>::kAlloc, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_rows_kernel<D, NT>, *tm, p, max_rows,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_rows_kernel<D, NT, kOwn>, *tm, p, max_rows,
                                              a.seqs == 1 ? grid / a.hkv : 0);
     if (e != cudaSuccess) return e;
     ++*launches;
@@ -1089,25 +1104,37 @@ cudaError_t kv8_rows_set_attributes() {
   const auto allow = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = allow(kv8_rows_kernel<64, 1>, RL<64, 1>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_rows_kernel<64, 2>, RL<64, 2>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_rows_kernel<64, 3>, RL<64, 3>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 3>, RL<128, 3>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 1>, RL<128, 1>::kAlloc);
-  if (e == cudaSuccess) e = allow(kv8_rows_kernel<128, 2>, RL<128, 2>::kAlloc);
+  cudaError_t e = cudaSuccess;
+#define TERN_ROWS_ATTR(D, NT)                                                                 \
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<D, NT, false>, RL<D, NT>::kAlloc);          \
+  if (e == cudaSuccess) e = allow(kv8_rows_kernel<D, NT, true>, RL<D, NT>::kAlloc);
+  TERN_ROWS_ATTR(64, 1)
+  TERN_ROWS_ATTR(64, 2)
+  TERN_ROWS_ATTR(64, 3)
+  TERN_ROWS_ATTR(128, 1)
+  TERN_ROWS_ATTR(128, 2)
+  TERN_ROWS_ATTR(128, 3)
+#undef TERN_ROWS_ATTR
   return e;
 }
 
-cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
-                            cudaStream_t stream, int* launches) {
+template <bool kOwn>
+static cudaError_t launch_tiles(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
+                                cudaStream_t stream, int* launches) {
   // as many tiles of rows as the largest of the kernel's sequences can have
   const long long most = static_cast<long long>(a.max_new) * a.group;
   const int tiles = static_cast<int>(((most < max_rows ? most : max_rows) + 7) / 8);
   const bool wide = a.dim == 128;
-  const auto launch = tiles == 1   ? (wide ? launch_one<128, 1> : launch_one<64, 1>)
-                      : tiles == 2 ? (wide ? launch_one<128, 2> : launch_one<64, 2>)
-                                   : (wide ? launch_one<128, 3> : launch_one<64, 3>);
+  const auto launch = tiles == 1   ? (wide ? launch_one<128, 1, kOwn> : launch_one<64, 1, kOwn>)
+                      : tiles == 2 ? (wide ? launch_one<128, 2, kOwn> : launch_one<64, 2, kOwn>)
+                                   : (wide ? launch_one<128, 3, kOwn> : launch_one<64, 3, kOwn>);
   return launch(tm, a, max_rows, num_sms, stream, launches);
+}
+
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, Kv8Mode mode, int max_rows,
+                            int num_sms, cudaStream_t stream, int* launches) {
+  return mode == kKvOwn ? launch_tiles<true>(tm, a, max_rows, num_sms, stream, launches)
+                        : launch_tiles<false>(tm, a, max_rows, num_sms, stream, launches);
 }
 
 }  // namespace tern

@@ -95,3 +95,27 @@ def test_norms_alignment():
                 dict(w=P + 8), dict(q=P + 8), dict(s=P + 4), dict(y=P + 8), dict(ld=258),
                 dict(gld=260)):
         assert norms(**bad) == EALIGN
+
+
+def shared(n=64, c=None, rows=2, heads=8, max_new=1, ws=1 << 40, scale=0.125, q=P, out=P, ld=1024):
+    return tl.load().tern_kv8_attention_shared(c or cache(), q, 1, ld, 128, rows, heads, n, max_new,
+                                               0, 0, scale, out, None, P, ws, None)
+
+
+@pytest.mark.parametrize("bad", [dict(n=-64), dict(n=1), dict(n=63), dict(n=320), dict(heads=12),
+                                 dict(rows=-1), dict(max_new=0), dict(scale=NAN), dict(q=None),
+                                 dict(out=None), dict(ld=64), dict(c=cache(dim=96)),
+                                 dict(c=cache(kv_heads=16384, width=64), rows=1 << 25,
+                                      heads=16384)])
+def test_shared_attention_refuses(bad):
+    assert shared(**bad) == EINVAL
+
+
+def test_shared_attention_workspace():
+    need = tl.tern_kv8_attention_shared_workspace_bytes(2, 2, 8, 8, 128)
+    plain = tl.tern_kv8_attention_workspace_bytes(2, 2, 8, 8, 128)
+    assert need > plain + 2 * 8 * 129 * 4
+    assert shared(ws=need - 1) == -3 and shared(ws=plain) == -3
+    assert shared(rows=0, max_new=0, ws=0) == 0 and shared(q=P + 2) == EALIGN
+    for bad in ((0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 1, 12, 8, 128), (1, 1, 8, 8, 96)):
+        assert tl.tern_kv8_attention_shared_workspace_bytes(*bad) == 0

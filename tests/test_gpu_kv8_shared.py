@@ -1,0 +1,329 @@
+"""GPU parity of tern_kv8_attention_shared against the fp64 oracle of the
+attention over each sequence's whole table (oracle/decoder.py).
+
+Bar: that of test_gpu_kv8_attention.py.  The join of the prefix's and the own
+tokens' parts adds to it only what fp32 log-sum-exps round: at most 3 * 2^-24 of
+a log-sum-exp below 64 in size, 2^-16 of a part's weight, which the 5 * 2^-11
+there (4.5 of them in use) covers.
+"""
+import numpy as np
+import pytest
+
+from oracle import decoder as od
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tl():
+    import torch
+    import ternary_weight_linear_gb300 as tl
+    tl.build()
+    tl.load()
+    torch.cuda.init()
+    return tl
+
+
+class Case:
+    """A batch whose sequences begin with the same pages.  own, new: tokens of
+    each sequence behind the shared ones, and how many of them are new (own None:
+    an empty sequence).  Rubbish in unused table entries, stale codes past the
+    last token, NaN scales in unused pages; `gap` rows of no sequence before the
+    first and behind the last."""
+
+    def __init__(self, shared, own, new, heads, kv_heads, dim, dtype="bfloat16", seed=0, spread=0.3,
+                 q_scale=1.0, gap=0):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.shared, self.heads, self.dim = shared, heads, dim
+        self.lens = np.array([0 if n is None else shared + n for n in own], np.int32)
+        self.start = (gap + np.concatenate([[0], np.cumsum(new)])).astype(np.int32)
+        common = shared // 64
+        each = [0 if n is None else (n + 63) // 64 for n in own]
+        pages = common + sum(each) + 2
+        order = rng.permutation(pages).astype(np.int32)
+        self.table = np.full((len(own), common + max(1, max(each)) + 1), -5, np.int32)
+        self.table[:, :common] = order[:common]
+        at = common
+        for b, e in enumerate(each):
+            self.table[b, common:common + e] = order[at:at + e]
+            at += e
+        self.codes = np.clip(np.rint(rng.standard_normal((pages, 2, kv_heads, 64, dim)) * 40), -127,
+                             127).astype(np.int8)
+        self.scales = (0.02 * np.exp(spread * rng.standard_normal((pages, 2, kv_heads)))).astype(
+            np.float32)
+        self.scales[order[at:]] = np.nan
+        self.rows = int(self.start[-1]) + gap
+        self.q_dev = (torch.from_numpy(rng.standard_normal((self.rows, heads, dim)).astype(
+            np.float32)) * q_scale).cuda().to(getattr(torch, dtype))
+        self.max_new = int(max(new))
+
+    def args(self):
+        import torch
+        return [torch.from_numpy(np.ascontiguousarray(a)).cuda()
+                for a in (self.codes, self.scales, self.table, self.start, self.lens)]
+
+    def run(self, tl, window=0, sinks=0, scale=None, q=None, **kw):
+        kw.setdefault("max_new", self.max_new)
+        return tl.tern_kv8_attention_shared(self.q_dev if q is None else q, *self.args(),
+                                            self.shared, window=window, sinks=sinks,
+                                            softmax_scale=scale, **kw)
+
+    def check(self, tl, window=0, sinks=0, scale=None, status=0, skipped=(), **kw):
+        import torch
+        lse = torch.full((self.rows, self.heads), 7.0, device="cuda")
+        out = torch.full((self.rows, self.heads, self.dim), 9.0, dtype=self.q_dev.dtype,
+                         device="cuda")
+        self.run(tl, window, sinks, scale, lse=lse, out=out, **kw)
+        torch.cuda.synchronize()
+        assert tl.tern_device_status() == status
+        lens, start = self.lens.copy(), self.start
+        live = np.zeros(self.rows, bool)
+        for b in range(len(lens)):
+            if b not in skipped:
+                live[start[b]:start[b + 1]] = True
+        q = self.q_dev.double().cpu().numpy()
+        ref, ref_lse, absum = od.kv8_attention(q, self.codes, self.scales, self.table, start,
+                                               np.where(np.isin(np.arange(len(lens)), skipped),
+                                                        np.maximum(np.diff(start), 1), lens),
+                                               window, sinks,
+                                               self.dim ** -0.5 if scale is None else scale)
+        got = out.double().cpu().numpy()
+        assert np.all(got[~live] == 9) and np.all(lse.cpu().numpy()[~live] == 7)
+        bound = 5 * 2.0 ** -11 * absum + 2.0 ** -9 * np.abs(ref) + 2.0 ** -25
+        err = np.abs(got - ref)
+        bad = ~(err <= bound) & live[:, None, None]
+        assert not bad.any(), (int(bad.sum()), float(np.max((err / bound)[live])),
+                               np.argwhere(bad)[:4].tolist())
+        ll = lse.cpu().numpy()[live]
+        ref_lse = ref_lse[live]
+        none = np.isneginf(ref_lse)
+        assert np.array_equal(np.isneginf(ll), none)
+        assert np.all(np.abs(ll[~none] - ref_lse[~none]) <= 2.5 * 2.0 ** -11)
+        return out, lse
+
+
+OWN = [1, 63, 64, 65, None, 200, 130, 77]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(4, 4), (6, 1), (16, 2), (20, 1)])
+@pytest.mark.parametrize("m", [1, 3])
+@pytest.mark.parametrize("shared", [64, 1088])
+def test_few_rows(tl, dim, heads, kv, m, shared):
+    new = [0 if n is None else min(m, n) for n in OWN]
+    new[-1] = 0
+    Case(shared, OWN, new, heads, kv, dim, seed=heads + m).check(tl)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seqs,m,group", [(2, 1, 1), (9, 1, 7), (11, 1, 6), (21, 1, 6), (22, 2, 6),
+                                          (43, 1, 6), (130, 1, 4), (300, 1, 2)])
+def test_rows_of_the_batch(tl, dim, seqs, m, group):
+    """Rows per key-value head on both sides of 64, 128 and 256, several blocks
+    of them, more sequences than a launch of the few-row kernel takes."""
+    own = [m + (17 * b) % 90 for b in range(seqs)]
+    Case(704, own, [m] * seqs, 2 * group, 2, dim, seed=seqs).check(tl)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shared", [64 * 7, 64 * 8, 64 * 33, 64 * 150])
+def test_lengths_of_the_prefix(tl, dim, shared):
+    """Too short to be cut, cut in parts of different lengths, long."""
+    Case(shared, [5, 70, 9], [1, 1, 2], 12, 2, dim, seed=shared).check(tl)
+    Case(shared, [30] * 20, [2] * 20, 8, 1, dim, seed=shared).check(tl)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[6, 4, 1], [20, 1, 0], [100, 7, 1], [300, 280, 1]])
+def test_verify_steps_and_prompt_chunks(tl, dim, new):
+    """Rows of a sequence for the few-row kernel, the split and the plain form of
+    the one on the tensor cores, and mixed."""
+    Case(640, [m + 90 for m in new], new, 12, 2, dim, seed=new[0]).check(tl)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (130, 7), (400, 64), (600, 100),
+                                          (900, 65), (100, 2000), (5000, 3)])
+def test_windows(tl, dim, window, sinks):
+    """From windows within the own tokens (no prefix token seen, or its sinks
+    alone) to ones that reach over all of it."""
+    Case(640, [40, 3, 150, 300], [2, 1, 3, 1], 12, 2, dim, seed=window).check(tl, window, sinks)
+    own = [200 + 9 * b for b in range(25)]
+    Case(640, own, [2] * 25, 12, 2, dim, seed=window).check(tl, window, sinks)
+
+
+def test_windows_over_a_cut_prefix(tl):
+    Case(64 * 60, [40, 800, 70], [1, 2, 1], 12, 2, 128, seed=1).check(tl, 2000, 70)
+    Case(64 * 60, [40 + b for b in range(40)], [2] * 40, 12, 2, 64, seed=2).check(tl, 1500, 129)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_types_and_strides(tl, dtype):
+    """Queries within a projection's rows."""
+    import torch
+    c = Case(256, [9, 30, 64], [3, 1, 2], 8, 2, 64, dtype, seed=3)
+    wide = torch.zeros(c.rows, 12, 64, dtype=c.q_dev.dtype, device="cuda")
+    wide[:, 2:10] = c.q_dev
+    out, lse = c.check(tl)
+    out2, lse2 = c.check(tl, q=wide[:, 2:10])
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("seqs", [4, 30])
+def test_rows_of_no_sequence_are_left(tl, seqs):
+    Case(320, [20] * seqs, [2] * seqs, 8, 1, 128, gap=5, seed=4).check(tl)
+    Case(64 * 40, [20] * seqs, [2] * seqs, 8, 1, 64, gap=37, seed=4).check(tl)
+
+
+@pytest.mark.parametrize("shared", [192, 64 * 40])
+@pytest.mark.parametrize("seqs", [5, 30])
+def test_inconsistent_sequences_are_skipped(tl, shared, seqs):
+    """One whose new tokens reach into the prefix, one too long for its table."""
+    c = Case(shared, [20] * seqs, [2] * seqs, 8, 1, 64, seed=5)
+    c.lens[1] = shared + 1
+    c.lens[3] = 10 ** 6
+    c.check(tl, status=-7, skipped=[1, 3])
+    c = Case(shared, [20] * seqs, [2] * seqs, 8, 1, 64, seed=5)
+    c.lens[:] = 3
+    c.check(tl, status=-7, skipped=list(range(seqs)))
+
+
+def test_a_lone_sequence(tl):
+    Case(256, [30], [2], 8, 2, 64, seed=6).check(tl)
+    c = Case(256, [30], [2], 8, 2, 64, seed=6)
+    c.lens[0] = 257
+    c.check(tl, status=-7, skipped=[0])
+    Case(0, [30, 5, 100], [2, 1, 1], 8, 2, 64, seed=6).check(tl)
+
+
+def test_first_sequence_without_tokens(tl):
+    """Its row of the table still names the shared pages."""
+    Case(320, [None, 30, 5], [0, 2, 1], 8, 2, 64, seed=7).check(tl)
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+def test_bad_pages(tl, seqs):
+    """Out of range: masked and reported."""
+    c = Case(64 * 20, [20] * seqs, [2] * seqs, 8, 2, 64, seed=8)
+    c.table[:, 3] = 10 ** 6
+    c.table[:, 19] = -1
+    c.table[2, 20] = 10 ** 6  # the third sequence's own tokens, all of them
+    c.check(tl, status=-7)
+    c.table[:, :20] = -1  # nothing left of the prefix
+    c.check(tl, status=-7)
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+def test_scales_that_cannot_be_used(tl, seqs):
+    """A NaN block of the prefix: its head's rows that see it, and only they."""
+    import torch
+    c = Case(64 * 20, [400 + b for b in range(seqs)], [1] * seqs, 8, 2, 64, seed=9)
+    c.scales[c.table[0, 4], 1, 1] = np.nan
+    out = c.run(tl)
+    assert torch.isnan(out[:, 4:]).all() and torch.isfinite(out[:, :4]).all()
+    out = c.run(tl, window=1370)  # (page 4 is seen by the shorter ones alone)
+    low = torch.from_numpy(c.lens - 1370).cuda() < 320
+    assert torch.isnan(out[low][:, 4:]).all() and torch.isfinite(out[~low]).all()
+    assert torch.isfinite(out[:, :4]).all()
+    # and one of a sequence's own
+    c = Case(64 * 20, [40] * seqs, [1] * seqs, 8, 2, 64, seed=9)
+    c.scales[c.table[1, 20], 0, 0] = -1.0
+    out = c.run(tl)
+    assert torch.isnan(out[1, :4]).all() and torch.isfinite(out[1, 4:]).all()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_value_scales_far_apart(tl, seqs, dim):
+    c = Case(64 * 30, [90] * seqs, [1] * seqs, 12, 2, dim, seed=10)
+    rng = np.random.default_rng(0)
+    c.scales[:, 1] *= (2.0 ** rng.integers(-20, 20, c.scales[:, 1].shape)).astype(np.float32)
+    c.check(tl)
+    c.scales[c.table[0, 5], 1] = 1e-20
+    c.scales[c.table[1, 30], 1] = 0
+    c.scales[c.table[2, 30], 1] = 1e-20
+    c.check(tl)
+
+
+def test_parts_of_very_different_weight(tl):
+    """All of the softmax in the prefix, or all of it in the own tokens."""
+    for big in (0, 1):
+        c = Case(64 * 20, [40, 70, 64], [1, 1, 1], 12, 2, 128, seed=11)
+        common = c.table[0, :20]
+        rest = np.setdiff1d(np.arange(len(c.scales)), common)
+        c.scales[(common, rest)[big], 0] *= 8
+        c.check(tl)
+
+
+def test_same_bits_as_before_and_the_workspace(tl):
+    """Call after call, with a workspace of its own or one kept, and after other
+    shapes have used it."""
+    import torch
+    cases = [Case(64 * 40, [40 + b for b in range(n)], [2] * n, 12, 2, 128, seed=12)
+             for n in (3, 40)]
+    need = max(tl.tern_kv8_attention_shared_workspace_bytes(len(c.lens), c.rows, 12, 2, 128)
+               for c in cases)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    first = [c.run(tl) for c in cases]
+    for _ in range(3):
+        for c, want in zip(cases, first):
+            assert torch.equal(c.run(tl, workspace=ws), want)
+    assert not ws[:tl.SYNC_BYTES].any()
+    assert tl.tern_device_status() == 0
+
+
+def test_max_new_left_out(tl):
+    c = Case(64 * 20, [40, 70, 64], [3, 1, 1], 12, 2, 64, seed=13)
+    c.check(tl, max_new=None)
+
+
+def test_captured_and_replayed_with_other_contents(tl):
+    """Two graphs with workspaces of their own, replayed side by side on two
+    streams, their lengths, tables and queries changed in between."""
+    import torch
+    cs = [Case(64 * 24, [100 + b for b in range(n)], [1] * n, 12, 2, 128, seed=n) for n in (4, 30)]
+    held, graphs = [], []
+    for c in cs:
+        args = c.args()
+        ws = torch.zeros(tl.tern_kv8_attention_shared_workspace_bytes(len(c.lens), c.rows, 12, 2,
+                                                                      128),
+                         dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(c.q_dev)
+        q = c.q_dev.clone()
+        call = lambda a=args, q=q, o=out, w=ws, s=c.shared: tl.tern_kv8_attention_shared(  # noqa: E731
+            q, *a, s, max_new=1, out=o, workspace=w)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        held.append((args, q, out, ws))  # (what the graph's launches point to lives as long)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for step in range(4):
+        wants = []
+        for c, (args, q, _, _) in zip(cs, held):
+            c.lens = (c.lens - 7 * (step > 0)).astype(np.int32)
+            c.q_dev = torch.randn_like(c.q_dev)
+            args[4].copy_(torch.from_numpy(c.lens))
+            q.copy_(c.q_dev)
+            wants.append(c.run(tl))
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for want, (_, _, out, _) in zip(wants, held):
+            assert torch.equal(out, want)
+    assert tl.tern_device_status() == 0
+
+
+def test_refusals_of_the_binding(tl):
+    c = Case(128, [20, 30], [1, 1], 8, 2, 64, seed=14)
+    for shared in (-64, 100, 64 * 1000, 2 ** 40):
+        c.shared = shared
+        with pytest.raises(tl.TernError):
+            c.run(tl)
