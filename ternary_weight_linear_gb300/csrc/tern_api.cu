@@ -339,11 +339,9 @@ bool kv8_strides_ok(long long ld, long long hd, int dim) {
 }
 
 // Tickets of the tensor-core attention in the synchronisation area, behind the
-// few-row kernel's, and of the shared prefix's launch.
-constexpr int kPromptTickets = 512, kPrefixTickets = 768;
-static_assert((kPrefixTickets + kSmallTMaxCtas) * sizeof(int) <= kSyncBytes &&
-                  kPromptTickets + kSmallTMaxCtas <= kPrefixTickets,
-              "sync area");
+// few-row kernel's.
+constexpr int kPromptTickets = 512;
+static_assert((kPromptTickets + kSmallTMaxCtas) * sizeof(int) <= kSyncBytes, "sync area");
 
 // The attention's arguments, but for what belongs to the workspace and the
 // device.
@@ -919,7 +917,7 @@ size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads, 
                                                  int head_dim) {
   const size_t n = tern_kv8_attention_workspace_bytes(seqs, rows, heads, kv_heads, head_dim);
   return n == 0 ? 0 : align_up(n, 256) + own_bytes(rows, heads, head_dim) +
-                          kv8_prompt_partial_bytes(head_dim);
+                          kv8_prefix_partial_bytes(rows, heads / kv_heads, kv_heads, head_dim);
 }
 
 int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type, long long ld,
@@ -950,26 +948,27 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
   if (a.seqs == 1 || shared == 0) {
     rc = run_kv8_attention(&a, kKvWhole, ws, d, st, &launches);
   } else {
-    // the own tokens' part in fp32, then the prefix's, which joins them
+    // the prefix's part, the own tokens' in fp32 beside it, and their join
     float* o = reinterpret_cast<float*>(ws + base);
     float* l = o + static_cast<size_t>(rows) * heads * a.dim;
+    float* parts = reinterpret_cast<float*>(ws + base + own_bytes(rows, heads, a.dim));
     Kv8Args own = a;
     own.shared = shared;
     own.table += shared / TERN_KV8_BLOCK;
     own.sinks = a.sinks > shared ? a.sinks - shared : 0;
     own.out = o;
     own.lse = l;
-    rc = run_kv8_attention(&own, kKvOwn, ws, d, st, &launches);
-    if (rc != TERN_OK) return rc;
     a.err = d->err;
     a.shared = shared;
     a.own = o;
     a.own_lse = l;
-    if (launch_kv8_prompt(a, kKvPrefix, 1,
-                          reinterpret_cast<float*>(ws + base + own_bytes(rows, heads, a.dim)),
-                          static_cast<int*>(workspace) + kPrefixTickets, d->sms, st,
-                          &launches) != cudaSuccess)
-      rc = TERN_ECUDA;
+    int cut = 0;
+    if (launch_kv8_prompt(a, kKvPrefix, 1, parts, nullptr, d->sms, st, &launches, &cut) !=
+        cudaSuccess)
+      return TERN_ECUDA;
+    rc = run_kv8_attention(&own, kKvOwn, ws, d, st, &launches);
+    if (rc != TERN_OK) return rc;
+    if (launch_kv8_join(a, cut, parts, st, &launches) != cudaSuccess) return TERN_ECUDA;
   }
   if (rc == TERN_OK) t_last_launches = launches;
   return rc;

@@ -268,7 +268,7 @@ struct Kv8Args {
 };
 // What an attention kernel computes: a call's result; the part of it that comes
 // from the tokens behind a shared prefix, in fp32; or the prefix's part for all
-// rows of the batch, joined with the former.
+// rows of the batch.
 enum Kv8Mode : int { kKvWhole, kKvOwn, kKvPrefix };
 // n / group = (high half of n * mul + n) >> shift for n < 2^31: with shift =
 // ceil(log2 group), mul = floor(2^32 (2^shift - group) / group) + 1.
@@ -313,6 +313,8 @@ constexpr int kKvFewRowsLong = 24, kKvLongPages = 40;
 constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
 size_t kv8_rows_partial_bytes(int dim);
 cudaError_t kv8_rows_set_attributes();
+// kKvOwn: the first launch begins beside the one before it (the prefix's), which
+// begins its dependents when what came before it is done.
 cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, Kv8Mode mode, int max_rows,
                             int num_sms, cudaStream_t stream, int* launches);
 
@@ -323,7 +325,13 @@ cudaError_t kv8_prompt_set_attributes();
 // Whether the kernel's grid holds the blocks of rows of such a call.
 bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs);
 cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
-                              int* tickets, int num_sms, cudaStream_t stream, int* launches);
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches,
+                              int* cut = nullptr);
+// kKvPrefix: *cut is the number of parts of each block of rows, which partials
+// then holds for the join.
+size_t kv8_prefix_partial_bytes(int rows, int group, int kv_heads, int dim);
+cudaError_t launch_kv8_join(const Kv8Args& a, int parts, const float* partials,
+                            cudaStream_t stream, int* launches);
 
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier
 // phase nobody completes; 1: a device counter nobody raises) and records the

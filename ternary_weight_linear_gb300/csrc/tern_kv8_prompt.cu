@@ -66,6 +66,7 @@ __host__ __device__ constexpr unsigned part_cost(unsigned pages, unsigned parts,
   return (items * parts + sms - 1) / sms * ((pages + parts - 1) / parts + kPartCost);
 }
 constexpr float kUp = 16777216.f;  // 2^24, 1 over the keys' unit
+constexpr float kNoRow = -1.f;     // in a sum's place: a row of no sequence
 
 template <int D>
 struct PL {
@@ -162,14 +163,11 @@ __device__ __forceinline__ void cta_barrier() {
 // A block's rows of the output, staged in shared memory where the queries were
 // (a warp's own rows, whose products are done): chunks of 16 bytes swizzled by
 // the row, written D / 8 lanes a row.
-// kPrefix: rows of skipped sequences, and of none, stay as they are (pos: the
-// tokens' positions from the block's first, negative for such).
-template <int D, bool kPrefix>
+template <int D>
 struct OutRows {
   const Kv8Args& a;
   uint8_t* stage;
   int r0, row0, hk;
-  const int* pos;
   __device__ __forceinline__ uint8_t* staged(int row, int c) const {
     return stage + row * (2 * D) + ((c ^ (row & 7)) << 4);
   }
@@ -178,17 +176,13 @@ struct OutRows {
     return static_cast<long long>(row0 + tok) * a.heads + hk * a.group +
            (r0 + r - tok * a.group);
   }
-  __device__ __forceinline__ bool written(int r) const {
-    return !kPrefix || pos[kv_token(a, r0 + r) - kv_token(a, r0)] >= 0;
-  }
   // (whole warp) rows [begin, end), none if end <= begin
   __device__ __forceinline__ void write_out(int lane, int begin, int end) const {
     constexpr int kLanes = D / 8;
 #pragma unroll 4
     for (int r = begin + lane / kLanes; r < end; r += 32 / kLanes)
-      if (written(r))
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row(r) * D +
-                                  8 * (lane % kLanes)) = lds_v4(staged(r, lane % kLanes));
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row(r) * D +
+                                8 * (lane % kLanes)) = lds_v4(staged(r, lane % kLanes));
   }
 };
 
@@ -201,18 +195,12 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// What a row's own tokens gave, as a part beside the prefix's: its weight in the
-// parts' units.
-__device__ __forceinline__ float own_weight(const Kv8Args& a, long long row) {
-  return fmaf(__ldcg(a.own_lse + row), 1.4426950408889634f, kPOff);
-}
-
 // The last part to arrive adds them all in order (every thread of the CTA) and
 // stages the rows, or writes them in fp32.
 template <int D, int kMode>
 __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, const float* first,
                                            int parts, int rows,
-                                           const OutRows<D, kMode == kKvPrefix>& put) {
+                                           const OutRows<D>& put) {
   using L = PL<D>;
   constexpr size_t kPart = 2 * kPRows * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,11 +218,6 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
       weight[p * rows32 + row] = w;
       top = fmaxf(top, w);
     }
-    float own = -INFINITY;
-    if (kMode == kKvPrefix) {
-      own = own_weight(a, put.row(row));
-      top = fmaxf(top, own);
-    }
     const float base = top == -INFINITY ? 0.f : top;
     float l = 0.f;
 #pragma unroll 4
@@ -243,15 +226,10 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
       weight[p * rows32 + row] = w;
       l += w;
     }
-    if (kMode == kKvPrefix) {
-      own = exp2f(own - base);
-      l += own;
-    }
     const float one = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) weight[p * rows32 + row] *= one;
-    if (kMode == kKvPrefix) weight[parts * rows32 + row] = own * one;
-    if (a.lse && put.written(row)) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
+    if (a.lse) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
   }
   cta_barrier();
   // sixteen elements of 32 rows per warp, four parts' loads in flight
@@ -283,18 +261,6 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
           acc[k].z = fmaf(w, v[p][k].z, acc[k].z);
           acc[k].w = fmaf(w, v[p][k].w, acc[k].w);
         }
-      }
-    }
-    if constexpr (kMode == kKvPrefix) {
-      const float w = weight[parts * rows32 + row];
-      const float4* own = reinterpret_cast<const float4*>(a.own + put.row(row) * D) + c;
-#pragma unroll
-      for (int k = 0; k < kC; ++k) {
-        const float4 v = __ldcg(own + k);
-        acc[k].x = fmaf(w, v.x, acc[k].x);
-        acc[k].y = fmaf(w, v.y, acc[k].y);
-        acc[k].z = fmaf(w, v.z, acc[k].z);
-        acc[k].w = fmaf(w, v.w, acc[k].w);
       }
     }
     if constexpr (kMode == kKvOwn) {
@@ -434,7 +400,8 @@ constexpr int kSplitRows = 64;
 // kMode kKvOwn: the part of the tokens behind a shared prefix, in fp32, whose
 // positions and pages count from its end.  kKvPrefix: the part of the prefix
 // itself, one "sequence" of all the call's rows, which see all of it (but for a
-// window); the result joins it with what kKvOwn wrote.
+// window).  Every block is cut into tail_parts parts (some of no pages under a
+// window), whose results kv8_join_kernel joins with what kKvOwn wrote.
 template <int D, bool kSplit, int kMode>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole,
@@ -465,6 +432,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int tail = static_cast<int>(blockIdx.x) - whole;  // of the items in parts
   const int part = tail < 0 ? 0 : tail % tail_parts;
   const int item = tail < 0 ? static_cast<int>(blockIdx.x) : whole + tail / tail_parts;
+  // A part's results: O in chunks of four elements, [D / 4][rows], then (ref, sum).
+  constexpr size_t kPart = 2 * kPRows * (D + 2);
   const int hk = item % a.hkv;
   const int b = kMode == kKvPrefix ? 0 : (item / a.hkv) % a.seqs;
   const int rb = row_blocks - 1 - item / a.hkv / (kMode == kKvPrefix ? 1 : a.seqs);
@@ -511,7 +480,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     cta_barrier();
     p_first = pos_range[0];
     p_last = pos_range[1];
-    if (p_last < 0) return;
+    if (p_last < 0) {  // none of the block's rows belongs to a sequence
+      if (threadIdx.x < rows)
+        reinterpret_cast<float2*>(partials + blockIdx.x * kPart + 2 * kPRows * D)[threadIdx.x] =
+            make_float2(-INFINITY, kNoRow);
+      return;
+    }
     pages = kv_prefix_pages(a, p_first);
   } else {
     p_first = p_base + tok0;
@@ -520,8 +494,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   // (The launch chose the parts by the table's width, the most pages that a
   // block can have: by its own it may need fewer, or none.)
-  int parts = 1;
-  if (tail >= 0 && tail_parts > 1) {
+  int parts = kMode == kKvPrefix ? tail_parts : 1;
+  if (kMode != kKvPrefix && tail >= 0 && tail_parts > 1) {
     const int fit = pages.count / kPartPages;
     const int p = tail_parts < fit ? tail_parts : fit;
     if (p > 1 && part_cost(pages.count, p, tail_items, sms) <
@@ -969,12 +943,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   __syncwarp();
   if (kSplit) cta_barrier();  // no converted page is read any more
-  // A part: O in chunks of four elements, [D / 4][rows], then (ref, sum).
-  constexpr size_t kPart = 2 * kPRows * (D + 2);
-  const OutRows<D, kMode == kKvPrefix> put{a, smem + L::kQOff, r0, sq.row0, hk, tok_pos};
+  const OutRows<D> put{a, smem + L::kQOff, r0, sq.row0, hk};
   int out0 = 0, out1 = 0;  // the staged rows that this warp writes
   if (soft) {
     const bool mine_out = !(kSplit && qt);  // (tile 0 writes for both)
+    const bool whole_rows = kMode != kKvPrefix && parts == 1;
     // both tiles' softmax warps
     auto softmax_barrier = [&] {
       asm volatile("bar.sync 1, %0;" ::"r"(64 * soft_warps(0)) : "memory");
@@ -998,24 +971,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       inv1 = all == 0.f ? 0.f : w1 / all;
       ref = top;
       sum = all;
-    }
-    // kKvPrefix, one part: the own tokens' share of the result
-    float own_f = 0.f;
-    const float* own = nullptr;
-    if constexpr (kMode == kKvPrefix) {
-      if (mine_out && live && parts == 1) {
-        own = a.own + put.row(r) * D;
-        const float w0 = sum == 0.f ? -INFINITY : ref + log2f(sum);
-        const float w1 = own_weight(a, put.row(r));
-        const float top = fmaxf(w0, w1), base = top == -INFINITY ? 0.f : top;
-        const float l0 = exp2f(w0 - base), l1 = exp2f(w1 - base), all = l0 + l1;
-        const float one = all == 0.f ? 0.f : 1.0f / all;
-        inv *= l0 * one;
-        inv1 *= l0 * one;
-        own_f = l1 * one;
-        ref = base;
-        sum = all;
-      }
     }
 #pragma unroll 2
     for (int q = 0; q < D / 16; ++q) {
@@ -1045,27 +1000,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       if (!mine_out) {
-      } else if (kMode == kKvOwn && live && parts == 1) {
+      } else if (kMode == kKvOwn && live && whole_rows) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + put.row(r) * D + 16 * q);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-      } else if (live && parts == 1) {
-        if constexpr (kMode == kKvPrefix) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(own + 16 * q) + k);
-            f[4 * k] = fmaf(own_f, v.x, f[4 * k]);
-            f[4 * k + 1] = fmaf(own_f, v.y, f[4 * k + 1]);
-            f[4 * k + 2] = fmaf(own_f, v.z, f[4 * k + 2]);
-            f[4 * k + 3] = fmaf(own_f, v.w, f[4 * k + 3]);
-          }
-        }
+      } else if (live && whole_rows) {
         uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = pack_out(a.type, f[2 * k], f[2 * k + 1]);
         if (kSplit) {  // (few rows: straight to their places)
-          if (!put.written(r)) continue;
           uint4* o =
               reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + put.row(r) * D + 16 * q);
           o[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1081,7 +1025,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           o[k * (2 * kPRows)] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
-    if (!kSplit && kMode != kKvOwn && parts == 1) {
+    if (!kSplit && kMode != kKvOwn && whole_rows) {
       out0 = r - lane;
       out1 = rows < out0 + 32 ? rows : out0 + 32;
     }
@@ -1089,13 +1033,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       *reinterpret_cast<float2*>(other + (D / 4) * kPRows) = make_float2(ref, sum);
       softmax_barrier();
     }
-    if (mine_out && live && parts > 1)
-      reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
-    if (mine_out && live && parts == 1 && a.lse && put.written(r))
-      a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
+    if (mine_out && live && !whole_rows)
+      reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] =
+          make_float2(ref, kMode == kKvPrefix && pos < 0 ? kNoRow : sum);
+    if (mine_out && live && whole_rows && a.lse) a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
   }
   __syncwarp();
-  if (parts > 1) {
+  if (kMode != kKvPrefix && parts > 1) {
     // The last part to arrive adds them all in order.
     __threadfence();
     cta_barrier();
@@ -1135,6 +1079,13 @@ static long long row_blocks_of(long long max_new, int group) {
   return (max_new * group + 2 * kPRows - 1) / (2 * kPRows);
 }
 
+size_t kv8_prefix_partial_bytes(int rows, int group, int kv_heads, int dim) {
+  // items in up to as many parts as there are SMs twice over, or whole
+  const size_t items = static_cast<size_t>(row_blocks_of(rows, group)) * kv_heads;
+  const size_t most = items > 2 * kSmallTMaxCtas ? items : 2 * kSmallTMaxCtas;
+  return most * 2 * kPRows * (dim + 2) * sizeof(float);
+}
+
 bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs) {
   return row_blocks_of(max_new, group) * kv_heads <=
          (0x7FFFFFFFll - 2 * kSmallTMaxCtas) / seqs;
@@ -1158,11 +1109,16 @@ cudaError_t kv8_prompt_set_attributes() {
 }
 
 cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
-                              int* tickets, int num_sms, cudaStream_t stream, int* launches) {
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches,
+                              int* cut) {
   const bool prefix = mode == kKvPrefix;
   const int longest = prefix ? a.rows : a.max_new;  // tokens of a "sequence"
   const int seqs = prefix ? 1 : a.seqs;
-  const int width = prefix ? a.shared / kBlk : a.width - a.shared / kBlk;  // its pages
+  int width = prefix ? a.shared / kBlk : a.width - a.shared / kBlk;  // its pages
+  if (prefix && a.window > 0) {
+    const long long seen = static_cast<long long>(a.window) / kBlk + a.sinks / kBlk + 3;
+    if (seen < width) width = static_cast<int>(seen);
+  }
   const long long most = static_cast<long long>(longest) * a.group;
   const long long row_blocks = row_blocks_of(longest, a.group);
   // Whole waves of items run as they are.  The keys of the items left (the
@@ -1174,12 +1130,11 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
   // 1227 us.
   const long long items = row_blocks * a.hkv * seqs;
   const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
-  const long long tail = items % sms, whole = items - tail;
+  const long long tail = prefix ? items : items % sms, whole = items - tail;
   unsigned parts = 1, best = width;
-  // (the join holds a weight per part, the own tokens' among them, and row in the
-  // converted pages' place)
+  // (the join holds a weight per part and row in the converted pages' place)
   const long long rows32 = most < 2 * kPRows ? (most + 31) / 32 * 32 : 2 * kPRows;
-  const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32 - (prefix ? 1 : 0);
+  const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32;
   static_assert(PL<64>::kConv * PL<64>::kTileB <= PL<128>::kConv * PL<128>::kTileB, "room");
   for (unsigned p = 2; p * tail <= 2 * sms && p <= static_cast<unsigned>(width) / kPartPages &&
                        p <= room;
@@ -1211,6 +1166,117 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
                                            static_cast<int>(whole), static_cast<int>(parts),
                                            static_cast<int>(tail), static_cast<int>(sms),
                                            partials, tickets);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (cut) *cut = static_cast<int>(parts);
+  return cudaSuccess;
+}
+
+// Joins the parts of the prefix and what the rows' own tokens gave, by their
+// log-sum-exps (base 2, in the parts' units).  A CTA takes kR rows of a
+// key-value head: a warp makes the weights of a row, then each thread adds four
+// elements of one over the parts, whose chunks are read 128 bytes at a time.
+// One CTA for each of the prefix's items instead (its last part) took 50 us of
+// 109 at 32 sequences of 6 heads behind 16384 tokens: 2 MB through one SM.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv8_join_kernel(const __grid_constant__ Kv8Args a, int parts, int row_blocks,
+                    const float* __restrict__ partials) {
+  constexpr int kR = kJoinThreads / (D / 4);
+  constexpr size_t kPart = 2 * kPRows * (D + 2);
+  grid_dependents_launch();
+  extern __shared__ float weight[];  // [kR][parts + 1], the own tokens' last
+  __shared__ bool s_row[kR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = blockIdx.y;
+  const int n0 = blockIdx.x * kR;  // first row of the head
+  const int R = a.rows * a.group;
+  const int rb = n0 / (2 * kPRows), r0 = n0 % (2 * kPRows);
+  const float* first =
+      partials +
+      (static_cast<size_t>(row_blocks - 1 - rb) * a.hkv + hk) * parts * kPart;
+  auto row_of = [&](int n) {
+    const int tok = kv_token(a, n);
+    return static_cast<long long>(tok) * a.heads + hk * a.group + (n - tok * a.group);
+  };
+  grid_dependency_wait();
+  for (int i = warp; i < kR; i += kJoinThreads / 32) {
+    float* w = weight + i * (parts + 1);
+    const bool there = n0 + i < R;
+    const float2* ms = reinterpret_cast<const float2*>(first + 2 * kPRows * D) + r0 + i;
+    const bool row = there && __ldcg(ms).y != kNoRow;
+    if (lane == 0) s_row[i] = row;
+    if (!row) continue;
+    const float own = fmaf(__ldcg(a.own_lse + row_of(n0 + i)), 1.4426950408889634f, kPOff);
+    float top = own;
+    for (int p = lane; p < parts; p += 32) {
+      const float2 v = __ldcg(ms + p * (kPart / 2));
+      const float x = v.y == 0.f ? -INFINITY : v.x + log2f(v.y);
+      w[p] = x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    for (int p = lane; p < parts; p += 32) {
+      w[p] = exp2f(w[p] - base);
+      l += w[p];
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    const float mine = exp2f(own - base);
+    l += mine;
+    const float one = l == 0.f ? 0.f : 1.0f / l;
+    for (int p = lane; p < parts; p += 32) w[p] *= one;
+    if (lane == 0) {
+      w[parts] = mine * one;
+      if (a.lse) a.lse[row_of(n0 + i)] = kv_log_sum(base, l, kPOff);
+    }
+  }
+  __syncthreads();
+  const int i = threadIdx.x % kR, c = threadIdx.x / kR;
+  if (!s_row[i]) return;
+  const float* w = weight + i * (parts + 1);
+  const long long row = row_of(n0 + i);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // (a part or own result of no weight may never have been written)
+  auto add = [&](float f, const float4& v) {
+    if (f == 0.f) return;
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  };
+  const float4 own = __ldcg(reinterpret_cast<const float4*>(a.own + row * D) + c);
+  const float4* from = reinterpret_cast<const float4*>(first) + c * (2 * kPRows) + r0 + i;
+  constexpr int kAtOnce = 8;
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += kAtOnce) {
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int p = 0; p < kAtOnce; ++p)
+      if (p0 + p < parts) v[p] = __ldcg(from + (p0 + p) * (kPart / 4));
+#pragma unroll
+    for (int p = 0; p < kAtOnce; ++p)
+      if (p0 + p < parts) add(w[p0 + p], v[p]);
+  }
+  add(w[parts], own);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 4 * c) =
+      make_uint2(pack_out(a.type, acc.x, acc.y), pack_out(a.type, acc.z, acc.w));
+}
+
+cudaError_t launch_kv8_join(const Kv8Args& a, int parts, const float* partials,
+                            cudaStream_t stream, int* launches) {
+  const int rows = a.rows * a.group, kr = kJoinThreads / (a.dim / 4);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      pdl_launch_config(attr, dim3((rows - 1) / kr + 1, a.hkv), dim3(kJoinThreads),
+                        sizeof(float) * kr * (parts + 1), stream);
+  const int row_blocks = static_cast<int>(row_blocks_of(a.rows, a.group));
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, a.dim == 128 ? kv8_join_kernel<128> : kv8_join_kernel<64>, a, parts, row_blocks, partials);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;

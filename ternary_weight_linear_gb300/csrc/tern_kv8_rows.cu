@@ -439,13 +439,15 @@ __device__ __forceinline__ FarRow<D> far_row(const Kv8Args& a, const uint8_t* qu
 }
 
 // kOwn: the part of the tokens behind a shared prefix (positions, pages and
-// lengths are those behind it), fp32 and with its log-sum-exp, for the launch
-// after it to join.  That launch does not wait for all of this one before it
-// begins, so it may begin once what came before this one is done.
+// lengths are those behind it), fp32 and with its log-sum-exp, for a later launch
+// to join.  beside: the launch before this one is the prefix's, which neither
+// writes what this one reads nor reads what it writes, and whose dependents
+// begin when what came before it is done: so this one waits for it at its end
+// alone (and is complete only when that one is).
 template <int D, int NT, bool kOwn>
 __global__ void __launch_bounds__(kRW * 32, 1)
     kv8_rows_kernel(const __grid_constant__ CUtensorMap tm, const Kv8Args a, int max_rows,
-                    int per_head) {
+                    int per_head, int beside) {
   using L = RL<D, NT>;
   constexpr int kRows = L::kRows;
   constexpr int kW = D / 16;   // words of a lane per key row: 8 or 4 (k steps)
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // (three tiles read their queries from shared memory at each half-page)
   constexpr bool kQRegs = NT < 3;
   constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
-  if (!kOwn) grid_dependents_launch();
+  grid_dependents_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -481,8 +483,8 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     fence_mbar_init();
     prefetch_tensormap(&tm);
   }
-  grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
-  if (kOwn) grid_dependents_launch();
+  // every input, the output and the workspace belong to earlier work
+  if (!kOwn || !beside) grid_dependency_wait();
 
   // ---- the launch's units: (sequence, head, page), pages fastest
   for (int b = threadIdx.x; b < a.seqs; b += kRW * 32) {
@@ -525,7 +527,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // sequence's heads are cut one by one, into equal numbers of ranges: no CTA
   // then has the end of one head and the start of the next to merge (one token
   // over 32000: 21.7 us instead of 25.8; two over 4000: 12.5 instead of 21.6).
-  if (U == 0) return;
+  if (U == 0) {
+    if (kOwn && beside) grid_dependency_wait();
+    return;
+  }
   const unsigned ctas = gridDim.x;
   const bool queue = U >= static_cast<long long>(kQueueUnits) * ctas;
   const bool heads = !queue && per_head > 0;  // one sequence, head by head
@@ -554,7 +559,10 @@ __global__ void __launch_bounds__(kRW * 32, 1)
     u_begin = static_cast<long long>(blockIdx.x) * per;
     u_end = U < u_begin + per ? U : u_begin + per;
   }
-  if (u_begin >= U) return;
+  if (u_begin >= U) {
+    if (kOwn && beside) grid_dependency_wait();
+    return;
+  }
   auto range_of = [&](long long u) {
     if (queue) return static_cast<int>(u < fixed ? u / per1 : ctas + (u - fixed) / per2);
     const unsigned v = static_cast<unsigned>(u);
@@ -1069,6 +1077,7 @@ __global__ void __launch_bounds__(kRW * 32, 1)
   // no copy of this warp outlives it
   for (; used < issued; ++used)
     if (!mbar_wait_clk(&full[used % L::kStages], (used / L::kStages) & 1, a.err)) break;
+  if (kOwn && beside) grid_dependency_wait();
 }
 
 template <int D, int NT, bool kOwn>
@@ -1085,7 +1094,7 @@ cudaError_t launch_one(const CUtensorMap* tm, const Kv8Args& a, int max_rows, in
     const cudaLaunchConfig_t cfg =
         pdl_launch_config(attr, dim3(grid), dim3(kRW * 32), RL<D, NT>::kAlloc, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_rows_kernel<D, NT, kOwn>, *tm, p, max_rows,
-                                             a.seqs == 1 ? grid / a.hkv : 0);
+                                             a.seqs == 1 ? grid / a.hkv : 0, kOwn && b0 == 0);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
