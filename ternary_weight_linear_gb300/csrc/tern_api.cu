@@ -380,9 +380,8 @@ int kv8_attention_args(const tern_kv8_cache* cache, const void* q, int type, lon
 }
 
 // The attention's launches, with the workspace that tern_kv8_attention asks for.
-int run_kv8_attention(Kv8Args* args, Kv8Mode mode, uint8_t* workspace, const DevState* d,
-                      cudaStream_t st, int* launches) {
-  Kv8Args& a = *args;
+int run_kv8_attention(Kv8Args a, uint8_t* workspace, const DevState* d, cudaStream_t st,
+                      int* launches) {
   a.tickets = reinterpret_cast<int*>(workspace);
   a.partials = reinterpret_cast<float*>(workspace + kSyncBytes);
   a.err = d->err;
@@ -398,7 +397,7 @@ int run_kv8_attention(Kv8Args* args, Kv8Mode mode, uint8_t* workspace, const Dev
   // cores.  A single sequence takes one launch, of the latter where
   // max_new allows more than the former takes.
   const long long most = static_cast<long long>(a.max_new) * a.group;
-  long long pages = a.width - a.shared / TERN_KV8_BLOCK;  // that a sequence's rows see, at most
+  long long pages = a.width;  // that a sequence's rows see, at most
   if (a.window > 0) {
     const long long seen = (static_cast<long long>(a.window) + a.max_new + a.sinks) / TERN_KV8_BLOCK + 4;
     if (seen < pages) pages = seen;
@@ -407,20 +406,15 @@ int run_kv8_attention(Kv8Args* args, Kv8Mode mode, uint8_t* workspace, const Dev
   const int few = most <= kKvFewRowsLong && long_batch ? kKvFewRowsLong : kKvFewRows;
   const bool many = most > few;
   if (!many || a.seqs > 1) {
-    if (launch_kv8_rows(&tm, a, mode, few, d->sms, st, launches) != cudaSuccess) return TERN_ECUDA;
+    if (launch_kv8_rows(&tm, a, few, d->sms, st, launches) != cudaSuccess) return TERN_ECUDA;
   }
   if (many) {
-    if (launch_kv8_prompt(a, mode, a.seqs > 1 ? few + 1 : 1,
+    if (launch_kv8_prompt(a, kKvWhole, a.seqs > 1 ? few + 1 : 1,
                           a.partials + kv8_rows_partial_bytes(a.dim) / sizeof(float),
                           a.tickets + kPromptTickets, d->sms, st, launches) != cudaSuccess)
       return TERN_ECUDA;
   }
   return TERN_OK;
-}
-
-// fp32 results and log-sum-exps of the rows' own tokens.
-size_t own_bytes(int rows, int heads, int dim) {
-  return align_up(sizeof(float) * rows * heads * (static_cast<size_t>(dim) + 1), 256);
 }
 
 // A rotation's arguments for heads of `dim` elements.
@@ -907,7 +901,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
   rc = device_state(&d);
   if (rc != TERN_OK) return rc;
   int launches = 0;
-  rc = run_kv8_attention(&a, kKvWhole, static_cast<uint8_t*>(workspace), d,
+  rc = run_kv8_attention(a, static_cast<uint8_t*>(workspace), d,
                          static_cast<cudaStream_t>(stream), &launches);
   if (rc == TERN_OK) t_last_launches = launches;
   return rc;
@@ -916,8 +910,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
 size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads, int kv_heads,
                                                  int head_dim) {
   const size_t n = tern_kv8_attention_workspace_bytes(seqs, rows, heads, kv_heads, head_dim);
-  return n == 0 ? 0 : align_up(n, 256) + own_bytes(rows, heads, head_dim) +
-                          kv8_prefix_partial_bytes(rows, heads / kv_heads, kv_heads, head_dim);
+  return n == 0 ? 0 : align_up(n, 256) + kv8_shared_part_bytes(rows, heads, kv_heads, head_dim);
 }
 
 int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type, long long ld,
@@ -929,7 +922,7 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
                               softmax_scale, out, lse, &a);
   if (rc != TERN_OK) return rc;
   if (shared < 0 || shared % TERN_KV8_BLOCK != 0 || shared / TERN_KV8_BLOCK > a.width ||
-      !kv8_prompt_fits(rows, heads / a.hkv, a.hkv, 1))
+      !kv8_shared_fits(rows, heads / a.hkv, a.hkv, a.seqs))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
   const size_t base = align_up(
@@ -946,29 +939,16 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
   int launches = 0;
   a.behind = shared;
   if (a.seqs == 1 || shared == 0) {
-    rc = run_kv8_attention(&a, kKvWhole, ws, d, st, &launches);
+    rc = run_kv8_attention(a, ws, d, st, &launches);
   } else {
-    // the prefix's part, the own tokens' in fp32 beside it, and their join
-    float* o = reinterpret_cast<float*>(ws + base);
-    float* l = o + static_cast<size_t>(rows) * heads * a.dim;
-    float* parts = reinterpret_cast<float*>(ws + base + own_bytes(rows, heads, a.dim));
-    Kv8Args own = a;
-    own.shared = shared;
-    own.table += shared / TERN_KV8_BLOCK;
-    own.sinks = a.sinks > shared ? a.sinks - shared : 0;
-    own.out = o;
-    own.lse = l;
-    a.err = d->err;
     a.shared = shared;
-    a.own = o;
-    a.own_lse = l;
-    int cut = 0;
-    if (launch_kv8_prompt(a, kKvPrefix, 1, parts, nullptr, d->sms, st, &launches, &cut) !=
-        cudaSuccess)
-      return TERN_ECUDA;
-    rc = run_kv8_attention(&own, kKvOwn, ws, d, st, &launches);
-    if (rc != TERN_OK) return rc;
-    if (launch_kv8_join(a, cut, parts, st, &launches) != cudaSuccess) return TERN_ECUDA;
+    a.part_o = reinterpret_cast<float*>(ws + base);
+    a.err = d->err;
+    if (launch_kv8_shared(a,
+                          reinterpret_cast<float*>(ws + kSyncBytes + kv8_rows_partial_bytes(a.dim)),
+                          static_cast<int*>(workspace) + kPromptTickets, d->sms, st,
+                          &launches) != cudaSuccess)
+      rc = TERN_ECUDA;
   }
   if (rc == TERN_OK) t_last_launches = launches;
   return rc;

@@ -258,17 +258,20 @@ struct Kv8Args {
   float* partials;
   int* err;
   // Attention behind a shared prefix.  shared: tokens that precede what table
-  // and lens are read for, the same for every sequence of the call (its first
-  // pages are left out of the table's rows); 0 otherwise.  behind: the position
-  // that no new token may precede.  own, own_lse: what the sequences' own tokens
-  // gave, fp32 [rows][heads][dim] and [rows][heads].
+  // and lens are read for, the same for every sequence of the call; 0 otherwise.
+  // behind: the position that no new token may precede.
   int shared, behind;
-  const float* own;
-  const float* own_lse;
+  // Its parts: `parts` of every row, the prefix's first (prefix_parts of them),
+  // then those of the row's own tokens.  part_o: fp32, of unit weight, in chunks of
+  // four elements [kv_heads][parts][dim / 4][rows * group][4]; part_w: the base-2
+  // logarithm of their weight [kv_heads][parts][rows * group].
+  float* part_o;
+  float* part_w;
+  int parts, prefix_parts;
 };
-// What an attention kernel computes: a call's result; the part of it that comes
-// from the tokens behind a shared prefix, in fp32; or the prefix's part for all
-// rows of the batch.
+// What the tensor-core attention computes: a call's result; the parts of it that
+// come from the tokens behind a shared prefix (one part, kKvOwn), or from the
+// prefix itself, for all rows of the batch (kKvPrefix).
 enum Kv8Mode : int { kKvWhole, kKvOwn, kKvPrefix };
 // n / group = (high half of n * mul + n) >> shift for n < 2^31: with shift =
 // ceil(log2 group), mul = floor(2^32 (2^shift - group) / group) + 1.
@@ -313,10 +316,8 @@ constexpr int kKvFewRowsLong = 24, kKvLongPages = 40;
 constexpr int kKvSeqsPerLaunch = 128;  // sequences of one launch
 size_t kv8_rows_partial_bytes(int dim);
 cudaError_t kv8_rows_set_attributes();
-// kKvOwn: the first launch begins beside the one before it (the prefix's), which
-// begins its dependents when what came before it is done.
-cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, Kv8Mode mode, int max_rows,
-                            int num_sms, cudaStream_t stream, int* launches);
+cudaError_t launch_kv8_rows(const CUtensorMap* tm, const Kv8Args& a, int max_rows, int num_sms,
+                            cudaStream_t stream, int* launches);
 
 // Attention of sequences with at least min_rows query rows per key-value
 // head, on the tensor cores.  tickets: kSmallTMaxCtas zeroed ints.
@@ -325,13 +326,18 @@ cudaError_t kv8_prompt_set_attributes();
 // Whether the kernel's grid holds the blocks of rows of such a call.
 bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs);
 cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
-                              int* tickets, int num_sms, cudaStream_t stream, int* launches,
-                              int* cut = nullptr);
-// kKvPrefix: *cut is the number of parts of each block of rows, which partials
-// then holds for the join.
-size_t kv8_prefix_partial_bytes(int rows, int group, int kv_heads, int dim);
-cudaError_t launch_kv8_join(const Kv8Args& a, int parts, const float* partials,
-                            cudaStream_t stream, int* launches);
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches);
+
+// Attention behind a shared prefix (a.shared, a.behind set, a.part_o at the
+// parts' memory): all its launches.  partials, tickets: as for launch_kv8_prompt.
+bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs);
+size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim);
+cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_sms,
+                              cudaStream_t stream, int* launches);
+// Rows of a sequence and key-value head up to which its own tokens are its spans'.
+constexpr int kSpanRows = 64;
+// Parts of the prefix's blocks of rows on the tensor cores, by its pages.
+int kv8_prefix_parts(const Kv8Args& a, int pages, int num_sms);
 
 // Diagnostic: one kernel whose bounded wait runs out (which = 0: an mbarrier
 // phase nobody completes; 1: a device counter nobody raises) and records the

@@ -78,6 +78,26 @@ __device__ __forceinline__ KvPages kv_prefix_pages(const Kv8Args& a, int p0) {
   return v;
 }
 
+// Row n of a key-value head in part p: chunk c of its output, and its weight
+// (behind a shared prefix; see Kv8Args).
+__device__ __forceinline__ float4* kv_part_o(const Kv8Args& a, int hk, int p, int c, long long n) {
+  return reinterpret_cast<float4*>(a.part_o) +
+         ((static_cast<size_t>(hk) * a.parts + p) * (a.dim / 4) + c) *
+             static_cast<size_t>(a.rows * a.group) + n;
+}
+__device__ __forceinline__ float* kv_part_w(const Kv8Args& a, int hk, int p, long long n) {
+  return a.part_w +
+         (static_cast<size_t>(hk) * a.parts + p) * static_cast<size_t>(a.rows * a.group) + n;
+}
+// The weight of a part, from its reference and sum (which are 2^10 times larger,
+// in all the kernels).
+__device__ __forceinline__ float part_weight(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : ref + log2f(sum);
+}
+// In the first part's weight: a row of no sequence, or of a skipped one.  (A NaN
+// that no arithmetic makes.)
+constexpr uint32_t kNoRow = 0x7FCDEAD5u;
+
 // Whether any row at positions [p0, p1] sees one of the tokens [j0, j1].
 __device__ __forceinline__ bool kv_any(const Kv8Args& a, int p0, int p1, int j0, int j1) {
   return j0 <= p1 && (a.window == 0 || j1 > p0 - a.window || j0 < a.sinks);

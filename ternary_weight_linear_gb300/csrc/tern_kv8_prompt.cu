@@ -65,8 +65,9 @@ __host__ __device__ constexpr unsigned part_cost(unsigned pages, unsigned parts,
                                                  unsigned sms) {
   return (items * parts + sms - 1) / sms * ((pages + parts - 1) / parts + kPartCost);
 }
+// Pages of time that a part of a shared prefix costs beside its own.
+constexpr unsigned kPrefixCost = 6;
 constexpr float kUp = 16777216.f;  // 2^24, 1 over the keys' unit
-constexpr float kNoRow = -1.f;     // in a sum's place: a row of no sequence
 
 template <int D>
 struct PL {
@@ -176,6 +177,20 @@ struct OutRows {
     return static_cast<long long>(row0 + tok) * a.heads + hk * a.group +
            (r0 + r - tok * a.group);
   }
+  // kKvOwn: the row in the first of its own tokens' parts, the only one that has
+  // weight
+  __device__ __forceinline__ long long part_row(int r) const {
+    return static_cast<long long>(row0) * a.group + r0 + r;
+  }
+  __device__ __forceinline__ float4* own(int r, int c) const {
+    return kv_part_o(a, hk, a.prefix_parts, c, part_row(r));
+  }
+  __device__ __forceinline__ void own_weight(int r, float w) const {
+    for (int p = a.prefix_parts; p < a.parts; ++p) {
+      *kv_part_w(a, hk, p, part_row(r)) = w;
+      w = -INFINITY;
+    }
+  }
   // (whole warp) rows [begin, end), none if end <= begin
   __device__ __forceinline__ void write_out(int lane, int begin, int end) const {
     constexpr int kLanes = D / 8;
@@ -229,7 +244,10 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
     const float one = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) weight[p * rows32 + row] *= one;
-    if (a.lse) a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
+    if constexpr (kMode == kKvOwn)
+      put.own_weight(row, part_weight(base, l));
+    else if (a.lse)
+      a.lse[put.row(row)] = kv_log_sum(base, l, kPOff);
   }
   cta_barrier();
   // sixteen elements of 32 rows per warp, four parts' loads in flight
@@ -264,9 +282,8 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, uint8_t* smem, cons
       }
     }
     if constexpr (kMode == kKvOwn) {
-      float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + put.row(row) * D) + c;
 #pragma unroll
-      for (int k = 0; k < kC; ++k) out[k] = acc[k];
+      for (int k = 0; k < kC; ++k) *put.own(row, c + k) = acc[k];
       continue;
     }
 #pragma unroll
@@ -397,11 +414,11 @@ __device__ __noinline__ SoftState wide_pages(uint8_t* smem, const Kv8Args& a, So
 // 16000).
 constexpr int kSplitRows = 64;
 //
-// kMode kKvOwn: the part of the tokens behind a shared prefix, in fp32, whose
-// positions and pages count from its end.  kKvPrefix: the part of the prefix
+// kMode kKvOwn: a part of the result, that of the tokens behind a shared prefix,
+// whose positions and pages count from its end.  kKvPrefix: the parts of the prefix
 // itself, one "sequence" of all the call's rows, which see all of it (but for a
-// window).  Every block is cut into tail_parts parts (some of no pages under a
-// window), whose results kv8_join_kernel joins with what kKvOwn wrote.
+// window): every block is cut into tail_parts of them (some of no pages under a
+// window).
 template <int D, bool kSplit, int kMode>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv8_prompt_kernel(const __grid_constant__ Kv8Args a, int min_rows, int row_blocks, int whole,
@@ -482,8 +499,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     p_last = pos_range[1];
     if (p_last < 0) {  // none of the block's rows belongs to a sequence
       if (threadIdx.x < rows)
-        reinterpret_cast<float2*>(partials + blockIdx.x * kPart + 2 * kPRows * D)[threadIdx.x] =
-            make_float2(-INFINITY, kNoRow);
+        *kv_part_w(a, hk, part, r0 + threadIdx.x) = __uint_as_float(kNoRow);
       return;
     }
     pages = kv_prefix_pages(a, p_first);
@@ -1001,10 +1017,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       if (!mine_out) {
       } else if (kMode == kKvOwn && live && whole_rows) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + put.row(r) * D + 16 * q);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          *put.own(r, 4 * q + k) = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       } else if (live && whole_rows) {
         uint32_t w[8];
 #pragma unroll
@@ -1019,10 +1034,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           *reinterpret_cast<uint4*>(put.staged(r, 2 * q + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       } else if (live) {
-        float4* o = reinterpret_cast<float4*>(mine) + 4 * q * (2 * kPRows) + r;
+        const size_t step = kMode == kKvPrefix ? static_cast<size_t>(R) : 2 * kPRows;
+        float4* o = kMode == kKvPrefix
+                        ? kv_part_o(a, hk, part, 4 * q, r0 + r)
+                        : reinterpret_cast<float4*>(mine) + 4 * q * (2 * kPRows) + r;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k * (2 * kPRows)] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          o[k * step] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
     if (!kSplit && kMode != kKvOwn && whole_rows) {
@@ -1033,10 +1051,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
       *reinterpret_cast<float2*>(other + (D / 4) * kPRows) = make_float2(ref, sum);
       softmax_barrier();
     }
-    if (mine_out && live && !whole_rows)
-      reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] =
-          make_float2(ref, kMode == kKvPrefix && pos < 0 ? kNoRow : sum);
-    if (mine_out && live && whole_rows && a.lse) a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
+    if (mine_out && live) {
+      if constexpr (kMode == kKvPrefix)
+        *kv_part_w(a, hk, part, r0 + r) =
+            pos < 0 ? __uint_as_float(kNoRow) : part_weight(ref, sum);
+      else if (!whole_rows)
+        reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
+      else if (kMode == kKvOwn)
+        put.own_weight(r, part_weight(ref, sum));
+      else if (a.lse)
+        a.lse[put.row(r)] = kv_log_sum(ref, sum, kPOff);
+    }
   }
   __syncwarp();
   if (kMode != kKvPrefix && parts > 1) {
@@ -1079,13 +1104,6 @@ static long long row_blocks_of(long long max_new, int group) {
   return (max_new * group + 2 * kPRows - 1) / (2 * kPRows);
 }
 
-size_t kv8_prefix_partial_bytes(int rows, int group, int kv_heads, int dim) {
-  // items in up to as many parts as there are SMs twice over, or whole
-  const size_t items = static_cast<size_t>(row_blocks_of(rows, group)) * kv_heads;
-  const size_t most = items > 2 * kSmallTMaxCtas ? items : 2 * kSmallTMaxCtas;
-  return most * 2 * kPRows * (dim + 2) * sizeof(float);
-}
-
 bool kv8_prompt_fits(int max_new, int group, int kv_heads, int seqs) {
   return row_blocks_of(max_new, group) * kv_heads <=
          (0x7FFFFFFFll - 2 * kSmallTMaxCtas) / seqs;
@@ -1102,23 +1120,31 @@ cudaError_t kv8_prompt_set_attributes() {
   if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, false, MODE>, PL<128>::kAlloc);     \
   if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, true, MODE>, PL<128>::kAlloc);
   TERN_PROMPT_ATTR(kKvWhole)
-  TERN_PROMPT_ATTR(kKvOwn)
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<64, false, kKvOwn>, PL<64>::kAlloc);
+  if (e == cudaSuccess) e = allow(kv8_prompt_kernel<128, false, kKvOwn>, PL<128>::kAlloc);
   TERN_PROMPT_ATTR(kKvPrefix)
 #undef TERN_PROMPT_ATTR
   return e;
 }
 
+int kv8_prefix_parts(const Kv8Args& a, int pages, int num_sms) {
+  const long long items = row_blocks_of(a.rows, a.group) * a.hkv;
+  const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
+  unsigned parts = 1, best = ~0u;
+  for (unsigned p = 1; p == 1 || (p * items <= 2 * sms && 2 * static_cast<int>(p) <= pages); ++p) {
+    const unsigned cost = static_cast<unsigned>((items * p + sms - 1) / sms) *
+                          ((pages + p - 1) / p + kPrefixCost);
+    if (cost < best) best = cost, parts = p;
+  }
+  return static_cast<int>(parts);
+}
+
 cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, float* partials,
-                              int* tickets, int num_sms, cudaStream_t stream, int* launches,
-                              int* cut) {
+                              int* tickets, int num_sms, cudaStream_t stream, int* launches) {
   const bool prefix = mode == kKvPrefix;
   const int longest = prefix ? a.rows : a.max_new;  // tokens of a "sequence"
   const int seqs = prefix ? 1 : a.seqs;
-  int width = prefix ? a.shared / kBlk : a.width - a.shared / kBlk;  // its pages
-  if (prefix && a.window > 0) {
-    const long long seen = static_cast<long long>(a.window) / kBlk + a.sinks / kBlk + 3;
-    if (seen < width) width = static_cast<int>(seen);
-  }
+  const int width = a.width - a.shared / kBlk;  // its pages, at most
   const long long most = static_cast<long long>(longest) * a.group;
   const long long row_blocks = row_blocks_of(longest, a.group);
   // Whole waves of items run as they are.  The keys of the items left (the
@@ -1131,12 +1157,12 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
   const long long items = row_blocks * a.hkv * seqs;
   const long long sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   const long long tail = prefix ? items : items % sms, whole = items - tail;
-  unsigned parts = 1, best = width;
+  unsigned parts = prefix ? a.prefix_parts : 1, best = width;
   // (the join holds a weight per part and row in the converted pages' place)
   const long long rows32 = most < 2 * kPRows ? (most + 31) / 32 * 32 : 2 * kPRows;
   const long long room = 2 * PL<64>::kConv * PL<64>::kTileB / 4 / rows32;
   static_assert(PL<64>::kConv * PL<64>::kTileB <= PL<128>::kConv * PL<128>::kTileB, "room");
-  for (unsigned p = 2; p * tail <= 2 * sms && p <= static_cast<unsigned>(width) / kPartPages &&
+  for (unsigned p = 2; !prefix && p * tail <= 2 * sms && p <= static_cast<unsigned>(width) / kPartPages &&
                        p <= room;
        ++p) {
     const unsigned cost = part_cost(width, p, static_cast<unsigned>(tail),
@@ -1158,7 +1184,10 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
   TERN_PROMPT_CASE(128, false, MODE) \
   TERN_PROMPT_CASE(128, true, MODE)
   TERN_PROMPT_CASES(kKvWhole)
-  TERN_PROMPT_CASES(kKvOwn)
+  // (kSpanRows rows and fewer of a sequence behind a prefix are not its own)
+  static_assert(kSpanRows >= kSplitRows, "forms");
+  TERN_PROMPT_CASE(64, false, kKvOwn)
+  TERN_PROMPT_CASE(128, false, kKvOwn)
   TERN_PROMPT_CASES(kKvPrefix)
 #undef TERN_PROMPT_CASES
 #undef TERN_PROMPT_CASE
@@ -1166,117 +1195,6 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
                                            static_cast<int>(whole), static_cast<int>(parts),
                                            static_cast<int>(tail), static_cast<int>(sms),
                                            partials, tickets);
-  if (e != cudaSuccess) return e;
-  ++*launches;
-  if (cut) *cut = static_cast<int>(parts);
-  return cudaSuccess;
-}
-
-// Joins the parts of the prefix and what the rows' own tokens gave, by their
-// log-sum-exps (base 2, in the parts' units).  A CTA takes kR rows of a
-// key-value head: a warp makes the weights of a row, then each thread adds four
-// elements of one over the parts, whose chunks are read 128 bytes at a time.
-// One CTA for each of the prefix's items instead (its last part) took 50 us of
-// 109 at 32 sequences of 6 heads behind 16384 tokens: 2 MB through one SM.
-constexpr int kJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
-    kv8_join_kernel(const __grid_constant__ Kv8Args a, int parts, int row_blocks,
-                    const float* __restrict__ partials) {
-  constexpr int kR = kJoinThreads / (D / 4);
-  constexpr size_t kPart = 2 * kPRows * (D + 2);
-  grid_dependents_launch();
-  extern __shared__ float weight[];  // [kR][parts + 1], the own tokens' last
-  __shared__ bool s_row[kR];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = blockIdx.y;
-  const int n0 = blockIdx.x * kR;  // first row of the head
-  const int R = a.rows * a.group;
-  const int rb = n0 / (2 * kPRows), r0 = n0 % (2 * kPRows);
-  const float* first =
-      partials +
-      (static_cast<size_t>(row_blocks - 1 - rb) * a.hkv + hk) * parts * kPart;
-  auto row_of = [&](int n) {
-    const int tok = kv_token(a, n);
-    return static_cast<long long>(tok) * a.heads + hk * a.group + (n - tok * a.group);
-  };
-  grid_dependency_wait();
-  for (int i = warp; i < kR; i += kJoinThreads / 32) {
-    float* w = weight + i * (parts + 1);
-    const bool there = n0 + i < R;
-    const float2* ms = reinterpret_cast<const float2*>(first + 2 * kPRows * D) + r0 + i;
-    const bool row = there && __ldcg(ms).y != kNoRow;
-    if (lane == 0) s_row[i] = row;
-    if (!row) continue;
-    const float own = fmaf(__ldcg(a.own_lse + row_of(n0 + i)), 1.4426950408889634f, kPOff);
-    float top = own;
-    for (int p = lane; p < parts; p += 32) {
-      const float2 v = __ldcg(ms + p * (kPart / 2));
-      const float x = v.y == 0.f ? -INFINITY : v.x + log2f(v.y);
-      w[p] = x;
-      top = fmaxf(top, x);
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-      w[p] = exp2f(w[p] - base);
-      l += w[p];
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    const float mine = exp2f(own - base);
-    l += mine;
-    const float one = l == 0.f ? 0.f : 1.0f / l;
-    for (int p = lane; p < parts; p += 32) w[p] *= one;
-    if (lane == 0) {
-      w[parts] = mine * one;
-      if (a.lse) a.lse[row_of(n0 + i)] = kv_log_sum(base, l, kPOff);
-    }
-  }
-  __syncthreads();
-  const int i = threadIdx.x % kR, c = threadIdx.x / kR;
-  if (!s_row[i]) return;
-  const float* w = weight + i * (parts + 1);
-  const long long row = row_of(n0 + i);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // (a part or own result of no weight may never have been written)
-  auto add = [&](float f, const float4& v) {
-    if (f == 0.f) return;
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
-  };
-  const float4 own = __ldcg(reinterpret_cast<const float4*>(a.own + row * D) + c);
-  const float4* from = reinterpret_cast<const float4*>(first) + c * (2 * kPRows) + r0 + i;
-  constexpr int kAtOnce = 8;
-#pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += kAtOnce) {
-    float4 v[kAtOnce];
-#pragma unroll
-    for (int p = 0; p < kAtOnce; ++p)
-      if (p0 + p < parts) v[p] = __ldcg(from + (p0 + p) * (kPart / 4));
-#pragma unroll
-    for (int p = 0; p < kAtOnce; ++p)
-      if (p0 + p < parts) add(w[p0 + p], v[p]);
-  }
-  add(w[parts], own);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 4 * c) =
-      make_uint2(pack_out(a.type, acc.x, acc.y), pack_out(a.type, acc.z, acc.w));
-}
-
-cudaError_t launch_kv8_join(const Kv8Args& a, int parts, const float* partials,
-                            cudaStream_t stream, int* launches) {
-  const int rows = a.rows * a.group, kr = kJoinThreads / (a.dim / 4);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      pdl_launch_config(attr, dim3((rows - 1) / kr + 1, a.hkv), dim3(kJoinThreads),
-                        sizeof(float) * kr * (parts + 1), stream);
-  const int row_blocks = static_cast<int>(row_blocks_of(a.rows, a.group));
-  const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, a.dim == 128 ? kv8_join_kernel<128> : kv8_join_kernel<64>, a, parts, row_blocks, partials);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;

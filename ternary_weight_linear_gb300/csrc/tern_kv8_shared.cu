@@ -1,0 +1,680 @@
+// tern_kv8_attention_shared: attention of a batch whose sequences begin with the
+// same pages.
+//
+// A row's softmax over the prefix and over its sequence's own tokens are parts
+// of one softmax: with O_p the output of part p and W_p = sum 2^s the weight of
+// its scores,
+//   o = sum_p (W_p / W) O_p,  W = sum_p W_p.
+// So the prefix is one "sequence" of all rows of the batch, whose every cache
+// byte is read once, cut into parts along its tokens; the own tokens are short
+// spans of few rows each.  All parts go to the workspace in fp32 and one launch
+// joins them (a CTA that joined all parts of 256 rows, as the last of them,
+// read 2 MB through one SM: 50 us of 109 at 32 sequences of 6 query heads a
+// key-value head behind 16384 tokens).
+//
+// The launches:
+//   the prefix on the tensor cores (kv8_prompt_kernel), where the batch has more
+//   rows than kSpanPrefixRows; below it is spans too;
+//   spans (kv8_span_kernel), of sequences of up to kSpanRows rows, beside the
+//   former: it waits for it at its end only;
+//   longer sequences' own tokens by kv8_prompt_kernel;
+//   the join.
+#include "tern_kv8_half.cuh"
+
+namespace tern {
+namespace {
+
+constexpr int kSW = 4;           // warps of a span's CTA
+constexpr int kSThreads = 32 * kSW;
+constexpr int kSpanRecs = 32;    // pages whose records are held at a time
+constexpr int kSpanCtas = 1216;  // CTAs that own tokens (or a prefix) are cut into, at most
+constexpr int kSpanPrefixRows = 32;
+
+// The pages of a span's list: [s0, s1), then from f0 on.
+struct SpanPages {
+  int s0, s1, f0, count;
+  __device__ __forceinline__ int page(int i) const {
+    return i < s1 - s0 ? s0 + i : f0 + i - (s1 - s0);
+  }
+};
+
+// One part of the prefix (for rows of the whole batch) or of a sequence's own
+// tokens: up to 8 NT rows of a key-value head over a range of pages.  Bound by
+// the cache's bytes where there are many pages, by latency elsewhere: small CTAs
+// without barriers in the loop, of which an SM holds several, so that one's
+// dependent reads (lengths, table, scales, codes) pass under another's work.
+// Codes go from global memory straight to the registers of the tensor
+// instructions (each 128-byte line is read whole by eight or four lanes): a
+// half-page's values while its scores are made, the next one's keys while its
+// values are used.
+template <int D, int NT>
+struct Span {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kW = D / 16;
+  static constexpr int kMT = D / 16;
+  static constexpr int kQStride = 2 * D + 16;
+  static constexpr int kMStride = D + 4;
+  static constexpr bool kBiased = biased(NT);
+
+  struct Smem {
+    alignas(16) uint8_t q[kRows * kQStride];
+    alignas(16) float merge[kSW * 8 * kMStride];
+    alignas(16) PageRec recs[kSpanRecs];
+    int blk[kSpanRecs];   // its place among the cache's (page, keys, head); -1: none
+    int meta[kSpanRecs];  // its number in the sequence * 16, kMHalf, kMAll
+    float2 ml[kSW][kRows];
+    float fac[kRows][kSW];
+    float weight[kRows], qscale[kRows];
+    int pos[kRows];
+    int range[2];
+    int far;
+  };
+
+  const Kv8Args& a;
+  Smem& sm;
+  int warp, lane, g, t;
+  int hk, slot, table_row;  // key-value head, part, row of the page table
+  int n0, rows;             // first row (of the head's) and how many
+  int p_first, p_last;
+  SpanPages pages;
+
+  // a lane's codes of half-page h
+  __device__ __forceinline__ const int8_t* half_at(int h, int values) const {
+    return a.codes + (static_cast<size_t>(sm.blk[h >> 1]) + values * a.hkv) * (kBlk * D) +
+           (h & 1) * (kHalf * D);
+  }
+  __device__ __forceinline__ void load_keys(int h, uint32_t (&kw)[4][kW]) const {
+    const int8_t* from = half_at(h, 0) + 2 * kW * 2 * t;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+      for (int i = 0; i < kW / 4; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + (8 * n + g) * D + 16 * i);
+        kw[n][4 * i] = x.x, kw[n][4 * i + 1] = x.y, kw[n][4 * i + 2] = x.z, kw[n][4 * i + 3] = x.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_values(int h, uint32_t (&vw)[2][4][D / 32]) const {
+    const int8_t* from = half_at(h, 1) + (D / 8) * g;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int8_t* p = from + (16 * k + 2 * t + (x & 1) + 8 * (x >> 1)) * D;
+        if constexpr (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          vw[k][x][0] = v.x, vw[k][x][1] = v.y, vw[k][x][2] = v.z, vw[k][x][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          vw[k][x][0] = v.x, vw[k][x][1] = v.y;
+        }
+      }
+  }
+
+  // The rows' queries in fp16, each scaled by a power of two; a row per warp.
+  __device__ __forceinline__ void stage_queries() {
+    constexpr int kX = kRows / kSW;
+    uint32_t raw[kX][D / 64];
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      const int r = warp + x * kSW;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) raw[x][e] = 0u;
+      if (r < rows) {
+        const int tok = kv_token(a, n0 + r);
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                              static_cast<long long>(tok) * a.ld +
+                              static_cast<long long>(hk * a.group + n0 + r - tok * a.group) * a.hd +
+                              lane * (D / 32);
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(src);
+          raw[x][0] = w.x, raw[x][1] = w.y;
+        } else {
+          raw[x][0] = *reinterpret_cast<const uint32_t*>(src);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      const int r = warp + x * kSW;
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) m2 = __vmaxu2(m2, raw[x][e] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, k));
+      const int up = q_exponent((m2 & 0xFFFFu) > (m2 >> 16) ? m2 & 0xFFFFu : m2 >> 16, a.type);
+      const float f = pow2f(up);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(sm.q + r * kQStride);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        float lo, hi;
+        unpack16(raw[x][e], a.type, lo, hi);
+        const int word = lane * (D / 64) + e;
+        const int unit = word >> 1;  // (placed as staged_query reads it)
+        dst[((unit ^ (unit / (D / 8))) << 1) | (word & 1)] = half2_bits(lo * f, hi * f);
+      }
+      if (lane == 0) sm.qscale[r] = pow2f(-up);
+    }
+  }
+
+  // Records of pages [c0, c0 + n) of the list.
+  __device__ __forceinline__ void make_records(int c0, int n) {
+    for (int i = threadIdx.x; i < n; i += kSThreads) {
+      const int lp = pages.page(c0 + i);
+      const int page = a.table[static_cast<size_t>(table_row) * a.width + lp];
+      PageRec rec = {0.f, 0.f, 1.f, 0.f};
+      int blk = -1, meta = lp * 16;
+      if (page < 0 || page >= a.pages) {
+        atomicOr(a.err, kErrIndex);
+      } else {
+        blk = page * 2 * a.hkv + hk;
+        const float ks = a.scales[blk], vs = a.scales[blk + a.hkv];
+        const bool far = far_scales(ks, vs);
+        if (far) sm.far = 1;
+        rec = page_rec(ks, vs);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int j0 = lp * kBlk + hf * kHalf, j1 = j0 + kHalf - 1;
+          if (!far && kv_any(a, p_first, p_last, j0, j1)) meta |= kMHalf << hf;
+          if (kv_all(a, p_first, p_last, j0, j1)) meta |= kMAll << hf;
+        }
+      }
+      sm.recs[i] = rec;
+      sm.blk[i] = blk;
+      sm.meta[i] = meta;
+    }
+  }
+
+  // Pages [begin, end) of the list, into part `slot` of the rows.
+  __device__ __forceinline__ void run(int begin, int end) {
+    if (threadIdx.x == 0) sm.far = 0;
+    stage_queries();
+    __syncthreads();
+
+    uint2 qf[NT == 1 ? kW : 1];  // one tile's query fragments
+#pragma unroll
+    for (int j = 0; NT == 1 && j < kW; ++j) qf[j] = staged_query<D>(sm.q, 0, j, g, t);
+    auto query = [&](int n, int j) {
+      if (NT == 1) return qf[j];
+      return staged_query<D>(sm.q, n, j, g, t);
+    };
+    float o[NT][kMT][4];
+    float ref[NT][2], sum[NT][2], cs[NT][2], s0[NT][4];
+    int pos[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 8 * n + 2 * t + x;
+        ref[n][x] = -INFINITY;
+        sum[n][x] = 0.f;
+        cs[n][x] = sm.qscale[r] * a.scale_log2;
+        pos[n][x] = sm.pos[r];
+      }
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
+      query_bias<D, kBiased>([&](int j) { return query(n, j); }, s0[n]);
+    }
+
+    constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
+    for (int c0 = begin; c0 < end; c0 += kSpanRecs) {
+      const int n_here = end - c0 < kSpanRecs ? end - c0 : kSpanRecs;
+      if (c0 > begin) __syncthreads();  // the records before have been read
+      make_records(c0, n_here);
+      __syncthreads();
+      const int h_end = 2 * n_here;
+      auto next = [&](int h) {  // the warp's half-page from h on that some row sees
+        while (h < h_end && !(sm.meta[h >> 1] & (kMHalf << (h & 1)))) h += kSW;
+        return h;
+      };
+      uint32_t kw[4][kW];
+      int h = next(warp);
+      if (h < h_end) load_keys(h, kw);
+      while (h < h_end) {
+        const int after = next(h + kSW);
+        const PageRec rec = sm.recs[h >> 1];
+        const int meta = sm.meta[h >> 1];
+        uint32_t vw[2][4][D / 32];
+        load_values(h, vw);
+        float sc[NT][2][4];
+        half_scores<D, NT>(kw, s0, sc, query);
+        if (after < h_end) load_keys(after, kw);
+        if (!(meta & (kMAll << (h & 1))))
+          half_mask<NT>(a, pos, (meta >> 4) * kBlk + (h & 1) * kHalf, g, sc);
+        bool raise = false;
+        float c[NT][2], big[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            // (a scale of 0 must not turn a masked -inf into a NaN)
+            c[n][x] = fmaxf(cs[n][x] * rec.ks * kUp, 1e-37f);
+            big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
+                              fmaxf(sc[n][1][x], sc[n][1][x + 2]));
+            raise = raise || fmaf(big[n][x], c[n][x], rec.lv) > ref[n][x] + kRLazy;
+          }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float scale[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float top = fmaf(big[n][x], c[n][x], rec.lv);  // -inf: no visible token
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+              scale[x] = 1.f;
+              if (top > ref[n][x] + kRLazy) {
+                scale[x] = exp2_approx(ref[n][x] - top);  // 0 for the row's first
+                sum[n][x] *= scale[x];
+                ref[n][x] = top;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float add = kROff + rec.lv - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int y = x; y < 4; y += 2) {
+                sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
+                part += sc[n][i][y];
+              }
+            // (scales that cannot be used: the rows that see the page, and only
+            // they, become NaN)
+            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rv, sum[n][x]);
+          }
+        }
+        half_products<D, NT>(sc, half2_bits(rec.any, rec.any), vw, o);
+        h = after;
+      }
+    }
+
+    // ---- the warps' results to one
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) sum[n][x] += __shfl_xor_sync(0xffffffffu, sum[n][x], k);
+        if (g == 0) sm.ml[warp][8 * n + 2 * t + x] = make_float2(ref[n][x], sum[n][x]);
+      }
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+      const int r = threadIdx.x;
+      float big = -INFINITY, l = 0.f, f[kSW];
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) {
+        const float2 v = sm.ml[w][r];
+        if (v.y != 0.f) big = fmaxf(big, v.x);
+      }
+      const float base = big == -INFINITY ? 0.f : big;
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) {
+        const float2 v = sm.ml[w][r];
+        f[w] = v.y == 0.f ? 0.f : exp2f(v.x - base);
+        if (v.y != 0.f) l = fmaf(v.y, f[w], l);
+      }
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) sm.fac[r][w] = l == 0.f ? 0.f : f[w] / l;
+      sm.weight[r] = part_weight(base, l);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+          *reinterpret_cast<float4*>(sm.merge + (warp * 8 + 2 * t + x) * kMStride + (D / 8) * g +
+                                     4 * q) =
+              make_float4(kUp * o[n][2 * q][x], kUp * o[n][2 * q][x + 2], kUp * o[n][2 * q + 1][x],
+                          kUp * o[n][2 * q + 1][x + 2]);
+      __syncthreads();
+      for (int i = threadIdx.x; i < 8 * (D / 4); i += kSThreads) {
+        const int row = i % 8, c = i / 8;
+        if (8 * n + row >= rows) continue;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kSW; ++w) {
+          const float f = sm.fac[8 * n + row][w];
+          const float4 v =
+              *reinterpret_cast<const float4*>(sm.merge + (w * 8 + row) * kMStride + 4 * c);
+          if (f != 0.f) {
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+        }
+        *kv_part_o(a, hk, slot, c, n0 + 8 * n + row) = acc;
+      }
+      if (n + 1 < NT) __syncthreads();
+    }
+    if (sm.far) {
+      // the pages left out join what has been written beside them
+      __syncthreads();
+      for (int r = warp; r < rows; r += kSW) {
+        const FarRow<D> f =
+            far_row<D>(a, sm.q + r * kQStride, sm.qscale[r] * a.scale_log2, sm.pos[r], table_row, hk,
+                       pages, begin, end);
+        constexpr int kV = D / 32;
+        float* to = reinterpret_cast<float*>(kv_part_o(a, hk, slot, lane * kV / 4, n0 + r)) +
+                    lane * kV % 4;
+        const float was = sm.weight[r], now = part_weight(f.ref, f.sum);
+        const float top = fmaxf(was, now), base = top == -INFINITY ? 0.f : top;
+        const float w0 = exp2f(was - base), w1 = exp2f(now - base), l = w0 + w1;
+        const float f0 = l == 0.f ? 0.f : w0 / l, f1 = l == 0.f ? 0.f : w1 / l;
+#pragma unroll
+        for (int y = 0; y < kV; ++y) to[y] = to[y] * f0 + f.o[y] * f1;
+        __syncwarp();
+        if (lane == 0) sm.weight[r] = part_weight(base, l);
+      }
+      __syncthreads();
+    }
+    write_weights(false);
+  }
+
+  // (every thread) none: the part has no pages
+  __device__ __forceinline__ void write_weights(bool none) {
+    const int r = threadIdx.x;
+    if (r < rows)
+      *kv_part_w(a, hk, slot, n0 + r) = sm.pos[r] < 0 ? __uint_as_float(kNoRow)
+                                        : none        ? -INFINITY
+                                                      : sm.weight[r];
+  }
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void span_part(const Kv8Args& a, int prefix_parts, int prefix_groups,
+                                          int own_parts, int groups, int max_rows) {
+  using S = Span<D, NT>;
+  __shared__ typename S::Smem sm;
+  const int lane = threadIdx.x & 31;
+  S s{a, sm, static_cast<int>(threadIdx.x >> 5), lane, lane >> 2, lane & 3};
+  int x = static_cast<int>(blockIdx.x);
+  const int pre = prefix_parts * prefix_groups * a.hkv;
+  const bool prefix = x < pre;
+  if (!prefix) x -= pre;
+  const int parts = prefix ? prefix_parts : own_parts;
+  const int part = x % parts;
+  x /= parts;
+  const int group = x % (prefix ? prefix_groups : groups);
+  x /= prefix ? prefix_groups : groups;
+  s.hk = x % a.hkv;
+  const int b = x / a.hkv;  // 0 for the prefix
+  const int r0 = group * S::kRows;
+  s.table_row = b;
+  s.slot = prefix ? part : a.prefix_parts + part;
+  int R;
+  if (prefix) {
+    // the rows' positions: those of the sequences that have them, -1 elsewhere
+    R = a.rows * a.group;
+    s.n0 = r0;
+    s.rows = R - r0 < S::kRows ? R - r0 : S::kRows;
+    if (threadIdx.x < S::kRows) sm.pos[threadIdx.x] = -1;
+    if (threadIdx.x == 0) sm.range[0] = 0x7FFFFFFF, sm.range[1] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.seqs; i += kSThreads) {
+      const KvSeq q = kv_seq(a, i);
+      if (!q.ok || q.m == 0) continue;
+      const long long first = static_cast<long long>(q.row0) * a.group;
+      const long long last = first + static_cast<long long>(q.m) * a.group;
+      for (int r = 0; r < s.rows; ++r) {
+        if (r0 + r < first || r0 + r >= last) continue;
+        const int p = a.shared + q.len - q.m + kv_token(a, r0 + r) - q.row0;
+        sm.pos[r] = p;
+        atomicMin(&sm.range[0], p);
+        atomicMax(&sm.range[1], p);
+      }
+    }
+    __syncthreads();
+    s.p_first = sm.range[0];
+    s.p_last = sm.range[1];
+    if (s.p_last < 0) {
+      s.write_weights(true);
+      return;
+    }
+  } else {
+    const KvSeq q = kv_seq(a, b);
+    if (!q.ok && part == 0 && group == 0 && s.hk == 0 && threadIdx.x == 0)
+      atomicOr(a.err, kErrIndex);
+    R = q.m * a.group;
+    if (!q.ok || R > max_rows || r0 >= R) return;
+    s.n0 = q.row0 * a.group + r0;
+    s.rows = R - r0 < S::kRows ? R - r0 : S::kRows;
+    s.p_first = a.shared + q.len - q.m;
+    s.p_last = a.shared + q.len - 1;
+    if (threadIdx.x < S::kRows)
+      sm.pos[threadIdx.x] = static_cast<int>(threadIdx.x) < s.rows
+                                ? s.p_first + kv_token(a, r0 + threadIdx.x)
+                                : -1;
+    __syncthreads();
+  }
+  // the pages that the rows see, before the prefix's end or behind it
+  const int common = a.shared / kBlk;
+  int first = 0, sinks = 0;
+  if (a.window > 0 && s.p_first >= a.window) {
+    first = (s.p_first - a.window + 1) / kBlk;
+    const int n = a.sinks / kBlk + (a.sinks % kBlk != 0);
+    sinks = n < first ? n : first;
+  }
+  int stop;
+  if (prefix) {
+    s.pages.f0 = first < common ? first : common;
+    s.pages.s0 = 0;
+    s.pages.s1 = sinks < s.pages.f0 ? sinks : s.pages.f0;
+    stop = common;
+  } else {
+    s.pages.f0 = first > common ? first : common;
+    s.pages.s0 = common;
+    s.pages.s1 = sinks > common ? sinks : common;
+    stop = s.p_last / kBlk + 1;
+  }
+  s.pages.count = s.pages.s1 - s.pages.s0 + stop - s.pages.f0;
+  const int begin = static_cast<int>(static_cast<long long>(s.pages.count) * part / parts);
+  const int end = static_cast<int>(static_cast<long long>(s.pages.count) * (part + 1) / parts);
+  if (begin == end)
+    s.write_weights(true);
+  else
+    s.run(begin, end);
+}
+
+// beside: the launch before this one is the prefix's on the tensor cores, which
+// neither writes what this one reads nor reads what it writes, and whose
+// dependents begin when all that came before it is done.  So this one waits for
+// it at its end alone (and is complete only when that one is).
+template <int D, int NT>
+__global__ void __launch_bounds__(kSThreads, NT == 1 ? 3 : 2)
+    kv8_span_kernel(const __grid_constant__ Kv8Args a, int prefix_parts, int prefix_groups,
+                    int own_parts, int groups, int max_rows, int beside) {
+  grid_dependents_launch();
+  if (!beside) grid_dependency_wait();
+  span_part<D, NT>(a, prefix_parts, prefix_groups, own_parts, groups, max_rows);
+  if (beside) grid_dependency_wait();
+}
+
+// The join.  A CTA takes kR rows of a key-value head: a warp makes the weights of
+// a row, then each thread adds four elements of one over the parts, whose chunks
+// are read 128 bytes at a time.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8Args a) {
+  constexpr int kR = kJoinThreads / (D / 4);
+  grid_dependents_launch();
+  extern __shared__ float weight[];  // [kR][parts]
+  __shared__ bool s_row[kR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = blockIdx.y;
+  const int n0 = blockIdx.x * kR;  // first row of the head
+  const int R = a.rows * a.group;
+  auto row_of = [&](int n) {
+    const int tok = kv_token(a, n);
+    return static_cast<long long>(tok) * a.heads + hk * a.group + (n - tok * a.group);
+  };
+  grid_dependency_wait();
+  for (int i = warp; i < kR; i += kJoinThreads / 32) {
+    float* w = weight + i * a.parts;
+    const float* from = kv_part_w(a, hk, 0, n0 + i);
+    const bool row = n0 + i < R && __float_as_uint(__ldcg(from)) != kNoRow;
+    if (lane == 0) s_row[i] = row;
+    if (!row) continue;
+    float top = -INFINITY;
+    for (int p = lane; p < a.parts; p += 32) {
+      const float x = __ldcg(from + static_cast<size_t>(p) * R);
+      w[p] = x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    for (int p = lane; p < a.parts; p += 32) {
+      w[p] = exp2f(w[p] - base);
+      l += w[p];
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    const float one = l == 0.f ? 0.f : 1.0f / l;
+    for (int p = lane; p < a.parts; p += 32) w[p] *= one;
+    if (a.lse && lane == 0) a.lse[row_of(n0 + i)] = kv_log_sum(base, l, kROff);
+  }
+  __syncthreads();
+  const int i = threadIdx.x % kR, c = threadIdx.x / kR;
+  if (!s_row[i]) return;
+  const float* w = weight + i * a.parts;
+  const float4* from = kv_part_o(a, hk, 0, c, n0 + i);
+  const size_t step = static_cast<size_t>(D / 4) * R;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAtOnce = 8;
+#pragma unroll 1
+  for (int p0 = 0; p0 < a.parts; p0 += kAtOnce) {
+    float4 v[kAtOnce];
+    float f[kAtOnce];
+#pragma unroll
+    for (int p = 0; p < kAtOnce; ++p) {
+      f[p] = p0 + p < a.parts ? w[p0 + p] : 0.f;
+      // (a part of no weight may never have been written)
+      if (f[p] != 0.f) v[p] = __ldcg(from + (p0 + p) * step);
+    }
+#pragma unroll
+    for (int p = 0; p < kAtOnce; ++p)
+      if (f[p] != 0.f) {
+        acc.x = fmaf(f[p], v[p].x, acc.x);
+        acc.y = fmaf(f[p], v[p].y, acc.y);
+        acc.z = fmaf(f[p], v[p].z, acc.z);
+        acc.w = fmaf(f[p], v[p].w, acc.w);
+      }
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row_of(n0 + i) * D + 4 * c) =
+      make_uint2(pack_out(a.type, acc.x, acc.y), pack_out(a.type, acc.z, acc.w));
+}
+
+// Rows (of all key-value heads) times parts that the workspace holds: a prefix's
+// blocks of 256 rows on the tensor cores are cut while there are fewer than two
+// for each SM, spans of up to 16 rows while there are fewer than kSpanCtas.
+constexpr long long kPrefixPartRows = 2ll * kSmallTMaxCtas * 256;
+constexpr long long kSpanPartRows = 16ll * kSpanCtas;
+// Parts of a row that spans cut the prefix, or its own tokens, into at most.
+// (The join's weights are in shared memory.)
+constexpr long long kSpanParts = 128;
+long long clamp_parts(long long parts, long long most, long long room, long long rows) {
+  if (parts > most) parts = most;
+  if (parts > kSpanParts) parts = kSpanParts;
+  if (parts * rows > room) parts = room / rows;
+  return parts < 1 ? 1 : parts;
+}
+
+}  // namespace
+
+bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
+  // (the spans' grid has up to kSpanRows / 8 CTAs a sequence and head)
+  return kv8_prompt_fits(rows, group, kv_heads, 1) &&
+         static_cast<long long>(seqs) * kv_heads <= (0x7FFFFFFFll - kSpanCtas) / (kSpanRows / 8);
+}
+
+size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim) {
+  const long long all = static_cast<long long>(rows) * heads;  // of all key-value heads
+  (void)kv_heads;
+  const long long prefix = all > kPrefixPartRows ? all : kPrefixPartRows;
+  const long long own = all > kSpanPartRows ? all : kSpanPartRows;
+  return static_cast<size_t>(prefix + own) * (dim + 1) * sizeof(float);
+}
+
+cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_sms,
+                              cudaStream_t stream, int* launches) {
+  const int R = a.rows * a.group;
+  const long long all = static_cast<long long>(R) * a.hkv;
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  const int common = a.shared / kBlk;
+  int pages = common, own_pages = a.width - common;  // seen, at most
+  if (a.window > 0) {
+    const long long seen = static_cast<long long>(a.window) / kBlk + 2;
+    const long long sinks = a.sinks / kBlk + 1;
+    if (seen + sinks < pages) pages = static_cast<int>(seen + sinks);
+    if (seen + a.max_new / kBlk + sinks < own_pages)
+      own_pages = static_cast<int>(seen + a.max_new / kBlk + sinks);
+  }
+  const int tiles = most <= 8 ? 1 : 2;
+  const int tile_rows = 8 * tiles;
+  const int groups =
+      static_cast<int>(((most < kSpanRows ? most : kSpanRows) + tile_rows - 1) / tile_rows);
+  const long long ctas = static_cast<long long>(a.seqs) * a.hkv * groups;
+  const bool prefix_spans = R <= kSpanPrefixRows;
+  const int prefix_groups = prefix_spans ? (R + tile_rows - 1) / tile_rows : 0;
+  a.prefix_parts =
+      prefix_spans
+          ? static_cast<int>(clamp_parts(kSpanCtas / 2 / (static_cast<long long>(a.hkv) * prefix_groups),
+                                         (pages + 1) / 2, kSpanPartRows, all))
+          : kv8_prefix_parts(a, pages, num_sms);
+  const int own_parts = static_cast<int>(
+      clamp_parts(kSpanCtas / ctas, (own_pages + 1) / 2, kSpanPartRows, all));
+  a.parts = a.prefix_parts + own_parts;
+  a.part_w = a.part_o + static_cast<size_t>(a.parts) * all * a.dim;
+
+  cudaError_t e;
+  if (!prefix_spans) {
+    e = launch_kv8_prompt(a, kKvPrefix, 1, nullptr, nullptr, num_sms, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  const long long grid =
+      ctas * own_parts + static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts;
+  cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),
+                                             dim3(kSThreads), 0, stream);
+  const auto span = tiles == 1 ? (a.dim == 128 ? kv8_span_kernel<128, 1> : kv8_span_kernel<64, 1>)
+                               : (a.dim == 128 ? kv8_span_kernel<128, 2> : kv8_span_kernel<64, 2>);
+  e = cudaLaunchKernelEx(&cfg, span, a, prefix_spans ? a.prefix_parts : 0, prefix_groups, own_parts,
+                         groups, kSpanRows, prefix_spans ? 0 : 1);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (most > kSpanRows) {
+    // (positions, pages and lengths from the prefix's end)
+    Kv8Args own = a;
+    own.table += common;
+    own.sinks = a.sinks > a.shared ? a.sinks - a.shared : 0;
+    e = launch_kv8_prompt(own, kKvOwn, kSpanRows + 1, partials, tickets, num_sms, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
+  const int kr = kJoinThreads / (a.dim / 4);
+  static_assert((2 * kSmallTMaxCtas + 2 * kSpanParts) * (kJoinThreads / 16) * sizeof(float) <= 48 << 10,
+                "the join's shared memory");
+  cfg = pdl_launch_config(attr, dim3((R - 1) / kr + 1, a.hkv), dim3(kJoinThreads),
+                          sizeof(float) * kr * a.parts, stream);
+  e = cudaLaunchKernelEx(&cfg, a.dim == 128 ? kv8_join_kernel<128> : kv8_join_kernel<64>, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  return cudaSuccess;
+}
+
+}  // namespace tern

@@ -5,6 +5,13 @@ Bar: that of test_gpu_kv8_attention.py.  The join of the prefix's and the own
 tokens' parts adds to it only what fp32 log-sum-exps round: at most 3 * 2^-24 of
 a log-sum-exp below 64 in size, 2^-16 of a part's weight, which the 5 * 2^-11
 there (4.5 of them in use) covers.
+
+One more term, for rows whose weight lies on tokens of small codes, where that
+bar is small: the values enter as code + 128 and -128 times the weights.  Within
+half a page's products the sums are at most 255 sum_j p_j v_scale_j in size and
+pass four tensor instructions (two of codes, two of the bias), each of which may
+cut 2^-23 of them: 4 * 255 * 2^-23 < 2^-13 times sum_j p_j v_scale_j over all
+tokens, beside sums of the size of the codes that are counted above.
 """
 import numpy as np
 import pytest
@@ -88,9 +95,16 @@ class Case:
                                                         np.maximum(np.diff(start), 1), lens),
                                                window, sinks,
                                                self.dim ** -0.5 if scale is None else scale)
+        ones = self.codes.copy()
+        ones[:, 1] = 1  # sum_j p_j v_scale_j
+        scales = od.kv8_attention(q, ones, self.scales, self.table, start,
+                                  np.where(np.isin(np.arange(len(lens)), skipped),
+                                           np.maximum(np.diff(start), 1), lens), window, sinks,
+                                  self.dim ** -0.5 if scale is None else scale)[2]
         got = out.double().cpu().numpy()
         assert np.all(got[~live] == 9) and np.all(lse.cpu().numpy()[~live] == 7)
         bound = 5 * 2.0 ** -11 * absum + 2.0 ** -9 * np.abs(ref) + 2.0 ** -25
+        bound = bound + 2.0 ** -13 * scales
         err = np.abs(got - ref)
         bad = ~(err <= bound) & live[:, None, None]
         assert not bad.any(), (int(bad.sum()), float(np.max((err / bound)[live])),
