@@ -94,10 +94,6 @@ __device__ __forceinline__ float* kv_part_w(const Kv8Args& a, int hk, int p, lon
 __device__ __forceinline__ float part_weight(float ref, float sum) {
   return sum == 0.f ? -INFINITY : ref + log2f(sum);
 }
-// In the first part's weight: a row of no sequence, or of a skipped one.  (A NaN
-// that no arithmetic makes.)
-constexpr uint32_t kNoRow = 0x7FCDEAD5u;
-
 // Whether any row at positions [p0, p1] sees one of the tokens [j0, j1].
 __device__ __forceinline__ bool kv_any(const Kv8Args& a, int p0, int p1, int j0, int j1) {
   return j0 <= p1 && (a.window == 0 || j1 > p0 - a.window || j0 < a.sinks);

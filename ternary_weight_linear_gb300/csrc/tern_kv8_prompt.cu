@@ -475,32 +475,36 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int p_first, p_last;
   KvPages pages;
   if constexpr (kMode == kKvPrefix) {
-    const int toks = kv_token(a, r0 + rows - 1) + 1;  // past the block's last
-    if (threadIdx.x < 2 * kPRows) tok_pos[threadIdx.x] = -1;
-    if (threadIdx.x == 0) {
-      pos_range[0] = INT_MAX;
-      pos_range[1] = -1;
-    }
-    cta_barrier();
-    for (int i = threadIdx.x; i < a.seqs; i += kPThreads) {
-      const KvSeq s = kv_seq(a, i);
-      if (!s.ok || s.m == 0) continue;
-      const int t0 = s.row0 > tok0 ? s.row0 : tok0;
-      const int t1 = s.row0 + s.m < toks ? s.row0 + s.m : toks;
-      const int from = a.shared + s.len - s.m - s.row0;  // position of row 0
-      for (int t = t0; t < t1; ++t) tok_pos[t - tok0] = from + t;
-      if (t0 < t1) {
-        atomicMin(&pos_range[0], from + t0);
-        atomicMax(&pos_range[1], from + t1 - 1);
+    p_first = p_last = a.shared;
+    if (a.window > 0) {
+      // the positions, which choose what is seen (without a window all rows see
+      // all of it, those of no sequence too: the join leaves them out)
+      const int toks = kv_token(a, r0 + rows - 1) + 1;  // past the block's last
+      if (threadIdx.x < 2 * kPRows) tok_pos[threadIdx.x] = -1;
+      if (threadIdx.x == 0) {
+        pos_range[0] = INT_MAX;
+        pos_range[1] = -1;
       }
-    }
-    cta_barrier();
-    p_first = pos_range[0];
-    p_last = pos_range[1];
-    if (p_last < 0) {  // none of the block's rows belongs to a sequence
-      if (threadIdx.x < rows)
-        *kv_part_w(a, hk, part, r0 + threadIdx.x) = __uint_as_float(kNoRow);
-      return;
+      cta_barrier();
+      for (int i = threadIdx.x; i < a.seqs; i += kPThreads) {
+        const KvSeq s = kv_seq(a, i);
+        if (!s.ok || s.m == 0) continue;
+        const int t0 = s.row0 > tok0 ? s.row0 : tok0;
+        const int t1 = s.row0 + s.m < toks ? s.row0 + s.m : toks;
+        const int from = a.shared + s.len - s.m - s.row0;  // position of row 0
+        for (int t = t0; t < t1; ++t) tok_pos[t - tok0] = from + t;
+        if (t0 < t1) {
+          atomicMin(&pos_range[0], from + t0);
+          atomicMax(&pos_range[1], from + t1 - 1);
+        }
+      }
+      cta_barrier();
+      p_first = pos_range[0];
+      p_last = pos_range[1];
+      if (p_last < 0) {  // none of the block's rows belongs to a sequence
+        if (threadIdx.x < rows) *kv_part_w(a, hk, part, r0 + threadIdx.x) = -INFINITY;
+        return;
+      }
     }
     pages = kv_prefix_pages(a, p_first);
   } else {
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tok = kv_token(a, rr);
     const int head = hk * a.group + rr - tok * a.group;
     const long long qrow = sq.row0 + tok;
-    if (live) pos = kMode == kKvPrefix ? tok_pos[tok - tok0] : p_base + tok;
+    if (live) pos = kMode != kKvPrefix ? p_base + tok : a.window > 0 ? tok_pos[tok - tok0] : p_first;
     // The warp's rows are copied to their places as they are, D / 8 lanes a
     // row, then each thread scales its own.
     const unsigned long long mine = reinterpret_cast<unsigned long long>(
@@ -1053,8 +1057,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (mine_out && live) {
       if constexpr (kMode == kKvPrefix)
-        *kv_part_w(a, hk, part, r0 + r) =
-            pos < 0 ? __uint_as_float(kNoRow) : part_weight(ref, sum);
+        *kv_part_w(a, hk, part, r0 + r) = part_weight(ref, sum);
       else if (!whole_rows)
         reinterpret_cast<float2*>(mine + 2 * kPRows * D)[r] = make_float2(ref, sum);
       else if (kMode == kKvOwn)

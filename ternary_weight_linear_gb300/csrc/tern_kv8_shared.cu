@@ -112,7 +112,9 @@ struct Span {
   }
 
   // The rows' queries in fp16, each scaled by a power of two; a row per warp.
-  __device__ __forceinline__ void stage_queries() {
+  // between: what is done while they are on their way.
+  template <typename Between>
+  __device__ __forceinline__ void stage_queries(const Between& between) {
     constexpr int kX = kRows / kSW;
     uint32_t raw[kX][D / 64];
 #pragma unroll
@@ -134,6 +136,7 @@ struct Span {
         }
       }
     }
+    between();
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       const int r = warp + x * kSW;
@@ -157,38 +160,45 @@ struct Span {
     }
   }
 
-  // Records of pages [c0, c0 + n) of the list.
-  __device__ __forceinline__ void make_records(int c0, int n) {
-    for (int i = threadIdx.x; i < n; i += kSThreads) {
-      const int lp = pages.page(c0 + i);
-      const int page = a.table[static_cast<size_t>(table_row) * a.width + lp];
-      PageRec rec = {0.f, 0.f, 1.f, 0.f};
-      int blk = -1, meta = lp * 16;
-      if (page < 0 || page >= a.pages) {
-        atomicOr(a.err, kErrIndex);
-      } else {
-        blk = page * 2 * a.hkv + hk;
-        const float ks = a.scales[blk], vs = a.scales[blk + a.hkv];
-        const bool far = far_scales(ks, vs);
-        if (far) sm.far = 1;
-        rec = page_rec(ks, vs);
+  // A thread's page of the table: entry c0 + threadIdx.x of the list, of n.
+  __device__ __forceinline__ int table_page(int c0, int n) const {
+    static_assert(kSpanRecs <= kSThreads, "a page per thread");
+    if (static_cast<int>(threadIdx.x) >= n) return -1;
+    return a.table[static_cast<size_t>(table_row) * a.width + pages.page(c0 + threadIdx.x)];
+  }
+  // Its record.
+  __device__ __forceinline__ void make_record(int c0, int n, int page) {
+    const int i = threadIdx.x;
+    if (i >= n) return;
+    const int lp = pages.page(c0 + i);
+    PageRec rec = {0.f, 0.f, 1.f, 0.f};
+    int blk = -1, meta = lp * 16;
+    if (page < 0 || page >= a.pages) {
+      atomicOr(a.err, kErrIndex);
+    } else {
+      blk = page * 2 * a.hkv + hk;
+      const float ks = a.scales[blk], vs = a.scales[blk + a.hkv];
+      const bool far = far_scales(ks, vs);
+      if (far) sm.far = 1;
+      rec = page_rec(ks, vs);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int j0 = lp * kBlk + hf * kHalf, j1 = j0 + kHalf - 1;
-          if (!far && kv_any(a, p_first, p_last, j0, j1)) meta |= kMHalf << hf;
-          if (kv_all(a, p_first, p_last, j0, j1)) meta |= kMAll << hf;
-        }
+      for (int hf = 0; hf < 2; ++hf) {
+        const int j0 = lp * kBlk + hf * kHalf, j1 = j0 + kHalf - 1;
+        if (!far && kv_any(a, p_first, p_last, j0, j1)) meta |= kMHalf << hf;
+        if (kv_all(a, p_first, p_last, j0, j1)) meta |= kMAll << hf;
       }
-      sm.recs[i] = rec;
-      sm.blk[i] = blk;
-      sm.meta[i] = meta;
     }
+    sm.recs[i] = rec;
+    sm.blk[i] = blk;
+    sm.meta[i] = meta;
   }
 
   // Pages [begin, end) of the list, into part `slot` of the rows.
   __device__ __forceinline__ void run(int begin, int end) {
-    if (threadIdx.x == 0) sm.far = 0;
-    stage_queries();
+    // the first pages' and the queries' dependent reads side by side
+    const int n_first = end - begin < kSpanRecs ? end - begin : kSpanRecs;
+    const int page = table_page(begin, n_first);
+    stage_queries([&] { make_record(begin, n_first, page); });
     __syncthreads();
 
     uint2 qf[NT == 1 ? kW : 1];  // one tile's query fragments
@@ -221,9 +231,11 @@ struct Span {
     constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
     for (int c0 = begin; c0 < end; c0 += kSpanRecs) {
       const int n_here = end - c0 < kSpanRecs ? end - c0 : kSpanRecs;
-      if (c0 > begin) __syncthreads();  // the records before have been read
-      make_records(c0, n_here);
-      __syncthreads();
+      if (c0 > begin) {
+        __syncthreads();  // the records before have been read
+        make_record(c0, n_here, table_page(c0, n_here));
+        __syncthreads();
+      }
       const int h_end = 2 * n_here;
       auto next = [&](int h) {  // the warp's half-page from h on that some row sees
         while (h < h_end && !(sm.meta[h >> 1] & (kMHalf << (h & 1)))) h += kSW;
@@ -388,10 +400,7 @@ struct Span {
   // (every thread) none: the part has no pages
   __device__ __forceinline__ void write_weights(bool none) {
     const int r = threadIdx.x;
-    if (r < rows)
-      *kv_part_w(a, hk, slot, n0 + r) = sm.pos[r] < 0 ? __uint_as_float(kNoRow)
-                                        : none        ? -INFINITY
-                                                      : sm.weight[r];
+    if (r < rows) *kv_part_w(a, hk, slot, n0 + r) = none ? -INFINITY : sm.weight[r];
   }
 };
 
@@ -402,6 +411,7 @@ __device__ __forceinline__ void span_part(const Kv8Args& a, int prefix_parts, in
   __shared__ typename S::Smem sm;
   const int lane = threadIdx.x & 31;
   S s{a, sm, static_cast<int>(threadIdx.x >> 5), lane, lane >> 2, lane & 3};
+  if (threadIdx.x == 0) sm.far = 0;  // (a barrier follows before it is set)
   int x = static_cast<int>(blockIdx.x);
   const int pre = prefix_parts * prefix_groups * a.hkv;
   const bool prefix = x < pre;
@@ -498,8 +508,9 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kSThreads, NT == 1 ? 3 : 2)
     kv8_span_kernel(const __grid_constant__ Kv8Args a, int prefix_parts, int prefix_groups,
                     int own_parts, int groups, int max_rows, int beside) {
-  grid_dependents_launch();
+  // (dependents may read the calls' inputs before they wait for this launch)
   if (!beside) grid_dependency_wait();
+  grid_dependents_launch();
   span_part<D, NT>(a, prefix_parts, prefix_groups, own_parts, groups, max_rows);
   if (beside) grid_dependency_wait();
 }
@@ -513,7 +524,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   constexpr int kR = kJoinThreads / (D / 4);
   grid_dependents_launch();
   extern __shared__ float weight[];  // [kR][parts]
-  __shared__ bool s_row[kR];
+  __shared__ bool s_row[kR];  // the row is one of a sequence that is not skipped
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
   const int n0 = blockIdx.x * kR;  // first row of the head
@@ -522,13 +533,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     const int tok = kv_token(a, n);
     return static_cast<long long>(tok) * a.heads + hk * a.group + (n - tok * a.group);
   };
+  // (the launch before this one begins its dependents when all that came before
+  // the call is done)
+  if (threadIdx.x < kR) s_row[threadIdx.x] = false;
+  __syncthreads();
+  const int tok0 = kv_token(a, n0), tok1 = kv_token(a, n0 + kR - 1 < R ? n0 + kR - 1 : R - 1);
+  for (int b = threadIdx.x; b < a.seqs; b += kJoinThreads) {
+    const KvSeq s = kv_seq(a, b);
+    if (!s.ok || s.row0 > tok1 || s.row0 + s.m <= tok0) continue;
+    for (int i = 0; i < kR; ++i) {
+      const int tok = kv_token(a, n0 + i);
+      if (n0 + i < R && tok >= s.row0 && tok < s.row0 + s.m) s_row[i] = true;
+    }
+  }
+  __syncthreads();
   grid_dependency_wait();
   for (int i = warp; i < kR; i += kJoinThreads / 32) {
     float* w = weight + i * a.parts;
     const float* from = kv_part_w(a, hk, 0, n0 + i);
-    const bool row = n0 + i < R && __float_as_uint(__ldcg(from)) != kNoRow;
-    if (lane == 0) s_row[i] = row;
-    if (!row) continue;
+    if (!s_row[i]) continue;
     float top = -INFINITY;
     for (int p = lane; p < a.parts; p += 32) {
       const float x = __ldcg(from + static_cast<size_t>(p) * R);
