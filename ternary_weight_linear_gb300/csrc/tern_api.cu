@@ -160,6 +160,7 @@ int device_state(DevState** out) {
     if (bf16_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (kv8_rows_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (kv8_prompt_set_attributes() != cudaSuccess) return TERN_ECUDA;
+    if (kv8_shared_set_attributes() != cudaSuccess) return TERN_ECUDA;
     if (!g_encode) {
       cudaDriverEntryPointQueryResult q;
       void* fn = nullptr;
@@ -379,6 +380,14 @@ int kv8_attention_args(const tern_kv8_cache* cache, const void* q, int type, lon
   return TERN_OK;
 }
 
+// The cache's codes for the few-row kernels.
+int kv8_codes_map(const Kv8Args& a, CUtensorMap* tm) {
+  const uint64_t dim = static_cast<uint64_t>(a.dim);
+  return make_map_u8(tm, a.codes, dim, static_cast<uint64_t>(a.pages) * 2 * a.hkv * TERN_KV8_BLOCK,
+                     dim, static_cast<uint32_t>(dim), kKvRowsBox,
+                     a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // The attention's launches, with the workspace that tern_kv8_attention asks for.
 int run_kv8_attention(Kv8Args a, uint8_t* workspace, const DevState* d, cudaStream_t st,
                       int* launches) {
@@ -386,11 +395,7 @@ int run_kv8_attention(Kv8Args a, uint8_t* workspace, const DevState* d, cudaStre
   a.partials = reinterpret_cast<float*>(workspace + kSyncBytes);
   a.err = d->err;
   CUtensorMap tm;
-  const uint64_t dim = static_cast<uint64_t>(a.dim);
-  const int rc = make_map_u8(&tm, a.codes, dim,
-                             static_cast<uint64_t>(a.pages) * 2 * a.hkv * TERN_KV8_BLOCK, dim,
-                             static_cast<uint32_t>(dim), kKvRowsBox,
-                             a.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  const int rc = kv8_codes_map(a, &tm);
   if (rc != TERN_OK) return rc;
   // Each sequence goes by its own rows: few of them per key-value head to the
   // kernel that is bound by the cache's bytes, more to the one on the tensor
@@ -944,7 +949,10 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
     a.shared = shared;
     a.part_o = reinterpret_cast<float*>(ws + base);
     a.err = d->err;
-    if (launch_kv8_shared(a,
+    CUtensorMap tm;
+    rc = kv8_codes_map(a, &tm);
+    if (rc != TERN_OK) return rc;
+    if (launch_kv8_shared(&tm, a,
                           reinterpret_cast<float*>(ws + kSyncBytes + kv8_rows_partial_bytes(a.dim)),
                           static_cast<int*>(workspace) + kPromptTickets, d->sms, st,
                           &launches) != cudaSuccess)

@@ -329,11 +329,12 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
                               int* tickets, int num_sms, cudaStream_t stream, int* launches);
 
 // Attention behind a shared prefix (a.shared, a.behind set, a.part_o at the
-// parts' memory): all its launches.  partials, tickets: as for launch_kv8_prompt.
+// parts' memory): all its launches.  tm as for launch_kv8_rows; partials, tickets: as for launch_kv8_prompt.
 bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs);
 size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim);
-cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_sms,
-                              cudaStream_t stream, int* launches);
+cudaError_t kv8_shared_set_attributes();
+cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials, int* tickets,
+                              int num_sms, cudaStream_t stream, int* launches);
 // Rows of a sequence and key-value head up to which its own tokens are its spans'.
 constexpr int kSpanRows = 64;
 // Parts of the prefix's blocks of rows on the tensor cores, by its pages.

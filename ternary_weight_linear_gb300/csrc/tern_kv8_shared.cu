@@ -27,7 +27,7 @@ namespace {
 constexpr int kSW = 4;           // warps of a span's CTA
 constexpr int kSThreads = 32 * kSW;
 constexpr int kSpanRecs = 32;    // pages whose records are held at a time
-constexpr int kSpanCtas = 1216;  // CTAs that own tokens (or a prefix) are cut into, at most
+constexpr int kSpanCtas = 608;  // CTAs that own tokens (or a prefix) are cut into, at most
 constexpr int kSpanPrefixRows = 32;
 
 // The pages of a span's list: [s0, s1), then from f0 on.
@@ -43,10 +43,11 @@ struct SpanPages {
 // the cache's bytes where there are many pages, by latency elsewhere: small CTAs
 // without barriers in the loop, of which an SM holds several, so that one's
 // dependent reads (lengths, table, scales, codes) pass under another's work.
-// Codes go from global memory straight to the registers of the tensor
-// instructions (each 128-byte line is read whole by eight or four lanes): a
-// half-page's values while its scores are made, the next one's keys while its
-// values are used.
+// Each warp takes every fourth half-page through a ring of TMA boxes of its own,
+// kStages ahead.  (Loads straight to the registers of the tensor instructions,
+// the values' under the scores and the next keys' under the values, left each
+// half-page waiting for its values: 52 us instead of 47 for 32 sequences behind
+// 16384 tokens, with 40 to 1500 of their own.)
 template <int D, int NT>
 struct Span {
   static constexpr int kRows = 8 * NT;
@@ -56,9 +57,15 @@ struct Span {
   static constexpr int kMStride = D + 4;
   static constexpr bool kBiased = biased(NT);
 
+  static constexpr int kStage = 2 * kHalf * D;  // bytes: keys, then values
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRing = kSW * kStages * kStage;
+  static_assert(kSW * 8 * kMStride * sizeof(float) <= kRing, "the merge is in the ring's place");
+
   struct Smem {
+    alignas(1024) uint8_t ring[kRing];  // [warp][stage]
     alignas(16) uint8_t q[kRows * kQStride];
-    alignas(16) float merge[kSW * 8 * kMStride];
+    uint64_t full[kSW][kStages];
     alignas(16) PageRec recs[kSpanRecs];
     int blk[kSpanRecs];   // its place among the cache's (page, keys, head); -1: none
     int meta[kSpanRecs];  // its number in the sequence * 16, kMHalf, kMAll
@@ -70,6 +77,7 @@ struct Span {
     int far;
   };
 
+  const CUtensorMap& tm;
   const Kv8Args& a;
   Smem& sm;
   int warp, lane, g, t;
@@ -78,37 +86,16 @@ struct Span {
   int p_first, p_last;
   SpanPages pages;
 
-  // a lane's codes of half-page h
-  __device__ __forceinline__ const int8_t* half_at(int h, int values) const {
-    return a.codes + (static_cast<size_t>(sm.blk[h >> 1]) + values * a.hkv) * (kBlk * D) +
-           (h & 1) * (kHalf * D);
-  }
-  __device__ __forceinline__ void load_keys(int h, uint32_t (&kw)[4][kW]) const {
-    const int8_t* from = half_at(h, 0) + 2 * kW * 2 * t;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-#pragma unroll
-      for (int i = 0; i < kW / 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(from + (8 * n + g) * D + 16 * i);
-        kw[n][4 * i] = x.x, kw[n][4 * i + 1] = x.y, kw[n][4 * i + 2] = x.z, kw[n][4 * i + 3] = x.w;
-      }
+  // (whole warp) half-page h into stage n % kStages of the warp's ring
+  __device__ __forceinline__ void request(int h, unsigned n) const {
+    if (lane == 0) {
+      uint64_t* full = &sm.full[warp][n % kStages];
+      uint8_t* to = sm.ring + (warp * kStages + n % kStages) * kStage;
+      const int row = sm.blk[h >> 1] * kBlk + (h & 1) * kHalf;
+      mbar_arrive_expect_tx(full, kStage);
+      tma_load_2d(to, &tm, 0, row, full);
+      tma_load_2d(to + kHalf * D, &tm, 0, row + a.hkv * kBlk, full);
     }
-  }
-  __device__ __forceinline__ void load_values(int h, uint32_t (&vw)[2][4][D / 32]) const {
-    const int8_t* from = half_at(h, 1) + (D / 8) * g;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int8_t* p = from + (16 * k + 2 * t + (x & 1) + 8 * (x >> 1)) * D;
-        if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p);
-          vw[k][x][0] = v.x, vw[k][x][1] = v.y, vw[k][x][2] = v.z, vw[k][x][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(p);
-          vw[k][x][0] = v.x, vw[k][x][1] = v.y;
-        }
-      }
   }
 
   // The rows' queries in fp16, each scaled by a power of two; a row per warp.
@@ -229,6 +216,7 @@ struct Span {
     }
 
     constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
+    unsigned issued = 0, used = 0;  // stages of the warp's ring
     for (int c0 = begin; c0 < end; c0 += kSpanRecs) {
       const int n_here = end - c0 < kSpanRecs ? end - c0 : kSpanRecs;
       if (c0 > begin) {
@@ -241,20 +229,27 @@ struct Span {
         while (h < h_end && !(sm.meta[h >> 1] & (kMHalf << (h & 1)))) h += kSW;
         return h;
       };
-      uint32_t kw[4][kW];
-      int h = next(warp);
-      if (h < h_end) load_keys(h, kw);
-      while (h < h_end) {
-        const int after = next(h + kSW);
+      int h = next(warp), ahead = h;
+      for (; ahead < h_end && issued - used < kStages; ahead = next(ahead + kSW))
+        request(ahead, issued++);
+      for (; h < h_end; h = next(h + kSW)) {
         const PageRec rec = sm.recs[h >> 1];
         const int meta = sm.meta[h >> 1];
-        uint32_t vw[2][4][D / 32];
-        load_values(h, vw);
+        const uint8_t* kb = sm.ring + (warp * kStages + used % kStages) * kStage;
+        const bool ok = __all_sync(
+            0xffffffffu, mbar_wait_clk(&sm.full[warp][used % kStages], (used / kStages) & 1, a.err));
+        if (!ok) break;
         float sc[NT][2][4];
-        half_scores<D, NT>(kw, s0, sc, query);
-        if (after < h_end) load_keys(after, kw);
+        {
+          uint32_t kw[4][kW];
+          half_keys<D>(kb, g, t, kw);
+          half_scores<D, NT>(kw, s0, sc, query);
+        }
         if (!(meta & (kMAll << (h & 1))))
           half_mask<NT>(a, pos, (meta >> 4) * kBlk + (h & 1) * kHalf, g, sc);
+        // the values' codes, on their way under the softmax
+        uint32_t vw[2][4][D / 32];
+        half_values<D>(kb + kHalf * D, g, t, vw);
         bool raise = false;
         float c[NT][2], big[NT][2];
 #pragma unroll
@@ -309,11 +304,20 @@ struct Span {
           }
         }
         half_products<D, NT>(sc, half2_bits(rec.any, rec.any), vw, o);
-        h = after;
+        __syncwarp();  // the stage has been read
+        ++used;
+        if (ahead < h_end) {
+          request(ahead, issued++);
+          ahead = next(ahead + kSW);
+        }
       }
     }
+    // (after a wait that ran out: no copy outlives the CTA)
+    for (; used < issued; ++used)
+      if (!mbar_wait_clk(&sm.full[warp][used % kStages], (used / kStages) & 1, a.err)) break;
 
     // ---- the warps' results to one
+    float* merge = reinterpret_cast<float*>(sm.ring);  // (behind the barrier below)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -323,7 +327,7 @@ struct Span {
         if (g == 0) sm.ml[warp][8 * n + 2 * t + x] = make_float2(ref[n][x], sum[n][x]);
       }
     __syncthreads();
-    if (threadIdx.x < kRows) {
+    if (threadIdx.x < kRows) {  // (the ring has been read, by every warp)
       const int r = threadIdx.x;
       float big = -INFINITY, l = 0.f, f[kSW];
 #pragma unroll
@@ -348,7 +352,7 @@ struct Span {
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int q = 0; q < D / 32; ++q)
-          *reinterpret_cast<float4*>(sm.merge + (warp * 8 + 2 * t + x) * kMStride + (D / 8) * g +
+          *reinterpret_cast<float4*>(merge + (warp * 8 + 2 * t + x) * kMStride + (D / 8) * g +
                                      4 * q) =
               make_float4(kUp * o[n][2 * q][x], kUp * o[n][2 * q][x + 2], kUp * o[n][2 * q + 1][x],
                           kUp * o[n][2 * q + 1][x + 2]);
@@ -361,7 +365,7 @@ struct Span {
         for (int w = 0; w < kSW; ++w) {
           const float f = sm.fac[8 * n + row][w];
           const float4 v =
-              *reinterpret_cast<const float4*>(sm.merge + (w * 8 + row) * kMStride + 4 * c);
+              *reinterpret_cast<const float4*>(merge + (w * 8 + row) * kMStride + 4 * c);
           if (f != 0.f) {
             acc.x = fmaf(f, v.x, acc.x);
             acc.y = fmaf(f, v.y, acc.y);
@@ -405,13 +409,20 @@ struct Span {
 };
 
 template <int D, int NT>
-__device__ __forceinline__ void span_part(const Kv8Args& a, int prefix_parts, int prefix_groups,
+__device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& a, int prefix_parts, int prefix_groups,
                                           int own_parts, int groups, int max_rows) {
   using S = Span<D, NT>;
-  __shared__ typename S::Smem sm;
+  extern __shared__ uint8_t smem_raw[];
+  typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(
+      smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int lane = threadIdx.x & 31;
-  S s{a, sm, static_cast<int>(threadIdx.x >> 5), lane, lane >> 2, lane & 3};
+  S s{tm, a, sm, static_cast<int>(threadIdx.x >> 5), lane, lane >> 2, lane & 3};
   if (threadIdx.x == 0) sm.far = 0;  // (a barrier follows before it is set)
+  if (lane == 0) {
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&sm.full[s.warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   int x = static_cast<int>(blockIdx.x);
   const int pre = prefix_parts * prefix_groups * a.hkv;
   const bool prefix = x < pre;
@@ -506,12 +517,13 @@ __device__ __forceinline__ void span_part(const Kv8Args& a, int prefix_parts, in
 // it at its end alone (and is complete only when that one is).
 template <int D, int NT>
 __global__ void __launch_bounds__(kSThreads, NT == 1 ? 3 : 2)
-    kv8_span_kernel(const __grid_constant__ Kv8Args a, int prefix_parts, int prefix_groups,
-                    int own_parts, int groups, int max_rows, int beside) {
+    kv8_span_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Kv8Args a,
+                    int prefix_parts, int prefix_groups, int own_parts, int groups,
+                    int max_rows, int beside) {
   // (dependents may read the calls' inputs before they wait for this launch)
   if (!beside) grid_dependency_wait();
   grid_dependents_launch();
-  span_part<D, NT>(a, prefix_parts, prefix_groups, own_parts, groups, max_rows);
+  span_part<D, NT>(tm, a, prefix_parts, prefix_groups, own_parts, groups, max_rows);
   if (beside) grid_dependency_wait();
 }
 
@@ -618,7 +630,25 @@ long long clamp_parts(long long parts, long long most, long long room, long long
   return parts < 1 ? 1 : parts;
 }
 
+// Shared memory of a span's CTA (whose layout starts on 1024 bytes).
+int span_bytes(int dim, int tiles) {
+  const size_t n = tiles == 1 ? (dim == 128 ? sizeof(Span<128, 1>::Smem) : sizeof(Span<64, 1>::Smem))
+                              : (dim == 128 ? sizeof(Span<128, 2>::Smem) : sizeof(Span<64, 2>::Smem));
+  return static_cast<int>(n) + 1024;
+}
+
 }  // namespace
+
+cudaError_t kv8_shared_set_attributes() {
+  const auto allow = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  cudaError_t e = allow(kv8_span_kernel<64, 1>, span_bytes(64, 1));
+  if (e == cudaSuccess) e = allow(kv8_span_kernel<64, 2>, span_bytes(64, 2));
+  if (e == cudaSuccess) e = allow(kv8_span_kernel<128, 1>, span_bytes(128, 1));
+  if (e == cudaSuccess) e = allow(kv8_span_kernel<128, 2>, span_bytes(128, 2));
+  return e;
+}
 
 bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
   // (the spans' grid has up to kSpanRows / 8 CTAs a sequence and head)
@@ -634,7 +664,7 @@ size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim) {
   return static_cast<size_t>(prefix + own) * (dim + 1) * sizeof(float);
 }
 
-cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_sms,
+cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials, int* tickets, int num_sms,
                               cudaStream_t stream, int* launches) {
   const int R = a.rows * a.group;
   const long long all = static_cast<long long>(R) * a.hkv;
@@ -657,7 +687,7 @@ cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_
   const int prefix_groups = prefix_spans ? (R + tile_rows - 1) / tile_rows : 0;
   a.prefix_parts =
       prefix_spans
-          ? static_cast<int>(clamp_parts(kSpanCtas / 2 / (static_cast<long long>(a.hkv) * prefix_groups),
+          ? static_cast<int>(clamp_parts(kSpanCtas * 3 / 4 / (static_cast<long long>(a.hkv) * prefix_groups),
                                          (pages + 1) / 2, kSpanPartRows, all))
           : kv8_prefix_parts(a, pages, num_sms);
   const int own_parts = static_cast<int>(
@@ -674,10 +704,10 @@ cudaError_t launch_kv8_shared(Kv8Args a, float* partials, int* tickets, int num_
   const long long grid =
       ctas * own_parts + static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts;
   cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),
-                                             dim3(kSThreads), 0, stream);
+                                             dim3(kSThreads), span_bytes(a.dim, tiles), stream);
   const auto span = tiles == 1 ? (a.dim == 128 ? kv8_span_kernel<128, 1> : kv8_span_kernel<64, 1>)
                                : (a.dim == 128 ? kv8_span_kernel<128, 2> : kv8_span_kernel<64, 2>);
-  e = cudaLaunchKernelEx(&cfg, span, a, prefix_spans ? a.prefix_parts : 0, prefix_groups, own_parts,
+  e = cudaLaunchKernelEx(&cfg, span, *tm, a, prefix_spans ? a.prefix_parts : 0, prefix_groups, own_parts,
                          groups, kSpanRows, prefix_spans ? 0 : 1);
   if (e != cudaSuccess) return e;
   ++*launches;
