@@ -292,7 +292,7 @@ struct Kv8Turn {
   long long q_ld, q_hd;
   void* out;
   int out_type;
-  int q_heads;  // heads of a CTA
+  int q_heads, q_cuts;  // heads of a CTA, CTAs that share a page's tokens
 };
 cudaError_t launch_kv8_append_rope(const Kv8Args& a, const Kv8Turn& t, cudaStream_t stream,
                                    int* launches);

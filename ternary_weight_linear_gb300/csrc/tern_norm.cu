@@ -204,11 +204,16 @@ cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
 //   y = (r w2) (mean(r^2) + eps)^-1/2;    codes and scale of y as above.
 // The same plan with a second reduction: one CTA per token, the row in
 // registers from the first load to the last store, so every input is read and
-// every output written once.  Rows of one vector a thread load what the second
-// half takes before the first barrier; longer ones, whose registers are the
-// row's, behind it.
-template <int XT, int RT, int NV>
-__global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a) {
+// every output written once.  Rows of one vector a thread load the residual before
+// the first barrier, longer ones, whose registers are the row's, behind it, as all
+// do with the weights and the gate, which other tokens' CTAs have left in L1.
+// (All of it before the barrier took 56 registers, one CTA of 640 threads an SM:
+// 41.8 us for 2048 rows of 5120, fp32 x, a gate a channel; now 25.4, bound by
+// instructions.  kBf16: weights and gate are all bf16, which saves the choice at
+// each load: 27.4 us with it.)
+template <int XT, int RT, int NV, bool kBf16>
+__global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
+    norm_pair_kernel(const NormPairArgs a) {
   grid_dependents_launch();
   __shared__ float red_x[32], red_s[32], red_m[32];
   const int t = blockIdx.x;
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a
   const long long xrow = static_cast<long long>(t) * a.x_ld;
   const long long grow = static_cast<long long>(t) * a.gate_ld;
   auto weight8 = [](const void* p, int type, long long i) {
-    return type == TERN_F32 ? load8<TERN_F32>(p, i) : load8<TERN_BF16>(p, i);
+    return !kBf16 && type == TERN_F32 ? load8<TERN_F32>(p, i) : load8<TERN_BF16>(p, i);
   };
   // what an element of the block's output is multiplied with beside its norm
   auto factors = [&](long long i) {
@@ -237,20 +242,16 @@ __global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a
     }
     return f;
   };
-  constexpr bool kEarly = NV == 1;
+  constexpr bool kEarly = NV <= 2;
   grid_dependency_wait();  // the inputs and the output buffers come from earlier work
-  F8 r[NV], f, res, w;
+  F8 r[NV], res[kEarly ? NV : 1];
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
     if (i < vecs) {
       r[j] = load8<XT>(a.x, xrow + 8ll * i);
-      if (kEarly) {
-        f = factors(8ll * i);
-        res = load8<RT>(a.residual, row + 8ll * i);
-        w = weight8(a.weight, a.weight_type, 8ll * i);
-      }
+      if (kEarly) res[j] = load8<RT>(a.residual, row + 8ll * i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(r[j].v[e], r[j].v[e], sum);
     }
@@ -272,18 +273,17 @@ __global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a
   for (int j = 0; j < NV; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
     if (i < vecs) {
-      if (!kEarly) {
-        // (the barriers to the compiler keep four vectors' loads out of each
-        // other's registers, which there are not enough of)
-        if (NV == 4) asm volatile("" ::: "memory");
-        f = factors(8ll * i);
-        res = load8<RT>(a.residual, row + 8ll * i);
-      }
+      // (the barriers to the compiler keep the loads out of each other's registers,
+      // which there are not enough of)
+      if (NV != 2) asm volatile("" ::: "memory");
+      const F8 f = factors(8ll * i);
+      F8& rs = res[kEarly ? j : 0];
+      if (!kEarly) rs = load8<RT>(a.residual, row + 8ll * i);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        r[j].v[e] = fmaf(r[j].v[e] * inv, f.v[e], a.residual_scale * res.v[e]);
-      if (NV == 4) asm volatile("" ::: "memory");
-      if (!kEarly) w = weight8(a.weight, a.weight_type, 8ll * i);
+        r[j].v[e] = fmaf(r[j].v[e] * inv, f.v[e], a.residual_scale * rs.v[e]);
+      if (NV != 2) asm volatile("" ::: "memory");
+      const F8 w = weight8(a.weight, a.weight_type, 8ll * i);
       round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -337,10 +337,13 @@ __global__ void __launch_bounds__(1024, 1) norm_pair_kernel(const NormPairArgs a
 
 template <int XT, int RT, int NV>
 cudaError_t launch_pair_one(const NormPairArgs& a, int threads, cudaStream_t stream) {
+  const bool bf16 = a.weight_type == TERN_BF16 && (!a.post || a.post_type == TERN_BF16) &&
+                    (!a.gate || a.gate_type == TERN_BF16);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       pdl_launch_config(attr, dim3(static_cast<unsigned>(a.T)), dim3(threads), 0, stream);
-  return cudaLaunchKernelEx(&cfg, norm_pair_kernel<XT, RT, NV>, a);
+  return cudaLaunchKernelEx(
+      &cfg, bf16 ? norm_pair_kernel<XT, RT, NV, true> : norm_pair_kernel<XT, RT, NV, false>, a);
 }
 
 template <int XT, int RT>

@@ -68,4 +68,25 @@ __device__ __forceinline__ uint2 quant_codes8(const float (&v)[8], float scale, 
   return make_uint2(lo, quant_codes4(v[4], v[5], v[6], v[7], scale, inv, fast));
 }
 
+
+// quant_codes4 for kernels that make codes at many places: the divisions, which
+// hardly any four values need, are a call there.
+static __device__ __noinline__ uint32_t quant_codes4_divided(float v0, float v1, float v2, float v3,
+                                                      float scale) {
+  return quant_codes4(v0, v1, v2, v3, scale, 0.f, false);
+}
+__device__ __forceinline__ uint32_t quant_codes4_short(const float (&v)[4], float scale, float inv,
+                                                       bool fast) {
+  constexpr float kMagic = 12582912.f;
+  const float m0 = fmaf(v[0], inv, kMagic), m1 = fmaf(v[1], inv, kMagic);
+  const float m2 = fmaf(v[2], inv, kMagic), m3 = fmaf(v[3], inv, kMagic);
+  const float far =
+      fmaxf(fmaxf(fabsf(fmaf(v[0], inv, kMagic - m0)), fabsf(fmaf(v[1], inv, kMagic - m1))),
+            fmaxf(fabsf(fmaf(v[2], inv, kMagic - m2)), fabsf(fmaf(v[3], inv, kMagic - m3))));
+  if (!(fast && far < 0.5f - kQMargin))
+    return quant_codes4_divided(v[0], v[1], v[2], v[3], scale);
+  return __byte_perm(__byte_perm(__float_as_uint(m0), __float_as_uint(m1), 0x0040),
+                     __byte_perm(__float_as_uint(m2), __float_as_uint(m3), 0x0040), 0x5410);
+}
+
 }  // namespace tern
