@@ -531,7 +531,55 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int w = (rows - (kSplit ? 0 : i * kPRows) + 31) / 32;
     return w < 0 ? 0 : w > 4 ? 4 : w;
   };
-  if (threadIdx.x == 0) {
+  // What the first pages' records and the queries are made of, on their way under
+  // the set-up (2200 cycles, most of them the TMEM's): a page for each of the threads
+  // that do not stage queries.
+  const int qt = warp >> 2;  // query tile (softmax warps)
+  const int tr = (warp & 3) * 32 + lane;  // row of the tile
+  const int r = (kSplit ? 0 : qt * kPRows) + tr;  // row of the block
+  const bool live = warp < kSoftW && r < rows;
+  const bool soft = warp < kSoftW && (warp & 3) < soft_warps(qt);
+  int pos = -1;  // the row's position
+  constexpr int kLanes = D / 8;
+  auto place = [&](int row, int c) {
+    return smem + L::kQOff + qt * L::kQTileB + (c >> 3) * L::kQBlockB + row * 128 +
+           (((c & 7) ^ (row & 7)) << 4);
+  };
+  int page0 = -1;
+  float ks0 = 0.f, vs0 = 0.f;
+  auto load_page_rec = [&](int lp, int& page, float& ks, float& vs) {
+    page = a.table[static_cast<size_t>(b) * a.width + lp];
+    if (page < 0 || page >= a.pages) {
+      page = -1;
+    } else {
+      const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
+      ks = sc[0];
+      vs = sc[a.hkv];
+    }
+  };
+  if (soft) {
+    const int rr = r0 + (live ? r : rows - 1);  // (past the last: a copy of it)
+    const int tok = kv_token(a, rr);
+    const int head = hk * a.group + rr - tok * a.group;
+    const long long qrow = sq.row0 + tok;
+    if (live) pos = kMode != kKvPrefix ? p_base + tok : a.window > 0 ? tok_pos[tok - tok0] : p_first;
+    // The warp's rows are copied to their places as they are, D / 8 lanes a
+    // row, then each thread scales its own.
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(
+        static_cast<const uint16_t*>(a.q) + qrow * a.ld + static_cast<long long>(head) * a.hd);
+#pragma unroll 4
+    for (int i = lane / kLanes; i < 32; i += 32 / kLanes)
+      cp_async_16(place((warp & 3) * 32 + i, lane % kLanes),
+                  reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, i)) +
+                      16 * (lane % kLanes),
+                  16);
+  }
+  if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
+  if (warp >= kSoftW) {
+    const int i = static_cast<int>(threadIdx.x) - kSoftW * 32;
+    if (i < t_end - t_begin && i < kPRecs) load_page_rec(pages.page(t_begin + i), page0, ks0, vs0);
+  }
+  if (threadIdx.x == kSoftW * 32) {
     for (int s = 0; s < L::kConv; ++s) {
       mbar_init(&k_full[s], kConvW);
       mbar_init(&v_full[s], kConvW);
@@ -547,7 +595,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
     mbar_init(mma_end, 4);
     fence_mbar_init();
   }
-  if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   cta_barrier();
   tc_fence_after();
@@ -557,36 +604,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   grid_dependents_launch();
 
   // ---- softmax warps: a row per thread
-  const int qt = warp >> 2;  // query tile (softmax warps)
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const int tr = (warp & 3) * 32 + lane;  // row of the tile
-  const int r = (kSplit ? 0 : qt * kPRows) + tr;  // row of the block
-  const bool live = warp < kSoftW && r < rows;
-  int pos = -1;           // its position
   float cs = 0.f;         // softmax scale * log2(e) * 2^-a
   float bias = 0.f;       // what 128 in every key's place adds to the row's scores
-  const bool soft = warp < kSoftW && (warp & 3) < soft_warps(qt);
   if (soft) {
-    const int rr = r0 + (live ? r : rows - 1);  // (past the last: a copy of it)
-    const int tok = kv_token(a, rr);
-    const int head = hk * a.group + rr - tok * a.group;
-    const long long qrow = sq.row0 + tok;
-    if (live) pos = kMode != kKvPrefix ? p_base + tok : a.window > 0 ? tok_pos[tok - tok0] : p_first;
-    // The warp's rows are copied to their places as they are, D / 8 lanes a
-    // row, then each thread scales its own.
-    const unsigned long long mine = reinterpret_cast<unsigned long long>(
-        static_cast<const uint16_t*>(a.q) + qrow * a.ld + static_cast<long long>(head) * a.hd);
-    constexpr int kLanes = D / 8;
-    auto place = [&](int row, int c) {
-      return smem + L::kQOff + qt * L::kQTileB + (c >> 3) * L::kQBlockB + row * 128 +
-             (((c & 7) ^ (row & 7)) << 4);
-    };
-#pragma unroll 4
-    for (int i = lane / kLanes; i < 32; i += 32 / kLanes)
-      cp_async_16(place((warp & 3) * 32 + i, lane % kLanes),
-                  reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, i)) +
-                      16 * (lane % kLanes),
-                  16);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     uint32_t m2 = 0;  // the largest magnitudes of the even and the odd elements
@@ -662,14 +683,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
       PageRec rec = {0.f, 0.f, 0.f, -1};
       {
         const int lp = pages.page(t0 + i);
-        int page = a.table[static_cast<size_t>(b) * a.width + lp];
-        if (page < 0 || page >= a.pages) {
+        int page = page0;
+        float ks = ks0, vs = vs0;
+        if (chunk > 0 || i >= kPThreads - kSoftW * 32) load_page_rec(lp, page, ks, vs);
+        if (page < 0) {
           atomicOr(a.err, kErrIndex);
-          page = -1;
         } else {
-          const float* sc = a.scales + static_cast<size_t>(page) * 2 * a.hkv + hk;
-          const float ks = sc[0];
-          const float vs = sc[a.hkv];
           // scales that cannot be used keep out of the arithmetic and make 1 / f
           // NaN
           const bool good = good_scales(ks, vs);
@@ -819,8 +838,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
       };
-      // (few rows: a page is read once, from HBM; a line per thread is
+      // (few rows, or a shared prefix: a page is read once, from HBM; lines are
       // requested into L2 kAhead pages before)
+      constexpr bool kRequest = kSplit || kMode == kKvPrefix;
       constexpr int kLines = L::kRawB / 128;  // of a page's keys or values
       auto request_page = [&](int j) {
         const int page = rec_page[j - jt];
@@ -828,15 +848,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           prefetch_l2(a.codes + ((static_cast<size_t>(page) * 2 + tid / kLines) * a.hkv + hk) *
                                     L::kRawB + tid % kLines * 128);
       };
-      if (kSplit)
+      if (kRequest)
         for (int j = jt + group; j < jt + kAhead && j < j_end; j += groups) request_page(j);
       if (!kSplit) load_page(jt);
       for (int j = jt + group; j < j_end; j += groups) {
         const int d = j % L::kConv;
-        if (kSplit) {
-          if (j + kAhead < j_end) request_page(j + kAhead);
-          load_page(j);
-        }
+        if (kRequest && j + kAhead < j_end) request_page(j + kAhead);
+        if (kSplit) load_page(j);
         ok = ok && (j < L::kConv ||
                     mbar_wait_clk(&conv_empty[d], ((j / L::kConv) & 1) ^ 1, a.err));
         ok = __all_sync(0xffffffffu, ok);

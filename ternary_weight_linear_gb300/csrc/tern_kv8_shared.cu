@@ -24,11 +24,13 @@
 namespace tern {
 namespace {
 
-constexpr int kSW = 4;           // warps of a span's CTA
+constexpr int kSW = 3;           // warps of a span's CTA
 constexpr int kSThreads = 32 * kSW;
 constexpr int kSpanRecs = 32;    // pages whose records are held at a time
-constexpr int kSpanCtas = 608;  // CTAs that own tokens (or a prefix) are cut into, at most
 constexpr int kSpanPrefixRows = 32;
+// CTAs of spans that an SM holds, by their tiles of rows (registers and rings).
+constexpr int span_ctas(int tiles) { return tiles == 1 ? 4 : 3; }
+constexpr int kSpanPages = 2;    // pages of a span at least, where there are more
 
 // The pages of a span's list: [s0, s1), then from f0 on.
 struct SpanPages {
@@ -43,7 +45,7 @@ struct SpanPages {
 // the cache's bytes where there are many pages, by latency elsewhere: small CTAs
 // without barriers in the loop, of which an SM holds several, so that one's
 // dependent reads (lengths, table, scales, codes) pass under another's work.
-// Each warp takes every fourth half-page through a ring of TMA boxes of its own,
+// Each warp takes every third half-page through a ring of TMA boxes of its own,
 // kStages ahead.  (Loads straight to the registers of the tensor instructions,
 // the values' under the scores and the next keys' under the values, left each
 // half-page waiting for its values: 52 us instead of 47 for 32 sequences behind
@@ -57,6 +59,7 @@ struct Span {
   static constexpr int kMStride = D + 4;
   static constexpr bool kBiased = biased(NT);
 
+  static constexpr int kFar = 1 << 30;  // (a place has less: 2^31 over a page's rows)
   static constexpr int kStage = 2 * kHalf * D;  // bytes: keys, then values
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kRing = kSW * kStages * kStage;
@@ -67,7 +70,7 @@ struct Span {
     alignas(16) uint8_t q[kRows * kQStride];
     uint64_t full[kSW][kStages];
     alignas(16) PageRec recs[kSpanRecs];
-    int blk[kSpanRecs];   // its place among the cache's (page, keys, head); -1: none
+    int blk[kSpanRecs];   // its place among the cache's (page, keys, head), kFar; -1: none
     int meta[kSpanRecs];  // its number in the sequence * 16, kMHalf, kMAll
     float2 ml[kSW][kRows];
     float fac[kRows][kSW];
@@ -86,12 +89,13 @@ struct Span {
   int p_first, p_last;
   SpanPages pages;
 
-  // (whole warp) half-page h into stage n % kStages of the warp's ring
-  __device__ __forceinline__ void request(int h, unsigned n) const {
+  // (whole warp) half h & 1 of the page at blk into stage n % kStages of the warp's
+  // ring
+  __device__ __forceinline__ void request(int blk, int h, unsigned n) const {
     if (lane == 0) {
       uint64_t* full = &sm.full[warp][n % kStages];
       uint8_t* to = sm.ring + (warp * kStages + n % kStages) * kStage;
-      const int row = sm.blk[h >> 1] * kBlk + (h & 1) * kHalf;
+      const int row = blk * kBlk + (h & 1) * kHalf;
       mbar_arrive_expect_tx(full, kStage);
       tma_load_2d(to, &tm, 0, row, full);
       tma_load_2d(to + kHalf * D, &tm, 0, row + a.hkv * kBlk, full);
@@ -102,7 +106,7 @@ struct Span {
   // between: what is done while they are on their way.
   template <typename Between>
   __device__ __forceinline__ void stage_queries(const Between& between) {
-    constexpr int kX = kRows / kSW;
+    constexpr int kX = (kRows + kSW - 1) / kSW;
     uint32_t raw[kX][D / 64];
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
@@ -127,6 +131,7 @@ struct Span {
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       const int r = warp + x * kSW;
+      if (r >= kRows) break;
       uint32_t m2 = 0;
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) m2 = __vmaxu2(m2, raw[x][e] & 0x7FFF7FFFu);
@@ -171,9 +176,10 @@ struct Span {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int j0 = lp * kBlk + hf * kHalf, j1 = j0 + kHalf - 1;
-        if (!far && kv_any(a, p_first, p_last, j0, j1)) meta |= kMHalf << hf;
-        if (kv_all(a, p_first, p_last, j0, j1)) meta |= kMAll << hf;
+        if (kv_any(a, p_first, p_last, j0, j1)) meta |= kMHalf << hf;
+        if (!far && kv_all(a, p_first, p_last, j0, j1)) meta |= kMAll << hf;
       }
+      if (far) blk |= kFar;
     }
     sm.recs[i] = rec;
     sm.blk[i] = blk;
@@ -185,6 +191,24 @@ struct Span {
     // the first pages' and the queries' dependent reads side by side
     const int n_first = end - begin < kSpanRecs ? end - begin : kSpanRecs;
     const int page = table_page(begin, n_first);
+    // each warp's first half-pages are requested as soon as it has read where they
+    // are: lane l < kStages, the l-th
+    unsigned issued = 0, used = 0;  // stages of the warp's ring
+    {
+      const int h = warp + lane * kSW;
+      int blk = -1;
+      if (lane < kStages && h < 2 * n_first) {
+        const int lp = pages.page(begin + (h >> 1)), j0 = lp * kBlk + (h & 1) * kHalf;
+        const int at = a.table[static_cast<size_t>(table_row) * a.width + lp];
+        if (at >= 0 && at < a.pages && kv_any(a, p_first, p_last, j0, j0 + kHalf - 1))
+          blk = at * 2 * a.hkv + hk;
+      }
+#pragma unroll
+      for (int l = 0; l < kStages; ++l) {
+        const int at = __shfl_sync(0xffffffffu, blk, l);
+        if (at >= 0) request(at, warp + l * kSW, issued++);
+      }
+    }
     stage_queries([&] { make_record(begin, n_first, page); });
     __syncthreads();
 
@@ -216,7 +240,6 @@ struct Span {
     }
 
     constexpr float kUp = kBiased ? kCodeUp : 1.f;  // 1 over the codes' unit
-    unsigned issued = 0, used = 0;  // stages of the warp's ring
     for (int c0 = begin; c0 < end; c0 += kSpanRecs) {
       const int n_here = end - c0 < kSpanRecs ? end - c0 : kSpanRecs;
       if (c0 > begin) {
@@ -229,9 +252,9 @@ struct Span {
         while (h < h_end && !(sm.meta[h >> 1] & (kMHalf << (h & 1)))) h += kSW;
         return h;
       };
-      int h = next(warp), ahead = h;
+      int h = next(warp), ahead = next(c0 == begin ? warp + kStages * kSW : warp);
       for (; ahead < h_end && issued - used < kStages; ahead = next(ahead + kSW))
-        request(ahead, issued++);
+        request(sm.blk[ahead >> 1] & ~kFar, ahead, issued++);
       for (; h < h_end; h = next(h + kSW)) {
         const PageRec rec = sm.recs[h >> 1];
         const int meta = sm.meta[h >> 1];
@@ -245,8 +268,16 @@ struct Span {
           half_keys<D>(kb, g, t, kw);
           half_scores<D, NT>(kw, s0, sc, query);
         }
-        if (!(meta & (kMAll << (h & 1))))
-          half_mask<NT>(a, pos, (meta >> 4) * kBlk + (h & 1) * kHalf, g, sc);
+        if (!(meta & (kMAll << (h & 1)))) {
+          if (sm.blk[h >> 1] & kFar) {  // left to far_row: none of it here
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) sc[n][x >> 2][x & 3] = -INFINITY;
+          } else {
+            half_mask<NT>(a, pos, (meta >> 4) * kBlk + (h & 1) * kHalf, g, sc);
+          }
+        }
         // the values' codes, on their way under the softmax
         uint32_t vw[2][4][D / 32];
         half_values<D>(kb + kHalf * D, g, t, vw);
@@ -307,7 +338,7 @@ struct Span {
         __syncwarp();  // the stage has been read
         ++used;
         if (ahead < h_end) {
-          request(ahead, issued++);
+          request(sm.blk[ahead >> 1] & ~kFar, ahead, issued++);
           ahead = next(ahead + kSW);
         }
       }
@@ -408,9 +439,127 @@ struct Span {
   }
 };
 
+// The pages that rows at positions p_first to p_last see, before the prefix's end
+// or behind it.
+__device__ __forceinline__ SpanPages span_pages(const Kv8Args& a, bool prefix, int p_first,
+                                                int p_last) {
+  const int common = a.shared / kBlk;
+  int first = 0, sinks = 0;
+  if (a.window > 0 && p_first >= a.window) {
+    first = (p_first - a.window + 1) / kBlk;
+    const int n = a.sinks / kBlk + (a.sinks % kBlk != 0);
+    sinks = n < first ? n : first;
+  }
+  SpanPages v;
+  int stop;
+  if (prefix) {
+    v.f0 = first < common ? first : common;
+    v.s0 = 0;
+    v.s1 = sinks < v.f0 ? sinks : v.f0;
+    stop = common;
+  } else {
+    v.f0 = first > common ? first : common;
+    v.s0 = common;
+    v.s1 = sinks > common ? sinks : common;
+    stop = p_last / kBlk + 1;
+  }
+  v.count = v.s1 - v.s0 + stop - v.f0;
+  return v;
+}
+
+// The spans of the sequences' own tokens: those of a sequence with pages and rows
+// for the kernel are cut into parts of `quota` pages and fewer, the same for all,
+// so that a launch of `slots` CTAs that are resident at once has about as many spans
+// of about the same length, however long the sequences are.
+struct OwnJob {
+  int seq, part, parts, group, hk;
+  KvSeq s;
+  SpanPages pages;
+};
+template <int kRows>
+struct OwnJobs {
+  const Kv8Args& a;
+  int slots, max_parts, max_rows;
+  // sequence i's pages and row groups (none: 0)
+  __device__ __forceinline__ void sequence(int i, KvSeq& s, SpanPages& pages, int& groups) const {
+    groups = 0;
+    pages = {0, 0, 0, 0};
+    s = {0, 0, 0, true};
+    if (i >= a.seqs) return;
+    s = kv_seq(a, i);
+    const int rows = s.m * a.group;
+    if (s.ok && s.m > 0 && rows <= max_rows) {
+      groups = static_cast<unsigned>(rows + kRows - 1) / kRows;
+      pages = span_pages(a, false, a.shared + s.len - s.m, a.shared + s.len - 1);
+    }
+  }
+  // Job x, false if there are not as many.  Every warp finds it for itself, 32
+  // sequences at a time: no barrier, and few reads one after the other.
+  __device__ __forceinline__ bool find(unsigned x, OwnJob& job) const {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    SpanPages pages;
+    KvSeq s;
+    int groups;
+    // all pages (times heads and groups), and the spans if no sequence were cut;
+    // the same order of the same sums in every warp
+    float all = 0.f, least = 0.f;
+    for (int i0 = 0; i0 < a.seqs; i0 += 32) {
+      sequence(i0 + lane, s, pages, groups);
+      if (!s.ok && x == 0) atomicOr(a.err, kErrIndex);
+      all += static_cast<float>(pages.count) * static_cast<float>(groups);
+      least += static_cast<float>(groups);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+      all += __shfl_xor_sync(kAll, all, k);
+      least += __shfl_xor_sync(kAll, least, k);
+    }
+    const float heads = static_cast<float>(a.hkv), most = static_cast<float>(slots);
+    const float room = fmaxf(most - least * heads, 0.25f * most);
+    const int quota = max(kSpanPages, static_cast<int>(fminf(ceilf(all * heads / room), 1e9f)));
+    unsigned before = 0;
+    for (int i0 = 0; i0 < a.seqs; i0 += 32) {
+      if (a.seqs > 32) sequence(i0 + lane, s, pages, groups);
+      const unsigned cut =
+          (static_cast<unsigned>(pages.count) + quota - 1) / static_cast<unsigned>(quota);
+      const unsigned parts = cut < static_cast<unsigned>(max_parts) ? cut : max_parts;
+      const unsigned mine = groups > 0 ? parts * groups * a.hkv : 0u;
+      unsigned end = mine;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const unsigned up = __shfl_up_sync(kAll, end, k);
+        if (lane >= k) end += up;
+      }
+      const unsigned here = __ballot_sync(kAll, x - before - (end - mine) < mine);
+      if (here) {
+        const int from = __ffs(here) - 1;
+        unsigned at = x - before - __shfl_sync(kAll, end - mine, from);
+        job.seq = i0 + from;
+        job.parts = __shfl_sync(kAll, static_cast<int>(parts), from);
+        groups = __shfl_sync(kAll, groups, from);
+        const unsigned rest = at / static_cast<unsigned>(job.parts);
+        job.part = at - rest * job.parts;
+        job.hk = rest / static_cast<unsigned>(groups);
+        job.group = rest - job.hk * groups;
+        job.s.len = __shfl_sync(kAll, s.len, from);
+        job.s.m = __shfl_sync(kAll, s.m, from);
+        job.s.row0 = __shfl_sync(kAll, s.row0, from);
+        job.pages.s0 = __shfl_sync(kAll, pages.s0, from);
+        job.pages.s1 = __shfl_sync(kAll, pages.s1, from);
+        job.pages.f0 = __shfl_sync(kAll, pages.f0, from);
+        job.pages.count = __shfl_sync(kAll, pages.count, from);
+        return true;
+      }
+      before += __shfl_sync(kAll, end, 31);
+    }
+    return false;
+  }
+};
+
 template <int D, int NT>
-__device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& a, int prefix_parts, int prefix_groups,
-                                          int own_parts, int groups, int max_rows) {
+__device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& a,
+                                          int prefix_groups, int slots, int max_rows) {
   using S = Span<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(
@@ -423,24 +572,19 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
     fence_mbar_init();
   }
   __syncwarp();
-  int x = static_cast<int>(blockIdx.x);
-  const int pre = prefix_parts * prefix_groups * a.hkv;
-  const bool prefix = x < pre;
-  if (!prefix) x -= pre;
-  const int parts = prefix ? prefix_parts : own_parts;
-  const int part = x % parts;
-  x /= parts;
-  const int group = x % (prefix ? prefix_groups : groups);
-  x /= prefix ? prefix_groups : groups;
-  s.hk = x % a.hkv;
-  const int b = x / a.hkv;  // 0 for the prefix
-  const int r0 = group * S::kRows;
-  s.table_row = b;
-  s.slot = prefix ? part : a.prefix_parts + part;
-  int R;
-  if (prefix) {
+  const int pre = a.prefix_parts * prefix_groups * a.hkv;  // CTAs of the prefix
+  int part, parts;
+  if (static_cast<int>(blockIdx.x) < pre) {
+    int x = static_cast<int>(blockIdx.x);
+    parts = a.prefix_parts;
+    part = x % parts;
+    x /= parts;
+    const int r0 = x % prefix_groups * S::kRows;
+    s.hk = x / prefix_groups;
+    s.table_row = 0;
+    s.slot = part;
     // the rows' positions: those of the sequences that have them, -1 elsewhere
-    R = a.rows * a.group;
+    const int R = a.rows * a.group;
     s.n0 = r0;
     s.rows = R - r0 < S::kRows ? R - r0 : S::kRows;
     if (threadIdx.x < S::kRows) sm.pos[threadIdx.x] = -1;
@@ -466,43 +610,32 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
       s.write_weights(true);
       return;
     }
+    s.pages = span_pages(a, true, s.p_first, s.p_last);
   } else {
-    const KvSeq q = kv_seq(a, b);
-    if (!q.ok && part == 0 && group == 0 && s.hk == 0 && threadIdx.x == 0)
-      atomicOr(a.err, kErrIndex);
-    R = q.m * a.group;
-    if (!q.ok || R > max_rows || r0 >= R) return;
-    s.n0 = q.row0 * a.group + r0;
+    OwnJob job;
+    const OwnJobs<S::kRows> jobs{a, slots, a.parts - a.prefix_parts, max_rows};
+    if (!jobs.find(blockIdx.x - pre, job)) return;
+    part = job.part;
+    parts = job.parts;
+    s.hk = job.hk;
+    s.table_row = job.seq;
+    s.slot = a.prefix_parts + part;
+    s.pages = job.pages;
+    const int r0 = job.group * S::kRows, R = job.s.m * a.group;
+    s.n0 = job.s.row0 * a.group + r0;
     s.rows = R - r0 < S::kRows ? R - r0 : S::kRows;
-    s.p_first = a.shared + q.len - q.m;
-    s.p_last = a.shared + q.len - 1;
+    s.p_first = a.shared + job.s.len - job.s.m;
+    s.p_last = a.shared + job.s.len - 1;
     if (threadIdx.x < S::kRows)
       sm.pos[threadIdx.x] = static_cast<int>(threadIdx.x) < s.rows
                                 ? s.p_first + kv_token(a, r0 + threadIdx.x)
                                 : -1;
+    // the parts that the sequence does not have
+    if (part == 0 && threadIdx.x < s.rows)
+      for (int p = a.prefix_parts + parts; p < a.parts; ++p)
+        *kv_part_w(a, s.hk, p, s.n0 + threadIdx.x) = -INFINITY;
     __syncthreads();
   }
-  // the pages that the rows see, before the prefix's end or behind it
-  const int common = a.shared / kBlk;
-  int first = 0, sinks = 0;
-  if (a.window > 0 && s.p_first >= a.window) {
-    first = (s.p_first - a.window + 1) / kBlk;
-    const int n = a.sinks / kBlk + (a.sinks % kBlk != 0);
-    sinks = n < first ? n : first;
-  }
-  int stop;
-  if (prefix) {
-    s.pages.f0 = first < common ? first : common;
-    s.pages.s0 = 0;
-    s.pages.s1 = sinks < s.pages.f0 ? sinks : s.pages.f0;
-    stop = common;
-  } else {
-    s.pages.f0 = first > common ? first : common;
-    s.pages.s0 = common;
-    s.pages.s1 = sinks > common ? sinks : common;
-    stop = s.p_last / kBlk + 1;
-  }
-  s.pages.count = s.pages.s1 - s.pages.s0 + stop - s.pages.f0;
   const int begin = static_cast<int>(static_cast<long long>(s.pages.count) * part / parts);
   const int end = static_cast<int>(static_cast<long long>(s.pages.count) * (part + 1) / parts);
   if (begin == end)
@@ -516,27 +649,29 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
 // dependents begin when all that came before it is done.  So this one waits for
 // it at its end alone (and is complete only when that one is).
 template <int D, int NT>
-__global__ void __launch_bounds__(kSThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kSThreads, span_ctas(NT))
     kv8_span_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Kv8Args a,
-                    int prefix_parts, int prefix_groups, int own_parts, int groups,
-                    int max_rows, int beside) {
+                    int prefix_groups, int slots, int max_rows, int beside) {
   // (dependents may read the calls' inputs before they wait for this launch)
   if (!beside) grid_dependency_wait();
   grid_dependents_launch();
-  span_part<D, NT>(tm, a, prefix_parts, prefix_groups, own_parts, groups, max_rows);
+  span_part<D, NT>(tm, a, prefix_groups, slots, max_rows);
   if (beside) grid_dependency_wait();
 }
 
-// The join.  A CTA takes kR rows of a key-value head: a warp makes the weights of
-// a row, then each thread adds four elements of one over the parts, whose chunks
-// are read 128 bytes at a time.
+// The join.  A CTA takes kJoinRows (4, or 8 of many) rows of a key-value head: a warp makes the
+// weights of a row, then each thread adds four elements of one over every kG-th
+// part, the first of them loaded under the weights, and the kG sums are added in
+// their order.  It is a chain of a few dependent reads from L2: with all parts of
+// eight rows' elements in a thread's hands, batch after batch, it took 5 us more (32
+// sequences behind 16384 tokens, with 12 parts of their own).
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, int kJoinRows>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8Args a) {
-  constexpr int kR = kJoinThreads / (D / 4);
-  grid_dependents_launch();
+  constexpr int kR = kJoinRows, kC = D / 4, kG = kJoinThreads / (kR * kC);
   extern __shared__ float weight[];  // [kR][parts]
   __shared__ bool s_row[kR];  // the row is one of a sequence that is not skipped
+  __shared__ float4 sums[kG > 1 ? kG - 1 : 1][kR * kC];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
   const int n0 = blockIdx.x * kR;  // first row of the head
@@ -549,24 +684,36 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   // the call is done)
   if (threadIdx.x < kR) s_row[threadIdx.x] = false;
   __syncthreads();
-  const int tok0 = kv_token(a, n0), tok1 = kv_token(a, n0 + kR - 1 < R ? n0 + kR - 1 : R - 1);
+  const int last = n0 + kR < R ? n0 + kR : R;
+  const int tok0 = kv_token(a, n0), tok1 = kv_token(a, last - 1);
   for (int b = threadIdx.x; b < a.seqs; b += kJoinThreads) {
     const KvSeq s = kv_seq(a, b);
     if (!s.ok || s.row0 > tok1 || s.row0 + s.m <= tok0) continue;
-    for (int i = 0; i < kR; ++i) {
-      const int tok = kv_token(a, n0 + i);
-      if (n0 + i < R && tok >= s.row0 && tok < s.row0 + s.m) s_row[i] = true;
+    for (int n = n0; n < last; ++n) {
+      const int tok = kv_token(a, n);
+      if (tok >= s.row0 && tok < s.row0 + s.m) s_row[n - n0] = true;
     }
   }
   __syncthreads();
   grid_dependency_wait();
-  for (int i = warp; i < kR; i += kJoinThreads / 32) {
-    float* w = weight + i * a.parts;
-    const float* from = kv_part_w(a, hk, 0, n0 + i);
-    if (!s_row[i]) continue;
+  grid_dependents_launch();
+  const int i = threadIdx.x % kR, c = threadIdx.x / kR % kC, g = threadIdx.x / (kR * kC);
+  const bool mine = n0 + i < R && s_row[i];
+  const float4* from = kv_part_o(a, hk, 0, c, n0 + i);
+  const size_t step = static_cast<size_t>(kC) * R;
+  constexpr int kAtOnce = 8;
+  float4 v[kAtOnce];
+  // (a part of no weight may never have been written: what it holds is not used)
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k)
+    if (mine && g + k * kG < a.parts) v[k] = __ldcg(from + (g + k * kG) * step);
+  for (int r = warp; r < kR; r += kJoinThreads / 32) {
+    if (!s_row[r]) continue;
+    float* w = weight + r * a.parts;
+    const float* ws = kv_part_w(a, hk, 0, n0 + r);
     float top = -INFINITY;
     for (int p = lane; p < a.parts; p += 32) {
-      const float x = __ldcg(from + static_cast<size_t>(p) * R);
+      const float x = __ldcg(ws + static_cast<size_t>(p) * R);
       w[p] = x;
       top = fmaxf(top, x);
     }
@@ -582,51 +729,55 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
     const float one = l == 0.f ? 0.f : 1.0f / l;
     for (int p = lane; p < a.parts; p += 32) w[p] *= one;
-    if (a.lse && lane == 0) a.lse[row_of(n0 + i)] = kv_log_sum(base, l, kROff);
+    if (a.lse && lane == 0) a.lse[row_of(n0 + r)] = kv_log_sum(base, l, kROff);
   }
   __syncthreads();
-  const int i = threadIdx.x % kR, c = threadIdx.x / kR;
-  if (!s_row[i]) return;
   const float* w = weight + i * a.parts;
-  const float4* from = kv_part_o(a, hk, 0, c, n0 + i);
-  const size_t step = static_cast<size_t>(D / 4) * R;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAtOnce = 8;
+  if (mine) {
 #pragma unroll 1
-  for (int p0 = 0; p0 < a.parts; p0 += kAtOnce) {
-    float4 v[kAtOnce];
-    float f[kAtOnce];
+    for (int p0 = g;;) {
 #pragma unroll
-    for (int p = 0; p < kAtOnce; ++p) {
-      f[p] = p0 + p < a.parts ? w[p0 + p] : 0.f;
-      // (a part of no weight may never have been written)
-      if (f[p] != 0.f) v[p] = __ldcg(from + (p0 + p) * step);
-    }
-#pragma unroll
-    for (int p = 0; p < kAtOnce; ++p)
-      if (f[p] != 0.f) {
-        acc.x = fmaf(f[p], v[p].x, acc.x);
-        acc.y = fmaf(f[p], v[p].y, acc.y);
-        acc.z = fmaf(f[p], v[p].z, acc.z);
-        acc.w = fmaf(f[p], v[p].w, acc.w);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float f = p0 + k * kG < a.parts ? w[p0 + k * kG] : 0.f;
+        if (f == 0.f) continue;
+        acc.x = fmaf(f, v[k].x, acc.x);
+        acc.y = fmaf(f, v[k].y, acc.y);
+        acc.z = fmaf(f, v[k].z, acc.z);
+        acc.w = fmaf(f, v[k].w, acc.w);
       }
+      p0 += kAtOnce * kG;
+      if (p0 >= a.parts) break;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (p0 + k * kG < a.parts && w[p0 + k * kG] != 0.f)
+          v[k] = __ldcg(from + (p0 + k * kG) * step);
+    }
+  }
+  if (g > 0) sums[g - 1][threadIdx.x % (kR * kC)] = acc;
+  __syncthreads();
+  if (g > 0 || !mine) return;
+#pragma unroll
+  for (int k = 0; k < kG - 1; ++k) {
+    const float4 x = sums[k][threadIdx.x];
+    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
   }
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row_of(n0 + i) * D + 4 * c) =
       make_uint2(pack_out(a.type, acc.x, acc.y), pack_out(a.type, acc.z, acc.w));
 }
 
-// Rows (of all key-value heads) times parts that the workspace holds: a prefix's
-// blocks of 256 rows on the tensor cores are cut while there are fewer than two
-// for each SM, spans of up to 16 rows while there are fewer than kSpanCtas.
+// Rows (of all key-value heads) times parts that the workspace holds beside one
+// part of each: a prefix's blocks of 256 rows on the tensor cores are cut while there
+// are fewer than two for each SM.
 constexpr long long kPrefixPartRows = 2ll * kSmallTMaxCtas * 256;
-constexpr long long kSpanPartRows = 16ll * kSpanCtas;
+constexpr long long kSpanPartRows = 40960;
 // Parts of a row that spans cut the prefix, or its own tokens, into at most.
 // (The join's weights are in shared memory.)
 constexpr long long kSpanParts = 128;
-long long clamp_parts(long long parts, long long most, long long room, long long rows) {
+long long clamp_parts(long long parts, long long most, long long rows) {
   if (parts > most) parts = most;
   if (parts > kSpanParts) parts = kSpanParts;
-  if (parts * rows > room) parts = room / rows;
+  if (parts * rows > kSpanPartRows) parts = kSpanPartRows / rows;
   return parts < 1 ? 1 : parts;
 }
 
@@ -653,7 +804,7 @@ cudaError_t kv8_shared_set_attributes() {
 bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
   // (the spans' grid has up to kSpanRows / 8 CTAs a sequence and head)
   return kv8_prompt_fits(rows, group, kv_heads, 1) &&
-         static_cast<long long>(seqs) * kv_heads <= (0x7FFFFFFFll - kSpanCtas) / (kSpanRows / 8);
+         static_cast<long long>(seqs) * kv_heads <= (0x7FFFFFFFll - 4 * kSmallTMaxCtas) / (kSpanRows / 8) / 2;
 }
 
 size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim) {
@@ -683,15 +834,21 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   const int groups =
       static_cast<int>(((most < kSpanRows ? most : kSpanRows) + tile_rows - 1) / tile_rows);
   const long long ctas = static_cast<long long>(a.seqs) * a.hkv * groups;
+  const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
+  int slots = sms * span_ctas(tiles);
   const bool prefix_spans = R <= kSpanPrefixRows;
   const int prefix_groups = prefix_spans ? (R + tile_rows - 1) / tile_rows : 0;
-  a.prefix_parts =
-      prefix_spans
-          ? static_cast<int>(clamp_parts(kSpanCtas * 3 / 4 / (static_cast<long long>(a.hkv) * prefix_groups),
-                                         (pages + 1) / 2, kSpanPartRows, all))
-          : kv8_prefix_parts(a, pages, num_sms);
+  if (prefix_spans) {
+    // three quarters of the CTAs that are resident at once
+    a.prefix_parts = static_cast<int>(
+        clamp_parts(slots * 3 / 4 / (static_cast<long long>(a.hkv) * prefix_groups), (pages + 1) / 2,
+                    all));
+    slots -= slots * 3 / 4;
+  } else {
+    a.prefix_parts = kv8_prefix_parts(a, pages, num_sms);
+  }
   const int own_parts = static_cast<int>(
-      clamp_parts(kSpanCtas / ctas, (own_pages + 1) / 2, kSpanPartRows, all));
+      clamp_parts(slots, (own_pages + kSpanPages - 1) / kSpanPages, all));
   a.parts = a.prefix_parts + own_parts;
   a.part_w = a.part_o + static_cast<size_t>(a.parts) * all * a.dim;
 
@@ -701,14 +858,15 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];
-  const long long grid =
-      ctas * own_parts + static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts;
+  // (own tokens: see OwnJobs; what is left over finds no job)
+  long long jobs = ctas + slots / 4 > slots ? ctas + slots / 4 : slots;
+  if (jobs > ctas * own_parts) jobs = ctas * own_parts;
+  const long long grid = static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts + jobs;
   cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),
                                              dim3(kSThreads), span_bytes(a.dim, tiles), stream);
   const auto span = tiles == 1 ? (a.dim == 128 ? kv8_span_kernel<128, 1> : kv8_span_kernel<64, 1>)
                                : (a.dim == 128 ? kv8_span_kernel<128, 2> : kv8_span_kernel<64, 2>);
-  e = cudaLaunchKernelEx(&cfg, span, *tm, a, prefix_spans ? a.prefix_parts : 0, prefix_groups, own_parts,
-                         groups, kSpanRows, prefix_spans ? 0 : 1);
+  e = cudaLaunchKernelEx(&cfg, span, *tm, a, prefix_groups, slots, kSpanRows, prefix_spans ? 0 : 1);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (most > kSpanRows) {
@@ -719,12 +877,17 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     e = launch_kv8_prompt(own, kKvOwn, kSpanRows + 1, partials, tickets, num_sms, stream, launches);
     if (e != cudaSuccess) return e;
   }
-  const int kr = kJoinThreads / (a.dim / 4);
-  static_assert((2 * kSmallTMaxCtas + 2 * kSpanParts) * (kJoinThreads / 16) * sizeof(float) <= 48 << 10,
+  // four rows a CTA make twice as many threads of as many parts: for few rows
+  const int join_rows = all < 24ll * num_sms ? 4 : 8;
+  static_assert((2 * kSmallTMaxCtas + 2 * kSpanParts) * 8 * sizeof(float) <= 32 << 10,
                 "the join's shared memory");
-  cfg = pdl_launch_config(attr, dim3((R - 1) / kr + 1, a.hkv), dim3(kJoinThreads),
-                          sizeof(float) * kr * a.parts, stream);
-  e = cudaLaunchKernelEx(&cfg, a.dim == 128 ? kv8_join_kernel<128> : kv8_join_kernel<64>, a);
+  cfg = pdl_launch_config(attr, dim3((R - 1) / join_rows + 1, a.hkv), dim3(kJoinThreads),
+                          sizeof(float) * join_rows * a.parts, stream);
+  e = cudaLaunchKernelEx(
+      &cfg,
+      join_rows == 4 ? (a.dim == 128 ? kv8_join_kernel<128, 4> : kv8_join_kernel<64, 4>)
+                     : (a.dim == 128 ? kv8_join_kernel<128, 8> : kv8_join_kernel<64, 8>),
+      a);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;
