@@ -194,22 +194,23 @@ struct Span {
     // each warp's first half-pages are requested as soon as it has read where they
     // are: lane l < kStages, the l-th
     unsigned issued = 0, used = 0;  // stages of the warp's ring
-    {
-      const int h = warp + lane * kSW;
+    const int h_lane = warp + lane * kSW;
+    int at_lane = -1;
+    if (lane < kStages && h_lane < 2 * n_first)
+      at_lane = a.table[static_cast<size_t>(table_row) * a.width + pages.page(begin + (h_lane >> 1))];
+    stage_queries([&] {
       int blk = -1;
-      if (lane < kStages && h < 2 * n_first) {
-        const int lp = pages.page(begin + (h >> 1)), j0 = lp * kBlk + (h & 1) * kHalf;
-        const int at = a.table[static_cast<size_t>(table_row) * a.width + lp];
-        if (at >= 0 && at < a.pages && kv_any(a, p_first, p_last, j0, j0 + kHalf - 1))
-          blk = at * 2 * a.hkv + hk;
+      if (at_lane >= 0 && at_lane < a.pages) {
+        const int j0 = pages.page(begin + (h_lane >> 1)) * kBlk + (h_lane & 1) * kHalf;
+        if (kv_any(a, p_first, p_last, j0, j0 + kHalf - 1)) blk = at_lane * 2 * a.hkv + hk;
       }
 #pragma unroll
       for (int l = 0; l < kStages; ++l) {
         const int at = __shfl_sync(0xffffffffu, blk, l);
         if (at >= 0) request(at, warp + l * kSW, issued++);
       }
-    }
-    stage_queries([&] { make_record(begin, n_first, page); });
+      make_record(begin, n_first, page);
+    });
     __syncthreads();
 
     uint2 qf[NT == 1 ? kW : 1];  // one tile's query fragments
