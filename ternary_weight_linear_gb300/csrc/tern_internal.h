@@ -262,9 +262,9 @@ struct Kv8Args {
   // behind: the position that no new token may precede.
   int shared, behind;
   // Its parts: `parts` of every row, the prefix's first (prefix_parts of them),
-  // then those of the row's own tokens.  part_o: fp32, of unit weight, in chunks of
-  // four elements [kv_heads][parts][dim / 4][rows * group][4]; part_w: the base-2
-  // logarithm of their weight [kv_heads][parts][rows * group].
+  // then those of the row's own tokens.  part_o: fp32, of unit weight, [kv_heads]
+  // [parts][rows * group][dim], a row's chunks of four elements swizzled (kv_part_o);
+  // part_w: the base-2 logarithm of their weight [kv_heads][parts][rows * group].
   float* part_o;
   float* part_w;
   int parts, prefix_parts;

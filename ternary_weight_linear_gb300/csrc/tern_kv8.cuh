@@ -79,11 +79,12 @@ __device__ __forceinline__ KvPages kv_prefix_pages(const Kv8Args& a, int p0) {
 }
 
 // Row n of a key-value head in part p: chunk c of its output, and its weight
-// (behind a shared prefix; see Kv8Args).
+// (behind a shared prefix; see Kv8Args).  A row's chunks are swizzled by it: rows in
+// shared memory, a thread each, so copy to their places as they are.
 __device__ __forceinline__ float4* kv_part_o(const Kv8Args& a, int hk, int p, int c, long long n) {
   return reinterpret_cast<float4*>(a.part_o) +
-         ((static_cast<size_t>(hk) * a.parts + p) * (a.dim / 4) + c) *
-             static_cast<size_t>(a.rows * a.group) + n;
+         ((static_cast<size_t>(hk) * a.parts + p) * static_cast<size_t>(a.rows * a.group) + n) *
+             (a.dim / 4) + (c ^ (n & 7));
 }
 __device__ __forceinline__ float* kv_part_w(const Kv8Args& a, int hk, int p, long long n) {
   return a.part_w +

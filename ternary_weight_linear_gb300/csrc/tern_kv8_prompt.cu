@@ -994,6 +994,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     float* mine = partials + static_cast<size_t>(tail < 0 ? 0 : tail) * kPart;
     const int n = kSplit ? (jt + 1 - qt) >> 1 : jt;  // pages of the tile
     const bool have = n > 0 && __all_sync(0xffffffffu, ok && wait_values(qt, n - 1));
+    if (kMode == kKvPrefix && !kSplit) mbar_wait_clk(mma_end, 0, a.err);  // (of both tiles)
     tc_fence_after();
     float inv = sum == 0.f ? 0.f : exp2f(lead) / sum;
     float inv1 = 0.f;  // tile 1's share of the sum
@@ -1055,14 +1056,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
           *reinterpret_cast<uint4*>(put.staged(r, 2 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
           *reinterpret_cast<uint4*>(put.staged(r, 2 * q + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
-      } else if (live) {
-        const size_t step = kMode == kKvPrefix ? static_cast<size_t>(R) : 2 * kPRows;
-        float4* o = kMode == kKvPrefix
-                        ? kv_part_o(a, hk, part, 4 * q, r0 + r)
-                        : reinterpret_cast<float4*>(mine) + 4 * q * (2 * kPRows) + r;
+      } else if (kMode == kKvPrefix) {
+        // (every MMA has read its operands: rows in their place, as kv_part_o has them)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k * step] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          *reinterpret_cast<float4*>(smem + L::kQOff + r * (4 * D) + (((4 * q + k) ^ (r & 7)) << 4)) =
+              make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+      } else if (live) {
+        float4* o = reinterpret_cast<float4*>(mine) + 4 * q * (2 * kPRows) + r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k * (2 * kPRows)] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
       }
     }
     if (!kSplit && kMode != kKvOwn && whole_rows) {
@@ -1072,6 +1076,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (kSplit && qt) {
       *reinterpret_cast<float2*>(other + (D / 4) * kPRows) = make_float2(ref, sum);
       softmax_barrier();
+    }
+    if (kMode == kKvPrefix && mine_out) {
+      // the warp's rows are one piece of memory (a bulk copy of it would be waited for)
+      __syncwarp();
+      const int first = r - lane, count = rows - first < 32 ? rows - first : 32;
+      const uint8_t* from = smem + L::kQOff + first * (4 * D);
+      uint4* to = reinterpret_cast<uint4*>(kv_part_o(a, hk, part, 0, r0 + first));
+#pragma unroll 8
+      for (int i = lane; i < count * (D / 4); i += 32) to[i] = lds_v4(from + 16 * i);
     }
     if (mine_out && live) {
       if constexpr (kMode == kKvPrefix)

@@ -390,8 +390,8 @@ struct Span {
                           kUp * o[n][2 * q + 1][x + 2]);
       __syncthreads();
       for (int i = threadIdx.x; i < 8 * (D / 4); i += kSThreads) {
-        const int row = i % 8, c = i / 8;
-        if (8 * n + row >= rows) continue;
+        const int row = i / (D / 4), c = i % (D / 4);
+        if (8 * n + row >= rows) break;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kSW; ++w) {
@@ -698,22 +698,28 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
-  const int i = threadIdx.x % kR, c = threadIdx.x / kR % kC, g = threadIdx.x / (kR * kC);
+  const int c = threadIdx.x % kC, i = threadIdx.x / kC % kR, g = threadIdx.x / (kR * kC);
   const bool mine = n0 + i < R && s_row[i];
   const float4* from = kv_part_o(a, hk, 0, c, n0 + i);
-  const size_t step = static_cast<size_t>(kC) * R;
+  const size_t step = static_cast<size_t>(R) * kC;
   constexpr int kAtOnce = 8;
   float4 v[kAtOnce];
+  // a row's weights, a warp each: loaded ahead of the parts, which would hold them
+  // up
+  const float* ws = kv_part_w(a, hk, 0, n0 + warp);
+  const bool weigh = warp < kR && s_row[warp < kR ? warp : 0];
+  float first = -INFINITY;
+  if (weigh && lane < a.parts) first = __ldcg(ws + static_cast<size_t>(lane) * R);
   // (a part of no weight may never have been written: what it holds is not used)
 #pragma unroll
   for (int k = 0; k < kAtOnce; ++k)
     if (mine && g + k * kG < a.parts) v[k] = __ldcg(from + (g + k * kG) * step);
-  for (int r = warp; r < kR; r += kJoinThreads / 32) {
-    if (!s_row[r]) continue;
-    float* w = weight + r * a.parts;
-    const float* ws = kv_part_w(a, hk, 0, n0 + r);
-    float top = -INFINITY;
-    for (int p = lane; p < a.parts; p += 32) {
+  static_assert(kR <= kJoinThreads / 32, "a warp a row");
+  if (weigh) {
+    float* w = weight + warp * a.parts;
+    float top = first;
+    if (lane < a.parts) w[lane] = first;
+    for (int p = lane + 32; p < a.parts; p += 32) {
       const float x = __ldcg(ws + static_cast<size_t>(p) * R);
       w[p] = x;
       top = fmaxf(top, x);
@@ -730,7 +736,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
     const float one = l == 0.f ? 0.f : 1.0f / l;
     for (int p = lane; p < a.parts; p += 32) w[p] *= one;
-    if (a.lse && lane == 0) a.lse[row_of(n0 + r)] = kv_log_sum(base, l, kROff);
+    if (a.lse && lane == 0) a.lse[row_of(n0 + warp)] = kv_log_sum(base, l, kROff);
   }
   __syncthreads();
   const float* w = weight + i * a.parts;
