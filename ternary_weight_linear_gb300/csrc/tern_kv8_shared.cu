@@ -13,8 +13,8 @@
 // key-value head behind 16384 tokens).
 //
 // The launches:
-//   the prefix on the tensor cores (kv8_prompt_kernel), where the batch has more
-//   rows than kSpanPrefixRows; below it is spans too;
+//   the prefix on the tensor cores (kv8_prompt_kernel), where it is long for
+//   the batch's rows (kSpanPrefixUnits); otherwise it is spans too;
 //   spans (kv8_span_kernel), of sequences of up to kSpanRows rows, beside the
 //   former: it waits for it at its end only;
 //   longer sequences' own tokens by kv8_prompt_kernel;
@@ -27,10 +27,10 @@ namespace {
 constexpr int kSW = 3;           // warps of a span's CTA
 constexpr int kSThreads = 32 * kSW;
 constexpr int kSpanRecs = 32;    // pages whose records are held at a time
-constexpr int kSpanPrefixRows = 32;
 // CTAs of spans that an SM holds, by their tiles of rows (registers and rings).
-constexpr int span_ctas(int tiles) { return tiles == 1 ? 4 : 3; }
+constexpr int span_ctas(int tiles) { return 5 - tiles; }
 constexpr int kSpanPages = 2;    // pages of a span at least, where there are more
+constexpr long long kSpanPrefixUnits = 4500;
 
 // The pages of a span's list: [s0, s1), then from f0 on.
 struct SpanPages {
@@ -790,8 +790,10 @@ long long clamp_parts(long long parts, long long most, long long rows) {
 
 // Shared memory of a span's CTA (whose layout starts on 1024 bytes).
 int span_bytes(int dim, int tiles) {
-  const size_t n = tiles == 1 ? (dim == 128 ? sizeof(Span<128, 1>::Smem) : sizeof(Span<64, 1>::Smem))
-                              : (dim == 128 ? sizeof(Span<128, 2>::Smem) : sizeof(Span<64, 2>::Smem));
+  const size_t n =
+      tiles == 1   ? (dim == 128 ? sizeof(Span<128, 1>::Smem) : sizeof(Span<64, 1>::Smem))
+      : tiles == 2 ? (dim == 128 ? sizeof(Span<128, 2>::Smem) : sizeof(Span<64, 2>::Smem))
+                   : (dim == 128 ? sizeof(Span<128, 3>::Smem) : sizeof(Span<64, 3>::Smem));
   return static_cast<int>(n) + 1024;
 }
 
@@ -805,6 +807,8 @@ cudaError_t kv8_shared_set_attributes() {
   if (e == cudaSuccess) e = allow(kv8_span_kernel<64, 2>, span_bytes(64, 2));
   if (e == cudaSuccess) e = allow(kv8_span_kernel<128, 1>, span_bytes(128, 1));
   if (e == cudaSuccess) e = allow(kv8_span_kernel<128, 2>, span_bytes(128, 2));
+  if (e == cudaSuccess) e = allow(kv8_span_kernel<64, 3>, span_bytes(64, 3));
+  if (e == cudaSuccess) e = allow(kv8_span_kernel<128, 3>, span_bytes(128, 3));
   return e;
 }
 
@@ -836,21 +840,30 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     if (seen + a.max_new / kBlk + sinks < own_pages)
       own_pages = static_cast<int>(seen + a.max_new / kBlk + sinks);
   }
-  const int tiles = most <= 8 ? 1 : 2;
+  // tiles of eight rows of a span: those of a sequence, where three hold them, or two
+  // at a time
+  const int tiles = most <= 8 ? 1 : most > 16 && most <= 24 ? 3 : 2;
   const int tile_rows = 8 * tiles;
   const int groups =
       static_cast<int>(((most < kSpanRows ? most : kSpanRows) + tile_rows - 1) / tile_rows);
   const long long ctas = static_cast<long long>(a.seqs) * a.hkv * groups;
   const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
   int slots = sms * span_ctas(tiles);
-  const bool prefix_spans = R <= kSpanPrefixRows;
-  const int prefix_groups = prefix_spans ? (R + tile_rows - 1) / tile_rows : 0;
+  // The prefix is spans too while its pages, times heads and groups of rows, are few:
+  // each group reads them again.
+  const long long all_groups = (R + tile_rows - 1) / tile_rows;
+  const long long units = pages * all_groups * a.hkv;
+  const bool prefix_spans = units * (tiles == 3 ? 2 : 1) <= kSpanPrefixUnits;
+  const int prefix_groups = prefix_spans ? static_cast<int>(all_groups) : 0;
   if (prefix_spans) {
-    // three quarters of the CTAs that are resident at once
+    // its share of the CTAs that are resident at once, were the sequences half as long
+    // as the table has room for
+    const long long own_units = ctas * ((own_pages + 1) / 2);
+    long long share = slots * units / (units + own_units);
+    if (share > slots * 3 / 4) share = slots * 3 / 4;
     a.prefix_parts = static_cast<int>(
-        clamp_parts(slots * 3 / 4 / (static_cast<long long>(a.hkv) * prefix_groups), (pages + 1) / 2,
-                    all));
-    slots -= slots * 3 / 4;
+        clamp_parts(share / (a.hkv * all_groups), (pages + kSpanPages - 1) / kSpanPages, all));
+    slots -= static_cast<int>(share);
   } else {
     a.prefix_parts = kv8_prefix_parts(a, pages, num_sms);
   }
@@ -871,8 +884,9 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   const long long grid = static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts + jobs;
   cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),
                                              dim3(kSThreads), span_bytes(a.dim, tiles), stream);
-  const auto span = tiles == 1 ? (a.dim == 128 ? kv8_span_kernel<128, 1> : kv8_span_kernel<64, 1>)
-                               : (a.dim == 128 ? kv8_span_kernel<128, 2> : kv8_span_kernel<64, 2>);
+  const auto span = tiles == 1   ? (a.dim == 128 ? kv8_span_kernel<128, 1> : kv8_span_kernel<64, 1>)
+                    : tiles == 2 ? (a.dim == 128 ? kv8_span_kernel<128, 2> : kv8_span_kernel<64, 2>)
+                                 : (a.dim == 128 ? kv8_span_kernel<128, 3> : kv8_span_kernel<64, 3>);
   e = cudaLaunchKernelEx(&cfg, span, *tm, a, prefix_groups, slots, kSpanRows, prefix_spans ? 0 : 1);
   if (e != cudaSuccess) return e;
   ++*launches;
