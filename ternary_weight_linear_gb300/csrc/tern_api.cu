@@ -943,7 +943,7 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int launches = 0;
   a.behind = shared;
-  if (a.seqs == 1 || shared == 0) {
+  if (!kv8_shared_pays(a, shared)) {
     rc = run_kv8_attention(a, ws, d, st, &launches);
   } else {
     a.shared = shared;

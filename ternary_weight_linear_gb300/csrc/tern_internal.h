@@ -331,6 +331,8 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
 // Attention behind a shared prefix (a.shared, a.behind set, a.part_o at the
 // parts' memory): all its launches.  tm as for launch_kv8_rows; partials, tickets: as for launch_kv8_prompt.
 bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs);
+// Whether the prefix is worth launches of its own; otherwise each sequence reads it.
+bool kv8_shared_pays(const Kv8Args& a, int shared);
 size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim);
 cudaError_t kv8_shared_set_attributes();
 cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials, int* tickets,

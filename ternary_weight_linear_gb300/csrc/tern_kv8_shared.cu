@@ -468,10 +468,16 @@ __device__ __forceinline__ SpanPages span_pages(const Kv8Args& a, bool prefix, i
   return v;
 }
 
+// CTAs of spans that are resident at once: beside the prefix's launch, and after it;
+// the launch is for the former if that takes no spans of more than `longest` pages.
+struct SpanSlots {
+  int free, all, longest;
+};
+
 // The spans of the sequences' own tokens: those of a sequence with pages and rows
 // for the kernel are cut into parts of `quota` pages and fewer, the same for all,
-// so that a launch of `slots` CTAs that are resident at once has about as many spans
-// of about the same length, however long the sequences are.
+// so that a launch has about as many spans as CTAs are resident at once, of about the
+// same length, however long the sequences are.
 struct OwnJob {
   int seq, part, parts, group, hk;
   KvSeq s;
@@ -480,7 +486,8 @@ struct OwnJob {
 template <int kRows>
 struct OwnJobs {
   const Kv8Args& a;
-  int slots, max_parts, max_rows;
+  SpanSlots slots;
+  int max_parts, max_rows;
   // sequence i's pages and row groups (none: 0)
   __device__ __forceinline__ void sequence(int i, KvSeq& s, SpanPages& pages, int& groups) const {
     groups = 0;
@@ -516,9 +523,15 @@ struct OwnJobs {
       all += __shfl_xor_sync(kAll, all, k);
       least += __shfl_xor_sync(kAll, least, k);
     }
-    const float heads = static_cast<float>(a.hkv), most = static_cast<float>(slots);
-    const float room = fmaxf(most - least * heads, 0.25f * most);
-    const int quota = max(kSpanPages, static_cast<int>(fminf(ceilf(all * heads / room), 1e9f)));
+    all *= static_cast<float>(a.hkv);
+    least *= static_cast<float>(a.hkv);
+    auto quota_of = [&](int ctas) {
+      const float most = static_cast<float>(ctas);
+      const float room = fmaxf(most - least, 0.25f * most);
+      return max(kSpanPages, static_cast<int>(fminf(ceilf(all / room), 1e9f)));
+    };
+    int quota = quota_of(slots.free);
+    if (quota > slots.longest) quota = quota_of(slots.all);
     unsigned before = 0;
     for (int i0 = 0; i0 < a.seqs; i0 += 32) {
       if (a.seqs > 32) sequence(i0 + lane, s, pages, groups);
@@ -560,7 +573,8 @@ struct OwnJobs {
 
 template <int D, int NT>
 __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& a,
-                                          int prefix_groups, int slots, int max_rows) {
+                                          int prefix_groups, const SpanSlots& slots,
+                                          int max_rows) {
   using S = Span<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   typename S::Smem& sm = *reinterpret_cast<typename S::Smem*>(
@@ -652,7 +666,7 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
 template <int D, int NT>
 __global__ void __launch_bounds__(kSThreads, span_ctas(NT))
     kv8_span_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Kv8Args a,
-                    int prefix_groups, int slots, int max_rows, int beside) {
+                    int prefix_groups, SpanSlots slots, int max_rows, int beside) {
   // (dependents may read the calls' inputs before they wait for this launch)
   if (!beside) grid_dependency_wait();
   grid_dependents_launch();
@@ -788,6 +802,56 @@ long long clamp_parts(long long parts, long long most, long long rows) {
   return parts < 1 ? 1 : parts;
 }
 
+// How the SMs are shared between the prefix's blocks on the tensor cores and the
+// spans of the own tokens.  Both are chains of dependent reads before anything else,
+// so a prefix's CTAs on some of the SMs, with the spans beside them on the others,
+// often end before the two one after the other on all.  Times in us, measured: a
+// part of the prefix 7 and 0.95 a page of two tiles of rows (0.62 of one in its split
+// form; heads of 64 two thirds), a span 6.5 and 0.77 a page of one tile of eight rows,
+// 5 between two launches that follow each other.  The launch knows the table's width,
+// not the sequences' lengths: they are taken to be half of it and at most 16 pages.
+// 32 sequences of 40 to 1500 tokens behind 16384: 80 SMs and 72 take 37.7 us, all of
+// them for both 43.6; 16 of up to 300 behind 4096 15.8 and 20.9.
+struct Plan {
+  int parts;  // of the prefix
+  SpanSlots slots;
+};
+Plan plan_prefix(const Kv8Args& a, int pages, int own_pages, int tiles, long long ctas, int sms) {
+  const int R = a.rows * a.group, on = span_ctas(tiles);
+  const long long items = (R + 255ll) / 256 * a.hkv;
+  const double narrow = a.dim == 64 ? 0.65 : 1.0;
+  const double page = (R <= 64 ? 0.62 : 0.95) * narrow, own_page = 0.77 * narrow * (tiles + 1) / 2;
+  const int average = own_pages < 32 ? (own_pages + 1) / 2 : 16;
+  const int longest = own_pages < 32 ? own_pages : 32;
+  auto prefix = [&](long long parts) {
+    return static_cast<double>((items * parts + sms - 1) / sms) * (7 + page * ((pages + parts - 1) / parts));
+  };
+  auto own = [&](int slots) {
+    if (ctas > slots)
+      return static_cast<double>((ctas + slots - 1) / slots) * (6.5 + own_page * average) +
+             own_page * (longest - average);
+    const double room = slots - ctas > slots / 4 ? slots - ctas : slots / 4;
+    const double quota = ctas * average / room;
+    return 6.5 + own_page * (quota < longest ? quota : longest);
+  };
+  const int all = sms * on;
+  Plan best = {kv8_prefix_parts(a, pages, sms), {all, all, 1 << 30}};
+  double least = prefix(best.parts) + 5 + own(all);
+  for (long long p = 1; p * 2 <= pages && items * p <= sms - sms / 8; ++p) {
+    const int free = static_cast<int>(sms - items * p) * on;
+    // (one span more than the SMs take beside the prefix waits for its end: 55 us
+    // where 38 were to be had)
+    if (ctas > free - free / 10) break;
+    const double t1 = prefix(p), t2 = own(free), t = t1 > t2 ? t1 : t2;
+    if (t < least) {
+      least = t;
+      const int fit = static_cast<int>(1.5 * (t - 6.5) / own_page);
+      best = {static_cast<int>(p), {free, all, fit < longest ? longest : fit}};
+    }
+  }
+  return best;
+}
+
 // Shared memory of a span's CTA (whose layout starts on 1024 bytes).
 int span_bytes(int dim, int tiles) {
   const size_t n =
@@ -816,6 +880,22 @@ bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
   // (the spans' grid has up to kSpanRows / 8 CTAs a sequence and head)
   return kv8_prompt_fits(rows, group, kv_heads, 1) &&
          static_cast<long long>(seqs) * kv_heads <= (0x7FFFFFFFll - 4 * kSmallTMaxCtas) / (kSpanRows / 8) / 2;
+}
+
+// Sequences of few rows share at any length (the spans are no slower than the few-row
+// kernel for so short own tokens; 8 sequences of 300 behind 64: 13.1 us, each for
+// itself 14.9).  Prompt chunks are bound by the tensor cores, which do the same work
+// either way, and the parts' way through the workspace is lost: 3 chunks of 600 behind
+// 512 to 16384 take 158 to 763 us with shared pages and 65 to 567 without.  In a mixed
+// batch the shorter sequences win a pass over the prefix each (2 bytes an element, and
+// there are seqs - R / most of them at least) and all rows lose their parts (some 12).
+bool kv8_shared_pays(const Kv8Args& a, int shared) {
+  if (a.seqs == 1 || shared == 0) return false;
+  const long long R = static_cast<long long>(a.rows) * a.group;
+  const long long most = static_cast<long long>(a.max_new) * a.group;
+  if (most <= kSpanRows) return true;
+  const long long shorter = a.seqs - (R + most - 1) / most;
+  return shorter * shared > 6 * R;
 }
 
 size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim) {
@@ -848,7 +928,8 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
       static_cast<int>(((most < kSpanRows ? most : kSpanRows) + tile_rows - 1) / tile_rows);
   const long long ctas = static_cast<long long>(a.seqs) * a.hkv * groups;
   const int sms = num_sms < kSmallTMaxCtas ? num_sms : kSmallTMaxCtas;
-  int slots = sms * span_ctas(tiles);
+  const int all_slots = sms * span_ctas(tiles);
+  SpanSlots slots = {all_slots, all_slots, 1 << 30};
   // The prefix is spans too while its pages, times heads and groups of rows, are few:
   // each group reads them again.
   const long long all_groups = (R + tile_rows - 1) / tile_rows;
@@ -859,16 +940,18 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     // its share of the CTAs that are resident at once, were the sequences half as long
     // as the table has room for
     const long long own_units = ctas * ((own_pages + 1) / 2);
-    long long share = slots * units / (units + own_units);
-    if (share > slots * 3 / 4) share = slots * 3 / 4;
+    long long share = all_slots * units / (units + own_units);
+    if (share > all_slots * 3 / 4) share = all_slots * 3 / 4;
     a.prefix_parts = static_cast<int>(
         clamp_parts(share / (a.hkv * all_groups), (pages + kSpanPages - 1) / kSpanPages, all));
-    slots -= static_cast<int>(share);
+    slots.free = slots.all = all_slots - static_cast<int>(share);
   } else {
-    a.prefix_parts = kv8_prefix_parts(a, pages, num_sms);
+    const Plan plan = plan_prefix(a, pages, own_pages, tiles, ctas, sms);
+    a.prefix_parts = plan.parts;
+    slots = plan.slots;
   }
   const int own_parts = static_cast<int>(
-      clamp_parts(slots, (own_pages + kSpanPages - 1) / kSpanPages, all));
+      clamp_parts(slots.all, (own_pages + kSpanPages - 1) / kSpanPages, all));
   a.parts = a.prefix_parts + own_parts;
   a.part_w = a.part_o + static_cast<size_t>(a.parts) * all * a.dim;
 
@@ -879,7 +962,7 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   }
   cudaLaunchAttribute attr[1];
   // (own tokens: see OwnJobs; what is left over finds no job)
-  long long jobs = ctas + slots / 4 > slots ? ctas + slots / 4 : slots;
+  long long jobs = ctas + slots.all / 4 > slots.all ? ctas + slots.all / 4 : slots.all;
   if (jobs > ctas * own_parts) jobs = ctas * own_parts;
   const long long grid = static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts + jobs;
   cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),

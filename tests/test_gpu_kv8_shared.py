@@ -157,6 +157,23 @@ def test_verify_steps_and_prompt_chunks(tl, dim, new):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shared,new,launches", [
+    (640, [100] + [1] * 20, 3), (640, [11] + [1] * 9 + [0, 2], 3), (64 * 90, [300, 40] + [1] * 14, 4),
+    (64 * 90, [1] * 30 + [64], 4), (640, [2] * 6, 2), (64 * 90, [2] * 40, 3), (640, [60, 50, 1], 2),
+    (64, [3], 1)])
+def test_mixed_batches_and_which_launches(tl, dim, shared, new, launches):
+    """Prompt chunks among decode steps: shared where those are many, each for
+    itself otherwise; a launch for the prefix where it is long for the rows, one
+    for the spans, one for the chunks' own tokens, the join."""
+    c = Case(shared, [m + 70 for m in new], new, 12, 2, dim, seed=len(new))
+    c.check(tl)
+    c.run(tl)
+    assert tl.tern_last_launches() == launches
+    if launches > 2:
+        c.check(tl, window=shared - 30, sinks=70)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (130, 7), (400, 64), (600, 100),
                                           (900, 65), (100, 2000), (5000, 3)])
 def test_windows(tl, dim, window, sinks):
