@@ -20,7 +20,7 @@ struct KvSeq {
   bool ok;
 };
 
-__device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
+__device__ __forceinline__ KvSeq kv_whole_seq(const Kv8Args& a, int b) {
   KvSeq s;
   s.len = a.lens[b];
   s.row0 = a.starts[b];
@@ -29,7 +29,12 @@ __device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
   s.m = s.ok ? end - s.row0 : 0;
   s.ok = s.ok && s.len >= 0 && (static_cast<long long>(s.len) + kBlk - 1) / kBlk <= a.width &&
          s.m <= s.len && s.m <= a.max_new;
-  // (new tokens lie behind what the call shares)
+  return s;
+}
+// The same for attention, whose call may share the sequences' first tokens: the new
+// ones lie behind these.
+__device__ __forceinline__ KvSeq kv_seq(const Kv8Args& a, int b) {
+  KvSeq s = kv_whole_seq(a, b);
   s.ok = s.ok && (s.m == 0 || s.len - s.m >= a.behind);
   s.len -= a.shared;
   return s;

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
   __shared__ float red[kAppThreads / 32];
   const int b = blockIdx.z;
   const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
-  const KvSeq s = kv_seq(a, b);
+  const KvSeq s = kv_whole_seq(a, b);
   if (!s.ok) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrIndex);
     return;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kTurnHeads * kAppThreads, 4 / kTurnHeads)
   RopeUnit unit(t.rope, threadIdx.x % kUnits);
   if (at_q < 0 && which) unit = RopeUnit(RopeArgs{nullptr, 0, 0, 1.f}, threadIdx.x % kUnits);
   grid_dependency_wait();  // every input and the cache come from earlier work
-  const KvSeq s = kv_seq(a, b);
+  const KvSeq s = kv_whole_seq(a, b);
   if (!s.ok) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrIndex);
     return;
