@@ -754,6 +754,7 @@ int tern_norm_add_norm_s8(const void* x, int x_type, long long x_ld, const void*
   a.y = y;
   a.T = T;
   a.K = K;
+  a.inv_k = 1.0f / static_cast<float>(K);
   if (launch_norm_add_norm_s8(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return TERN_ECUDA;
   t_last_launches = 1;

@@ -204,6 +204,7 @@ struct NormPairArgs {
   const void* weight;
   int weight_type;
   float residual_scale, branch_scale, eps;
+  float inv_k;  // 1 / K
   int8_t* q;       // may be null
   float* x_scale;  // with q
   uint16_t* y;     // may be null

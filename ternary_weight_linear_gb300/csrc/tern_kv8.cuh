@@ -228,26 +228,6 @@ __device__ __forceinline__ float kv_log_sum(float ref, float sum, float off) {
   return sum == 0.f ? -INFINITY : (ref - off + log2f(sum)) * 0.6931471805599453f;
 }
 
-// fp32 pairs in one 64-bit register (each half as its scalar instruction).
-__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpair_f32(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // 2^k as an fp16 bit pattern for k <= 0 (0 below the smallest subnormal).
 __device__ __forceinline__ uint32_t half_pow2(int k) {
   return k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : (k >= -24 ? 1u << (k + 24) : 0u);

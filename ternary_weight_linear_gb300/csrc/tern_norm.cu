@@ -225,23 +225,6 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
   auto weight8 = [](const void* p, int type, long long i) {
     return !kBf16 && type == TERN_F32 ? load8<TERN_F32>(p, i) : load8<TERN_BF16>(p, i);
   };
-  // what an element of the block's output is multiplied with beside its norm
-  auto factors = [&](long long i) {
-    F8 f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = a.branch_scale;
-    if (a.post) {
-      const F8 p = weight8(a.post, a.post_type, i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f.v[e] *= p.v[e];
-    }
-    if (a.gate) {
-      const F8 g = weight8(a.gate, a.gate_type, grow + i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f.v[e] *= g.v[e];
-    }
-    return f;
-  };
   constexpr bool kEarly = NV <= 2;
   grid_dependency_wait();  // the inputs and the output buffers come from earlier work
   F8 r[NV], res[kEarly ? NV : 1];
@@ -252,11 +235,18 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
     if (i < vecs) {
       r[j] = load8<XT>(a.x, xrow + 8ll * i);
       if (kEarly) res[j] = load8<RT>(a.residual, row + 8ll * i);
+      uint64_t s2 = 0;  // pairs of sums from +0
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(r[j].v[e], r[j].v[e], sum);
+      for (int e = 0; e < 8; e += 2) {
+        const uint64_t x = pair_f32(r[j].v[e], r[j].v[e + 1]);
+        s2 = fma_pair(x, x, s2);
+      }
+      float s0, s1;
+      unpair_f32(s2, s0, s1);
+      sum += s0 + s1;
     }
   }
-  float inv = 1.f;
+  float inv = 1.f;  // of the block's output, with the branch's scale below
   if (a.post) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -265,8 +255,9 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
     sum = lane < warps ? red_x[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    inv = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
+    inv = rsqrtf(sum * a.inv_k + a.eps);
   }
+  inv *= a.branch_scale;
   sum = 0.f;
   float big = 0.f;
 #pragma unroll
@@ -276,21 +267,33 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
       // (the barriers to the compiler keep the loads out of each other's registers,
       // which there are not enough of)
       if (NV != 2) asm volatile("" ::: "memory");
-      const F8 f = factors(8ll * i);
       F8& rs = res[kEarly ? j : 0];
       if (!kEarly) rs = load8<RT>(a.residual, row + 8ll * i);
+      auto times = [&](const F8& f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        r[j].v[e] = fmaf(r[j].v[e] * inv, f.v[e], a.residual_scale * rs.v[e]);
+        for (int e = 0; e < 8; e += 2)
+          unpair_f32(mul_pair(pair_f32(r[j].v[e], r[j].v[e + 1]), pair_f32(f.v[e], f.v[e + 1])),
+                     r[j].v[e], r[j].v[e + 1]);
+      };
+      if (a.post) times(weight8(a.post, a.post_type, 8ll * i));
+      if (a.gate) times(weight8(a.gate, a.gate_type, grow + 8ll * i));
+      const uint64_t inv2 = pair_f32(inv, inv);
+      const uint64_t rs2 = pair_f32(a.residual_scale, a.residual_scale);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2)
+        unpair_f32(fma_pair(pair_f32(r[j].v[e], r[j].v[e + 1]), inv2,
+                            mul_pair(pair_f32(rs.v[e], rs.v[e + 1]), rs2)),
+                   r[j].v[e], r[j].v[e + 1]);
+      round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
       if (NV != 2) asm volatile("" ::: "memory");
       const F8 w = weight8(a.weight, a.weight_type, 8ll * i);
       round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum = fmaf(r[j].v[e], r[j].v[e], sum);
-        r[j].v[e] *= w.v[e];
+      for (int e = 0; e < 8; ++e) sum = fmaf(r[j].v[e], r[j].v[e], sum);
+      times(w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
         big = max_nan(big, fabsf(r[j].v[e]));  // (the weight's NaN is not in the sum)
-      }
     }
   }
 #pragma unroll
@@ -321,14 +324,21 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
     const int i = threadIdx.x + j * blockDim.x;
     if (i < vecs) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[j].v[e] *= inv;
+      for (int e = 0; e < 8; e += 2)
+        unpair_f32(mul_pair(pair_f32(r[j].v[e], r[j].v[e + 1]), pair_f32(inv, inv)), r[j].v[e],
+                   r[j].v[e + 1]);
       if (a.y)
         *reinterpret_cast<uint4*>(a.y + row + 8ll * i) =
             make_uint4(pack_bf16(r[j].v[0], r[j].v[1]), pack_bf16(r[j].v[2], r[j].v[3]),
                        pack_bf16(r[j].v[4], r[j].v[5]), pack_bf16(r[j].v[6], r[j].v[7]));
       if (a.q) {
         uint2 out = make_uint2(0u, 0u);
-        if (amax > 0.f) out = quant_codes8(r[j].v, scale, sinv, fast);
+        if (amax > 0.f) {
+          const float lo[4] = {r[j].v[0], r[j].v[1], r[j].v[2], r[j].v[3]};
+          const float hi[4] = {r[j].v[4], r[j].v[5], r[j].v[6], r[j].v[7]};
+          out.x = quant_codes4_short(lo, scale, sinv, fast);
+          out.y = quant_codes4_short(hi, scale, sinv, fast);
+        }
         *reinterpret_cast<uint2*>(a.q + row + 8ll * i) = out;
       }
     }

@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "tern_device.cuh"
+
 namespace tern {
 
 // max that keeps a NaN.
@@ -75,18 +77,25 @@ static __device__ __noinline__ uint32_t quant_codes4_divided(float v0, float v1,
                                                       float scale) {
   return quant_codes4(v0, v1, v2, v3, scale, 0.f, false);
 }
+// (The same arithmetic, element by element, two at a time.)
 __device__ __forceinline__ uint32_t quant_codes4_short(const float (&v)[4], float scale, float inv,
                                                        bool fast) {
   constexpr float kMagic = 12582912.f;
-  const float m0 = fmaf(v[0], inv, kMagic), m1 = fmaf(v[1], inv, kMagic);
-  const float m2 = fmaf(v[2], inv, kMagic), m3 = fmaf(v[3], inv, kMagic);
-  const float far =
-      fmaxf(fmaxf(fabsf(fmaf(v[0], inv, kMagic - m0)), fabsf(fmaf(v[1], inv, kMagic - m1))),
-            fmaxf(fabsf(fmaf(v[2], inv, kMagic - m2)), fabsf(fmaf(v[3], inv, kMagic - m3))));
+  const uint64_t inv2 = pair_f32(inv, inv), magic2 = pair_f32(kMagic, kMagic);
+  const uint64_t minus2 = pair_f32(-1.f, -1.f);
+  float m[4], d[4];
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint64_t v2 = pair_f32(v[i], v[i + 1]);
+    const uint64_t m2 = fma_pair(v2, inv2, magic2);
+    unpair_f32(m2, m[i], m[i + 1]);
+    unpair_f32(fma_pair(v2, inv2, fma_pair(m2, minus2, magic2)), d[i], d[i + 1]);
+  }
+  const float far = fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3])));
   if (!(fast && far < 0.5f - kQMargin))
     return quant_codes4_divided(v[0], v[1], v[2], v[3], scale);
-  return __byte_perm(__byte_perm(__float_as_uint(m0), __float_as_uint(m1), 0x0040),
-                     __byte_perm(__float_as_uint(m2), __float_as_uint(m3), 0x0040), 0x5410);
+  return __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                     __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
 }
 
 }  // namespace tern
