@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
 
 // The append with the keys and the rows' queries turned on the way, in one launch
 // that takes a projection's output to the cache and to the attention's queries.
-// CTAs of a page's keys or values of kTurnHeads heads (two, or for few tokens one),
-// 256 threads each, and behind them CTAs of some of its new tokens and t.q_heads query heads.  A thread holds
+// CTAs of a page's keys or values of some heads (two of 128 elements or four of 64,
+// half as many for few tokens), kPer threads each, and behind them CTAs of some of its new tokens and t.q_heads query heads.  A thread holds
 // units of eight elements (whole pairs) as they are stored, and turns them twice,
 // for the block's largest and for its codes.  A CTA makes its tokens' turns, some
 // 30 instructions each, once for its heads, while the rows are on their way; what
@@ -140,15 +140,16 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Args a
 // waited for instructions: 39 us for three ragged
 // chunks of 3554 tokens, 48 query and 8 other heads of 128 in fp32; 34 here, 4.9
 // TB/s, 0.72 of the copy rate.)
-template <int TYPE, int D, int kTurnHeads>
-__global__ void __launch_bounds__(kTurnHeads * kAppThreads, 4 / kTurnHeads)
+template <int TYPE, int D, int kTurnThreads>
+__global__ void __launch_bounds__(kTurnThreads, 1024 / kTurnThreads)
     kv8_append_rope_kernel(const Kv8Args a, const Kv8Turn t) {
-  constexpr int kTurnThreads = kTurnHeads * kAppThreads;
+  constexpr int kPer = 2 * D;  // threads of a head: four steps of sixteen tokens
+  constexpr int kTurnHeads = kTurnThreads / kPer;
   grid_dependents_launch();
   constexpr int kUnits = D / 8;
-  constexpr int kTok = kAppThreads / kUnits;  // tokens per step
+  constexpr int kTok = kPer / kUnits;  // tokens per step
   constexpr int kSteps = kBlk / kTok;
-  __shared__ float red[kTurnHeads][kAppThreads / 32];
+  __shared__ float red[kTurnHeads][kPer / 32];
   __shared__ float4 block[kTurnHeads];  // scale, 1 / scale, old / scale, grew
   __shared__ float4 turns[2][kBlk * kUnits];
   const int b = blockIdx.z;
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(kTurnHeads * kAppThreads, 4 / kTurnHeads)
     }
     return;
   }
-  const int half = threadIdx.x / kAppThreads, tid = threadIdx.x % kAppThreads;
-  const int head = (blockIdx.y >> 1) * kTurnHeads + half;
+  const int at = threadIdx.x / kPer, tid = threadIdx.x % kPer;
+  const int head = (blockIdx.y >> 1) * kTurnHeads + at;
   const bool live = head < a.hkv;
   const int slot0 = tid / kUnits;
   const int page = a.table[static_cast<size_t>(b) * a.width + pg];
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kTurnHeads * kAppThreads, 4 / kTurnHeads)
     unpack4<TYPE>(raw[k][0], u);
     unpack4<TYPE>(raw[k][1], v);
     if (turned) {
-      const float4 x = turns[0][k * kAppThreads + tid], y = turns[1][k * kAppThreads + tid];
+      const float4 x = turns[0][k * kPer + tid], y = turns[1][k * kPer + tid];
       const float2 turn[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y),
                               make_float2(y.z, y.w)};
       rope_apply(t.rope, turn, u, v);
@@ -262,23 +263,23 @@ __global__ void __launch_bounds__(kTurnHeads * kAppThreads, 4 / kTurnHeads)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) red[half][tid >> 5] = amax;
+  if ((tid & 31) == 0) red[at][tid >> 5] = amax;
   __syncthreads();
   if (tid < 32) {
-    amax = red[half][tid % (kAppThreads / 32)];
+    amax = red[at][tid % (kPer / 32)];
 #pragma unroll
-    for (int o = kAppThreads / 64; o > 0; o >>= 1)
+    for (int o = kPer / 64; o > 0; o >>= 1)
       amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     bool grew;
     const float scale = block_scale(amax, old, grew);
     if (tid == 0) {
-      block[half] = make_float4(scale, 1.0f / scale, old / scale, grew ? 1.f : 0.f);
+      block[at] = make_float4(scale, 1.0f / scale, old / scale, grew ? 1.f : 0.f);
       if (live && (grew || first == 0)) a.scales[blk] = scale;
     }
   }
   __syncthreads();
   if (!live) return;
-  const float4 bl = block[half];
+  const float4 bl = block[at];
   const float scale = bl.x, inv = bl.y, ratio = bl.z;
   const bool grew = bl.w != 0.f, fast = quant_fast(scale);
   int8_t* codes = a.codes + blk * (kBlk * D) + slot0 * D;
@@ -346,29 +347,28 @@ cudaError_t launch_kv8_append_rope(const Kv8Args& a, const Kv8Turn& turn, cudaSt
   Kv8Turn t = turn;
   // few tokens have few turns to share
   const bool few = a.max_new * kRopeBatch < kAppThreads / (a.dim / 8);
-  const int heads = few ? 1 : 2;
-  const int kv = 2 * ((a.hkv - 1) / heads + 1);
+  const int threads = few ? 256 : 512;
+  const int kv = 2 * ((a.hkv - 1) / (threads / (2 * a.dim)) + 1);
   unsigned chunks = 0;
   if (a.q) {
     // Heads of a query CTA, and CTAs that take its page's tokens in turn: few tokens
     // fill its threads with heads, many are batches of heads for each thread and
     // one step of tokens a CTA.  The grid's second index has 16 bits.
-    const int lanes = heads * kAppThreads / (a.dim / 8);  // tokens of a step
+    const int lanes = threads / (a.dim / 8);  // tokens of a step
     t.q_heads = few ? lanes : 2 * kRopeBatch;
     t.q_cuts = few || lanes >= kBlk ? 1 : kBlk / lanes;
     const int room = (65535 - kv) / t.q_cuts;
     if ((a.heads - 1) / t.q_heads >= room) t.q_heads = (a.heads - 1) / room + 1;
     chunks = (a.heads - 1) / t.q_heads * t.q_cuts + t.q_cuts;
   }
-#define TERN_APP_CASE(TYPE, D, H)                                                               \
-  if (a.type == TYPE && a.dim == D && heads == H)                                               \
-    return launch_pages(a, kv + chunks, H * kAppThreads, kv8_append_rope_kernel<TYPE, D, H>,    \
-                        stream, launches, t);
-#define TERN_APP_CASES(TYPE)  \
-  TERN_APP_CASE(TYPE, 64, 1)  \
-  TERN_APP_CASE(TYPE, 64, 2)  \
-  TERN_APP_CASE(TYPE, 128, 1) \
-  TERN_APP_CASE(TYPE, 128, 2)
+#define TERN_APP_CASE(TYPE, D, N)                                                            \
+  if (a.type == TYPE && a.dim == D && threads == N)                                          \
+    return launch_pages(a, kv + chunks, N, kv8_append_rope_kernel<TYPE, D, N>, stream, launches, t);
+#define TERN_APP_CASES(TYPE)    \
+  TERN_APP_CASE(TYPE, 64, 256)  \
+  TERN_APP_CASE(TYPE, 64, 512)  \
+  TERN_APP_CASE(TYPE, 128, 256) \
+  TERN_APP_CASE(TYPE, 128, 512)
   TERN_APP_CASES(TERN_F32)
   TERN_APP_CASES(TERN_BF16)
   TERN_APP_CASES(TERN_F16)
