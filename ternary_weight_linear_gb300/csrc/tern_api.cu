@@ -787,6 +787,9 @@ int tern_rope(const void* x, int type, long long ld, long long hd, void* out, in
       type < TERN_F32 || type > TERN_F16 || out_type < TERN_F32 || out_type > TERN_F16 ||
       !kv8_strides_ok(ld, hd, dim) || !kv8_strides_ok(out_ld, out_hd, dim))
     return TERN_EINVAL;
+  // in place as it is, or not at all
+  if (out == x && (type != out_type || (T > 1 && ld != out_ld) || (heads > 1 && hd != out_hd)))
+    return TERN_EINVAL;
   const int size = type == TERN_F32 ? 4 : 2, out_size = out_type == TERN_F32 ? 4 : 2;
   if (!aligned16(x) || !aligned16(out) || !aligned16(positions) || ld * size % 16 != 0 ||
       hd * size % 16 != 0 || out_ld * out_size % 16 != 0 || out_hd * out_size % 16 != 0)

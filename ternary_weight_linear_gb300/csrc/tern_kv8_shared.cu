@@ -962,7 +962,9 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   }
   cudaLaunchAttribute attr[1];
   // (own tokens: see OwnJobs; what is left over finds no job)
+  // (room for the quota's rounding in fp32: 2^-24 for each 32 sequences)
   long long jobs = ctas + slots.all / 4 > slots.all ? ctas + slots.all / 4 : slots.all;
+  jobs += jobs / 16 + 8;
   if (jobs > ctas * own_parts) jobs = ctas * own_parts;
   const long long grid = static_cast<long long>(prefix_groups) * a.hkv * a.prefix_parts + jobs;
   cudaLaunchConfig_t cfg = pdl_launch_config(attr, dim3(static_cast<unsigned>(grid)),

@@ -21,7 +21,7 @@ def rotation(freq=P, rotary=64, interleaved=0, magnitude=1.0):
     return ctypes.byref(tl._Rotation(freq, rotary, interleaved, magnitude))
 
 
-def rope(x=P, t=0, ld=1024, hd=128, out=P, ot=1, old=1024, ohd=128, pos=P, rot=None, T=1, heads=8,
+def rope(x=P, t=0, ld=1024, hd=128, out=2 * P, ot=1, old=1024, ohd=128, pos=P, rot=None, T=1, heads=8,
          dim=128):
     return tl.load().tern_rope(x, t, ld, hd, out, ot, old, ohd, pos, rot or rotation(), T, heads,
                                dim, None)
@@ -41,6 +41,14 @@ def test_rope_refuses(bad):
 def test_rotations_that_are_refused(bad):
     assert rope(rot=rotation(**bad)) == EINVAL
     assert append(rot=rotation(**bad)) == EINVAL
+
+
+def test_rope_in_place_keeps_type_and_strides():
+    Q = 8192
+    for bad in (dict(ot=1), dict(t=1, ot=0), dict(ot=0, old=2048, T=2), dict(ot=0, ohd=256)):
+        assert rope(out=P, **bad) == EINVAL
+    # (of one token, or apart, the next check is the alignment's)
+    assert rope(ot=0, old=2048, pos=P + 4) == EALIGN and rope(out=Q, pos=P + 4) == EALIGN
 
 
 def test_rope_alignment():
