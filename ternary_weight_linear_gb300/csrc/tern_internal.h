@@ -338,7 +338,10 @@ size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim);
 cudaError_t kv8_shared_set_attributes();
 cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches);
-// Rows of a sequence and key-value head up to which its own tokens are its spans'.
+// Rows of a sequence and key-value head up to which its own tokens are its spans'
+// (those of the prompt kernel's split form, whose parts have another layout).  120
+// rows as spans or by the prompt kernel: 44 and 37 us (8 sequences of up to 300
+// tokens behind 4096), 70 and 52 (up to 1500).
 constexpr int kSpanRows = 64;
 // Parts of the prefix's blocks of rows on the tensor cores, by its pages.
 int kv8_prefix_parts(const Kv8Args& a, int pages, int num_sms);

@@ -19,6 +19,14 @@
 //   former: it waits for it at its end only;
 //   longer sequences' own tokens by kv8_prompt_kernel;
 //   the join.
+//
+// Measured, 32 sequences of 40 to 1500 tokens (6 query heads on each of 8 key-value
+// heads of 128) behind 16384: 37 us; 2 bytes an element of every page once are 12.7
+// at the copy rate, each sequence for itself takes 150.  Alone, the prefix's launch
+// (80 CTAs) takes 33 us, 1700 cycles a page, whose scores' products read the queries
+// from shared memory: its tensor pipe is 48 % busy.  The spans beside it take 30, of
+// which some 5 go until the first codes arrive, three warps a scheduler; the join 5
+// to 8, dependent reads from L2.
 #include "tern_kv8_half.cuh"
 
 namespace tern {
@@ -30,6 +38,11 @@ constexpr int kSpanRecs = 32;    // pages whose records are held at a time
 // CTAs of spans that an SM holds, by their tiles of rows (registers and rings).
 constexpr int span_ctas(int tiles) { return 5 - tiles; }
 constexpr int kSpanPages = 2;    // pages of a span at least, where there are more
+// A prefix of up to this many pages, times key-value heads and groups of rows (twice
+// of 24 rows), is spans as well.  Measured, as spans and on the tensor cores, in us: 4
+// sequences of 6 rows behind 2048 tokens (768 of the units) 11.6 and 14.0; 8 (1536)
+// 13.7 and 19.5; 4 behind 8192 17.2 and 21.5; 16 behind 4096 (6144) 25.3 and 20.9; 32
+// 41.8 and 25.5; 8 of 24 rows behind 4096 (twice 4096) 36.5 and 25.8.
 constexpr long long kSpanPrefixUnits = 4500;
 
 // The pages of a span's list: [s0, s1), then from f0 on.
@@ -920,8 +933,12 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     if (seen + a.max_new / kBlk + sinks < own_pages)
       own_pages = static_cast<int>(seen + a.max_new / kBlk + sinks);
   }
-  // tiles of eight rows of a span: those of a sequence, where three hold them, or two
-  // at a time
+  // Tiles of eight rows of a span: those of a sequence, where three hold them, or two
+  // at a time.  24 rows in one span of three tiles, or in two of two, whose registers
+  // and rings let an SM hold three CTAs instead of two: 8 sequences of up to 2000
+  // tokens behind 8192 29.9 and 37.1 us, 32 of up to 4000 behind 2048 100 and 110, 16
+  // of up to 1500 behind 4096 42.0 and 40.9.  36 rows in two of three tiles 29.8, in
+  // three of two 26.7 (8 sequences of up to 300 behind 4096).
   const int tiles = most <= 8 ? 1 : most > 16 && most <= 24 ? 3 : 2;
   const int tile_rows = 8 * tiles;
   const int groups =
@@ -983,8 +1000,10 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     e = launch_kv8_prompt(own, kKvOwn, kSpanRows + 1, partials, tickets, num_sms, stream, launches);
     if (e != cudaSuccess) return e;
   }
-  // four rows a CTA make twice as many threads of as many parts: for few rows
-  const int join_rows = all < 24ll * num_sms ? 4 : 8;
+  // Four rows a CTA make twice as many threads of as many parts: for few rows.  With
+  // 4 and 8: 288 rows (times key-value heads) 12.7 and 13.6 us a call, 1536 18.3 and
+  // 19.4, 12288 70.4 and 63.5.
+  const int join_rows = all < 16ll * num_sms ? 4 : 8;
   static_assert((2 * kSmallTMaxCtas + 2 * kSpanParts) * 8 * sizeof(float) <= 32 << 10,
                 "the join's shared memory");
   cfg = pdl_launch_config(attr, dim3((R - 1) / join_rows + 1, a.hkv), dim3(kJoinThreads),

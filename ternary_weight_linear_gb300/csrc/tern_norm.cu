@@ -207,10 +207,11 @@ cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
 // every output written once.  Rows of one vector a thread load the residual before
 // the first barrier, longer ones, whose registers are the row's, behind it, as all
 // do with the weights and the gate, which other tokens' CTAs have left in L1.
-// (All of it before the barrier took 56 registers, one CTA of 640 threads an SM:
-// 41.8 us for 2048 rows of 5120, fp32 x, a gate a channel; now 25.4, bound by
-// instructions.  kBf16: weights and gate are all bf16, which saves the choice at
-// each load: 27.4 us with it.)
+// Bound by instructions: 2048 rows of 5120, fp32 x, a gate a channel, bf16 weights
+// take 22.6 us (their bytes 13.9 at the copy rate; the issue slots were 67 % busy at
+// 25.5), 41.8 with all loads before the barrier, whose 56 registers left one CTA of
+// 640 threads an SM.  kBf16: weights and gate are all bf16, which saves the choice
+// at each load, 2 us of it.
 template <int XT, int RT, int NV, bool kBf16>
 __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
     norm_pair_kernel(const NormPairArgs a) {
@@ -284,7 +285,6 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
         unpair_f32(fma_pair(pair_f32(r[j].v[e], r[j].v[e + 1]), inv2,
                             mul_pair(pair_f32(rs.v[e], rs.v[e + 1]), rs2)),
                    r[j].v[e], r[j].v[e + 1]);
-      round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
       if (NV != 2) asm volatile("" ::: "memory");
       const F8 w = weight8(a.weight, a.weight_type, 8ll * i);
       round_store8<RT>(r[j], a.residual_out, row + 8ll * i);
@@ -297,22 +297,17 @@ __global__ void __launch_bounds__(1024, NV == 1 ? 2 : 1)
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  big = warp_max_nan(big);
   if (lane == 0) {
     red_s[warp] = sum;
     red_m[warp] = big;
   }
   __syncthreads();
   sum = lane < warps ? red_s[lane] : 0.f;
-  big = lane < warps ? red_m[lane] : 0.f;
+  big = warp_max_nan(lane < warps ? red_m[lane] : 0.f);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   inv = 1.0f / sqrtf(sum / static_cast<float>(a.K) + a.eps);
   const float amax = big * inv;
   const float scale = amax / 127.0f;  // IEEE single-precision division
