@@ -511,7 +511,8 @@ size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
  * first `shared` tokens of every sequence with new tokens lie in the same pages
  * (the first shared / 64 entries of their rows of page_table are alike), written
  * once and not by this step.  Keys and values of those pages are read once for
- * all rows of the batch instead of once for each sequence; the result is
+ * all rows of the batch instead of once for each sequence (prompt chunks, which
+ * are bound by their products, read them each for itself); the result is
  * tern_kv8_attention's of the same arguments, up to the roundings stated there.
  *   shared   tokens, a multiple of 64, 0 (none) to 64 * table_width; a sequence
  *            whose new tokens do not all lie behind them is inconsistent

@@ -208,7 +208,7 @@ cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
 // the first barrier, longer ones, whose registers are the row's, behind it, as all
 // do with the weights and the gate, which other tokens' CTAs have left in L1.
 // Bound by instructions: 2048 rows of 5120, fp32 x, a gate a channel, bf16 weights
-// take 22.6 us (their bytes 13.9 at the copy rate; the issue slots were 67 % busy at
+// take 22.5 us (their bytes 13.9 at the copy rate; the issue slots were 67 % busy at
 // 25.5), 41.8 with all loads before the barrier, whose 56 registers left one CTA of
 // 640 threads an SM.  kBf16: weights and gate are all bf16, which saves the choice
 // at each load, 2 us of it.
