@@ -21,7 +21,7 @@
 //   the join.
 //
 // Measured, 32 sequences of 40 to 1500 tokens (6 query heads on each of 8 key-value
-// heads of 128) behind 16384: 37 us; 2 bytes an element of every page once are 12.7
+// heads of 128) behind 16384: 36.5 us; 2 bytes an element of every page once are 12.7
 // at the copy rate, each sequence for itself takes 150.  Alone, the prefix's launch
 // (80 CTAs) takes 33 us, 1700 cycles a page, whose scores' products read the queries
 // from shared memory: its tensor pipe is 48 % busy.  The spans beside it take 30, of
@@ -525,17 +525,20 @@ struct OwnJobs {
     // all pages (times heads and groups), and the spans if no sequence were cut;
     // the same order of the same sums in every warp
     float all = 0.f, least = 0.f;
+    int top = 0;  // pages of the longest sequence
     for (int i0 = 0; i0 < a.seqs; i0 += 32) {
       sequence(i0 + lane, s, pages, groups);
       if (!s.ok && x == 0) atomicOr(a.err, kErrIndex);
       all += static_cast<float>(pages.count) * static_cast<float>(groups);
       least += static_cast<float>(groups);
+      if (groups > 0 && pages.count > top) top = pages.count;
     }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) {
       all += __shfl_xor_sync(kAll, all, k);
       least += __shfl_xor_sync(kAll, least, k);
     }
+    top = __reduce_max_sync(kAll, top);
     all *= static_cast<float>(a.hkv);
     least *= static_cast<float>(a.hkv);
     auto quota_of = [&](int ctas) {
@@ -544,7 +547,7 @@ struct OwnJobs {
       return max(kSpanPages, static_cast<int>(fminf(ceilf(all / room), 1e9f)));
     };
     int quota = quota_of(slots.free);
-    if (quota > slots.longest) quota = quota_of(slots.all);
+    if (min(quota, top) > slots.longest) quota = quota_of(slots.all);
     unsigned before = 0;
     for (int i0 = 0; i0 < a.seqs; i0 += 32) {
       if (a.seqs > 32) sequence(i0 + lane, s, pages, groups);
@@ -674,8 +677,10 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
 
 // beside: the launch before this one is the prefix's on the tensor cores, which
 // neither writes what this one reads nor reads what it writes, and whose
-// dependents begin when all that came before it is done.  So this one waits for
-// it at its end alone (and is complete only when that one is).
+// dependents begin when all that came before it is done.  So one CTA of this one
+// waits for it, at its end (and the launch is complete only when both are).
+// (With all of them waiting, those that find no job begin when the prefix has left
+// its SMs, and the join 2 us later.)
 template <int D, int NT>
 __global__ void __launch_bounds__(kSThreads, span_ctas(NT))
     kv8_span_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Kv8Args a,
@@ -684,7 +689,7 @@ __global__ void __launch_bounds__(kSThreads, span_ctas(NT))
   if (!beside) grid_dependency_wait();
   grid_dependents_launch();
   span_part<D, NT>(tm, a, prefix_groups, slots, max_rows);
-  if (beside) grid_dependency_wait();
+  if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
 // The join.  A CTA takes kJoinRows (4, or 8 of many) rows of a key-value head: a warp makes the
@@ -821,10 +826,12 @@ long long clamp_parts(long long parts, long long most, long long rows) {
 // often end before the two one after the other on all.  Times in us, measured: a
 // part of the prefix 7 and 0.95 a page of two tiles of rows (0.62 of one in its split
 // form; heads of 64 two thirds), a span 6.5 and 0.77 a page of one tile of eight rows,
-// 5 between two launches that follow each other.  The launch knows the table's width,
-// not the sequences' lengths: they are taken to be half of it and at most 16 pages.
-// 32 sequences of 40 to 1500 tokens behind 16384: 80 SMs and 72 take 37.7 us, all of
-// them for both 43.6; 16 of up to 300 behind 4096 15.8 and 20.9.
+// a quarter more for each further tile, 5 between two launches that follow each other.
+// The launch knows the table's width, not the sequences' lengths: they are taken to be
+// half of it and at most 24 pages.  The best split and all SMs for both: 32 sequences
+// of 40 to 1500 tokens behind 16384 36.5 (80 SMs and 72) and 43.6; 16 of up to 300
+// behind 4096 15.6 and 20.9; 40 of 20 rows, up to 900 tokens, behind 32768 133 (128
+// SMs, and 24 that take all spans in turn) and 145.
 struct Plan {
   int parts;  // of the prefix
   SpanSlots slots;
@@ -833,16 +840,17 @@ Plan plan_prefix(const Kv8Args& a, int pages, int own_pages, int tiles, long lon
   const int R = a.rows * a.group, on = span_ctas(tiles);
   const long long items = (R + 255ll) / 256 * a.hkv;
   const double narrow = a.dim == 64 ? 0.65 : 1.0;
-  const double page = (R <= 64 ? 0.62 : 0.95) * narrow, own_page = 0.77 * narrow * (tiles + 1) / 2;
-  const int average = own_pages < 32 ? (own_pages + 1) / 2 : 16;
-  const int longest = own_pages < 32 ? own_pages : 32;
+  const double page = (R <= 64 ? 0.62 : 0.95) * narrow, own_page = 0.77 * narrow * (tiles + 3) / 4;
+  const int average = own_pages < 48 ? (own_pages + 1) / 2 : 24;
+  const int longest = own_pages < 48 ? own_pages : 48;
   auto prefix = [&](long long parts) {
     return static_cast<double>((items * parts + sms - 1) / sms) * (7 + page * ((pages + parts - 1) / parts));
   };
   auto own = [&](int slots) {
-    if (ctas > slots)
-      return static_cast<double>((ctas + slots - 1) / slots) * (6.5 + own_page * average) +
-             own_page * (longest - average);
+    if (ctas > slots) {
+      const double waves = ctas > 2ll * slots ? static_cast<double>(ctas) / slots : 2;
+      return waves * (6.5 + own_page * average) + own_page * (longest - average);
+    }
     const double room = slots - ctas > slots / 4 ? slots - ctas : slots / 4;
     const double quota = ctas * average / room;
     return 6.5 + own_page * (quota < longest ? quota : longest);
@@ -852,9 +860,6 @@ Plan plan_prefix(const Kv8Args& a, int pages, int own_pages, int tiles, long lon
   double least = prefix(best.parts) + 5 + own(all);
   for (long long p = 1; p * 2 <= pages && items * p <= sms - sms / 8; ++p) {
     const int free = static_cast<int>(sms - items * p) * on;
-    // (one span more than the SMs take beside the prefix waits for its end: 55 us
-    // where 38 were to be had)
-    if (ctas > free - free / 10) break;
     const double t1 = prefix(p), t2 = own(free), t = t1 > t2 ? t1 : t2;
     if (t < least) {
       least = t;
