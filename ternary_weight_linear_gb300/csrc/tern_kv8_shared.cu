@@ -38,12 +38,17 @@ constexpr int kSpanRecs = 32;    // pages whose records are held at a time
 // CTAs of spans that an SM holds, by their tiles of rows (registers and rings).
 constexpr int span_ctas(int tiles) { return 5 - tiles; }
 constexpr int kSpanPages = 2;    // pages of a span at least, where there are more
+// Halvings of the range that a quota is looked for in (each costs 0.05 us; 32 sequences
+// of up to 2000 tokens behind 128 take 40.9 us with none, 34.2 with two, 32.7 with four).
+constexpr int kQuotaSteps = 4;
 // A prefix of up to this many pages, times key-value heads and groups of rows (twice
-// of 24 rows), is spans as well.  Measured, as spans and on the tensor cores, in us: 4
-// sequences of 6 rows behind 2048 tokens (768 of the units) 11.6 and 14.0; 8 (1536)
-// 13.7 and 19.5; 4 behind 8192 17.2 and 21.5; 16 behind 4096 (6144) 25.3 and 20.9; 32
-// 41.8 and 25.5; 8 of 24 rows behind 4096 (twice 4096) 36.5 and 25.8.
-constexpr long long kSpanPrefixUnits = 4500;
+// of 24 rows), is spans as well, where a CTA for each and one for each of the own
+// tokens' are resident at once.  Measured, as spans and on the tensor cores, in us: 4
+// sequences of 6 rows behind 2048 tokens (768 of the units) 11.3 and 13.6; 6 (1280)
+// 12.7 and 14.1; 8 (1536) 13.7 and 13.7; 8 behind 4096 17.4 and 15.0; 2 of 24 rows
+// behind 4096 (twice 1024) 17.8 and 16.5; 32 of 20 rows behind 256, 472 CTAs where 304
+// are resident, 28.6 and 20.3.
+constexpr long long kSpanPrefixUnits = 1500;
 
 // The pages of a span's list: [s0, s1), then from f0 on.
 struct SpanPages {
@@ -541,13 +546,31 @@ struct OwnJobs {
     top = __reduce_max_sync(kAll, top);
     all *= static_cast<float>(a.hkv);
     least *= static_cast<float>(a.hkv);
-    auto quota_of = [&](int ctas) {
-      const float most = static_cast<float>(ctas);
+    // The quota that makes `most` spans: with most - least of them for the cuts it
+    // makes no more, whatever the lengths are; up to 32 sequences are counted for less.
+    int quota;
+#pragma unroll 1
+    for (int slot = slots.free;; slot = slots.all) {
+      const float most = static_cast<float>(slot);
       const float room = fmaxf(most - least, 0.25f * most);
-      return max(kSpanPages, static_cast<int>(fminf(ceilf(all / room), 1e9f)));
-    };
-    int quota = quota_of(slots.free);
-    if (min(quota, top) > slots.longest) quota = quota_of(slots.all);
+      quota = max(kSpanPages, static_cast<int>(fminf(ceilf(all / room), 1e9f)));
+      if (a.seqs <= 32) {
+        if (quota > top) quota = max(kSpanPages, top);
+        int low = max(kSpanPages, static_cast<int>(fminf(ceilf(all / most), 1e9f)));
+#pragma unroll 1
+        for (int step = 0; step < kQuotaSteps && low < quota; ++step) {
+          const int q = (low + quota) >> 1;
+          const unsigned cut =
+              static_cast<unsigned>(pages.count + q - 1) / static_cast<unsigned>(q);
+          const unsigned spans = __reduce_add_sync(kAll, cut * groups);
+          if (static_cast<float>(spans) * a.hkv <= most)
+            quota = q;
+          else
+            low = q + 1;
+        }
+      }
+      if (min(quota, top) <= slots.longest || slot == slots.all) break;
+    }
     unsigned before = 0;
     for (int i0 = 0; i0 < a.seqs; i0 += 32) {
       if (a.seqs > 32) sequence(i0 + lane, s, pages, groups);
@@ -901,7 +924,7 @@ bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
 }
 
 // Sequences of few rows share at any length (the spans are no slower than the few-row
-// kernel for so short own tokens; 8 sequences of 300 behind 64: 13.1 us, each for
+// kernel for so short own tokens; 8 sequences of 300 behind 64: 9.4 us, each for
 // itself 14.9).  Prompt chunks are bound by the tensor cores, which do the same work
 // either way, and the parts' way through the workspace is lost: 3 chunks of 600 behind
 // 512 to 16384 take 158 to 763 us with shared pages and 65 to 567 without.  In a mixed
@@ -956,7 +979,8 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   // each group reads them again.
   const long long all_groups = (R + tile_rows - 1) / tile_rows;
   const long long units = pages * all_groups * a.hkv;
-  const bool prefix_spans = units * (tiles == 3 ? 2 : 1) <= kSpanPrefixUnits;
+  const bool prefix_spans = units * (tiles == 3 ? 2 : 1) <= kSpanPrefixUnits &&
+                            all_groups * a.hkv + ctas <= all_slots;
   const int prefix_groups = prefix_spans ? static_cast<int>(all_groups) : 0;
   if (prefix_spans) {
     // its share of the CTAs that are resident at once, were the sequences half as long
@@ -966,7 +990,8 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
     if (share > all_slots * 3 / 4) share = all_slots * 3 / 4;
     a.prefix_parts = static_cast<int>(
         clamp_parts(share / (a.hkv * all_groups), (pages + kSpanPages - 1) / kSpanPages, all));
-    slots.free = slots.all = all_slots - static_cast<int>(share);
+    slots.free = slots.all =
+        all_slots - static_cast<int>(a.prefix_parts * all_groups * a.hkv);
   } else {
     const Plan plan = plan_prefix(a, pages, own_pages, tiles, ctas, sms);
     a.prefix_parts = plan.parts;
