@@ -21,8 +21,8 @@
 //   the join.
 //
 // Measured, 32 sequences of 40 to 1500 tokens (6 query heads on each of 8 key-value
-// heads of 128) behind 16384: 36.5 us; 2 bytes an element of every page once are 12.7
-// at the copy rate, each sequence for itself takes 150.  Alone, the prefix's launch
+// heads of 128) behind 16384: 36.5 us; every page's codes once are 12.7 at the copy
+// rate, each sequence for itself takes 150.  Alone, the prefix's launch
 // (80 CTAs) takes 33 us, 1700 cycles a page, whose scores' products read the queries
 // from shared memory: its tensor pipe is 48 % busy.  The spans beside it take 30, of
 // which some 5 go until the first codes arrive, three warps a scheduler; the join 5
@@ -852,7 +852,7 @@ long long clamp_parts(long long parts, long long most, long long rows) {
 // a quarter more for each further tile, 5 between two launches that follow each other.
 // The launch knows the table's width, not the sequences' lengths: they are taken to be
 // half of it and at most 24 pages.  The best split and all SMs for both: 32 sequences
-// of 40 to 1500 tokens behind 16384 36.5 (80 SMs and 72) and 43.6; 16 of up to 300
+// of 40 to 1500 tokens behind 16384 36.5 (88 SMs and 64) and 43.6; 16 of up to 300
 // behind 4096 15.6 and 20.9; 40 of 20 rows, up to 900 tokens, behind 32768 133 (128
 // SMs, and 24 that take all spans in turn) and 145.
 struct Plan {
