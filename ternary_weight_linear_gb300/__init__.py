@@ -231,6 +231,24 @@ def _heads_strides(t: torch.Tensor):
     return t.stride(0) if rows > 1 else heads * dim, hd
 
 
+def _heads(t: torch.Tensor, name: str, dtypes):
+    """A [rows, heads, dim] operand as _strided and _heads_strides take it, each of
+    its properties read once (they cost 0.1 us, of calls that take three): pointer,
+    shape, (row, head) strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {len(shape)}")
+    rows, heads, dim = shape
+    ld, hd, step = t.stride()
+    if step != 1 and dim > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), shape, (ld if rows > 1 else heads * dim, hd if heads > 1 else dim)
+
+
 def _most(n) -> int:
     """An upper bound as a C int, which holds every size that there can be
     (ctypes would keep the low bits of a larger one)."""
@@ -497,8 +515,8 @@ def tern_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
 
 
 def _rotation(freq, interleaved, magnitude) -> _Rotation:
-    p = _dev(freq, "freq", torch.int64, (freq.numel(),))
-    return _Rotation(p, 2 * freq.numel(), int(bool(interleaved)), float(magnitude))
+    n = freq.numel()
+    return _Rotation(_dev(freq, "freq", torch.int64, (n,)), 2 * n, bool(interleaved), magnitude)
 
 
 def tern_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *,
@@ -512,19 +530,19 @@ def tern_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *,
     tern_rope_frequencies.  `out` may be x itself, or of another of the three
     types; it is allocated like a dense x when omitted.  Negated positions turn
     backwards, which is also the gradient."""
-    px = _strided(x, "x", _TYPES, 3)
-    T, heads, dim = x.shape
+    px, shape, xs = _heads(x, "x", _TYPES)
+    T, heads, dim = shape
     if out is None:
         with _allocating(stream):
-            out = torch.empty((T, heads, dim), dtype=x.dtype, device=x.device)
-    po = _strided(out, "out", _TYPES, 3)
-    if out.shape != x.shape:
-        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    po, out_shape, os = _heads(out, "out", _TYPES)
+    if out_shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out_shape)}")
     if T == 0 or heads == 0:
         return out
     rot = _rotation(freq, interleaved, magnitude)
     rc = load().tern_rope(
-        px, _TYPES[x.dtype], *_heads_strides(x), po, _TYPES[out.dtype], *_heads_strides(out),
+        px, _TYPES[x.dtype], *xs, po, _TYPES[out.dtype], *os,
         _dev(positions, "positions", torch.int32, (T,)), ctypes.byref(rot), T, heads, dim,
         _stream(stream))
     _check("tern_rope", rc)
@@ -532,13 +550,15 @@ def tern_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *,
 
 
 def _kv8_cache(codes, scales, page_table, row_start, seq_lens) -> _KV8Cache:
-    if codes.dim() != 5 or codes.shape[1] != 2 or codes.shape[3] != KV8_BLOCK:
+    shape = codes.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != KV8_BLOCK:
         raise ValueError(f"codes must be [pages, 2, kv_heads, {KV8_BLOCK}, head_dim], "
-                         f"got {tuple(codes.shape)}")
-    pages, _, heads, _, dim = codes.shape
-    if page_table.dim() != 2:
+                         f"got {tuple(shape)}")
+    pages, _, heads, _, dim = shape
+    table = page_table.shape
+    if len(table) != 2:
         raise ValueError("page_table must be [seqs, pages of a sequence]")
-    seqs, width = page_table.shape
+    seqs, width = table
     return _KV8Cache(
         _dev(codes, "codes", torch.int8), _dev(scales, "scales", torch.float32, (pages, 2, heads)),
         _dev(page_table, "page_table", torch.int32),
@@ -586,30 +606,31 @@ def tern_kv8_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
     The rotation as in tern_rope, at the tokens' positions in the cache or at
     int32 `positions` [rows].  Returns q_out."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
-    pk = _strided(k, "k", _TYPES, 3)
-    pv = _strided(v, "v", (k.dtype,), 3)
-    if (k.shape != v.shape or _heads_strides(k) != _heads_strides(v)
-            or k.shape[1:] != (codes.shape[2], codes.shape[4])):
+    pk, shape, ks = _heads(k, "k", _TYPES)
+    dtype = k.dtype
+    pv, v_shape, vs = _heads(v, "v", (dtype,))
+    rows, kv_heads, dim = shape
+    if shape != v_shape or ks != vs or kv_heads != cache.kv_heads or dim != cache.head_dim:
         raise ValueError("k and v must be [rows, kv_heads, head_dim] with the same strides")
-    rows, _, dim = k.shape
     pq = po = None
     qs, heads, qt = (0, 0), 0, 0
     if q is not None:
-        pq = _strided(q, "q", (k.dtype,), 3)
-        heads = q.shape[1]
-        if q.shape != (rows, heads, dim):
-            raise ValueError(f"q must be [{rows}, heads, {dim}], got {tuple(q.shape)}")
+        pq, q_shape, qs = _heads(q, "q", (dtype,))
+        heads = q_shape[1]
+        if q_shape != (rows, heads, dim):
+            raise ValueError(f"q must be [{rows}, heads, {dim}], got {tuple(q_shape)}")
         if q_out is None:
             with _allocating(stream):
                 q_out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=q.device)
-        if q_out.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError(f"q_out must be bfloat16 or float16, got {q_out.dtype}")
-        po, qt, qs = _dev(q_out, "q_out", q_out.dtype, q.shape), _TYPES[q_out.dtype], _heads_strides(q)
+        q_type = q_out.dtype
+        if q_type not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"q_out must be bfloat16 or float16, got {q_type}")
+        po, qt = _dev(q_out, "q_out", q_type, q_shape), _TYPES[q_type]
     elif q_out is not None:
         raise ValueError("q_out without q")
     rot = _rotation(freq, interleaved, magnitude)
     rc = load().tern_kv8_append_rope(
-        ctypes.byref(cache), pq, pk, pv, _TYPES[k.dtype], *qs, heads, *_heads_strides(k),
+        ctypes.byref(cache), pq, pk, pv, _TYPES[dtype], *qs, heads, *ks,
         _dev(positions, "positions", torch.int32, (rows,)) if positions is not None else None,
         ctypes.byref(rot), po, qt, rows, max(1, rows) if max_new is None else _most(max_new),
         _stream(stream))
@@ -694,25 +715,25 @@ def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torc
     them.  The result is tern_kv8_attention's; the other arguments are as there,
     the workspace of tern_kv8_attention_shared_workspace_bytes bytes."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
-    pq = _strided(q, "q", (torch.bfloat16, torch.float16), 3)
-    rows, heads, dim = q.shape
-    kv_heads = codes.shape[2]
-    if dim != codes.shape[4]:
-        raise ValueError(f"q's head_dim {dim} is not the cache's {codes.shape[4]}")
+    pq, shape, qs = _heads(q, "q", (torch.bfloat16, torch.float16))
+    rows, heads, dim = shape
+    dtype = q.dtype
+    if dim != cache.head_dim:
+        raise ValueError(f"q's head_dim {dim} is not the cache's {cache.head_dim}")
     with _allocating(stream):
         if out is None:
-            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=dtype, device=q.device)
         if workspace is None:
             workspace = torch.empty(
                 tern_kv8_attention_shared_workspace_bytes(cache.seqs, max(1, rows), heads,
-                                                          kv_heads, dim),
+                                                          cache.kv_heads, dim),
                 dtype=torch.uint8, device=q.device)
             workspace[:SYNC_BYTES].zero_()  # the rest is scratch
     rc = load().tern_kv8_attention_shared(
-        ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads, _most(shared),
+        ctypes.byref(cache), pq, _TYPES[dtype], *qs, rows, heads, _most(shared),
         max(1, rows) if max_new is None else _most(max_new), _most(window), _most(sinks),
         1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
-        _dev(out, "out", q.dtype, (rows, heads, dim)),
+        _dev(out, "out", dtype, shape),
         _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("tern_kv8_attention_shared", rc)
