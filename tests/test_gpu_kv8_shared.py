@@ -189,6 +189,17 @@ def test_windows_over_a_cut_prefix(tl):
     Case(64 * 60, [40 + b for b in range(40)], [2] * 40, 12, 2, 64, seed=2).check(tl, 1500, 129)
 
 
+@pytest.mark.parametrize("seqs,m,group,longest", [(40, 4, 5, 200), (30, 1, 6, 1500),
+                                                  (36, 1, 2, 900), (9, 2, 12, 2000)])
+def test_spans_beside_the_prefix(tl, seqs, m, group, longest):
+    """More sequences and heads than the SMs beside the prefix hold spans, and own
+    tokens of very different lengths, a few of them cut."""
+    own = [m + (b * b * 37) % longest if b % 3 else m for b in range(seqs)]
+    c = Case(64 * 40, own, [m] * seqs, 8 * group, 8, 64, seed=longest)
+    c.check(tl)
+    c.check(tl, window=1700, sinks=40)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_types_and_strides(tl, dtype):
     """Queries within a projection's rows."""
