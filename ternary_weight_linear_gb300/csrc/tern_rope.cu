@@ -9,8 +9,8 @@
 // decode step by one load after the position's.  Several heads a thread where
 // that leaves work for all SMs: a turn costs some 30 instructions, a unit's loads
 // and stores 4.  (Units of sixteen elements, at 61 registers, kept 14 warps an SM:
-// 15.4 us for 2048 tokens of 56 heads in bf16, 12.3 here, 0.70 of the copy rate;
-// the issue slots are 63 % busy.  One or two heads a token leave the turns alone:
+// 15.4 us for 2048 tokens of 56 heads in bf16, 11.4 here, 0.76 of the copy rate;
+// the issue slots were 61 % busy at 12.6.  One or two heads a token leave the turns alone:
 // 65536 tokens of one head 13.2 us, their bytes 4.9.)
 #include <math.h>
 
@@ -43,13 +43,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeRows a) {
 
 cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream) {
   const int units = a.dim / 8;
-  // One head a thread until every SM has its threads, then four.  With one and four:
-  // 32 tokens of 48 heads of 128 2.07 and 2.20 us, 256 of 40 3.17 and 3.29, 8192 of 8
-  // 13.1 and 7.5.
+  // One head a thread until every SM has its threads, then four and more, in CTAs of 128
+  // threads.  With one and four: 32 tokens of 48 heads of 128 2.07 and 2.20 us, 256 of
+  // 40 3.17 and 3.29, 8192 of 8 13.1 and 7.5.  2048 of 56 heads take 12.1 with 14 of them
+  // side by side, 11.2 with 8, 11.6 with 4, 16.6 with 2.
   const long long all = static_cast<long long>(a.T) * a.heads * units;
   const int each = all < static_cast<long long>(num_sms) * 2048 ? 1 : 4;
   int lanes = (a.heads + each - 1) / each;
-  if (lanes > kRopeThreads / units) lanes = kRopeThreads / units;
+  const int most = (each == 1 ? kRopeThreads : 128) / units;  // (at least one)
+  if (lanes > most) lanes = most;
   int tokens = 128 / (units * lanes);
   if (tokens < 1) tokens = 1;
   if (tokens > a.T) tokens = a.T;
