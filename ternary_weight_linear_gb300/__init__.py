@@ -252,7 +252,8 @@ def _heads(t: torch.Tensor, name: str, dtypes):
 def _most(n) -> int:
     """An upper bound as a C int, which holds every size that there can be
     (ctypes would keep the low bits of a larger one)."""
-    return max(-1, min(int(n), 2 ** 31 - 1))
+    n = int(n)
+    return n if -1 <= n < 2 ** 31 else -1 if n < 0 else 2 ** 31 - 1
 
 
 _CURRENT = contextlib.nullcontext()
