@@ -342,7 +342,10 @@ bool kv8_strides_ok(long long ld, long long hd, int dim) {
 // Tickets of the tensor-core attention in the synchronisation area, behind the
 // few-row kernel's.
 constexpr int kPromptTickets = 512;
-static_assert((kPromptTickets + kSmallTMaxCtas) * sizeof(int) <= kSyncBytes, "sync area");
+// And behind those, in a line of its own, Kv8Args::ready.
+constexpr int kReadyWord = 704;
+static_assert(kPromptTickets + kSmallTMaxCtas <= kReadyWord && kReadyWord % 32 == 0 &&
+              kReadyWord * sizeof(int) < kSyncBytes, "sync area");
 
 // The attention's arguments, but for what belongs to the workspace and the
 // device.
@@ -952,6 +955,7 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
   } else {
     a.shared = shared;
     a.part_o = reinterpret_cast<float*>(ws + base);
+    a.ready = static_cast<int*>(workspace) + kReadyWord;
     a.err = d->err;
     CUtensorMap tm;
     rc = kv8_codes_map(a, &tm);

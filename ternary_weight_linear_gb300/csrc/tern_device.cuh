@@ -164,6 +164,10 @@ __device__ __forceinline__ bool wait_counter_at_least(const unsigned long long* 
   }
 }
 
+// One store of *p with release semantics at GPU scope.
+__device__ __forceinline__ void st_release_gpu(int* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 // atomicAdd with acquire-release semantics at GPU scope; returns the old value.
 __device__ __forceinline__ int atomic_add_acq_rel_gpu(int* p, int v) {
   int old;
@@ -261,6 +265,19 @@ __device__ __forceinline__ void grid_dependency_wait() {
 }
 __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// For a kernel whose predecessor's predecessors wrote what it reads, and which reads it
+// before its predecessor has ended: that its predecessor's CTAs trigger behind their own
+// wait orders the starts, but a wait makes earlier grids' writes visible to the grid that
+// waits, not to one that a trigger lets begin.  So a thread that has waited releases
+// *ready, and whoever acquires it sees what that thread could (also through TMA, by the
+// proxy fence); a thread that does not find it raised waits as others do.  A later
+// kernel of the same call, behind its own wait, lowers it.
+__device__ __forceinline__ void grid_ready(int* ready) { st_release_gpu(ready, 1); }
+__device__ __forceinline__ void grid_ready_or_wait(const int* ready) {
+  if (ld_acquire_gpu(ready) == 0) grid_dependency_wait();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {

@@ -257,6 +257,7 @@ struct Kv8Args {
   float* lse;
   int* tickets;
   float* partials;
+  int* ready;  // in the synchronisation area: 1 from the first launch's wait to the last's
   int* err;
   // Attention behind a shared prefix.  shared: tokens that precede what table
   // and lens are read for, the same for every sequence of the call; 0 otherwise.

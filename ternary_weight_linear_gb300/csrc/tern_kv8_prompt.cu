@@ -445,6 +445,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int* rec_e = rec_page + kPRecs;
 
   grid_dependency_wait();  // every input, the output and the workspace belong to earlier work
+  // (for the launches behind a prefix's, which begin before this one has ended)
+  if (kMode == kKvPrefix && blockIdx.x == 0 && threadIdx.x == kPThreads - 1) grid_ready(a.ready);
 
   // ---- this CTA's block of rows, sequence, head and part; late rows first
   const int tail = static_cast<int>(blockIdx.x) - whole;  // of the items in parts

@@ -700,16 +700,20 @@ __device__ __forceinline__ void span_part(const CUtensorMap& tm, const Kv8Args& 
 
 // beside: the launch before this one is the prefix's on the tensor cores, which
 // neither writes what this one reads nor reads what it writes, and whose
-// dependents begin when all that came before it is done.  So one CTA of this one
-// waits for it, at its end (and the launch is complete only when both are).
-// (With all of them waiting, those that find no job begin when the prefix has left
-// its SMs, and the join 2 us later.)
+// dependents begin when all that came before it is done.  So what came before is seen
+// through a.ready, and one CTA of this launch waits for the prefix's, at its end (and
+// the launch is complete only when both are).  (With all of them waiting, those that
+// find no job begin when the prefix has left its SMs, and the join 2 us later.)
 template <int D, int NT>
 __global__ void __launch_bounds__(kSThreads, span_ctas(NT))
     kv8_span_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Kv8Args a,
                     int prefix_groups, SpanSlots slots, int max_rows, int beside) {
-  // (dependents may read the calls' inputs before they wait for this launch)
-  if (!beside) grid_dependency_wait();
+  if (beside) {
+    grid_ready_or_wait(a.ready);
+  } else {
+    grid_dependency_wait();
+    if (blockIdx.x == 0 && threadIdx.x == kSThreads - 1) grid_ready(a.ready);
+  }
   grid_dependents_launch();
   span_part<D, NT>(tm, a, prefix_groups, slots, max_rows);
   if (beside && blockIdx.x == 0) grid_dependency_wait();
@@ -736,8 +740,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     const int tok = kv_token(a, n);
     return static_cast<long long>(tok) * a.heads + hk * a.group + (n - tok * a.group);
   };
-  // (the launch before this one begins its dependents when all that came before
-  // the call is done)
+  // (the call's inputs, before the parts)
+  grid_ready_or_wait(a.ready);
   if (threadIdx.x < kR) s_row[threadIdx.x] = false;
   __syncthreads();
   const int last = n0 + kR < R ? n0 + kR : R;
@@ -752,6 +756,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   }
   __syncthreads();
   grid_dependency_wait();
+  // (who finds it lowered waits instead)
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) st_release_gpu(a.ready, 0);
   grid_dependents_launch();
   const int c = threadIdx.x % kC, i = threadIdx.x / kC % kR, g = threadIdx.x / (kR * kC);
   const bool mine = n0 + i < R && s_row[i];

@@ -180,6 +180,81 @@ def test_attention_reads_what_the_append_wrote(example, seqs, m, shared):
     assert tl.tern_device_status() == 0
 
 
+# the prefix as spans, beside the spans, under a window, and a chunk among single tokens
+@pytest.mark.parametrize("new,shared,window", [([1] * 3, 128, 0), ([1, 2, 1, 0, 3] * 8, 64 * 90, 0),
+                                               ([2] * 21, 64 * 90, 64 * 70),
+                                               ([20] + [1] * 20, 64 * 90, 0)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_lengths_and_tables_that_the_device_advances(example, new, shared, window, captured):
+    """What a serving loop does between steps, on the stream alone: lengths, rows,
+    the table, the cache and the queries are written by kernels before each call, and
+    every launch of the call has to see them.  Bit for bit the same call with the GPU
+    idle between the calls."""
+    import torch
+    tl = example.tl
+    seqs, heads, kv, dim, count, own = len(new), 12, 2, 128, 8, 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seqs)
+    common = shared // 64
+    codes0 = torch.randint(-127, 128, (common + own * seqs, 2, kv, 64, dim), generator=g,
+                           device="cuda", dtype=torch.int8)
+    scales0 = torch.rand(len(codes0), 2, kv, generator=g, device="cuda") * 0.02
+    codes, scales = codes0.clone(), scales0.clone()
+    rng = np.random.default_rng(seqs)
+    tables, lens, starts = [], [], []
+    for i in range(count):
+        m = rng.permutation(new)
+        starts.append(np.concatenate([[0], np.cumsum(m)]))
+        lens.append(shared + m + rng.integers(0, 64 * own - 63, seqs))
+        order = rng.permutation(len(codes0))
+        tables.append(np.concatenate([np.tile(order[:common], (seqs, 1)),
+                                      order[common:].reshape(seqs, own)], 1))
+    dev = lambda a: torch.from_numpy(np.stack(a).astype(np.int32)).cuda()  # noqa: E731
+    tables, lens, starts = dev(tables), dev(lens), dev(starts)
+    table, length, start = (torch.zeros_like(t[0]) for t in (tables, lens, starts))
+    rows = sum(new)
+    ys = [torch.randn(rows, heads + 2 * kv, dim, generator=g, device="cuda") for _ in range(count)]
+    freq, _ = tl.tern_rope_frequencies(64)
+    ws = torch.zeros(tl.tern_kv8_attention_shared_workspace_bytes(seqs, rows, heads, kv, dim),
+                     dtype=torch.uint8, device="cuda")
+    turned = torch.empty(rows, heads, dim, device="cuda").bfloat16()
+
+    def step(i, out):
+        codes.copy_(codes0)
+        scales.copy_(scales0)
+        torch.add(tables[i], 0, out=table)
+        torch.add(starts[i], 0, out=start)
+        torch.add(lens[i], 0, out=length)
+        q, k, v = ys[i].split((heads, kv, kv), 1)
+        tl.tern_kv8_append_rope(q, k, v, codes, scales, table, start, length, freq,
+                                max_new=max(new), q_out=turned)
+        return tl.tern_kv8_attention_shared(turned, codes, scales, table, start, length, shared,
+                                            max_new=max(new), window=window, sinks=3, out=out,
+                                            workspace=ws)
+
+    outs = [torch.zeros_like(turned) for _ in range(count)]
+    if captured:
+        step(0, outs[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(count):
+                step(i, outs[i])
+        for _ in range(3):
+            graph.replay()
+    else:
+        for i in range(count):
+            step(i, outs[i])
+    torch.cuda.synchronize()
+    for i in range(count):
+        want = torch.zeros_like(turned)
+        step(i, want)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want) and (want != 0).any(2).all(), i
+    assert not ws[:tl.SYNC_BYTES].any()
+    assert tl.tern_device_status() == 0
+
+
 @pytest.mark.parametrize("T", [1, 5, 40])
 def test_norms_and_rotation_in_a_chain(example, T):
     """rotation -> norms -> layer, in buffers that each step writes again."""
