@@ -200,6 +200,53 @@ def test_spans_beside_the_prefix(tl, seqs, m, group, longest):
     c.check(tl, window=1700, sinks=40)
 
 
+def check_twice(tl, c, launches, **kw):
+    """Against the oracle on a workspace that is kept, and again, bit for bit."""
+    import torch
+    kv = c.codes.shape[2]
+    ws = torch.zeros(tl.tern_kv8_attention_shared_workspace_bytes(len(c.lens), c.rows, c.heads, kv,
+                                                                  c.dim),
+                     dtype=torch.uint8, device="cuda")
+    first, _ = c.check(tl, workspace=ws, **kw)
+    assert tl.tern_last_launches() == launches
+    assert torch.equal(c.run(tl, workspace=ws, **kw), first)
+    assert not ws[:tl.SYNC_BYTES].any()
+
+
+@pytest.mark.parametrize("group,m,shared,tokens,launches", [
+    (3, 1, 512, 11000, 2), (9, 1, 512, 8000, 2), (17, 1, 1280, 5500, 3), (5, 4, 1280, 5500, 3)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9, 10)])
+def test_spans_of_more_pages_than_records(tl, group, m, shared, tokens, launches, window, sinks):
+    """16 sequences of `tokens` and up to 1.4 times as many, 8 heads of them: 26000,
+    19000 and 13000 pages for 608, 456 and 304 resident spans, 40 and more for each,
+    whose records are held 32 at a time.  The window is nine tenths of them."""
+    own = [tokens + tokens // 40 * b for b in range(16)]
+    window, sinks = tokens * window // 10, 10 * sinks
+    c = Case(shared, own, [m] * 16, 8 * group, 8, 64, seed=group)
+    check_twice(tl, c, launches, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("long", [3000, 6100])
+def test_more_parts_than_the_workspace_holds(tl, long):
+    """300 rows of 48 heads leave room for 40960 / 14400 = 2 parts of own tokens; the
+    long sequence's pages, 3 and 5 times the quota of all, go into those."""
+    own = [20] * 300
+    own[137] = long
+    c = Case(64 * 10, own, [1] * 300, 48, 8, 64, seed=long)
+    check_twice(tl, c, 3)
+    check_twice(tl, c, 3, window=1700, sinks=10)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1400, 0), (1500, 700)])
+def test_chunks_whose_own_tokens_are_cut(tl, dim, window, sinks):
+    """Chunks of more than 64 rows over 25 to 60 pages of their own (cut from 16 on)
+    among single tokens, whose parts of the own tokens are joined once more."""
+    own = [1700] + [30] * 12 + [3800, 1530] + [70] * 15
+    c = Case(640, own, [40] + [1] * 12 + [33, 11] + [1] * 15, 12, 2, dim, seed=window)
+    check_twice(tl, c, 3, window=window, sinks=sinks)  # spans (the prefix's too), chunks, join
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_types_and_strides(tl, dtype):
     """Queries within a projection's rows."""
