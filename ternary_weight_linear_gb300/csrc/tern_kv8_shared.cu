@@ -495,7 +495,11 @@ struct SpanSlots {
 // The spans of the sequences' own tokens: those of a sequence with pages and rows
 // for the kernel are cut into parts of `quota` pages and fewer, the same for all,
 // so that a launch has about as many spans as CTAs are resident at once, of about the
-// same length, however long the sequences are.
+// same length, however long the sequences are; but into no more parts than the
+// workspace holds of every row (kSpanPartRows): of 256 rows of 48 heads 3, from 427 on 1.
+// There a sequence that is far longer than the others has the launch's longest spans:
+// 256 sequences of up to 300 tokens behind 4096 94 us, with one of 32000 among them 208;
+// behind 64 70 and 195 (each for itself 106 and 137).
 struct OwnJob {
   int seq, part, parts, group, hk;
   KvSeq s;
@@ -899,6 +903,30 @@ Plan plan_prefix(const Kv8Args& a, int pages, int own_pages, int tiles, long lon
   return best;
 }
 
+// Pages that a sequence's rows see at most, of the prefix and of their own.
+struct SeenPages {
+  int prefix, own;
+};
+SeenPages seen_pages(const Kv8Args& a, int shared) {
+  SeenPages s = {shared / kBlk, a.width - shared / kBlk};
+  if (a.window > 0) {
+    const long long seen = static_cast<long long>(a.window) / kBlk + 2;
+    const long long sinks = a.sinks / kBlk + 1;
+    if (seen + sinks < s.prefix) s.prefix = static_cast<int>(seen + sinks);
+    if (seen + a.max_new / kBlk + sinks < s.own)
+      s.own = static_cast<int>(seen + a.max_new / kBlk + sinks);
+  }
+  return s;
+}
+
+// Tiles of eight rows of a span: those of a sequence, where three hold them, or two
+// at a time.  24 rows in one span of three tiles, or in two of two, whose registers
+// and rings let an SM hold three CTAs instead of two: 8 sequences of up to 2000
+// tokens behind 8192 29.9 and 37.1 us, 32 of up to 4000 behind 2048 100 and 110, 16
+// of up to 1500 behind 4096 42.0 and 40.9.  36 rows in two of three tiles 29.8, in
+// three of two 26.7 (8 sequences of up to 300 behind 4096).
+int span_tiles(long long most) { return most <= 8 ? 1 : most > 16 && most <= 24 ? 3 : 2; }
+
 // Shared memory of a span's CTA (whose layout starts on 1024 bytes).
 int span_bytes(int dim, int tiles) {
   const size_t n =
@@ -929,18 +957,51 @@ bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
          static_cast<long long>(seqs) * kv_heads <= (0x7FFFFFFFll - 4 * kSmallTMaxCtas) / (kSpanRows / 8) / 2;
 }
 
-// Sequences of few rows share at any length (the spans are no slower than the few-row
-// kernel for so short own tokens; 8 sequences of 300 behind 64: 9.4 us, each for
-// itself 14.9).  Prompt chunks are bound by the tensor cores, which do the same work
-// either way, and the parts' way through the workspace is lost: 3 chunks of 600 behind
-// 512 to 16384 take 158 to 763 us with shared pages and 65 to 567 without.  In a mixed
-// batch the shorter sequences win a pass over the prefix each (2 bytes an element, and
-// there are seqs - R / most of them at least) and all rows lose their parts (some 12).
+// What sharing wins is a pass over the prefix a sequence.  What it loses:
+//
+// The own tokens' pages in spans take longer than in the ordinary kernels, the more
+// so the more rows a span or its groups have.  The launch knows the table's width, not
+// the lengths, which may be anything up to it: it shares up to about the width at which
+// short sequences would lose by the ordinary kernels what full ones win.  Measured, the
+// time of each for itself over that of sharing, for 8 and 32 sequences (8 key-value
+// heads of 128) of up to 1000 own tokens, then of up to 17000 (up to 20 rows) or 4000:
+//   rows    behind 64               512                      4096 shared tokens
+//     6   1.4  1.2   0.96 0.74   1.3  1.4   0.96 0.91   1.3  2.0   0.70 0.95
+//    12   1.5  1.1   0.88 0.44   1.3  1.3   0.88 0.78   1.3  1.9   0.86 1.02
+//    20   1.3  0.89  0.79 0.59   1.4  1.3   0.81 0.59   1.6  1.7   0.90 0.67
+//    30   1.05 0.83  0.85 0.84   1.1  0.90  0.90 0.86   1.4  1.7   1.2  1.25
+//    60   0.77 0.56  0.58 0.50   0.86 0.63  0.55 0.53   0.99 1.2   0.67 0.80
+// (What the width does not tell: short sequences in a wide table lose by the ordinary
+// kernels, 128 of up to 300 tokens with 20 rows behind 512 75 and 101 us; a long one
+// among many short ones loses in spans, see OwnJobs.)
+//
+// Every span's CTA looks through all sequences for its own: 24 rows, up to 300 tokens,
+// behind 64 shared ones 1.18 times as fast at 256 sequences, 1.03 at 512, 0.76 at 1024;
+// behind 512 1.25, 1.08, 0.81; behind 4096 1.2 at 2048.  6 rows behind 64 1.43 at 512,
+// 1.02 at 1024, 0.62 at 2048; behind 512 1.10 and 0.68 at 1024 and 2048.
+//
+// Chunks of more than kSpanRows rows go through the tensor cores either way, and what
+// sharing loses is the parts' way through the workspace and launches that follow each
+// other.  Each for itself over shared: 3600 rows 0.38
+// to 0.9 (2 to 16 sequences behind 512 to 16384); 72, 128 and 258 rows, up to 2000 own
+// tokens, behind 512 0.5 to 0.8, behind 4096 0.6 to 1.05 at up to 16 sequences.  Longer
+// prefixes of more sequences would gain, which the rule leaves: 32 sequences of 72 rows
+// behind 16384 2.3 (454 and 200 us), of 258 rows 1.4; 4 of 72 rows 1.04.  In a mixed batch
+// the shorter sequences win a pass over the prefix each (2 bytes an element, and there
+// are seqs - R / most of them at least) and all rows lose their parts (some 12).
 bool kv8_shared_pays(const Kv8Args& a, int shared) {
   if (a.seqs == 1 || shared == 0) return false;
   const long long R = static_cast<long long>(a.rows) * a.group;
   const long long most = static_cast<long long>(a.max_new) * a.group;
-  if (most <= kSpanRows) return true;
+  if (most <= kSpanRows) {
+    const SeenPages seen = seen_pages(a, shared);
+    const long long prefix = seen.prefix;
+    if (a.seqs > (most <= 8 ? 640 : 384) + 64 * prefix) return false;
+    const long long groups = (most + 15) / 16;  // beyond 24 rows
+    return most <= 8 || seen.own <= (most <= 16   ? 64 * (prefix + 1)
+                                     : most <= 24 ? 8 * (prefix + 8)
+                                                  : (8 * prefix) >> groups);
+  }
   const long long shorter = a.seqs - (R + most - 1) / most;
   return shorter * shared > 6 * R;
 }
@@ -959,21 +1020,9 @@ cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials,
   const long long all = static_cast<long long>(R) * a.hkv;
   const long long most = static_cast<long long>(a.max_new) * a.group;
   const int common = a.shared / kBlk;
-  int pages = common, own_pages = a.width - common;  // seen, at most
-  if (a.window > 0) {
-    const long long seen = static_cast<long long>(a.window) / kBlk + 2;
-    const long long sinks = a.sinks / kBlk + 1;
-    if (seen + sinks < pages) pages = static_cast<int>(seen + sinks);
-    if (seen + a.max_new / kBlk + sinks < own_pages)
-      own_pages = static_cast<int>(seen + a.max_new / kBlk + sinks);
-  }
-  // Tiles of eight rows of a span: those of a sequence, where three hold them, or two
-  // at a time.  24 rows in one span of three tiles, or in two of two, whose registers
-  // and rings let an SM hold three CTAs instead of two: 8 sequences of up to 2000
-  // tokens behind 8192 29.9 and 37.1 us, 32 of up to 4000 behind 2048 100 and 110, 16
-  // of up to 1500 behind 4096 42.0 and 40.9.  36 rows in two of three tiles 29.8, in
-  // three of two 26.7 (8 sequences of up to 300 behind 4096).
-  const int tiles = most <= 8 ? 1 : most > 16 && most <= 24 ? 3 : 2;
+  const SeenPages seen = seen_pages(a, a.shared);
+  const int pages = seen.prefix, own_pages = seen.own;
+  const int tiles = span_tiles(most);
   const int tile_rows = 8 * tiles;
   const int groups =
       static_cast<int>(((most < kSpanRows ? most : kSpanRows) + tile_rows - 1) / tile_rows);

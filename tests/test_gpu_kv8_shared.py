@@ -173,6 +173,33 @@ def test_mixed_batches_and_which_launches(tl, dim, shared, new, launches):
         c.check(tl, window=shared - 30, sinks=70)
 
 
+# (shared tokens, sequences, new tokens, columns of the table behind the shared pages)
+@pytest.mark.parametrize("shared,seqs,m,columns,shares", [
+    (64, 32, 1, 2000, True), (64, 5, 2, 128, True), (64, 5, 2, 129, False), (512, 5, 2, 300, True),
+    (64, 5, 4, 72, True), (64, 5, 4, 73, False), (512, 5, 4, 128, True), (512, 5, 4, 129, False),
+    (512, 5, 5, 16, True), (512, 5, 5, 17, False), (512, 5, 8, 8, True), (512, 5, 8, 9, False),
+    (512, 5, 10, 4, True), (512, 5, 10, 5, False), (64, 2, 10, 320, False),
+    (64, 704, 1, 2, True), (64, 705, 1, 2, False), (64, 448, 2, 2, True), (64, 449, 2, 2, False),
+    (0, 3, 1, 2, False), (64, 1, 1, 2, False)])
+def test_what_does_not_gain_reads_each_for_itself(tl, shared, seqs, m, columns, shares):
+    """Where the table is too wide for the rows and the prefix, or the sequences too
+    many for it, the ordinary kernels run, with their very bits; 6 query heads."""
+    import torch
+    c = Case(shared, [m + 7 * (b % 9) for b in range(seqs)], [m] * seqs, 6, 1, 64, seed=columns)
+    wide = np.full((seqs, shared // 64 + columns), -7, np.int32)
+    n = min(wide.shape[1], c.table.shape[1])
+    wide[:, :n] = c.table[:, :n]
+    c.table = wide
+    out, lse = c.check(tl)
+    c.run(tl)
+    launches = tl.tern_last_launches()
+    lse2 = torch.full_like(lse, 7.0)
+    whole = tl.tern_kv8_attention(c.q_dev, *c.args(), max_new=c.max_new, lse=lse2)
+    assert (torch.equal(out, whole) and torch.equal(lse, lse2)) == (not shares)
+    if not shares:
+        assert launches == tl.tern_last_launches()
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (130, 7), (400, 64), (600, 100),
                                           (900, 65), (100, 2000), (5000, 3)])
