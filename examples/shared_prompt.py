@@ -56,10 +56,11 @@ class Block:
         turned = tl.tern_kv8_append_rope(
             y[:, :n], y[:, n:n + kv], y[:, n + kv:], self.codes, self.scales, table, start, lens,
             self.freq, magnitude=self.magnitude, max_new=max_new)
+        need = (tl.tern_kv8_attention_shared_workspace_bytes if shared and len(lens) > 1
+                else tl.tern_kv8_attention_workspace_bytes)
         o = tl.tern_kv8_attention_shared(
             turned, self.codes, self.scales, table, start, lens, shared, max_new=max_new,
-            workspace=self._workspace("attention", tl.tern_kv8_attention_shared_workspace_bytes(
-                len(lens), rows, n, kv, d)))
+            workspace=self._workspace("attention", need(len(lens), rows, n, kv, d)))
         h = tl.tern_linear(*self.out, o.view(rows, n * d), workspace=self._workspace(
             "linear", tl.tern_linear_workspace_bytes(rows, n * d, hidden)))
         return tl.tern_norm_add_norm_s8(h, self.post, residual, self.norm, gate=self.gate)

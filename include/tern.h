@@ -503,7 +503,8 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type,
 
 /* Bytes of device workspace tern_kv8_attention_shared needs: that of
  * tern_kv8_attention, fp32 results of the rows' own tokens, and partial results
- * of the prefix.  Host-only; 0 for sizes out of range. */
+ * of the prefix.  A call that can share nothing (shared 0, or one sequence) needs
+ * the former alone.  Host-only; 0 for sizes out of range. */
 size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
                                                  int kv_heads, int head_dim);
 
@@ -520,8 +521,9 @@ size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
  *            the call: a captured call keeps it
  *   page_table the shared entries are read from its first row (which must so
  *            hold them, even where the first sequence has no tokens) or from each
- *   rows, heads ceil(rows * heads / kv_heads / 256) * kv_heads has to stay below
- *            2^31 - 1000
+ *   rows, heads, seqs: behind a prefix of several sequences ceil(rows * heads /
+ *            kv_heads / 256) * kv_heads has to stay below 2^31 - 1000, and
+ *            seqs * kv_heads below 2^27 - 100
  *   the others as for tern_kv8_attention; workspace of
  *            tern_kv8_attention_shared_workspace_bytes, zeroed and kept as there.
  * The prefix's and the own tokens' parts are joined in fp32 by their

@@ -714,7 +714,8 @@ def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torc
     same pages: the first shared / 64 entries of the rows of page_table are
     alike.  They are read once for all rows of the batch.  New tokens lie behind
     them.  The result is tern_kv8_attention's; the other arguments are as there,
-    the workspace of tern_kv8_attention_shared_workspace_bytes bytes."""
+    the workspace of tern_kv8_attention_shared_workspace_bytes bytes (of
+    tern_kv8_attention's where `shared` is 0 or there is one sequence)."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
     pq, shape, qs = _heads(q, "q", (torch.bfloat16, torch.float16))
     rows, heads, dim = shape
@@ -725,10 +726,10 @@ def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torc
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=q.device)
         if workspace is None:
-            workspace = torch.empty(
-                tern_kv8_attention_shared_workspace_bytes(cache.seqs, max(1, rows), heads,
-                                                          cache.kv_heads, dim),
-                dtype=torch.uint8, device=q.device)
+            need = (tern_kv8_attention_shared_workspace_bytes if shared and cache.seqs > 1
+                    else tern_kv8_attention_workspace_bytes)
+            workspace = torch.empty(need(cache.seqs, max(1, rows), heads, cache.kv_heads, dim),
+                                    dtype=torch.uint8, device=q.device)
             workspace[:SYNC_BYTES].zero_()  # the rest is scratch
     rc = load().tern_kv8_attention_shared(
         ctypes.byref(cache), pq, _TYPES[dtype], *qs, rows, heads, _most(shared),

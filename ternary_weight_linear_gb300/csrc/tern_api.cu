@@ -933,14 +933,17 @@ int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int ty
   int rc = kv8_attention_args(cache, q, type, ld, hd, rows, heads, max_new, window, sinks,
                               softmax_scale, out, lse, &a);
   if (rc != TERN_OK) return rc;
+  const bool may_share = shared > 0 && a.seqs > 1;  // (see kv8_shared_pays)
   if (shared < 0 || shared % TERN_KV8_BLOCK != 0 || shared / TERN_KV8_BLOCK > a.width ||
-      !kv8_shared_fits(rows, heads / a.hkv, a.hkv, a.seqs))
+      (may_share && !kv8_shared_fits(rows, heads / a.hkv, a.hkv, a.seqs)))
     return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
-  const size_t base = align_up(
-      tern_kv8_attention_workspace_bytes(a.seqs, rows, heads, a.hkv, a.dim), 256);
-  if (!workspace || workspace_bytes < tern_kv8_attention_shared_workspace_bytes(
-                                          a.seqs, rows, heads, a.hkv, a.dim))
+  const size_t plain = tern_kv8_attention_workspace_bytes(a.seqs, rows, heads, a.hkv, a.dim);
+  const size_t base = align_up(plain, 256);
+  if (!workspace ||
+      workspace_bytes < (may_share ? tern_kv8_attention_shared_workspace_bytes(a.seqs, rows, heads,
+                                                                               a.hkv, a.dim)
+                                   : plain))
     return TERN_ENOSPACE;
   if (!aligned16(workspace)) return TERN_EALIGN;
   DevState* d = nullptr;

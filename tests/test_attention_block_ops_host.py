@@ -127,3 +127,12 @@ def test_shared_attention_workspace():
     assert shared(rows=0, max_new=0, ws=0) == 0 and shared(q=P + 2) == EALIGN
     for bad in ((0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 1, 12, 8, 128), (1, 1, 8, 8, 96)):
         assert tl.tern_kv8_attention_shared_workspace_bytes(*bad) == 0
+
+
+def test_nothing_to_share_needs_the_ordinary_workspace():
+    """Refused for its alignment, the check behind the size's."""
+    for n, seqs in ((0, 2), (64, 1), (0, 1)):
+        plain = tl.tern_kv8_attention_workspace_bytes(seqs, 2, 8, 8, 128)
+        call = lambda ws, at: tl.load().tern_kv8_attention_shared(  # noqa: E731
+            cache(seqs=seqs), P, 1, 1024, 128, 2, 8, n, 1, 0, 0, 0.125, P, None, at, ws, None)
+        assert call(plain - 1, P) == -3 and call(plain, P + 4) == EALIGN

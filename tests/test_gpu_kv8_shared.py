@@ -313,6 +313,17 @@ def test_a_lone_sequence(tl):
     Case(0, [30, 5, 100], [2, 1, 1], 8, 2, 64, seed=6).check(tl)
 
 
+@pytest.mark.parametrize("shared,new", [(0, [2, 1, 1]), (256, [2]), (256, [70])])
+def test_the_ordinary_workspace_where_nothing_is_shared(tl, shared, new):
+    import torch
+    c = Case(shared, [m + 30 for m in new], new, 8, 2, 64, seed=6)
+    need = tl.tern_kv8_attention_workspace_bytes(len(new), c.rows, 8, 2, 64)
+    held = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    held[need:] = 77
+    c.check(tl, workspace=held[:need])
+    assert (held[need:] == 77).all()
+
+
 def test_first_sequence_without_tokens(tl):
     """Its row of the table still names the shared pages."""
     Case(320, [None, 30, 5], [0, 2, 1], 8, 2, 64, seed=7).check(tl)
