@@ -94,8 +94,9 @@ def serve(block, hidden, prompt, seqs, steps, gen):
 
     # the shared pages, by the first sequence alone; then what is left of the prompt
     # behind them, in pages of each
-    block(*tokens(common * page), table[:1], lengths(0, common * page), lengths(common * page),
-          common * page, 0)
+    if common:
+        block(*tokens(common * page), table[:1], lengths(0, common * page),
+              lengths(common * page), common * page, 0)
     rest = prompt - common * page
     if rest:
         q, x_scale, r = tokens(rest)

@@ -133,6 +133,28 @@ def test_the_examples_links(example, monkeypatch, prompt):
     assert rec.seen.count("tern_kv8_attention_shared") == calls
 
 
+@pytest.mark.parametrize("prompt", [0, 40])
+def test_the_example_without_a_whole_page_to_share(example, monkeypatch, prompt):
+    import torch
+    tl = example.tl
+    hidden, heads, kv, dim, seqs = 256, 6, 2, 64, 5
+    cq = synth.case("tiny", 1, K=hidden, N=(heads + 2 * kv) * dim, seed=1)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    freq, magnitude = tl.tern_rope_frequencies(dim)
+    ones = torch.ones(hidden, device="cuda").bfloat16()
+    qkv = (tl.tern_pack(torch.from_numpy(cq.W).cuda()),
+           torch.from_numpy(cq.scales.view(np.uint16)).view(torch.float16).cuda())
+    block = example.Block(qkv, example.random_projection(hidden, heads * dim, gen), ones, ones, ones,
+                          freq, magnitude, heads, kv, dim, pages=16)
+    rec = Recorder(tl, (cq, oracle.pack(cq.W)[0]))
+    monkeypatch.setattr(example, "tl", rec)
+    got = example.serve(block, hidden, prompt, seqs, 3, gen)
+    assert tl.tern_device_status() == 0
+    assert got[0].shape == (seqs, hidden)
+    assert rec.seen.count("tern_kv8_attention_shared") == (prompt > 0) + 3
+
+
 def _same(step, count):
     """step(i) -> tensors: `count` of them back to back and one by one."""
     import torch
