@@ -359,7 +359,7 @@ int tern_rope_frequencies(int rotary_dim, double base, int scaling,
  *   positions device int32 [T]; a negative one turns backwards, so the call
  *            with all of them negated is the inverse (for magnitude 1) and the
  *            transpose, which is its gradient
- *   T, heads >= 1; dim a multiple of 16, at most 1024.
+ *   T >= 1; heads 1..2^30; dim a multiple of 16, at most 1024.
  * The angle is exact modulo a turn for every position; its sine and cosine and
  * the products are fp32 (an element is off by less than 2^-21 m (|u| + |v|)),
  * rounded once to out_type. */

@@ -786,7 +786,8 @@ int tern_rope(const void* x, int type, long long ld, long long hd, void* out, in
   RopeArgs r;
   int rc = rope_args(rotation, dim, &r);
   if (rc != TERN_OK) return rc;
-  if (!x || !out || !positions || T < 1 || heads < 1 || dim % 16 != 0 || dim > kRopeMaxDim ||
+  if (!x || !out || !positions || T < 1 || heads < 1 || heads > kRopeMaxHeads || dim % 16 != 0 ||
+      dim > kRopeMaxDim ||
       type < TERN_F32 || type > TERN_F16 || out_type < TERN_F32 || out_type > TERN_F16 ||
       !kv8_strides_ok(ld, hd, dim) || !kv8_strides_ok(out_ld, out_hd, dim))
     return TERN_EINVAL;

@@ -229,6 +229,7 @@ struct RopeRows {
 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 1024;
+constexpr int kRopeMaxHeads = 1 << 30;  // (a thread's next heads are 32-bit numbers too)
 cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream);
 // false: a frequency of a turn a token and more.  All in range otherwise.
 bool rope_frequencies(int rotary, double base, int scaling, double factor, double trained,

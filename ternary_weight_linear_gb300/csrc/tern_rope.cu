@@ -58,8 +58,7 @@ cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream) {
   if (tokens > 64) tokens = 64;  // (a block's third extent)
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
-      pdl_launch_config(attr, dim3((a.T + tokens - 1) / tokens), dim3(units, lanes, tokens), 0,
-                        stream);
+      pdl_launch_config(attr, dim3((a.T - 1) / tokens + 1), dim3(units, lanes, tokens), 0, stream);
 #define TERN_ROPE_CASE(TYPE, OUT) \
   if (a.type == TYPE && a.out_type == OUT) return cudaLaunchKernelEx(&cfg, rope_kernel<TYPE, OUT>, a);
   TERN_ROPE_CASE(TERN_F32, TERN_F32)

@@ -129,6 +129,12 @@ def test_shared_attention_workspace():
         assert tl.tern_kv8_attention_shared_workspace_bytes(*bad) == 0
 
 
+def test_rope_refuses_more_heads_than_it_counts():
+    for heads in ((1 << 30) + 1, 2 ** 31 - 4, 2 ** 31 - 1):
+        assert rope(heads=heads, pos=P + 4) == EINVAL
+    assert rope(heads=1 << 30, pos=P + 4) == EALIGN
+
+
 def test_nothing_to_share_needs_the_ordinary_workspace():
     """Refused for its alignment, the check behind the size's."""
     for n, seqs in ((0, 2), (64, 1), (0, 1)):

@@ -346,3 +346,24 @@ def test_append_refusals_of_the_binding(tl):
         call(positions=torch.zeros(3, dtype=torch.int32, device="cuda"))
     with pytest.raises(tl.TernError):
         call(freq=_table(tl, 128)[0])
+
+
+def test_as_many_tokens_as_a_call_can_name(tl):
+    """2^31 - 1 of one head of 16, in place: tokens, units and bytes past 31 bits."""
+    import torch
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 78 GB")
+    x = torch.zeros(T, 1, 16, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    at = [0, 1, 2 ** 30 + 5, T - 64, T - 2, T - 1]
+    rows = torch.randn(len(at), 1, 16, device="cuda").bfloat16()
+    places = torch.arange(7, 7 + len(at), dtype=torch.int32, device="cuda") * 1000
+    for i, row, place in zip(at, rows, places):
+        x[i], pos[i] = row, place
+    freq, _ = tl.tern_rope_frequencies(16)
+    tl.tern_rope(x, pos, freq, out=x)
+    assert torch.equal(torch.stack([x[i] for i in at]), tl.tern_rope(rows, places, freq))
+    assert not x[2:2000].any() and not x[T - 63:T - 2].any()
+    del x, pos
+    torch.cuda.empty_cache()
