@@ -775,9 +775,8 @@ int tern_rope_frequencies(int rotary_dim, double base, int scaling, double facto
       (!(trained > 0.0) || !isfinite(trained) || !(low > 0.0) || !(high > low) || !isfinite(high)))
     return TERN_EINVAL;
   if (scaling == TERN_ROPE_NONE) factor = 1.0;
-  return rope_frequencies(rotary_dim, base, scaling, factor, trained, low, high, freq, magnitude)
-             ? TERN_OK
-             : TERN_EINVAL;
+  rope_frequencies(rotary_dim, base, scaling, factor, trained, low, high, freq, magnitude);
+  return TERN_OK;
 }
 
 int tern_rope(const void* x, int type, long long ld, long long hd, void* out, int out_type,
@@ -923,7 +922,7 @@ int tern_kv8_attention(const tern_kv8_cache* cache, const void* q, int type, lon
 size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads, int kv_heads,
                                                  int head_dim) {
   const size_t n = tern_kv8_attention_workspace_bytes(seqs, rows, heads, kv_heads, head_dim);
-  return n == 0 ? 0 : align_up(n, 256) + kv8_shared_part_bytes(rows, heads, kv_heads, head_dim);
+  return n == 0 ? 0 : align_up(n, 256) + kv8_shared_part_bytes(rows, heads, head_dim);
 }
 
 int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type, long long ld,

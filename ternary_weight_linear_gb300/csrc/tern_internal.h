@@ -231,8 +231,8 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 1024;
 constexpr int kRopeMaxHeads = 1 << 30;  // (a thread's next heads are 32-bit numbers too)
 cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream);
-// false: a frequency of a turn a token and more.  All in range otherwise.
-bool rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
+// All in the range that tern_rope_frequencies checks.
+void rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
                       double low, double high, uint64_t* freq, float* magnitude);
 
 // The int8 cache (see tern_kv8_cache) and one call's rows.
@@ -336,7 +336,7 @@ cudaError_t launch_kv8_prompt(const Kv8Args& a, Kv8Mode mode, int min_rows, floa
 bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs);
 // Whether the prefix is worth launches of its own; otherwise each sequence reads it.
 bool kv8_shared_pays(const Kv8Args& a, int shared);
-size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim);
+size_t kv8_shared_part_bytes(int rows, int heads, int dim);
 cudaError_t kv8_shared_set_attributes();
 cudaError_t launch_kv8_shared(const CUtensorMap* tm, Kv8Args a, float* partials, int* tickets,
                               int num_sms, cudaStream_t stream, int* launches);

@@ -1006,9 +1006,8 @@ bool kv8_shared_pays(const Kv8Args& a, int shared) {
   return shorter * shared > 6 * R;
 }
 
-size_t kv8_shared_part_bytes(int rows, int heads, int kv_heads, int dim) {
+size_t kv8_shared_part_bytes(int rows, int heads, int dim) {
   const long long all = static_cast<long long>(rows) * heads;  // of all key-value heads
-  (void)kv_heads;
   const long long prefix = all > kPrefixPartRows ? all : kPrefixPartRows;
   const long long own = all > kSpanPartRows ? all : kSpanPartRows;
   return static_cast<size_t>(prefix + own) * (dim + 1) * sizeof(float);

@@ -74,7 +74,7 @@ cudaError_t launch_rope(const RopeRows& a, int num_sms, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-bool rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
+void rope_frequencies(int rotary, double base, int scaling, double factor, double trained,
                       double low, double high, uint64_t* freq, float* magnitude) {
   const double kTurn = 6.283185307179586;
   double grow = 1.0;
@@ -99,12 +99,10 @@ bool rope_frequencies(int rotary, double base, int scaling, double factor, doubl
       keep = 1.0 - (i - first) / (last - first > 0.001 ? last - first : 0.001);
     keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
     theta *= keep + (1.0 - keep) / factor;
-    const double turns = ldexp(theta / kTurn, 64);
-    if (!(turns < 18446744073709551616.0)) return false;
-    freq[i] = static_cast<uint64_t>(turns);
+    // (base > 1 and factor >= 1: at most a radian, 0.16 of 2^64)
+    freq[i] = static_cast<uint64_t>(ldexp(theta / kTurn, 64));
   }
   *magnitude = static_cast<float>(grow);
-  return true;
 }
 
 }  // namespace tern
