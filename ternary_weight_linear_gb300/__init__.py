@@ -223,18 +223,10 @@ def _strided(t: torch.Tensor, name: str, dtypes, ndim: int) -> int:
     return t.data_ptr()
 
 
-def _heads_strides(t: torch.Tensor):
-    """(row, head) strides of a [rows, heads, dim] tensor; where there is one
-    row or head its stride does not matter."""
-    rows, heads, dim = t.shape
-    hd = t.stride(1) if heads > 1 else dim
-    return t.stride(0) if rows > 1 else heads * dim, hd
-
-
 def _heads(t: torch.Tensor, name: str, dtypes):
-    """A [rows, heads, dim] operand as _strided and _heads_strides take it, each of
-    its properties read once (they cost 0.1 us, of calls that take three): pointer,
-    shape, (row, head) strides."""
+    """The same for a [rows, heads, dim] operand: pointer, shape, (row, head) strides;
+    where there is one row or head its stride does not matter.  Each of its properties
+    is read once (they cost 0.1 us, of calls that take three)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -581,14 +573,13 @@ def tern_kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale
     many pages of every sequence).  tern_device_status tells of inconsistent
     index arrays, whose sequences or pages are skipped."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
-    pk = _strided(k, "k", _TYPES, 3)
-    pv = _strided(v, "v", (k.dtype,), 3)
-    if (k.shape != v.shape or _heads_strides(k) != _heads_strides(v)
-            or k.shape[1:] != (codes.shape[2], codes.shape[4])):
+    pk, shape, ks = _heads(k, "k", _TYPES)
+    pv, v_shape, vs = _heads(v, "v", (k.dtype,))
+    rows, kv_heads, dim = shape
+    if shape != v_shape or ks != vs or kv_heads != cache.kv_heads or dim != cache.head_dim:
         raise ValueError("k and v must be [rows, kv_heads, head_dim] with the same strides")
-    rows = k.shape[0]
     rc = load().tern_kv8_append(
-        ctypes.byref(cache), pk, pv, _TYPES[k.dtype], *_heads_strides(k), rows,
+        ctypes.byref(cache), pk, pv, _TYPES[k.dtype], *ks, rows,
         max(1, rows) if max_new is None else _most(max_new), _stream(stream))
     _check("tern_kv8_append", rc)
 
@@ -669,29 +660,37 @@ def tern_kv8_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     `workspace` (uint8, tern_kv8_attention_workspace_bytes bytes) is allocated
     zeroed per call when omitted; one kept across calls starts with SYNC_BYTES
     zero bytes and is then left alone."""
+    return _attention("tern_kv8_attention", (), q, codes, scales, page_table, row_start, seq_lens,
+                      max_new, window, sinks, softmax_scale, out, lse, workspace, stream)
+
+
+def _attention(name, shared, q, codes, scales, page_table, row_start, seq_lens, max_new, window,
+               sinks, softmax_scale, out, lse, workspace, stream):
+    """The entry `name`; shared: its arguments that the ordinary one lacks."""
     cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
-    pq = _strided(q, "q", (torch.bfloat16, torch.float16), 3)
-    rows, heads, dim = q.shape
-    kv_heads = codes.shape[2]
-    if dim != codes.shape[4]:
-        raise ValueError(f"q's head_dim {dim} is not the cache's {codes.shape[4]}")
+    pq, shape, qs = _heads(q, "q", (torch.bfloat16, torch.float16))
+    rows, heads, dim = shape
+    dtype = q.dtype
+    if dim != cache.head_dim:
+        raise ValueError(f"q's head_dim {dim} is not the cache's {cache.head_dim}")
     with _allocating(stream):
         if out is None:
-            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=dtype, device=q.device)
         if workspace is None:
-            workspace = torch.empty(
-                tern_kv8_attention_workspace_bytes(cache.seqs, max(1, rows), heads, kv_heads,
-                                                   dim),
-                dtype=torch.uint8, device=q.device)
+            need = (tern_kv8_attention_shared_workspace_bytes
+                    if shared and shared[0] and cache.seqs > 1
+                    else tern_kv8_attention_workspace_bytes)
+            workspace = torch.empty(need(cache.seqs, max(1, rows), heads, cache.kv_heads, dim),
+                                    dtype=torch.uint8, device=q.device)
             workspace[:SYNC_BYTES].zero_()  # the rest is scratch
-    rc = load().tern_kv8_attention(
-        ctypes.byref(cache), pq, _TYPES[q.dtype], *_heads_strides(q), rows, heads,
+    rc = getattr(load(), name)(
+        ctypes.byref(cache), pq, _TYPES[dtype], *qs, rows, heads, *shared,
         max(1, rows) if max_new is None else _most(max_new), _most(window), _most(sinks),
         1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
-        _dev(out, "out", q.dtype, (rows, heads, dim)),
+        _dev(out, "out", dtype, shape),
         _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check("tern_kv8_attention", rc)
+    _check(name, rc)
     return out
 
 
@@ -716,30 +715,9 @@ def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torc
     them.  The result is tern_kv8_attention's; the other arguments are as there,
     the workspace of tern_kv8_attention_shared_workspace_bytes bytes (of
     tern_kv8_attention's where `shared` is 0 or there is one sequence)."""
-    cache = _kv8_cache(codes, scales, page_table, row_start, seq_lens)
-    pq, shape, qs = _heads(q, "q", (torch.bfloat16, torch.float16))
-    rows, heads, dim = shape
-    dtype = q.dtype
-    if dim != cache.head_dim:
-        raise ValueError(f"q's head_dim {dim} is not the cache's {cache.head_dim}")
-    with _allocating(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=q.device)
-        if workspace is None:
-            need = (tern_kv8_attention_shared_workspace_bytes if shared and cache.seqs > 1
-                    else tern_kv8_attention_workspace_bytes)
-            workspace = torch.empty(need(cache.seqs, max(1, rows), heads, cache.kv_heads, dim),
-                                    dtype=torch.uint8, device=q.device)
-            workspace[:SYNC_BYTES].zero_()  # the rest is scratch
-    rc = load().tern_kv8_attention_shared(
-        ctypes.byref(cache), pq, _TYPES[dtype], *qs, rows, heads, _most(shared),
-        max(1, rows) if max_new is None else _most(max_new), _most(window), _most(sinks),
-        1 / math.sqrt(dim) if softmax_scale is None else float(softmax_scale),
-        _dev(out, "out", dtype, shape),
-        _dev(lse, "lse", torch.float32, (rows, heads)) if lse is not None else None,
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check("tern_kv8_attention_shared", rc)
-    return out
+    return _attention("tern_kv8_attention_shared", (_most(shared),), q, codes, scales, page_table,
+                      row_start, seq_lens, max_new, window, sinks, softmax_scale, out, lse,
+                      workspace, stream)
 
 
 def tern_linear_small_t_noalloc(Wpacked: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
