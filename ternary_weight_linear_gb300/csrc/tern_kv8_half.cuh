@@ -197,6 +197,67 @@ __device__ __forceinline__ void half_values(const uint8_t* vb, int g, int t,
   }
 }
 
+// The online softmax of a half-page: its scores sc to weights, with the rows' references
+// and sums, and the output so far where a reference rises.  cs: what a row's scores are
+// times, but for the key scale.
+template <int D, int NT>
+__device__ __forceinline__ void half_softmax(const PageRec& rec, const float (&cs)[NT][2],
+                                             float (&sc)[NT][2][4], float (&ref)[NT][2],
+                                             float (&sum)[NT][2], float (&o)[NT][D / 16][4]) {
+  constexpr float kUp = biased(NT) ? kCodeUp : 1.f;  // 1 over the codes' unit
+  bool raise = false;
+  float c[NT][2], big[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      // (a scale of 0 must not turn a masked -inf into a NaN)
+      c[n][x] = fmaxf(cs[n][x] * rec.ks * kUp, 1e-37f);
+      big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]), fmaxf(sc[n][1][x], sc[n][1][x + 2]));
+      raise = raise || fmaf(big[n][x], c[n][x], rec.lv) > ref[n][x] + kRLazy;
+    }
+  if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float scale[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = fmaf(big[n][x], c[n][x], rec.lv);  // -inf: no visible token
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        scale[x] = 1.f;
+        if (top > ref[n][x] + kRLazy) {
+          scale[x] = exp2_approx(ref[n][x] - top);  // 0 for the row's first
+          sum[n][x] *= scale[x];
+          ref[n][x] = top;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float add = kROff + rec.lv - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int y = x; y < 4; y += 2) {
+          sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
+          part += sc[n][i][y];
+        }
+      // (scales that cannot be used: the rows that see the page, and only they, become
+      // NaN)
+      if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rv, sum[n][x]);
+    }
+  }
+}
+
 // O^T += Vc^T P^T, the weights P in the scores' place, times any (a pair of 1 or 0
 // in fp16).
 template <int D, int NT>

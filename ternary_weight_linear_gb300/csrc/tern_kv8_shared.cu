@@ -300,59 +300,7 @@ struct Span {
         // the values' codes, on their way under the softmax
         uint32_t vw[2][4][D / 32];
         half_values<D>(kb + kHalf * D, g, t, vw);
-        bool raise = false;
-        float c[NT][2], big[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // (a scale of 0 must not turn a masked -inf into a NaN)
-            c[n][x] = fmaxf(cs[n][x] * rec.ks * kUp, 1e-37f);
-            big[n][x] = fmaxf(fmaxf(sc[n][0][x], sc[n][0][x + 2]),
-                              fmaxf(sc[n][1][x], sc[n][1][x + 2]));
-            raise = raise || fmaf(big[n][x], c[n][x], rec.lv) > ref[n][x] + kRLazy;
-          }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float scale[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float top = fmaf(big[n][x], c[n][x], rec.lv);  // -inf: no visible token
-#pragma unroll
-              for (int k = 4; k < 32; k <<= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-              scale[x] = 1.f;
-              if (top > ref[n][x] + kRLazy) {
-                scale[x] = exp2_approx(ref[n][x] - top);  // 0 for the row's first
-                sum[n][x] *= scale[x];
-                ref[n][x] = top;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kMT; ++i)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) o[n][i][x] *= scale[x & 1];
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float add = kROff + rec.lv - (ref[n][x] == -INFINITY ? 0.f : ref[n][x]);
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int y = x; y < 4; y += 2) {
-                sc[n][i][y] = exp2_approx(fmaf(sc[n][i][y], c[n][x], add));
-                part += sc[n][i][y];
-              }
-            // (scales that cannot be used: the rows that see the page, and only
-            // they, become NaN)
-            if (big[n][x] != -INFINITY) sum[n][x] = fmaf(part, rec.rv, sum[n][x]);
-          }
-        }
+        half_softmax<D, NT>(rec, cs, sc, ref, sum, o);
         half_products<D, NT>(sc, half2_bits(rec.any, rec.any), vw, o);
         __syncwarp();  // the stage has been read
         ++used;
