@@ -414,7 +414,7 @@ __device__ __noinline__ SoftState wide_pages(uint8_t* smem, const Kv8Args& a, So
 // 96 rows, where no warps are idle, it loses (46.5 and 43.2 us, 16 tokens over
 // 16000).
 constexpr int kSplitRows = 64;
-//
+
 // kMode kKvOwn: a part of the result, that of the tokens behind a shared prefix,
 // whose positions and pages count from its end.  kKvPrefix: the parts of the prefix
 // itself, one "sequence" of all the call's rows, which see all of it (but for a

@@ -204,9 +204,9 @@ cudaError_t launch_types(const NormArgs& a, cudaStream_t stream) {
 //   y = (r w2) (mean(r^2) + eps)^-1/2;    codes and scale of y as above.
 // The same plan with a second reduction: one CTA per token, the row in
 // registers from the first load to the last store, so every input is read and
-// every output written once.  Rows of one vector a thread load the residual before
-// the first barrier, longer ones, whose registers are the row's, behind it, as all
-// do with the weights and the gate, which other tokens' CTAs have left in L1.
+// every output written once.  Rows of one and two vectors a thread load the residual
+// before the first barrier, those of four, whose registers are the row's, behind it, as
+// all do with the weights and the gate, which other tokens' CTAs have left in L1.
 // Bound by instructions: 2048 rows of 5120, fp32 x, a gate a channel, bf16 weights
 // take 22.5 us (their bytes 13.9 at the copy rate; the issue slots were 67 % busy at
 // 25.5), 41.8 with all loads before the barrier, whose 56 registers left one CTA of

@@ -93,6 +93,18 @@ def test_types(tl, xt, rt, wt, post):
           with_y=True, seed=3)
 
 
+# two vectors a thread from 8208 on, four from 16400
+@pytest.mark.parametrize("K", [8208, 16384, 16400, 30000])
+@pytest.mark.parametrize("xt,rt,wt,post,gate", [
+    ("float32", "float32", "float32", "bfloat16", None),
+    ("bfloat16", "float32", "bfloat16", "bfloat16", "bfloat16"),
+    ("float32", "bfloat16", "float32", None, "float32"),
+    ("bfloat16", "bfloat16", "bfloat16", "float32", "float32")])
+def test_types_of_long_rows_in_place(tl, K, xt, rt, wt, post, gate):
+    check(tl, 3, K, xt, rt, wt, post, gate=gate, gate_rows=True, rs=0.9, bs=-1.25, with_y=True,
+          in_place=True, seed=5)
+
+
 def test_gates(tl):
     """A row for all tokens, rows of their own, expanded and strided ones."""
     import torch
