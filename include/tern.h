@@ -512,8 +512,10 @@ size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
  * first `shared` tokens of every sequence with new tokens lie in the same pages
  * (the first shared / 64 entries of their rows of page_table are alike), written
  * once and not by this step.  Keys and values of those pages are read once for
- * all rows of the batch instead of once for each sequence (prompt chunks, which
- * are bound by their products, read them each for itself); the result is
+ * all rows of the batch instead of once for each sequence, where that is expected
+ * to gain: prompt chunks, tables far wider than the prefix (the launch knows
+ * table_width, not the lengths: a tight table is best) and very many sequences
+ * behind a short one read them each for itself.  The result is
  * tern_kv8_attention's of the same arguments, up to the roundings stated there.
  *   shared   tokens, a multiple of 64, 0 (none) to 64 * table_width; a sequence
  *            whose new tokens do not all lie behind them is inconsistent
@@ -525,7 +527,8 @@ size_t tern_kv8_attention_shared_workspace_bytes(int seqs, int rows, int heads,
  *            kv_heads / 256) * kv_heads has to stay below 2^31 - 1000, and
  *            seqs * kv_heads below 2^27 - 100
  *   the others as for tern_kv8_attention; workspace of
- *            tern_kv8_attention_shared_workspace_bytes, zeroed and kept as there.
+ *            tern_kv8_attention_shared_workspace_bytes, zeroed and kept as there
+ *            (zero it again after TERN_ECUDA too).
  * The prefix's and the own tokens' parts are joined in fp32 by their
  * log-sum-exps; results are bit-for-bit reproducible. */
 int tern_kv8_attention_shared(const tern_kv8_cache* cache, const void* q, int type,

@@ -21,7 +21,7 @@
 //   the join.
 //
 // Measured, 32 sequences of 40 to 1500 tokens (6 query heads on each of 8 key-value
-// heads of 128) behind 16384: 36.5 us; every page's codes once are 12.7 at the copy
+// heads of 128) behind 16384: 36.8 us; every page's codes once are 12.7 at the copy
 // rate, each sequence for itself takes 150.  Alone, the prefix's launch
 // (80 CTAs) takes 33 us, 1700 cycles a page, whose scores' products read the queries
 // from shared memory: its tensor pipe is 48 % busy.  The spans beside it take 30, of
