@@ -712,9 +712,10 @@ def tern_kv8_attention_shared(q: torch.Tensor, codes: torch.Tensor, scales: torc
     The first `shared` tokens (a multiple of 64) of every sequence lie in the
     same pages: the first shared / 64 entries of the rows of page_table are
     alike.  They are read once for all rows of the batch where that gains by the
-    table's width (a tight table is best).  New tokens lie behind them.  The result is tern_kv8_attention's; the other arguments are as there,
-    the workspace of tern_kv8_attention_shared_workspace_bytes bytes (of
-    tern_kv8_attention's where `shared` is 0 or there is one sequence)."""
+    table's width (a tight table is best).  New tokens lie behind them.  The result
+    is tern_kv8_attention's; the other arguments are as there, the workspace of
+    tern_kv8_attention_shared_workspace_bytes bytes (of tern_kv8_attention's where
+    `shared` is 0 or there is one sequence)."""
     return _attention("tern_kv8_attention_shared", (_most(shared),), q, codes, scales, page_table,
                       row_start, seq_lens, max_new, window, sinks, softmax_scale, out, lse,
                       workspace, stream)

@@ -930,28 +930,37 @@ bool kv8_shared_fits(int rows, int group, int kv_heads, int seqs) {
 //
 // Chunks of more than kSpanRows rows go through the tensor cores either way, and what
 // sharing loses is the parts' way through the workspace and launches that follow each
-// other.  Each for itself over shared: 3600 rows 0.38
-// to 0.9 (2 to 16 sequences behind 512 to 16384); 72, 128 and 258 rows, up to 2000 own
-// tokens, behind 512 0.5 to 0.8, behind 4096 0.6 to 1.05 at up to 16 sequences.  Longer
-// prefixes of more sequences would gain, which the rule leaves: 32 sequences of 72 rows
-// behind 16384 2.3 (454 and 200 us), of 258 rows 1.4; 4 of 72 rows 1.04.  In a mixed batch
-// the shorter sequences win a pass over the prefix each (2 bytes an element, and there
-// are seqs - R / most of them at least) and all rows lose their parts (some 12).
+// other.  Each for itself over shared: 3600 rows 0.38 to 0.9 (2 to 16 sequences behind
+// 512 to 16384); 72, 128 and 258 rows, up to 2000 own tokens, behind 512 0.5 to 0.8,
+// behind 4096 0.6 to 1.05 at up to 16 sequences.  Longer prefixes of more sequences would
+// gain, which the rule leaves: 32 sequences of 72 rows behind 16384 2.3 (454 and 200 us),
+// of 258 rows 1.4; 4 of 72 rows 1.04.
+//
+// In a mixed batch the shorter sequences win a pass over the prefix each (2 bytes an
+// element, and there are seqs - R / most of them at least) and all rows lose their parts
+// (some 12), with the losses above, sooner, since the spans are of 16 rows.  A chunk of 12
+// to 600 tokens among single ones of up to 300 own tokens, behind 64 shared ones 1.0 to
+// 1.17 at 128 sequences, 0.88 at 256; behind 512 0.98 to 1.23, then 0.94 to 0.98, 0.71 to
+// 0.82 at 512; behind 4096 1.1 at 1024, 0.63 to 0.71 at 2048.  32 sequences of up to 17000,
+// with a chunk of 12 or without any (max_new left out), behind 64 0.91 and 0.78, behind 512
+// 0.93 and 0.79, of up to 4000 1.02 and 0.97; behind 4096 1.1 and 1.0 (with a chunk of 600
+// tokens 0.71, and 1.24 of up to 300).
 bool kv8_shared_pays(const Kv8Args& a, int shared) {
   if (a.seqs == 1 || shared == 0) return false;
   const long long R = static_cast<long long>(a.rows) * a.group;
   const long long most = static_cast<long long>(a.max_new) * a.group;
+  const SeenPages seen = seen_pages(a, shared);
+  const long long prefix = seen.prefix;
   if (most <= kSpanRows) {
-    const SeenPages seen = seen_pages(a, shared);
-    const long long prefix = seen.prefix;
     if (a.seqs > (most <= 8 ? 640 : 384) + 64 * prefix) return false;
     const long long groups = (most + 15) / 16;  // beyond 24 rows
     return most <= 8 || seen.own <= (most <= 16   ? 64 * (prefix + 1)
                                      : most <= 24 ? 8 * (prefix + 8)
                                                   : (8 * prefix) >> groups);
   }
+  const long long limit = 16 * (prefix + 7);  // of sequences, and of own pages
   const long long shorter = a.seqs - (R + most - 1) / most;
-  return shorter * shared > 6 * R;
+  return a.seqs <= limit && seen.own <= limit && shorter * shared > 6 * R;
 }
 
 size_t kv8_shared_part_bytes(int rows, int heads, int dim) {

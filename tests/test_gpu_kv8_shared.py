@@ -200,6 +200,23 @@ def test_what_does_not_gain_reads_each_for_itself(tl, shared, seqs, m, columns, 
         assert launches == tl.tern_last_launches()
 
 
+@pytest.mark.parametrize("seqs,columns,shares", [(128, 3, True), (129, 3, False), (40, 128, True),
+                                                 (40, 129, False)])
+def test_a_chunk_among_too_many_or_in_too_wide_a_table(tl, seqs, columns, shares):
+    """66 rows of one sequence, 6 of the others, behind a page: 16 * (1 + 7) sequences and
+    own pages at most."""
+    import torch
+    new = [11] + [1] * (seqs - 1)
+    c = Case(64, [m + 7 * (b % 9) for b, m in enumerate(new)], new, 6, 1, 64, seed=columns)
+    wide = np.full((seqs, 1 + columns), -7, np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    out, lse = c.check(tl)
+    lse2 = torch.full_like(lse, 7.0)
+    whole = tl.tern_kv8_attention(c.q_dev, *c.args(), max_new=c.max_new, lse=lse2)
+    assert (torch.equal(out, whole) and torch.equal(lse, lse2)) == (not shares)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (130, 7), (400, 64), (600, 100),
                                           (900, 65), (100, 2000), (5000, 3)])
